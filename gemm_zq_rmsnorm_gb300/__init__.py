@@ -32,13 +32,19 @@ EXPORTS = ("zq_rmsnorm_q8_1", "zq_q4k_gemv", "zq_q4k_gemv_pair", "zq_q4k_gemm",
            "zq_q5k_gemm", "zq_q6k_gemm", "zq_q5k_gemv", "zq_q6k_gemv", "zq_rmsnorm_q6k_gemv",
            "zq_q5k_bytes", "zq_q6k_bytes", "zq_debug_stream_plan", "zq_debug_peak_probe",
            "zq_debug_wait_expiry", "zq_q8_1_dequant_f16", "zq_f16_gemm_workspace_bytes", "zq_f16_gemm",
-           "zq_rmsnorm_q4k_gemm", "zq_copy")
+           "zq_rmsnorm_q4k_gemm", "zq_copy", "zq_rope_table", "zq_head_norm_rope")
 
 
 class ZQError(RuntimeError):
     def __init__(self, status: int, msg: str):
         super().__init__(f"{STATUS_NAMES.get(status, status)}: {msg}")
         self.status = status
+
+
+class _Cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int), ("pages", ctypes.c_int),
+                ("page", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int), ("k_scale", ctypes.c_float),
+                ("v_scale", ctypes.c_float)]
 
 
 class _Q8(ctypes.Structure):
@@ -58,6 +64,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
                            "`python gemm_zq_rmsnorm_gb300/build.py` (needs nvcc)")
     lib = ctypes.CDLL(path)
     P, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    ll = ctypes.c_longlong
     sig = {
         "zq_rmsnorm_q8_1": ([P, P, i, i, f, _Q8, P], i),
         "zq_q4k_gemv": ([P, i, i, _Q8, P, P], i),
@@ -91,6 +98,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "zq_q8_1_dequant_f16": ([_Q8, i, i, P, P], i),
         "zq_f16_gemm_workspace_bytes": ([i, i, i], sz),
         "zq_f16_gemm": ([P, i, i, P, i, P, P, sz, P], i),
+        "zq_rope_table": ([P, P, i, P], i),
+        "zq_head_norm_rope": ([P, ll, P, ll, P, ll, i, i, P, P, f, P, i, i, P, i, P, P, P, ll, P], i),
         "zq_rmsnorm_q4k_gemm": ([P, P, f, i, i, P, i, P, ctypes.POINTER(_Q8), P, sz, P], i),
     }
     for name, (args, res) in sig.items():
@@ -428,6 +437,103 @@ def debug_wait_expiry(W: torch.Tensor, N: int, K: int, a: Q8_1, y: torch.Tensor,
     in device_status()."""
     _check(load().zq_debug_wait_expiry(_ptr(W), N, K, a._c(), _ptr(y), withhold_stage, wait_us, ctas,
                                        _stream(stream)))
+
+
+# ------------------------------------------------------------ attention side
+_TYPES = {torch.float16: 1, torch.bfloat16: 2, torch.float8_e4m3fn: 3}   # ZQ_F16, ZQ_BF16, ZQ_E4M3
+
+
+class KVCache:
+    """A paged key-value cache: k and v of [pages][Hk][page][D], float16,
+    bfloat16 or float8_e4m3fn, holding values of stored * scale (zq_kv_cache).
+    A handle on the caller's tensors; make it once and keep it."""
+
+    __slots__ = ("k", "v", "pages", "Hk", "page", "D", "device", "index", "_c", "_ref")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: float = 1.0, v_scale: float = 1.0):
+        if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device:
+            raise ValueError("KVCache: k and v must be [pages][Hk][page][D] of one type and device")
+        if k.dtype not in _TYPES:
+            raise ValueError(f"KVCache: type {k.dtype} is not float16, bfloat16 or float8_e4m3fn")
+        if not (k.is_cuda and k.is_contiguous() and v.is_contiguous()):
+            raise ValueError("KVCache: k and v must be contiguous CUDA tensors")
+        self.k, self.v = k, v
+        self.pages, self.Hk, self.page, self.D = k.shape
+        self.device, self.index = k.device, k.device.index
+        self._c = _Cache(k.data_ptr(), v.data_ptr(), _TYPES[k.dtype], self.pages, self.page, self.Hk, self.D,
+                         float(k_scale), float(v_scale))
+        self._ref = ctypes.byref(self._c)
+
+
+def _on(index: int, what: str, *tensors):
+    """Every tensor on the current CUDA device, where the call launches."""
+    if torch.cuda.current_device() != index:
+        raise ValueError(f"{what}: the tensors are on cuda:{index}, which is not the current device")
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{what}: a tensor is not on cuda:{index}")
+
+
+def _head_rows(t: torch.Tensor, T: int, D: int, what: str):
+    """(address, row stride, heads) of fp32 rows [T][H][D] or [T][H * D]."""
+    shape, stride = t.shape, t.stride()
+    n = shape[1] if len(shape) == 2 else shape[1] * D if len(shape) == 3 and shape[2] == D else 0
+    if (t.dtype != torch.float32 or shape[0] != T or n < D or n % D or stride[-1] != 1
+            or (len(shape) == 3 and shape[1] > 1 and stride[1] != D)):
+        raise ValueError(f"{what} must be fp32 rows [{T}][H][{D}] or [{T}][H * {D}] with the heads of a row together")
+    return t.data_ptr(), stride[0] if T > 1 else n, n // D
+
+
+def _ints(t: torch.Tensor, n: int, what: str) -> int:
+    if t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be {n} contiguous int32 values")
+    return t.data_ptr()
+
+
+def rope_table(inv_freq, axis=None, device="cuda") -> torch.Tensor:
+    """The rotation table of head_norm_rope for the pairs' frequencies (radians
+    per position, float64) and position axes (see zq_rope_table)."""
+    freq = torch.as_tensor(inv_freq, dtype=torch.float64).cpu().contiguous()
+    n = freq.numel()
+    ax = None if axis is None else torch.as_tensor(axis, dtype=torch.int32).cpu().contiguous()
+    if ax is not None and ax.numel() != n:
+        raise ValueError("rope_table: one axis for each frequency")
+    out = torch.empty(n, dtype=torch.int64)
+    _check(load().zq_rope_table(_ptr(freq), _ptr(ax), n, _ptr(out)))
+    return out.to(device)
+
+
+def head_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma_q, gamma_k, eps: float, table, pos,
+                   cache: KVCache, slots: torch.Tensor, interleaved: bool = False, q_out: torch.Tensor | None = None,
+                   stream=None) -> torch.Tensor:
+    """Per-head RMSNorm of q and k [T][H][D] (or [T][H * D], rows strided),
+    rotation by pos int32 [T] or [axes][T], keys and values written to their
+    slots int32 [T] of the cache (see zq_head_norm_rope); returns the queries."""
+    lib = _lib or load()
+    D, T = cache.D, q.shape[0]
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    _on(cache.index, "head_norm_rope", q, k, v, gamma_q, gamma_k, table, pos, slots, q_out)
+    qp, qs, Hq = _head_rows(q, T, D, "head_norm_rope: q")
+    kp, ks, Hk = _head_rows(k, T, D, "head_norm_rope: k")
+    vp, vs, Hv = _head_rows(v, T, D, "head_norm_rope: v")
+    op, os_, Ho = _head_rows(q_out, T, D, "head_norm_rope: q_out")
+    if Hk != cache.Hk or Hv != cache.Hk or Ho != Hq:
+        raise ValueError("head_norm_rope: the heads of k and v must be the cache's, those of q_out q's")
+    for g in (gamma_q, gamma_k):
+        if g is not None and (g.dtype != torch.float32 or g.numel() != D or not g.is_contiguous()):
+            raise ValueError(f"head_norm_rope: gamma must be {D} contiguous fp32 values")
+    rot, axes, pp = 0, 1, None
+    if table is not None:
+        if table.dtype != torch.int64 or not table.is_contiguous():
+            raise ValueError("head_norm_rope: table must be contiguous int64 (rope_table)")
+        rot = 2 * table.numel()
+        axes = pos.shape[0] if pos.dim() == 2 else 1
+        pp = _ints(pos, axes * T, "head_norm_rope: pos")
+    _check(lib.zq_head_norm_rope(qp, qs, kp, ks, vp, vs, T, Hq, _ptr(gamma_q), _ptr(gamma_k), eps,
+                                 table.data_ptr() if rot else None, rot, interleaved, pp, axes, cache._ref,
+                                 _ints(slots, T, "head_norm_rope: slots"), op, os_, _stream(stream)))
+    return q_out
 
 
 # operations per probe launch, by kind (zq_debug_peak_probe)

@@ -6,6 +6,7 @@
 // build cannot serve fails instead of falling back (Zynfer README: forced
 // unsupported paths exit with an error).  Nothing here computes: every step of
 // the path runs in the kernels of the other translation units.
+#include <cmath>
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
@@ -13,6 +14,7 @@
 #include <string>
 
 #include "zq_internal.cuh"
+#include "zq_kv.cuh"
 #include "zq_tc_common.cuh"
 
 __device__ unsigned int g_zq_device_status;
@@ -673,6 +675,116 @@ int zq_debug_q4k_isums(const void *W, int N, int K, zq_q8_1 a, int B, int32_t *i
     if (path == 0) return launched(launch_gemv(W, nullptr, N, K, a, B, nullptr, nullptr, isums, s), "isums (dp4a)");
     return launched(launch_isums_tc(W, N, K, a, B, isums, workspace, s),
                     path == 1 ? "isums (tensor cores, prefill sizes)" : "isums (tensor cores, chunk sizes)");
+}
+
+}  // extern "C"
+
+namespace {
+
+// The limits of include/zq.h on a paged cache.
+int check_cache(const zq_kv_cache *c, const char *name)
+{
+    if (!c || !c->k || !c->v) return fail(ZQ_ERR_ARG, "%s: null cache", name);
+    if (!aligned16(c->k) || !aligned16(c->v)) return fail(ZQ_ERR_ALIGN, "%s: the cache must be 16-byte aligned", name);
+    if (c->type != ZQ_F16 && c->type != ZQ_BF16 && c->type != ZQ_E4M3)
+        return fail(ZQ_ERR_ARG, "%s: cache type %d unknown", name, c->type);
+    if (c->D != 64 && c->D != 128 && c->D != 256)
+        return fail(ZQ_ERR_SHAPE, "%s: D = %d must be 64, 128 or 256", name, c->D);
+    if (c->page < 16 || c->page > 256 || (c->page & (c->page - 1)))
+        return fail(ZQ_ERR_SHAPE, "%s: page = %d must be a power of two in [16, 256]", name, c->page);
+    if (c->Hk < 1 || c->Hk > 1024) return fail(ZQ_ERR_SHAPE, "%s: Hk = %d out of range", name, c->Hk);
+    if (c->pages < 1 || (long long)c->pages * c->page > INT32_MAX)
+        return fail(ZQ_ERR_SHAPE, "%s: %d pages of %d tokens out of range", name, c->pages, c->page);
+    if (!(c->k_scale > 0.0f) || !(c->v_scale > 0.0f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
+        return fail(ZQ_ERR_ARG, "%s: cache scales must be positive and finite", name);
+    return ZQ_OK;
+}
+
+// One of the strided fp32 row blocks of the attention-side calls.
+int check_rows(const float *p, long long stride, long long width, const char *name, const char *what)
+{
+    if (!p) return fail(ZQ_ERR_ARG, "%s: null %s", name, what);
+    if (!aligned16(p)) return fail(ZQ_ERR_ALIGN, "%s: %s must be 16-byte aligned", name, what);
+    if (stride < width || stride % 4 || stride > (1LL << 40))
+        return fail(ZQ_ERR_SHAPE, "%s: stride %lld of %s must be a multiple of 4 and at least %lld", name, stride, what,
+                    width);
+    return ZQ_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+int zq_rope_table(const double *inv_freq, const int *axis, int n, uint64_t *table)
+{
+    if (!inv_freq || !table || n < 1) return fail(ZQ_ERR_ARG, "zq_rope_table: null array or n < 1");
+    for (int i = 0; i < n; ++i) {
+        if (!std::isfinite(inv_freq[i])) return fail(ZQ_ERR_ARG, "zq_rope_table: inv_freq[%d] is not finite", i);
+        const int ax = axis ? axis[i] : 0;
+        if (ax < 0 || ax > 2) return fail(ZQ_ERR_ARG, "zq_rope_table: axis[%d] = %d must be 0, 1 or 2", i, ax);
+        double turns = inv_freq[i] / 6.283185307179586477;
+        turns -= std::floor(turns);   // in [0, 1]
+        const uint64_t step = turns < 1.0 ? (uint64_t)std::ldexp(turns, 64) : 0;
+        table[i] = ((step + 2) & ~(uint64_t)3) | (uint64_t)ax;   // rounded to a multiple of four
+    }
+    return ZQ_OK;
+}
+
+int zq_head_norm_rope(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
+                      long long v_stride, int T, int Hq, const float *gamma_q, const float *gamma_k, float eps,
+                      const uint64_t *table, int rot, int interleaved, const int32_t *pos, int axes,
+                      const zq_kv_cache *cache, const int32_t *slots, float *q_out, long long q_out_stride,
+                      void *stream)
+{
+    static const char *name = "zq_head_norm_rope";
+    int st = check_cache(cache, name);
+    if (st) return st;
+    const int D = cache->D, Hk = cache->Hk;
+    if (T < 1 || Hq < 1 || (long long)T * (Hq + 2LL * Hk) > INT32_MAX)
+        return fail(ZQ_ERR_SHAPE, "%s: T = %d, Hq = %d out of range", name, T, Hq);
+    if (rot < 0 || rot > D || rot % 16)
+        return fail(ZQ_ERR_SHAPE, "%s: rot = %d must be a multiple of 16 in [0, %d]", name, rot, D);
+    if (axes < 1 || axes > 3) return fail(ZQ_ERR_SHAPE, "%s: axes = %d must be 1, 2 or 3", name, axes);
+    if (!(eps >= 0.0f)) return fail(ZQ_ERR_ARG, "%s: eps must be >= 0", name);
+    if ((st = check_rows(q, q_stride, (long long)Hq * D, name, "q"))) return st;
+    if ((st = check_rows(k, k_stride, (long long)Hk * D, name, "k"))) return st;
+    if ((st = check_rows(v, v_stride, (long long)Hk * D, name, "v"))) return st;
+    if ((st = check_rows(q_out, q_out_stride, (long long)Hq * D, name, "q_out"))) return st;
+    if (q_out == q && q_out_stride != q_stride)
+        return fail(ZQ_ERR_ARG, "%s: q_out in place needs q's stride", name);
+    if (!slots || (rot && (!pos || !table))) return fail(ZQ_ERR_ARG, "%s: null slots, pos or table", name);
+    if (!aligned16(gamma_q) || !aligned16(gamma_k) || !aligned16(slots) || !aligned16(pos) || !aligned16(table))
+        return fail(ZQ_ERR_ALIGN, "%s: gamma, slots, pos and table must be 16-byte aligned", name);
+    int dev;
+    if ((st = check_device(&dev))) return st;
+    HeadNormRopeArgs a{};
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hk = Hk;
+    a.gamma_q = gamma_q;
+    a.gamma_k = gamma_k;
+    a.eps = eps;
+    a.table = table;
+    a.rot = rot;
+    a.interleaved = interleaved != 0;
+    a.pos = pos;
+    a.axes = axes;
+    a.kc = cache->k;
+    a.vc = cache->v;
+    a.page_shift = page_shift(cache->page);
+    a.nslots = (long long)cache->pages * cache->page;
+    a.k_scale = cache->k_scale;
+    a.v_scale = cache->v_scale;
+    a.slots = slots;
+    a.q_out = q_out;
+    a.q_out_stride = q_out_stride;
+    return launched(launch_head_norm_rope(a, D, cache->type, (cudaStream_t)stream), name);
 }
 
 }  // extern "C"

@@ -1,0 +1,69 @@
+// zq_kv.cuh -- the paged key-value cache as the kernels see it, and the
+// rounding of fp32 values to its types.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <stdint.h>
+
+#include "zq.h"
+
+namespace zq {
+
+template <int TYPE> struct KvBytes { static constexpr int value = TYPE == ZQ_E4M3 ? 1 : 2; };
+
+// Two fp32 values to two stored ones, `lo` at the lower address: nearest even;
+// e4m3 saturates, NaN stays NaN.
+template <int TYPE>
+__device__ __forceinline__ uint32_t kv_pack2(float lo, float hi)
+{
+    uint32_t r;
+    if constexpr (TYPE == ZQ_F16) {
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    } else if constexpr (TYPE == ZQ_BF16) {
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    } else {
+        uint16_t h;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(hi), "f"(lo));
+        r = h;
+    }
+    return r;
+}
+
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+
+// log2 of the page size (host; page is a power of two)
+inline int page_shift(int page)
+{
+    int s = 0;
+    while ((1 << s) < page) ++s;
+    return s;
+}
+
+struct HeadNormRopeArgs {
+    const float *q, *k, *v;
+    long long q_stride, k_stride, v_stride;
+    int T, Hq, Hk;
+    const float *gamma_q, *gamma_k;
+    float eps;
+    const uint64_t *table;
+    int rot, interleaved;
+    const int32_t *pos;
+    int axes;
+    void *kc, *vc;
+    int page_shift;
+    long long nslots;
+    float k_scale, v_scale;
+    const int32_t *slots;
+    float *q_out;
+    long long q_out_stride;
+    int chunk, chunks;   // rows per warp, warps per token (set by the launcher)
+};
+cudaError_t launch_head_norm_rope(const HeadNormRopeArgs &a, int D, int type, cudaStream_t st);
+
+}  // namespace zq

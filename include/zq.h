@@ -454,6 +454,64 @@ ZQ_API int zq_debug_wait_expiry(const void *W, int N, int K, zq_q8_1 a, float *y
  */
 ZQ_API int zq_copy(void *dst, const void *src, size_t bytes, void *stream);
 
+/*
+ * ------------------------------------------------ attention-side operators
+ * What a step does between its q/k/v projections and its o projection
+ * (MIInfer README, "Status": one launch for the heads' RMS norms; cached
+ * single-query attention; Zynfer README: persistent per-layer K and V).
+ *
+ * Paged key-value cache: `pages` pages of `page` tokens, for K and for V
+ *   [pages][Hk][page][D]   of `type`, caller-owned device memory;
+ * token slot s is row s % page of page s / page.  The value held is the
+ * stored one times k_scale (v_scale); storing rounds x / scale once, e4m3
+ * saturating at +-448 (NaN stays NaN), f16 overflowing to infinity.
+ * Limits: page a power of two in 16..256, D 64, 128 or 256, 1 <= Hk <= 1024,
+ * pages * page < 2^31 (offsets into the cache are 64-bit), scales positive
+ * and finite.
+ */
+enum { ZQ_F16 = 1, ZQ_BF16 = 2, ZQ_E4M3 = 3 };
+
+typedef struct zq_kv_cache {
+    void *k, *v;              /* [pages][Hk][page][D] */
+    int type;                 /* ZQ_F16, ZQ_BF16 or ZQ_E4M3 */
+    int pages, page, Hk, D;
+    float k_scale, v_scale;
+} zq_kv_cache;
+
+/*
+ * Entries of a rotation table: for each of n pairs the phase step
+ * inv_freq / (2 pi) as a fraction of 2^64 turns (times a position, modulo
+ * 2^64, it is the angle, to 2^-31 turns at any 32-bit position), its two low
+ * bits replaced by the position axis the pair follows.  Host arrays;
+ * inv_freq finite; axis 0..2, or NULL for axis 0.
+ */
+ZQ_API int zq_rope_table(const double *inv_freq, const int *axis, int n, uint64_t *table);
+
+/*
+ * RMSNorm of every query and key head, rotation by position, and the write of
+ * keys and values into the cache, in one pass over the stacked q/k/v output.
+ *   q : fp32, head h of token t at q + t * q_stride + h * D; k, v alike with
+ *       Hk heads (strides in floats, multiples of 4);
+ *   gamma_q, gamma_k : fp32 [D], either may be NULL (that norm is left out);
+ *   xh = (x / sqrt(mean(x^2) + eps)) * gamma over the head's D values;
+ *   table : device uint64 [rot / 2] (zq_rope_table); rot a multiple of 16,
+ *       0..D (0: no rotation, table may be NULL); the first rot values are
+ *       rotated, pair p being (p, p + rot/2), or (2p, 2p + 1) with
+ *       `interleaved`: (a, b) -> (a cos - b sin, b cos + a sin);
+ *   pos : int32 [axes][T], axes 1..3, any sign (a pair whose axis is not
+ *       below `axes` follows the last one);
+ *   slots : int32 [T]; a token whose slot is outside the cache is not
+ *       written.  Tokens of one call have slots of their own: when two share
+ *       one, its contents are a mixture of the two;
+ *   q_out : fp32, laid out as q with q_out_stride; may be q itself.
+ * T >= 1, T * (Hq + 2 Hk) < 2^31, Hq >= 1.
+ */
+ZQ_API int zq_head_norm_rope(const float *q, long long q_stride, const float *k, long long k_stride,
+                             const float *v, long long v_stride, int T, int Hq, const float *gamma_q,
+                             const float *gamma_k, float eps, const uint64_t *table, int rot, int interleaved,
+                             const int32_t *pos, int axes, const zq_kv_cache *cache, const int32_t *slots,
+                             float *q_out, long long q_out_stride, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -1,0 +1,104 @@
+"""CPU-only checks of the attention-side calls: refusals on the host with the
+documented status, and the rotation table's values."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import gemm_zq_rmsnorm_gb300 as zq
+
+A16, A8 = 0x10000, 0x10008
+
+
+@pytest.fixture(scope="module")
+def lib():
+    return zq.load()
+
+
+def cache(k=A16, v=A16, type=1, pages=4, page=16, Hk=2, D=128, ks=1.0, vs=1.0):
+    return ctypes.byref(zq._Cache(k, v, type, pages, page, Hk, D, ks, vs))
+
+
+def norm_rope(lib, q=A16, qs=512, k=A16, ks=256, v=A16, vs=256, T=3, Hq=4, gq=A16, gk=A16, eps=1e-6, table=A16,
+              rot=128, inter=0, pos=A16, axes=1, c=None, slots=A16, out=A16 + 4096, os=512):
+    return lib.zq_head_norm_rope(q, qs, k, ks, v, vs, T, Hq, gq, gk, eps, table, rot, inter, pos, axes,
+                                 cache() if c is None else c, slots, out, os, None)
+
+
+BAD_CACHES = [
+    (dict(k=None), -1), (dict(v=None), -1), (dict(k=A8), -3), (dict(v=A8), -3), (dict(type=0), -1), (dict(type=4), -1),
+    (dict(D=96), -2), (dict(D=0), -2), (dict(page=8), -2), (dict(page=48), -2), (dict(page=512), -2),
+    (dict(page=0), -2), (dict(Hk=0), -2), (dict(Hk=1025), -2), (dict(pages=0), -2), (dict(pages=2 ** 31 - 1), -2),
+    (dict(ks=0.0), -1), (dict(vs=-1.0), -1), (dict(ks=math.nan), -1), (dict(vs=math.inf), -1)]
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_head_norm_rope_refuses_caches(lib, bad, status):
+    assert norm_rope(lib, c=cache(**bad)) == status
+    assert lib.zq_last_error()
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(q=None), -1), (dict(q=A8), -3), (dict(qs=508), -2), (dict(qs=514), -2), (dict(k=None), -1),
+    (dict(ks=252), -2), (dict(v=A8), -3), (dict(vs=0), -2), (dict(vs=-256), -2), (dict(T=0), -2), (dict(T=-1), -2),
+    (dict(T=2 ** 30), -2), (dict(Hq=0), -2), (dict(eps=-1.0), -1), (dict(eps=math.nan), -1), (dict(rot=8), -2),
+    (dict(rot=144), -2), (dict(rot=-16), -2), (dict(axes=0), -2), (dict(axes=4), -2), (dict(table=None), -1),
+    (dict(pos=None), -1), (dict(slots=None), -1), (dict(gq=A8), -3), (dict(slots=A8), -3), (dict(out=None), -1),
+    (dict(out=A8), -3), (dict(os=4), -2), (dict(out=A16, os=516), -1)])
+def test_head_norm_rope_refuses(lib, bad, status):
+    assert norm_rope(lib, **bad) == status
+    assert lib.zq_last_error()
+
+
+def test_valid_head_norm_rope_without_gpu(lib):
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert norm_rope(lib) == -5
+    assert norm_rope(lib, gq=None, gk=None, table=None, rot=0, pos=None) == -5
+    assert norm_rope(lib, out=A16) == -5          # in place
+
+
+def test_null_cache_is_refused(lib):
+    assert lib.zq_head_norm_rope(A16, 512, A16, 256, A16, 256, 3, 4, None, None, 0.0, None, 0, 0, None, 1, None, A16,
+                                 A16, 512, None) == -1
+
+
+def test_rope_table_values(lib):
+    """Each entry is inv_freq / 2 pi as a fraction of 2^64 to the nearest multiple of four, plus the axis."""
+    freq = np.array([0.0, 1.0, -1.0, 2 * math.pi * 0.25, 1e-9, 7.5, 2 * math.pi])
+    axis = [0, 1, 2, 0, 1, 2, 0]
+    out = np.zeros(len(freq), np.uint64)
+    ax = (ctypes.c_int * len(axis))(*axis)
+    assert lib.zq_rope_table(freq.ctypes.data, ctypes.addressof(ax), len(freq), out.ctypes.data) == 0
+    for f, a, e in zip(freq, axis, out):
+        e = int(e)
+        assert e & 3 == a
+        turns = f / (2 * math.pi) % 1.0
+        off = ((e & ~3) - int(turns * 2 ** 64) + 2 ** 63) % 2 ** 64 - 2 ** 63
+        assert abs(off) <= 2 ** 64 * 2.0 ** -52 * max(1.0, abs(f) / (2 * math.pi))
+
+
+def test_rope_table_refuses(lib):
+    out = np.zeros(2, np.uint64)
+    f = np.array([1.0, 1.0])
+    bad = np.array([1.0, math.inf])
+    ax = (ctypes.c_int * 2)(0, 3)
+    assert lib.zq_rope_table(None, None, 2, out.ctypes.data) == -1
+    assert lib.zq_rope_table(f.ctypes.data, None, 0, out.ctypes.data) == -1
+    assert lib.zq_rope_table(bad.ctypes.data, None, 2, out.ctypes.data) == -1
+    assert lib.zq_rope_table(f.ctypes.data, ctypes.addressof(ax), 2, out.ctypes.data) == -1
+
+
+def test_python_refusals_on_the_host():
+    torch = pytest.importorskip("torch")
+    k = torch.zeros(2, 1, 16, 64, dtype=torch.float16)
+    with pytest.raises(ValueError):
+        zq.KVCache(k, k)                                   # not on a GPU
+    with pytest.raises(ValueError):
+        zq.KVCache(k, k[:1])
+    with pytest.raises(ValueError):
+        zq.KVCache(k.float(), k.float())
+    with pytest.raises(ValueError):
+        zq.rope_table([1.0, 2.0], [0], device="cpu")
