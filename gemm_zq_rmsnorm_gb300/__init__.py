@@ -32,7 +32,8 @@ EXPORTS = ("zq_rmsnorm_q8_1", "zq_q4k_gemv", "zq_q4k_gemv_pair", "zq_q4k_gemm",
            "zq_q5k_gemm", "zq_q6k_gemm", "zq_q5k_gemv", "zq_q6k_gemv", "zq_rmsnorm_q6k_gemv",
            "zq_q5k_bytes", "zq_q6k_bytes", "zq_debug_stream_plan", "zq_debug_peak_probe",
            "zq_debug_wait_expiry", "zq_q8_1_dequant_f16", "zq_f16_gemm_workspace_bytes", "zq_f16_gemm",
-           "zq_rmsnorm_q4k_gemm", "zq_copy", "zq_rope_table", "zq_head_norm_rope")
+           "zq_rmsnorm_q4k_gemm", "zq_copy", "zq_rope_table", "zq_head_norm_rope",
+           "zq_paged_attn_workspace_bytes", "zq_paged_attn")
 
 
 class ZQError(RuntimeError):
@@ -100,6 +101,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "zq_f16_gemm": ([P, i, i, P, i, P, P, sz, P], i),
         "zq_rope_table": ([P, P, i, P], i),
         "zq_head_norm_rope": ([P, ll, P, ll, P, ll, i, i, P, P, f, P, i, i, P, i, P, P, P, ll, P], i),
+        "zq_paged_attn_workspace_bytes": ([i, i, i], sz),
+        "zq_paged_attn": ([P, ll, i, i, P, P, i, P, f, i, P, ll, P, P, P, sz, P], i),
         "zq_rmsnorm_q4k_gemm": ([P, P, f, i, i, P, i, P, ctypes.POINTER(_Q8), P, sz, P], i),
     }
     for name, (args, res) in sig.items():
@@ -490,6 +493,14 @@ def _ints(t: torch.Tensor, n: int, what: str) -> int:
     return t.data_ptr()
 
 
+def _q8_planes(a: Q8_1, B: int, K: int, what: str):
+    """The planes of B tokens x K codes, contiguous."""
+    if not (a.qs.dtype == torch.int8 and a.d.dtype == a.s.dtype == torch.float16 and a.qs.numel() == B * K
+            and a.d.numel() == a.s.numel() == B * (K // 32)
+            and a.qs.is_contiguous() and a.d.is_contiguous() and a.s.is_contiguous()):
+        raise ValueError(f"{what} must be contiguous Q8_1 planes of {B} tokens x {K}")
+
+
 def rope_table(inv_freq, axis=None, device="cuda") -> torch.Tensor:
     """The rotation table of head_norm_rope for the pairs' frequencies (radians
     per position, float64) and position axes (see zq_rope_table)."""
@@ -534,6 +545,48 @@ def head_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma_q, g
                                  table.data_ptr() if rot else None, rot, interleaved, pp, axes, cache._ref,
                                  _ints(slots, T, "head_norm_rope: slots"), op, os_, _stream(stream)))
     return q_out
+
+
+def paged_attn_workspace_bytes(Hq: int, Hk: int, D: int) -> int:
+    return int(load().zq_paged_attn_workspace_bytes(Hq, Hk, D))
+
+
+def paged_attn(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch.Tensor, scale: float | None = None,
+               window: int = 0, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+               q8_out: Q8_1 | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Attention of one new token per sequence, q fp32 [B][Hq][D] (or
+    [B][Hq * D], rows strided), over lens int32 [B] rows of the cache by way of
+    table int32 [B][width] (see zq_paged_attn); scale defaults to 1 / sqrt(D).
+    Returns out (None when only q8_out, the codes of [B][Hq * D], is asked for)."""
+    lib = _lib or load()
+    D, B = cache.D, q.shape[0]
+    qp, qs, Hq = _head_rows(q, B, D, "paged_attn: q")
+    if out is None and q8_out is None:
+        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+    if workspace is None:
+        workspace = torch.empty(lib.zq_paged_attn_workspace_bytes(Hq, cache.Hk, D), dtype=torch.uint8,
+                                device=q.device)
+    _on(cache.index, "paged_attn", q, table, lens, out, lse, workspace)
+    op, os_ = None, 0
+    if out is not None:
+        op, os_, Ho = _head_rows(out, B, D, "paged_attn: out")
+        if Ho != Hq:
+            raise ValueError("paged_attn: out must have q's heads")
+    if table.dim() != 2 or table.shape[0] != B:
+        raise ValueError(f"paged_attn: table must be [{B}][width]")
+    width = table.shape[1]
+    if lse is not None and (lse.dtype != torch.float32 or lse.numel() != B * Hq or not lse.is_contiguous()):
+        raise ValueError(f"paged_attn: lse must be contiguous fp32 [{B}][{Hq}]")
+    q8 = None
+    if q8_out is not None:
+        _on(cache.index, "paged_attn", q8_out.qs, q8_out.d, q8_out.s)
+        _q8_planes(q8_out, B, Hq * D, "paged_attn: q8_out")
+        q8 = ctypes.byref(q8_out._c())
+    _check(lib.zq_paged_attn(qp, qs, B, Hq, cache._ref, _ints(table, B * width, "paged_attn: table"), width,
+                             _ints(lens, B, "paged_attn: lens"), D ** -0.5 if scale is None else scale, window, op, os_,
+                             None if lse is None else lse.data_ptr(), q8, workspace.data_ptr(),
+                             workspace.numel() * workspace.element_size(), _stream(stream)))
+    return out
 
 
 # operations per probe launch, by kind (zq_debug_peak_probe)

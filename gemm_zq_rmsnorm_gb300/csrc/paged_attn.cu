@@ -1,0 +1,853 @@
+// paged_attn.cu -- attention of one new token per sequence over a paged
+// key-value cache, split over the cache's length and joined (MIInfer README,
+// "Status": cached single-query attention).
+//
+//   s_j = scale q.k_j,  o = sum_j exp(s_j) v_j / sum_j exp(s_j),
+// in one pass: each warp keeps the running maximum m, the sum l and the
+// unnormalised output of its tokens; two such pieces of a row join as
+//   m = max(m1, m2), l = l1 2^(m1-m) + l2 2^(m2-m), o alike (base 2).
+//
+// Bound: HBM, 2 D Hk es bytes per token against 4 D Hq operations.  With G =
+// Hq / Hk query heads on a key head the FP32 units would take G times the
+// products' time of one head (at G = 6 about the whole HBM time), so the
+// products run on the tensor cores through mma.sync: keys (16 tokens) are the
+// 16-row operand and the query heads the 8-column one, so G <= 8 heads cost
+// one pass.  (tcgen05 takes 64 or 128 rows from shared memory through a
+// descriptor and returns through tensor memory; at 8 columns the tensor pipe is
+// idle either way, and the warp-level form needs no hand-over between warps.)
+//
+// Work: every (sequence, key head) has ceil(len / 16) tiles of 16 tokens (at
+// least one, so that an empty row is written too); all tiles of the call form
+// one line, cut into equal contiguous ranges for the warps, whatever the
+// lengths.  A warp writes the rows it covers whole; open pieces join
+// in the CTA through shared memory, and those that cross CTAs in a second
+// kernel that reads at most two pieces per CTA, in order: no atomics, the same
+// result every time.
+//
+// Loads: a lane copies (cp.async) exactly the 16-byte chunks that it will feed
+// to its MMAs -- the order of the head's columns in a K-step and of the output
+// rows is free, so the fragment of lane 4g + c is, for keys, 16 bytes of token
+// rows g and g + 8, and for values 16 bytes of rows 2c, 2c + 1, 2c + 8, 2c + 9.
+// Each lane reads back only what it copied, so the ring needs no barrier and no
+// shared-memory transpose, and its accesses are conflict-free.  Rows past
+// the end, before the window or on a page outside the cache are filled
+// with zeros instead of read: whatever the cache holds there (infinities, NaN)
+// never meets a product.
+//
+// Precision: q is split exactly into parts of the cache's 16-bit type (three
+// bf16 parts; two binary16 parts after scaling the row to [1, 2), 2^-22 of its
+// largest value), every product is exact, sums are fp32.  p in [0, 1] goes to
+// the value product as two parts (2^-17 relative in bf16, 2^-22 in binary16);
+// l sums the unrounded p.  e4m3 values are binary16 values.
+#include <math.h>
+
+#include "zq_async.cuh"
+#include "zq_internal.cuh"
+#include "zq_kv.cuh"
+
+namespace zq {
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTile = 16;       // tokens of an MMA
+constexpr int kHeads = 8;       // query heads of a pass: the MMA's columns
+constexpr int kMinTiles = 2;    // tiles a warp takes at least, before more CTAs join in
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr unsigned kAll = 0xffffffffu;
+
+template <int D, int TYPE>
+struct Cfg {
+    static constexpr int kBytes = KvBytes<TYPE>::value;
+    static constexpr int kRow = D * kBytes;             // bytes of a token's head
+    static constexpr int kSlot = kTile * kRow;          // one tile's keys, or values
+    // ring slots of a warp: as many as fit beside nothing else, eight at most
+    static constexpr int kFit = 196608 / (kWarps * kSlot);
+    static constexpr int kSlots = kFit > 8 ? 8 : kFit;
+    static constexpr int kRing = kWarps * kSlot * kSlots;
+    static constexpr int kMerge = kWarps * kHeads * D * 4;   // the warps' open pieces, after the ring is done
+    static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kSplits = TYPE == ZQ_BF16 ? 3 : 2;  // parts of q
+    static constexpr int kKRun = 16 / kBytes;           // columns of a lane's key chunk
+    static constexpr int kVRun = kRow >= 128 ? 16 / kBytes : 8;   // columns of a lane's value chunk
+    static constexpr int kVBytes = kVRun * kBytes;      // 16, or 8 for 64-byte rows
+    static constexpr int kVSegs = D / (8 * kVRun);
+};
+
+// A piece of a row block in the workspace: kHeads rows of D, then m and l.
+__host__ __device__ constexpr size_t piece_floats(int D) { return (size_t)kHeads * D + 2 * kHeads; }
+
+// What a CTA leaves open: `a` continues a row block of an earlier CTA
+// (1: goes on, 2: ends here), `b` one that begins here and goes on.
+struct Meta {
+    int a, b, seq, vh;
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <int TYPE>
+__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                    uint32_t b1)
+{
+    if constexpr (TYPE == ZQ_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// 8 x 8 transpose of 16-bit values across the warp
+__device__ __forceinline__ uint32_t transpose8(uint32_t x)
+{
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+// two e4m3 values to two binary16 values (exact)
+__device__ __forceinline__ uint32_t e4m3_f16(uint32_t pair)
+{
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
+    return r;
+}
+
+// The MMA's 16-bit type: bf16 for a bf16 cache, else binary16.
+template <int TYPE>
+__device__ __forceinline__ uint32_t pack16(float lo, float hi)
+{
+    return kv_pack2<TYPE == ZQ_BF16 ? ZQ_BF16 : ZQ_F16>(lo, hi);
+}
+template <int TYPE>
+__device__ __forceinline__ float2 unpack16(uint32_t w)
+{
+    if constexpr (TYPE == ZQ_BF16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
+}
+
+// cp.async of 8 bytes (16: cp_async16), zeros when src_bytes = 0
+__device__ __forceinline__ void cp_async8(void *dst, const void *src, uint32_t src_bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
+                 : "memory");
+}
+
+// Q8_1 codes of a block of 32 outputs held by lanes that differ in the bits of
+// `group` (shuffle masks), N neighbouring values each: the steps of q8_1_pack.
+// `at` is the block-ordered index of this lane's first value; `first` marks the
+// lane that writes the block's scales.
+template <int N, int M0, int M1, int M2>
+__device__ __forceinline__ void q8_block(const zq_q8_1 &o, size_t at, const float (&v)[N], bool store, bool first)
+{
+    float amax = 0.0f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) amax = fmaxf(amax, fabsf(v[i]));
+    if (M0) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, M0));
+    if (M1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, M1));
+    if (M2) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, M2));
+    const float d = __fdiv_rn(amax, 127.0f);
+    const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+    int sum = 0;
+    uint32_t word[N / 4];
+#pragma unroll
+    for (int w = 0; w < N / 4; ++w) {
+        word[w] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float q = roundf(__fmul_rn(v[4 * w + i], id));
+            q = fminf(fmaxf(q, -127.0f), 127.0f);
+            const int qi = (int)q;
+            sum += qi;
+            word[w] |= (uint32_t)(qi & 0xFF) << (8 * i);
+        }
+    }
+    if (M0) sum += __shfl_xor_sync(kAll, sum, M0);
+    if (M1) sum += __shfl_xor_sync(kAll, sum, M1);
+    if (M2) sum += __shfl_xor_sync(kAll, sum, M2);
+    if (!store) return;
+#pragma unroll
+    for (int w = 0; w < N / 4; ++w) reinterpret_cast<uint32_t *>(o.qs + at)[w] = word[w];
+    if (first) {
+        o.d[at >> 5] = __half_as_ushort(__float2half_rn(d));
+        o.s[at >> 5] = __half_as_ushort(__float2half_rn(__fmul_rn(d, (float)sum)));
+    }
+}
+
+// Factor of a finished row: v_scale / l; an empty row (l = 0) is zeros.
+__device__ __forceinline__ float row_factor(float l, float v_scale) { return l == 0.0f ? 0.0f : __fdiv_rn(v_scale, l); }
+
+__device__ __forceinline__ float row_lse(float m, float l)
+{
+    return l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+__device__ __forceinline__ int seq_len(const PagedAttnArgs &a, int b)
+{
+    return min(max(a.lens[b], 0), a.width << a.page_shift);
+}
+__device__ __forceinline__ int seq_first(const PagedAttnArgs &a, int len)
+{
+    return a.window > 0 && len > a.window ? len - a.window : 0;
+}
+// tiles of a sequence with rows [lo, len): at least one
+__device__ __forceinline__ int seq_tiles(int lo, int len)
+{
+    return max(1, (len + kTile - 1) / kTile - lo / kTile);
+}
+
+// A place on the line of tiles: sequence, pass (key head and group of up to
+// eight of its query heads), tile.
+struct Walk {
+    int b, vh, t, t0, tend, lo, len;
+    __device__ __forceinline__ void sequence(const PagedAttnArgs &a, int seq)
+    {
+        b = seq;
+        len = seq_len(a, seq);
+        lo = seq_first(a, len);
+        t0 = lo / kTile;
+        tend = t0 + seq_tiles(lo, len);
+        t = t0;
+    }
+    // from the end of a row block to the next one
+    __device__ __forceinline__ void next_block(const PagedAttnArgs &a)
+    {
+        t = t0;
+        if (++vh == a.passes * a.Hk) {
+            vh = 0;
+            if (++b < a.B) sequence(a, b);
+        }
+    }
+};
+
+// Query heads of pass vh: the first one, and how many.
+__device__ __forceinline__ int pass_head(const PagedAttnArgs &a, int vh)
+{
+    return vh / a.passes * a.G + vh % a.passes * a.per_pass;
+}
+__device__ __forceinline__ int pass_heads(const PagedAttnArgs &a, int vh)
+{
+    return min(a.per_pass, a.G - vh % a.passes * a.per_pass);
+}
+
+template <int D, int TYPE>
+__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a)
+{
+    using C = Cfg<D, TYPE>;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ long long before_s[kThreads];   // tiles ahead of each thread's sequences
+    __shared__ long long total_s[kWarps];
+    __shared__ int head_s[kWarps];             // an ending piece in the workspace
+    __shared__ Meta open_s[kWarps];            // the warp's last piece (b = 1: begins in the warp, 2: before)
+    __shared__ float m_s[kWarps][kHeads], l_s[kWarps][kHeads];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int vheads = a.passes * a.Hk;
+    pdl_wait();   // queries, cache, table and lengths come from earlier kernels
+    pdl_launch_dependents();
+
+    // ---- the line of tiles: thread t adds up the sequences t * per ..
+    const int per = (a.B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+        const int len = seq_len(a, b);
+        mine += (long long)seq_tiles(seq_first(a, len), len) * vheads;
+    }
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long up = __shfl_up_sync(kAll, incl, off);
+        if (lane >= off) incl += up;
+    }
+    if (lane == 31) total_s[warp] = incl;
+    __syncthreads();
+    long long total = 0, base = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w == warp) base = total;
+        total += total_s[w];
+    }
+    before_s[tid] = base + incl - mine;
+    const long long wanted = (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles);
+    const int ctas = (int)min((long long)gridDim.x, max(1ll, wanted));
+    Meta *meta = reinterpret_cast<Meta *>(a.meta);
+    if (blockIdx.x >= ctas) {
+        if (tid == 0) meta[blockIdx.x] = Meta{0, 0, 0, 0};
+        return;
+    }
+    __syncthreads();
+
+    const long long nw = (long long)ctas * kWarps, gw = (long long)blockIdx.x * kWarps + warp;
+    const long long u0 = gw * total / nw;
+    long long left = (gw + 1) * total / nw - u0;
+
+    Walk at;
+    if (left > 0) {
+        int i = 0;
+#pragma unroll
+        for (int step = kThreads / 2; step >= 1; step >>= 1)
+            if (before_s[i + step] <= u0 && (i + step) * per < a.B) i += step;
+        long long rem = u0 - before_s[i];
+        at.sequence(a, i * per);
+        while (rem >= (long long)(at.tend - at.t0) * vheads) {
+            rem -= (long long)(at.tend - at.t0) * vheads;
+            at.sequence(a, at.b + 1);
+        }
+        const int n = at.tend - at.t0;
+        at.vh = (int)(rem / n);
+        at.t = at.t0 + (int)(rem % n);
+    }
+
+    // ---- the ring: items are keys of a tile, then its values
+    uint8_t *ring = smem + (size_t)warp * C::kSlots * C::kSlot;
+    Walk ld = at;
+    long long ld_left = left;
+    int ld_item = 0;        // 0: keys next, 1: values
+    int ld_slot = 0;
+    uint32_t page_ok = 0;   // bit of a slot: its tile's page is in the cache
+    size_t ld_base = 0;
+    bool ld_ok = false;
+    const int page_mask = (1 << a.page_shift) - 1;
+
+    auto issue = [&]() {
+        if (ld_left > 0) {
+            uint8_t *dst = ring + ld_slot * C::kSlot;
+            const int tok = ld.t * kTile;
+            if (ld_item == 0) {
+                const int pid = a.table[(size_t)ld.b * a.width + (tok >> a.page_shift)];
+                ld_ok = (unsigned)pid < (unsigned)a.pages;
+                ld_base = ld_ok ? ((((size_t)pid * a.Hk + ld.vh / a.passes) << a.page_shift) + (tok & page_mask)) *
+                                      C::kRow
+                                : 0;
+                page_ok = (page_ok & ~(1u << ld_slot)) | (uint32_t)ld_ok << ld_slot;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = g + 8 * h;
+                    const bool in = ld_ok && tok + row >= ld.lo && tok + row < ld.len;
+                    const char *src = a.k + (in ? ld_base + (size_t)row * C::kRow + 16 * c : 0);
+#pragma unroll
+                    for (int s = 0; s < C::kRow / 64; ++s)
+                        cp_async16(dst + (2 * s + h) * 512 + lane * 16, src + 64 * s, in ? 16 : 0);
+                }
+                ld_item = 1;
+            } else {
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                    const bool in = ld_ok && tok + row >= ld.lo && tok + row < ld.len;
+                    const char *src = a.v + (in ? ld_base + (size_t)row * C::kRow + C::kVBytes * g : 0);
+#pragma unroll
+                    for (int s = 0; s < C::kVSegs; ++s) {
+                        uint8_t *to = dst + (4 * s + r) * (32 * C::kVBytes) + lane * C::kVBytes;
+                        if constexpr (C::kVBytes == 16) cp_async16(to, src + 128 * s, in ? 16 : 0);
+                        else cp_async8(to, src, in ? 8 : 0);
+                    }
+                }
+                ld_item = 0;
+                --ld_left;
+                if (++ld.t == ld.tend) ld.next_block(a);
+            }
+        }
+        cp_async_commit();
+        if (++ld_slot == C::kSlots) ld_slot = 0;
+    };
+#pragma unroll 1
+    for (int i = 0; i < C::kSlots; ++i) issue();
+
+    int slot = 0;
+    float o[D / 16][4];
+    float m0 = 0, m1 = 0, l0 = 0, l1 = 0;
+    int has_head = 0;
+    Meta open{0, 0, 0, 0};
+    float *head_piece = a.pieces + (size_t)(2 * gridDim.x + gw) * piece_floats(D);
+
+    while (left > 0) {
+        const int n = (int)min(left, (long long)(at.tend - at.t));
+        const bool starts = at.t == at.t0, ends = at.t + n == at.tend;
+        const int heads = pass_heads(a, at.vh), head0 = pass_head(a, at.vh);
+
+        // queries of head g, in the columns' order of the key chunks
+        uint32_t qf[C::kSplits][D / 16][2];
+        float scale0, scale1;
+        {
+            float x[D / 4];
+            const float *qr = a.q + (long long)at.b * a.q_stride + (long long)(head0 + min(g, heads - 1)) * D;
+#pragma unroll
+            for (int s = 0; s < D / (4 * C::kKRun); ++s)
+#pragma unroll
+                for (int i = 0; i < C::kKRun / 4; ++i) {
+                    const float4 f = *reinterpret_cast<const float4 *>(qr + (4 * s + c) * C::kKRun + 4 * i);
+                    float *y = x + s * C::kKRun + 4 * i;
+                    y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
+                }
+            float back = 1.0f;
+            if constexpr (TYPE != ZQ_BF16) {
+                float amax = 0.0f;
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) amax = fmaxf(amax, fabsf(x[i]));
+                amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 1));
+                amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, 2));
+                const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
+                const float down = __int_as_float((127 - e) << 23);
+                back = __int_as_float((127 + e) << 23);
+#pragma unroll
+                for (int i = 0; i < D / 4; ++i) x[i] *= down;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+                float lo = x[2 * i], hi = x[2 * i + 1];
+#pragma unroll
+                for (int p = 0; p < C::kSplits; ++p) {
+                    const uint32_t w = pack16<TYPE>(lo, hi);
+                    qf[p][i / 2][i % 2] = w;
+                    const float2 f = unpack16<TYPE>(w);
+                    lo -= f.x;
+                    hi -= f.y;
+                }
+            }
+            scale0 = a.qk_scale * __shfl_sync(kAll, back, 8 * c);
+            scale1 = a.qk_scale * __shfl_sync(kAll, back, 8 * c + 4);
+        }
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.0f;
+
+#pragma unroll 1
+        for (int i = 0; i < n; ++i) {
+            // scores: S^T [16 tokens x 8 heads], two accumulators per part of q
+            cp_async_wait<C::kSlots - 1>();
+            const uint8_t *src = ring + slot * C::kSlot;
+            float acc[2 * C::kSplits][4] = {};
+#pragma unroll
+            for (int s = 0; s < C::kRow / 64; ++s) {
+                const uint4 ra = *reinterpret_cast<const uint4 *>(src + (2 * s) * 512 + lane * 16);
+                const uint4 rb = *reinterpret_cast<const uint4 *>(src + (2 * s + 1) * 512 + lane * 16);
+                const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+                if constexpr (TYPE == ZQ_E4M3) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int p = 0; p < C::kSplits; ++p)
+                            mma<TYPE>(acc[2 * p + (j & 1)], e4m3_f16(wa[j]), e4m3_f16(wb[j]), e4m3_f16(wa[j] >> 16),
+                                      e4m3_f16(wb[j] >> 16), qf[p][4 * s + j][0], qf[p][4 * s + j][1]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int p = 0; p < C::kSplits; ++p)
+                            mma<TYPE>(acc[2 * p + j], wa[2 * j], wb[2 * j], wa[2 * j + 1], wb[2 * j + 1],
+                                      qf[p][2 * s + j][0], qf[p][2 * s + j][1]);
+                }
+            }
+            const bool ok = page_ok >> slot & 1;
+            issue();
+            if (++slot == C::kSlots) slot = 0;
+            float sc[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {   // the small parts first
+                float v = acc[2 * C::kSplits - 2][e] + acc[2 * C::kSplits - 1][e];
+#pragma unroll
+                for (int p = C::kSplits - 2; p >= 0; --p) v += acc[2 * p][e] + acc[2 * p + 1][e];
+                sc[e] = v * (e & 1 ? scale1 : scale0);
+            }
+            const int tok = (at.t + i) * kTile + g;
+            const bool in0 = ok && tok >= at.lo && tok < at.len, in1 = ok && tok + 8 >= at.lo && tok + 8 < at.len;
+
+            // running maximum over the tile's tokens, per head (columns 2c, 2c + 1)
+            float x0 = fmaxf(in0 ? sc[0] : -INFINITY, in1 ? sc[2] : -INFINITY);
+            float x1 = fmaxf(in0 ? sc[1] : -INFINITY, in1 ? sc[3] : -INFINITY);
+#pragma unroll
+            for (int off = 4; off <= 16; off <<= 1) {
+                x0 = fmaxf(x0, __shfl_xor_sync(kAll, x0, off));
+                x1 = fmaxf(x1, __shfl_xor_sync(kAll, x1, off));
+            }
+            x0 = fmaxf(x0, m0);
+            x1 = fmaxf(x1, m1);
+            // nothing seen yet: subtract 0, not the -infinity
+            const float u0m = x0 == -INFINITY ? 0.0f : x0, u1m = x1 == -INFINITY ? 0.0f : x1;
+            if (__any_sync(kAll, x0 != m0 || x1 != m1)) {
+                const float f0 = ex2(m0 - u0m), f1 = ex2(m1 - u1m);
+                l0 *= f0;
+                l1 *= f1;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k) {
+                    o[k][0] *= f0;
+                    o[k][1] *= f1;
+                    o[k][2] *= f0;
+                    o[k][3] *= f1;
+                }
+                m0 = x0;
+                m1 = x1;
+            }
+            const float p0 = in0 ? ex2(sc[0] - u0m) : 0.0f, p1 = in0 ? ex2(sc[1] - u1m) : 0.0f;
+            const float p2 = in1 ? ex2(sc[2] - u0m) : 0.0f, p3 = in1 ? ex2(sc[3] - u1m) : 0.0f;
+            l0 += p0 + p2;
+            l1 += p1 + p3;
+            const uint32_t h0 = pack16<TYPE>(p0, p1), h1 = pack16<TYPE>(p2, p3);
+            const float2 r0 = unpack16<TYPE>(h0), r1 = unpack16<TYPE>(h1);
+            const uint32_t bh0 = transpose8(h0), bh1 = transpose8(h1);
+            const uint32_t bl0 = transpose8(pack16<TYPE>(p0 - r0.x, p1 - r0.y));
+            const uint32_t bl1 = transpose8(pack16<TYPE>(p2 - r1.x, p3 - r1.y));
+
+            // O^T [16 columns x 8 heads] += V^T p: rows g and g + 8 of a product are two neighbouring columns
+            cp_async_wait<C::kSlots - 1>();
+            src = ring + slot * C::kSlot;
+#pragma unroll
+            for (int s = 0; s < C::kVSegs; ++s) {
+                uint32_t w[4][C::kVBytes / 4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const uint8_t *from = src + (4 * s + r) * (32 * C::kVBytes) + lane * C::kVBytes;
+                    if constexpr (C::kVBytes == 16) {
+                        const uint4 f = *reinterpret_cast<const uint4 *>(from);
+                        w[r][0] = f.x, w[r][1] = f.y, w[r][2] = f.z, w[r][3] = f.w;
+                    } else {
+                        const uint2 f = *reinterpret_cast<const uint2 *>(from);
+                        w[r][0] = f.x, w[r][1] = f.y;
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < C::kVRun / 2; ++j) {
+                    uint32_t t[4];   // the four tokens' values of this pair of columns
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        if constexpr (TYPE == ZQ_E4M3) t[r] = e4m3_f16(w[r][j / 2] >> (16 * (j & 1)));
+                        else t[r] = w[r][j];
+                    }
+                    const uint32_t a0 = __byte_perm(t[0], t[1], 0x5410), a1 = __byte_perm(t[0], t[1], 0x7632);
+                    const uint32_t a2 = __byte_perm(t[2], t[3], 0x5410), a3 = __byte_perm(t[2], t[3], 0x7632);
+                    float(&to)[4] = o[s * (C::kVRun / 2) + j];
+                    mma<TYPE>(to, a0, a1, a2, a3, bh0, bh1);
+                    mma<TYPE>(to, a0, a1, a2, a3, bl0, bl1);
+                }
+            }
+            issue();
+            if (++slot == C::kSlots) slot = 0;
+        }
+#pragma unroll
+        for (int off = 4; off <= 16; off <<= 1) {
+            l0 += __shfl_xor_sync(kAll, l0, off);
+            l1 += __shfl_xor_sync(kAll, l1, off);
+        }
+        left -= n;
+
+        if (starts && ends) {   // the whole row block: finish it
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = 2 * c + e;
+                const bool store = h < heads;
+                const float l = e ? l1 : l0, f = row_factor(l, a.v_scale);
+                const long long row = (long long)at.b * a.out_stride + (long long)(head0 + h) * D;
+#pragma unroll
+                for (int s = 0; s < C::kVSegs; ++s) {
+                    float y[C::kVRun];
+#pragma unroll
+                    for (int j = 0; j < C::kVRun / 2; ++j) {
+                        y[2 * j] = o[s * (C::kVRun / 2) + j][e] * f;
+                        y[2 * j + 1] = o[s * (C::kVRun / 2) + j][2 + e] * f;
+                    }
+                    const int d0 = (8 * s + g) * C::kVRun;
+                    if (store && a.out) {
+#pragma unroll
+                        for (int q = 0; q < C::kVRun / 4; ++q)
+                            reinterpret_cast<float4 *>(a.out + row + d0)[q] =
+                                make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+                    }
+                    if (a.q8.qs) {
+                        const size_t to = ((size_t)at.b * a.Hq + head0 + h) * D + d0;
+                        q8_block<C::kVRun, 4, C::kVRun == 8 ? 8 : 0, 0>(a.q8, to, y, store,
+                                                                       (d0 & 31) == 0);
+                    }
+                }
+                if (store && a.lse && g == 0) a.lse[(size_t)at.b * a.Hq + head0 + h] = row_lse(e ? m1 : m0, l);
+            }
+            at.t += n;
+            at.next_block(a);
+        } else if (ends) {      // began in an earlier warp: to the workspace
+            has_head = 1;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int h = 2 * c + e;
+#pragma unroll
+                for (int s = 0; s < C::kVSegs; ++s)
+#pragma unroll
+                    for (int j = 0; j < C::kVRun / 2; ++j)
+                        *reinterpret_cast<float2 *>(head_piece + h * D + (8 * s + g) * C::kVRun + 2 * j) =
+                            make_float2(o[s * (C::kVRun / 2) + j][e], o[s * (C::kVRun / 2) + j][2 + e]);
+                if (g == 0) {
+                    head_piece[kHeads * D + h] = e ? m1 : m0;
+                    head_piece[kHeads * D + kHeads + h] = e ? l1 : l0;
+                }
+            }
+            at.t += n;
+            at.next_block(a);
+        } else {                // goes on in the next warp: the last one here
+            open = Meta{0, starts ? 1 : 2, at.b, at.vh};
+        }
+    }
+    cp_async_wait<0>();
+    __syncthreads();   // every warp's ring is done: its place holds the open pieces now
+    float *pieces_s = reinterpret_cast<float *>(smem);
+    if (open.b) {
+        float *to = pieces_s + (size_t)warp * kHeads * D;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int h = 2 * c + e;
+#pragma unroll
+            for (int s = 0; s < C::kVSegs; ++s)
+#pragma unroll
+                for (int j = 0; j < C::kVRun / 2; ++j)
+                    *reinterpret_cast<float2 *>(to + h * D + (8 * s + g) * C::kVRun + 2 * j) =
+                        make_float2(o[s * (C::kVRun / 2) + j][e], o[s * (C::kVRun / 2) + j][2 + e]);
+            if (g == 0) {
+                m_s[warp][h] = e ? m1 : m0;
+                l_s[warp][h] = e ? l1 : l0;
+            }
+        }
+    }
+    if (lane == 0) {
+        head_s[warp] = has_head;
+        open_s[warp] = open;
+    }
+    __syncthreads();
+
+    // ---- join the CTA's pieces: a run is the open pieces of warps w0 .. w1 - 1
+    // and, when it ends here, the ending piece of warp w1
+    auto join = [&](int w0, int w1, bool begins, bool finishes, int seq, int vh) {
+        const int heads = begins ? pass_heads(a, vh) : kHeads, head0 = begins ? pass_head(a, vh) : 0;
+        const float *tail = a.pieces + (size_t)(2 * gridDim.x + (size_t)blockIdx.x * kWarps + w1) * piece_floats(D);
+        float *to = a.pieces + (size_t)(2 * blockIdx.x + (begins ? 1 : 0)) * piece_floats(D);
+        const int items = heads * (D / 4);
+        for (int i = tid; i < (items + 31) / 32 * 32; i += kThreads) {
+            const bool store = i < items;
+            const int h = store ? i / (D / 4) : 0, d = i % (D / 4) * 4;
+            float m = -INFINITY;
+            for (int w = w0; w < w1; ++w)   // a call of fewer tiles than warps leaves some without any
+                if (open_s[w].b) m = fmaxf(m, m_s[w][h]);
+            if (finishes) m = fmaxf(m, tail[kHeads * D + h]);
+            const float u = m == -INFINITY ? 0.0f : m;
+            float l = 0.0f;
+            float y[4] = {};
+            for (int w = w0; w < w1 + (finishes ? 1 : 0); ++w) {
+                const bool last = w == w1;
+                if (!last && !open_s[w].b) continue;
+                const float f = ex2((last ? tail[kHeads * D + h] : m_s[w][h]) - u);
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    (last ? tail : pieces_s + (size_t)w * kHeads * D) + h * D + d);
+                l += f * (last ? tail[kHeads * D + kHeads + h] : l_s[w][h]);
+                y[0] += f * v.x;
+                y[1] += f * v.y;
+                y[2] += f * v.z;
+                y[3] += f * v.w;
+            }
+            if (begins && finishes) {
+                const float f = row_factor(l, a.v_scale);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) y[e] *= f;
+                if (store && a.out)
+                    *reinterpret_cast<float4 *>(a.out + (long long)seq * a.out_stride + (long long)(head0 + h) * D +
+                                                d) = make_float4(y[0], y[1], y[2], y[3]);
+                if (a.q8.qs)
+                    q8_block<4, 1, 2, 4>(a.q8, ((size_t)seq * a.Hq + head0 + h) * D + d, y, store, (d & 31) == 0);
+                if (store && a.lse && d == 0) a.lse[(size_t)seq * a.Hq + head0 + h] = row_lse(m, l);
+            } else if (store) {
+                *reinterpret_cast<float4 *>(to + h * D + d) = make_float4(y[0], y[1], y[2], y[3]);
+                if (d == 0) {
+                    to[kHeads * D + h] = m;
+                    to[kHeads * D + kHeads + h] = l;
+                }
+            }
+        }
+    };
+    int run = 0;               // first warp of the run at hand
+    bool running = false, begins = false;
+    Meta info{0, 0, 0, 0};     // what this CTA leaves to the second kernel
+    int seq = 0, vh = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (head_s[w]) {
+            join(running ? run : w, w, running && begins, true, seq, vh);
+            if (!(running && begins)) info.a = 2;
+            running = false;
+        }
+        if (open_s[w].b) {
+            if (!running) {
+                running = true;
+                run = w;
+                begins = open_s[w].b == 1;
+                seq = open_s[w].seq;
+                vh = open_s[w].vh;
+            }
+        }
+    }
+    if (running) {
+        join(run, kWarps, begins, false, seq, vh);
+        if (begins) info.b = 1, info.seq = seq, info.vh = vh;
+        else info.a = 1;
+    }
+    if (tid == 0) meta[blockIdx.x] = info;
+}
+
+// Row blocks that cross CTAs: block (c, h) joins head h of the one that begins
+// in CTA c of the first kernel, from that CTA's piece and those of the CTAs
+// that follow, to the one where it ends.
+template <int D>
+__global__ void __launch_bounds__(kThreads) paged_attn_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas)
+{
+    __shared__ float w_s[kMaxAttnCtas];
+    __shared__ float red_s[kWarps];
+    __shared__ int end_s[kWarps];
+    __shared__ float4 part_s[kThreads];
+    pdl_wait();
+    pdl_launch_dependents();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, first = blockIdx.x, h = blockIdx.y;
+    const Meta *meta = reinterpret_cast<const Meta *>(a.meta);
+    const Meta mine = meta[first];
+    if (!mine.b || h >= pass_heads(a, mine.vh)) return;
+
+    int end = ctas;
+    for (int i = first + 1 + tid; i < ctas; i += kThreads)
+        if (meta[i].a == 2) {
+            end = i;
+            break;
+        }
+    end = __reduce_min_sync(kAll, end);
+    if (lane == 0) end_s[warp] = end;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) end = min(end, end_s[w]);
+    const int n = min(end, ctas - 1) - first + 1;
+
+    // piece i: the beginning in its CTA's second place, the others in their first
+    auto piece = [&](int i) { return a.pieces + (size_t)(2 * (first + i) + (i == 0)) * piece_floats(D); };
+    float m = -INFINITY;
+    for (int i = tid; i < n; i += kThreads) m = fmaxf(m, piece(i)[kHeads * D + h]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
+    if (lane == 0) red_s[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) m = fmaxf(m, red_s[w]);
+    const float u = m == -INFINITY ? 0.0f : m;
+    float l = 0.0f;
+    for (int i = tid; i < n; i += kThreads) {
+        const float f = ex2(piece(i)[kHeads * D + h] - u);
+        w_s[i] = f;
+        l += f * piece(i)[kHeads * D + kHeads + h];
+    }
+    l = warp_sum(l);
+    __syncthreads();
+    if (lane == 0) red_s[warp] = l;
+    __syncthreads();
+    l = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) l += red_s[w];
+
+    constexpr int kCols = D / 4, kGroups = kThreads / kCols;
+    const int d4 = tid % kCols, grp = tid / kCols;
+    float4 y = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    for (int i = grp; i < n; i += kGroups) {
+        const float f = w_s[i];
+        const float4 v = *reinterpret_cast<const float4 *>(piece(i) + h * D + 4 * d4);
+        y.x += f * v.x;
+        y.y += f * v.y;
+        y.z += f * v.z;
+        y.w += f * v.w;
+    }
+    part_s[tid] = y;
+    __syncthreads();
+    if (tid >= (kCols < 32 ? 32 : kCols)) return;   // whole warps stay for the block's shuffles
+    const bool store = tid < kCols;
+    const int col = tid % kCols;
+    float v[4] = {};
+    for (int i = 0; i < kGroups; ++i) {
+        const float4 f = part_s[i * kCols + col];
+        v[0] += f.x;
+        v[1] += f.y;
+        v[2] += f.z;
+        v[3] += f.w;
+    }
+    const float f = row_factor(l, a.v_scale);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] *= f;
+    const int head = pass_head(a, mine.vh) + h;
+    if (store && a.out)
+        *reinterpret_cast<float4 *>(a.out + (long long)mine.seq * a.out_stride + (long long)head * D + 4 * col) =
+            make_float4(v[0], v[1], v[2], v[3]);
+    if (a.q8.qs)
+        q8_block<4, 1, 2, 4>(a.q8, ((size_t)mine.seq * a.Hq + head) * D + 4 * col, v, store, (col & 7) == 0);
+    if (tid == 0 && a.lse) a.lse[(size_t)mine.seq * a.Hq + head] = row_lse(m, l);
+}
+
+template <int D, int TYPE>
+cudaError_t launch_one(const PagedAttnArgs &a, int ctas, cudaStream_t st)
+{
+    using C = Cfg<D, TYPE>;
+    static bool set[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!set[dev]) {
+        e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+        if (e != cudaSuccess) return e;
+        set[dev] = true;
+    }
+    e = launch_pdl(paged_attn_kernel<D, TYPE>, dim3(ctas), dim3(kThreads), C::kSmem, st, a);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(paged_attn_join_kernel<D>, dim3(ctas, a.per_pass), dim3(kThreads), 0, st, a, ctas);
+}
+
+template <int D>
+cudaError_t launch_type(const PagedAttnArgs &a, int type, int ctas, cudaStream_t st)
+{
+    switch (type) {
+    case ZQ_F16: return launch_one<D, ZQ_F16>(a, ctas, st);
+    case ZQ_BF16: return launch_one<D, ZQ_BF16>(a, ctas, st);
+    default: return launch_one<D, ZQ_E4M3>(a, ctas, st);
+    }
+}
+
+int attn_ctas()
+{
+    const int n = num_sms();
+    return n < kMaxAttnCtas ? n : kMaxAttnCtas;
+}
+
+size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+}  // namespace
+
+// Pieces: two per CTA, one per warp; then the CTAs' records.
+size_t paged_attn_workspace(int D)
+{
+    const size_t n = (size_t)attn_ctas();
+    return pad256(n * (2 + kWarps) * piece_floats(D) * sizeof(float)) + pad256(n * sizeof(Meta));
+}
+
+cudaError_t launch_paged_attn(const PagedAttnArgs &args, int D, int type, void *workspace, cudaStream_t st)
+{
+    PagedAttnArgs a = args;
+    const int ctas = attn_ctas();
+    a.G = a.Hq / a.Hk;
+    a.passes = (a.G + kHeads - 1) / kHeads;
+    a.per_pass = (a.G + a.passes - 1) / a.passes;
+    a.pieces = static_cast<float *>(workspace);
+    a.meta = static_cast<char *>(workspace) + pad256((size_t)ctas * (2 + kWarps) * piece_floats(D) * sizeof(float));
+    switch (D) {
+    case 64: return launch_type<64>(a, type, ctas, st);
+    case 128: return launch_type<128>(a, type, ctas, st);
+    default: return launch_type<256>(a, type, ctas, st);
+    }
+}
+
+}  // namespace zq

@@ -787,4 +787,63 @@ int zq_head_norm_rope(const float *q, long long q_stride, const float *k, long l
     return launched(launch_head_norm_rope(a, D, cache->type, (cudaStream_t)stream), name);
 }
 
+size_t zq_paged_attn_workspace_bytes(int Hq, int Hk, int D)
+{
+    if (Hq < 1 || Hk < 1 || Hq % Hk || (D != 64 && D != 128 && D != 256)) return 0;
+    return paged_attn_workspace(D);
+}
+
+int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, const zq_kv_cache *cache, const int32_t *table,
+                  int width, const int32_t *lens, float scale, int window, float *out, long long out_stride, float *lse,
+                  const zq_q8_1 *q8_out, void *workspace, size_t workspace_bytes, void *stream)
+{
+    static const char *name = "zq_paged_attn";
+    int st = check_cache(cache, name);
+    if (st) return st;
+    const int D = cache->D, Hk = cache->Hk;
+    if (B < 1 || B > 65535) return fail(ZQ_ERR_SHAPE, "%s: B = %d out of range", name, B);
+    if (Hq < Hk || Hq % Hk || Hq / Hk > 64)
+        return fail(ZQ_ERR_SHAPE, "%s: Hq = %d must be 1 to 64 times Hk = %d", name, Hq, Hk);
+    if (width < 1 || (long long)width * cache->page > INT32_MAX || (long long)B * Hk * width >= 1LL << 40)
+        return fail(ZQ_ERR_SHAPE, "%s: width = %d out of range", name, width);
+    if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(ZQ_ERR_ARG, "%s: scale must be positive and finite", name);
+    if (window < 0) return fail(ZQ_ERR_ARG, "%s: window must be >= 0", name);
+    if ((st = check_rows(q, q_stride, (long long)Hq * D, name, "q"))) return st;
+    if (!out && !q8_out) return fail(ZQ_ERR_ARG, "%s: neither out nor q8_out", name);
+    if (out && (st = check_rows(out, out_stride, (long long)Hq * D, name, "out"))) return st;
+    if (out == q) return fail(ZQ_ERR_ARG, "%s: out must not be q", name);
+    if (q8_out && (st = check_q8(*q8_out, "zq_paged_attn (q8_out)"))) return st;
+    if (!table || !lens) return fail(ZQ_ERR_ARG, "%s: null table or lens", name);
+    if (!aligned16(table) || !aligned16(lens) || !aligned16(lse))
+        return fail(ZQ_ERR_ALIGN, "%s: table, lens and lse must be 16-byte aligned", name);
+    int dev;
+    if ((st = check_device(&dev))) return st;
+    const size_t need = paged_attn_workspace(D);
+    if (!workspace || workspace_bytes < need)
+        return fail(ZQ_ERR_WORKSPACE, "%s: workspace of %zu bytes required", name, need);
+    if (reinterpret_cast<uintptr_t>(workspace) & 255)
+        return fail(ZQ_ERR_ALIGN, "%s: the workspace must be 256-byte aligned", name);
+    PagedAttnArgs a{};
+    a.q = q;
+    a.q_stride = q_stride;
+    a.B = B;
+    a.Hq = Hq;
+    a.Hk = Hk;
+    a.k = static_cast<const char *>(cache->k);
+    a.v = static_cast<const char *>(cache->v);
+    a.pages = cache->pages;
+    a.page_shift = page_shift(cache->page);
+    a.table = table;
+    a.width = width;
+    a.lens = lens;
+    a.window = window;
+    a.qk_scale = (float)((double)scale * cache->k_scale * 1.4426950408889634);
+    a.v_scale = cache->v_scale;
+    a.out = out;
+    a.out_stride = out_stride;
+    a.lse = lse;
+    if (q8_out) a.q8 = *q8_out;
+    return launched(launch_paged_attn(a, D, cache->type, workspace, (cudaStream_t)stream), name);
+}
+
 }  // extern "C"

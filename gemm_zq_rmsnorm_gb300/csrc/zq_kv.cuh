@@ -66,4 +66,29 @@ struct HeadNormRopeArgs {
 };
 cudaError_t launch_head_norm_rope(const HeadNormRopeArgs &a, int D, int type, cudaStream_t st);
 
+constexpr int kMaxAttnCtas = 512;   // more SMs than any GPU of this architecture has
+struct PagedAttnArgs {
+    const float *q;
+    long long q_stride;
+    int B, Hq, Hk;
+    const char *k, *v;
+    int pages, page_shift;
+    const int32_t *table;
+    int width;
+    const int32_t *lens;
+    int window;
+    float qk_scale;   // scale * k_scale * log2 e
+    float v_scale;
+    float *out;       // may be null
+    long long out_stride;
+    float *lse;       // may be null
+    zq_q8_1 q8;       // qs may be null
+    // set by the launcher
+    int G, passes, per_pass;   // query heads of a key head, in passes of up to eight
+    float *pieces;
+    void *meta;
+};
+size_t paged_attn_workspace(int D);
+cudaError_t launch_paged_attn(const PagedAttnArgs &a, int D, int type, void *workspace, cudaStream_t st);
+
 }  // namespace zq

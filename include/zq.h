@@ -512,6 +512,42 @@ ZQ_API int zq_head_norm_rope(const float *q, long long q_stride, const float *k,
                              const int32_t *pos, int axes, const zq_kv_cache *cache, const int32_t *slots,
                              float *q_out, long long q_out_stride, void *stream);
 
+/*
+ * Attention of one new token per sequence over the paged cache (MIInfer
+ * README, "Status": cached single-query attention), split over the length of
+ * every sequence and joined.  For sequence b, query head h and n =
+ * lens[b], over the rows j in [max(0, n - window), n) (window = 0: all n):
+ *   s_j = scale * (q . k_j),  out = sum_j exp(s_j) v_j / sum_j exp(s_j),
+ *   lse = log sum_j exp(s_j);
+ * key head h / (Hq / Hk).  Row j is row j % page of page
+ * table[b * width + j / page].  A row on a page outside the cache is left out
+ * as if masked; a sequence without rows (n <= 0, or all left out) has out = 0
+ * and lse = -infinity.  Nothing outside the rows is read, whatever it
+ * holds; table entries past a sequence's last page may hold anything.
+ *   q     : fp32, head h of sequence b at q + b * q_stride + h * D;
+ *   table : int32 [B][width]; lens : int32 [B], the new token counted, cut to
+ *           width * page;
+ *   scale : positive and finite (1 / sqrt(D) is usual);  window >= 0;
+ *   out   : fp32 as q with out_stride; may be NULL when q8_out is given; may
+ *           not be q;
+ *   lse   : fp32 [B][Hq], may be NULL;
+ *   q8_out : planes of B x (Hq D) codes of out, packed as zq_rmsnorm_q8_1
+ *           packs xh: the o projection's input; may be NULL;
+ *   workspace : zq_paged_attn_workspace_bytes(Hq, Hk, D) bytes, 256-byte
+ *           aligned; contents do not matter.  Calls that may run at the same
+ *           time (other streams, captured graphs) need workspaces of their own.
+ * q is not rounded: products with the cache's values are exact (an f16 or e4m3
+ * cache takes q to 2^-22 of its row's largest value), sums fp32.  The result
+ * does not change from one call to the next.
+ * Shapes: Hq a multiple of Hk, Hq / Hk <= 64, 1 <= B <= 65535, width >= 1,
+ * width * page < 2^31, B * Hk * width < 2^40.  strides multiples of 4.
+ */
+ZQ_API size_t zq_paged_attn_workspace_bytes(int Hq, int Hk, int D);
+ZQ_API int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, const zq_kv_cache *cache,
+                         const int32_t *table, int width, const int32_t *lens, float scale, int window, float *out,
+                         long long out_stride, float *lse, const zq_q8_1 *q8_out, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

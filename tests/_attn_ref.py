@@ -46,3 +46,16 @@ def attn(q, k, v, tokens, scale):
         out[h] = p @ v[tokens, h // G] / p.sum()
         lse[h] = m + np.log(p.sum())
     return out, lse
+
+
+def q8_1(x):
+    """Q8_1 planes (codes, d, s as float16) of fp32 rows [B][K], step by step as the library packs them."""
+    b = x.reshape(x.shape[0], -1, 32)
+    d = np.abs(b).max(-1) / np.float32(127)
+    inv = np.where(d != 0, np.float32(1) / np.where(d != 0, d, np.float32(1)), np.float32(0))
+    v = b * inv[..., None]
+    a = np.abs(v)
+    q = np.floor(a)
+    q = np.minimum(q + (a - q >= 0.5), 127) * np.sign(v)
+    s = d * q.sum(-1).astype(np.float32)
+    return q.astype(np.int8).reshape(x.shape), d.astype(np.float16), s.astype(np.float16)

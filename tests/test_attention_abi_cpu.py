@@ -102,3 +102,43 @@ def test_python_refusals_on_the_host():
         zq.KVCache(k.float(), k.float())
     with pytest.raises(ValueError):
         zq.rope_table([1.0, 2.0], [0], device="cpu")
+
+
+def attn(lib, q=A16, qs=512, B=3, Hq=4, table=A16, width=2, lens=A16, scale=0.1, window=0, out=A16 + 4096, os=512,
+         lse=A16, q8=None, ws=A16, wsb=1 << 30, c=None):
+    return lib.zq_paged_attn(q, qs, B, Hq, cache() if c is None else c, table, width, lens, scale, window, out, os, lse,
+                             q8, ws, wsb, None)
+
+
+@pytest.mark.parametrize("bad,status", BAD_CACHES)
+def test_paged_attn_refuses_caches(lib, bad, status):
+    assert attn(lib, c=cache(**bad)) == status
+    assert lib.zq_last_error()
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(q=None), -1), (dict(q=A8), -3), (dict(qs=500), -2), (dict(qs=513), -2), (dict(B=0), -2), (dict(B=65536), -2),
+    (dict(Hq=0), -2), (dict(Hq=1), -2), (dict(Hq=5, qs=1024, os=1024), -2), (dict(Hq=130, qs=1 << 20, os=1 << 20), -2),
+    (dict(table=None), -1), (dict(table=A8), -3), (dict(width=0), -2), (dict(width=2 ** 31 - 1), -2),
+    (dict(lens=None), -1), (dict(lens=A8), -3), (dict(scale=0.0), -1), (dict(scale=-1.0), -1),
+    (dict(scale=math.inf), -1), (dict(scale=math.nan), -1), (dict(window=-1), -1), (dict(out=None), -1),
+    (dict(out=A8), -3), (dict(os=500), -2), (dict(out=A16), -1), (dict(lse=A8), -3),
+    (dict(q8=ctypes.byref(zq._Q8(A16, A8, A16))), -3), (dict(q8=ctypes.byref(zq._Q8(A16, None, A16))), -1)])
+def test_paged_attn_refuses(lib, bad, status):
+    assert attn(lib, **bad) == status
+    assert lib.zq_last_error()
+
+
+def test_paged_attn_workspace(lib):
+    assert lib.zq_paged_attn_workspace_bytes(4, 3, 128) == 0
+    assert lib.zq_paged_attn_workspace_bytes(4, 2, 96) == 0
+    small, large = (lib.zq_paged_attn_workspace_bytes(4, 2, D) for D in (64, 256))
+    assert 0 < small < large < 64 << 20
+
+
+def test_valid_paged_attn_without_gpu(lib):
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert attn(lib) == -5
+    assert attn(lib, out=None, os=0, q8=ctypes.byref(zq._Q8(A16, A16, A16))) == -5
