@@ -16,7 +16,7 @@
 // descriptor and returns through tensor memory; at 8 columns the tensor pipe is
 // idle either way, and the warp-level form needs no hand-over between warps.)
 //
-// Work: every (sequence, key head) has ceil(len / 16) tiles of 16 tokens (at
+// Work: every (sequence, key head) has ceil(len / 32) tiles of 32 tokens (at
 // least one, so that an empty row is written too); all tiles of the call form
 // one line, cut into equal contiguous ranges for the warps, whatever the
 // lengths.  A warp writes the rows it covers whole; open pieces join
@@ -24,15 +24,17 @@
 // kernel that reads at most two pieces per CTA, in order: no atomics, the same
 // result every time.
 //
-// Loads: a lane copies (cp.async) exactly the 16-byte chunks that it will feed
-// to its MMAs -- the order of the head's columns in a K-step and of the output
-// rows is free, so the fragment of lane 4g + c is, for keys, 16 bytes of token
-// rows g and g + 8, and for values 16 bytes of rows 2c, 2c + 1, 2c + 8, 2c + 9.
-// Each lane reads back only what it copied, so the ring needs no barrier and no
-// shared-memory transpose, and its accesses are conflict-free.  Rows past
-// the end, before the window or on a page outside the cache are filled
-// with zeros instead of read: whatever the cache holds there (infinities, NaN)
-// never meets a product.
+// Loads: one lane of a warp copies the keys, or the values, of 16 tokens of a
+// page by TMA into the warp's own ring, two halves of a tile one after the
+// other.  (With cp.async of 16 bytes a lane the same loop stopped at 4.4 TB/s
+// whatever the depth of the ring.)  The box is [segment of 128 bytes][token],
+// 128-byte swizzled, and the order of the head's columns in a K-step and of
+// the output rows is free: lane 4g + c reads 16-byte chunks 2c and 2c + 1 of
+// the key rows g and g + 8, and chunk g of the value rows 2c, 2c + 1, 2c + 8,
+// 2c + 9, which are fragments as they stand and fall on all banks.
+// Rows past the end, before the window or on a page outside the cache never
+// meet a product: their scores are replaced by -infinity and their value words
+// by zeros, whatever the cache holds there (infinities, NaN).
 //
 // Precision: q is split exactly into parts of the cache's 16-bit type (three
 // bf16 parts; two binary16 parts after scaling the row to [1, 2), 2^-22 of its
@@ -44,13 +46,16 @@
 #include "zq_async.cuh"
 #include "zq_internal.cuh"
 #include "zq_kv.cuh"
+#include "zq_tc.cuh"
+#include "zq_tc_common.cuh"
 
 namespace zq {
 namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kTile = 16;       // tokens of an MMA
+constexpr int kHalf = 16;       // tokens of an MMA
+constexpr int kTile = 32;       // tokens of a step: two MMAs' worth, so that a warp has independent chains
 constexpr int kHeads = 8;       // query heads of a pass: the MMA's columns
 constexpr int kMinTiles = 2;    // tiles a warp takes at least, before more CTAs join in
 constexpr float kLn2 = 0.6931471805599453f;
@@ -60,18 +65,20 @@ template <int D, int TYPE>
 struct Cfg {
     static constexpr int kBytes = KvBytes<TYPE>::value;
     static constexpr int kRow = D * kBytes;             // bytes of a token's head
-    static constexpr int kSlot = kTile * kRow;          // one tile's keys, or values
+    static constexpr int kSlot = kHalf * kRow;          // the keys, or the values, of 16 tokens
     // ring slots of a warp: as many as fit beside nothing else, eight at most
     static constexpr int kFit = 196608 / (kWarps * kSlot);
     static constexpr int kSlots = kFit > 8 ? 8 : kFit;
     static constexpr int kRing = kWarps * kSlot * kSlots;
     static constexpr int kMerge = kWarps * kHeads * D * 4;   // the warps' open pieces, after the ring is done
-    static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+    static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;   // aligned to the swizzle's 1024 bytes
     static constexpr int kSplits = TYPE == ZQ_BF16 ? 3 : 2;  // parts of q
-    static constexpr int kKRun = 16 / kBytes;           // columns of a lane's key chunk
-    static constexpr int kVRun = kRow >= 128 ? 16 / kBytes : 8;   // columns of a lane's value chunk
-    static constexpr int kVBytes = kVRun * kBytes;      // 16, or 8 for 64-byte rows
-    static constexpr int kVSegs = D / (8 * kVRun);
+    static constexpr int kSeg = kRow < 128 ? kRow : 128;          // bytes of a segment of a row
+    static constexpr int kSegs = kRow / kSeg;
+    static constexpr int kKBytes = kSeg / 4;            // a lane's keys of a segment: two chunks, or one
+    static constexpr int kKRun = kKBytes / kBytes;
+    static constexpr int kVBytes = kSeg / 8;            // a lane's values of a segment: a chunk, or half of one
+    static constexpr int kVRun = kVBytes / kBytes;
 };
 
 // A piece of a row block in the workspace: kHeads rows of D, then m and l.
@@ -135,11 +142,12 @@ __device__ __forceinline__ float2 unpack16(uint32_t w)
     else return __half22float2(*reinterpret_cast<const __half2 *>(&w));
 }
 
-// cp.async of 8 bytes (16: cp_async16), zeros when src_bytes = 0
-__device__ __forceinline__ void cp_async8(void *dst, const void *src, uint32_t src_bytes)
+// Byte of 16-byte chunk `chunk` of token row `row` in a segment as TMA left it:
+// rows of 128 bytes, 128-byte swizzle, or of 64 bytes, 64-byte swizzle.
+template <int SEG>
+__device__ __forceinline__ int swizzled(int row, int chunk)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem_u32(dst)), "l"(src), "r"(src_bytes)
-                 : "memory");
+    return row * SEG + ((chunk ^ (SEG == 128 ? row & 7 : row >> 1 & 3)) << 4);
 }
 
 // Q8_1 codes of a block of 32 outputs held by lanes that differ in the bits of
@@ -240,10 +248,14 @@ __device__ __forceinline__ int pass_heads(const PagedAttnArgs &a, int vh)
 }
 
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_constant__ PagedAttnArgs a)
+__global__ void __launch_bounds__(kThreads, 1)
+paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap map_k,
+                  const __grid_constant__ CUtensorMap map_v)
 {
     using C = Cfg<D, TYPE>;
-    extern __shared__ __align__(16) uint8_t smem[];
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+    __shared__ uint64_t full_s[kWarps][8];     // a ring slot's copy has landed
     __shared__ long long before_s[kThreads];   // tiles ahead of each thread's sequences
     __shared__ long long total_s[kWarps];
     __shared__ int head_s[kWarps];             // an ending piece in the workspace
@@ -252,6 +264,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int vheads = a.passes * a.Hk;
+    if (lane == 0) {
+        for (int i = 0; i < C::kSlots; ++i) mbar_init(&full_s[warp][i], 1);
+        fence_mbar_init();
+        prefetch_tmap(&map_k);
+        prefetch_tmap(&map_v);
+    }
     pdl_wait();   // queries, cache, table and lengths come from earlier kernels
     pdl_launch_dependents();
 
@@ -307,58 +325,64 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         at.t = at.t0 + (int)(rem % n);
     }
 
-    // ---- the ring: items are keys of a tile, then its values
+    // ---- the ring: the items of a tile are keys, keys, values, values, 16 tokens each
     uint8_t *ring = smem + (size_t)warp * C::kSlots * C::kSlot;
+    uint64_t *full = full_s[warp];
     Walk ld = at;
     long long ld_left = left;
-    int ld_item = 0;        // 0: keys next, 1: values
-    int ld_slot = 0;
-    uint32_t page_ok = 0;   // bit of a slot: its tile's page is in the cache
-    size_t ld_base = 0;
-    bool ld_ok = false;
+    int ld_item = 0, ld_slot = 0;
+    uint32_t loaded = 0;    // bit of a slot: its page is in the cache, so a copy was asked for
+    uint32_t flying = 0;    // and has not been waited for yet
+    int pid[2] = {-1, -1};
     const int page_mask = (1 << a.page_shift) - 1;
 
+    // the next item into the ring, by the whole warp after it has read what the slot held
     auto issue = [&]() {
         if (ld_left > 0) {
-            uint8_t *dst = ring + ld_slot * C::kSlot;
-            const int tok = ld.t * kTile;
+            const int h = ld_item & 1, tok = ld.t * kTile;
             if (ld_item == 0) {
-                const int pid = a.table[(size_t)ld.b * a.width + (tok >> a.page_shift)];
-                ld_ok = (unsigned)pid < (unsigned)a.pages;
-                ld_base = ld_ok ? ((((size_t)pid * a.Hk + ld.vh / a.passes) << a.page_shift) + (tok & page_mask)) *
-                                      C::kRow
-                                : 0;
-                page_ok = (page_ok & ~(1u << ld_slot)) | (uint32_t)ld_ok << ld_slot;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int row = g + 8 * h;
-                    const bool in = ld_ok && tok + row >= ld.lo && tok + row < ld.len;
-                    const char *src = a.k + (in ? ld_base + (size_t)row * C::kRow + 16 * c : 0);
-#pragma unroll
-                    for (int s = 0; s < C::kRow / 64; ++s)
-                        cp_async16(dst + (2 * s + h) * 512 + lane * 16, src + 64 * s, in ? 16 : 0);
+                for (int i = 0; i < 2; ++i) {   // a page holds both halves, or one each
+                    const int col = (tok + kHalf * i) >> a.page_shift;
+                    pid[i] = col < a.width ? a.table[(size_t)ld.b * a.width + col] : -1;
                 }
-                ld_item = 1;
-            } else {
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int row = 2 * c + (r & 1) + 8 * (r >> 1);
-                    const bool in = ld_ok && tok + row >= ld.lo && tok + row < ld.len;
-                    const char *src = a.v + (in ? ld_base + (size_t)row * C::kRow + C::kVBytes * g : 0);
-#pragma unroll
-                    for (int s = 0; s < C::kVSegs; ++s) {
-                        uint8_t *to = dst + (4 * s + r) * (32 * C::kVBytes) + lane * C::kVBytes;
-                        if constexpr (C::kVBytes == 16) cp_async16(to, src + 128 * s, in ? 16 : 0);
-                        else cp_async8(to, src, in ? 8 : 0);
-                    }
-                }
+            }
+            const int p = h ? pid[1] : pid[0];
+            const bool ok = (unsigned)p < (unsigned)a.pages;
+            loaded = (loaded & ~(1u << ld_slot)) | (uint32_t)ok << ld_slot;
+            flying |= (uint32_t)ok << ld_slot;
+            __syncwarp();
+            if (ok && lane == 0) {
+                mbar_arrive_expect_tx(&full[ld_slot], C::kSlot);
+                tma_load_5d(ring + ld_slot * C::kSlot, ld_item < 2 ? &map_k : &map_v, 0,
+                            (tok + kHalf * h) & page_mask, 0, ld.vh / a.passes, p, &full[ld_slot]);
+            }
+            if (++ld_item == 4) {
                 ld_item = 0;
                 --ld_left;
                 if (++ld.t == ld.tend) ld.next_block(a);
             }
+        } else {
+            loaded &= ~(1u << ld_slot);
         }
-        cp_async_commit();
         if (++ld_slot == C::kSlots) ld_slot = 0;
+    };
+    // Wait for the slot's copy; true when it holds one.  After an expired wait
+    // (the status word says so) no further copy is asked for or waited for.
+    uint32_t parity = 0;    // bit of a slot: the phase to wait for
+    bool failed = false;
+    auto landed = [&](int slot) {
+        const bool has = loaded >> slot & 1;
+        if (has && !failed) {
+            if (__all_sync(kAll, mbar_wait(&full[slot], parity >> slot & 1, a.status))) {
+                parity ^= 1u << slot;
+                flying &= ~(1u << slot);
+            } else {
+                failed = true;
+                ld_left = 0;
+            }
+        }
+        return has;
     };
 #pragma unroll 1
     for (int i = 0; i < C::kSlots; ++i) issue();
@@ -424,48 +448,67 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
 
 #pragma unroll 1
         for (int i = 0; i < n; ++i) {
-            // scores: S^T [16 tokens x 8 heads], two accumulators per part of q
-            cp_async_wait<C::kSlots - 1>();
-            const uint8_t *src = ring + slot * C::kSlot;
-            float acc[2 * C::kSplits][4] = {};
+            // scores: two S^T [16 tokens x 8 heads], an accumulator for each part of q
+            float sc[2][4];
+            bool ok[2];
 #pragma unroll
-            for (int s = 0; s < C::kRow / 64; ++s) {
-                const uint4 ra = *reinterpret_cast<const uint4 *>(src + (2 * s) * 512 + lane * 16);
-                const uint4 rb = *reinterpret_cast<const uint4 *>(src + (2 * s + 1) * 512 + lane * 16);
-                const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-                if constexpr (TYPE == ZQ_E4M3) {
+            for (int h = 0; h < 2; ++h) {
+                ok[h] = landed(slot);
+                const uint8_t *src = ring + slot * C::kSlot;
+                float acc[C::kSplits][4] = {};
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
+                for (int s = 0; s < C::kSegs; ++s)
 #pragma unroll
-                        for (int p = 0; p < C::kSplits; ++p)
-                            mma<TYPE>(acc[2 * p + (j & 1)], e4m3_f16(wa[j]), e4m3_f16(wb[j]), e4m3_f16(wa[j] >> 16),
-                                      e4m3_f16(wb[j] >> 16), qf[p][4 * s + j][0], qf[p][4 * s + j][1]);
-                } else {
+                    for (int u = 0; u < C::kKBytes / 16; ++u) {
+                        const int chunk = C::kKBytes / 16 * c + u;
+                        const uint8_t *from = src + s * kHalf * C::kSeg;
+                        const uint4 ra = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(g, chunk));
+                        const uint4 rb = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(g + 8, chunk));
+                        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
+                        const int k0 = (s * (C::kKBytes / 16) + u) * (4 / C::kBytes);
+                        if constexpr (TYPE == ZQ_E4M3) {
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                            for (int j = 0; j < 4; ++j) {
+                                const uint32_t a0 = e4m3_f16(wa[j]), a1 = e4m3_f16(wb[j]);
+                                const uint32_t a2 = e4m3_f16(wa[j] >> 16), a3 = e4m3_f16(wb[j] >> 16);
 #pragma unroll
-                        for (int p = 0; p < C::kSplits; ++p)
-                            mma<TYPE>(acc[2 * p + j], wa[2 * j], wb[2 * j], wa[2 * j + 1], wb[2 * j + 1],
-                                      qf[p][2 * s + j][0], qf[p][2 * s + j][1]);
+                                for (int p = 0; p < C::kSplits; ++p)
+                                    mma<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k0 + j][0], qf[p][k0 + j][1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                                for (int p = 0; p < C::kSplits; ++p)
+                                    mma<TYPE>(acc[p], wa[2 * j], wb[2 * j], wa[2 * j + 1], wb[2 * j + 1],
+                                              qf[p][k0 + j][0], qf[p][k0 + j][1]);
+                        }
+                    }
+                issue();
+                if (++slot == C::kSlots) slot = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {   // the small parts first
+                    float v = acc[C::kSplits - 1][e];
+#pragma unroll
+                    for (int p = C::kSplits - 2; p >= 0; --p) v += acc[p][e];
+                    sc[h][e] = v * (e & 1 ? scale1 : scale0);
                 }
             }
-            const bool ok = page_ok >> slot & 1;
-            issue();
-            if (++slot == C::kSlots) slot = 0;
-            float sc[4];
+            const int tok = (at.t + i) * kTile;
+            const bool whole = ok[0] && ok[1] && tok >= at.lo && tok + kTile <= at.len;
+            if (!whole) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {   // the small parts first
-                float v = acc[2 * C::kSplits - 2][e] + acc[2 * C::kSplits - 1][e];
+                for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int p = C::kSplits - 2; p >= 0; --p) v += acc[2 * p][e] + acc[2 * p + 1][e];
-                sc[e] = v * (e & 1 ? scale1 : scale0);
+                    for (int e = 0; e < 4; ++e) {
+                        const int row = tok + kHalf * h + g + 8 * (e >> 1);
+                        if (!(ok[h] && row >= at.lo && row < at.len)) sc[h][e] = -INFINITY;
+                    }
             }
-            const int tok = (at.t + i) * kTile + g;
-            const bool in0 = ok && tok >= at.lo && tok < at.len, in1 = ok && tok + 8 >= at.lo && tok + 8 < at.len;
 
             // running maximum over the tile's tokens, per head (columns 2c, 2c + 1)
-            float x0 = fmaxf(in0 ? sc[0] : -INFINITY, in1 ? sc[2] : -INFINITY);
-            float x1 = fmaxf(in0 ? sc[1] : -INFINITY, in1 ? sc[3] : -INFINITY);
+            float x0 = fmaxf(fmaxf(sc[0][0], sc[0][2]), fmaxf(sc[1][0], sc[1][2]));
+            float x1 = fmaxf(fmaxf(sc[0][1], sc[0][3]), fmaxf(sc[1][1], sc[1][3]));
 #pragma unroll
             for (int off = 4; off <= 16; off <<= 1) {
                 x0 = fmaxf(x0, __shfl_xor_sync(kAll, x0, off));
@@ -475,64 +518,83 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             x1 = fmaxf(x1, m1);
             // nothing seen yet: subtract 0, not the -infinity
             const float u0m = x0 == -INFINITY ? 0.0f : x0, u1m = x1 == -INFINITY ? 0.0f : x1;
-            if (__any_sync(kAll, x0 != m0 || x1 != m1)) {
-                const float f0 = ex2(m0 - u0m), f1 = ex2(m1 - u1m);
-                l0 *= f0;
-                l1 *= f1;
+            const float f0 = ex2(m0 - u0m), f1 = ex2(m1 - u1m);
+            m0 = x0;
+            m1 = x1;
+            l0 *= f0;
+            l1 *= f1;
+            uint32_t bh[2][2], bl[2][2];   // weights of 16 tokens x 8 heads, both parts
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k) {
-                    o[k][0] *= f0;
-                    o[k][1] *= f1;
-                    o[k][2] *= f0;
-                    o[k][3] *= f1;
-                }
-                m0 = x0;
-                m1 = x1;
+            for (int h = 0; h < 2; ++h) {
+                const float p0 = ex2(sc[h][0] - u0m), p1 = ex2(sc[h][1] - u1m);
+                const float p2 = ex2(sc[h][2] - u0m), p3 = ex2(sc[h][3] - u1m);
+                l0 += p0 + p2;
+                l1 += p1 + p3;
+                const uint32_t h0 = pack16<TYPE>(p0, p1), h1 = pack16<TYPE>(p2, p3);
+                const float2 r0 = unpack16<TYPE>(h0), r1 = unpack16<TYPE>(h1);
+                bh[h][0] = transpose8(h0);
+                bh[h][1] = transpose8(h1);
+                bl[h][0] = transpose8(pack16<TYPE>(p0 - r0.x, p1 - r0.y));
+                bl[h][1] = transpose8(pack16<TYPE>(p2 - r1.x, p3 - r1.y));
             }
-            const float p0 = in0 ? ex2(sc[0] - u0m) : 0.0f, p1 = in0 ? ex2(sc[1] - u1m) : 0.0f;
-            const float p2 = in1 ? ex2(sc[2] - u0m) : 0.0f, p3 = in1 ? ex2(sc[3] - u1m) : 0.0f;
-            l0 += p0 + p2;
-            l1 += p1 + p3;
-            const uint32_t h0 = pack16<TYPE>(p0, p1), h1 = pack16<TYPE>(p2, p3);
-            const float2 r0 = unpack16<TYPE>(h0), r1 = unpack16<TYPE>(h1);
-            const uint32_t bh0 = transpose8(h0), bh1 = transpose8(h1);
-            const uint32_t bl0 = transpose8(pack16<TYPE>(p0 - r0.x, p1 - r0.y));
-            const uint32_t bl1 = transpose8(pack16<TYPE>(p2 - r1.x, p3 - r1.y));
 
-            // O^T [16 columns x 8 heads] += V^T p: rows g and g + 8 of a product are two neighbouring columns
-            cp_async_wait<C::kSlots - 1>();
-            src = ring + slot * C::kSlot;
+            // O^T [16 columns x 8 heads] += V^T p: rows g and g + 8 of a product are two neighbouring columns.
+            // A tile's products start from zero and are added to the scaled output outside the tensor core,
+            // whose accumulator truncates: summed there, hundreds of tiles of one sign lose 1e-5.
 #pragma unroll
-            for (int s = 0; s < C::kVSegs; ++s) {
-                uint32_t w[4][C::kVBytes / 4];
+            for (int h = 0; h < 2; ++h) {
+                landed(slot);
+                const uint8_t *src = ring + slot * C::kSlot;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const uint8_t *from = src + (4 * s + r) * (32 * C::kVBytes) + lane * C::kVBytes;
-                    if constexpr (C::kVBytes == 16) {
-                        const uint4 f = *reinterpret_cast<const uint4 *>(from);
-                        w[r][0] = f.x, w[r][1] = f.y, w[r][2] = f.z, w[r][3] = f.w;
-                    } else {
-                        const uint2 f = *reinterpret_cast<const uint2 *>(from);
-                        w[r][0] = f.x, w[r][1] = f.y;
-                    }
-                }
-#pragma unroll
-                for (int j = 0; j < C::kVRun / 2; ++j) {
-                    uint32_t t[4];   // the four tokens' values of this pair of columns
+                for (int s = 0; s < C::kSegs; ++s) {
+                    uint32_t w[4][C::kVBytes / 4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        if constexpr (TYPE == ZQ_E4M3) t[r] = e4m3_f16(w[r][j / 2] >> (16 * (j & 1)));
-                        else t[r] = w[r][j];
+                        const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                        const uint8_t *from = src + s * kHalf * C::kSeg;
+                        if constexpr (C::kVBytes == 16) {
+                            const uint4 f = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(row, g));
+                            w[r][0] = f.x, w[r][1] = f.y, w[r][2] = f.z, w[r][3] = f.w;
+                        } else {
+                            const uint2 f = *reinterpret_cast<const uint2 *>(
+                                from + swizzled<C::kSeg>(row, g >> 1) + 8 * (g & 1));
+                            w[r][0] = f.x, w[r][1] = f.y;
+                        }
+                        if (!whole) {
+                            const int at_row = tok + kHalf * h + row;
+                            if (!(ok[h] && at_row >= at.lo && at_row < at.len))
+#pragma unroll
+                                for (int j = 0; j < C::kVBytes / 4; ++j) w[r][j] = 0;
+                        }
                     }
-                    const uint32_t a0 = __byte_perm(t[0], t[1], 0x5410), a1 = __byte_perm(t[0], t[1], 0x7632);
-                    const uint32_t a2 = __byte_perm(t[2], t[3], 0x5410), a3 = __byte_perm(t[2], t[3], 0x7632);
-                    float(&to)[4] = o[s * (C::kVRun / 2) + j];
-                    mma<TYPE>(to, a0, a1, a2, a3, bh0, bh1);
-                    mma<TYPE>(to, a0, a1, a2, a3, bl0, bl1);
+#pragma unroll
+                    for (int j = 0; j < C::kVRun / 2; ++j) {
+                        uint32_t v[4];   // the four tokens' values of this pair of columns
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            if constexpr (TYPE == ZQ_E4M3) v[r] = e4m3_f16(w[r][j / 2] >> (16 * (j & 1)));
+                            else v[r] = w[r][j];
+                        }
+                        const uint32_t a0 = __byte_perm(v[0], v[1], 0x5410), a1 = __byte_perm(v[0], v[1], 0x7632);
+                        const uint32_t a2 = __byte_perm(v[2], v[3], 0x5410), a3 = __byte_perm(v[2], v[3], 0x7632);
+                        float y[4] = {};
+                        mma<TYPE>(y, a0, a1, a2, a3, bl[h][0], bl[h][1]);
+                        mma<TYPE>(y, a0, a1, a2, a3, bh[h][0], bh[h][1]);
+                        float(&to)[4] = o[s * (C::kVRun / 2) + j];
+                        if (h == 0) {
+                            to[0] = to[0] * f0 + y[0];
+                            to[1] = to[1] * f1 + y[1];
+                            to[2] = to[2] * f0 + y[2];
+                            to[3] = to[3] * f1 + y[3];
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) to[e] += y[e];
+                        }
+                    }
                 }
+                issue();
+                if (++slot == C::kSlots) slot = 0;
             }
-            issue();
-            if (++slot == C::kSlots) slot = 0;
         }
 #pragma unroll
         for (int off = 4; off <= 16; off <<= 1) {
@@ -549,7 +611,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
                 const float l = e ? l1 : l0, f = row_factor(l, a.v_scale);
                 const long long row = (long long)at.b * a.out_stride + (long long)(head0 + h) * D;
 #pragma unroll
-                for (int s = 0; s < C::kVSegs; ++s) {
+                for (int s = 0; s < C::kSegs; ++s) {
                     float y[C::kVRun];
 #pragma unroll
                     for (int j = 0; j < C::kVRun / 2; ++j) {
@@ -579,7 +641,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             for (int e = 0; e < 2; ++e) {
                 const int h = 2 * c + e;
 #pragma unroll
-                for (int s = 0; s < C::kVSegs; ++s)
+                for (int s = 0; s < C::kSegs; ++s)
 #pragma unroll
                     for (int j = 0; j < C::kVRun / 2; ++j)
                         *reinterpret_cast<float2 *>(head_piece + h * D + (8 * s + g) * C::kVRun + 2 * j) =
@@ -595,7 +657,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
             open = Meta{0, starts ? 1 : 2, at.b, at.vh};
         }
     }
-    cp_async_wait<0>();
+    if (failed) {   // copies still in flight land before the ring's place is used again
+        for (int i = 0; i < C::kSlots; ++i)
+            if (flying >> i & 1) mbar_wait_for(&full[i], parity >> i & 1, nullptr, 1000000ull);
+    }
     __syncthreads();   // every warp's ring is done: its place holds the open pieces now
     float *pieces_s = reinterpret_cast<float *>(smem);
     if (open.b) {
@@ -604,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_attn_kernel(const __grid_co
         for (int e = 0; e < 2; ++e) {
             const int h = 2 * c + e;
 #pragma unroll
-            for (int s = 0; s < C::kVSegs; ++s)
+            for (int s = 0; s < C::kSegs; ++s)
 #pragma unroll
                 for (int j = 0; j < C::kVRun / 2; ++j)
                     *reinterpret_cast<float2 *>(to + h * D + (8 * s + g) * C::kVRun + 2 * j) =
@@ -802,7 +867,16 @@ cudaError_t launch_one(const PagedAttnArgs &a, int ctas, cudaStream_t st)
         if (e != cudaSuccess) return e;
         set[dev] = true;
     }
-    e = launch_pdl(paged_attn_kernel<D, TYPE>, dim3(ctas), dim3(kThreads), C::kSmem, st, a);
+    // [page][key head][segment][row][bytes of a segment]; a box is all segments of 16 rows
+    const uint64_t page = (uint64_t)1 << a.page_shift;
+    const uint64_t dims[5] = {C::kSeg, page, C::kSegs, (uint64_t)a.Hk, (uint64_t)a.pages};
+    const uint64_t strides[4] = {C::kRow, C::kSeg, page * C::kRow, page * C::kRow * a.Hk};
+    const uint32_t box[5] = {C::kSeg, kHalf, C::kSegs, 1, 1};
+    const CUtensorMapSwizzle sw = C::kSeg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+    CUtensorMap mk, mv;
+    if ((e = make_tmap_u8(&mk, 5, a.k, dims, strides, box, sw)) != cudaSuccess) return e;
+    if ((e = make_tmap_u8(&mv, 5, a.v, dims, strides, box, sw)) != cudaSuccess) return e;
+    e = launch_pdl(paged_attn_kernel<D, TYPE>, dim3(ctas), dim3(kThreads), C::kSmem, st, a, mk, mv);
     if (e != cudaSuccess) return e;
     return launch_pdl(paged_attn_join_kernel<D>, dim3(ctas, a.per_pass), dim3(kThreads), 0, st, a, ctas);
 }
@@ -841,6 +915,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &args, int D, int type, void *
     a.G = a.Hq / a.Hk;
     a.passes = (a.G + kHeads - 1) / kHeads;
     a.per_pass = (a.G + a.passes - 1) / a.passes;
+    a.status = device_status_word();
     a.pieces = static_cast<float *>(workspace);
     a.meta = static_cast<char *>(workspace) + pad256((size_t)ctas * (2 + kWarps) * piece_floats(D) * sizeof(float));
     switch (D) {

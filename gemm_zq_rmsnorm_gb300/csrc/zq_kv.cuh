@@ -87,6 +87,7 @@ struct PagedAttnArgs {
     int G, passes, per_pass;   // query heads of a key head, in passes of up to eight
     float *pieces;
     void *meta;
+    unsigned int *status;
 };
 size_t paged_attn_workspace(int D);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int D, int type, void *workspace, cudaStream_t st);

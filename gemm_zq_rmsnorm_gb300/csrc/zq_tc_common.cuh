@@ -70,6 +70,10 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, volati
 cudaError_t make_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, uint32_t esize, const void *base, uint64_t cols,
                          uint64_t rows, uint32_t box_cols, uint32_t box_rows, CUtensorMapSwizzle sw);
 
+// Tensor of bytes of `rank` <= 5 dimensions; strides (bytes) of dimensions 1 ..
+cudaError_t make_tmap_u8(CUtensorMap *m, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
+                         const uint32_t *box, CUtensorMapSwizzle sw);
+
 // q8 activation codes -> fp16 (exact), n codes, n a multiple of 16.
 cudaError_t launch_q8_to_f16(const int8_t *qs, __half *out, size_t n, cudaStream_t st);
 
