@@ -24,9 +24,9 @@
 // kernel that reads at most two pieces per CTA, in order: no atomics, the same
 // result every time.
 //
-// Loads: one lane of a warp copies the keys, or the values, of 16 tokens of a
-// page by TMA into the warp's own ring, two halves of a tile one after the
-// other.  (With cp.async of 16 bytes a lane the same loop stopped at 4.4 TB/s
+// Loads: one lane of a warp copies the keys, or the values, of a tile (two
+// pages' halves when pages have 16 tokens; half a tile of 512-byte rows) by TMA
+// into the warp's own ring.  (With cp.async of 16 bytes a lane the same loop stopped at 4.4 TB/s
 // whatever the depth of the ring.)  The box is [segment of 128 bytes][token],
 // 128-byte swizzled, and the order of the head's columns in a K-step and of
 // the output rows is free: lane 4g + c reads 16-byte chunks 2c and 2c + 1 of
@@ -65,7 +65,10 @@ template <int D, int TYPE>
 struct Cfg {
     static constexpr int kBytes = KvBytes<TYPE>::value;
     static constexpr int kRow = D * kBytes;             // bytes of a token's head
-    static constexpr int kSlot = kHalf * kRow;          // the keys, or the values, of 16 tokens
+    // an item of the ring: the keys, or the values, of a tile, or of half a tile of 512-byte rows
+    static constexpr int kItem = kRow > 256 ? kHalf : kTile;
+    static constexpr int kItems = kTile / kItem;        // of keys (and of values) in a tile
+    static constexpr int kSlot = kItem * kRow;
     // ring slots of a warp: as many as fit beside nothing else, eight at most
     static constexpr int kFit = 196608 / (kWarps * kSlot);
     static constexpr int kSlots = kFit > 8 ? 8 : kFit;
@@ -331,48 +334,64 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     Walk ld = at;
     long long ld_left = left;
     int ld_item = 0, ld_slot = 0;
-    uint32_t loaded = 0;    // bit of a slot: its page is in the cache, so a copy was asked for
-    uint32_t flying = 0;    // and has not been waited for yet
+    uint32_t loaded = 0;    // two bits of a slot, its halves: the page is in the cache, so a copy was asked for
+    uint32_t flying = 0;    // bit of a slot: the copy has not been waited for yet
     int pid[2] = {-1, -1};
     const int page_mask = (1 << a.page_shift) - 1;
+    // an item lies as its boxes came: [segment][row], of 32 rows or twice of 16
+    const int seg_stride = (C::kItem > kHalf ? a.box : kHalf) * C::kSeg;
+    const int half_stride = a.box == kTile ? kHalf * C::kSeg : kHalf * C::kRow;
 
     // the next item into the ring, by the whole warp after it has read what the slot held
     auto issue = [&]() {
         if (ld_left > 0) {
-            const int h = ld_item & 1, tok = ld.t * kTile;
+            const int tok = ld.t * kTile;
             if (ld_item == 0) {
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {   // a page holds both halves, or one each
                     const int col = (tok + kHalf * i) >> a.page_shift;
                     pid[i] = col < a.width ? a.table[(size_t)ld.b * a.width + col] : -1;
+                    pid[i] = (unsigned)pid[i] < (unsigned)a.pages ? pid[i] : -1;
                 }
             }
-            const int p = h ? pid[1] : pid[0];
-            const bool ok = (unsigned)p < (unsigned)a.pages;
-            loaded = (loaded & ~(1u << ld_slot)) | (uint32_t)ok << ld_slot;
-            flying |= (uint32_t)ok << ld_slot;
+            const CUtensorMap *map = ld_item < C::kItems ? &map_k : &map_v;
+            const int first = ld_item % C::kItems;   // half of the tile the item begins with
+            uint8_t *dst = ring + ld_slot * C::kSlot;
+            uint32_t ok = 0;
+#pragma unroll
+            for (int i = 0; i < C::kItem / kHalf; ++i) ok |= (uint32_t)(pid[first + i] >= 0) << i;
+            loaded = (loaded & ~(3u << 2 * ld_slot)) | ok << 2 * ld_slot;
+            flying |= (uint32_t)(ok != 0) << ld_slot;
             __syncwarp();
             if (ok && lane == 0) {
-                mbar_arrive_expect_tx(&full[ld_slot], C::kSlot);
-                tma_load_5d(ring + ld_slot * C::kSlot, ld_item < 2 ? &map_k : &map_v, 0,
-                            (tok + kHalf * h) & page_mask, 0, ld.vh / a.passes, p, &full[ld_slot]);
+                const int key_head = ld.vh / a.passes;
+                mbar_arrive_expect_tx(&full[ld_slot], (ok == 3 ? 2 : 1) * kHalf * C::kRow);
+                if (C::kItem > kHalf && a.box == kTile) {
+                    tma_load_5d(dst, map, 0, tok & page_mask, 0, key_head, pid[0], &full[ld_slot]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < C::kItem / kHalf; ++i)
+                        if (ok >> i & 1)
+                            tma_load_5d(dst + i * kHalf * C::kRow, map, 0, (tok + kHalf * (first + i)) & page_mask, 0,
+                                        key_head, pid[first + i], &full[ld_slot]);
+                }
             }
-            if (++ld_item == 4) {
+            if (++ld_item == 2 * C::kItems) {
                 ld_item = 0;
                 --ld_left;
                 if (++ld.t == ld.tend) ld.next_block(a);
             }
         } else {
-            loaded &= ~(1u << ld_slot);
+            loaded &= ~(3u << 2 * ld_slot);
         }
         if (++ld_slot == C::kSlots) ld_slot = 0;
     };
-    // Wait for the slot's copy; true when it holds one.  After an expired wait
+    // Wait for the slot's copy; the bits of its halves.  After an expired wait
     // (the status word says so) no further copy is asked for or waited for.
     uint32_t parity = 0;    // bit of a slot: the phase to wait for
     bool failed = false;
     auto landed = [&](int slot) {
-        const bool has = loaded >> slot & 1;
+        const uint32_t has = loaded >> 2 * slot & 3;
         if (has && !failed) {
             if (__all_sync(kAll, mbar_wait(&full[slot], parity >> slot & 1, a.status))) {
                 parity ^= 1u << slot;
@@ -451,17 +470,19 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             // scores: two S^T [16 tokens x 8 heads], an accumulator for each part of q
             float sc[2][4];
             bool ok[2];
+            uint32_t has = 0;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                ok[h] = landed(slot);
-                const uint8_t *src = ring + slot * C::kSlot;
+                if (C::kItems == 2 || h == 0) has = landed(slot);
+                ok[h] = has >> (C::kItems == 2 ? 0 : h) & 1;
+                const uint8_t *src = ring + slot * C::kSlot + (C::kItems == 2 ? 0 : h * half_stride);
                 float acc[C::kSplits][4] = {};
 #pragma unroll
                 for (int s = 0; s < C::kSegs; ++s)
 #pragma unroll
                     for (int u = 0; u < C::kKBytes / 16; ++u) {
                         const int chunk = C::kKBytes / 16 * c + u;
-                        const uint8_t *from = src + s * kHalf * C::kSeg;
+                        const uint8_t *from = src + s * seg_stride;
                         const uint4 ra = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(g, chunk));
                         const uint4 rb = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(g + 8, chunk));
                         const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
@@ -484,8 +505,10 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                                               qf[p][k0 + j][0], qf[p][k0 + j][1]);
                         }
                     }
-                issue();
-                if (++slot == C::kSlots) slot = 0;
+                if (C::kItems == 2 || h == 1) {
+                    issue();
+                    if (++slot == C::kSlots) slot = 0;
+                }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {   // the small parts first
                     float v = acc[C::kSplits - 1][e];
@@ -543,15 +566,15 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             // whose accumulator truncates: summed there, hundreds of tiles of one sign lose 1e-5.
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                landed(slot);
-                const uint8_t *src = ring + slot * C::kSlot;
+                if (C::kItems == 2 || h == 0) landed(slot);
+                const uint8_t *src = ring + slot * C::kSlot + (C::kItems == 2 ? 0 : h * half_stride);
 #pragma unroll
                 for (int s = 0; s < C::kSegs; ++s) {
                     uint32_t w[4][C::kVBytes / 4];
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
                         const int row = 2 * c + (r & 1) + 8 * (r >> 1);
-                        const uint8_t *from = src + s * kHalf * C::kSeg;
+                        const uint8_t *from = src + s * seg_stride;
                         if constexpr (C::kVBytes == 16) {
                             const uint4 f = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(row, g));
                             w[r][0] = f.x, w[r][1] = f.y, w[r][2] = f.z, w[r][3] = f.w;
@@ -592,8 +615,10 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                         }
                     }
                 }
-                issue();
-                if (++slot == C::kSlots) slot = 0;
+                if (C::kItems == 2 || h == 1) {
+                    issue();
+                    if (++slot == C::kSlots) slot = 0;
+                }
             }
         }
 #pragma unroll
@@ -867,11 +892,11 @@ cudaError_t launch_one(const PagedAttnArgs &a, int ctas, cudaStream_t st)
         if (e != cudaSuccess) return e;
         set[dev] = true;
     }
-    // [page][key head][segment][row][bytes of a segment]; a box is all segments of 16 rows
+    // [page][key head][segment][row][bytes of a segment]; a box is all segments of 16 or 32 rows
     const uint64_t page = (uint64_t)1 << a.page_shift;
     const uint64_t dims[5] = {C::kSeg, page, C::kSegs, (uint64_t)a.Hk, (uint64_t)a.pages};
     const uint64_t strides[4] = {C::kRow, C::kSeg, page * C::kRow, page * C::kRow * a.Hk};
-    const uint32_t box[5] = {C::kSeg, kHalf, C::kSegs, 1, 1};
+    const uint32_t box[5] = {C::kSeg, (uint32_t)(C::kItem > kHalf ? a.box : kHalf), C::kSegs, 1, 1};
     const CUtensorMapSwizzle sw = C::kSeg == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
     CUtensorMap mk, mv;
     if ((e = make_tmap_u8(&mk, 5, a.k, dims, strides, box, sw)) != cudaSuccess) return e;
@@ -915,6 +940,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &args, int D, int type, void *
     a.G = a.Hq / a.Hk;
     a.passes = (a.G + kHeads - 1) / kHeads;
     a.per_pass = (a.G + a.passes - 1) / a.passes;
+    a.box = a.page_shift > 4 ? kTile : kHalf;   // rows of a page that one copy brings
     a.status = device_status_word();
     a.pieces = static_cast<float *>(workspace);
     a.meta = static_cast<char *>(workspace) + pad256((size_t)ctas * (2 + kWarps) * piece_floats(D) * sizeof(float));

@@ -87,6 +87,7 @@ struct PagedAttnArgs {
     int G, passes, per_pass;   // query heads of a key head, in passes of up to eight
     float *pieces;
     void *meta;
+    int box;
     unsigned int *status;
 };
 size_t paged_attn_workspace(int D);
