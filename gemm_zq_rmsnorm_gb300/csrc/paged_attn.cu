@@ -52,17 +52,22 @@
 namespace zq {
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
+constexpr int kMaxWarps = 16;
+constexpr int kPlanners = 256;  // threads that add up the line of tiles
+constexpr int kJoinThreads = 256;
 constexpr int kHalf = 16;       // tokens of an MMA
 constexpr int kTile = 32;       // tokens of a step: two MMAs' worth, so that a warp has independent chains
 constexpr int kHeads = 8;       // query heads of a pass: the MMA's columns
-constexpr int kMinTiles = 2;    // tiles a warp takes at least, before more CTAs join in
+constexpr int kMinTiles = 1;    // places of the line a warp takes at least, before more CTAs join in
+constexpr int kBlockCost = 3;   // what a row block costs besides its tiles, in tiles
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int D, int TYPE>
 struct Cfg {
+    // As many warps as the registers of their fragments allow (q and the output are D / 2 to D / 1.3 registers)
+    static constexpr int kWarps = D == 64 ? 16 : D == 128 ? 12 : 8;
+    static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBytes = KvBytes<TYPE>::value;
     static constexpr int kRow = D * kBytes;             // bytes of a token's head
     // an item of the ring: the keys, or the values, of a tile, or of half a tile of 512-byte rows
@@ -90,7 +95,13 @@ __host__ __device__ constexpr size_t piece_floats(int D) { return (size_t)kHeads
 // What a CTA leaves open: `a` continues a row block of an earlier CTA
 // (1: goes on, 2: ends here), `b` one that begins here and goes on.
 struct Meta {
-    int a, b, seq, vh;
+    int a, b, seq, head, heads;
+};
+
+// Pieces of one row block in a CTA: the open ones of warps w0 .. w1 - 1 and,
+// when it ends here, the ending one of warp w1.
+struct Run {
+    int w0, w1, begins, ends, seq, head, heads;
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -124,12 +135,12 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x)
     return y;
 }
 
-// two e4m3 values to two binary16 values (exact)
-__device__ __forceinline__ uint32_t e4m3_f16(uint32_t pair)
+// four e4m3 values to binary16 (exact): the lower two, the upper two
+__device__ __forceinline__ void e4m3_f16(uint32_t w, uint32_t &lo, uint32_t &hi)
 {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)pair));
-    return r;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 
 // The MMA's 16-bit type: bf16 for a bf16 cache, else binary16.
@@ -216,10 +227,10 @@ __device__ __forceinline__ int seq_tiles(int lo, int len)
     return max(1, (len + kTile - 1) / kTile - lo / kTile);
 }
 
-// A place on the line of tiles: sequence, pass (key head and group of up to
+// A place on the line of tiles: sequence, key head, pass (a group of up to
 // eight of its query heads), tile.
 struct Walk {
-    int b, vh, t, t0, tend, lo, len;
+    int b, kh, pass, t, t0, tend, lo, len;
     __device__ __forceinline__ void sequence(const PagedAttnArgs &a, int seq)
     {
         b = seq;
@@ -233,37 +244,37 @@ struct Walk {
     __device__ __forceinline__ void next_block(const PagedAttnArgs &a)
     {
         t = t0;
-        if (++vh == a.passes * a.Hk) {
-            vh = 0;
-            if (++b < a.B) sequence(a, b);
-        }
+        if (++pass < a.passes) return;
+        pass = 0;
+        if (++kh < a.Hk) return;
+        kh = 0;
+        if (++b < a.B) sequence(a, b);
+    }
+    // its query heads: the first one, and how many
+    __device__ __forceinline__ int head(const PagedAttnArgs &a) const { return kh * a.G + pass * a.per_pass; }
+    __device__ __forceinline__ int heads(const PagedAttnArgs &a) const
+    {
+        return min(a.per_pass, a.G - pass * a.per_pass);
     }
 };
 
-// Query heads of pass vh: the first one, and how many.
-__device__ __forceinline__ int pass_head(const PagedAttnArgs &a, int vh)
-{
-    return vh / a.passes * a.G + vh % a.passes * a.per_pass;
-}
-__device__ __forceinline__ int pass_heads(const PagedAttnArgs &a, int vh)
-{
-    return min(a.per_pass, a.G - vh % a.passes * a.per_pass);
-}
-
 template <int D, int TYPE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, TYPE>::kThreads, 1)
 paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant__ CUtensorMap map_k,
                   const __grid_constant__ CUtensorMap map_v)
 {
     using C = Cfg<D, TYPE>;
+    constexpr int kWarps = C::kWarps;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
     __shared__ uint64_t full_s[kWarps][8];     // a ring slot's copy has landed
-    __shared__ long long before_s[kThreads];   // tiles ahead of each thread's sequences
-    __shared__ long long total_s[kWarps];
+    __shared__ long long before_s[kPlanners];  // the line ahead of each planner's sequences
+    __shared__ long long total_s[kPlanners / 32];
     __shared__ int head_s[kWarps];             // an ending piece in the workspace
     __shared__ Meta open_s[kWarps];            // the warp's last piece (b = 1: begins in the warp, 2: before)
     __shared__ float m_s[kWarps][kHeads], l_s[kWarps][kHeads];
+    __shared__ Run runs_s[kWarps + 1];
+    __shared__ int nruns_s;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int vheads = a.passes * a.Hk;
@@ -276,56 +287,60 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     pdl_wait();   // queries, cache, table and lengths come from earlier kernels
     pdl_launch_dependents();
 
-    // ---- the line of tiles: thread t adds up the sequences t * per ..
-    const int per = (a.B + kThreads - 1) / kThreads;
-    long long mine = 0;
-    for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-        const int len = seq_len(a, b);
-        mine += (long long)seq_tiles(seq_first(a, len), len) * vheads;
-    }
-    long long incl = mine;
+    // ---- the line: every row block is kBlockCost places and its tiles; planner t adds up sequences t * per ..
+    const int per = (a.B + kPlanners - 1) / kPlanners;
+    long long mine = 0, incl = 0;
+    if (tid < kPlanners) {
+        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
+            const int len = seq_len(a, b);
+            mine += (long long)(seq_tiles(seq_first(a, len), len) + kBlockCost) * vheads;
+        }
+        incl = mine;
 #pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-        const long long up = __shfl_up_sync(kAll, incl, off);
-        if (lane >= off) incl += up;
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long up = __shfl_up_sync(kAll, incl, off);
+            if (lane >= off) incl += up;
+        }
+        if (lane == 31) total_s[warp] = incl;
     }
-    if (lane == 31) total_s[warp] = incl;
     __syncthreads();
     long long total = 0, base = 0;
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
+    for (int w = 0; w < kPlanners / 32; ++w) {
         if (w == warp) base = total;
         total += total_s[w];
     }
-    before_s[tid] = base + incl - mine;
-    const long long wanted = (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles);
-    const int ctas = (int)min((long long)gridDim.x, max(1ll, wanted));
+    if (tid < kPlanners) before_s[tid] = base + incl - mine;
+    const int ctas = (int)min((long long)gridDim.x, max(1ll, total / (kWarps * kMinTiles)));
     Meta *meta = reinterpret_cast<Meta *>(a.meta);
     if (blockIdx.x >= ctas) {
-        if (tid == 0) meta[blockIdx.x] = Meta{0, 0, 0, 0};
+        if (tid == 0) meta[blockIdx.x] = Meta{0, 0, 0, 0, 0};
         return;
     }
     __syncthreads();
 
+    // this warp's places [u0, u1); `left` counts them down, a tile at a time
     const long long nw = (long long)ctas * kWarps, gw = (long long)blockIdx.x * kWarps + warp;
     const long long u0 = gw * total / nw;
     long long left = (gw + 1) * total / nw - u0;
-
     Walk at;
     if (left > 0) {
         int i = 0;
 #pragma unroll
-        for (int step = kThreads / 2; step >= 1; step >>= 1)
-            if (before_s[i + step] <= u0 && (i + step) * per < a.B) i += step;
+        for (int step = kPlanners / 2; step >= 1; step >>= 1)
+            if ((i + step) * per < a.B && before_s[i + step] <= u0) i += step;
         long long rem = u0 - before_s[i];
         at.sequence(a, i * per);
-        while (rem >= (long long)(at.tend - at.t0) * vheads) {
-            rem -= (long long)(at.tend - at.t0) * vheads;
+        while (rem >= (long long)(at.tend - at.t0 + kBlockCost) * vheads) {
+            rem -= (long long)(at.tend - at.t0 + kBlockCost) * vheads;
             at.sequence(a, at.b + 1);
         }
-        const int n = at.tend - at.t0;
-        at.vh = (int)(rem / n);
-        at.t = at.t0 + (int)(rem % n);
+        const int n = at.tend - at.t0 + kBlockCost;
+        const int vh = (int)(rem / n), r = (int)(rem - (long long)vh * n);
+        at.kh = vh / a.passes;
+        at.pass = vh - at.kh * a.passes;
+        at.t = at.t0 + max(0, r - kBlockCost);
+        left -= max(0, kBlockCost - r);
     }
 
     // ---- the ring: the items of a tile are keys, keys, values, values, 16 tokens each
@@ -348,11 +363,12 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             const int tok = ld.t * kTile;
             if (ld_item == 0) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {   // a page holds both halves, or one each
-                    const int col = (tok + kHalf * i) >> a.page_shift;
-                    pid[i] = col < a.width ? a.table[(size_t)ld.b * a.width + col] : -1;
+                for (int i = 0; i < 2; ++i) {   // a page holds both halves, or one each; the table ends at len
+                    const int row = tok + kHalf * i, col = row >> a.page_shift;
+                    pid[i] = row < ld.len ? a.table[(size_t)ld.b * a.width + col] : -1;
                     pid[i] = (unsigned)pid[i] < (unsigned)a.pages ? pid[i] : -1;
                 }
+                if (a.box == kTile) pid[1] = pid[0];
             }
             const CUtensorMap *map = ld_item < C::kItems ? &map_k : &map_v;
             const int first = ld_item % C::kItems;   // half of the tile the item begins with
@@ -364,22 +380,24 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             flying |= (uint32_t)(ok != 0) << ld_slot;
             __syncwarp();
             if (ok && lane == 0) {
-                const int key_head = ld.vh / a.passes;
                 mbar_arrive_expect_tx(&full[ld_slot], (ok == 3 ? 2 : 1) * kHalf * C::kRow);
                 if (C::kItem > kHalf && a.box == kTile) {
-                    tma_load_5d(dst, map, 0, tok & page_mask, 0, key_head, pid[0], &full[ld_slot]);
+                    tma_load_5d(dst, map, 0, tok & page_mask, 0, ld.kh, pid[0], &full[ld_slot]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < C::kItem / kHalf; ++i)
                         if (ok >> i & 1)
                             tma_load_5d(dst + i * kHalf * C::kRow, map, 0, (tok + kHalf * (first + i)) & page_mask, 0,
-                                        key_head, pid[first + i], &full[ld_slot]);
+                                        ld.kh, pid[first + i], &full[ld_slot]);
                 }
             }
             if (++ld_item == 2 * C::kItems) {
                 ld_item = 0;
                 --ld_left;
-                if (++ld.t == ld.tend) ld.next_block(a);
+                if (++ld.t == ld.tend) {
+                    ld_left -= kBlockCost;
+                    ld.next_block(a);
+                }
             }
         } else {
             loaded &= ~(3u << 2 * ld_slot);
@@ -410,13 +428,13 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     float o[D / 16][4];
     float m0 = 0, m1 = 0, l0 = 0, l1 = 0;
     int has_head = 0;
-    Meta open{0, 0, 0, 0};
-    float *head_piece = a.pieces + (size_t)(2 * gridDim.x + gw) * piece_floats(D);
+    Meta open{0, 0, 0, 0, 0};
+    float *head_piece = a.pieces + ((size_t)2 * gridDim.x + (size_t)gw) * piece_floats(D);
 
     while (left > 0) {
         const int n = (int)min(left, (long long)(at.tend - at.t));
         const bool starts = at.t == at.t0, ends = at.t + n == at.tend;
-        const int heads = pass_heads(a, at.vh), head0 = pass_head(a, at.vh);
+        const int heads = at.heads(a), head0 = at.head(a);
 
         // queries of head g, in the columns' order of the key chunks
         uint32_t qf[C::kSplits][D / 16][2];
@@ -490,8 +508,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                         if constexpr (TYPE == ZQ_E4M3) {
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
-                                const uint32_t a0 = e4m3_f16(wa[j]), a1 = e4m3_f16(wb[j]);
-                                const uint32_t a2 = e4m3_f16(wa[j] >> 16), a3 = e4m3_f16(wb[j] >> 16);
+                                uint32_t a0, a1, a2, a3;
+                                e4m3_f16(wa[j], a0, a2);
+                                e4m3_f16(wb[j], a1, a3);
 #pragma unroll
                                 for (int p = 0; p < C::kSplits; ++p)
                                     mma<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k0 + j][0], qf[p][k0 + j][1]);
@@ -592,14 +611,17 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                     }
 #pragma unroll
                     for (int j = 0; j < C::kVRun / 2; ++j) {
-                        uint32_t v[4];   // the four tokens' values of this pair of columns
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) {
-                            if constexpr (TYPE == ZQ_E4M3) v[r] = e4m3_f16(w[r][j / 2] >> (16 * (j & 1)));
-                            else v[r] = w[r][j];
+                        uint32_t a0, a1, a2, a3;   // two columns of tokens 2c, 2c + 1, and of 2c + 8, 2c + 9
+                        if constexpr (TYPE == ZQ_E4M3) {
+                            const int sel = j & 1 ? 0x7362 : 0x5140;
+                            e4m3_f16(__byte_perm(w[0][j / 2], w[1][j / 2], sel), a0, a1);
+                            e4m3_f16(__byte_perm(w[2][j / 2], w[3][j / 2], sel), a2, a3);
+                        } else {
+                            a0 = __byte_perm(w[0][j], w[1][j], 0x5410);
+                            a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
+                            a2 = __byte_perm(w[2][j], w[3][j], 0x5410);
+                            a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
                         }
-                        const uint32_t a0 = __byte_perm(v[0], v[1], 0x5410), a1 = __byte_perm(v[0], v[1], 0x7632);
-                        const uint32_t a2 = __byte_perm(v[2], v[3], 0x5410), a3 = __byte_perm(v[2], v[3], 0x7632);
                         float y[4] = {};
                         mma<TYPE>(y, a0, a1, a2, a3, bl[h][0], bl[h][1]);
                         mma<TYPE>(y, a0, a1, a2, a3, bh[h][0], bh[h][1]);
@@ -658,7 +680,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 }
                 if (store && a.lse && g == 0) a.lse[(size_t)at.b * a.Hq + head0 + h] = row_lse(e ? m1 : m0, l);
             }
-            at.t += n;
+            left -= kBlockCost;
             at.next_block(a);
         } else if (ends) {      // began in an earlier warp: to the workspace
             has_head = 1;
@@ -676,10 +698,10 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                     head_piece[kHeads * D + kHeads + h] = e ? l1 : l0;
                 }
             }
-            at.t += n;
+            left -= kBlockCost;
             at.next_block(a);
         } else {                // goes on in the next warp: the last one here
-            open = Meta{0, starts ? 1 : 2, at.b, at.vh};
+            open = Meta{0, starts ? 1 : 2, at.b, head0, heads};
         }
     }
     if (failed) {   // copies still in flight land before the ring's place is used again
@@ -711,46 +733,79 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     }
     __syncthreads();
 
-    // ---- join the CTA's pieces: a run is the open pieces of warps w0 .. w1 - 1
-    // and, when it ends here, the ending piece of warp w1
-    auto join = [&](int w0, int w1, bool begins, bool finishes, int seq, int vh) {
-        const int heads = begins ? pass_heads(a, vh) : kHeads, head0 = begins ? pass_head(a, vh) : 0;
-        const float *tail = a.pieces + (size_t)(2 * gridDim.x + (size_t)blockIdx.x * kWarps + w1) * piece_floats(D);
-        float *to = a.pieces + (size_t)(2 * blockIdx.x + (begins ? 1 : 0)) * piece_floats(D);
-        const int items = heads * (D / 4);
-        for (int i = tid; i < (items + 31) / 32 * 32; i += kThreads) {
-            const bool store = i < items;
-            const int h = store ? i / (D / 4) : 0, d = i % (D / 4) * 4;
-            float m = -INFINITY;
-            for (int w = w0; w < w1; ++w)   // a call of fewer tiles than warps leaves some without any
-                if (open_s[w].b) m = fmaxf(m, m_s[w][h]);
-            if (finishes) m = fmaxf(m, tail[kHeads * D + h]);
-            const float u = m == -INFINITY ? 0.0f : m;
+    // ---- join the CTA's pieces: first the runs, then one warp for each head of a run
+    if (tid == 0) {
+        Meta info{0, 0, 0, 0, 0};   // what this CTA leaves to the second kernel
+        int n = 0;
+        bool running = false;
+        Run run{};
+        for (int w = 0; w < kWarps; ++w) {
+            if (head_s[w]) {
+                if (!running) run = Run{w, w, 0, 1, 0, 0, kHeads};
+                run.w1 = w;
+                run.ends = 1;
+                if (!run.begins) info.a = 2;
+                runs_s[n++] = run;
+                running = false;
+            }
+            if (open_s[w].b && !running) {
+                running = true;
+                run = Run{w, kWarps, open_s[w].b == 1, 0, open_s[w].seq, open_s[w].head, open_s[w].heads};
+            }
+        }
+        if (running) {
+            runs_s[n++] = run;
+            if (run.begins) info.b = 1, info.seq = run.seq, info.head = run.head, info.heads = run.heads;
+            else info.a = 1;
+        }
+        nruns_s = n;
+        meta[blockIdx.x] = info;
+    }
+    __syncthreads();
+    for (int i = warp; i < nruns_s * kHeads; i += kWarps) {
+        const Run run = runs_s[i / kHeads];
+        const int h = i % kHeads;
+        if (h >= run.heads) continue;
+        const float *tail =
+            a.pieces + ((size_t)2 * gridDim.x + (size_t)blockIdx.x * kWarps + run.w1) * piece_floats(D);
+        float m = -INFINITY;
+        for (int w = run.w0; w < run.w1; ++w)   // a call of fewer tiles than warps leaves some without any
+            if (open_s[w].b) m = fmaxf(m, m_s[w][h]);
+        if (run.ends) m = fmaxf(m, tail[kHeads * D + h]);
+        const float u = m == -INFINITY ? 0.0f : m;
+#pragma unroll
+        for (int d0 = 0; d0 < D; d0 += 128) {
+            const int d = d0 + 4 * lane;
+            const bool in = d < D;
             float l = 0.0f;
             float y[4] = {};
-            for (int w = w0; w < w1 + (finishes ? 1 : 0); ++w) {
-                const bool last = w == w1;
+            for (int w = run.w0; w < run.w1 + run.ends; ++w) {
+                const bool last = w == run.w1;
                 if (!last && !open_s[w].b) continue;
                 const float f = ex2((last ? tail[kHeads * D + h] : m_s[w][h]) - u);
-                const float4 v = *reinterpret_cast<const float4 *>(
-                    (last ? tail : pieces_s + (size_t)w * kHeads * D) + h * D + d);
                 l += f * (last ? tail[kHeads * D + kHeads + h] : l_s[w][h]);
-                y[0] += f * v.x;
-                y[1] += f * v.y;
-                y[2] += f * v.z;
-                y[3] += f * v.w;
+                if (in) {
+                    const float4 v = *reinterpret_cast<const float4 *>(
+                        (last ? tail : pieces_s + (size_t)w * kHeads * D) + h * D + d);
+                    y[0] += f * v.x;
+                    y[1] += f * v.y;
+                    y[2] += f * v.z;
+                    y[3] += f * v.w;
+                }
             }
-            if (begins && finishes) {
+            if (run.begins && run.ends) {
                 const float f = row_factor(l, a.v_scale);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] *= f;
-                if (store && a.out)
-                    *reinterpret_cast<float4 *>(a.out + (long long)seq * a.out_stride + (long long)(head0 + h) * D +
-                                                d) = make_float4(y[0], y[1], y[2], y[3]);
+                const int head = run.head + h;
+                if (in && a.out)
+                    *reinterpret_cast<float4 *>(a.out + (long long)run.seq * a.out_stride + (long long)head * D + d) =
+                        make_float4(y[0], y[1], y[2], y[3]);
                 if (a.q8.qs)
-                    q8_block<4, 1, 2, 4>(a.q8, ((size_t)seq * a.Hq + head0 + h) * D + d, y, store, (d & 31) == 0);
-                if (store && a.lse && d == 0) a.lse[(size_t)seq * a.Hq + head0 + h] = row_lse(m, l);
-            } else if (store) {
+                    q8_block<4, 1, 2, 4>(a.q8, ((size_t)run.seq * a.Hq + head) * D + d, y, in, (d & 31) == 0);
+                if (d == 0 && a.lse) a.lse[(size_t)run.seq * a.Hq + head] = row_lse(m, l);
+            } else if (in) {
+                float *to = a.pieces + (size_t)(2 * blockIdx.x + (run.begins ? 1 : 0)) * piece_floats(D);
                 *reinterpret_cast<float4 *>(to + h * D + d) = make_float4(y[0], y[1], y[2], y[3]);
                 if (d == 0) {
                     to[kHeads * D + h] = m;
@@ -758,41 +813,16 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 }
             }
         }
-    };
-    int run = 0;               // first warp of the run at hand
-    bool running = false, begins = false;
-    Meta info{0, 0, 0, 0};     // what this CTA leaves to the second kernel
-    int seq = 0, vh = 0;
-    for (int w = 0; w < kWarps; ++w) {
-        if (head_s[w]) {
-            join(running ? run : w, w, running && begins, true, seq, vh);
-            if (!(running && begins)) info.a = 2;
-            running = false;
-        }
-        if (open_s[w].b) {
-            if (!running) {
-                running = true;
-                run = w;
-                begins = open_s[w].b == 1;
-                seq = open_s[w].seq;
-                vh = open_s[w].vh;
-            }
-        }
     }
-    if (running) {
-        join(run, kWarps, begins, false, seq, vh);
-        if (begins) info.b = 1, info.seq = seq, info.vh = vh;
-        else info.a = 1;
-    }
-    if (tid == 0) meta[blockIdx.x] = info;
 }
 
 // Row blocks that cross CTAs: block (c, h) joins head h of the one that begins
 // in CTA c of the first kernel, from that CTA's piece and those of the CTAs
 // that follow, to the one where it ends.
 template <int D>
-__global__ void __launch_bounds__(kThreads) paged_attn_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas)
+__global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas)
 {
+    constexpr int kThreads = kJoinThreads, kWarps = kJoinThreads / 32;
     __shared__ float w_s[kMaxAttnCtas];
     __shared__ float red_s[kWarps];
     __shared__ int end_s[kWarps];
@@ -802,7 +832,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_join_kernel(const __grid_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, first = blockIdx.x, h = blockIdx.y;
     const Meta *meta = reinterpret_cast<const Meta *>(a.meta);
     const Meta mine = meta[first];
-    if (!mine.b || h >= pass_heads(a, mine.vh)) return;
+    if (!mine.b || h >= mine.heads) return;
 
     int end = ctas;
     for (int i = first + 1 + tid; i < ctas; i += kThreads)
@@ -869,7 +899,7 @@ __global__ void __launch_bounds__(kThreads) paged_attn_join_kernel(const __grid_
     const float f = row_factor(l, a.v_scale);
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] *= f;
-    const int head = pass_head(a, mine.vh) + h;
+    const int head = mine.head + h;
     if (store && a.out)
         *reinterpret_cast<float4 *>(a.out + (long long)mine.seq * a.out_stride + (long long)head * D + 4 * col) =
             make_float4(v[0], v[1], v[2], v[3]);
@@ -901,9 +931,9 @@ cudaError_t launch_one(const PagedAttnArgs &a, int ctas, cudaStream_t st)
     CUtensorMap mk, mv;
     if ((e = make_tmap_u8(&mk, 5, a.k, dims, strides, box, sw)) != cudaSuccess) return e;
     if ((e = make_tmap_u8(&mv, 5, a.v, dims, strides, box, sw)) != cudaSuccess) return e;
-    e = launch_pdl(paged_attn_kernel<D, TYPE>, dim3(ctas), dim3(kThreads), C::kSmem, st, a, mk, mv);
+    e = launch_pdl(paged_attn_kernel<D, TYPE>, dim3(ctas), dim3(C::kThreads), C::kSmem, st, a, mk, mv);
     if (e != cudaSuccess) return e;
-    return launch_pdl(paged_attn_join_kernel<D>, dim3(ctas, a.per_pass), dim3(kThreads), 0, st, a, ctas);
+    return launch_pdl(paged_attn_join_kernel<D>, dim3(ctas, a.per_pass), dim3(kJoinThreads), 0, st, a, ctas);
 }
 
 template <int D>
@@ -930,7 +960,7 @@ size_t pad256(size_t n) { return (n + 255) & ~(size_t)255; }
 size_t paged_attn_workspace(int D)
 {
     const size_t n = (size_t)attn_ctas();
-    return pad256(n * (2 + kWarps) * piece_floats(D) * sizeof(float)) + pad256(n * sizeof(Meta));
+    return pad256(n * (2 + kMaxWarps) * piece_floats(D) * sizeof(float)) + pad256(n * sizeof(Meta));
 }
 
 cudaError_t launch_paged_attn(const PagedAttnArgs &args, int D, int type, void *workspace, cudaStream_t st)
@@ -943,7 +973,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &args, int D, int type, void *
     a.box = a.page_shift > 4 ? kTile : kHalf;   // rows of a page that one copy brings
     a.status = device_status_word();
     a.pieces = static_cast<float *>(workspace);
-    a.meta = static_cast<char *>(workspace) + pad256((size_t)ctas * (2 + kWarps) * piece_floats(D) * sizeof(float));
+    a.meta = static_cast<char *>(workspace) + pad256((size_t)ctas * (2 + kMaxWarps) * piece_floats(D) * sizeof(float));
     switch (D) {
     case 64: return launch_type<64>(a, type, ctas, st);
     case 128: return launch_type<128>(a, type, ctas, st);

@@ -804,7 +804,7 @@ int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, const zq_kv
     if (B < 1 || B > 65535) return fail(ZQ_ERR_SHAPE, "%s: B = %d out of range", name, B);
     if (Hq < Hk || Hq % Hk || Hq / Hk > 64)
         return fail(ZQ_ERR_SHAPE, "%s: Hq = %d must be 1 to 64 times Hk = %d", name, Hq, Hk);
-    if (width < 1 || (long long)width * cache->page > INT32_MAX || (long long)B * Hk * width >= 1LL << 40)
+    if (width < 1 || (long long)width * cache->page > 1 << 30 || (long long)B * Hk * width >= 1LL << 40)
         return fail(ZQ_ERR_SHAPE, "%s: width = %d out of range", name, width);
     if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(ZQ_ERR_ARG, "%s: scale must be positive and finite", name);
     if (window < 0) return fail(ZQ_ERR_ARG, "%s: window must be >= 0", name);

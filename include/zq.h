@@ -540,7 +540,7 @@ ZQ_API int zq_head_norm_rope(const float *q, long long q_stride, const float *k,
  * cache takes q to 2^-22 of its row's largest value), sums fp32.  The result
  * does not change from one call to the next.
  * Shapes: Hq a multiple of Hk, Hq / Hk <= 64, 1 <= B <= 65535, width >= 1,
- * width * page < 2^31, B * Hk * width < 2^40.  strides multiples of 4.
+ * width * page <= 2^30, B * Hk * width < 2^40; strides multiples of 4.
  */
 ZQ_API size_t zq_paged_attn_workspace_bytes(int Hq, int Hk, int D);
 ZQ_API int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, const zq_kv_cache *cache,
