@@ -33,7 +33,7 @@ EXPORTS = ("zq_rmsnorm_q8_1", "zq_q4k_gemv", "zq_q4k_gemv_pair", "zq_q4k_gemm",
            "zq_q5k_bytes", "zq_q6k_bytes", "zq_debug_stream_plan", "zq_debug_peak_probe",
            "zq_debug_wait_expiry", "zq_q8_1_dequant_f16", "zq_f16_gemm_workspace_bytes", "zq_f16_gemm",
            "zq_rmsnorm_q4k_gemm", "zq_copy", "zq_rope_table", "zq_head_norm_rope",
-           "zq_paged_attn_workspace_bytes", "zq_paged_attn")
+           "zq_paged_attn_workspace_bytes", "zq_paged_attn", "zq_lora_workspace_bytes", "zq_lora")
 
 
 class ZQError(RuntimeError):
@@ -103,6 +103,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "zq_head_norm_rope": ([P, ll, P, ll, P, ll, i, i, P, P, f, P, i, i, P, i, P, P, P, ll, P], i),
         "zq_paged_attn_workspace_bytes": ([i, i, i], sz),
         "zq_paged_attn": ([P, ll, i, i, P, P, i, P, f, i, P, ll, P, P, P, sz, P], i),
+        "zq_lora_workspace_bytes": ([i, i, i], sz),
+        "zq_lora": ([_Q8, i, i, P, i, P, P, i, i, P, i, P, ll, P, ll, P, sz, P], i),
         "zq_rmsnorm_q4k_gemm": ([P, P, f, i, i, P, i, P, ctypes.POINTER(_Q8), P, sz, P], i),
     }
     for name, (args, res) in sig.items():
@@ -587,6 +589,52 @@ def paged_attn(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch
                              None if lse is None else lse.data_ptr(), q8, workspace.data_ptr(),
                              workspace.numel() * workspace.element_size(), _stream(stream)))
     return out
+
+
+def lora_workspace_bytes(B: int, K: int, R: int) -> int:
+    return int(load().zq_lora_workspace_bytes(B, K, R))
+
+
+def _out_rows(t: torch.Tensor, B: int, N: int, what: str):
+    """(address, row stride) of fp32 rows [B][N], the values of a row together."""
+    if t.dtype != torch.float32 or t.shape != (B, N) or (N > 1 and t.stride(1) != 1):
+        raise ValueError(f"{what} must be fp32 rows [{B}][{N}]")
+    return t.data_ptr(), t.stride(0) if B > 1 else N
+
+
+def lora(a: Q8_1, ids: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, scales: torch.Tensor | None = None,
+         base: torch.Tensor | None = None, y: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
+         stream=None) -> torch.Tensor:
+    """base + scales[id] B[id] (A[id] x) for every token of the Q8_1 activations,
+    A [n][R][K], Bm [n][N][R], ids int32 [B], an id outside [0, n) for none
+    (see zq_lora); base fp32 [B][N] may be y itself, or None for zeros."""
+    lib = _lib or load()
+    B, K = a.qs.shape
+    n, R, _ = A.shape
+    N = Bm.shape[1]
+    if A.shape[2] != K or Bm.shape != (n, N, R):
+        raise ValueError(f"lora: A must be [n][R][{K}] and Bm [n][N][R]")
+    if A.dtype != Bm.dtype or A.dtype not in (torch.float16, torch.bfloat16):
+        raise ValueError("lora: A and Bm must both be float16 or both bfloat16")
+    if not (A.is_contiguous() and Bm.is_contiguous()):
+        raise ValueError("lora: A and Bm must be contiguous")
+    if not a.qs.is_cuda:
+        raise ValueError("lora: CUDA tensors are needed")
+    dev = a.qs.device
+    if y is None:
+        y = torch.empty((B, N), dtype=torch.float32, device=dev)
+    if workspace is None:
+        workspace = torch.empty(lib.zq_lora_workspace_bytes(B, K, R), dtype=torch.uint8, device=dev)
+    _on(dev.index, "lora", a.d, a.s, ids, A, Bm, scales, base, y, workspace)
+    _q8_planes(a, B, K, "lora: a")
+    yp, ys = _out_rows(y, B, N, "lora: y")
+    bp, bs = (None, 0) if base is None else _out_rows(base, B, N, "lora: base")
+    if scales is not None and (scales.dtype != torch.float32 or scales.numel() != n or not scales.is_contiguous()):
+        raise ValueError(f"lora: scales must be {n} contiguous fp32 values")
+    _check(lib.zq_lora(a._c(), B, K, _ints(ids, B, "lora: ids"), n, A.data_ptr(), Bm.data_ptr(), R, _TYPES[A.dtype],
+                       _ptr(scales), N, bp, bs, yp, ys, workspace.data_ptr(),
+                       workspace.numel() * workspace.element_size(), _stream(stream)))
+    return y
 
 
 # operations per probe launch, by kind (zq_debug_peak_probe)

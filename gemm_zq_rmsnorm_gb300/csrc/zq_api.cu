@@ -846,4 +846,55 @@ int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, const zq_kv
     return launched(launch_paged_attn(a, D, cache->type, workspace, (cudaStream_t)stream), name);
 }
 
+static bool lora_shape(int B, int K, int R)
+{
+    return B >= 1 && B <= 65536 && K >= 32 && K % 32 == 0 && K <= 1 << 20 &&
+           (R == 8 || R == 16 || R == 32 || R == 64);
+}
+
+size_t zq_lora_workspace_bytes(int B, int K, int R) { return lora_shape(B, K, R) ? lora_workspace(B, K, R) : 0; }
+
+int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const void *A, const void *Bm, int R, int type,
+            const float *scales, int N, const float *base, long long base_stride, float *y, long long y_stride,
+            void *workspace, size_t workspace_bytes, void *stream)
+{
+    static const char *name = "zq_lora";
+    if (!a.qs || !a.d || !ids || !A || !Bm || !y) return fail(ZQ_ERR_ARG, "%s: null pointer", name);
+    if (!lora_shape(B, K, R)) return fail(ZQ_ERR_SHAPE, "%s: B = %d, K = %d, R = %d out of range", name, B, K, R);
+    if (n < 1 || n > 1 << 20 || N < 1 || N > 1 << 22)
+        return fail(ZQ_ERR_SHAPE, "%s: n = %d or N = %d out of range", name, n, N);
+    if (type != ZQ_F16 && type != ZQ_BF16) return fail(ZQ_ERR_ARG, "%s: type %d must be f16 or bf16", name, type);
+    if (!aligned16(a.qs) || !aligned16(a.d) || !aligned16(ids) || !aligned16(A) || !aligned16(Bm) ||
+        !aligned16(scales) || !aligned16(workspace))
+        return fail(ZQ_ERR_ALIGN, "%s: codes, ids, weights, scales and workspace must be 16-byte aligned", name);
+    if ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(base)) & 3)
+        return fail(ZQ_ERR_ALIGN, "%s: base and y must be 4-byte aligned", name);
+    if (y_stride < N || y_stride > 1LL << 40 || (base && (base_stride < N || base_stride > 1LL << 40)))
+        return fail(ZQ_ERR_SHAPE, "%s: strides must be at least N = %d", name, N);
+    if (base == y && base_stride != y_stride) return fail(ZQ_ERR_ARG, "%s: base in place needs y's stride", name);
+    int dev, st;
+    if ((st = check_device(&dev))) return st;
+    const size_t need = lora_workspace(B, K, R);
+    if (!workspace || workspace_bytes < need)
+        return fail(ZQ_ERR_WORKSPACE, "%s: workspace of %zu bytes required", name, need);
+    LoraArgs p{};
+    p.qs = a.qs;
+    p.d = a.d;
+    p.B = B;
+    p.K = K;
+    p.ids = ids;
+    p.n = n;
+    p.A = static_cast<const char *>(A);
+    p.Bm = static_cast<const char *>(Bm);
+    p.scales = scales;
+    p.N = N;
+    p.base = base;
+    p.base_stride = base_stride;
+    p.y = y;
+    p.y_stride = y_stride;
+    p.vec = aligned16(y) && y_stride % 4 == 0 && (!base || (aligned16(base) && base_stride % 4 == 0));
+    p.h = static_cast<float *>(workspace);
+    return launched(launch_lora(p, R, type, (cudaStream_t)stream), name);
+}
+
 }  // extern "C"

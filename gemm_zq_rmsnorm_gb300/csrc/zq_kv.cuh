@@ -1,5 +1,5 @@
-// zq_kv.cuh -- the paged key-value cache as the kernels see it, and the
-// rounding of fp32 values to its types.
+// zq_kv.cuh -- launch descriptions of the attention-side and adapter
+// operators, and the rounding of fp32 values to their types.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -92,5 +92,25 @@ struct PagedAttnArgs {
 };
 size_t paged_attn_workspace(int D);
 cudaError_t launch_paged_attn(const PagedAttnArgs &a, int D, int type, void *workspace, cudaStream_t st);
+
+struct LoraArgs {
+    const int8_t *qs;       // activations of B tokens x K
+    const uint16_t *d;
+    int B, K;
+    const int32_t *ids;
+    int n;                  // adapters
+    const char *A, *Bm;
+    const float *scales;    // may be null
+    int N;
+    const float *base;      // may be null, or y
+    long long base_stride;
+    float *y;
+    long long y_stride;
+    int vec;                // base and y rows allow 16-byte pieces
+    float *h;               // workspace [splits][B][R]
+    int splits, per_split;  // set by the launcher
+};
+size_t lora_workspace(int B, int K, int R);
+cudaError_t launch_lora(const LoraArgs &a, int R, int type, cudaStream_t st);
 
 }  // namespace zq

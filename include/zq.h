@@ -548,6 +548,39 @@ ZQ_API int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, cons
                          long long out_stride, float *lse, const zq_q8_1 *q8_out, void *workspace,
                          size_t workspace_bytes, void *stream);
 
+/*
+ * Low-rank adapters of many requests beside a shared projection (no
+ * counterpart on the pages; it reads the Q8_1 activations that the shared
+ * projection of the same tokens reads, ZINC docs "ROCm backend": packed once
+ * and reused):
+ *   y[t] = base[t] + scales[a] * B_a (A_a x_t),  a = ids[t],
+ *   x_t[k] = d8 * q8 of the codes (s is not used).
+ *   a      : Q8_1 of B tokens x K;  ids : int32 [B], an id outside
+ *            [0, n) means no adapter: y[t] = base[t];
+ *   A, Bm  : [n][R][K] and [n][N][R] of `type` ZQ_F16 or ZQ_BF16 (an adapter
+ *            of smaller rank is filled up with zeros);
+ *   scales : fp32 [n], or NULL for 1;
+ *   base   : fp32, row t at base + t * base_stride (the shared projection's
+ *            output), y itself (same stride), or NULL for 0;
+ *   y      : fp32, N values at y + t * y_stride; what lies between the rows
+ *            is not written.  base and y need 4-byte alignment only, so they
+ *            may be columns of a stacked output; 16-byte aligned rows are
+ *            faster;
+ *   workspace : zq_lora_workspace_bytes(B, K, R) bytes, 16-byte aligned;
+ *            contents do not matter.  Calls that may run at the same time need
+ *            workspaces of their own.
+ * Products are exact, sums fp32; A x is rounded only to two 16-bit parts (2^-22
+ * of a token's largest value in f16, 2^-17 in bf16).  The result does not
+ * change from one call to the next, nor with the other tokens of the call's
+ * batch beyond the number of tokens B.
+ * Shapes: 1 <= B <= 65536, K % 32 == 0, 32 <= K <= 2^20, 1 <= N <= 2^22, R 8,
+ * 16, 32 or 64, 1 <= n <= 2^20; strides >= N.
+ */
+ZQ_API size_t zq_lora_workspace_bytes(int B, int K, int R);
+ZQ_API int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const void *A, const void *Bm, int R, int type,
+                   const float *scales, int N, const float *base, long long base_stride, float *y, long long y_stride,
+                   void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif

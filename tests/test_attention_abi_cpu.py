@@ -142,3 +142,40 @@ def test_valid_paged_attn_without_gpu(lib):
         pytest.skip("a GPU is present")
     assert attn(lib) == -5
     assert attn(lib, out=None, os=0, q8=ctypes.byref(zq._Q8(A16, A16, A16))) == -5
+
+
+def lora(lib, q8=None, B=3, K=256, ids=A16, n=2, A=A16, Bm=A16, R=16, type=1, scales=A16, N=64, base=A16, bs=64,
+         y=A16 + 4096, ys=64, ws=A16, wsb=1 << 30):
+    return lib.zq_lora(zq._Q8(A16, A16, A16) if q8 is None else q8, B, K, ids, n, A, Bm, R, type, scales, N, base, bs, y,
+                       ys, ws, wsb, None)
+
+
+@pytest.mark.parametrize("bad,status", [
+    (dict(q8=zq._Q8(None, A16, A16)), -1), (dict(q8=zq._Q8(A8, A16, A16)), -3), (dict(q8=zq._Q8(A16, A8, A16)), -3),
+    (dict(B=0), -2), (dict(B=65537), -2), (dict(K=0), -2), (dict(K=48), -2), (dict(K=(1 << 20) + 32), -2),
+    (dict(ids=None), -1), (dict(ids=A8), -3), (dict(n=0), -2), (dict(n=(1 << 20) + 1), -2), (dict(A=None), -1),
+    (dict(A=A8), -3), (dict(Bm=None), -1), (dict(Bm=A8), -3), (dict(R=0), -2), (dict(R=24), -2), (dict(R=128), -2),
+    (dict(type=3), -1), (dict(type=0), -1), (dict(scales=A8), -3), (dict(N=0), -2), (dict(N=(1 << 22) + 1), -2),
+    (dict(base=A16 + 2), -3), (dict(bs=63), -2), (dict(y=None), -1), (dict(y=A16 + 2), -3), (dict(ys=63), -2),
+    (dict(base=A16, y=A16, bs=64, ys=68), -1), (dict(ws=A8), -3)])
+def test_lora_refuses(lib, bad, status):
+    assert lora(lib, **bad) == status
+    assert lib.zq_last_error()
+
+
+def test_lora_workspace(lib):
+    assert lib.zq_lora_workspace_bytes(0, 256, 16) == 0
+    assert lib.zq_lora_workspace_bytes(4, 100, 16) == 0
+    assert lib.zq_lora_workspace_bytes(4, 256, 12) == 0
+    for B, K, R in ((1, 32, 8), (64, 5120, 16), (512, 17408, 64), (65536, 1024, 8)):
+        need = lib.zq_lora_workspace_bytes(B, K, R)
+        assert need % (B * R * 4) == 0 and 1 <= need // (B * R * 4) <= max(1, -(-K // 1024))
+
+
+def test_valid_lora_without_gpu(lib):
+    torch = pytest.importorskip("torch")
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    assert lora(lib) == -5
+    assert lora(lib, base=None, bs=0, scales=None) == -5
+    assert lora(lib, base=A16 + 4096) == -5       # in place
