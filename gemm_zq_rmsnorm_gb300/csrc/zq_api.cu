@@ -882,6 +882,7 @@ int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const void *A, c
     p.d = a.d;
     p.B = B;
     p.K = K;
+    p.R = R;
     p.ids = ids;
     p.n = n;
     p.A = static_cast<const char *>(A);
@@ -894,7 +895,7 @@ int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const void *A, c
     p.y_stride = y_stride;
     p.vec = aligned16(y) && y_stride % 4 == 0 && (!base || (aligned16(base) && base_stride % 4 == 0));
     p.h = static_cast<float *>(workspace);
-    return launched(launch_lora(p, R, type, (cudaStream_t)stream), name);
+    return launched(launch_lora(p, type, (cudaStream_t)stream), name);
 }
 
 }  // extern "C"

@@ -59,6 +59,13 @@ __device__ __forceinline__ void st_cluster_u32(uint32_t cl_addr, uint32_t v)
     asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cl_addr), "r"(v) : "memory");
 }
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cl_addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cl_addr) : "memory");
+    return v;
+}
+
 // Phase test of a barrier whose arrivals may come from the peer CTA (its
 // converter and epilogue warps' st.async bytes, its TMA bytes, the pair's MMA
 // commits).  Default (CTA-scope acquire) semantics: the peer's signals are

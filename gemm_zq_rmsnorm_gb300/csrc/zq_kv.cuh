@@ -96,7 +96,7 @@ cudaError_t launch_paged_attn(const PagedAttnArgs &a, int D, int type, void *wor
 struct LoraArgs {
     const int8_t *qs;       // activations of B tokens x K
     const uint16_t *d;
-    int B, K;
+    int B, K, R;
     const int32_t *ids;
     int n;                  // adapters
     const char *A, *Bm;
@@ -107,10 +107,10 @@ struct LoraArgs {
     float *y;
     long long y_stride;
     int vec;                // base and y rows allow 16-byte pieces
-    float *h;               // workspace [splits][B][R]
-    int splits, per_split;  // set by the launcher
+    float *h;               // workspace [parts][B][R]
+    int cluster, parts, per_split;   // set by the launcher
 };
 size_t lora_workspace(int B, int K, int R);
-cudaError_t launch_lora(const LoraArgs &a, int R, int type, cudaStream_t st);
+cudaError_t launch_lora(const LoraArgs &a, int type, cudaStream_t st);
 
 }  // namespace zq
