@@ -7,11 +7,11 @@
 // expansion of h by B_a onto base.  Bound: HBM, the adapters once, and base and
 // y (8 B N bytes), which dominate; a few tokens are launch bound.
 //
-// Tokens come in tiles of 32.  Each warp finds the distinct adapters of its tile
-// itself (one match of the lanes' ids) and takes the members of one after the
-// other as the columns of its MMAs, eight at a time, so a prompt's tokens share
-// each adapter row and a decode batch reads each of its adapters once a tile; no
-// sorting pass, no plan to keep, any mixture of both.
+// Tokens come in tiles of 64.  A CTA sorts its tile's tokens by adapter itself
+// (64 ids: a scan of comparisons) and takes them eight at a time as the columns
+// of its MMAs, so a prompt's tokens share each adapter row and a decode batch
+// reads each of its adapters once a tile; no sorting pass, no plan to keep, any
+// mixture of both.
 //
 // First kernel: m16n8k16 with adapter rows as the 16-row operand and tokens as
 // the columns.  The order of K inside a step is free, so lane 4g + c loads 8
@@ -35,14 +35,18 @@
 namespace zq {
 namespace {
 
-constexpr int kTokens = 32;      // tokens of a tile: a warp's lanes, and four MMAs' columns
-constexpr int kQ = kTokens / 8;
-constexpr int kThreads = 256;
+constexpr int kTokens = 64;      // tokens of a tile
+constexpr int kQ = 4;            // groups of eight members a unit has at most
+constexpr int kThreads = 256;    // first kernel
 constexpr int kWarps = kThreads / 32;
 constexpr int kDownRows = 32;    // rows of A a CTA of the first kernel takes at most
 constexpr int kCluster = 8;      // CTAs of a cluster at most, which add up their K ranges
 constexpr int kParts = 4;        // sums the second kernel is left with at most
-constexpr int kCols = 32 * kWarps;   // outputs of a CTA of the second kernel
+constexpr int kUpThreads = 128;  // second kernel
+constexpr int kUpWarps = kUpThreads / 32;
+constexpr int kUpGroups = 16;    // groups whose h it has in shared memory at a time
+constexpr int kBlock = 32;       // outputs of a warp at a time
+constexpr int kNone = 255;
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int TYPE>
@@ -98,32 +102,83 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t &lo, uint32_t &hi)
     }
 }
 
-// A tile's tokens by adapter, found by each warp for itself.
+// A tile's tokens by adapter: each adapter's tokens in groups of eight (an
+// MMA's columns), its groups in units of up to four.
 struct Tile {
-    int id;           // adapter of token `lane`, -1: none (or past the last token)
-    uint32_t lead;    // tokens that are the first of their adapter
+    int id[kTokens];               // adapter of a token, -1: none (or past the last token)
+    int base[kTokens];             // first group of a token's adapter, at the adapter's first token
+    int half, groups, units;       // groups | units << 16 of the lower 32 tokens; in all
+    int adapter[kTokens];          // of a group
+    uint32_t tok[kTokens][2];      // tokens of a group's eight columns, a byte each, kNone: no more
+    uint8_t unit[kTokens], unit_groups[kTokens];   // first group of a unit, number of its groups
 
-    __device__ __forceinline__ void open(const LoraArgs &a, int tile)
+    __device__ __forceinline__ int token(int group, int col) const
     {
-        const int lane = threadIdx.x & 31, t = tile * kTokens + lane;
-        id = t < a.B ? a.ids[t] : -1;
-        if (id < 0 || id >= a.n) id = -1;
-        const uint32_t same = __match_any_sync(kAll, id);   // by every lane, adapter or none
-        lead = __ballot_sync(kAll, id >= 0 && __ffs((int)same) - 1 == lane);
-    }
-    // Tokens of the j-th adapter, and the adapter; 0: there are no more.
-    __device__ __forceinline__ uint32_t members(int j, int &adapter) const
-    {
-        uint32_t m = lead;
-        for (int i = 0; i < j && m; ++i) m &= m - 1;
-        if (m == 0) return 0;
-        adapter = __shfl_sync(kAll, id, __ffs((int)m) - 1);
-        return __ballot_sync(kAll, id == adapter);
+        return reinterpret_cast<const uint8_t *>(tok[group])[col];
     }
 };
 
+__device__ __forceinline__ void tile_open(Tile &s, const LoraArgs &a, int tile)
+{
+    const int t = threadIdx.x, lane = t & 31;
+    int id = -1;
+    if (t < kTokens) {
+        const int at = tile * kTokens + t;
+        if (at < a.B) id = a.ids[at];
+        if (id < 0 || id >= a.n) id = -1;
+        s.id[t] = id;
+        s.tok[t][0] = s.tok[t][1] = 0xffffffffu;
+    }
+    __syncthreads();
+    int before = 0, total = 0, first = t, incl = 0, own = 0;
+    if (t < kTokens) {
+#pragma unroll
+        for (int j = 0; j < kTokens; j += 4) {
+            const int4 o = *reinterpret_cast<const int4 *>(s.id + j);
+            const int v[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const bool same = v[k] == id;
+                total += same;
+                before += same && j + k < t;
+                if (same) first = min(first, j + k);
+            }
+        }
+        if (id >= 0 && before == 0) {
+            const int groups = (total + 7) / 8;
+            own = groups | (groups + kQ - 1) / kQ << 16;
+        }
+        incl = own;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int up = __shfl_up_sync(kAll, incl, off);
+            if (lane >= off) incl += up;
+        }
+        if (t == 31) s.half = incl;
+    }
+    __syncthreads();
+    if (t < kTokens) {
+        if (t >= 32) incl += s.half;
+        if (t == kTokens - 1) {
+            s.groups = incl & 0xffff;
+            s.units = incl >> 16;
+        }
+        const int at = (incl - own) & 0xffff, unit = (incl - own) >> 16, n = own & 0xffff;
+        s.base[t] = at;
+        for (int i = 0; i < n; ++i) s.adapter[at + i] = id;
+        for (int i = 0; i < own >> 16; ++i) {
+            s.unit[unit + i] = (uint8_t)(at + kQ * i);
+            s.unit_groups[unit + i] = (uint8_t)min(kQ, n - kQ * i);
+        }
+    }
+    __syncthreads();
+    if (t < kTokens && id >= 0)
+        reinterpret_cast<uint8_t *>(s.tok[s.base[first] + before / 8])[before % 8] = (uint8_t)t;
+    __syncthreads();
+}
+
 // h[part][t][r] = sum over the part's K of A[a][r][k] x[t][k].  Grid: (tiles
-// and groups of RR rows, adapters of a tile at the same time, K ranges); the
+// and groups of RR rows, units of a tile at the same time, K ranges); the
 // ranges of a cluster are added up through distributed shared memory into one
 // part.
 template <int RR, int TYPE>
@@ -131,35 +186,28 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
 {
     constexpr int kRows = RR < 16 ? 1 : RR / 16;   // 16-row operands
     __shared__ float red[kWarps / 2][kRows][kQ][4][32];
-    __shared__ uint8_t list_s[kWarps][kTokens];
+    __shared__ __align__(16) Tile tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();   // codes and ids come from earlier kernels
     pdl_launch_dependents();
     const int halves = a.R / RR, row0 = (int)blockIdx.x % halves * RR;
     const size_t tok0 = (size_t)(blockIdx.x / halves) * kTokens;
-    Tile tile;
-    tile.open(a, blockIdx.x / halves);
+    tile_open(tile, a, blockIdx.x / halves);
     const int blocks = a.K >> 5;
     const int b0 = min(blocks, (int)blockIdx.z * a.per_split), b1 = min(blocks, b0 + a.per_split);
     const int rank = blockIdx.z % a.cluster;
     float *h = a.h + (size_t)(blockIdx.z / a.cluster) * a.B * a.R + row0;
 
-    for (int j = blockIdx.y;; j += gridDim.y) {
-        int adapter;
-        const uint32_t mask = tile.members(j, adapter);   // the same in all CTAs of the cluster
-        if (mask == 0) return;
-        const int members = __popc(mask);
-        __syncwarp();
-        if (mask >> lane & 1) list_s[warp][__popc(mask & ((1u << lane) - 1))] = (uint8_t)lane;
-        __syncwarp();
-        const int nq = (members + 7) / 8;   // MMAs' columns in use
+    for (int u = blockIdx.y; u < tile.units; u += gridDim.y) {   // the same in all CTAs of the cluster
+        const int group0 = tile.unit[u], nq = tile.unit_groups[u], adapter = tile.adapter[group0];
         const char *A = a.A + (((size_t)adapter * a.R + row0 + g) * a.K + 8 * c) * 2;
         const size_t step = (size_t)8 * a.K * 2;   // eight rows on
         const int8_t *x[kQ];
         const uint16_t *d[kQ];
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {   // columns past the last member repeat it, unused
-            const size_t t = tok0 + list_s[warp][min(members - 1, 8 * q + g)];
+        for (int q = 0; q < kQ; ++q) {   // columns without a member repeat the first, unused
+            const int of = q < nq ? tile.token(group0 + q, g) : kNone;
+            const size_t t = tok0 + (of == kNone ? tile.token(group0, 0) : of);
             x[q] = a.qs + t * a.K + 8 * c;
             d[q] = a.d + t * blocks;
         }
@@ -256,11 +304,12 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
         const uint32_t local = smem_u32(&red[0][0][0][0][0]);
         for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += kThreads) {
             const int l = i & 31, e = i >> 5 & 3, q = i >> 7 & (kQ - 1), r = i / (kQ * 128);
-            const int m = 8 * q + 2 * (l & 3) + (e & 1), row = 16 * r + 8 * (e >> 1) + (l >> 2);
-            if (m < members && row < RR) {
+            const int row = 16 * r + 8 * (e >> 1) + (l >> 2);
+            const int of = q < nq ? tile.token(group0 + q, 2 * (l & 3) + (e & 1)) : kNone;
+            if (of != kNone && row < RR) {
                 float v = 0.0f;
                 for (int k = 0; k < a.cluster; ++k) v += ld_cluster_f32(cluster_addr(local + 4 * i, k));
-                h[(tok0 + list_s[warp][m]) * a.R + row] = v;
+                h[(tok0 + of) * a.R + row] = v;
             }
         }
         __syncwarp();
@@ -268,90 +317,98 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
     }
 }
 
-// y[t] = base[t] + scale_a B_a h_t for the CTA's kCols outputs.  Grid: (tiles,
-// column blocks, adapters of a tile at the same time).
+// y[t] = base[t] + scale_a B_a h_t.  Grid: (tiles, column ranges of a.blocks
+// blocks of 32).  A task is one block for one group of eight tokens; a warp takes
+// neighbouring tasks of one block after the other, the next one's values on
+// their way while it works on one.
 template <int R, int TYPE>
-__global__ void __launch_bounds__(kThreads) lora_up_kernel(const __grid_constant__ LoraArgs a)
+__global__ void __launch_bounds__(kUpThreads, 5) lora_up_kernel(const __grid_constant__ LoraArgs a)
 {
     constexpr int kSteps = R < 16 ? 1 : R / 16;
     constexpr int kRun = R < 32 ? R / 4 : 8;   // neighbouring values of R that a lane's fragment takes
-    __shared__ uint8_t list_s[kWarps][kTokens];
-    __shared__ float back_s[kTokens];          // 2^e of a token's scaling
-    __shared__ uint2 hi_s[kQ][kSteps][32], lo_s[kQ][kSteps][32];
+    __shared__ __align__(16) Tile tile;
+    __shared__ uint4 h_s[kUpGroups][kSteps][32];      // fragments of h: x, y the upper parts, z, w the lower ones
+    __shared__ float back_s[kUpGroups][8];            // 2^e of a member's scaling
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const size_t tok0 = (size_t)blockIdx.x * kTokens;
-    const int warp0 = blockIdx.y * kCols + 32 * warp;   // a whole warp has outputs, or none
-    const int n0 = warp0 + 4 * g;                       // this lane's four outputs
-    const bool vec = a.vec && warp0 + 32 <= a.N;        // they are all there, and aligned
+    const int block0 = blockIdx.y * a.blocks, blocks = min(a.blocks, (a.N + kBlock - 1) / kBlock - block0);
     // The first kernel lets this one start only when all before it is complete:
     // ids, base and weights may be read ahead of the wait, h may not.
-    Tile tile;
-    tile.open(a, blockIdx.x);
+    tile_open(tile, a, blockIdx.x);
     bool waited = false;
 
-    for (int j = blockIdx.z;; j += gridDim.z) {
-        int adapter;
-        const uint32_t mask = tile.members(j, adapter);
-        if (mask == 0) break;
-        const int members = __popc(mask), groups = (members + 7) / 8;
-        __syncthreads();   // the previous adapter's fragments have been used
-        if (mask >> lane & 1) list_s[warp][__popc(mask & ((1u << lane) - 1))] = (uint8_t)lane;
-        __syncwarp();
+    struct Task {
         uint32_t w[2][kSteps][4];   // fragments of rows n0 + 2i (upper) and n0 + 2i + 1 (lower)
+        float4 v[2];                // base of columns 2c, 2c + 1
+    };
+    auto fetch = [&](int group, int n0, bool vec, bool weights, Task &f) {
+        if (weights) {
+            const char *row0 = a.Bm + (size_t)tile.adapter[group] * a.N * R * 2 + kRun * 2 * c;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const char *row = a.Bm + ((size_t)adapter * a.N + min(a.N - 1, n0 + i)) * R * 2 + kRun * 2 * c;
-            if constexpr (R == 8) {
-                w[i >> 1][0][i & 1] = __ldg(reinterpret_cast<const uint32_t *>(row));
-                w[i >> 1][0][2 + (i & 1)] = 0;
-            } else if constexpr (R == 16) {
-                const uint2 f = __ldg(reinterpret_cast<const uint2 *>(row));
-                w[i >> 1][0][i & 1] = f.x;
-                w[i >> 1][0][2 + (i & 1)] = f.y;
-            } else {
+            for (int i = 0; i < 4; ++i) {
+                const char *row = row0 + (size_t)min(a.N - 1, n0 + i) * R * 2;
+                if constexpr (R == 8) {
+                    f.w[i >> 1][0][i & 1] = __ldg(reinterpret_cast<const uint32_t *>(row));
+                    f.w[i >> 1][0][2 + (i & 1)] = 0;
+                } else if constexpr (R == 16) {
+                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(row));
+                    f.w[i >> 1][0][i & 1] = x.x;
+                    f.w[i >> 1][0][2 + (i & 1)] = x.y;
+                } else {
 #pragma unroll
-                for (int s = 0; s < kSteps / 2; ++s) {
-                    const uint4 f = __ldg(reinterpret_cast<const uint4 *>(row + 64 * s));
-                    w[i >> 1][2 * s][i & 1] = f.x;
-                    w[i >> 1][2 * s][2 + (i & 1)] = f.y;
-                    w[i >> 1][2 * s + 1][i & 1] = f.z;
-                    w[i >> 1][2 * s + 1][2 + (i & 1)] = f.w;
-                }
-            }
-        }
-        float4 v[kQ][2];        // base of the members 8q + 2c, 8q + 2c + 1
-#pragma unroll
-        for (int q = 0; q < kQ; ++q)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int m = 8 * q + 2 * c + e;
-                v[q][e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (a.base && m < members) {
-                    const float *p = a.base + (tok0 + list_s[warp][m]) * a.base_stride + n0;
-                    if (vec) {
-                        v[q][e] = *reinterpret_cast<const float4 *>(p);
-                    } else {
-                        if (n0 < a.N) v[q][e].x = p[0];
-                        if (n0 + 1 < a.N) v[q][e].y = p[1];
-                        if (n0 + 2 < a.N) v[q][e].z = p[2];
-                        if (n0 + 3 < a.N) v[q][e].w = p[3];
+                    for (int s = 0; s < kSteps / 2; ++s) {
+                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row + 64 * s));
+                        f.w[i >> 1][2 * s][i & 1] = x.x;
+                        f.w[i >> 1][2 * s][2 + (i & 1)] = x.y;
+                        f.w[i >> 1][2 * s + 1][i & 1] = x.z;
+                        f.w[i >> 1][2 * s + 1][2 + (i & 1)] = x.w;
                     }
                 }
             }
+        }
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int t = tile.token(group, 2 * c + e);
+            f.v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (a.base && t != kNone) {
+                const float *p = a.base + (tok0 + t) * a.base_stride + n0;
+                if (vec) {
+                    f.v[e] = *reinterpret_cast<const float4 *>(p);
+                } else {
+                    if (n0 < a.N) f.v[e].x = p[0];
+                    if (n0 + 1 < a.N) f.v[e].y = p[1];
+                    if (n0 + 2 < a.N) f.v[e].z = p[2];
+                    if (n0 + 3 < a.N) f.v[e].w = p[3];
+                }
+            }
+        }
+    };
+
+    for (int g0 = 0; g0 < tile.groups; g0 += kUpGroups) {
+        const int n = min(kUpGroups, tile.groups - g0);
+        // this warp's tasks, block by block
+        const int t0 = warp * blocks * n / kUpWarps, t1 = (warp + 1) * blocks * n / kUpWarps;
+        int block = t0 / n, group = t0 - block * n;
+        auto col0 = [&](int block) { return (block0 + block) * kBlock + 4 * g; };
+        auto aligned = [&](int block) { return a.vec && (block0 + block + 1) * kBlock <= a.N; };
+        Task now;
+        if (t0 < t1) fetch(g0 + group, col0(block), aligned(block), true, now);
         if (!waited) {
             pdl_wait();
             pdl_launch_dependents();
             waited = true;
         }
-        // h of the members: its parts in order, times the adapter's scale, as two 16-bit parts in the order of
-        // the fragments; R / 4 neighbouring threads have a token, four values each
-        const float scale = a.scales ? a.scales[adapter] : 1.0f;
-        const int items = groups * 8 * (R / 4);
-        for (int i = tid; i < (items + 31) / 32 * 32; i += kThreads) {
-            const int m = i / (R / 4), r = i % (R / 4) * 4;
+        // h of the groups' members: its parts in order, times the adapter's scale, as two 16-bit parts in the
+        // fragments' order; R / 4 neighbouring threads have a member, four values each
+        const int items = n * 8 * (R / 4);
+        for (int i = tid; i < (items + 31) / 32 * 32; i += kUpThreads) {
+            const int m = min(i / (R / 4), n * 8 - 1), r = i % (R / 4) * 4;
+            const int of = tile.token(g0 + m / 8, m % 8);
             float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (m < members) {
-                const float *h = a.h + (tok0 + list_s[warp][m]) * R + r;
+            float scale = 1.0f;
+            if (of != kNone) {
+                if (a.scales) scale = a.scales[tile.adapter[g0 + m / 8]];
+                const float *h = a.h + (tok0 + of) * R + r;
 #pragma unroll
                 for (int s = 0; s < kParts; ++s)
                     if (s < a.parts) {
@@ -363,15 +420,16 @@ __global__ void __launch_bounds__(kThreads) lora_up_kernel(const __grid_constant
                     }
             }
             float x[4] = {scale * f.x, scale * f.y, scale * f.z, scale * f.w};
-            if (TYPE == ZQ_F16) {   // binary16 parts need the row near 1
+            float up = 1.0f;
+            if constexpr (TYPE == ZQ_F16) {   // binary16 parts need the row near 1
                 float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
                 for (int off = 1; off < R / 4; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
                 const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
                 const float down = __int_as_float((127 - e) << 23);
+                up = __int_as_float((127 + e) << 23);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x[k] *= down;
-                if (r == 0 && i < items) back_s[m] = __int_as_float((127 + e) << 23);
             }
             uint32_t hi[2], lo[2];
 #pragma unroll
@@ -384,44 +442,64 @@ __global__ void __launch_bounds__(kThreads) lora_up_kernel(const __grid_constant
                 lo[k] = kv_pack2<TYPE>(x[2 * k] - y.x, x[2 * k + 1] - y.y);
             }
             if (i < items) {
-                const int q = m >> 3, l = (m & 7) * 4;
+                const int l = m % 8 * 4;
+                if (r == 0) back_s[m / 8][m % 8] = up;
                 if constexpr (R == 8) {   // two lanes' pairs; their second registers are zeros
-                    hi_s[q][0][l + r / 2] = make_uint2(hi[0], 0);
-                    hi_s[q][0][l + r / 2 + 1] = make_uint2(hi[1], 0);
-                    lo_s[q][0][l + r / 2] = make_uint2(lo[0], 0);
-                    lo_s[q][0][l + r / 2 + 1] = make_uint2(lo[1], 0);
+                    h_s[m / 8][0][l + r / 2] = make_uint4(hi[0], 0, lo[0], 0);
+                    h_s[m / 8][0][l + r / 2 + 1] = make_uint4(hi[1], 0, lo[1], 0);
                 } else {                  // one lane's values of a step
                     const int s = R == 16 ? 0 : 2 * (r / 32) + (r >> 2 & 1);
-                    const int to = l + (R == 16 ? r / 4 : (r & 31) >> 3);
-                    hi_s[q][s][to] = make_uint2(hi[0], hi[1]);
-                    lo_s[q][s][to] = make_uint2(lo[0], lo[1]);
+                    h_s[m / 8][s][l + (R == 16 ? r / 4 : (r & 31) >> 3)] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
                 }
             }
         }
         __syncthreads();
-        if (warp0 >= a.N) continue;
+        for (int task = t0; task < t1; ++task) {
+            const int here = group, n0 = col0(block);
+            const bool vec = aligned(block);
+            // the next task: the block's next group, or the next block's first
+            const int adapter = tile.adapter[g0 + group];
+            bool weights = false;
+            if (++group == n) {
+                group = 0;
+                ++block;
+                weights = true;
+            }
+            Task next;
+            if (task + 1 < t1) {
+                weights |= tile.adapter[g0 + group] != adapter;
+                if (!weights) {
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {
-            if (q >= groups) break;
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) next.w[i][s][k] = now.w[i][s][k];
+                }
+                fetch(g0 + group, col0(block), aligned(block), weights, next);
+            }
             float p[2][4];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                const uint2 hi = hi_s[q][s][lane], lo = lo_s[q][s][lane];
+                const uint4 f = h_s[here][s][lane];
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    if (s == 0) mma16_first<TYPE>(p[i], w[i][s][0], w[i][s][1], w[i][s][2], w[i][s][3], lo.x, lo.y);
-                    else mma16<TYPE>(p[i], w[i][s][0], w[i][s][1], w[i][s][2], w[i][s][3], lo.x, lo.y);
-                    mma16<TYPE>(p[i], w[i][s][0], w[i][s][1], w[i][s][2], w[i][s][3], hi.x, hi.y);
+                    if (s == 0)
+                        mma16_first<TYPE>(p[i], now.w[i][s][0], now.w[i][s][1], now.w[i][s][2], now.w[i][s][3], f.z,
+                                          f.w);
+                    else
+                        mma16<TYPE>(p[i], now.w[i][s][0], now.w[i][s][1], now.w[i][s][2], now.w[i][s][3], f.z, f.w);
+                    mma16<TYPE>(p[i], now.w[i][s][0], now.w[i][s][1], now.w[i][s][2], now.w[i][s][3], f.x, f.y);
                 }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int m = 8 * q + 2 * c + e;
-                if (m < members) {
-                    const float f = TYPE == ZQ_F16 ? back_s[m] : 1.0f;
-                    float *to = a.y + (tok0 + list_s[warp][m]) * a.y_stride + n0;
-                    const float4 y = make_float4(v[q][e].x + p[0][e] * f, v[q][e].y + p[0][2 + e] * f,
-                                                 v[q][e].z + p[1][e] * f, v[q][e].w + p[1][2 + e] * f);
+                const int t = tile.token(g0 + here, 2 * c + e);
+                if (t != kNone) {
+                    const float f = TYPE == ZQ_F16 ? back_s[here][2 * c + e] : 1.0f;
+                    float *to = a.y + (tok0 + t) * a.y_stride + n0;
+                    const float4 y = make_float4(now.v[e].x + p[0][e] * f, now.v[e].y + p[0][2 + e] * f,
+                                                 now.v[e].z + p[1][e] * f, now.v[e].w + p[1][2 + e] * f);
                     if (vec) {
                         *reinterpret_cast<float4 *>(to) = y;
                     } else {
@@ -433,18 +511,22 @@ __global__ void __launch_bounds__(kThreads) lora_up_kernel(const __grid_constant
                 }
             }
             __syncwarp();
+            now = next;
         }
+        __syncthreads();   // the fragments have been used
     }
     if (!waited) {
         pdl_wait();
         pdl_launch_dependents();
     }
     // tokens without an adapter
-    if (blockIdx.z == 0 && a.base != a.y) {
-        const int col = blockIdx.y * kCols + tid;
-        for (int i = 0; i < kTokens && tok0 + i < (size_t)a.B; ++i)
-            if (__shfl_sync(kAll, tile.id, i) < 0 && col < a.N)
+    if (a.base != a.y) {
+        const int n0 = block0 * kBlock, n1 = min(a.N, n0 + blocks * kBlock);
+        for (int i = warp; i < kTokens && tok0 + i < (size_t)a.B; i += kUpWarps) {
+            if (tile.id[i] >= 0) continue;
+            for (int col = n0 + lane; col < n1; col += 32)
                 a.y[(tok0 + i) * a.y_stride + col] = a.base ? a.base[(tok0 + i) * a.base_stride + col] : 0.0f;
+        }
     }
 }
 
@@ -466,7 +548,7 @@ cudaError_t launch_rank(const LoraArgs &a, dim3 down, dim3 up, cudaStream_t st)
     cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, lora_down_kernel<(R < kDownRows ? R : kDownRows), TYPE>, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(lora_up_kernel<R, TYPE>, up, dim3(kThreads), 0, st, a);
+    return launch_pdl(lora_up_kernel<R, TYPE>, up, dim3(kUpThreads), 0, st, a);
 }
 
 template <int TYPE>
@@ -509,16 +591,17 @@ cudaError_t launch_lora(const LoraArgs &args, int type, cudaStream_t st)
     a.parts = cut.parts;
     a.per_split = cut.per_split;
     const int splits = cut.cluster * cut.parts, halves = a.R > kDownRows ? a.R / kDownRows : 1;
-    const int cols = (a.N + kCols - 1) / kCols;
-    // adapters of a tile taken at the same time: as many as there can be, while
-    // the grid is not several times the GPU already (a CTA takes the others in turn)
-    auto at_once = [&](long long others) {
-        const int most = min(a.n, min(a.B, kTokens));
-        const long long n = 8LL * num_sms() / others;
-        return (unsigned)(n < 1 ? 1 : n > most ? most : n);
-    };
-    const dim3 down(cut.tiles * halves, at_once((long long)cut.tiles * halves * splits), splits);
-    const dim3 up(cut.tiles, cols, at_once((long long)cut.tiles * cols));
+    // units of a tile taken at the same time: as many as there can be, while the
+    // grid is not several times the GPU already (a CTA takes the others in turn)
+    const int most = min(a.n, min(a.B, kTokens)) + (a.B > 8 * kQ ? 1 : 0);
+    const long long room = 8LL * num_sms() / ((long long)cut.tiles * halves * splits);
+    const dim3 down(cut.tiles * halves, (unsigned)(room < 1 ? 1 : room > most ? most : room), splits);
+    // column blocks of a CTA of the second kernel: a power of two that leaves
+    // about six CTAs for every SM
+    const long long cols = (a.N + kBlock - 1) / kBlock;
+    a.blocks = 1;
+    while (a.blocks < 64 && cols * cut.tiles > 6LL * num_sms() * a.blocks) a.blocks *= 2;
+    const dim3 up(cut.tiles, (unsigned)((cols + a.blocks - 1) / a.blocks));
     return type == ZQ_BF16 ? launch_type<ZQ_BF16>(a, down, up, st) : launch_type<ZQ_F16>(a, down, up, st);
 }
 

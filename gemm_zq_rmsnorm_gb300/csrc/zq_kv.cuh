@@ -108,7 +108,7 @@ struct LoraArgs {
     long long y_stride;
     int vec;                // base and y rows allow 16-byte pieces
     float *h;               // workspace [parts][B][R]
-    int cluster, parts, per_split;   // set by the launcher
+    int cluster, parts, per_split, blocks;   // set by the launcher
 };
 size_t lora_workspace(int B, int K, int R);
 cudaError_t launch_lora(const LoraArgs &a, int type, cudaStream_t st);
