@@ -127,12 +127,46 @@ __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uin
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same onto zero
+template <int TYPE>
+__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                          uint32_t b0, uint32_t b1)
+{
+    if constexpr (TYPE == ZQ_BF16)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                     "{%10,%10,%10,%10};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
+}
+
 // 8 x 8 transpose of 16-bit values across the warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t x)
 {
     uint32_t y;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
     return y;
+}
+
+// Four 8 x 8 matrices of 16-bit values, rows of 16 bytes at the lanes'
+// addresses (lanes 8i .. 8i + 7: matrix i); TRANS: transposed
+template <bool TRANS>
+__device__ __forceinline__ void ldmatrix4(uint32_t addr, uint32_t &r0, uint32_t &r1, uint32_t &r2, uint32_t &r3)
+{
+    if constexpr (TRANS)
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                     : "r"(addr)
+                     : "memory");
+    else
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r0), "=r"(r1), "=r"(r2), "=r"(r3)
+                     : "r"(addr)
+                     : "memory");
 }
 
 // four e4m3 values to binary16 (exact): the lower two, the upper two
@@ -200,6 +234,32 @@ __device__ __forceinline__ void q8_block(const zq_q8_1 &o, size_t at, const floa
 #pragma unroll
     for (int w = 0; w < N / 4; ++w) reinterpret_cast<uint32_t *>(o.qs + at)[w] = word[w];
     if (first) {
+        o.d[at >> 5] = __half_as_ushort(__float2half_rn(d));
+        o.s[at >> 5] = __half_as_ushort(__float2half_rn(__fmul_rn(d, (float)sum)));
+    }
+}
+
+// The same for the lanes with one c and g = 0 .. 7, each with the values 8k + g
+// of the block that begins at `at`.
+__device__ __forceinline__ void q8_block_strided(const zq_q8_1 &o, size_t at, const float (&v)[4], int g, bool store)
+{
+    float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));
+#pragma unroll
+    for (int off = 4; off <= 16; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
+    const float d = __fdiv_rn(amax, 127.0f);
+    const float id = d != 0.0f ? __fdiv_rn(1.0f, d) : 0.0f;
+    int sum = 0, q[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        q[k] = (int)fminf(fmaxf(roundf(__fmul_rn(v[k], id)), -127.0f), 127.0f);
+        sum += q[k];
+    }
+#pragma unroll
+    for (int off = 4; off <= 16; off <<= 1) sum += __shfl_xor_sync(kAll, sum, off);
+    if (!store) return;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o.qs[at + 8 * k + g] = (int8_t)q[k];
+    if (g == 0) {
         o.d[at >> 5] = __half_as_ushort(__float2half_rn(d));
         o.s[at >> 5] = __half_as_ushort(__float2half_rn(__fmul_rn(d, (float)sum)));
     }
@@ -424,12 +484,36 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
 #pragma unroll 1
     for (int i = 0; i < C::kSlots; ++i) issue();
 
+    // 16-bit rows: a lane's row of the matrices that make a fragment, k-step (or 16 columns) 0 of a segment
+    const uint32_t ring_a = smem_u32(ring);
+    const int lane_k = ((lane & 15) << 7) + (((lane >> 4) ^ (lane & 7)) << 4);
+    const int lane_v = (((lane & 7) + (lane >> 4 << 3)) << 7) + (((lane >> 3 & 1) ^ (lane & 7)) << 4);
+
     int slot = 0;
     float o[D / 16][4];
     float m0 = 0, m1 = 0, l0 = 0, l1 = 0;
     int has_head = 0;
     Meta open{0, 0, 0, 0, 0};
     float *head_piece = a.pieces + ((size_t)2 * gridDim.x + (size_t)gw) * piece_floats(D);
+
+    // the output as it stands, eight rows of D
+    auto put_rows = [&](float *to) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float *row = to + (2 * c + e) * D;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+                if constexpr (TYPE == ZQ_E4M3) {
+                    constexpr int kPairs = C::kVRun / 2;
+                    *reinterpret_cast<float2 *>(row + (8 * (i / kPairs) + g) * C::kVRun + 2 * (i % kPairs)) =
+                        make_float2(o[i][e], o[i][2 + e]);
+                } else {
+                    row[16 * i + g] = o[i][e];
+                    row[16 * i + 8 + g] = o[i][2 + e];
+                }
+            }
+        }
+    };
 
     while (left > 0) {
         const int n = (int)min(left, (long long)(at.tend - at.t));
@@ -442,14 +526,23 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         {
             float x[D / 4];
             const float *qr = a.q + (long long)at.b * a.q_stride + (long long)(head0 + min(g, heads - 1)) * D;
+            if constexpr (TYPE == ZQ_E4M3) {   // the columns of the lane's chunks
 #pragma unroll
-            for (int s = 0; s < D / (4 * C::kKRun); ++s)
+                for (int s = 0; s < D / (4 * C::kKRun); ++s)
 #pragma unroll
-                for (int i = 0; i < C::kKRun / 4; ++i) {
-                    const float4 f = *reinterpret_cast<const float4 *>(qr + (4 * s + c) * C::kKRun + 4 * i);
-                    float *y = x + s * C::kKRun + 4 * i;
-                    y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
+                    for (int i = 0; i < C::kKRun / 4; ++i) {
+                        const float4 f = *reinterpret_cast<const float4 *>(qr + (4 * s + c) * C::kKRun + 4 * i);
+                        float *y = x + s * C::kKRun + 4 * i;
+                        y[0] = f.x, y[1] = f.y, y[2] = f.z, y[3] = f.w;
+                    }
+            } else {                           // 2c, 2c + 1 of every eight columns
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const float2 f = *reinterpret_cast<const float2 *>(qr + 8 * i + 2 * c);
+                    x[2 * i] = f.x;
+                    x[2 * i + 1] = f.y;
                 }
+            }
             float back = 1.0f;
             if constexpr (TYPE != ZQ_BF16) {
                 float amax = 0.0f;
@@ -493,37 +586,41 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             for (int h = 0; h < 2; ++h) {
                 if (C::kItems == 2 || h == 0) has = landed(slot);
                 ok[h] = has >> (C::kItems == 2 ? 0 : h) & 1;
-                const uint8_t *src = ring + slot * C::kSlot + (C::kItems == 2 ? 0 : h * half_stride);
-                float acc[C::kSplits][4] = {};
+                const int from = slot * C::kSlot + (C::kItems == 2 ? 0 : h * half_stride);
+                float acc[C::kSplits][4];
+                auto product = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
-                for (int s = 0; s < C::kSegs; ++s)
+                    for (int p = 0; p < C::kSplits; ++p) {
+                        if (k == 0) mma_first<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k][0], qf[p][k][1]);
+                        else mma<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k][0], qf[p][k][1]);
+                    }
+                };
+                if constexpr (TYPE == ZQ_E4M3) {
 #pragma unroll
-                    for (int u = 0; u < C::kKBytes / 16; ++u) {
-                        const int chunk = C::kKBytes / 16 * c + u;
-                        const uint8_t *from = src + s * seg_stride;
-                        const uint4 ra = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(g, chunk));
-                        const uint4 rb = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(g + 8, chunk));
-                        const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
-                        const int k0 = (s * (C::kKBytes / 16) + u) * (4 / C::kBytes);
-                        if constexpr (TYPE == ZQ_E4M3) {
+                    for (int s = 0; s < C::kSegs; ++s)
+#pragma unroll
+                        for (int u = 0; u < C::kKBytes / 16; ++u) {
+                            const int chunk = C::kKBytes / 16 * c + u;
+                            const uint8_t *src = ring + from + s * seg_stride;
+                            const uint4 ra = *reinterpret_cast<const uint4 *>(src + swizzled<C::kSeg>(g, chunk));
+                            const uint4 rb = *reinterpret_cast<const uint4 *>(src + swizzled<C::kSeg>(g + 8, chunk));
+                            const uint32_t wa[4] = {ra.x, ra.y, ra.z, ra.w}, wb[4] = {rb.x, rb.y, rb.z, rb.w};
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 uint32_t a0, a1, a2, a3;
                                 e4m3_f16(wa[j], a0, a2);
                                 e4m3_f16(wb[j], a1, a3);
-#pragma unroll
-                                for (int p = 0; p < C::kSplits; ++p)
-                                    mma<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k0 + j][0], qf[p][k0 + j][1]);
+                                product((s * (C::kKBytes / 16) + u) * 4 + j, a0, a1, a2, a3);
                             }
-                        } else {
-#pragma unroll
-                            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                                for (int p = 0; p < C::kSplits; ++p)
-                                    mma<TYPE>(acc[p], wa[2 * j], wb[2 * j], wa[2 * j + 1], wb[2 * j + 1],
-                                              qf[p][k0 + j][0], qf[p][k0 + j][1]);
                         }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t a0, a1, a2, a3;
+                        ldmatrix4<false>(ring_a + from + k / 4 * seg_stride + (lane_k ^ (k % 4 << 5)), a0, a1, a2, a3);
+                        product(k, a0, a1, a2, a3);
                     }
+                }
                 if (C::kItems == 2 || h == 1) {
                     issue();
                     if (++slot == C::kSlots) slot = 0;
@@ -586,55 +683,72 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (C::kItems == 2 || h == 0) landed(slot);
-                const uint8_t *src = ring + slot * C::kSlot + (C::kItems == 2 ? 0 : h * half_stride);
+                const int from = slot * C::kSlot + (C::kItems == 2 ? 0 : h * half_stride);
+                auto product = [&](float(&to)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+                    float y[4];
+                    mma_first<TYPE>(y, a0, a1, a2, a3, bl[h][0], bl[h][1]);
+                    mma<TYPE>(y, a0, a1, a2, a3, bh[h][0], bh[h][1]);
+                    if (h == 0) {
+                        to[0] = to[0] * f0 + y[0];
+                        to[1] = to[1] * f1 + y[1];
+                        to[2] = to[2] * f0 + y[2];
+                        to[3] = to[3] * f1 + y[3];
+                    } else {
 #pragma unroll
-                for (int s = 0; s < C::kSegs; ++s) {
-                    uint32_t w[4][C::kVBytes / 4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r) {
-                        const int row = 2 * c + (r & 1) + 8 * (r >> 1);
-                        const uint8_t *from = src + s * seg_stride;
-                        if constexpr (C::kVBytes == 16) {
-                            const uint4 f = *reinterpret_cast<const uint4 *>(from + swizzled<C::kSeg>(row, g));
-                            w[r][0] = f.x, w[r][1] = f.y, w[r][2] = f.z, w[r][3] = f.w;
-                        } else {
-                            const uint2 f = *reinterpret_cast<const uint2 *>(
-                                from + swizzled<C::kSeg>(row, g >> 1) + 8 * (g & 1));
-                            w[r][0] = f.x, w[r][1] = f.y;
-                        }
-                        if (!whole) {
-                            const int at_row = tok + kHalf * h + row;
-                            if (!(ok[h] && at_row >= at.lo && at_row < at.len))
-#pragma unroll
-                                for (int j = 0; j < C::kVBytes / 4; ++j) w[r][j] = 0;
-                        }
+                        for (int e = 0; e < 4; ++e) to[e] += y[e];
                     }
+                };
+                // rows 2c, 2c + 1, 2c + 8, 2c + 9 of the half are attended to
+                bool in[4];
 #pragma unroll
-                    for (int j = 0; j < C::kVRun / 2; ++j) {
-                        uint32_t a0, a1, a2, a3;   // two columns of tokens 2c, 2c + 1, and of 2c + 8, 2c + 9
-                        if constexpr (TYPE == ZQ_E4M3) {
+                for (int r = 0; r < 4; ++r) {
+                    const int row = tok + kHalf * h + 2 * c + (r & 1) + 8 * (r >> 1);
+                    in[r] = whole || (ok[h] && row >= at.lo && row < at.len);
+                }
+                if constexpr (TYPE == ZQ_E4M3) {
+#pragma unroll
+                    for (int s = 0; s < C::kSegs; ++s) {
+                        uint32_t w[4][C::kVBytes / 4];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) {
+                            const int row = 2 * c + (r & 1) + 8 * (r >> 1);
+                            const uint8_t *src = ring + from + s * seg_stride;
+                            if constexpr (C::kVBytes == 16) {
+                                const uint4 f = *reinterpret_cast<const uint4 *>(src + swizzled<C::kSeg>(row, g));
+                                w[r][0] = f.x, w[r][1] = f.y, w[r][2] = f.z, w[r][3] = f.w;
+                            } else {
+                                const uint2 f = *reinterpret_cast<const uint2 *>(
+                                    src + swizzled<C::kSeg>(row, g >> 1) + 8 * (g & 1));
+                                w[r][0] = f.x, w[r][1] = f.y;
+                            }
+                            if (!whole) {
+#pragma unroll
+                                for (int j = 0; j < C::kVBytes / 4; ++j) w[r][j] = in[r] ? w[r][j] : 0;
+                            }
+                        }
+#pragma unroll
+                        for (int j = 0; j < C::kVRun / 2; ++j) {
+                            uint32_t a0, a1, a2, a3;   // two columns of tokens 2c, 2c + 1, and of 2c + 8, 2c + 9
                             const int sel = j & 1 ? 0x7362 : 0x5140;
                             e4m3_f16(__byte_perm(w[0][j / 2], w[1][j / 2], sel), a0, a1);
                             e4m3_f16(__byte_perm(w[2][j / 2], w[3][j / 2], sel), a2, a3);
-                        } else {
-                            a0 = __byte_perm(w[0][j], w[1][j], 0x5410);
-                            a1 = __byte_perm(w[0][j], w[1][j], 0x7632);
-                            a2 = __byte_perm(w[2][j], w[3][j], 0x5410);
-                            a3 = __byte_perm(w[2][j], w[3][j], 0x7632);
+                            product(o[s * (C::kVRun / 2) + j], a0, a1, a2, a3);
                         }
-                        float y[4] = {};
-                        mma<TYPE>(y, a0, a1, a2, a3, bl[h][0], bl[h][1]);
-                        mma<TYPE>(y, a0, a1, a2, a3, bh[h][0], bh[h][1]);
-                        float(&to)[4] = o[s * (C::kVRun / 2) + j];
-                        if (h == 0) {
-                            to[0] = to[0] * f0 + y[0];
-                            to[1] = to[1] * f1 + y[1];
-                            to[2] = to[2] * f0 + y[2];
-                            to[3] = to[3] * f1 + y[3];
-                        } else {
+                    }
+                } else {
+                    const uint32_t keep0 = (in[0] ? 0xffffu : 0) | (in[1] ? 0xffff0000u : 0);
+                    const uint32_t keep1 = (in[2] ? 0xffffu : 0) | (in[3] ? 0xffff0000u : 0);
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) to[e] += y[e];
+                    for (int k = 0; k < D / 16; ++k) {
+                        uint32_t a0, a1, a2, a3;
+                        ldmatrix4<true>(ring_a + from + k / 4 * seg_stride + (lane_v ^ (k % 4 << 5)), a0, a1, a2, a3);
+                        if (!whole) {
+                            a0 &= keep0;
+                            a1 &= keep0;
+                            a2 &= keep1;
+                            a3 &= keep1;
                         }
+                        product(o[k], a0, a1, a2, a3);
                     }
                 }
                 if (C::kItems == 2 || h == 1) {
@@ -656,26 +770,37 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 const int h = 2 * c + e;
                 const bool store = h < heads;
                 const float l = e ? l1 : l0, f = row_factor(l, a.v_scale);
-                const long long row = (long long)at.b * a.out_stride + (long long)(head0 + h) * D;
+                float *row = a.out + (long long)at.b * a.out_stride + (long long)(head0 + h) * D;
+                const size_t code0 = ((size_t)at.b * a.Hq + head0 + h) * D;
+                if constexpr (TYPE == ZQ_E4M3) {
 #pragma unroll
-                for (int s = 0; s < C::kSegs; ++s) {
-                    float y[C::kVRun];
+                    for (int s = 0; s < C::kSegs; ++s) {
+                        float y[C::kVRun];
 #pragma unroll
-                    for (int j = 0; j < C::kVRun / 2; ++j) {
-                        y[2 * j] = o[s * (C::kVRun / 2) + j][e] * f;
-                        y[2 * j + 1] = o[s * (C::kVRun / 2) + j][2 + e] * f;
+                        for (int j = 0; j < C::kVRun / 2; ++j) {
+                            y[2 * j] = o[s * (C::kVRun / 2) + j][e] * f;
+                            y[2 * j + 1] = o[s * (C::kVRun / 2) + j][2 + e] * f;
+                        }
+                        const int d0 = (8 * s + g) * C::kVRun;
+                        if (store && a.out) {
+#pragma unroll
+                            for (int q = 0; q < C::kVRun / 4; ++q)
+                                reinterpret_cast<float4 *>(row + d0)[q] =
+                                    make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
+                        }
+                        if (a.q8.qs)
+                            q8_block<C::kVRun, 4, C::kVRun == 8 ? 8 : 0, 0>(a.q8, code0 + d0, y, store,
+                                                                           (d0 & 31) == 0);
                     }
-                    const int d0 = (8 * s + g) * C::kVRun;
-                    if (store && a.out) {
+                } else {
 #pragma unroll
-                        for (int q = 0; q < C::kVRun / 4; ++q)
-                            reinterpret_cast<float4 *>(a.out + row + d0)[q] =
-                                make_float4(y[4 * q], y[4 * q + 1], y[4 * q + 2], y[4 * q + 3]);
-                    }
-                    if (a.q8.qs) {
-                        const size_t to = ((size_t)at.b * a.Hq + head0 + h) * D + d0;
-                        q8_block<C::kVRun, 4, C::kVRun == 8 ? 8 : 0, 0>(a.q8, to, y, store,
-                                                                       (d0 & 31) == 0);
+                    for (int i = 0; i < D / 16; i += 2) {
+                        const float y[4] = {o[i][e] * f, o[i][2 + e] * f, o[i + 1][e] * f, o[i + 1][2 + e] * f};
+                        if (store && a.out) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) row[16 * i + 8 * k + g] = y[k];
+                        }
+                        if (a.q8.qs) q8_block_strided(a.q8, code0 + 16 * i, y, g, store);
                     }
                 }
                 if (store && a.lse && g == 0) a.lse[(size_t)at.b * a.Hq + head0 + h] = row_lse(e ? m1 : m0, l);
@@ -684,18 +809,12 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             at.next_block(a);
         } else if (ends) {      // began in an earlier warp: to the workspace
             has_head = 1;
+            put_rows(head_piece);
+            if (g == 0) {
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int h = 2 * c + e;
-#pragma unroll
-                for (int s = 0; s < C::kSegs; ++s)
-#pragma unroll
-                    for (int j = 0; j < C::kVRun / 2; ++j)
-                        *reinterpret_cast<float2 *>(head_piece + h * D + (8 * s + g) * C::kVRun + 2 * j) =
-                            make_float2(o[s * (C::kVRun / 2) + j][e], o[s * (C::kVRun / 2) + j][2 + e]);
-                if (g == 0) {
-                    head_piece[kHeads * D + h] = e ? m1 : m0;
-                    head_piece[kHeads * D + kHeads + h] = e ? l1 : l0;
+                for (int e = 0; e < 2; ++e) {
+                    head_piece[kHeads * D + 2 * c + e] = e ? m1 : m0;
+                    head_piece[kHeads * D + kHeads + 2 * c + e] = e ? l1 : l0;
                 }
             }
             left -= kBlockCost;
@@ -711,19 +830,12 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     __syncthreads();   // every warp's ring is done: its place holds the open pieces now
     float *pieces_s = reinterpret_cast<float *>(smem);
     if (open.b) {
-        float *to = pieces_s + (size_t)warp * kHeads * D;
+        put_rows(pieces_s + (size_t)warp * kHeads * D);
+        if (g == 0) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int h = 2 * c + e;
-#pragma unroll
-            for (int s = 0; s < C::kSegs; ++s)
-#pragma unroll
-                for (int j = 0; j < C::kVRun / 2; ++j)
-                    *reinterpret_cast<float2 *>(to + h * D + (8 * s + g) * C::kVRun + 2 * j) =
-                        make_float2(o[s * (C::kVRun / 2) + j][e], o[s * (C::kVRun / 2) + j][2 + e]);
-            if (g == 0) {
-                m_s[warp][h] = e ? m1 : m0;
-                l_s[warp][h] = e ? l1 : l0;
+            for (int e = 0; e < 2; ++e) {
+                m_s[warp][2 * c + e] = e ? m1 : m0;
+                l_s[warp][2 * c + e] = e ? l1 : l0;
             }
         }
     }
