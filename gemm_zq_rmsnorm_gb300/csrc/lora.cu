@@ -8,25 +8,25 @@
 // y (8 B N bytes), which dominate; a few tokens are launch bound.
 //
 // Tokens come in tiles of 64.  A CTA sorts its tile's tokens by adapter itself
-// (64 ids: a scan of comparisons) and takes them eight at a time as the columns
-// of its MMAs, so a prompt's tokens share each adapter row and a decode batch
-// reads each of its adapters once a tile; no sorting pass, no plan to keep, any
+// (64 ids: a scan of comparisons) and takes them sixteen at a time as the rows of
+// its MMAs, so a prompt's tokens share each adapter row and a decode batch reads
+// each of its adapters once a tile; no sorting pass, no plan to keep, any
 // mixture of both.
 //
-// First kernel: m16n8k16 with adapter rows as the 16-row operand and tokens as
-// the columns.  The order of K inside a step is free, so lane 4g + c loads 8
-// neighbouring values of rows g and g + 8, and of token g's codes, which are
-// fragments as they stand.  Codes are whole numbers of at most 8 bits, exact in
-// binary16 and bf16: a Q8_1 block's products are summed by the tensor core and
+// First kernel: m16n8k16 with tokens as the rows and eight adapter rows as the
+// columns.  The order of K inside a step is free, so lane 4g + c loads 8
+// neighbouring values of adapter row g, two steps' fragments as they stand (as
+// the 16-row operand they would have to be moved together from two loads), and
+// 8 codes of tokens g and g + 8.  Codes are whole numbers of at most 8 bits, exact
+// in binary16 and bf16: a Q8_1 block's products are summed by the tensor core and
 // scaled by the block's d in fp32.  Warps split the blocks of a CTA's K range
 // and add up in a fixed tree, the CTAs of a cluster add up their ranges in order
 // through distributed shared memory, the second kernel the clusters'.
 //
-// Second kernel: rows of B_a are the 16-row operand, tokens the columns; h is
-// two 16-bit parts (binary16 after scaling the token's row to [1, 2), 2^-22 of
-// its largest value; bf16 2^-17).  The rows of two MMAs are dealt so that a
-// lane holds four neighbouring outputs of its tokens: base and y move as 16-byte
-// pieces.
+// Second kernel: tokens are the rows, outputs the columns; h is two 16-bit parts
+// (binary16 after scaling the token's row to [1, 2), 2^-22 of its largest value;
+// bf16 2^-17).  The outputs are dealt to the MMAs' columns so that a lane holds
+// four neighbouring ones of its tokens: base and y move as 16-byte pieces.
 #include "zq_async.cuh"
 #include "zq_cluster.cuh"
 #include "zq_internal.cuh"
@@ -36,15 +36,14 @@ namespace zq {
 namespace {
 
 constexpr int kTokens = 64;      // tokens of a tile
-constexpr int kQ = 4;            // groups of eight members a unit has at most
-constexpr int kThreads = 256;    // first kernel
+constexpr int kGroup = 16;       // tokens of a group: an MMA's rows
+constexpr int kQ = 2;            // groups a unit has at most
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kDownRows = 32;    // rows of A a CTA of the first kernel takes at most
 constexpr int kCluster = 8;      // CTAs of a cluster at most, which add up their K ranges
 constexpr int kParts = 4;        // sums the second kernel is left with at most
-constexpr int kUpThreads = 128;  // second kernel
-constexpr int kUpWarps = kUpThreads / 32;
-constexpr int kUpGroups = 16;    // groups whose h it has in shared memory at a time
+constexpr int kUpGroups = 8;     // groups whose h the second kernel has in shared memory at a time
 constexpr int kBlock = 32;       // outputs of a warp at a time
 constexpr int kNone = 255;
 constexpr unsigned kAll = 0xffffffffu;
@@ -82,6 +81,36 @@ __device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t
                      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
+// Onto zero with eight products a value
+template <int TYPE>
+__device__ __forceinline__ void mma8_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0)
+{
+    if constexpr (TYPE == ZQ_BF16)
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+                     "{%7,%7,%7,%7};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
+    else
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+                     "{%7,%7,%7,%7};"
+                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
+}
+template <int TYPE>
+__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0)
+{
+    if constexpr (TYPE == ZQ_BF16)
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(b0));
+    else
+        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
+                     "{%0,%1,%2,%3};"
+                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                     : "r"(a0), "r"(a1), "r"(b0));
+}
+
 // Four int8 codes to two pairs of the MMA's type, exactly: binary16 1024 + (q
 // + 128) has the byte in its low bits.
 template <int TYPE>
@@ -102,19 +131,19 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t &lo, uint32_t &hi)
     }
 }
 
-// A tile's tokens by adapter: each adapter's tokens in groups of eight (an
-// MMA's columns), its groups in units of up to four.
+// A tile's tokens by adapter: each adapter's tokens in groups of sixteen (an
+// MMA's rows), its groups in units of up to two.
 struct Tile {
     int id[kTokens];               // adapter of a token, -1: none (or past the last token)
     int base[kTokens];             // first group of a token's adapter, at the adapter's first token
     int half, groups, units;       // groups | units << 16 of the lower 32 tokens; in all
     int adapter[kTokens];          // of a group
-    uint32_t tok[kTokens][2];      // tokens of a group's eight columns, a byte each, kNone: no more
+    uint32_t tok[kTokens][kGroup / 4];   // tokens of a group's rows, a byte each, kNone: no more
     uint8_t unit[kTokens], unit_groups[kTokens];   // first group of a unit, number of its groups
 
-    __device__ __forceinline__ int token(int group, int col) const
+    __device__ __forceinline__ int token(int group, int row) const
     {
-        return reinterpret_cast<const uint8_t *>(tok[group])[col];
+        return reinterpret_cast<const uint8_t *>(tok[group])[row];
     }
 };
 
@@ -127,7 +156,8 @@ __device__ __forceinline__ void tile_open(Tile &s, const LoraArgs &a, int tile)
         if (at < a.B) id = a.ids[at];
         if (id < 0 || id >= a.n) id = -1;
         s.id[t] = id;
-        s.tok[t][0] = s.tok[t][1] = 0xffffffffu;
+#pragma unroll
+        for (int i = 0; i < kGroup / 4; ++i) s.tok[t][i] = 0xffffffffu;
     }
     __syncthreads();
     int before = 0, total = 0, first = t, incl = 0, own = 0;
@@ -145,7 +175,7 @@ __device__ __forceinline__ void tile_open(Tile &s, const LoraArgs &a, int tile)
             }
         }
         if (id >= 0 && before == 0) {
-            const int groups = (total + 7) / 8;
+            const int groups = (total + kGroup - 1) / kGroup;
             own = groups | (groups + kQ - 1) / kQ << 16;
         }
         incl = own;
@@ -173,7 +203,7 @@ __device__ __forceinline__ void tile_open(Tile &s, const LoraArgs &a, int tile)
     }
     __syncthreads();
     if (t < kTokens && id >= 0)
-        reinterpret_cast<uint8_t *>(s.tok[s.base[first] + before / 8])[before % 8] = (uint8_t)t;
+        reinterpret_cast<uint8_t *>(s.tok[s.base[first] + before / kGroup])[before % kGroup] = (uint8_t)t;
     __syncthreads();
 }
 
@@ -184,8 +214,8 @@ __device__ __forceinline__ void tile_open(Tile &s, const LoraArgs &a, int tile)
 template <int RR, int TYPE>
 __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_constant__ LoraArgs a)
 {
-    constexpr int kRows = RR < 16 ? 1 : RR / 16;   // 16-row operands
-    __shared__ float red[kWarps / 2][kRows][kQ][4][32];
+    constexpr int kCols = RR / 8;   // MMAs' columns: rows of A
+    __shared__ float red[kWarps / 2][kCols][kQ][4][32];
     __shared__ __align__(16) Tile tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();   // codes and ids come from earlier kernels
@@ -202,54 +232,57 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
         const int group0 = tile.unit[u], nq = tile.unit_groups[u], adapter = tile.adapter[group0];
         const char *A = a.A + (((size_t)adapter * a.R + row0 + g) * a.K + 8 * c) * 2;
         const size_t step = (size_t)8 * a.K * 2;   // eight rows on
-        const int8_t *x[kQ];
-        const uint16_t *d[kQ];
+        const int8_t *x[kQ][2];
+        const uint16_t *d[kQ][2];
 #pragma unroll
-        for (int q = 0; q < kQ; ++q) {   // columns without a member repeat the first, unused
-            const int of = q < nq ? tile.token(group0 + q, g) : kNone;
-            const size_t t = tok0 + (of == kNone ? tile.token(group0, 0) : of);
-            x[q] = a.qs + t * a.K + 8 * c;
-            d[q] = a.d + t * blocks;
-        }
-        float sum[kRows][kQ][4] = {};
+        for (int q = 0; q < kQ; ++q)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {   // rows without a token repeat the first, unused
+                const int of = q < nq ? tile.token(group0 + q, g + 8 * e) : kNone;
+                const size_t t = tok0 + (of == kNone ? tile.token(group0, 0) : of);
+                x[q][e] = a.qs + t * a.K + 8 * c;
+                d[q][e] = a.d + t * blocks;
+            }
+        float sum[kCols][kQ][4] = {};
         // the next block's values are on their way while this one's are used
         struct Block {
-            uint4 w[kRows][2];
-            uint2 codes[kQ];
-            uint16_t d[kQ];
+            uint4 w[kCols];
+            uint2 codes[kQ][2];
+            uint16_t d[kQ][2];
         };
         auto fetch = [&](int b, Block &f) {
             b = min(b, blocks - 1);   // past the end: read, not used
 #pragma unroll
-            for (int r = 0; r < kRows; ++r) {
-                f.w[r][0] = __ldg(reinterpret_cast<const uint4 *>(A + 2 * r * step + 64 * (size_t)b));
-                if (RR >= 16) f.w[r][1] = __ldg(reinterpret_cast<const uint4 *>(A + (2 * r + 1) * step + 64 * (size_t)b));
-                else f.w[r][1] = make_uint4(0, 0, 0, 0);
-            }
+            for (int r = 0; r < kCols; ++r)
+                f.w[r] = __ldg(reinterpret_cast<const uint4 *>(A + r * step + 64 * (size_t)b));
 #pragma unroll
             for (int q = 0; q < kQ; ++q)
-                if (q < nq) {
-                    f.codes[q] = __ldg(reinterpret_cast<const uint2 *>(x[q] + 32 * b));
-                    f.d[q] = __ldg(d[q] + b);
-                }
+                if (q < nq)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        f.codes[q][e] = __ldg(reinterpret_cast<const uint2 *>(x[q][e] + 32 * b));
+                        f.d[q][e] = __ldg(d[q][e] + b);
+                    }
         };
         auto use = [&](const Block &f) {
 #pragma unroll
             for (int q = 0; q < kQ; ++q) {
                 if (q >= nq) break;
-                const float dq = h2f(f.d[q]);
-                const float d0 = __shfl_sync(kAll, dq, 8 * c), d1 = __shfl_sync(kAll, dq, 8 * c + 4);
-                uint32_t k0, k1, k2, k3;
-                codes4<TYPE>(f.codes[q].x, k0, k1);
-                codes4<TYPE>(f.codes[q].y, k2, k3);
+                const float d0 = h2f(f.d[q][0]), d1 = h2f(f.d[q][1]);
+                uint32_t k[2][4];
 #pragma unroll
-                for (int r = 0; r < kRows; ++r) {
+                for (int e = 0; e < 2; ++e) {
+                    codes4<TYPE>(f.codes[q][e].x, k[e][0], k[e][1]);
+                    codes4<TYPE>(f.codes[q][e].y, k[e][2], k[e][3]);
+                }
+#pragma unroll
+                for (int r = 0; r < kCols; ++r) {
                     float p[4];
-                    mma16_first<TYPE>(p, f.w[r][0].x, f.w[r][1].x, f.w[r][0].y, f.w[r][1].y, k0, k1);
-                    mma16<TYPE>(p, f.w[r][0].z, f.w[r][1].z, f.w[r][0].w, f.w[r][1].w, k2, k3);
+                    mma16_first<TYPE>(p, k[0][0], k[1][0], k[0][1], k[1][1], f.w[r].x, f.w[r].y);
+                    mma16<TYPE>(p, k[0][2], k[1][2], k[0][3], k[1][3], f.w[r].z, f.w[r].w);
                     sum[r][q][0] += d0 * p[0];
-                    sum[r][q][1] += d1 * p[1];
-                    sum[r][q][2] += d0 * p[2];
+                    sum[r][q][1] += d0 * p[1];
+                    sum[r][q][2] += d1 * p[2];
                     sum[r][q][3] += d1 * p[3];
                 }
             }
@@ -268,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
             __syncthreads();
             if (warp >= half && warp < 2 * half) {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
+                for (int r = 0; r < kCols; ++r)
 #pragma unroll
                     for (int q = 0; q < kQ; ++q)
                         if (q < nq)
@@ -278,7 +311,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
             __syncthreads();
             if (warp < half) {
 #pragma unroll
-                for (int r = 0; r < kRows; ++r)
+                for (int r = 0; r < kCols; ++r)
 #pragma unroll
                     for (int q = 0; q < kQ; ++q)
                         if (q < nq)
@@ -288,7 +321,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
         }
         if (warp == 0) {
 #pragma unroll
-            for (int r = 0; r < kRows; ++r)
+            for (int r = 0; r < kCols; ++r)
 #pragma unroll
                 for (int q = 0; q < kQ; ++q)
                     if (q < nq)
@@ -299,17 +332,16 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
         __syncwarp();
         if (a.cluster > 1) cluster_sync();
         else __syncthreads();
-        constexpr int kValues = kRows * kQ * 4 * 32;
+        constexpr int kValues = kCols * kQ * 4 * 32;
         const int share = kValues / a.cluster;
         const uint32_t local = smem_u32(&red[0][0][0][0][0]);
         for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += kThreads) {
             const int l = i & 31, e = i >> 5 & 3, q = i >> 7 & (kQ - 1), r = i / (kQ * 128);
-            const int row = 16 * r + 8 * (e >> 1) + (l >> 2);
-            const int of = q < nq ? tile.token(group0 + q, 2 * (l & 3) + (e & 1)) : kNone;
-            if (of != kNone && row < RR) {
+            const int of = q < nq ? tile.token(group0 + q, (l >> 2) + 8 * (e >> 1)) : kNone;
+            if (of != kNone) {
                 float v = 0.0f;
                 for (int k = 0; k < a.cluster; ++k) v += ld_cluster_f32(cluster_addr(local + 4 * i, k));
-                h[(tok0 + of) * a.R + row] = v;
+                h[(tok0 + of) * a.R + 8 * r + 2 * (l & 3) + (e & 1)] = v;
             }
         }
         __syncwarp();
@@ -318,17 +350,17 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
 }
 
 // y[t] = base[t] + scale_a B_a h_t.  Grid: (tiles, column ranges of a.blocks
-// blocks of 32).  A task is one block for one group of eight tokens; a warp takes
-// neighbouring tasks of one block after the other, the next one's values on
-// their way while it works on one.
+// blocks of 32).  A task is one block for one group of sixteen tokens; a warp
+// takes neighbouring tasks of one block after the other, the next one's values
+// on their way while it works on one.
 template <int R, int TYPE>
-__global__ void __launch_bounds__(kUpThreads, 5) lora_up_kernel(const __grid_constant__ LoraArgs a)
+__global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(const __grid_constant__ LoraArgs a)
 {
     constexpr int kSteps = R < 16 ? 1 : R / 16;
     constexpr int kRun = R < 32 ? R / 4 : 8;   // neighbouring values of R that a lane's fragment takes
     __shared__ __align__(16) Tile tile;
-    __shared__ uint4 h_s[kUpGroups][kSteps][32];      // fragments of h: x, y the upper parts, z, w the lower ones
-    __shared__ float back_s[kUpGroups][8];            // 2^e of a member's scaling
+    __shared__ uint4 h_s[kUpGroups][kSteps][2][32];   // fragments of h: the upper parts, the lower ones
+    __shared__ float back_s[kUpGroups][kGroup];       // 2^e of a member's scaling
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const size_t tok0 = (size_t)blockIdx.x * kTokens;
     const int block0 = blockIdx.y * a.blocks, blocks = min(a.blocks, (a.N + kBlock - 1) / kBlock - block0);
@@ -337,48 +369,57 @@ __global__ void __launch_bounds__(kUpThreads, 5) lora_up_kernel(const __grid_con
     tile_open(tile, a, blockIdx.x);
     bool waited = false;
 
+    // The columns of MMA (p, i) are outputs 16 p + 4 (col / 2) + 2 i + col % 2 of
+    // the block, so that lane 4g + c ends with outputs 16 p + 4c .. 4c + 3.
     struct Task {
-        uint32_t w[2][kSteps][4];   // fragments of rows n0 + 2i (upper) and n0 + 2i + 1 (lower)
-        float4 v[2];                // base of columns 2c, 2c + 1
+        uint32_t w[2][2][kSteps][2];
+        float4 v[2][2];             // base of rows g, g + 8
     };
-    auto fetch = [&](int group, int n0, bool vec, bool weights, Task &f) {
+    auto fetch = [&](int group, int col0, bool vec, bool weights, Task &f) {
         if (weights) {
             const char *row0 = a.Bm + (size_t)tile.adapter[group] * a.N * R * 2 + kRun * 2 * c;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const char *row = row0 + (size_t)min(a.N - 1, n0 + i) * R * 2;
-                if constexpr (R == 8) {
-                    f.w[i >> 1][0][i & 1] = __ldg(reinterpret_cast<const uint32_t *>(row));
-                    f.w[i >> 1][0][2 + (i & 1)] = 0;
-                } else if constexpr (R == 16) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(row));
-                    f.w[i >> 1][0][i & 1] = x.x;
-                    f.w[i >> 1][0][2 + (i & 1)] = x.y;
-                } else {
+            for (int p = 0; p < 2; ++p)
 #pragma unroll
-                    for (int s = 0; s < kSteps / 2; ++s) {
-                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row + 64 * s));
-                        f.w[i >> 1][2 * s][i & 1] = x.x;
-                        f.w[i >> 1][2 * s][2 + (i & 1)] = x.y;
-                        f.w[i >> 1][2 * s + 1][i & 1] = x.z;
-                        f.w[i >> 1][2 * s + 1][2 + (i & 1)] = x.w;
+                for (int i = 0; i < 2; ++i) {
+                    const int n = col0 + 16 * p + 4 * (g >> 1) + 2 * i + (g & 1);
+                    const char *row = row0 + (size_t)min(a.N - 1, n) * R * 2;
+                    if constexpr (R == 8) {
+                        f.w[p][i][0][0] = __ldg(reinterpret_cast<const uint32_t *>(row));
+                        f.w[p][i][0][1] = 0;
+                    } else if constexpr (R == 16) {
+                        const uint2 x = __ldg(reinterpret_cast<const uint2 *>(row));
+                        f.w[p][i][0][0] = x.x;
+                        f.w[p][i][0][1] = x.y;
+                    } else {
+#pragma unroll
+                        for (int s = 0; s < kSteps / 2; ++s) {
+                            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(row + 64 * s));
+                            f.w[p][i][2 * s][0] = x.x;
+                            f.w[p][i][2 * s][1] = x.y;
+                            f.w[p][i][2 * s + 1][0] = x.z;
+                            f.w[p][i][2 * s + 1][1] = x.w;
+                        }
                     }
                 }
-            }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            const int t = tile.token(group, 2 * c + e);
-            f.v[e] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (a.base && t != kNone) {
-                const float *p = a.base + (tok0 + t) * a.base_stride + n0;
+            const int t = tile.token(group, g + 8 * e);
+            const bool in = a.base && t != kNone;
+            const float *from = a.base + (in ? (tok0 + t) * a.base_stride + col0 + 4 * c : 0);
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                f.v[e][p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (!in) continue;
                 if (vec) {
-                    f.v[e] = *reinterpret_cast<const float4 *>(p);
+                    f.v[e][p] = *reinterpret_cast<const float4 *>(from + 16 * p);
                 } else {
-                    if (n0 < a.N) f.v[e].x = p[0];
-                    if (n0 + 1 < a.N) f.v[e].y = p[1];
-                    if (n0 + 2 < a.N) f.v[e].z = p[2];
-                    if (n0 + 3 < a.N) f.v[e].w = p[3];
+                    const int left = a.N - (col0 + 16 * p + 4 * c);
+                    if (left > 0) f.v[e][p].x = from[16 * p];
+                    if (left > 1) f.v[e][p].y = from[16 * p + 1];
+                    if (left > 2) f.v[e][p].z = from[16 * p + 2];
+                    if (left > 3) f.v[e][p].w = from[16 * p + 3];
                 }
             }
         }
@@ -387,12 +428,12 @@ __global__ void __launch_bounds__(kUpThreads, 5) lora_up_kernel(const __grid_con
     for (int g0 = 0; g0 < tile.groups; g0 += kUpGroups) {
         const int n = min(kUpGroups, tile.groups - g0);
         // this warp's tasks, block by block
-        const int t0 = warp * blocks * n / kUpWarps, t1 = (warp + 1) * blocks * n / kUpWarps;
+        const int t0 = warp * blocks * n / kWarps, t1 = (warp + 1) * blocks * n / kWarps;
         int block = t0 / n, group = t0 - block * n;
-        auto col0 = [&](int block) { return (block0 + block) * kBlock + 4 * g; };
+        auto col_of = [&](int block) { return (block0 + block) * kBlock; };
         auto aligned = [&](int block) { return a.vec && (block0 + block + 1) * kBlock <= a.N; };
         Task now;
-        if (t0 < t1) fetch(g0 + group, col0(block), aligned(block), true, now);
+        if (t0 < t1) fetch(g0 + group, col_of(block), aligned(block), true, now);
         if (!waited) {
             pdl_wait();
             pdl_launch_dependents();
@@ -400,14 +441,14 @@ __global__ void __launch_bounds__(kUpThreads, 5) lora_up_kernel(const __grid_con
         }
         // h of the groups' members: its parts in order, times the adapter's scale, as two 16-bit parts in the
         // fragments' order; R / 4 neighbouring threads have a member, four values each
-        const int items = n * 8 * (R / 4);
-        for (int i = tid; i < (items + 31) / 32 * 32; i += kUpThreads) {
-            const int m = min(i / (R / 4), n * 8 - 1), r = i % (R / 4) * 4;
-            const int of = tile.token(g0 + m / 8, m % 8);
+        const int items = n * kGroup * (R / 4);
+        for (int i = tid; i < items; i += kThreads) {   // whole warps: items is a multiple of 32
+            const int m = i / (R / 4), r = i % (R / 4) * 4, grp = m / kGroup, row = m % kGroup;
+            const int of = tile.token(g0 + grp, row);
             float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
             float scale = 1.0f;
             if (of != kNone) {
-                if (a.scales) scale = a.scales[tile.adapter[g0 + m / 8]];
+                if (a.scales) scale = a.scales[tile.adapter[g0 + grp]];
                 const float *h = a.h + (tok0 + of) * R + r;
 #pragma unroll
                 for (int s = 0; s < kParts; ++s)
@@ -431,31 +472,28 @@ __global__ void __launch_bounds__(kUpThreads, 5) lora_up_kernel(const __grid_con
 #pragma unroll
                 for (int k = 0; k < 4; ++k) x[k] *= down;
             }
-            uint32_t hi[2], lo[2];
+            if (r == 0) back_s[grp][row] = up;
+            const int s = R <= 16 ? 0 : 2 * (r / 32) + (r >> 2 & 1), l = row % 8 * 4;
+            uint32_t *hi_to = reinterpret_cast<uint32_t *>(h_s[grp][s][0]), *lo_to =
+                reinterpret_cast<uint32_t *>(h_s[grp][s][1]);
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                hi[k] = kv_pack2<TYPE>(x[2 * k], x[2 * k + 1]);
+                const uint32_t hi = kv_pack2<TYPE>(x[2 * k], x[2 * k + 1]);
                 float2 y;
                 if constexpr (TYPE == ZQ_BF16)
-                    y = make_float2(__uint_as_float(hi[k] << 16), __uint_as_float(hi[k] & 0xffff0000u));
-                else y = __half22float2(*reinterpret_cast<const __half2 *>(&hi[k]));
-                lo[k] = kv_pack2<TYPE>(x[2 * k] - y.x, x[2 * k + 1] - y.y);
-            }
-            if (i < items) {
-                const int l = m % 8 * 4;
-                if (r == 0) back_s[m / 8][m % 8] = up;
-                if constexpr (R == 8) {   // two lanes' pairs; their second registers are zeros
-                    h_s[m / 8][0][l + r / 2] = make_uint4(hi[0], 0, lo[0], 0);
-                    h_s[m / 8][0][l + r / 2 + 1] = make_uint4(hi[1], 0, lo[1], 0);
-                } else {                  // one lane's values of a step
-                    const int s = R == 16 ? 0 : 2 * (r / 32) + (r >> 2 & 1);
-                    h_s[m / 8][s][l + (R == 16 ? r / 4 : (r & 31) >> 3)] = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-                }
+                    y = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+                else y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                const uint32_t lo = kv_pack2<TYPE>(x[2 * k] - y.x, x[2 * k + 1] - y.y);
+                // register row / 8 (+ 2 for a step's upper eight) of the lane that has these values
+                const int at = R == 8 ? 4 * (l + r / 2 + k) + row / 8
+                                      : 4 * (l + (R == 16 ? r / 4 : (r & 31) >> 3)) + row / 8 + 2 * k;
+                hi_to[at] = hi;
+                lo_to[at] = lo;
             }
         }
         __syncthreads();
         for (int task = t0; task < t1; ++task) {
-            const int here = group, n0 = col0(block);
+            const int here = group, col0 = col_of(block);
             const bool vec = aligned(block);
             // the next task: the block's next group, or the next block's first
             const int adapter = tile.adapter[g0 + group];
@@ -470,43 +508,55 @@ __global__ void __launch_bounds__(kUpThreads, 5) lora_up_kernel(const __grid_con
                 weights |= tile.adapter[g0 + group] != adapter;
                 if (!weights) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
+                    for (int p = 0; p < 2; ++p)
 #pragma unroll
-                        for (int s = 0; s < kSteps; ++s)
+                        for (int i = 0; i < 2; ++i)
 #pragma unroll
-                            for (int k = 0; k < 4; ++k) next.w[i][s][k] = now.w[i][s][k];
+                            for (int s = 0; s < kSteps; ++s)
+#pragma unroll
+                                for (int k = 0; k < 2; ++k) next.w[p][i][s][k] = now.w[p][i][s][k];
                 }
-                fetch(g0 + group, col0(block), aligned(block), weights, next);
+                fetch(g0 + group, col_of(block), aligned(block), weights, next);
             }
-            float p[2][4];
+            float y[2][2][4];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                const uint4 f = h_s[here][s][lane];
+                const uint4 hi = h_s[here][s][0][lane], lo = h_s[here][s][1][lane];
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (s == 0)
-                        mma16_first<TYPE>(p[i], now.w[i][s][0], now.w[i][s][1], now.w[i][s][2], now.w[i][s][3], f.z,
-                                          f.w);
-                    else
-                        mma16<TYPE>(p[i], now.w[i][s][0], now.w[i][s][1], now.w[i][s][2], now.w[i][s][3], f.z, f.w);
-                    mma16<TYPE>(p[i], now.w[i][s][0], now.w[i][s][1], now.w[i][s][2], now.w[i][s][3], f.x, f.y);
-                }
+                for (int p = 0; p < 2; ++p)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t(&w)[2] = now.w[p][i][s];
+                        if constexpr (R == 8) {
+                            mma8_first<TYPE>(y[p][i], lo.x, lo.y, w[0]);
+                            mma8<TYPE>(y[p][i], hi.x, hi.y, w[0]);
+                        } else {
+                            if (s == 0) mma16_first<TYPE>(y[p][i], lo.x, lo.y, lo.z, lo.w, w[0], w[1]);
+                            else mma16<TYPE>(y[p][i], lo.x, lo.y, lo.z, lo.w, w[0], w[1]);
+                            mma16<TYPE>(y[p][i], hi.x, hi.y, hi.z, hi.w, w[0], w[1]);
+                        }
+                    }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int t = tile.token(g0 + here, 2 * c + e);
+                const int t = tile.token(g0 + here, g + 8 * e);
                 if (t != kNone) {
-                    const float f = TYPE == ZQ_F16 ? back_s[here][2 * c + e] : 1.0f;
-                    float *to = a.y + (tok0 + t) * a.y_stride + n0;
-                    const float4 y = make_float4(now.v[e].x + p[0][e] * f, now.v[e].y + p[0][2 + e] * f,
-                                                 now.v[e].z + p[1][e] * f, now.v[e].w + p[1][2 + e] * f);
-                    if (vec) {
-                        *reinterpret_cast<float4 *>(to) = y;
-                    } else {
-                        if (n0 < a.N) to[0] = y.x;
-                        if (n0 + 1 < a.N) to[1] = y.y;
-                        if (n0 + 2 < a.N) to[2] = y.z;
-                        if (n0 + 3 < a.N) to[3] = y.w;
+                    const float f = TYPE == ZQ_F16 ? back_s[here][g + 8 * e] : 1.0f;
+                    float *to = a.y + (tok0 + t) * a.y_stride + col0 + 4 * c;
+#pragma unroll
+                    for (int p = 0; p < 2; ++p) {
+                        const float4 v = now.v[e][p];
+                        const float4 r = make_float4(v.x + y[p][0][2 * e] * f, v.y + y[p][0][2 * e + 1] * f,
+                                                     v.z + y[p][1][2 * e] * f, v.w + y[p][1][2 * e + 1] * f);
+                        if (vec) {
+                            *reinterpret_cast<float4 *>(to + 16 * p) = r;
+                        } else {
+                            const int left = a.N - (col0 + 16 * p + 4 * c);
+                            if (left > 0) to[16 * p] = r.x;
+                            if (left > 1) to[16 * p + 1] = r.y;
+                            if (left > 2) to[16 * p + 2] = r.z;
+                            if (left > 3) to[16 * p + 3] = r.w;
+                        }
                     }
                 }
             }
@@ -522,7 +572,7 @@ __global__ void __launch_bounds__(kUpThreads, 5) lora_up_kernel(const __grid_con
     // tokens without an adapter
     if (a.base != a.y) {
         const int n0 = block0 * kBlock, n1 = min(a.N, n0 + blocks * kBlock);
-        for (int i = warp; i < kTokens && tok0 + i < (size_t)a.B; i += kUpWarps) {
+        for (int i = warp; i < kTokens && tok0 + i < (size_t)a.B; i += kWarps) {
             if (tile.id[i] >= 0) continue;
             for (int col = n0 + lane; col < n1; col += 32)
                 a.y[(tok0 + i) * a.y_stride + col] = a.base ? a.base[(tok0 + i) * a.base_stride + col] : 0.0f;
@@ -548,7 +598,7 @@ cudaError_t launch_rank(const LoraArgs &a, dim3 down, dim3 up, cudaStream_t st)
     cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, lora_down_kernel<(R < kDownRows ? R : kDownRows), TYPE>, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(lora_up_kernel<R, TYPE>, up, dim3(kUpThreads), 0, st, a);
+    return launch_pdl(lora_up_kernel<R, TYPE>, up, dim3(kThreads), 0, st, a);
 }
 
 template <int TYPE>
@@ -573,7 +623,7 @@ Cut cut_k(int B, int K, int R)
     const int wanted = (blocks + 2 * kWarps - 1) / (2 * kWarps);
     Cut c{(B + kTokens - 1) / kTokens, 1, 1, 0};
     while (c.cluster < kCluster && c.cluster < wanted) c.cluster *= 2;
-    const int room = 2 * num_sms() / (c.tiles * halves * kCluster);
+    const int room = 2 * num_sms() / ((B + kGroup * kQ - 1) / (kGroup * kQ) * halves * kCluster);
     while (c.parts < kParts && c.parts * 2 * kCluster <= wanted && c.parts * 2 <= room) c.parts *= 2;
     c.per_split = (blocks + c.cluster * c.parts - 1) / (c.cluster * c.parts);
     return c;
@@ -593,14 +643,13 @@ cudaError_t launch_lora(const LoraArgs &args, int type, cudaStream_t st)
     const int splits = cut.cluster * cut.parts, halves = a.R > kDownRows ? a.R / kDownRows : 1;
     // units of a tile taken at the same time: as many as there can be, while the
     // grid is not several times the GPU already (a CTA takes the others in turn)
-    const int most = min(a.n, min(a.B, kTokens)) + (a.B > 8 * kQ ? 1 : 0);
+    const int most = min(a.n, min(a.B, kTokens)) + (a.B > kGroup * kQ ? 1 : 0);
     const long long room = 8LL * num_sms() / ((long long)cut.tiles * halves * splits);
     const dim3 down(cut.tiles * halves, (unsigned)(room < 1 ? 1 : room > most ? most : room), splits);
-    // column blocks of a CTA of the second kernel: a power of two that leaves
-    // about six CTAs for every SM
-    const long long cols = (a.N + kBlock - 1) / kBlock;
-    a.blocks = 1;
-    while (a.blocks < 64 && cols * cut.tiles > 6LL * num_sms() * a.blocks) a.blocks *= 2;
+    // column blocks of a CTA of the second kernel: about two CTAs for every SM,
+    // each of which prepares its tile's h once
+    const long long cols = (a.N + kBlock - 1) / kBlock, want = (cols * cut.tiles + 2 * num_sms() - 1) / (2 * num_sms());
+    a.blocks = (int)(want < 1 ? 1 : want > 64 ? 64 : want);
     const dim3 up(cut.tiles, (unsigned)((cols + a.blocks - 1) / a.blocks));
     return type == ZQ_BF16 ? launch_type<ZQ_BF16>(a, down, up, st) : launch_type<ZQ_F16>(a, down, up, st);
 }
