@@ -215,7 +215,9 @@ template <int RR, int TYPE>
 __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_constant__ LoraArgs a)
 {
     constexpr int kCols = RR / 8;   // MMAs' columns: rows of A
-    __shared__ float red[kWarps / 2][kCols][kQ][4][32];
+    constexpr int kValues = kCols * kQ * 4 * 32;
+    __shared__ float part_s[kWarps][kCols][kQ][4][32];   // the warps' sums
+    __shared__ float sum_s[kValues];                     // the CTA's
     __shared__ __align__(16) Tile tile;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();   // codes and ids come from earlier kernels
@@ -230,18 +232,21 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
 
     for (int u = blockIdx.y; u < tile.units; u += gridDim.y) {   // the same in all CTAs of the cluster
         const int group0 = tile.unit[u], nq = tile.unit_groups[u], adapter = tile.adapter[group0];
-        const char *A = a.A + (((size_t)adapter * a.R + row0 + g) * a.K + 8 * c) * 2;
-        const size_t step = (size_t)8 * a.K * 2;   // eight rows on
+        const int first = b0 + warp;               // this warp's blocks: first, first + kWarps, .. below b1
+        const char *A[kCols];
         const int8_t *x[kQ][2];
         const uint16_t *d[kQ][2];
+#pragma unroll
+        for (int r = 0; r < kCols; ++r)
+            A[r] = a.A + (((size_t)adapter * a.R + row0 + 8 * r + g) * a.K + 32 * (size_t)first + 8 * c) * 2;
 #pragma unroll
         for (int q = 0; q < kQ; ++q)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {   // rows without a token repeat the first, unused
                 const int of = q < nq ? tile.token(group0 + q, g + 8 * e) : kNone;
                 const size_t t = tok0 + (of == kNone ? tile.token(group0, 0) : of);
-                x[q][e] = a.qs + t * a.K + 8 * c;
-                d[q][e] = a.d + t * blocks;
+                x[q][e] = a.qs + t * a.K + 32 * (size_t)first + 8 * c;
+                d[q][e] = a.d + t * blocks + first;
             }
         float sum[kCols][kQ][4] = {};
         // the next block's values are on their way while this one's are used
@@ -250,18 +255,21 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
             uint2 codes[kQ][2];
             uint16_t d[kQ][2];
         };
-        auto fetch = [&](int b, Block &f) {
-            b = min(b, blocks - 1);   // past the end: read, not used
+        auto fetch = [&](Block &f) {   // and on to the block after it
 #pragma unroll
-            for (int r = 0; r < kCols; ++r)
-                f.w[r] = __ldg(reinterpret_cast<const uint4 *>(A + r * step + 64 * (size_t)b));
+            for (int r = 0; r < kCols; ++r) {
+                f.w[r] = __ldg(reinterpret_cast<const uint4 *>(A[r]));
+                A[r] += 64 * kWarps;
+            }
 #pragma unroll
             for (int q = 0; q < kQ; ++q)
                 if (q < nq)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        f.codes[q][e] = __ldg(reinterpret_cast<const uint2 *>(x[q][e] + 32 * b));
-                        f.d[q][e] = __ldg(d[q][e] + b);
+                        f.codes[q][e] = __ldg(reinterpret_cast<const uint2 *>(x[q][e]));
+                        f.d[q][e] = __ldg(d[q][e]);
+                        x[q][e] += 32 * kWarps;
+                        d[q][e] += kWarps;
                     }
         };
         auto use = [&](const Block &f) {
@@ -288,53 +296,34 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
             }
         };
         Block even, odd;
-        if (b0 + warp < b1) fetch(b0 + warp, even);
-        for (int b = b0 + warp; b < b1; b += 2 * kWarps) {
-            fetch(b + kWarps, odd);
+        if (first < b1) fetch(even);
+        for (int b = first; b < b1; b += 2 * kWarps) {
+            if (b + kWarps < b1) fetch(odd);
             use(even);
-            fetch(b + 2 * kWarps, even);
+            if (b + 2 * kWarps < b1) fetch(even);
             if (b + kWarps < b1) use(odd);
         }
-        // the warps' sums, as a tree: the upper half hands over, the lower half adds
+        // the warps' sums, in order
 #pragma unroll
-        for (int half = kWarps / 2; half >= 1; half >>= 1) {
-            __syncthreads();
-            if (warp >= half && warp < 2 * half) {
+        for (int r = 0; r < kCols; ++r)
 #pragma unroll
-                for (int r = 0; r < kCols; ++r)
+            for (int q = 0; q < kQ; ++q)
+                if (q < nq)
 #pragma unroll
-                    for (int q = 0; q < kQ; ++q)
-                        if (q < nq)
+                    for (int e = 0; e < 4; ++e) part_s[warp][r][q][e][lane] = sum[r][q][e];
+        __syncthreads();
+        for (int i = threadIdx.x; i < kValues; i += kThreads) {
+            float v = 0.0f;
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) red[warp - half][r][q][e][lane] = sum[r][q][e];
-            }
-            __syncthreads();
-            if (warp < half) {
-#pragma unroll
-                for (int r = 0; r < kCols; ++r)
-#pragma unroll
-                    for (int q = 0; q < kQ; ++q)
-                        if (q < nq)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) sum[r][q][e] += red[warp][r][q][e][lane];
-            }
-        }
-        if (warp == 0) {
-#pragma unroll
-            for (int r = 0; r < kCols; ++r)
-#pragma unroll
-                for (int q = 0; q < kQ; ++q)
-                    if (q < nq)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) red[0][r][q][e][lane] = sum[r][q][e];
+            for (int w = 0; w < kWarps; ++w) v += (&part_s[w][0][0][0][0])[i];
+            sum_s[i] = v;
         }
         // each CTA of the cluster adds up its share of the values, in the order of the ranges
         __syncwarp();
         if (a.cluster > 1) cluster_sync();
         else __syncthreads();
-        constexpr int kValues = kCols * kQ * 4 * 32;
         const int share = kValues / a.cluster;
-        const uint32_t local = smem_u32(&red[0][0][0][0][0]);
+        const uint32_t local = smem_u32(sum_s);
         for (int i = rank * share + threadIdx.x; i < (rank + 1) * share; i += kThreads) {
             const int l = i & 31, e = i >> 5 & 3, q = i >> 7 & (kQ - 1), r = i / (kQ * 128);
             const int of = q < nq ? tile.token(group0 + q, (l >> 2) + 8 * (e >> 1)) : kNone;
@@ -441,54 +430,67 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
         }
         // h of the groups' members: its parts in order, times the adapter's scale, as two 16-bit parts in the
         // fragments' order; R / 4 neighbouring threads have a member, four values each
+        constexpr int kAhead = 4;
         const int items = n * kGroup * (R / 4);
-        for (int i = tid; i < items; i += kThreads) {   // whole warps: items is a multiple of 32
-            const int m = i / (R / 4), r = i % (R / 4) * 4, grp = m / kGroup, row = m % kGroup;
-            const int of = tile.token(g0 + grp, row);
-            float4 f = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            float scale = 1.0f;
-            if (of != kNone) {
-                if (a.scales) scale = a.scales[tile.adapter[g0 + grp]];
-                const float *h = a.h + (tok0 + of) * R + r;
+        for (int i0 = tid; i0 < items; i0 += kAhead * kThreads) {   // whole warps: items is a multiple of 32
+            float4 read[kAhead];
+            float scales[kAhead];
 #pragma unroll
-                for (int s = 0; s < kParts; ++s)
-                    if (s < a.parts) {
-                        const float4 p = *reinterpret_cast<const float4 *>(h + (size_t)s * a.B * R);
-                        f.x += p.x;
-                        f.y += p.y;
-                        f.z += p.z;
-                        f.w += p.w;
-                    }
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kThreads, m = i / (R / 4), grp = min(m / kGroup, n - 1);
+                const int of = i < items ? tile.token(g0 + grp, m % kGroup) : kNone;
+                read[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                scales[k] = 1.0f;
+                if (of == kNone) continue;
+                if (a.scales) scales[k] = a.scales[tile.adapter[g0 + grp]];
+                const float *h = a.h + (tok0 + of) * R + i % (R / 4) * 4;
+                read[k] = *reinterpret_cast<const float4 *>(h);
+#pragma unroll 1
+                for (int s = 1; s < a.parts; ++s) {
+                    const float4 p = *reinterpret_cast<const float4 *>(h + (size_t)s * a.B * R);
+                    read[k].x += p.x;
+                    read[k].y += p.y;
+                    read[k].z += p.z;
+                    read[k].w += p.w;
+                }
             }
-            float x[4] = {scale * f.x, scale * f.y, scale * f.z, scale * f.w};
-            float up = 1.0f;
-            if constexpr (TYPE == ZQ_F16) {   // binary16 parts need the row near 1
-                float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
-                for (int off = 1; off < R / 4; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
-                const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
-                const float down = __int_as_float((127 - e) << 23);
-                up = __int_as_float((127 + e) << 23);
+            for (int k = 0; k < kAhead; ++k) {
+                const int i = i0 + k * kThreads;
+                if (i >= items) break;
+                const int m = i / (R / 4), r = i % (R / 4) * 4, grp = m / kGroup, row = m % kGroup;
+                const float4 f = read[k];
+                const float scale = scales[k];
+                float x[4] = {scale * f.x, scale * f.y, scale * f.z, scale * f.w};
+                float up = 1.0f;
+                if constexpr (TYPE == ZQ_F16) {   // binary16 parts need the row near 1
+                    float amax = fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3])));
 #pragma unroll
-                for (int k = 0; k < 4; ++k) x[k] *= down;
-            }
-            if (r == 0) back_s[grp][row] = up;
-            const int s = R <= 16 ? 0 : 2 * (r / 32) + (r >> 2 & 1), l = row % 8 * 4;
-            uint32_t *hi_to = reinterpret_cast<uint32_t *>(h_s[grp][s][0]), *lo_to =
-                reinterpret_cast<uint32_t *>(h_s[grp][s][1]);
+                    for (int off = 1; off < R / 4; off <<= 1) amax = fmaxf(amax, __shfl_xor_sync(kAll, amax, off));
+                    const int e = min(max((int)(__float_as_uint(amax) >> 23) - 127, -126), 126);
+                    const float down = __int_as_float((127 - e) << 23);
+                    up = __int_as_float((127 + e) << 23);
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint32_t hi = kv_pack2<TYPE>(x[2 * k], x[2 * k + 1]);
-                float2 y;
-                if constexpr (TYPE == ZQ_BF16)
-                    y = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
-                else y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                const uint32_t lo = kv_pack2<TYPE>(x[2 * k] - y.x, x[2 * k + 1] - y.y);
-                // register row / 8 (+ 2 for a step's upper eight) of the lane that has these values
-                const int at = R == 8 ? 4 * (l + r / 2 + k) + row / 8
-                                      : 4 * (l + (R == 16 ? r / 4 : (r & 31) >> 3)) + row / 8 + 2 * k;
-                hi_to[at] = hi;
-                lo_to[at] = lo;
+                    for (int j = 0; j < 4; ++j) x[j] *= down;
+                }
+                if (r == 0) back_s[grp][row] = up;
+                const int s = R <= 16 ? 0 : 2 * (r / 32) + (r >> 2 & 1), l = row % 8 * 4;
+                uint32_t *hi_to = reinterpret_cast<uint32_t *>(h_s[grp][s][0]), *lo_to =
+                    reinterpret_cast<uint32_t *>(h_s[grp][s][1]);
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const uint32_t hi = kv_pack2<TYPE>(x[2 * j], x[2 * j + 1]);
+                    float2 y;
+                    if constexpr (TYPE == ZQ_BF16)
+                        y = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
+                    else y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
+                    const uint32_t lo = kv_pack2<TYPE>(x[2 * j] - y.x, x[2 * j + 1] - y.y);
+                    // register row / 8 (+ 2 for a step's upper eight) of the lane that has these values
+                    const int at = R == 8 ? 4 * (l + r / 2 + j) + row / 8
+                                          : 4 * (l + (R == 16 ? r / 4 : (r & 31) >> 3)) + row / 8 + 2 * j;
+                    hi_to[at] = hi;
+                    lo_to[at] = lo;
+                }
             }
         }
         __syncthreads();
