@@ -135,6 +135,7 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t &lo, uint32_t &hi)
 // MMA's rows), its groups in units of up to two.
 struct Tile {
     int id[kTokens];               // adapter of a token, -1: none (or past the last token)
+    int seen[kTokens];             // tokens of its adapter | those before it << 8 | the first one << 16
     int base[kTokens];             // first group of a token's adapter, at the adapter's first token
     int half, groups, units;       // groups | units << 16 of the lower 32 tokens; in all
     int adapter[kTokens];          // of a group
@@ -147,35 +148,51 @@ struct Tile {
     }
 };
 
+// By all kThreads threads: four of them compare a token's adapter with the
+// tile's, then the lower 64 have a token each.
 __device__ __forceinline__ void tile_open(Tile &s, const LoraArgs &a, int tile)
 {
     const int t = threadIdx.x, lane = t & 31;
-    int id = -1;
     if (t < kTokens) {
         const int at = tile * kTokens + t;
-        if (at < a.B) id = a.ids[at];
+        int id = at < a.B ? a.ids[at] : -1;
         if (id < 0 || id >= a.n) id = -1;
         s.id[t] = id;
 #pragma unroll
         for (int i = 0; i < kGroup / 4; ++i) s.tok[t][i] = 0xffffffffu;
     }
     __syncthreads();
-    int before = 0, total = 0, first = t, incl = 0, own = 0;
-    if (t < kTokens) {
+    {
+        const int me = t / 4, j0 = t % 4 * 16, mine = s.id[me];
+        int total = 0, before = 0, first = kTokens;
 #pragma unroll
-        for (int j = 0; j < kTokens; j += 4) {
-            const int4 o = *reinterpret_cast<const int4 *>(s.id + j);
+        for (int j = 0; j < 16; j += 4) {
+            const int4 o = *reinterpret_cast<const int4 *>(s.id + j0 + j);
             const int v[4] = {o.x, o.y, o.z, o.w};
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                const bool same = v[k] == id;
+                const bool same = v[k] == mine;
                 total += same;
-                before += same && j + k < t;
-                if (same) first = min(first, j + k);
+                before += same && j0 + j + k < me;
+                if (same) first = min(first, j0 + j + k);
             }
         }
+#pragma unroll
+        for (int off = 1; off <= 2; off <<= 1) {
+            total += __shfl_xor_sync(kAll, total, off);
+            before += __shfl_xor_sync(kAll, before, off);
+            first = min(first, __shfl_xor_sync(kAll, first, off));
+        }
+        if (t % 4 == 0) s.seen[me] = total | before << 8 | first << 16;
+    }
+    __syncthreads();
+    int id = -1, before = 0, first = 0, own = 0, incl = 0;
+    if (t < kTokens) {
+        id = s.id[t];
+        before = s.seen[t] >> 8 & 0xff;
+        first = s.seen[t] >> 16;
         if (id >= 0 && before == 0) {
-            const int groups = (total + kGroup - 1) / kGroup;
+            const int groups = ((s.seen[t] & 0xff) + kGroup - 1) / kGroup;
             own = groups | (groups + kQ - 1) / kQ << 16;
         }
         incl = own;
@@ -421,8 +438,8 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
         int block = t0 / n, group = t0 - block * n;
         auto col_of = [&](int block) { return (block0 + block) * kBlock; };
         auto aligned = [&](int block) { return a.vec && (block0 + block + 1) * kBlock <= a.N; };
-        Task now;
-        if (t0 < t1) fetch(g0 + group, col_of(block), aligned(block), true, now);
+        Task even, odd;
+        if (t0 < t1) fetch(g0 + group, col_of(block), aligned(block), true, even);
         if (!waited) {
             pdl_wait();
             pdl_launch_dependents();
@@ -494,10 +511,10 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
             }
         }
         __syncthreads();
-        for (int task = t0; task < t1; ++task) {
+        // One task, the one after it (the block's next group, or the next block's first) on its way.
+        auto work = [&](bool more, const Task &now, Task &next) {
             const int here = group, col0 = col_of(block);
             const bool vec = aligned(block);
-            // the next task: the block's next group, or the next block's first
             const int adapter = tile.adapter[g0 + group];
             bool weights = false;
             if (++group == n) {
@@ -505,8 +522,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                 ++block;
                 weights = true;
             }
-            Task next;
-            if (task + 1 < t1) {
+            if (more) {
                 weights |= tile.adapter[g0 + group] != adapter;
                 if (!weights) {
 #pragma unroll
@@ -563,7 +579,10 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                 }
             }
             __syncwarp();
-            now = next;
+        };
+        for (int task = t0; task < t1; task += 2) {
+            work(task + 1 < t1, even, odd);
+            if (task + 1 < t1) work(task + 2 < t1, odd, even);
         }
         __syncthreads();   // the fragments have been used
     }
@@ -643,10 +662,11 @@ cudaError_t launch_lora(const LoraArgs &args, int type, cudaStream_t st)
     a.parts = cut.parts;
     a.per_split = cut.per_split;
     const int splits = cut.cluster * cut.parts, halves = a.R > kDownRows ? a.R / kDownRows : 1;
-    // units of a tile taken at the same time: as many as there can be, while the
-    // grid is not several times the GPU already (a CTA takes the others in turn)
+    // units of a tile taken at the same time: as many as there can be, in a grid
+    // that the GPU holds at once (a CTA takes the others in turn: starting one
+    // costs more than two blocks' worth of its work)
     const int most = min(a.n, min(a.B, kTokens)) + (a.B > kGroup * kQ ? 1 : 0);
-    const long long room = 8LL * num_sms() / ((long long)cut.tiles * halves * splits);
+    const long long room = 2LL * num_sms() / ((long long)cut.tiles * halves * splits);
     const dim3 down(cut.tiles * halves, (unsigned)(room < 1 ? 1 : room > most ? most : room), splits);
     // column blocks of a CTA of the second kernel: about two CTAs for every SM,
     // each of which prepares its tile's h once
