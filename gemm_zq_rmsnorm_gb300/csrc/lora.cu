@@ -359,7 +359,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
 // blocks of 32).  A task is one block for one group of sixteen tokens; a warp
 // takes neighbouring tasks of one block after the other, the next one's values
 // on their way while it works on one.
-template <int R, int TYPE>
+// VEC: rows of base and y are 16-byte aligned and N is a multiple of four, so
+// four outputs move at once (values alone cost the 17408-wide decode batch half
+// as much again).
+template <int R, int TYPE, bool VEC>
 __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(const __grid_constant__ LoraArgs a)
 {
     constexpr int kSteps = R < 16 ? 1 : R / 16;
@@ -367,11 +370,17 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
     __shared__ __align__(16) Tile tile;
     __shared__ uint4 h_s[kUpGroups][kSteps][2][32];   // fragments of h: the upper parts, the lower ones
     __shared__ float back_s[kUpGroups][kGroup];       // 2^e of a member's scaling
+    __shared__ const float *from_s[kTokens];          // rows of base and y
+    __shared__ float *to_s[kTokens];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const size_t tok0 = (size_t)blockIdx.x * kTokens;
     const int block0 = blockIdx.y * a.blocks, blocks = min(a.blocks, (a.N + kBlock - 1) / kBlock - block0);
     // The first kernel lets this one start only when all before it is complete:
     // ids, base and weights may be read ahead of the wait, h may not.
+    if (tid < kTokens) {
+        from_s[tid] = a.base + (a.base ? (tok0 + tid) * a.base_stride : 0);
+        to_s[tid] = a.y + (tok0 + tid) * a.y_stride;
+    }
     tile_open(tile, a, blockIdx.x);
     bool waited = false;
 
@@ -381,7 +390,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
         uint32_t w[2][2][kSteps][2];
         float4 v[2][2];             // base of rows g, g + 8
     };
-    auto fetch = [&](int group, int col0, bool vec, bool weights, Task &f) {
+    auto fetch = [&](int group, int col0, bool weights, Task &f) {
         if (weights) {
             const char *row0 = a.Bm + (size_t)tile.adapter[group] * a.N * R * 2 + kRun * 2 * c;
 #pragma unroll
@@ -389,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int n = col0 + 16 * p + 4 * (g >> 1) + 2 * i + (g & 1);
-                    const char *row = row0 + (size_t)min(a.N - 1, n) * R * 2;
+                    const char *row = row0 + (uint32_t)min(a.N - 1, n) * (R * 2);
                     if constexpr (R == 8) {
                         f.w[p][i][0][0] = __ldg(reinterpret_cast<const uint32_t *>(row));
                         f.w[p][i][0][1] = 0;
@@ -409,23 +418,22 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                     }
                 }
         }
+        // a row without a token reads the group's first, a column past the last the last: neither is stored
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int t = tile.token(group, g + 8 * e);
-            const bool in = a.base && t != kNone;
-            const float *from = a.base + (in ? (tok0 + t) * a.base_stride + col0 + 4 * c : 0);
+            const float *from = from_s[t == kNone ? tile.token(group, 0) : t];
 #pragma unroll
             for (int p = 0; p < 2; ++p) {
-                f.v[e][p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                if (!in) continue;
-                if (vec) {
-                    f.v[e][p] = *reinterpret_cast<const float4 *>(from + 16 * p);
+                const int n = col0 + 16 * p + 4 * c;
+                if (!a.base) {
+                    f.v[e][p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                } else if constexpr (VEC) {
+                    f.v[e][p] = *reinterpret_cast<const float4 *>(from + min(n, a.N - 4));
                 } else {
-                    const int left = a.N - (col0 + 16 * p + 4 * c);
-                    if (left > 0) f.v[e][p].x = from[16 * p];
-                    if (left > 1) f.v[e][p].y = from[16 * p + 1];
-                    if (left > 2) f.v[e][p].z = from[16 * p + 2];
-                    if (left > 3) f.v[e][p].w = from[16 * p + 3];
+                    const int last = a.N - 1;
+                    f.v[e][p] = make_float4(from[min(n, last)], from[min(n + 1, last)], from[min(n + 2, last)],
+                                            from[min(n + 3, last)]);
                 }
             }
         }
@@ -437,9 +445,8 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
         const int t0 = warp * blocks * n / kWarps, t1 = (warp + 1) * blocks * n / kWarps;
         int block = t0 / n, group = t0 - block * n;
         auto col_of = [&](int block) { return (block0 + block) * kBlock; };
-        auto aligned = [&](int block) { return a.vec && (block0 + block + 1) * kBlock <= a.N; };
         Task even, odd;
-        if (t0 < t1) fetch(g0 + group, col_of(block), aligned(block), true, even);
+        if (t0 < t1) fetch(g0 + group, col_of(block), true, even);
         if (!waited) {
             pdl_wait();
             pdl_launch_dependents();
@@ -514,7 +521,6 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
         // One task, the one after it (the block's next group, or the next block's first) on its way.
         auto work = [&](bool more, const Task &now, Task &next) {
             const int here = group, col0 = col_of(block);
-            const bool vec = aligned(block);
             const int adapter = tile.adapter[g0 + group];
             bool weights = false;
             if (++group == n) {
@@ -534,7 +540,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
 #pragma unroll
                                 for (int k = 0; k < 2; ++k) next.w[p][i][s][k] = now.w[p][i][s][k];
                 }
-                fetch(g0 + group, col_of(block), aligned(block), weights, next);
+                fetch(g0 + group, col_of(block), weights, next);
             }
             float y[2][2][4];
 #pragma unroll
@@ -560,20 +566,20 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                 const int t = tile.token(g0 + here, g + 8 * e);
                 if (t != kNone) {
                     const float f = TYPE == ZQ_F16 ? back_s[here][g + 8 * e] : 1.0f;
-                    float *to = a.y + (tok0 + t) * a.y_stride + col0 + 4 * c;
+                    float *to = to_s[t];
 #pragma unroll
                     for (int p = 0; p < 2; ++p) {
+                        const int n = col0 + 16 * p + 4 * c;
                         const float4 v = now.v[e][p];
                         const float4 r = make_float4(v.x + y[p][0][2 * e] * f, v.y + y[p][0][2 * e + 1] * f,
                                                      v.z + y[p][1][2 * e] * f, v.w + y[p][1][2 * e + 1] * f);
-                        if (vec) {
-                            *reinterpret_cast<float4 *>(to + 16 * p) = r;
+                        if constexpr (VEC) {
+                            if (n < a.N) *reinterpret_cast<float4 *>(to + n) = r;
                         } else {
-                            const int left = a.N - (col0 + 16 * p + 4 * c);
-                            if (left > 0) to[16 * p] = r.x;
-                            if (left > 1) to[16 * p + 1] = r.y;
-                            if (left > 2) to[16 * p + 2] = r.z;
-                            if (left > 3) to[16 * p + 3] = r.w;
+                            if (n < a.N) to[n] = r.x;
+                            if (n + 1 < a.N) to[n + 1] = r.y;
+                            if (n + 2 < a.N) to[n + 2] = r.z;
+                            if (n + 3 < a.N) to[n + 3] = r.w;
                         }
                     }
                 }
@@ -619,7 +625,8 @@ cudaError_t launch_rank(const LoraArgs &a, dim3 down, dim3 up, cudaStream_t st)
     cfg.numAttrs = 2;
     cudaError_t e = cudaLaunchKernelEx(&cfg, lora_down_kernel<(R < kDownRows ? R : kDownRows), TYPE>, a);
     if (e != cudaSuccess) return e;
-    return launch_pdl(lora_up_kernel<R, TYPE>, up, dim3(kThreads), 0, st, a);
+    return a.vec ? launch_pdl(lora_up_kernel<R, TYPE, true>, up, dim3(kThreads), 0, st, a)
+                 : launch_pdl(lora_up_kernel<R, TYPE, false>, up, dim3(kThreads), 0, st, a);
 }
 
 template <int TYPE>

@@ -893,7 +893,7 @@ int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const void *A, c
     p.base_stride = base_stride;
     p.y = y;
     p.y_stride = y_stride;
-    p.vec = aligned16(y) && y_stride % 4 == 0 && (!base || (aligned16(base) && base_stride % 4 == 0));
+    p.vec = N % 4 == 0 && aligned16(y) && y_stride % 4 == 0 && (!base || (aligned16(base) && base_stride % 4 == 0));
     p.h = static_cast<float *>(workspace);
     return launched(launch_lora(p, type, (cudaStream_t)stream), name);
 }

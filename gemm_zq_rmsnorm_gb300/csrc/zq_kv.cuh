@@ -106,7 +106,7 @@ struct LoraArgs {
     long long base_stride;
     float *y;
     long long y_stride;
-    int vec;                // base and y rows allow 16-byte pieces
+    int vec;                // base and y rows are 16-byte pieces
     float *h;               // workspace [parts][B][R]
     int cluster, parts, per_split, blocks;   // set by the launcher
 };
