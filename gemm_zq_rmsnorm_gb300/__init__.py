@@ -479,12 +479,29 @@ def _on(index: int, what: str, *tensors):
             raise ValueError(f"{what}: a tensor is not on cuda:{index}")
 
 
+def _stream_on(stream, index: int) -> int:
+    """Address of the stream, the current one of the device by default (without
+    the Stream object of torch.cuda.current_stream, most of a small call's time)."""
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+
+
+def _new(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor for the call, which its memory outlives on the call's own stream."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
+
+
 def _head_rows(t: torch.Tensor, T: int, D: int, what: str):
     """(address, row stride, heads) of fp32 rows [T][H][D] or [T][H * D]."""
     shape, stride = t.shape, t.stride()
-    n = shape[1] if len(shape) == 2 else shape[1] * D if len(shape) == 3 and shape[2] == D else 0
-    if (t.dtype != torch.float32 or shape[0] != T or n < D or n % D or stride[-1] != 1
-            or (len(shape) == 3 and shape[1] > 1 and stride[1] != D)):
+    if len(shape) == 2:
+        n, ok = shape[1], stride[1] == 1
+    else:
+        ok = len(shape) == 3 and shape[2] == D and stride[2] == 1 and (shape[1] == 1 or stride[1] == D)
+        n = shape[1] * D if ok else 0
+    if not ok or shape[0] != T or n < D or n % D or t.dtype != torch.float32:
         raise ValueError(f"{what} must be fp32 rows [{T}][H][{D}] or [{T}][H * {D}] with the heads of a row together")
     return t.data_ptr(), stride[0] if T > 1 else n, n // D
 
@@ -525,7 +542,7 @@ def head_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma_q, g
     lib = _lib or load()
     D, T = cache.D, q.shape[0]
     if q_out is None:
-        q_out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        q_out = _new(q.shape, torch.float32, q.device, stream)
     _on(cache.index, "head_norm_rope", q, k, v, gamma_q, gamma_k, table, pos, slots, q_out)
     qp, qs, Hq = _head_rows(q, T, D, "head_norm_rope: q")
     kp, ks, Hk = _head_rows(k, T, D, "head_norm_rope: k")
@@ -533,9 +550,12 @@ def head_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma_q, g
     op, os_, Ho = _head_rows(q_out, T, D, "head_norm_rope: q_out")
     if Hk != cache.Hk or Hv != cache.Hk or Ho != Hq:
         raise ValueError("head_norm_rope: the heads of k and v must be the cache's, those of q_out q's")
-    for g in (gamma_q, gamma_k):
-        if g is not None and (g.dtype != torch.float32 or g.numel() != D or not g.is_contiguous()):
-            raise ValueError(f"head_norm_rope: gamma must be {D} contiguous fp32 values")
+    gamma = [None, None]
+    for i, g in enumerate((gamma_q, gamma_k)):
+        if g is not None:
+            if g.dtype != torch.float32 or g.numel() != D or not g.is_contiguous():
+                raise ValueError(f"head_norm_rope: gamma must be {D} contiguous fp32 values")
+            gamma[i] = g.data_ptr()
     rot, axes, pp = 0, 1, None
     if table is not None:
         if table.dtype != torch.int64 or not table.is_contiguous():
@@ -543,9 +563,11 @@ def head_norm_rope(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, gamma_q, g
         rot = 2 * table.numel()
         axes = pos.shape[0] if pos.dim() == 2 else 1
         pp = _ints(pos, axes * T, "head_norm_rope: pos")
-    _check(lib.zq_head_norm_rope(qp, qs, kp, ks, vp, vs, T, Hq, _ptr(gamma_q), _ptr(gamma_k), eps,
-                                 table.data_ptr() if rot else None, rot, interleaved, pp, axes, cache._ref,
-                                 _ints(slots, T, "head_norm_rope: slots"), op, os_, _stream(stream)))
+    status = lib.zq_head_norm_rope(qp, qs, kp, ks, vp, vs, T, Hq, gamma[0], gamma[1], eps,
+                                   table.data_ptr() if rot else None, rot, interleaved, pp, axes, cache._ref,
+                                   _ints(slots, T, "head_norm_rope: slots"), op, os_, _stream_on(stream, cache.index))
+    if status:
+        _check(status)
     return q_out
 
 
@@ -564,10 +586,9 @@ def paged_attn(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch
     D, B = cache.D, q.shape[0]
     qp, qs, Hq = _head_rows(q, B, D, "paged_attn: q")
     if out is None and q8_out is None:
-        out = torch.empty(q.shape, dtype=torch.float32, device=q.device)
+        out = _new(q.shape, torch.float32, q.device, stream)
     if workspace is None:
-        workspace = torch.empty(lib.zq_paged_attn_workspace_bytes(Hq, cache.Hk, D), dtype=torch.uint8,
-                                device=q.device)
+        workspace = _new(lib.zq_paged_attn_workspace_bytes(Hq, cache.Hk, D), torch.uint8, q.device, stream)
     _on(cache.index, "paged_attn", q, table, lens, out, lse, workspace)
     op, os_ = None, 0
     if out is not None:
@@ -584,10 +605,13 @@ def paged_attn(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch
         _on(cache.index, "paged_attn", q8_out.qs, q8_out.d, q8_out.s)
         _q8_planes(q8_out, B, Hq * D, "paged_attn: q8_out")
         q8 = ctypes.byref(q8_out._c())
-    _check(lib.zq_paged_attn(qp, qs, B, Hq, cache._ref, _ints(table, B * width, "paged_attn: table"), width,
-                             _ints(lens, B, "paged_attn: lens"), D ** -0.5 if scale is None else scale, window, op, os_,
-                             None if lse is None else lse.data_ptr(), q8, workspace.data_ptr(),
-                             workspace.numel() * workspace.element_size(), _stream(stream)))
+    status = lib.zq_paged_attn(qp, qs, B, Hq, cache._ref, _ints(table, B * width, "paged_attn: table"), width,
+                               _ints(lens, B, "paged_attn: lens"), D ** -0.5 if scale is None else scale, window,
+                               op, os_,
+                               None if lse is None else lse.data_ptr(), q8, workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), _stream_on(stream, cache.index))
+    if status:
+        _check(status)
     return out
 
 
@@ -622,18 +646,20 @@ def lora(a: Q8_1, ids: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, scales: 
         raise ValueError("lora: CUDA tensors are needed")
     dev = a.qs.device
     if y is None:
-        y = torch.empty((B, N), dtype=torch.float32, device=dev)
+        y = _new((B, N), torch.float32, dev, stream)
     if workspace is None:
-        workspace = torch.empty(lib.zq_lora_workspace_bytes(B, K, R), dtype=torch.uint8, device=dev)
+        workspace = _new(lib.zq_lora_workspace_bytes(B, K, R), torch.uint8, dev, stream)
     _on(dev.index, "lora", a.d, a.s, ids, A, Bm, scales, base, y, workspace)
     _q8_planes(a, B, K, "lora: a")
     yp, ys = _out_rows(y, B, N, "lora: y")
     bp, bs = (None, 0) if base is None else _out_rows(base, B, N, "lora: base")
     if scales is not None and (scales.dtype != torch.float32 or scales.numel() != n or not scales.is_contiguous()):
         raise ValueError(f"lora: scales must be {n} contiguous fp32 values")
-    _check(lib.zq_lora(a._c(), B, K, _ints(ids, B, "lora: ids"), n, A.data_ptr(), Bm.data_ptr(), R, _TYPES[A.dtype],
-                       _ptr(scales), N, bp, bs, yp, ys, workspace.data_ptr(),
-                       workspace.numel() * workspace.element_size(), _stream(stream)))
+    status = lib.zq_lora(a._c(), B, K, _ints(ids, B, "lora: ids"), n, A.data_ptr(), Bm.data_ptr(), R, _TYPES[A.dtype],
+                         None if scales is None else scales.data_ptr(), N, bp, bs, yp, ys, workspace.data_ptr(),
+                         workspace.numel() * workspace.element_size(), _stream_on(stream, dev.index))
+    if status:
+        _check(status)
     return y
 
 

@@ -43,7 +43,6 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kDownRows = 32;    // rows of A a CTA of the first kernel takes at most
 constexpr int kCluster = 8;      // CTAs of a cluster at most, which add up their K ranges
 constexpr int kParts = 4;        // sums the second kernel is left with at most
-constexpr int kUpGroups = 8;     // groups whose h the second kernel has in shared memory at a time
 constexpr int kBlock = 32;       // outputs of a warp at a time
 constexpr int kNone = 255;
 constexpr unsigned kAll = 0xffffffffu;
@@ -367,6 +366,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
 {
     constexpr int kSteps = R < 16 ? 1 : R / 16;
     constexpr int kRun = R < 32 ? R / 4 : 8;   // neighbouring values of R that a lane's fragment takes
+    constexpr int kUpGroups = R < 32 ? 16 : 8; // groups whose h is in shared memory at a time
     __shared__ __align__(16) Tile tile;
     __shared__ uint4 h_s[kUpGroups][kSteps][2][32];   // fragments of h: the upper parts, the lower ones
     __shared__ float back_s[kUpGroups][kGroup];       // 2^e of a member's scaling
@@ -675,9 +675,12 @@ cudaError_t launch_lora(const LoraArgs &args, int type, cudaStream_t st)
     const int most = min(a.n, min(a.B, kTokens)) + (a.B > kGroup * kQ ? 1 : 0);
     const long long room = 2LL * num_sms() / ((long long)cut.tiles * halves * splits);
     const dim3 down(cut.tiles * halves, (unsigned)(room < 1 ? 1 : room > most ? most : room), splits);
-    // column blocks of a CTA of the second kernel: about two CTAs for every SM,
-    // each of which prepares its tile's h once
-    const long long cols = (a.N + kBlock - 1) / kBlock, want = (cols * cut.tiles + 2 * num_sms() - 1) / (2 * num_sms());
+    // column blocks of a CTA of the second kernel: as many CTAs as the GPU holds
+    // at once (one an SM at R = 64, else two), each of which prepares its tile's
+    // h once (512 tokens at R = 64: 33.6 us, 37.0 with two an SM; 56 tokens at
+    // R = 16: 11.3 us, 11.9 with one)
+    const long long cols = (a.N + kBlock - 1) / kBlock, ctas = (a.R == 64 ? 1LL : 2LL) * num_sms();
+    const long long want = (cols * cut.tiles + ctas - 1) / ctas;
     a.blocks = (int)(want < 1 ? 1 : want > 64 ? 64 : want);
     const dim3 up(cut.tiles, (unsigned)((cols + a.blocks - 1) / a.blocks));
     return type == ZQ_BF16 ? launch_type<ZQ_BF16>(a, down, up, st) : launch_type<ZQ_F16>(a, down, up, st);
