@@ -57,13 +57,13 @@ __device__ __forceinline__ void store_row(float *p, const float (&x)[E])
     }
 }
 
-// x / scale rounded to the cache type, E neighbouring values
+// x times 1 / scale rounded to the cache type, E neighbouring values
 template <int TYPE, int E>
-__device__ __forceinline__ void store_cache(void *dst, const float (&x)[E], float scale)
+__device__ __forceinline__ void store_cache(void *dst, const float (&x)[E], float inverse)
 {
     float y[E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) y[e] = scale == 1.0f ? x[e] : __fdiv_rn(x[e], scale);
+    for (int e = 0; e < E; ++e) y[e] = x[e] * inverse;
     if constexpr (TYPE == ZQ_E4M3) {
         if constexpr (E == 2) {
             *static_cast<uint16_t *>(dst) = (uint16_t)kv_pack2<TYPE>(y[0], y[1]);
@@ -83,118 +83,127 @@ __device__ __forceinline__ void store_cache(void *dst, const float (&x)[E], floa
     }
 }
 
-template <int D, int TYPE>
+template <int D, int TYPE, bool INTER>
 __global__ void __launch_bounds__(kThreads) head_norm_rope_kernel(const __grid_constant__ HeadNormRopeArgs a)
 {
     constexpr int E = D / 32;
     pdl_wait();   // q/k/v, positions and slots come from earlier kernels
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const long long w = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-    const int t = (int)(w / a.chunks);
+    const int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    const int t = w / a.chunks;
     if (t >= a.T) return;
-    const int rows = a.Hq + 2 * a.Hk;
-    const int r0 = (int)(w - (long long)t * a.chunks) * a.chunk;
-    const int r1 = min(rows, r0 + a.chunk);
+    const int keys = a.Hq, values = a.Hq + a.Hk, rows = a.Hq + 2 * a.Hk;   // rows: queries, keys, values
+    const int r0 = (w - t * a.chunks) * a.chunk, r1 = min(rows, r0 + a.chunk);
     const int col = lane * E;
 
+    const float *q = a.q + (long long)t * a.q_stride + col;
+    const float *k = a.k + (long long)t * a.k_stride + col, *v = a.v + (long long)t * a.v_stride + col;
     auto src = [&](int r) {
-        if (r < a.Hq) return a.q + (long long)t * a.q_stride + (long long)r * D + col;
-        if (r < a.Hq + a.Hk) return a.k + (long long)t * a.k_stride + (long long)(r - a.Hq) * D + col;
-        return a.v + (long long)t * a.v_stride + (long long)(r - a.Hq - a.Hk) * D + col;
+        return r < keys ? q + r * D : r < values ? k + (r - keys) * D : v + (r - values) * D;
     };
-
     float x[kBatch][E];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
         if (r0 + u < r1) load_row(src(r0 + u), x[u]);
 
-    const bool qk = r0 < a.Hq + a.Hk;   // this warp has rows to norm and rotate
+    const bool qk = r0 < values;   // this warp has rows to norm and rotate
     float gq[E], gk[E], cs[E], sn[E];
     int partner = lane;
     const bool turned = qk && col < a.rot;
+    const int slot = a.slots[t];
     if (qk) {
         if (a.gamma_q) load_row(a.gamma_q + col, gq);
         if (a.gamma_k) load_row(a.gamma_k + col, gk);
     }
     if (turned) {
         const int half = a.rot >> 1;
-        const bool second = !a.interleaved && col >= half;
-        if (!a.interleaved) partner = second ? lane - half / E : lane + half / E;
+        const bool second = !INTER && col >= half;
+        if (!INTER) partner = second ? lane - half / E : lane + half / E;
+        // the positions are read beside the entries that choose between them
+        const int at0 = a.pos[t];
+        const int at1 = a.axes > 1 ? a.pos[(long long)a.T + t] : at0;
+        const int at2 = a.axes > 2 ? a.pos[2LL * a.T + t] : at1;
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-            const int p = a.interleaved ? (col + e) >> 1 : col + e - (second ? half : 0);
-            const uint64_t entry = a.table[p];
-            const int ax = min((int)(entry & 3u), a.axes - 1);
-            const int64_t at = a.pos[(long long)ax * a.T + t];
+            if (INTER && (e & 1)) {   // the pair's first value has the angle already
+                cs[e] = cs[e - 1];
+                sn[e] = -sn[e - 1];
+                continue;
+            }
+            const uint64_t entry = a.table[INTER ? (col + e) >> 1 : col + e - (second ? half : 0)];
+            const int ax = (int)(entry & 3u);
+            const int64_t at = ax == 0 ? at0 : ax == 1 ? at1 : at2;
             const uint64_t turns = (entry & ~(uint64_t)3) * (uint64_t)at;
             // top 32 bits as a signed fraction of a turn, times two: the argument in half turns
             sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn[e], &cs[e]);
             // the first of a pair takes -sin of its partner
-            if (a.interleaved ? !(e & 1) : !second) sn[e] = -sn[e];
+            if (!second) sn[e] = -sn[e];
         }
     }
-    const long long slot = a.slots[t];
+    __syncwarp();
     const bool keep = slot >= 0 && slot < a.nslots;
-    const int page = 1 << a.page_shift;
-    const long long cache_page = keep ? slot >> a.page_shift : 0;
-    const long long cache_off = keep ? slot & (page - 1) : 0;
+    // the token's place in the cache, at key head 0; a head further is a page's rows further
+    const long long place =
+        keep ? ((((long long)(slot >> a.page_shift) * a.Hk) << a.page_shift) + (slot & ((1 << a.page_shift) - 1))) * D : 0;
+    char *kc = static_cast<char *>(a.kc) + (place + col) * KvBytes<TYPE>::value;
+    char *vc = static_cast<char *>(a.vc) + (place + col) * KvBytes<TYPE>::value;
+    const long long head = ((long long)D << a.page_shift) * KvBytes<TYPE>::value;
+    float *out = a.q_out + (long long)t * a.q_out_stride + col;
+    const float k_inverse = 1.0f / a.k_scale, v_inverse = 1.0f / a.v_scale;
 
-    for (int rb = r0; rb < r1; rb += kBatch) {
-        if (rb != r0) {
+    auto row = [&](int r, float(&x)[E]) {
+        float y[E];
 #pragma unroll
-            for (int u = 0; u < kBatch; ++u)
-                if (rb + u < r1) load_row(src(rb + u), x[u]);
+        for (int e = 0; e < E; ++e) y[e] = x[e];
+        if (r + kBatch < r1) load_row(src(r + kBatch), x);   // the row four further on takes its place
+        if (r >= values) {
+            if (keep) store_cache<TYPE, E>(vc + (r - values) * head, y, v_inverse);
+            return;
         }
+        const bool is_q = r < keys;
+        if (is_q ? a.gamma_q != nullptr : a.gamma_k != nullptr) {
+            float ss = 0.0f;
 #pragma unroll
-        for (int u = 0; u < kBatch; ++u) {
-            const int r = rb + u;
-            if (r >= r1) break;
-            const bool is_q = r < a.Hq, is_v = r >= a.Hq + a.Hk;
-            if (!is_v) {
-                if (is_q ? a.gamma_q != nullptr : a.gamma_k != nullptr) {
-                    float ss = 0.0f;
+            for (int e = 0; e < E; ++e) ss = __fmaf_rn(y[e], y[e], ss);
+            ss = warp_sum(ss);
+            const float rms = rsqrtf(__fmaf_rn(ss, 1.0f / D, a.eps));
 #pragma unroll
-                    for (int e = 0; e < E; ++e) ss = __fmaf_rn(x[u][e], x[u][e], ss);
-                    ss = warp_sum(ss);
-                    const float rms = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(ss * (1.0f / D), a.eps)));
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[u][e] = x[u][e] * rms * (is_q ? gq[e] : gk[e]);
-                }
-                if (a.rot) {
-                    float y[E];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) {
-                        const float other = __shfl_sync(0xffffffffu, x[u][e], partner);
-                        y[e] = a.interleaved ? x[u][e ^ 1] : other;
-                    }
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        if (turned) y[e] = __fmaf_rn(x[u][e], cs[e], y[e] * sn[e]);
-                        else y[e] = x[u][e];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) x[u][e] = y[e];
-                }
-            }
-            if (is_q) {
-                store_row(a.q_out + (long long)t * a.q_out_stride + (long long)r * D + col, x[u]);
-            } else if (keep) {
-                const int h = r - a.Hq - (is_v ? a.Hk : 0);
-                const long long row = ((cache_page * a.Hk + h) << a.page_shift) + cache_off;
-                char *dst = static_cast<char *>(is_v ? a.vc : a.kc) + (row * D + col) * KvBytes<TYPE>::value;
-                store_cache<TYPE, E>(dst, x[u], is_v ? a.v_scale : a.k_scale);
-            }
+            for (int e = 0; e < E; ++e) y[e] = y[e] * rms * (is_q ? gq[e] : gk[e]);
         }
-    }
+        if (a.rot) {
+            float z[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) z[e] = INTER ? y[e ^ 1] : __shfl_sync(0xffffffffu, y[e], partner);
+#pragma unroll
+            for (int e = 0; e < E; ++e) y[e] = turned ? __fmaf_rn(y[e], cs[e], z[e] * sn[e]) : y[e];
+        }
+        if (is_q) store_row(out + r * D, y);
+        else if (keep) store_cache<TYPE, E>(kc + (r - keys) * head, y, k_inverse);
+    };
+    int r = r0;
+    for (; r + kBatch <= r1; r += kBatch)
+#pragma unroll
+        for (int u = 0; u < kBatch; ++u) row(r + u, x[u]);
+#pragma unroll
+    for (int u = 0; u < kBatch - 1; ++u)
+        if (r + u < r1) row(r + u, x[u]);
+}
+
+template <int D, int TYPE>
+cudaError_t launch_one(const HeadNormRopeArgs &a, dim3 grid, cudaStream_t st)
+{
+    return a.interleaved ? launch_pdl(head_norm_rope_kernel<D, TYPE, true>, grid, dim3(kThreads), 0, st, a)
+                         : launch_pdl(head_norm_rope_kernel<D, TYPE, false>, grid, dim3(kThreads), 0, st, a);
 }
 
 template <int D>
 cudaError_t launch_type(const HeadNormRopeArgs &a, int type, dim3 grid, cudaStream_t st)
 {
     switch (type) {
-    case ZQ_F16: return launch_pdl(head_norm_rope_kernel<D, ZQ_F16>, grid, dim3(kThreads), 0, st, a);
-    case ZQ_BF16: return launch_pdl(head_norm_rope_kernel<D, ZQ_BF16>, grid, dim3(kThreads), 0, st, a);
-    default: return launch_pdl(head_norm_rope_kernel<D, ZQ_E4M3>, grid, dim3(kThreads), 0, st, a);
+    case ZQ_F16: return launch_one<D, ZQ_F16>(a, grid, st);
+    case ZQ_BF16: return launch_one<D, ZQ_BF16>(a, grid, st);
+    default: return launch_one<D, ZQ_E4M3>(a, grid, st);
     }
 }
 
@@ -204,11 +213,12 @@ cudaError_t launch_head_norm_rope(const HeadNormRopeArgs &args, int D, int type,
 {
     HeadNormRopeArgs a = args;
     const long long rows = a.Hq + 2LL * a.Hk;
-    // Enough warps for every SM first (one row each, latency counts), then up
-    // to eight rows a warp, which share the warp's angles.
+    // Enough warps for every SM first (one row each, latency counts), then four
+    // to 16 rows a warp, which share the warp's angles.
     long long chunk = a.T * rows / ((long long)num_sms() * 32);
-    a.chunk = (int)(chunk < 1 ? 1 : chunk > 8 ? 8 : chunk);
-    a.chunks = (int)((rows + a.chunk - 1) / a.chunk);
+    chunk = chunk < kBatch ? (chunk < 1 ? 1 : chunk) : chunk > 16 ? 16 : chunk / kBatch * kBatch;
+    a.chunk = (int)chunk;
+    a.chunks = (int)((rows + chunk - 1) / chunk);
     const long long warps = (long long)a.T * a.chunks;
     const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
     switch (D) {

@@ -463,7 +463,7 @@ ZQ_API int zq_copy(void *dst, const void *src, size_t bytes, void *stream);
  * Paged key-value cache: `pages` pages of `page` tokens, for K and for V
  *   [pages][Hk][page][D]   of `type`, caller-owned device memory;
  * token slot s is row s % page of page s / page.  The value held is the
- * stored one times k_scale (v_scale); storing rounds x / scale once, e4m3
+ * stored one times k_scale (v_scale); storing rounds x * (1 / scale), e4m3
  * saturating at +-448 (NaN stays NaN), f16 overflowing to infinity.
  * Limits: page a power of two in 16..256, D 64, 128 or 256, 1 <= Hk <= 1024,
  * pages * page < 2^31 (offsets into the cache are 64-bit), scales positive
