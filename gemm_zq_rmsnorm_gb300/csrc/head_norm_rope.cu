@@ -116,30 +116,47 @@ __global__ void __launch_bounds__(kThreads) head_norm_rope_kernel(const __grid_c
         if (a.gamma_q) load_row(a.gamma_q + col, gq);
         if (a.gamma_k) load_row(a.gamma_k + col, gk);
     }
-    if (turned) {
+    if (qk && a.rot) {
         const int half = a.rot >> 1;
         const bool second = !INTER && col >= half;
-        if (!INTER) partner = second ? lane - half / E : lane + half / E;
+        if (!INTER && turned) partner = second ? lane - half / E : lane + half / E;
         // the positions are read beside the entries that choose between them
         const int at0 = a.pos[t];
         const int at1 = a.axes > 1 ? a.pos[(long long)a.T + t] : at0;
         const int at2 = a.axes > 2 ? a.pos[2LL * a.T + t] : at1;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-            if (INTER && (e & 1)) {   // the pair's first value has the angle already
-                cs[e] = cs[e - 1];
-                sn[e] = -sn[e - 1];
-                continue;
-            }
-            const uint64_t entry = a.table[INTER ? (col + e) >> 1 : col + e - (second ? half : 0)];
+        auto angle = [&](int pair, float &s, float &c) {
+            const uint64_t entry = a.table[pair];
             const int ax = (int)(entry & 3u);
             const int64_t at = ax == 0 ? at0 : ax == 1 ? at1 : at2;
             const uint64_t turns = (entry & ~(uint64_t)3) * (uint64_t)at;
             // top 32 bits as a signed fraction of a turn, times two: the argument in half turns
-            sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &sn[e], &cs[e]);
-            // the first of a pair takes -sin of its partner
-            if (!second) sn[e] = -sn[e];
+            sincospif((float)(int32_t)(turns >> 32) * 0x1p-31f, &s, &c);
+        };
+        auto pair_of = [&](int e) { return INTER ? (col + e) >> 1 : col + e - (second ? half : 0); };
+        if (a.rot <= 64) {   // at most one pair a lane: each angle once, passed on (an 8 times smaller share of
+                             // 256-wide rows with 64 turned values than an angle for every value)
+            float s, c;
+            angle(min(lane, half - 1), s, c);
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                sn[e] = __shfl_sync(0xffffffffu, s, pair_of(e) & 31);
+                cs[e] = __shfl_sync(0xffffffffu, c, pair_of(e) & 31);
+            }
+        } else if (turned) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                if (INTER && (e & 1)) {   // the pair's first value has the angle already
+                    cs[e] = cs[e - 1];
+                    sn[e] = sn[e - 1];
+                } else {
+                    angle(pair_of(e), sn[e], cs[e]);
+                }
+            }
         }
+        // the first of a pair takes -sin of its partner
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            if (INTER ? !(e & 1) : !second) sn[e] = -sn[e];
     }
     __syncwarp();
     const bool keep = slot >= 0 && slot < a.nslots;

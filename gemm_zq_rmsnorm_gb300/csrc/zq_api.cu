@@ -695,8 +695,9 @@ int check_cache(const zq_kv_cache *c, const char *name)
     if (c->Hk < 1 || c->Hk > 1024) return fail(ZQ_ERR_SHAPE, "%s: Hk = %d out of range", name, c->Hk);
     if (c->pages < 1 || (long long)c->pages * c->page > INT32_MAX)
         return fail(ZQ_ERR_SHAPE, "%s: %d pages of %d tokens out of range", name, c->pages, c->page);
-    if (!(c->k_scale > 0.0f) || !(c->v_scale > 0.0f) || !std::isfinite(c->k_scale) || !std::isfinite(c->v_scale))
-        return fail(ZQ_ERR_ARG, "%s: cache scales must be positive and finite", name);
+    for (float s : {c->k_scale, c->v_scale})
+        if (!(s > 0.0f) || !std::isfinite(s) || !std::isfinite(1.0f / s))
+            return fail(ZQ_ERR_ARG, "%s: cache scales and their inverses must be positive and finite", name);
     return ZQ_OK;
 }
 
@@ -740,7 +741,7 @@ int zq_head_norm_rope(const float *q, long long q_stride, const float *k, long l
     int st = check_cache(cache, name);
     if (st) return st;
     const int D = cache->D, Hk = cache->Hk;
-    if (T < 1 || Hq < 1 || (long long)T * (Hq + 2LL * Hk) > INT32_MAX)
+    if (T < 1 || Hq < 1 || Hq > 65536 || (long long)T * (Hq + 2LL * Hk) > INT32_MAX)
         return fail(ZQ_ERR_SHAPE, "%s: T = %d, Hq = %d out of range", name, T, Hq);
     if (rot < 0 || rot > D || rot % 16)
         return fail(ZQ_ERR_SHAPE, "%s: rot = %d must be a multiple of 16 in [0, %d]", name, rot, D);

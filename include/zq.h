@@ -466,8 +466,8 @@ ZQ_API int zq_copy(void *dst, const void *src, size_t bytes, void *stream);
  * stored one times k_scale (v_scale); storing rounds x * (1 / scale), e4m3
  * saturating at +-448 (NaN stays NaN), f16 overflowing to infinity.
  * Limits: page a power of two in 16..256, D 64, 128 or 256, 1 <= Hk <= 1024,
- * pages * page < 2^31 (offsets into the cache are 64-bit), scales positive
- * and finite.
+ * pages * page < 2^31 (offsets into the cache are 64-bit), scales and their
+ * inverses positive and finite.
  */
 enum { ZQ_F16 = 1, ZQ_BF16 = 2, ZQ_E4M3 = 3 };
 
@@ -504,7 +504,7 @@ ZQ_API int zq_rope_table(const double *inv_freq, const int *axis, int n, uint64_
  *       written.  Tokens of one call have slots of their own: when two share
  *       one, its contents are a mixture of the two;
  *   q_out : fp32, laid out as q with q_out_stride; may be q itself.
- * T >= 1, T * (Hq + 2 Hk) < 2^31, Hq >= 1.
+ * T >= 1, T * (Hq + 2 Hk) < 2^31, 1 <= Hq <= 65536.
  */
 ZQ_API int zq_head_norm_rope(const float *q, long long q_stride, const float *k, long long k_stride,
                              const float *v, long long v_stride, int T, int Hq, const float *gamma_q,

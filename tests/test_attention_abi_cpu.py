@@ -30,7 +30,7 @@ BAD_CACHES = [
     (dict(k=None), -1), (dict(v=None), -1), (dict(k=A8), -3), (dict(v=A8), -3), (dict(type=0), -1), (dict(type=4), -1),
     (dict(D=96), -2), (dict(D=0), -2), (dict(page=8), -2), (dict(page=48), -2), (dict(page=512), -2),
     (dict(page=0), -2), (dict(Hk=0), -2), (dict(Hk=1025), -2), (dict(pages=0), -2), (dict(pages=2 ** 31 - 1), -2),
-    (dict(ks=0.0), -1), (dict(vs=-1.0), -1), (dict(ks=math.nan), -1), (dict(vs=math.inf), -1)]
+    (dict(ks=0.0), -1), (dict(vs=-1.0), -1), (dict(ks=1e-39), -1), (dict(ks=math.nan), -1), (dict(vs=math.inf), -1)]
 
 
 @pytest.mark.parametrize("bad,status", BAD_CACHES)
@@ -42,7 +42,7 @@ def test_head_norm_rope_refuses_caches(lib, bad, status):
 @pytest.mark.parametrize("bad,status", [
     (dict(q=None), -1), (dict(q=A8), -3), (dict(qs=508), -2), (dict(qs=514), -2), (dict(k=None), -1),
     (dict(ks=252), -2), (dict(v=A8), -3), (dict(vs=0), -2), (dict(vs=-256), -2), (dict(T=0), -2), (dict(T=-1), -2),
-    (dict(T=2 ** 30), -2), (dict(Hq=0), -2), (dict(eps=-1.0), -1), (dict(eps=math.nan), -1), (dict(rot=8), -2),
+    (dict(T=2 ** 30), -2), (dict(Hq=0), -2), (dict(T=1, Hq=65537, qs=1 << 24, os=1 << 24), -2), (dict(eps=-1.0), -1), (dict(eps=math.nan), -1), (dict(rot=8), -2),
     (dict(rot=144), -2), (dict(rot=-16), -2), (dict(axes=0), -2), (dict(axes=4), -2), (dict(table=None), -1),
     (dict(pos=None), -1), (dict(slots=None), -1), (dict(gq=A8), -3), (dict(slots=A8), -3), (dict(out=None), -1),
     (dict(out=A8), -3), (dict(os=4), -2), (dict(out=A16, os=516), -1)])
