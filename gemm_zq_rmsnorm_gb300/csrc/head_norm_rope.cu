@@ -24,7 +24,7 @@ namespace zq {
 namespace {
 
 constexpr int kThreads = 128;   // four warps per CTA
-constexpr int kBatch = 4;       // rows whose loads are in flight together
+constexpr int kBatch = 2;       // rows of a warp in flight together (four cost 256-wide rows a third of their warps)
 
 template <int E>
 __device__ __forceinline__ void load_row(const float *p, float (&x)[E])
@@ -173,7 +173,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_rope_kernel(const __grid_c
         float y[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) y[e] = x[e];
-        if (r + kBatch < r1) load_row(src(r + kBatch), x);   // the row four further on takes its place
+        if (r + kBatch < r1) load_row(src(r + kBatch), x);   // the row kBatch further on takes its place
         if (r >= values) {
             if (keep) store_cache<TYPE, E>(vc + (r - values) * head, y, v_inverse);
             return;
@@ -233,7 +233,7 @@ cudaError_t launch_head_norm_rope(const HeadNormRopeArgs &args, int D, int type,
     // Enough warps for every SM first (one row each, latency counts), then four
     // to 16 rows a warp, which share the warp's angles.
     long long chunk = a.T * rows / ((long long)num_sms() * 32);
-    chunk = chunk < kBatch ? (chunk < 1 ? 1 : chunk) : chunk > 16 ? 16 : chunk / kBatch * kBatch;
+    chunk = chunk < 4 ? (chunk < 1 ? 1 : chunk) : chunk > 16 ? 16 : chunk / 4 * 4;
     a.chunk = (int)chunk;
     a.chunks = (int)((rows + chunk - 1) / chunk);
     const long long warps = (long long)a.T * a.chunks;

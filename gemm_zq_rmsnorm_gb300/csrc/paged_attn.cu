@@ -98,12 +98,6 @@ struct Meta {
     int a, b, seq, head, heads;
 };
 
-// Pieces of one row block in a CTA: the open ones of warps w0 .. w1 - 1 and,
-// when it ends here, the ending one of warp w1.
-struct Run {
-    int w0, w1, begins, ends, seq, head, heads;
-};
-
 __device__ __forceinline__ float ex2(float x)
 {
     float y;
@@ -333,8 +327,6 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     __shared__ int head_s[kWarps];             // an ending piece in the workspace
     __shared__ Meta open_s[kWarps];            // the warp's last piece (b = 1: begins in the warp, 2: before)
     __shared__ float m_s[kWarps][kHeads], l_s[kWarps][kHeads];
-    __shared__ Run runs_s[kWarps + 1];
-    __shared__ int nruns_s;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int vheads = a.passes * a.Hk;
@@ -344,59 +336,98 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         prefetch_tmap(&map_k);
         prefetch_tmap(&map_v);
     }
+    __syncwarp();   // a warp's barriers are its own
     pdl_wait();   // queries, cache, table and lengths come from earlier kernels
     pdl_launch_dependents();
 
-    // ---- the line: every row block is kBlockCost places and its tiles; planner t adds up sequences t * per ..
-    const int per = (a.B + kPlanners - 1) / kPlanners;
-    long long mine = 0, incl = 0;
-    if (tid < kPlanners) {
-        for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) {
-            const int len = seq_len(a, b);
-            mine += (long long)(seq_tiles(seq_first(a, len), len) + kBlockCost) * vheads;
+    // ---- the line: every row block is kBlockCost places and its tiles.  `total`
+    // places; the CTAs that take part share them, their warps one after the
+    // other: this warp's are [u0, u0 + left), from place `rem` of sequence `at.b` on
+    auto places = [&](int b) {
+        const int len = seq_len(a, b);
+        return (long long)(seq_tiles(seq_first(a, len), len) + kBlockCost) * vheads;
+    };
+    const long long gw = (long long)blockIdx.x * kWarps + warp;
+    Meta *meta = reinterpret_cast<Meta *>(a.meta);
+    long long total, u0 = 0, left = 0, rem = 0;
+    int ctas;
+    Walk at;
+    auto share = [&]() {   // false: this CTA takes no part
+        ctas = (int)min((long long)gridDim.x, max(1ll, total / (kWarps * kMinTiles)));
+        if (blockIdx.x >= ctas) return false;
+        const uint32_t nw = ctas * kWarps;
+        long long q, r;    // the first r warps have a place more
+        if (total >> 32) {
+            q = total / nw;
+            r = total - q * nw;
+        } else {
+            q = (uint32_t)total / nw;
+            r = (uint32_t)total - (uint32_t)q * nw;
         }
-        incl = mine;
+        u0 = gw * q + min(gw, r);
+        left = q + (gw < r ? 1 : 0);
+        return true;
+    };
+    if (a.B <= 32) {       // every warp by itself: lane b has sequence b
+        const long long mine = lane < a.B ? places(lane) : 0;
+        long long incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const long long up = __shfl_up_sync(kAll, incl, off);
             if (lane >= off) incl += up;
         }
-        if (lane == 31) total_s[warp] = incl;
-    }
-    __syncthreads();
-    long long total = 0, base = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanners / 32; ++w) {
-        if (w == warp) base = total;
-        total += total_s[w];
-    }
-    if (tid < kPlanners) before_s[tid] = base + incl - mine;
-    const int ctas = (int)min((long long)gridDim.x, max(1ll, total / (kWarps * kMinTiles)));
-    Meta *meta = reinterpret_cast<Meta *>(a.meta);
-    if (blockIdx.x >= ctas) {
-        if (tid == 0) meta[blockIdx.x] = Meta{0, 0, 0, 0, 0};
-        return;
-    }
-    __syncthreads();
-
-    // this warp's places [u0, u1); `left` counts them down, a tile at a time
-    const long long nw = (long long)ctas * kWarps, gw = (long long)blockIdx.x * kWarps + warp;
-    const long long u0 = gw * total / nw;
-    long long left = (gw + 1) * total / nw - u0;
-    Walk at;
-    if (left > 0) {
-        int i = 0;
-#pragma unroll
-        for (int step = kPlanners / 2; step >= 1; step >>= 1)
-            if ((i + step) * per < a.B && before_s[i + step] <= u0) i += step;
-        long long rem = u0 - before_s[i];
-        at.sequence(a, i * per);
-        while (rem >= (long long)(at.tend - at.t0 + kBlockCost) * vheads) {
-            rem -= (long long)(at.tend - at.t0 + kBlockCost) * vheads;
-            at.sequence(a, at.b + 1);
+        total = __shfl_sync(kAll, incl, 31);
+        if (!share()) {
+            if (tid == 0) meta[blockIdx.x] = Meta{0, 0, 0, 0, 0};
+            return;
         }
+        const int b = min(__popc(__ballot_sync(kAll, incl <= u0)), a.B - 1);
+        rem = u0 - __shfl_sync(kAll, incl - mine, b);
+        if (left > 0) at.sequence(a, b);
+    } else {               // planner t adds up sequences t * per ..
+        const int per = (a.B + kPlanners - 1) / kPlanners;
+        long long mine = 0, incl = 0;
+        if (tid < kPlanners) {
+            for (int b = tid * per; b < min(a.B, (tid + 1) * per); ++b) mine += places(b);
+            incl = mine;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const long long up = __shfl_up_sync(kAll, incl, off);
+                if (lane >= off) incl += up;
+            }
+            if (lane == 31) total_s[warp] = incl;
+        }
+        __syncthreads();
+        long long base = 0;
+        total = 0;
+#pragma unroll
+        for (int w = 0; w < kPlanners / 32; ++w) {
+            if (w == warp) base = total;
+            total += total_s[w];
+        }
+        if (tid < kPlanners) before_s[tid] = base + incl - mine;
+        if (!share()) {
+            if (tid == 0) meta[blockIdx.x] = Meta{0, 0, 0, 0, 0};
+            return;
+        }
+        __syncthreads();
+        if (left > 0) {
+            int i = 0;
+#pragma unroll
+            for (int step = kPlanners / 2; step >= 1; step >>= 1)
+                if ((i + step) * per < a.B && before_s[i + step] <= u0) i += step;
+            rem = u0 - before_s[i];
+            at.sequence(a, i * per);
+            while (rem >= (long long)(at.tend - at.t0 + kBlockCost) * vheads) {
+                rem -= (long long)(at.tend - at.t0 + kBlockCost) * vheads;
+                at.sequence(a, at.b + 1);
+            }
+        }
+    }
+    if (left > 0) {        // key head, pass and tile
         const int n = at.tend - at.t0 + kBlockCost;
-        const int vh = (int)(rem / n), r = (int)(rem - (long long)vh * n);
+        const int vh = rem >> 32 ? (int)(rem / n) : (int)((uint32_t)rem / (uint32_t)n);
+        const int r = (int)(rem - (long long)vh * n);
         at.kh = vh / a.passes;
         at.pass = vh - at.kh * a.passes;
         at.t = at.t0 + max(0, r - kBlockCost);
@@ -845,79 +876,97 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     }
     __syncthreads();
 
-    // ---- join the CTA's pieces: first the runs, then one warp for each head of a run
+    // ---- join the CTA's pieces, one warp for each head of a run: the open pieces of
+    // warps w0 .. w1 - 1 of one row block and, when it ends here, the ending one of
+    // warp w1.  Bits of a warp: an ending piece, an open one, one that begins in it.
+    const bool there = lane < kWarps;
+    const uint32_t ending = __ballot_sync(kAll, there && head_s[there ? lane : 0]);
+    const uint32_t opened = __ballot_sync(kAll, there && open_s[there ? lane : 0].b);
+    const uint32_t begun = __ballot_sync(kAll, there && open_s[there ? lane : 0].b == 1);
+    const int ends_here = __popc(ending);
+    // run r < ends_here ends with the r-th ending piece; after them there may be one that goes on
+    const uint32_t after = ending ? ~0u << (31 - __clz((int)ending)) : ~0u;
+    const int runs = ends_here + ((opened & after) != 0);
+    auto run_of = [&](int r, int &w0, int &w1, bool &begins) {
+        uint32_t e = ending, from = ~0u;
+        for (int i = 0; i < r; ++i) {
+            from = ~0u << (__ffs((int)e) - 1);
+            e &= e - 1;
+        }
+        w1 = e ? __ffs((int)e) - 1 : kWarps;
+        const uint32_t o = opened & from & ((1u << w1) - 1);
+        w0 = o ? __ffs((int)o) - 1 : w1;
+        begins = o && (begun >> w0 & 1);
+    };
     if (tid == 0) {
         Meta info{0, 0, 0, 0, 0};   // what this CTA leaves to the second kernel
-        int n = 0;
-        bool running = false;
-        Run run{};
-        for (int w = 0; w < kWarps; ++w) {
-            if (head_s[w]) {
-                if (!running) run = Run{w, w, 0, 1, 0, 0, kHeads};
-                run.w1 = w;
-                run.ends = 1;
-                if (!run.begins) info.a = 2;
-                runs_s[n++] = run;
-                running = false;
-            }
-            if (open_s[w].b && !running) {
-                running = true;
-                run = Run{w, kWarps, open_s[w].b == 1, 0, open_s[w].seq, open_s[w].head, open_s[w].heads};
-            }
+        int w0, w1;
+        bool begins;
+        if (runs) {
+            run_of(0, w0, w1, begins);
+            const int a_state = begins ? 0 : ends_here ? 2 : 1;
+            run_of(runs - 1, w0, w1, begins);
+            if (runs > ends_here && begins) info = open_s[w0];
+            info.a = a_state;
         }
-        if (running) {
-            runs_s[n++] = run;
-            if (run.begins) info.b = 1, info.seq = run.seq, info.head = run.head, info.heads = run.heads;
-            else info.a = 1;
-        }
-        nruns_s = n;
         meta[blockIdx.x] = info;
     }
-    __syncthreads();
-    for (int i = warp; i < nruns_s * kHeads; i += kWarps) {
-        const Run run = runs_s[i / kHeads];
+    for (int i = warp; i < runs * kHeads; i += kWarps) {
         const int h = i % kHeads;
-        if (h >= run.heads) continue;
-        const float *tail =
-            a.pieces + ((size_t)2 * gridDim.x + (size_t)blockIdx.x * kWarps + run.w1) * piece_floats(D);
-        float m = -INFINITY;
-        for (int w = run.w0; w < run.w1; ++w)   // a call of fewer tiles than warps leaves some without any
-            if (open_s[w].b) m = fmaxf(m, m_s[w][h]);
-        if (run.ends) m = fmaxf(m, tail[kHeads * D + h]);
-        const float u = m == -INFINITY ? 0.0f : m;
+        int w0, w1;
+        bool begins;
+        run_of(i / kHeads, w0, w1, begins);
+        const bool ends = i / kHeads < ends_here;
+        const Meta block = begins ? open_s[w0] : Meta{0, 0, 0, 0, kHeads};
+        if (h >= block.heads) continue;
+        // lane w has the maximum, the sum and then the weight of warp w's piece, lane 31 the ending one's
+        const float *tail = a.pieces + ((size_t)2 * gridDim.x + (size_t)blockIdx.x * kWarps + w1) * piece_floats(D);
+        const uint32_t pieces = opened & ((1u << w1) - 1) & (~0u << w0);   // (a call of few tiles leaves gaps)
+        float pm = -INFINITY, pl = 0.0f;
+        if (pieces >> lane & 1) {
+            pm = m_s[lane][h];
+            pl = l_s[lane][h];
+        } else if (ends && lane == 31) {
+            pm = tail[kHeads * D + h];
+            pl = tail[kHeads * D + kHeads + h];
+        }
+        float m = pm;
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
+        const float f = ex2(pm - (m == -INFINITY ? 0.0f : m));
+        const float l = warp_sum((pieces >> lane & 1) || (ends && lane == 31) ? f * pl : 0.0f);
 #pragma unroll
         for (int d0 = 0; d0 < D; d0 += 128) {
             const int d = d0 + 4 * lane;
             const bool in = d < D;
-            float l = 0.0f;
             float y[4] = {};
-            for (int w = run.w0; w < run.w1 + run.ends; ++w) {
-                const bool last = w == run.w1;
-                if (!last && !open_s[w].b) continue;
-                const float f = ex2((last ? tail[kHeads * D + h] : m_s[w][h]) - u);
-                l += f * (last ? tail[kHeads * D + kHeads + h] : l_s[w][h]);
-                if (in) {
-                    const float4 v = *reinterpret_cast<const float4 *>(
-                        (last ? tail : pieces_s + (size_t)w * kHeads * D) + h * D + d);
-                    y[0] += f * v.x;
-                    y[1] += f * v.y;
-                    y[2] += f * v.z;
-                    y[3] += f * v.w;
-                }
+            auto add = [&](const float *from, float f) {
+                const float4 v = *reinterpret_cast<const float4 *>(from + h * D + (in ? d : 0));
+                y[0] += f * v.x;
+                y[1] += f * v.y;
+                y[2] += f * v.z;
+                y[3] += f * v.w;
+            };
+#pragma unroll 4
+            for (int w = w0; w < w1; ++w) {
+                const float fw = __shfl_sync(kAll, f, w);
+                if (pieces >> w & 1) add(pieces_s + (size_t)w * kHeads * D, fw);
             }
-            if (run.begins && run.ends) {
-                const float f = row_factor(l, a.v_scale);
+            const float ft = __shfl_sync(kAll, f, 31);
+            if (ends) add(tail, ft);
+            if (begins && ends) {
+                const float g = row_factor(l, a.v_scale);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) y[e] *= f;
-                const int head = run.head + h;
+                for (int e = 0; e < 4; ++e) y[e] *= g;
+                const int head = block.head + h;
                 if (in && a.out)
-                    *reinterpret_cast<float4 *>(a.out + (long long)run.seq * a.out_stride + (long long)head * D + d) =
-                        make_float4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<float4 *>(a.out + (long long)block.seq * a.out_stride + (long long)head * D +
+                                                d) = make_float4(y[0], y[1], y[2], y[3]);
                 if (a.q8.qs)
-                    q8_block<4, 1, 2, 4>(a.q8, ((size_t)run.seq * a.Hq + head) * D + d, y, in, (d & 31) == 0);
-                if (d == 0 && a.lse) a.lse[(size_t)run.seq * a.Hq + head] = row_lse(m, l);
+                    q8_block<4, 1, 2, 4>(a.q8, ((size_t)block.seq * a.Hq + head) * D + d, y, in, (d & 31) == 0);
+                if (d == 0 && a.lse) a.lse[(size_t)block.seq * a.Hq + head] = row_lse(m, l);
             } else if (in) {
-                float *to = a.pieces + (size_t)(2 * blockIdx.x + (run.begins ? 1 : 0)) * piece_floats(D);
+                float *to = a.pieces + (size_t)(2 * blockIdx.x + (begins ? 1 : 0)) * piece_floats(D);
                 *reinterpret_cast<float4 *>(to + h * D + d) = make_float4(y[0], y[1], y[2], y[3]);
                 if (d == 0) {
                     to[kHeads * D + h] = m;
