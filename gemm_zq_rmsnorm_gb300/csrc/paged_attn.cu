@@ -661,7 +661,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                     float v = acc[C::kSplits - 1][e];
 #pragma unroll
                     for (int p = C::kSplits - 2; p >= 0; --p) v += acc[p][e];
-                    sc[h][e] = v * (e & 1 ? scale1 : scale0);
+                    sc[h][e] = v;
                 }
             }
             const int tok = (at.t + i) * kTile;
@@ -684,8 +684,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 x0 = fmaxf(x0, __shfl_xor_sync(kAll, x0, off));
                 x1 = fmaxf(x1, __shfl_xor_sync(kAll, x1, off));
             }
-            x0 = fmaxf(x0, m0);
-            x1 = fmaxf(x1, m1);
+            x0 = fmaxf(x0 * scale0, m0);   // the scales are positive
+            x1 = fmaxf(x1 * scale1, m1);
             // nothing seen yet: subtract 0, not the -infinity
             const float u0m = x0 == -INFINITY ? 0.0f : x0, u1m = x1 == -INFINITY ? 0.0f : x1;
             const float f0 = ex2(m0 - u0m), f1 = ex2(m1 - u1m);
@@ -696,8 +696,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             uint32_t bh[2][2], bl[2][2];   // weights of 16 tokens x 8 heads, both parts
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const float p0 = ex2(sc[h][0] - u0m), p1 = ex2(sc[h][1] - u1m);
-                const float p2 = ex2(sc[h][2] - u0m), p3 = ex2(sc[h][3] - u1m);
+                const float p0 = ex2(__fmaf_rn(sc[h][0], scale0, -u0m)), p1 = ex2(__fmaf_rn(sc[h][1], scale1, -u1m));
+                const float p2 = ex2(__fmaf_rn(sc[h][2], scale0, -u0m)), p3 = ex2(__fmaf_rn(sc[h][3], scale1, -u1m));
                 l0 += p0 + p2;
                 l1 += p1 + p3;
                 const uint32_t h0 = pack16<TYPE>(p0, p1), h1 = pack16<TYPE>(p2, p3);
@@ -729,13 +729,11 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                         for (int e = 0; e < 4; ++e) to[e] += y[e];
                     }
                 };
-                // rows 2c, 2c + 1, 2c + 8, 2c + 9 of the half are attended to
-                bool in[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
+                // row r of 2c, 2c + 1, 2c + 8, 2c + 9 of the half is attended to (asked only where some are not)
+                auto in = [&](int r) {
                     const int row = tok + kHalf * h + 2 * c + (r & 1) + 8 * (r >> 1);
-                    in[r] = whole || (ok[h] && row >= at.lo && row < at.len);
-                }
+                    return ok[h] && row >= at.lo && row < at.len;
+                };
                 if constexpr (TYPE == ZQ_E4M3) {
 #pragma unroll
                     for (int s = 0; s < C::kSegs; ++s) {
@@ -752,10 +750,12 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                                     src + swizzled<C::kSeg>(row, g >> 1) + 8 * (g & 1));
                                 w[r][0] = f.x, w[r][1] = f.y;
                             }
-                            if (!whole) {
+                        }
+                        if (!whole) {
 #pragma unroll
-                                for (int j = 0; j < C::kVBytes / 4; ++j) w[r][j] = in[r] ? w[r][j] : 0;
-                            }
+                            for (int r = 0; r < 4; ++r)
+#pragma unroll
+                                for (int j = 0; j < C::kVBytes / 4; ++j) w[r][j] = in(r) ? w[r][j] : 0;
                         }
 #pragma unroll
                         for (int j = 0; j < C::kVRun / 2; ++j) {
@@ -767,8 +767,11 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                         }
                     }
                 } else {
-                    const uint32_t keep0 = (in[0] ? 0xffffu : 0) | (in[1] ? 0xffff0000u : 0);
-                    const uint32_t keep1 = (in[2] ? 0xffffu : 0) | (in[3] ? 0xffff0000u : 0);
+                    uint32_t keep0 = ~0u, keep1 = ~0u;
+                    if (!whole) {
+                        keep0 = (in(0) ? 0xffffu : 0) | (in(1) ? 0xffff0000u : 0);
+                        keep1 = (in(2) ? 0xffffu : 0) | (in(3) ? 0xffff0000u : 0);
+                    }
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
                         uint32_t a0, a1, a2, a3;
