@@ -52,21 +52,22 @@
 namespace zq {
 namespace {
 
-constexpr int kMaxWarps = 16;
+constexpr int kMaxWarps = 12;
 constexpr int kPlanners = 256;  // threads that add up the line of tiles
 constexpr int kJoinThreads = 256;
 constexpr int kHalf = 16;       // tokens of an MMA
 constexpr int kTile = 32;       // tokens of a step: two MMAs' worth, so that a warp has independent chains
 constexpr int kHeads = 8;       // query heads of a pass: the MMA's columns
 constexpr int kMinTiles = 1;    // places of the line a warp takes at least, before more CTAs join in
-constexpr int kBlockCost = 3;   // what a row block costs besides its tiles, in tiles
+constexpr int kBlockCost = 1;   // what a row block costs besides its tiles, in tiles (with 6, 54 us for 49)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int D, int TYPE>
 struct Cfg {
-    // As many warps as the registers of their fragments allow (q and the output are D / 2 to D / 1.3 registers)
-    static constexpr int kWarps = D == 64 ? 16 : D == 128 ? 12 : 8;
+    // As many warps as the registers of their fragments allow (q and the output take D / 2 to D / 1.3 of a
+    // lane's); 16 at D = 64 spill and gain nothing (49.4 against 49.1 us, 200 windows of 1024)
+    static constexpr int kWarps = D <= 128 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBytes = KvBytes<TYPE>::value;
     static constexpr int kRow = D * kBytes;             // bytes of a token's head
