@@ -23,9 +23,9 @@
 // and add up in a fixed tree, the CTAs of a cluster add up their ranges in order
 // through distributed shared memory, the second kernel the clusters'.
 //
-// Second kernel: tokens are the rows, outputs the columns; h is two 16-bit parts
-// (binary16 after scaling the token's row to [1, 2), 2^-22 of its largest value;
-// bf16 2^-17).  The outputs are dealt to the MMAs' columns so that a lane holds
+// Second kernel: tokens are the rows, outputs the columns; h is three bf16 parts
+// (2^-24), or two binary16 ones after scaling the token's row to [1, 2) (2^-22 of
+// its largest value).  The outputs are dealt to the MMAs' columns so that a lane holds
 // four neighbouring ones of its tokens: base and y move as 16-byte pieces.
 #include "zq_async.cuh"
 #include "zq_cluster.cuh"
@@ -366,9 +366,10 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
 {
     constexpr int kSteps = R < 16 ? 1 : R / 16;
     constexpr int kRun = R < 32 ? R / 4 : 8;   // neighbouring values of R that a lane's fragment takes
-    constexpr int kUpGroups = R < 32 ? 16 : 8; // groups whose h is in shared memory at a time
+    constexpr int kHParts = TYPE == ZQ_BF16 ? 3 : 2;   // 16-bit parts of h
+    constexpr int kUpGroups = R < 32 ? 16 : R == 64 && TYPE == ZQ_BF16 ? 4 : 8;   // groups whose h is in shared memory
     __shared__ __align__(16) Tile tile;
-    __shared__ uint4 h_s[kUpGroups][kSteps][2][32];   // fragments of h: the upper parts, the lower ones
+    __shared__ uint4 h_s[kUpGroups][kSteps][kHParts][32];   // fragments of h, the upper parts first
     __shared__ float back_s[kUpGroups][kGroup];       // 2^e of a member's scaling
     __shared__ const float *from_s[kTokens];          // rows of base and y
     __shared__ float *to_s[kTokens];
@@ -452,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
             pdl_launch_dependents();
             waited = true;
         }
-        // h of the groups' members: its parts in order, times the adapter's scale, as two 16-bit parts in the
+        // h of the groups' members: its parts in order, times the adapter's scale, as 16-bit parts in the
         // fragments' order; R / 4 neighbouring threads have a member, four values each
         constexpr int kAhead = 4;
         const int items = n * kGroup * (R / 4);
@@ -499,21 +500,23 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                 }
                 if (r == 0) back_s[grp][row] = up;
                 const int s = R <= 16 ? 0 : 2 * (r / 32) + (r >> 2 & 1), l = row % 8 * 4;
-                uint32_t *hi_to = reinterpret_cast<uint32_t *>(h_s[grp][s][0]), *lo_to =
-                    reinterpret_cast<uint32_t *>(h_s[grp][s][1]);
 #pragma unroll
                 for (int j = 0; j < 2; ++j) {
-                    const uint32_t hi = kv_pack2<TYPE>(x[2 * j], x[2 * j + 1]);
-                    float2 y;
-                    if constexpr (TYPE == ZQ_BF16)
-                        y = make_float2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xffff0000u));
-                    else y = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-                    const uint32_t lo = kv_pack2<TYPE>(x[2 * j] - y.x, x[2 * j + 1] - y.y);
                     // register row / 8 (+ 2 for a step's upper eight) of the lane that has these values
                     const int at = R == 8 ? 4 * (l + r / 2 + j) + row / 8
                                           : 4 * (l + (R == 16 ? r / 4 : (r & 31) >> 3)) + row / 8 + 2 * j;
-                    hi_to[at] = hi;
-                    lo_to[at] = lo;
+                    float x0 = x[2 * j], x1 = x[2 * j + 1];
+#pragma unroll
+                    for (int p = 0; p < kHParts; ++p) {
+                        const uint32_t w = kv_pack2<TYPE>(x0, x1);
+                        reinterpret_cast<uint32_t *>(h_s[grp][s][p])[at] = w;
+                        float2 y;
+                        if constexpr (TYPE == ZQ_BF16)
+                            y = make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                        else y = __half22float2(*reinterpret_cast<const __half2 *>(&w));
+                        x0 -= y.x;
+                        x1 -= y.y;
+                    }
                 }
             }
         }
@@ -545,21 +548,25 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
             float y[2][2][4];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
-                const uint4 hi = h_s[here][s][0][lane], lo = h_s[here][s][1][lane];
+                // the lower parts first
 #pragma unroll
-                for (int p = 0; p < 2; ++p)
+                for (int part = kHParts - 1; part >= 0; --part) {
+                    const uint4 f = h_s[here][s][part][lane];
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t(&w)[2] = now.w[p][i][s];
-                        if constexpr (R == 8) {
-                            mma8_first<TYPE>(y[p][i], lo.x, lo.y, w[0]);
-                            mma8<TYPE>(y[p][i], hi.x, hi.y, w[0]);
-                        } else {
-                            if (s == 0) mma16_first<TYPE>(y[p][i], lo.x, lo.y, lo.z, lo.w, w[0], w[1]);
-                            else mma16<TYPE>(y[p][i], lo.x, lo.y, lo.z, lo.w, w[0], w[1]);
-                            mma16<TYPE>(y[p][i], hi.x, hi.y, hi.z, hi.w, w[0], w[1]);
+                    for (int p = 0; p < 2; ++p)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t(&w)[2] = now.w[p][i][s];
+                            const bool onto_zero = s == 0 && part == kHParts - 1;
+                            if constexpr (R == 8) {
+                                if (onto_zero) mma8_first<TYPE>(y[p][i], f.x, f.y, w[0]);
+                                else mma8<TYPE>(y[p][i], f.x, f.y, w[0]);
+                            } else {
+                                if (onto_zero) mma16_first<TYPE>(y[p][i], f.x, f.y, f.z, f.w, w[0], w[1]);
+                                else mma16<TYPE>(y[p][i], f.x, f.y, f.z, f.w, w[0], w[1]);
+                            }
                         }
-                    }
+                }
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {

@@ -39,8 +39,8 @@
 // Precision: q is split exactly into parts of the cache's 16-bit type (three
 // bf16 parts; two binary16 parts after scaling the row to [1, 2), 2^-22 of its
 // largest value), every product is exact, sums are fp32.  p in [0, 1] goes to
-// the value product as two parts (2^-17 relative in bf16, 2^-22 in binary16);
-// l sums the unrounded p.  e4m3 values are binary16 values.
+// the value product in as many parts (exact to 2^-24 in three of bf16, 2^-22 in two
+// of binary16; two of bf16, 2^-17, would be 2 to 3 % faster); l sums the unrounded p.  e4m3 values are binary16 values.
 #include <math.h>
 
 #include "zq_async.cuh"
@@ -81,7 +81,7 @@ struct Cfg {
     static constexpr int kRing = kWarps * kSlot * kSlots;
     static constexpr int kMerge = kWarps * kHeads * D * 4;   // the warps' open pieces, after the ring is done
     static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;   // aligned to the swizzle's 1024 bytes
-    static constexpr int kSplits = TYPE == ZQ_BF16 ? 3 : 2;  // parts of q
+    static constexpr int kSplits = TYPE == ZQ_BF16 ? 3 : 2;  // parts of q and of the weights
     static constexpr int kSeg = kRow < 128 ? kRow : 128;          // bytes of a segment of a row
     static constexpr int kSegs = kRow / kSeg;
     static constexpr int kKBytes = kSeg / 4;            // a lane's keys of a segment: two chunks, or one
@@ -694,19 +694,25 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
             m1 = x1;
             l0 *= f0;
             l1 *= f1;
-            uint32_t bh[2][2], bl[2][2];   // weights of 16 tokens x 8 heads, both parts
+            uint32_t bp[2][C::kSplits][2];   // weights of 16 tokens x 8 heads, their parts
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float p0 = ex2(__fmaf_rn(sc[h][0], scale0, -u0m)), p1 = ex2(__fmaf_rn(sc[h][1], scale1, -u1m));
                 const float p2 = ex2(__fmaf_rn(sc[h][2], scale0, -u0m)), p3 = ex2(__fmaf_rn(sc[h][3], scale1, -u1m));
                 l0 += p0 + p2;
                 l1 += p1 + p3;
-                const uint32_t h0 = pack16<TYPE>(p0, p1), h1 = pack16<TYPE>(p2, p3);
-                const float2 r0 = unpack16<TYPE>(h0), r1 = unpack16<TYPE>(h1);
-                bh[h][0] = transpose8(h0);
-                bh[h][1] = transpose8(h1);
-                bl[h][0] = transpose8(pack16<TYPE>(p0 - r0.x, p1 - r0.y));
-                bl[h][1] = transpose8(pack16<TYPE>(p2 - r1.x, p3 - r1.y));
+                float r[4] = {p0, p1, p2, p3};
+#pragma unroll
+                for (int p = 0; p < C::kSplits; ++p) {
+                    const uint32_t w0 = pack16<TYPE>(r[0], r[1]), w1 = pack16<TYPE>(r[2], r[3]);
+                    const float2 f0 = unpack16<TYPE>(w0), f1 = unpack16<TYPE>(w1);
+                    bp[h][p][0] = transpose8(w0);
+                    bp[h][p][1] = transpose8(w1);
+                    r[0] -= f0.x;
+                    r[1] -= f0.y;
+                    r[2] -= f1.x;
+                    r[3] -= f1.y;
+                }
             }
 
             // O^T [16 columns x 8 heads] += V^T p: rows g and g + 8 of a product are two neighbouring columns.
@@ -718,8 +724,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 const int from = slot * C::kSlot + (C::kItems == 2 ? 0 : h * half_stride);
                 auto product = [&](float(&to)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
                     float y[4];
-                    mma_first<TYPE>(y, a0, a1, a2, a3, bl[h][0], bl[h][1]);
-                    mma<TYPE>(y, a0, a1, a2, a3, bh[h][0], bh[h][1]);
+                    mma_first<TYPE>(y, a0, a1, a2, a3, bp[h][C::kSplits - 1][0], bp[h][C::kSplits - 1][1]);
+#pragma unroll
+                    for (int p = C::kSplits - 2; p >= 0; --p) mma<TYPE>(y, a0, a1, a2, a3, bp[h][p][0], bp[h][p][1]);
                     if (h == 0) {
                         to[0] = to[0] * f0 + y[0];
                         to[1] = to[1] * f1 + y[1];

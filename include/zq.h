@@ -569,8 +569,8 @@ ZQ_API int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, cons
  *   workspace : zq_lora_workspace_bytes(B, K, R) bytes, 16-byte aligned;
  *            contents do not matter.  Calls that may run at the same time need
  *            workspaces of their own.
- * Products are exact, sums fp32; A x is rounded only to two 16-bit parts (2^-22
- * of a token's largest value in f16, 2^-17 in bf16).  The result does not
+ * Products are exact, sums fp32; A x is rounded only to two f16 parts (2^-22 of
+ * a token's largest value) or three bf16 ones (2^-24).  The result does not
  * change from one call to the next, nor with the other tokens of the call's
  * batch beyond the number of tokens B.
  * Shapes: 1 <= B <= 65536, K % 32 == 0, 32 <= K <= 2^20, 1 <= N <= 2^22, R 8,

@@ -3,9 +3,10 @@
 Tolerance.  h = A x: the 32 products of a Q8_1 block are summed by two MMAs
 (each off by at most 2^-21 of its terms' magnitudes), the blocks by a chain of
 at most K/256 + 1 additions a warp, three levels of a tree and the splits (at
-most 34): e_h = (K/256 + 42) 2^-23 sum |A x|.  h to its two 16-bit parts: 2^-17
-|h| in bf16, 2^-22 of the token's largest |h| in f16.  The expansion sums R
-products in MMAs (2^-21 of their magnitudes each 16) and base in one rounding:
+most 34): e_h = (K/256 + 42) 2^-23 sum |A x|.  h to its 16-bit parts: 2^-24 |h|
+in three of bf16, 2^-22 of the token's largest |h| in two of f16.  The expansion sums R
+products in MMAs (2^-21 of their magnitudes each 16, once more for each lower
+part) and base in one rounding:
 |y - ref| <= |scale| sum |B| (e_h + part + (R/16 + 2) 2^-21 |h|) + 2^-23 |ref|."""
 import numpy as np
 import pytest
@@ -50,7 +51,7 @@ def check(y, a, A, Bm, scales, base, ids):
         h = x[t] @ Ai.T
         want[t] += s * (h @ Bi.T)
         e_h = (K / 256 + 42) * 2.0 ** -23 * (np.abs(x[t]) @ np.abs(Ai).T)
-        part = 2.0 ** -17 * np.abs(h) if A.dtype == BF16 else 2.0 ** -22 * np.abs(h).max(-1, keepdims=True)
+        part = 2.0 ** -24 * np.abs(h) if A.dtype == BF16 else 2.0 ** -22 * np.abs(h).max(-1, keepdims=True)
         tol[t] = abs(s) * ((e_h + part + (R / 16 + 2) * 2.0 ** -21 * np.abs(h)) @ np.abs(Bi).T)
     tol += 2.0 ** -23 * np.abs(want)
     off = np.abs(y - want)
