@@ -44,6 +44,7 @@ int fail(int status, const char *fmt, ...)
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+bool aligned4(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
 
 // Device check, once per device: the kernels are built for sm_103a only.
 int check_device(int *dev_out)
@@ -754,8 +755,9 @@ int zq_head_norm_rope(const float *q, long long q_stride, const float *k, long l
     if (q_out == q && q_out_stride != q_stride)
         return fail(ZQ_ERR_ARG, "%s: q_out in place needs q's stride", name);
     if (!slots || (rot && (!pos || !table))) return fail(ZQ_ERR_ARG, "%s: null slots, pos or table", name);
-    if (!aligned16(gamma_q) || !aligned16(gamma_k) || !aligned16(slots) || !aligned16(pos) || !aligned16(table))
-        return fail(ZQ_ERR_ALIGN, "%s: gamma, slots, pos and table must be 16-byte aligned", name);
+    if (!aligned16(gamma_q) || !aligned16(gamma_k) || (reinterpret_cast<uintptr_t>(table) & 7) ||
+        !aligned4(slots) || !aligned4(pos))
+        return fail(ZQ_ERR_ALIGN, "%s: gamma must be 16-byte, table 8-byte, slots and pos 4-byte aligned", name);
     int dev;
     if ((st = check_device(&dev))) return st;
     HeadNormRopeArgs a{};
@@ -815,8 +817,11 @@ int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, const zq_kv
     if (out == q) return fail(ZQ_ERR_ARG, "%s: out must not be q", name);
     if (q8_out && (st = check_q8(*q8_out, "zq_paged_attn (q8_out)"))) return st;
     if (!table || !lens) return fail(ZQ_ERR_ARG, "%s: null table or lens", name);
-    if (!aligned16(table) || !aligned16(lens) || !aligned16(lse))
-        return fail(ZQ_ERR_ALIGN, "%s: table, lens and lse must be 16-byte aligned", name);
+    if (!aligned4(table) || !aligned4(lens) || !aligned4(lse))
+        return fail(ZQ_ERR_ALIGN, "%s: table, lens and lse must be 4-byte aligned", name);
+    const float qk_scale = (float)((double)scale * cache->k_scale * 1.4426950408889634);
+    if (!(qk_scale > 0.0f) || !std::isfinite(qk_scale))
+        return fail(ZQ_ERR_ARG, "%s: scale times the cache's k_scale is out of range", name);
     int dev;
     if ((st = check_device(&dev))) return st;
     const size_t need = paged_attn_workspace(D);
@@ -838,7 +843,7 @@ int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, const zq_kv
     a.width = width;
     a.lens = lens;
     a.window = window;
-    a.qk_scale = (float)((double)scale * cache->k_scale * 1.4426950408889634);
+    a.qk_scale = qk_scale;
     a.v_scale = cache->v_scale;
     a.out = out;
     a.out_stride = out_stride;
@@ -865,11 +870,10 @@ int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const void *A, c
     if (n < 1 || n > 1 << 20 || N < 1 || N > 1 << 22)
         return fail(ZQ_ERR_SHAPE, "%s: n = %d or N = %d out of range", name, n, N);
     if (type != ZQ_F16 && type != ZQ_BF16) return fail(ZQ_ERR_ARG, "%s: type %d must be f16 or bf16", name, type);
-    if (!aligned16(a.qs) || !aligned16(a.d) || !aligned16(ids) || !aligned16(A) || !aligned16(Bm) ||
-        !aligned16(scales) || !aligned16(workspace))
-        return fail(ZQ_ERR_ALIGN, "%s: codes, ids, weights, scales and workspace must be 16-byte aligned", name);
-    if ((reinterpret_cast<uintptr_t>(y) | reinterpret_cast<uintptr_t>(base)) & 3)
-        return fail(ZQ_ERR_ALIGN, "%s: base and y must be 4-byte aligned", name);
+    if (!aligned16(a.qs) || !aligned16(a.d) || !aligned16(A) || !aligned16(Bm) || !aligned16(workspace))
+        return fail(ZQ_ERR_ALIGN, "%s: codes, weights and workspace must be 16-byte aligned", name);
+    if (!aligned4(ids) || !aligned4(scales) || !aligned4(y) || !aligned4(base))
+        return fail(ZQ_ERR_ALIGN, "%s: ids, scales, base and y must be 4-byte aligned", name);
     if (y_stride < N || y_stride > 1LL << 40 || (base && (base_stride < N || base_stride > 1LL << 40)))
         return fail(ZQ_ERR_SHAPE, "%s: strides must be at least N = %d", name, N);
     if (base == y && base_stride != y_stride) return fail(ZQ_ERR_ARG, "%s: base in place needs y's stride", name);

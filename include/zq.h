@@ -456,6 +456,9 @@ ZQ_API int zq_copy(void *dst, const void *src, size_t bytes, void *stream);
 
 /*
  * ------------------------------------------------ attention-side operators
+ * The int32 arrays of these calls (positions, slots, tables, lengths, ids), lse
+ * and scales need 4-byte alignment only, so a part of a batch's arrays serves.
+ *
  * What a step does between its q/k/v projections and its o projection
  * (MIInfer README, "Status": one launch for the heads' RMS norms; cached
  * single-query attention; Zynfer README: persistent per-layer K and V).

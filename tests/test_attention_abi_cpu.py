@@ -8,7 +8,7 @@ import pytest
 
 import gemm_zq_rmsnorm_gb300 as zq
 
-A16, A8 = 0x10000, 0x10008
+A16, A8, A2 = 0x10000, 0x10008, 0x10002
 
 
 @pytest.fixture(scope="module")
@@ -44,7 +44,7 @@ def test_head_norm_rope_refuses_caches(lib, bad, status):
     (dict(ks=252), -2), (dict(v=A8), -3), (dict(vs=0), -2), (dict(vs=-256), -2), (dict(T=0), -2), (dict(T=-1), -2),
     (dict(T=2 ** 30), -2), (dict(Hq=0), -2), (dict(T=1, Hq=65537, qs=1 << 24, os=1 << 24), -2), (dict(eps=-1.0), -1), (dict(eps=math.nan), -1), (dict(rot=8), -2),
     (dict(rot=144), -2), (dict(rot=-16), -2), (dict(axes=0), -2), (dict(axes=4), -2), (dict(table=None), -1),
-    (dict(pos=None), -1), (dict(slots=None), -1), (dict(gq=A8), -3), (dict(slots=A8), -3), (dict(out=None), -1),
+    (dict(pos=None), -1), (dict(slots=None), -1), (dict(gq=A8), -3), (dict(slots=A2), -3), (dict(pos=A2), -3), (dict(table=A2), -3), (dict(out=None), -1),
     (dict(out=A8), -3), (dict(os=4), -2), (dict(out=A16, os=516), -1)])
 def test_head_norm_rope_refuses(lib, bad, status):
     assert norm_rope(lib, **bad) == status
@@ -119,10 +119,10 @@ def test_paged_attn_refuses_caches(lib, bad, status):
 @pytest.mark.parametrize("bad,status", [
     (dict(q=None), -1), (dict(q=A8), -3), (dict(qs=500), -2), (dict(qs=513), -2), (dict(B=0), -2), (dict(B=65536), -2),
     (dict(Hq=0), -2), (dict(Hq=1), -2), (dict(Hq=5, qs=1024, os=1024), -2), (dict(Hq=130, qs=1 << 20, os=1 << 20), -2),
-    (dict(table=None), -1), (dict(table=A8), -3), (dict(width=0), -2), (dict(width=2 ** 31 - 1), -2),
-    (dict(lens=None), -1), (dict(lens=A8), -3), (dict(scale=0.0), -1), (dict(scale=-1.0), -1),
+    (dict(table=None), -1), (dict(table=A2), -3), (dict(width=0), -2), (dict(width=2 ** 31 - 1), -2),
+    (dict(lens=None), -1), (dict(lens=A2), -3), (dict(scale=3e38, c=cache(ks=100.0)), -1), (dict(scale=0.0), -1), (dict(scale=-1.0), -1),
     (dict(scale=math.inf), -1), (dict(scale=math.nan), -1), (dict(window=-1), -1), (dict(out=None), -1),
-    (dict(out=A8), -3), (dict(os=500), -2), (dict(out=A16), -1), (dict(lse=A8), -3),
+    (dict(out=A8), -3), (dict(os=500), -2), (dict(out=A16), -1), (dict(lse=A2), -3),
     (dict(q8=ctypes.byref(zq._Q8(A16, A8, A16))), -3), (dict(q8=ctypes.byref(zq._Q8(A16, None, A16))), -1)])
 def test_paged_attn_refuses(lib, bad, status):
     assert attn(lib, **bad) == status
@@ -153,9 +153,9 @@ def lora(lib, q8=None, B=3, K=256, ids=A16, n=2, A=A16, Bm=A16, R=16, type=1, sc
 @pytest.mark.parametrize("bad,status", [
     (dict(q8=zq._Q8(None, A16, A16)), -1), (dict(q8=zq._Q8(A8, A16, A16)), -3), (dict(q8=zq._Q8(A16, A8, A16)), -3),
     (dict(B=0), -2), (dict(B=65537), -2), (dict(K=0), -2), (dict(K=48), -2), (dict(K=(1 << 20) + 32), -2),
-    (dict(ids=None), -1), (dict(ids=A8), -3), (dict(n=0), -2), (dict(n=(1 << 20) + 1), -2), (dict(A=None), -1),
+    (dict(ids=None), -1), (dict(ids=A2), -3), (dict(n=0), -2), (dict(n=(1 << 20) + 1), -2), (dict(A=None), -1),
     (dict(A=A8), -3), (dict(Bm=None), -1), (dict(Bm=A8), -3), (dict(R=0), -2), (dict(R=24), -2), (dict(R=128), -2),
-    (dict(type=3), -1), (dict(type=0), -1), (dict(scales=A8), -3), (dict(N=0), -2), (dict(N=(1 << 22) + 1), -2),
+    (dict(type=3), -1), (dict(type=0), -1), (dict(scales=A2), -3), (dict(N=0), -2), (dict(N=(1 << 22) + 1), -2),
     (dict(base=A16 + 2), -3), (dict(bs=63), -2), (dict(y=None), -1), (dict(y=A16 + 2), -3), (dict(ys=63), -2),
     (dict(base=A16, y=A16, bs=64, ys=68), -1), (dict(ws=A8), -3)])
 def test_lora_refuses(lib, bad, status):

@@ -312,6 +312,26 @@ def test_two_graphs_with_their_own_workspaces_at_once():
         assert torch.equal(o, w)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, E4M3), (128, BF16)])
+def test_thousands_of_short_sequences(D, dtype):
+    """More sequences than threads plan them, empty ones among them."""
+    g = np.random.default_rng(5)
+    c = Case(5, [int(n) for n in g.choice([0, 1, 2, 17, 40], 2500)], 2, 1, D, dtype, 16)
+    c.check(*c.run())
+
+
+def test_parts_of_a_batchs_arrays():
+    """Table rows, lengths and lse of a part of a batch: addresses of any multiple of four bytes."""
+    c = Case(6, [5, 70, 33, 9], 4, 2, 128, F16, 16, extra_width=1)
+    want, want_lse = c.run()
+    lse = torch.full((5, 4), 3.0, device="cuda").view(-1)[1:9].view(2, 4)
+    out = zq.paged_attn(c.q[1:3], c.cache, c.table[1:3], c.t_lens[1:3], lse=lse)
+    torch.cuda.synchronize()
+    # the work is shared out anew, so pieces join in other places: the tests' tolerance, not equality
+    c.lens, c.q, c.table = c.lens[1:3], c.q[1:3], c.table[1:3]
+    c.check(out, lse)
+
+
 def test_lengths_beyond_the_table_and_below_zero():
     c = Case(41, [64, 64, 0], 4, 2, 64, F16, 16)
     c.t_lens.copy_(torch.tensor([2 ** 31 - 1, 64, -5], dtype=torch.int32))
