@@ -66,7 +66,7 @@ struct HeadNormRopeArgs {
 };
 cudaError_t launch_head_norm_rope(const HeadNormRopeArgs &a, int D, int type, cudaStream_t st);
 
-constexpr int kMaxAttnCtas = 512;   // more SMs than any GPU of this architecture has
+constexpr int kMaxAttnCtas = 256;   // more SMs than any GPU of this architecture has
 struct PagedAttnArgs {
     const float *q;
     long long q_stride;
