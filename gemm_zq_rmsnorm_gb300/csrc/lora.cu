@@ -5,7 +5,12 @@
 //
 // Two kernels, one after the other: h_t = A_a x_t split over K, then the
 // expansion of h by B_a onto base.  Bound: HBM, the adapters once, and base and
-// y (8 B N bytes), which dominate; a few tokens are launch bound.
+// y (8 B N bytes); a few tokens are launch bound.  Measured in a graph: one token,
+// 1024 -> 2048, 6.0 us; 56 tokens of 12 adapters, 5120 -> 17408, R = 16, bf16:
+// 11.5 us (16.7 MB: 2.5 us at the copy rate; two launches in a row and their chains of
+// dependent loads are the rest); 512 tokens of 4 adapters, 17408 -> 5120, R = 64,
+// f16: 33 us (42 MB, 6.2 us; the first kernel's half is 54 MB of 32- and 64-byte
+// pieces from L2, as each 32 tokens read their adapter again).
 //
 // Tokens come in tiles of 64.  A CTA sorts its tile's tokens by adapter itself
 // (64 ids: a scan of comparisons) and takes them sixteen at a time as the rows of
@@ -19,9 +24,9 @@
 // the 16-row operand they would have to be moved together from two loads), and
 // 8 codes of tokens g and g + 8.  Codes are whole numbers of at most 8 bits, exact
 // in binary16 and bf16: a Q8_1 block's products are summed by the tensor core and
-// scaled by the block's d in fp32.  Warps split the blocks of a CTA's K range
-// and add up in a fixed tree, the CTAs of a cluster add up their ranges in order
-// through distributed shared memory, the second kernel the clusters'.
+// scaled by the block's d in fp32.  The warps split the blocks of a CTA's K
+// range; their sums are added up in order, so are those of a cluster's CTAs,
+// through distributed shared memory, and by the second kernel the clusters'.
 //
 // Second kernel: tokens are the rows, outputs the columns; h is three bf16 parts
 // (2^-24), or two binary16 ones after scaling the token's row to [1, 2) (2^-22 of
@@ -31,6 +36,7 @@
 #include "zq_cluster.cuh"
 #include "zq_internal.cuh"
 #include "zq_kv.cuh"
+#include "zq_mma.cuh"
 
 namespace zq {
 namespace {
@@ -46,69 +52,6 @@ constexpr int kParts = 4;        // sums the second kernel is left with at most
 constexpr int kBlock = 32;       // outputs of a warp at a time
 constexpr int kNone = 255;
 constexpr unsigned kAll = 0xffffffffu;
-
-template <int TYPE>
-__device__ __forceinline__ void mma16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                      uint32_t b1)
-{
-    if constexpr (TYPE == ZQ_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The same onto zero
-template <int TYPE>
-__device__ __forceinline__ void mma16_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                            uint32_t b0, uint32_t b1)
-{
-    if constexpr (TYPE == ZQ_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%10,%10,%10,%10};"
-                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%10,%10,%10,%10};"
-                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-}
-
-// Onto zero with eight products a value
-template <int TYPE>
-__device__ __forceinline__ void mma8_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0)
-{
-    if constexpr (TYPE == ZQ_BF16)
-        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-                     "{%7,%7,%7,%7};"
-                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
-    else
-        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-                     "{%7,%7,%7,%7};"
-                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(b0), "f"(0.0f));
-}
-template <int TYPE>
-__device__ __forceinline__ void mma8(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0)
-{
-    if constexpr (TYPE == ZQ_BF16)
-        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(b0));
-    else
-        asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(b0));
-}
 
 // Four int8 codes to two pairs of the MMA's type, exactly: binary16 1024 + (q
 // + 128) has the byte in its low bits.

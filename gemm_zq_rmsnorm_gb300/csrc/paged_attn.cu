@@ -10,11 +10,20 @@
 // Bound: HBM, 2 D Hk es bytes per token against 4 D Hq operations.  With G =
 // Hq / Hk query heads on a key head the FP32 units would take G times the
 // products' time of one head (at G = 6 about the whole HBM time), so the
-// products run on the tensor cores through mma.sync: keys (16 tokens) are the
-// 16-row operand and the query heads the 8-column one, so G <= 8 heads cost
-// one pass.  (tcgen05 takes 64 or 128 rows from shared memory through a
-// descriptor and returns through tensor memory; at 8 columns the tensor pipe is
-// idle either way, and the warp-level form needs no hand-over between warps.)
+// products run on the tensor cores through mma.sync: 16 tokens are the 16-row
+// operand and the query heads the 8-column one, so G <= 8 heads cost one pass.
+// (tcgen05 takes 64 or 128 rows from shared memory through a descriptor and
+// returns through tensor memory; at 8 columns the tensor pipe is a third busy at
+// most, and the warp-level form needs no hand-over between warps.)
+// Measured, kernel pairs in a graph: 48 sequences of 1 to 12000 rows, 48 query
+// and 8 key heads of 128, bf16: 129 us, 5.8 TB/s (0.86 of the measured copy
+// rate); one sequence of 131071, 24 and 4 heads of 256, bf16: 95 us, 5.7 TB/s; 64
+// sequences of 8000 to 24000, e4m3: 285 us, 6.2 TB/s.  What is left of the 16-bit
+// cases is their end: the SMs of some GPCs get 10 % less of the bandwidth, and
+// the shares are equal.  200 windows of up to 1024 rows, 64-wide heads, e4m3: 49 us,
+// 2.9 TB/s, bound by the instructions of 4 KB tiles and of 1600 row blocks' ends.
+// One sequence of 1000: 11.5 us, a chain of latencies (lengths, table, keys, two
+// joins) over two launches.
 //
 // Work: every (sequence, key head) has ceil(len / 32) tiles of 32 tokens (at
 // least one, so that an empty row is written too); all tiles of the call form
@@ -26,26 +35,30 @@
 //
 // Loads: one lane of a warp copies the keys, or the values, of a tile (two
 // pages' halves when pages have 16 tokens; half a tile of 512-byte rows) by TMA
-// into the warp's own ring.  (With cp.async of 16 bytes a lane the same loop stopped at 4.4 TB/s
-// whatever the depth of the ring.)  The box is [segment of 128 bytes][token],
-// 128-byte swizzled, and the order of the head's columns in a K-step and of
-// the output rows is free: lane 4g + c reads 16-byte chunks 2c and 2c + 1 of
-// the key rows g and g + 8, and chunk g of the value rows 2c, 2c + 1, 2c + 8,
-// 2c + 9, which are fragments as they stand and fall on all banks.
+// into the warp's own ring, which needs no other warp.  (With cp.async of 16
+// bytes a lane the same loop stopped at 4.4 TB/s whatever the depth of the ring.)
+// The box is [segment of 128 bytes][token], 128-byte swizzled.  Fragments of 16-bit
+// rows come by ldmatrix, keys as they lie and values transposed; put together
+// from 16-byte loads they cost two register moves a product (141 us for 128).
+// 8-bit rows are loaded in 16-byte chunks (the order of the head's columns in a
+// K-step and of the output rows is free) and converted in pairs, the values' bytes
+// paired by token first; every access falls on all banks.
 // Rows past the end, before the window or on a page outside the cache never
 // meet a product: their scores are replaced by -infinity and their value words
 // by zeros, whatever the cache holds there (infinities, NaN).
 //
 // Precision: q is split exactly into parts of the cache's 16-bit type (three
 // bf16 parts; two binary16 parts after scaling the row to [1, 2), 2^-22 of its
-// largest value), every product is exact, sums are fp32.  p in [0, 1] goes to
-// the value product in as many parts (exact to 2^-24 in three of bf16, 2^-22 in two
-// of binary16; two of bf16, 2^-17, would be 2 to 3 % faster); l sums the unrounded p.  e4m3 values are binary16 values.
+// largest value), every product is exact, sums are fp32; e4m3 values are binary16
+// values.  p in [0, 1] goes to the value product in as many parts (exact to 2^-24
+// in three of bf16, 2^-22 in two of binary16; two of bf16, 2^-17, would be 2 to
+// 3 % faster); l sums the unrounded p.
 #include <math.h>
 
 #include "zq_async.cuh"
 #include "zq_internal.cuh"
 #include "zq_kv.cuh"
+#include "zq_mma.cuh"
 #include "zq_tc.cuh"
 #include "zq_tc_common.cuh"
 
@@ -104,39 +117,6 @@ __device__ __forceinline__ float ex2(float x)
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-
-template <int TYPE>
-__device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                    uint32_t b1)
-{
-    if constexpr (TYPE == ZQ_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%0,%1,%2,%3};"
-                     : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-
-// The same onto zero
-template <int TYPE>
-__device__ __forceinline__ void mma_first(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                          uint32_t b0, uint32_t b1)
-{
-    if constexpr (TYPE == ZQ_BF16)
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%10,%10,%10,%10};"
-                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
-    else
-        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-                     "{%10,%10,%10,%10};"
-                     : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-                     : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 
 // 8 x 8 transpose of 16-bit values across the warp
@@ -623,8 +603,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 auto product = [&](int k, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
                     for (int p = 0; p < C::kSplits; ++p) {
-                        if (k == 0) mma_first<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k][0], qf[p][k][1]);
-                        else mma<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k][0], qf[p][k][1]);
+                        if (k == 0) mma16_first<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k][0], qf[p][k][1]);
+                        else mma16<TYPE>(acc[p], a0, a1, a2, a3, qf[p][k][0], qf[p][k][1]);
                     }
                 };
                 if constexpr (TYPE == ZQ_E4M3) {
@@ -724,9 +704,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 const int from = slot * C::kSlot + (C::kItems == 2 ? 0 : h * half_stride);
                 auto product = [&](float(&to)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
                     float y[4];
-                    mma_first<TYPE>(y, a0, a1, a2, a3, bp[h][C::kSplits - 1][0], bp[h][C::kSplits - 1][1]);
+                    mma16_first<TYPE>(y, a0, a1, a2, a3, bp[h][C::kSplits - 1][0], bp[h][C::kSplits - 1][1]);
 #pragma unroll
-                    for (int p = C::kSplits - 2; p >= 0; --p) mma<TYPE>(y, a0, a1, a2, a3, bp[h][p][0], bp[h][p][1]);
+                    for (int p = C::kSplits - 2; p >= 0; --p) mma16<TYPE>(y, a0, a1, a2, a3, bp[h][p][0], bp[h][p][1]);
                     if (h == 0) {
                         to[0] = to[0] * f0 + y[0];
                         to[1] = to[1] * f1 + y[1];
