@@ -269,7 +269,7 @@ struct Walk {
     __device__ __forceinline__ void sequence(const PagedAttnArgs &a, int seq)
     {
         b = seq;
-        len = seq_len(a, seq);
+        len = __shfl_sync(kAll, seq_len(a, seq), 0);
         lo = seq_first(a, len);
         t0 = lo / kTile;
         tend = t0 + seq_tiles(lo, len);
@@ -309,7 +309,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     __shared__ Meta open_s[kWarps];            // the warp's last piece (b = 1: begins in the warp, 2: before)
     __shared__ float m_s[kWarps][kHeads], l_s[kWarps][kHeads];
 
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    // (a shuffle tells the compiler that the whole warp has the value: what follows from it is kept and
+    // computed once a warp, in uniform registers)
+    const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     const int vheads = a.passes * a.Hk;
     if (lane == 0) {
         for (int i = 0; i < C::kSlots; ++i) mbar_init(&full_s[warp][i], 1);
@@ -397,7 +399,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
 #pragma unroll
             for (int step = kPlanners / 2; step >= 1; step >>= 1)
                 if ((i + step) * per < a.B && before_s[i + step] <= u0) i += step;
-            rem = u0 - before_s[i];
+            i = __shfl_sync(kAll, i, 0);
+            rem = u0 - __shfl_sync(kAll, before_s[i], 0);
             at.sequence(a, i * per);
             while (rem >= (long long)(at.tend - at.t0 + kBlockCost) * vheads) {
                 rem -= (long long)(at.tend - at.t0 + kBlockCost) * vheads;
@@ -438,7 +441,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 for (int i = 0; i < 2; ++i) {   // a page holds both halves, or one each; the table ends at len
                     const int row = tok + kHalf * i, col = row >> a.page_shift;
                     pid[i] = row < ld.len ? a.table[(size_t)ld.b * a.width + col] : -1;
-                    pid[i] = (unsigned)pid[i] < (unsigned)a.pages ? pid[i] : -1;
+                    pid[i] = __shfl_sync(kAll, (unsigned)pid[i] < (unsigned)a.pages ? pid[i] : -1, 0);
                 }
                 if (a.box == kTile) pid[1] = pid[0];
             }
