@@ -94,7 +94,9 @@ __global__ void __launch_bounds__(kThreads) head_norm_rope_kernel(const __grid_c
     pdl_wait();   // q/k/v, positions and slots come from earlier kernels
     pdl_launch_dependents();
     const int lane = threadIdx.x & 31;
-    const int w = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+    // (a shuffle tells the compiler that the whole warp has the value: token, rows and addresses are then computed
+    // once a warp, in uniform registers)
+    const int w = blockIdx.x * (kThreads / 32) + __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);
     const int t = w / a.chunks;
     if (t >= a.T) return;
     const int keys = a.Hq, values = a.Hq + a.Hk, rows = a.Hq + 2 * a.Hk;   // rows: queries, keys, values
@@ -115,7 +117,7 @@ __global__ void __launch_bounds__(kThreads) head_norm_rope_kernel(const __grid_c
     float gq[E], gk[E], cs[E], sn[E];
     int partner = lane;
     const bool turned = qk && col < a.rot;
-    const int slot = a.slots[t];
+    const int slot = __shfl_sync(0xffffffffu, a.slots[t], 0);
     if (qk) {
         if (a.gamma_q) load_row(a.gamma_q + col, gq);
         if (a.gamma_k) load_row(a.gamma_k + col, gk);

@@ -178,7 +178,8 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
     __shared__ float part_s[kWarps][kCols][kQ][4][32];   // the warps' sums
     __shared__ float sum_s[kValues];                     // the CTA's
     __shared__ __align__(16) Tile tile;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    // (a shuffle tells the compiler that the whole warp has the value)
+    const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     pdl_wait();   // codes and ids come from earlier kernels
     pdl_launch_dependents();
     const int halves = a.R / RR, row0 = (int)blockIdx.x % halves * RR;
@@ -189,8 +190,9 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
     const int rank = blockIdx.z % a.cluster;
     float *h = a.h + (size_t)(blockIdx.z / a.cluster) * a.B * a.R + row0;
 
-    for (int u = blockIdx.y; u < tile.units; u += gridDim.y) {   // the same in all CTAs of the cluster
-        const int group0 = tile.unit[u], nq = tile.unit_groups[u], adapter = tile.adapter[group0];
+    for (int u = blockIdx.y, units = __shfl_sync(kAll, tile.units, 0); u < units; u += gridDim.y) {   // the same in all CTAs of the cluster
+        const int group0 = __shfl_sync(kAll, tile.unit[u], 0), nq = __shfl_sync(kAll, tile.unit_groups[u], 0);
+        const int adapter = __shfl_sync(kAll, tile.adapter[group0], 0);
         const int first = b0 + warp;               // this warp's blocks: first, first + kWarps, .. below b1
         const char *A[kCols];
         const int8_t *x[kQ][2];
@@ -316,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
     __shared__ float back_s[kUpGroups][kGroup];       // 2^e of a member's scaling
     __shared__ const float *from_s[kTokens];          // rows of base and y
     __shared__ float *to_s[kTokens];
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, c = lane & 3;
+    const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     const size_t tok0 = (size_t)blockIdx.x * kTokens;
     const int block0 = blockIdx.y * a.blocks, blocks = min(a.blocks, (a.N + kBlock - 1) / kBlock - block0);
     // The first kernel lets this one start only when all before it is complete:
@@ -336,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
     };
     auto fetch = [&](int group, int col0, bool weights, Task &f) {
         if (weights) {
-            const char *row0 = a.Bm + (size_t)tile.adapter[group] * a.N * R * 2 + kRun * 2 * c;
+            const char *row0 = a.Bm + (size_t)__shfl_sync(kAll, tile.adapter[group], 0) * a.N * R * 2 + kRun * 2 * c;
 #pragma unroll
             for (int p = 0; p < 2; ++p)
 #pragma unroll
@@ -383,8 +385,9 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
         }
     };
 
-    for (int g0 = 0; g0 < tile.groups; g0 += kUpGroups) {
-        const int n = min(kUpGroups, tile.groups - g0);
+    const int groups = __shfl_sync(kAll, tile.groups, 0);
+    for (int g0 = 0; g0 < groups; g0 += kUpGroups) {
+        const int n = min(kUpGroups, groups - g0);
         // this warp's tasks, block by block
         const int t0 = warp * blocks * n / kWarps, t1 = (warp + 1) * blocks * n / kWarps;
         int block = t0 / n, group = t0 - block * n;
@@ -467,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
         // One task, the one after it (the block's next group, or the next block's first) on its way.
         auto work = [&](bool more, const Task &now, Task &next) {
             const int here = group, col0 = col_of(block);
-            const int adapter = tile.adapter[g0 + group];
+            const int adapter = __shfl_sync(kAll, tile.adapter[g0 + group], 0);
             bool weights = false;
             if (++group == n) {
                 group = 0;
@@ -475,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                 weights = true;
             }
             if (more) {
-                weights |= tile.adapter[g0 + group] != adapter;
+                weights |= __shfl_sync(kAll, tile.adapter[g0 + group], 0) != adapter;
                 if (!weights) {
 #pragma unroll
                     for (int p = 0; p < 2; ++p)
