@@ -16,8 +16,8 @@
 //
 // HBM bound for long prompts: 4 D (2 Hq + 2 Hk) + 2 es D Hk bytes per token;
 // launch bound for a few tokens.  Measured in a graph: 4096 tokens of 48 + 8 + 8
-// heads of 128 to an f16 cache 47.6 us, 5.3 TB/s (0.78 of the measured copy rate);
-// 777 tokens of 24 + 4 + 4 heads of 256 to an e4m3 cache 14.3 us, 3.2 TB/s (two
+// heads of 128 to an f16 cache 43.0 us, 5.9 TB/s (0.86 of the measured copy rate);
+// 777 tokens of 24 + 4 + 4 heads of 256 to an e4m3 cache 12.5 us, 3.7 TB/s (two
 // rounds of warps, whose 8 values a lane make the instructions count); 61 tokens
 // 4.0 us, one token 2.5 us.
 #include "zq_async.cuh"

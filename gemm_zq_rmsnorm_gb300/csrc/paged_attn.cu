@@ -18,11 +18,11 @@
 // Measured, kernel pairs in a graph: 48 sequences of 1 to 12000 rows, 48 query
 // and 8 key heads of 128, bf16: 129 us, 5.8 TB/s (0.86 of the measured copy
 // rate); one sequence of 131071, 24 and 4 heads of 256, bf16: 95 us, 5.7 TB/s; 64
-// sequences of 8000 to 24000, e4m3: 285 us, 6.2 TB/s.  What is left of the 16-bit
+// sequences of 8000 to 24000, e4m3: 278 us, 6.3 TB/s.  What is left of the 16-bit
 // cases is their end: the SMs of some GPCs get 10 % less of the bandwidth, and
-// the shares are equal.  200 windows of up to 1024 rows, 64-wide heads, e4m3: 49 us,
-// 2.9 TB/s, bound by the instructions of 4 KB tiles and of 1600 row blocks' ends.
-// One sequence of 1000: 11.5 us, a chain of latencies (lengths, table, keys, two
+// the shares are equal.  200 windows of up to 1024 rows, 64-wide heads, e4m3: 44 us,
+// 3.2 TB/s, bound by the instructions of 4 KB tiles and of 1600 row blocks' ends.
+// One sequence of 1000: 10 us, a chain of latencies (lengths, table, keys, two
 // joins) over two launches.
 //
 // Work: every (sequence, key head) has ceil(len / 32) tiles of 32 tokens (at
@@ -65,22 +65,22 @@
 namespace zq {
 namespace {
 
-constexpr int kMaxWarps = 12;
+constexpr int kMaxWarps = 16;
 constexpr int kPlanners = 256;  // threads that add up the line of tiles
 constexpr int kJoinThreads = 256;
 constexpr int kHalf = 16;       // tokens of an MMA
 constexpr int kTile = 32;       // tokens of a step: two MMAs' worth, so that a warp has independent chains
 constexpr int kHeads = 8;       // query heads of a pass: the MMA's columns
 constexpr int kMinTiles = 1;    // places of the line a warp takes at least, before more CTAs join in
-constexpr int kBlockCost = 1;   // what a row block costs besides its tiles, in tiles (with 6, 54 us for 49)
+constexpr int kBlockCost = 1;   // what a row block costs besides its tiles, in tiles (with 6, those windows took 10 % longer)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kAll = 0xffffffffu;
 
 template <int D, int TYPE>
 struct Cfg {
     // As many warps as the registers of their fragments allow (q and the output take D / 2 to D / 1.3 of a
-    // lane's); 16 at D = 64 spill and gain nothing (49.4 against 49.1 us, 200 windows of 1024)
-    static constexpr int kWarps = D <= 128 ? 12 : 8;
+    // lane's): 200 windows of 1024 at D = 64 took 45.8 us with 12, 43.9 with 16
+    static constexpr int kWarps = D == 64 ? 16 : D <= 128 ? 12 : 8;
     static constexpr int kThreads = 32 * kWarps;
     static constexpr int kBytes = KvBytes<TYPE>::value;
     static constexpr int kRow = D * kBytes;             // bytes of a token's head
