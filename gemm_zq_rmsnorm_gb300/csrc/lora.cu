@@ -597,6 +597,11 @@ cudaError_t launch_type(const LoraArgs &a, dim3 down, dim3 up, cudaStream_t st)
 // and up to four clusters where K is long and the tiles leave SMs idle.
 struct Cut {
     int tiles, cluster, parts, per_split;
+    void set(int K, int p)
+    {
+        parts = p;
+        per_split = (K / 32 + cluster * parts - 1) / (cluster * parts);
+    }
 };
 Cut cut_k(int B, int K, int R)
 {
@@ -605,8 +610,9 @@ Cut cut_k(int B, int K, int R)
     Cut c{(B + kTokens - 1) / kTokens, 1, 1, 0};
     while (c.cluster < kCluster && c.cluster < wanted) c.cluster *= 2;
     const int room = 2 * num_sms() / ((B + kGroup * kQ - 1) / (kGroup * kQ) * halves * kCluster);
-    while (c.parts < kParts && c.parts * 2 * kCluster <= wanted && c.parts * 2 <= room) c.parts *= 2;
-    c.per_split = (blocks + c.cluster * c.parts - 1) / (c.cluster * c.parts);
+    int parts = 1;
+    while (parts < kParts && parts * 2 * kCluster <= wanted && parts * 2 <= room) parts *= 2;
+    c.set(K, parts);
     return c;
 }
 
@@ -617,17 +623,23 @@ size_t lora_workspace(int B, int K, int R) { return (size_t)cut_k(B, K, R).parts
 cudaError_t launch_lora(const LoraArgs &args, int type, cudaStream_t st)
 {
     LoraArgs a = args;
-    const Cut cut = cut_k(a.B, a.K, a.R);
+    const int halves = a.R > kDownRows ? a.R / kDownRows : 1;
+    // units that a tile can have
+    const int most = min(a.n, min(a.B, kTokens)) + (a.B > kGroup * kQ ? 1 : 0);
+    Cut cut = cut_k(a.B, a.K, a.R);
+    auto taken = [&] { return (long long)cut.tiles * halves * cut.cluster * cut.parts; };   // CTAs of a unit, over all tiles
+    // no more parts of K than leave an SM to each CTA with all units taken at the same time (17408
+    // wide, 16 tokens of 4 adapters of R = 64: 10.9 us, 14.5 with four parts; 56 tokens of 12 of R = 16:
+    // 10.8, 15.6)
+    while (cut.parts > 1 && taken() * most > num_sms()) cut.set(a.K, cut.parts / 2);
     a.cluster = cut.cluster;
     a.parts = cut.parts;
     a.per_split = cut.per_split;
-    const int splits = cut.cluster * cut.parts, halves = a.R > kDownRows ? a.R / kDownRows : 1;
     // units of a tile taken at the same time: as many as there can be, in a grid
     // that the GPU holds at once (a CTA takes the others in turn: starting one
     // costs more than two blocks' worth of its work)
-    const int most = min(a.n, min(a.B, kTokens)) + (a.B > kGroup * kQ ? 1 : 0);
-    const long long room = 2LL * num_sms() / ((long long)cut.tiles * halves * splits);
-    const dim3 down(cut.tiles * halves, (unsigned)(room < 1 ? 1 : room > most ? most : room), splits);
+    const long long room = 2LL * num_sms() / taken();
+    const dim3 down(cut.tiles * halves, (unsigned)(room < 1 ? 1 : room > most ? most : room), cut.cluster * cut.parts);
     // column blocks of a CTA of the second kernel: as many CTAs as the GPU holds
     // at once (one an SM at R = 64, else two), each of which prepares its tile's
     // h once (512 tokens at R = 64: 33.6 us, 37.0 with two an SM; 56 tokens at
