@@ -193,10 +193,11 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
     for (int u = blockIdx.y, units = __shfl_sync(kAll, tile.units, 0); u < units; u += gridDim.y) {   // the same in all CTAs of the cluster
         const int group0 = __shfl_sync(kAll, tile.unit[u], 0), nq = __shfl_sync(kAll, tile.unit_groups[u], 0);
         const int adapter = __shfl_sync(kAll, tile.adapter[group0], 0);
-        const int first = b0 + warp;               // this warp's blocks: first, first + kWarps, .. below b1
+        const int chunk = (b1 - b0 + kWarps - 1) / kWarps, first = b0 + warp * chunk;
+        const int last = min(b1, first + chunk);   // this warp's blocks: first .. last - 1
         const char *A[kCols];
         const int8_t *x[kQ][2];
-        const uint16_t *d[kQ][2];
+        const uint16_t *d[kQ][2];          // of block first + c
 #pragma unroll
         for (int r = 0; r < kCols; ++r)
             A[r] = a.A + (((size_t)adapter * a.R + row0 + 8 * r + g) * a.K + 32 * (size_t)first + 8 * c) * 2;
@@ -207,20 +208,19 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
                 const int of = q < nq ? tile.token(group0 + q, g + 8 * e) : kNone;
                 const size_t t = tok0 + (of == kNone ? tile.token(group0, 0) : of);
                 x[q][e] = a.qs + t * a.K + 32 * (size_t)first + 8 * c;
-                d[q][e] = a.d + t * blocks + first;
+                d[q][e] = a.d + t * blocks + first + c;
             }
         float sum[kCols][kQ][4] = {};
         // the next block's values are on their way while this one's are used
         struct Block {
             uint4 w[kCols];
             uint2 codes[kQ][2];
-            uint16_t d[kQ][2];
         };
         auto fetch = [&](Block &f) {   // and on to the block after it
 #pragma unroll
             for (int r = 0; r < kCols; ++r) {
                 f.w[r] = __ldg(reinterpret_cast<const uint4 *>(A[r]));
-                A[r] += 64 * kWarps;
+                A[r] += 64;
             }
 #pragma unroll
             for (int q = 0; q < kQ; ++q)
@@ -228,16 +228,29 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         f.codes[q][e] = __ldg(reinterpret_cast<const uint2 *>(x[q][e]));
-                        f.d[q][e] = __ldg(d[q][e]);
-                        x[q][e] += 32 * kWarps;
-                        d[q][e] += kWarps;
+                        x[q][e] += 32;
                     }
         };
-        auto use = [&](const Block &f) {
+        // the d of four blocks, one a lane of the four that share a token: a load of its own for each
+        // block is a third of the L1's work (the call: 200 tokens, 5120 -> 17408, R = 16, 27.1 -> 25.5 us;
+        // 512 tokens, R = 64, 33.3 -> 33.0)
+        uint32_t dn[kQ][2], dv[kQ][2];
+        auto fetch_d = [&](int b) {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q)
+                if (q < nq)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        dn[q][e] = b + c < last ? __ldg(d[q][e]) : 0;
+                        d[q][e] += 4;
+                    }
+        };
+        auto use = [&](const Block &f, int j) {
 #pragma unroll
             for (int q = 0; q < kQ; ++q) {
                 if (q >= nq) break;
-                const float d0 = h2f(f.d[q][0]), d1 = h2f(f.d[q][1]);
+                const float d0 = h2f((uint16_t)__shfl_sync(kAll, dv[q][0], (lane & ~3) + j));
+                const float d1 = h2f((uint16_t)__shfl_sync(kAll, dv[q][1], (lane & ~3) + j));
                 uint32_t k[2][4];
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -257,12 +270,22 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
             }
         };
         Block even, odd;
-        if (first < b1) fetch(even);
-        for (int b = first; b < b1; b += 2 * kWarps) {
-            if (b + kWarps < b1) fetch(odd);
-            use(even);
-            if (b + 2 * kWarps < b1) fetch(even);
-            if (b + kWarps < b1) use(odd);
+        if (first < last) {
+            fetch_d(first);
+            fetch(even);
+        }
+        for (int b = first; b < last; b += 4) {
+#pragma unroll
+            for (int q = 0; q < kQ; ++q)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) dv[q][e] = dn[q][e];
+            if (b + 4 < last) fetch_d(b + 4);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if (b + j >= last) break;
+                if (b + j + 1 < last) fetch(j & 1 ? even : odd);
+                use(j & 1 ? odd : even, j);
+            }
         }
         // the warps' sums, in order
 #pragma unroll
@@ -629,8 +652,8 @@ cudaError_t launch_lora(const LoraArgs &args, int type, cudaStream_t st)
     Cut cut = cut_k(a.B, a.K, a.R);
     auto taken = [&] { return (long long)cut.tiles * halves * cut.cluster * cut.parts; };   // CTAs of a unit, over all tiles
     // no more parts of K than leave an SM to each CTA with all units taken at the same time (17408
-    // wide, 16 tokens of 4 adapters of R = 64: 10.9 us, 14.5 with four parts; 56 tokens of 12 of R = 16:
-    // 10.8, 15.6)
+    // wide, 16 tokens of 4 adapters of R = 64: 11.1 us, 14.5 with four parts; 56 tokens of 12 of R = 16:
+    // 10.7, 15.6)
     while (cut.parts > 1 && taken() * most > num_sms()) cut.set(a.K, cut.parts / 2);
     a.cluster = cut.cluster;
     a.parts = cut.parts;
