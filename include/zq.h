@@ -575,7 +575,7 @@ ZQ_API int zq_paged_attn(const float *q, long long q_stride, int B, int Hq, cons
  * Products are exact, sums fp32; A x is rounded only to two f16 parts (2^-22 of
  * a token's largest value) or three bf16 ones (2^-24).  The result does not
  * change from one call to the next, nor with the other tokens of the call's
- * batch beyond the number of tokens B.
+ * batch beyond their number B (it may with n).
  * Shapes: 1 <= B <= 65536, K % 32 == 0, 32 <= K <= 2^20, 1 <= N <= 2^22, R 8,
  * 16, 32 or 64, 1 <= n <= 2^20; strides >= N.
  */

@@ -141,3 +141,24 @@ def test_steps_eager_and_captured(B, dtype):
         torch.cuda.synchronize()
         layer.check(at)
     assert zq.device_status() == 0
+
+
+def test_tensors_off_the_current_device_are_refused(monkeypatch):
+    """A call launches on the current device: tensors of another one are refused before anything runs."""
+    layer = Layer(1, torch.float16)
+    layer.give(0)
+    layer.step()
+    torch.cuda.synchronize()
+    was = layer.k.view(torch.int16).clone(), layer.q.clone(), layer.y.clone()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    q = layer.qkv[:, :HQ * D]
+    for call in (lambda: zq.head_norm_rope(q, layer.qkv[:, HQ * D:-HK * D], layer.qkv[:, -HK * D:], layer.gq, layer.gk,
+                                           1e-6, layer.rope, layer.pos, layer.cache, layer.slots, q_out=layer.q),
+                 lambda: zq.paged_attn(layer.q, layer.cache, layer.table, layer.lens, out=layer.o),
+                 lambda: zq.lora(layer.q8o, layer.ids, *layer.lora_o, layer.scales, base=layer.y0, y=layer.y)):
+        with pytest.raises(ValueError, match="current device"):
+            call()
+    monkeypatch.undo()
+    torch.cuda.synchronize()
+    for now, then in zip((layer.k.view(torch.int16), layer.q, layer.y), was):
+        assert torch.equal(now, then)

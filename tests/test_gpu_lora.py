@@ -121,6 +121,13 @@ def test_extreme_values():
     check(zq.lora(a, ids, A, Bm, scales, base=base), a, A, Bm, scales, base, ids)
 
 
+@pytest.mark.parametrize("B,n,R", [(3, 2, 16), (56, 1, 16), (56, 12, 16), (17, 4, 64), (40, 3, 64)])
+def test_long_rows_are_cut_by_the_units_of_a_tile(B, n, R):
+    """17408-wide rows: four, two or one sums of parts of K, as the tile's tokens and adapters fill the GPU."""
+    a, A, Bm, scales, base, ids = make(B, B, 17408, 160, R, n, F16, [i % (n + 1) - 1 for i in range(B)])
+    check(zq.lora(a, ids, A, Bm, scales, base=base), a, A, Bm, scales, base, ids)
+
+
 def test_large_batch_of_runs():
     B, K, N, R = 2500, 256, 128, 16
     ids = np.repeat(np.arange(7) - 1, 400)[:B]
