@@ -49,8 +49,11 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kDownRows = 32;    // rows of A a CTA of the first kernel takes at most
 constexpr int kCluster = 8;      // CTAs of a cluster at most, which add up their K ranges
 constexpr int kParts = 4;        // sums the second kernel is left with at most
-constexpr int kBlock = 32;       // outputs of a warp at a time
+// outputs that a warp of the second kernel works on at a time, in 16 (at R = 64 registers allow two an SM
+// with one: 512 tokens 25.2 us the call, 33.0 with two and half the warps)
+__host__ __device__ constexpr int up_pieces(int R) { return R == 64 ? 1 : 2; }
 constexpr int kNone = 255;
+constexpr int kLong = 6;         // tasks of a warp of the second kernel from which on it asks L2 for those ahead
 constexpr unsigned kAll = 0xffffffffu;
 
 // Four int8 codes to two pairs of the MMA's type, exactly: binary16 1024 + (q
@@ -72,6 +75,8 @@ __device__ __forceinline__ void codes4(uint32_t w, uint32_t &lo, uint32_t &hi)
         hi = kv_pack2<ZQ_BF16>(f1.x, f1.y);
     }
 }
+
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 
 // A tile's tokens by adapter: each adapter's tokens in groups of sixteen (an
 // MMA's rows), its groups in units of up to two.
@@ -330,9 +335,10 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
 // four outputs move at once (values alone cost the 17408-wide decode batch half
 // as much again).
 template <int R, int TYPE, bool VEC>
-__global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(const __grid_constant__ LoraArgs a)
+__global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_constant__ LoraArgs a)
 {
     constexpr int kSteps = R < 16 ? 1 : R / 16;
+    constexpr int kP = up_pieces(R), kBlock = 16 * kP;
     constexpr int kRun = R < 32 ? R / 4 : 8;   // neighbouring values of R that a lane's fragment takes
     constexpr int kHParts = TYPE == ZQ_BF16 ? 3 : 2;   // 16-bit parts of h
     constexpr int kUpGroups = R < 32 ? 16 : R == 64 && TYPE == ZQ_BF16 ? 4 : 8;   // groups whose h is in shared memory
@@ -356,14 +362,14 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
     // The columns of MMA (p, i) are outputs 16 p + 4 (col / 2) + 2 i + col % 2 of
     // the block, so that lane 4g + c ends with outputs 16 p + 4c .. 4c + 3.
     struct Task {
-        uint32_t w[2][2][kSteps][2];
-        float4 v[2][2];             // base of rows g, g + 8
+        uint32_t w[kP][2][kSteps][2];
+        float4 v[2][kP];            // base of rows g, g + 8
     };
     auto fetch = [&](int group, int col0, bool weights, Task &f) {
         if (weights) {
             const char *row0 = a.Bm + (size_t)__shfl_sync(kAll, tile.adapter[group], 0) * a.N * R * 2 + kRun * 2 * c;
 #pragma unroll
-            for (int p = 0; p < 2; ++p)
+            for (int p = 0; p < kP; ++p)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const int n = col0 + 16 * p + 4 * (g >> 1) + 2 * i + (g & 1);
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
             const int t = tile.token(group, g + 8 * e);
             const float *from = from_s[t == kNone ? tile.token(group, 0) : t];
 #pragma unroll
-            for (int p = 0; p < 2; ++p) {
+            for (int p = 0; p < kP; ++p) {
                 const int n = col0 + 16 * p + 4 * c;
                 if (!a.base) {
                     f.v[e][p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -415,6 +421,31 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
         const int t0 = warp * blocks * n / kWarps, t1 = (warp + 1) * blocks * n / kWarps;
         int block = t0 / n, group = t0 - block * n;
         auto col_of = [&](int block) { return (block0 + block) * kBlock; };
+        // The lines of the task after the next to L2, base's rows and a new block's weights: a warp with
+        // many tasks waits for HBM at each (4096 tokens, R = 16: 140.8 us the call, 125.7 so; 512: 24.9,
+        // 22.6), one with few loses more on the way (512 tokens, R = 64, 4 or 5 tasks: 25.2, 26.5)
+        int far = t1 - t0 < kLong ? t1 : t0, far_block = block, far_group = group;
+        auto step_far = [&]() {
+            ++far;
+            if (++far_group == n) {
+                far_group = 0;
+                ++far_block;
+            }
+        };
+        auto ahead = [&]() {
+            if (far >= t1) return;
+            const int t = tile.token(g0 + far_group, lane & 15), col0 = col_of(far_block);
+            if (a.base && lane < kGroup && t != kNone) prefetch_l2(from_s[t] + col0);
+            if (far_group == 0) {
+                const char *w = a.Bm + ((size_t)tile.adapter[g0] * a.N + col0) * R * 2;
+                const int bytes = min(kBlock, a.N - col0) * R * 2;
+                if (128 * lane < bytes) prefetch_l2(w + 128 * lane);   // 4 KB at most
+            }
+            step_far();
+        };
+        static_assert(kBlock * R * 2 <= 32 * 128, "a lane a line");
+        step_far();
+        step_far();
         Task even, odd;
         if (t0 < t1) fetch(g0 + group, col_of(block), true, even);
         if (!waited) {
@@ -495,6 +526,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
             const int here = group, col0 = col_of(block);
             const int adapter = __shfl_sync(kAll, tile.adapter[g0 + group], 0);
             bool weights = false;
+            ahead();
             if (++group == n) {
                 group = 0;
                 ++block;
@@ -504,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                 weights |= __shfl_sync(kAll, tile.adapter[g0 + group], 0) != adapter;
                 if (!weights) {
 #pragma unroll
-                    for (int p = 0; p < 2; ++p)
+                    for (int p = 0; p < kP; ++p)
 #pragma unroll
                         for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -514,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                 }
                 fetch(g0 + group, col_of(block), weights, next);
             }
-            float y[2][2][4];
+            float y[kP][2][4];
 #pragma unroll
             for (int s = 0; s < kSteps; ++s) {
                 // the lower parts first
@@ -522,7 +554,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                 for (int part = kHParts - 1; part >= 0; --part) {
                     const uint4 f = h_s[here][s][part][lane];
 #pragma unroll
-                    for (int p = 0; p < 2; ++p)
+                    for (int p = 0; p < kP; ++p)
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t(&w)[2] = now.w[p][i][s];
@@ -544,7 +576,7 @@ __global__ void __launch_bounds__(kThreads, R == 64 ? 1 : 2) lora_up_kernel(cons
                     const float f = TYPE == ZQ_F16 ? back_s[here][g + 8 * e] : 1.0f;
                     float *to = to_s[t];
 #pragma unroll
-                    for (int p = 0; p < 2; ++p) {
+                    for (int p = 0; p < kP; ++p) {
                         const int n = col0 + 16 * p + 4 * c;
                         const float4 v = now.v[e][p];
                         const float4 r = make_float4(v.x + y[p][0][2 * e] * f, v.y + y[p][0][2 * e + 1] * f,
@@ -664,10 +696,10 @@ cudaError_t launch_lora(const LoraArgs &args, int type, cudaStream_t st)
     const long long room = 2LL * num_sms() / taken();
     const dim3 down(cut.tiles * halves, (unsigned)(room < 1 ? 1 : room > most ? most : room), cut.cluster * cut.parts);
     // column blocks of a CTA of the second kernel: as many CTAs as the GPU holds
-    // at once (one an SM at R = 64, else two), each of which prepares its tile's
-    // h once (512 tokens at R = 64: 33.6 us, 37.0 with two an SM; 56 tokens at
-    // R = 16: 11.3 us, 11.9 with one)
-    const long long cols = (a.N + kBlock - 1) / kBlock, ctas = (a.R == 64 ? 1LL : 2LL) * num_sms();
+    // at once, two an SM, each of which prepares its tile's h once (with one an
+    // SM 512 tokens at R = 64 take 31.5 us, 25.2 so; 56 tokens at R = 16 11.9, 11.3)
+    const int width = 16 * up_pieces(a.R);
+    const long long cols = (a.N + width - 1) / width, ctas = 2LL * num_sms();
     const long long want = (cols * cut.tiles + ctas - 1) / ctas;
     a.blocks = (int)(want < 1 ? 1 : want > 64 ? 64 : want);
     const dim3 up(cut.tiles, (unsigned)((cols + a.blocks - 1) / a.blocks));
