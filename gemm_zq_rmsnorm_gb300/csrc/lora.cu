@@ -687,6 +687,15 @@ cudaError_t launch_lora(const LoraArgs &args, int type, cudaStream_t st)
     // wide, 16 tokens of 4 adapters of R = 64: 11.1 us, 14.5 with four parts; 56 tokens of 12 of R = 16:
     // 10.7, 15.6)
     while (cut.parts > 1 && taken() * most > num_sms()) cut.set(a.K, cut.parts / 2);
+    // Smaller clusters where not all units fit at the same time, as long as a warp has few blocks: a
+    // turn costs about as much as five (5120 wide, 12 adapters, mixed: 200 tokens 17.3 -> 14.9 us, 1024 46.9 ->
+    // 38.9; 4 in runs, a tile's two or three units: 512 23.0 -> 23.8; 17408 wide they would lose: 200 tokens 19.8,
+    // 25.0)
+    while (cut.cluster > 1 && taken() * most > 2 * num_sms() &&
+           a.K / 32 <= 5 * kWarps * (cut.cluster / 2) * cut.parts) {
+        cut.cluster /= 2;
+        cut.set(a.K, cut.parts);
+    }
     a.cluster = cut.cluster;
     a.parts = cut.parts;
     a.per_split = cut.per_split;
