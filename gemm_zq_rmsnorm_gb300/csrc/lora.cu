@@ -6,11 +6,13 @@
 // Two kernels, one after the other: h_t = A_a x_t split over K, then the
 // expansion of h by B_a onto base.  Bound: HBM, the adapters once, and base and
 // y (8 B N bytes); a few tokens are launch bound.  Measured in a graph: one token,
-// 1024 -> 2048, 6.0 us; 56 tokens of 12 adapters, 5120 -> 17408, R = 16, bf16:
+// 1024 -> 2048, 5.9 us; 56 tokens of 12 adapters, 5120 -> 17408, R = 16, bf16:
 // 11.5 us (16.7 MB: 2.5 us at the copy rate; two launches in a row and their chains of
 // dependent loads are the rest); 512 tokens of 4 adapters, 17408 -> 5120, R = 64,
-// f16: 33 us (42 MB, 6.2 us; the first kernel's half is 54 MB of 32- and 64-byte
-// pieces from L2, as each 32 tokens read their adapter again).
+// f16: 25.7 us (42 MB, 6.2 us; the first kernel's two thirds are 54 MB of 32- and 64-byte
+// pieces from L2, as each 32 tokens read their adapter again, at 6.7 TB/s, and a
+// second turn where a tile has three units); 4096 tokens, 5120 -> 17408, R = 16:
+// 126 us, 4.9 TB/s.
 //
 // Tokens come in tiles of 64.  A CTA sorts its tile's tokens by adapter itself
 // (64 ids: a scan of comparisons) and takes them sixteen at a time as the rows of
