@@ -17,7 +17,7 @@
 // most, and the warp-level form needs no hand-over between warps.)
 // Measured, kernel pairs in a graph: 48 sequences of 1 to 12000 rows, 48 query
 // and 8 key heads of 128, bf16: 129 us, 5.8 TB/s (0.86 of the measured copy
-// rate); one sequence of 131071, 24 and 4 heads of 256, bf16: 95 us, 5.7 TB/s; 64
+// rate); one sequence of 131071, 24 and 4 heads of 256, bf16: 94 us, 5.7 TB/s; 64
 // sequences of 8000 to 24000, e4m3: 278 us, 6.3 TB/s.  What is left of the 16-bit
 // cases is their end: the SMs of some GPCs get 10 % less of the bandwidth, and
 // the shares are equal.  200 windows of up to 1024 rows, 64-wide heads, e4m3: 44 us,
@@ -980,13 +980,13 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const __grid_constant__ PagedAttnArgs a, int ctas)
 {
-    constexpr int kWarps = kJoinThreads / 32, kChunks = (D + 127) / 128;
+    constexpr int kWarps = kJoinThreads / 32, kChunks = (D + 127) / 128, kAhead = 4;
     static_assert(kWarps * 32 >= kMaxAttnCtas, "a warp's lanes hold the weights of its pieces");
     __shared__ float m_s[kWarps], l_s[kWarps];
     __shared__ float4 y_s[kWarps][D / 4];
     pdl_wait();
     pdl_launch_dependents();
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, first = blockIdx.x, h = blockIdx.y;
+    const int warp = __shfl_sync(kAll, threadIdx.x >> 5, 0), lane = threadIdx.x & 31, first = blockIdx.x, h = blockIdx.y;
     const Meta *meta = reinterpret_cast<const Meta *>(a.meta);
     const Meta mine = meta[first];
     // the CTA where it ends, 32 of those that follow at a time
@@ -1009,6 +1009,14 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const __g
         pm = piece(warp + kWarps * lane)[kHeads * D + h];
         pl = piece(warp + kWarps * lane)[kHeads * D + kHeads + h];
     }
+    const int col = D < 128 ? 4 * (lane % (D / 4)) : 4 * lane;   // (64-wide rows: half the lanes repeat the other)
+    auto row = [&](int j) { return piece(warp + kWarps * j) + h * D + col; };
+    float4 v[kAhead][kChunks];   // the first pieces' values come beside their m and l
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+        if (j < count)
+#pragma unroll
+            for (int k = 0; k < kChunks; ++k) v[j][k] = *reinterpret_cast<const float4 *>(row(j) + 128 * k);
     float4 y[kChunks];
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) y[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -1017,19 +1025,24 @@ __global__ void __launch_bounds__(kJoinThreads) paged_attn_join_kernel(const __g
     for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
     const float f = ex2(pm - (m == -INFINITY ? 0.0f : m));
     const float l = warp_sum(lane < count ? f * pl : 0.0f);
-    const int col = D < 128 ? 4 * (lane % (D / 4)) : 4 * lane;   // (64-wide rows: half the lanes repeat the other)
-#pragma unroll 4
-    for (int j = 0; j < count; ++j) {
-        const float fj = __shfl_sync(kAll, f, j);
-        const float *from = piece(warp + kWarps * j) + h * D + col;
+    auto add = [&](float fj, const float4(&v)[kChunks]) {
 #pragma unroll
         for (int k = 0; k < kChunks; ++k) {
-            const float4 v = *reinterpret_cast<const float4 *>(from + 128 * k);
-            y[k].x += fj * v.x;
-            y[k].y += fj * v.y;
-            y[k].z += fj * v.z;
-            y[k].w += fj * v.w;
+            y[k].x += fj * v[k].x;
+            y[k].y += fj * v[k].y;
+            y[k].z += fj * v[k].z;
+            y[k].w += fj * v[k].w;
         }
+    };
+#pragma unroll
+    for (int j = 0; j < kAhead; ++j)
+        if (j < count) add(__shfl_sync(kAll, f, j), v[j]);
+#pragma unroll 4
+    for (int j = kAhead; j < count; ++j) {
+        float4 x[kChunks];
+#pragma unroll
+        for (int k = 0; k < kChunks; ++k) x[k] = *reinterpret_cast<const float4 *>(row(j) + 128 * k);
+        add(__shfl_sync(kAll, f, j), x);
     }
 #pragma unroll
     for (int k = 0; k < kChunks; ++k) y_s[warp][col / 4 + 32 * k] = y[k];
