@@ -53,6 +53,7 @@
 // values.  p in [0, 1] goes to the value product in as many parts (exact to 2^-24
 // in three of bf16, 2^-22 in two of binary16; two of bf16, 2^-17, would be 2 to
 // 3 % faster); l sums the unrounded p.
+#include <float.h>
 #include <math.h>
 
 #include "zq_async.cuh"
@@ -583,8 +584,10 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                     hi -= f.y;
                 }
             }
-            scale0 = a.qk_scale * __shfl_sync(kAll, back, 8 * c);
-            scale1 = a.qk_scale * __shfl_sync(kAll, back, 8 * c + 4);
+            // positive and finite: times 0 a masked -infinity, times infinity a score of 0 would be NaN
+            back = fminf(fmaxf(a.qk_scale * back, __uint_as_float(1)), FLT_MAX);
+            scale0 = __shfl_sync(kAll, back, 8 * c);
+            scale1 = __shfl_sync(kAll, back, 8 * c + 4);
         }
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.0f;

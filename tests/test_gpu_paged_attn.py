@@ -194,6 +194,26 @@ def test_large_and_small_queries(dtype):
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("k_scale", [2.0 ** -100, 2.0 ** 100])
+@pytest.mark.parametrize("dtype", [F16, BF16, E4M3])
+def test_cache_scales_far_from_one_and_queries_of_zeros(k_scale, dtype):
+    """The scale of the scores may leave fp32's range where they are zeros: masked rows stay out, the others count alike."""
+    c = Case(22, [40, 1, 700, 0], 8, 2, 64, dtype, 16)
+    c.ks, c.cache = k_scale, zq.KVCache(c.k, c.v, k_scale, 1.0)
+    c.q *= min(1.0, 1 / k_scale)
+    c.q[:, 1::2] = 0.0
+    c.check(*c.run())
+
+
+@pytest.mark.parametrize("dtype", [F16, E4M3])
+def test_keys_of_zeros_under_large_queries(dtype):
+    c = Case(24, [33, 5], 4, 2, 128, dtype, 16)
+    c.k.copy_(torch.zeros_like(c.k, dtype=torch.float32).to(dtype))
+    c.cache = zq.KVCache(c.k, c.v, 2.0 ** 30, 1.0)
+    c.q *= 1e30
+    c.check(*c.run())
+
+
 def test_large_scores_pick_one_row():
     """Scores in the thousands: all weight on one row, none overflows."""
     c = Case(23, [90], 4, 2, 128, BF16, 16)
