@@ -496,8 +496,8 @@ ZQ_API int zq_rope_table(const double *inv_freq, const int *axis, int n, uint64_
  *   q : fp32, head h of token t at q + t * q_stride + h * D; k, v alike with
  *       Hk heads (strides in floats, multiples of 4);
  *   gamma_q, gamma_k : fp32 [D], either may be NULL (that norm is left out);
- *   xh = (x / sqrt(mean(x^2) + eps)) * gamma over the head's D values, the mean
- *       in fp32 (a head whose squares leave its range is normed as if by it);
+ *   xh = (x / sqrt(mean(x^2) + eps)) * gamma over the head's D values (the
+ *       mean in fp32: where it overflows xh is 0, where it vanishes eps norms);
  *   table : device uint64 [rot / 2] (zq_rope_table); rot a multiple of 16,
  *       0..D (0: no rotation, table may be NULL); the first rot values are
  *       rotated, pair p being (p, p + rot/2), or (2p, 2p + 1) with
