@@ -17,9 +17,9 @@
 // HBM bound for long prompts: 4 D (2 Hq + 2 Hk) + 2 es D Hk bytes per token;
 // launch bound for a few tokens.  Measured in a graph: 4096 tokens of 48 + 8 + 8
 // heads of 128 to an f16 cache 43.0 us, 5.9 TB/s (0.86 of the measured copy rate);
-// 777 tokens of 24 + 4 + 4 heads of 256 to an e4m3 cache 12.5 us, 3.7 TB/s (two
-// rounds of warps, whose 8 values a lane make the instructions count); 61 tokens
-// 4.0 us, one token 2.5 us.
+// 777 tokens of 24 + 4 + 4 heads of 256 to an e4m3 cache 11.1 us, 4.2 TB/s (one
+// round of warps, whose 8 values a lane make the instructions count); 61 tokens
+// 3.4 us, one token 2.3 us.
 #include "zq_async.cuh"
 #include "zq_internal.cuh"
 #include "zq_kv.cuh"
@@ -213,41 +213,65 @@ __global__ void __launch_bounds__(kThreads) head_norm_rope_kernel(const __grid_c
         if (r + u < r1) row(r + u, x[u]);
 }
 
-template <int D, int TYPE>
-cudaError_t launch_one(const HeadNormRopeArgs &a, dim3 grid, cudaStream_t st)
+// Rows of a warp: a warp's start (slot, positions, angles, gamma) costs about as
+// much as two rows, and a second round of warps as much as the first, so as few
+// rows as let all warps run at the same time, between 2 and 16 (1 for a few
+// tokens, where latency counts).  777 tokens of 32 rows of 256: 8 rows, one
+// round, 11.1 us; 4 rows, two rounds, 12.6; 16 rows 13.7.  500 of 64 rows of 128: 7 rows
+// 8.2 us, 4 9.1, 16 10.2.  Rows of up to 128 want 16 warps an SM and no more while a
+// warp has up to ten rows (200 tokens of 64 rows: 6 rows 4.7 us, 3 rows and all the
+// SM holds 5.2); rows of 256 all of it (400 tokens of 32 rows: 4 rows 6.0, 6 7.2).
+template <int D, int TYPE, bool INTER>
+cudaError_t launch_kernel(const HeadNormRopeArgs &args, cudaStream_t st)
 {
-    return a.interleaved ? launch_pdl(head_norm_rope_kernel<D, TYPE, true>, grid, dim3(kThreads), 0, st, a)
-                         : launch_pdl(head_norm_rope_kernel<D, TYPE, false>, grid, dim3(kThreads), 0, st, a);
+    static int per_sm;   // CTAs that an SM holds, the same on every device of the architecture
+    auto *kernel = head_norm_rope_kernel<D, TYPE, INTER>;
+    if (!per_sm) {
+        int n = 0;
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0);
+        if (e != cudaSuccess) return e;
+        per_sm = n > 0 ? n : 1;
+    }
+    HeadNormRopeArgs a = args;
+    const long long rows = a.Hq + 2LL * a.Hk, sms = num_sms();
+    auto chunk_of = [&](long long warps) {   // rows of a warp when so many share the rows
+        const long long chunks = warps / a.T < 1 ? 1 : warps / a.T;
+        return (rows + chunks - 1) / chunks;
+    };
+    long long chunk = chunk_of(16 * sms);
+    if (D == 256 || chunk > 10) chunk = chunk_of(sms * per_sm * (kThreads / 32));
+    const long long least = a.T * rows <= 8 * sms ? 1 : 2;
+    chunk = chunk < least ? least : chunk > 16 ? 16 : chunk;
+    a.chunk = (int)chunk;
+    a.chunks = (int)((rows + chunk - 1) / chunk);
+    const long long warps = (long long)a.T * a.chunks;
+    return launch_pdl(kernel, dim3((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32))), dim3(kThreads), 0, st, a);
+}
+
+template <int D, int TYPE>
+cudaError_t launch_one(const HeadNormRopeArgs &a, cudaStream_t st)
+{
+    return a.interleaved ? launch_kernel<D, TYPE, true>(a, st) : launch_kernel<D, TYPE, false>(a, st);
 }
 
 template <int D>
-cudaError_t launch_type(const HeadNormRopeArgs &a, int type, dim3 grid, cudaStream_t st)
+cudaError_t launch_type(const HeadNormRopeArgs &a, int type, cudaStream_t st)
 {
     switch (type) {
-    case ZQ_F16: return launch_one<D, ZQ_F16>(a, grid, st);
-    case ZQ_BF16: return launch_one<D, ZQ_BF16>(a, grid, st);
-    default: return launch_one<D, ZQ_E4M3>(a, grid, st);
+    case ZQ_F16: return launch_one<D, ZQ_F16>(a, st);
+    case ZQ_BF16: return launch_one<D, ZQ_BF16>(a, st);
+    default: return launch_one<D, ZQ_E4M3>(a, st);
     }
 }
 
 }  // namespace
 
-cudaError_t launch_head_norm_rope(const HeadNormRopeArgs &args, int D, int type, cudaStream_t st)
+cudaError_t launch_head_norm_rope(const HeadNormRopeArgs &a, int D, int type, cudaStream_t st)
 {
-    HeadNormRopeArgs a = args;
-    const long long rows = a.Hq + 2LL * a.Hk;
-    // Enough warps for every SM first (one row each, latency counts), then four
-    // to 16 rows a warp, which share the warp's angles.
-    long long chunk = a.T * rows / ((long long)num_sms() * 32);
-    chunk = chunk < 4 ? (chunk < 1 ? 1 : chunk) : chunk > 16 ? 16 : chunk / 4 * 4;
-    a.chunk = (int)chunk;
-    a.chunks = (int)((rows + chunk - 1) / chunk);
-    const long long warps = (long long)a.T * a.chunks;
-    const dim3 grid((unsigned)((warps + kThreads / 32 - 1) / (kThreads / 32)));
     switch (D) {
-    case 64: return launch_type<64>(a, type, grid, st);
-    case 128: return launch_type<128>(a, type, grid, st);
-    default: return launch_type<256>(a, type, grid, st);
+    case 64: return launch_type<64>(a, type, st);
+    case 128: return launch_type<128>(a, type, st);
+    default: return launch_type<256>(a, type, st);
     }
 }
 
