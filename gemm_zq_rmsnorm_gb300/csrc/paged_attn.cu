@@ -908,62 +908,78 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         }
         meta[blockIdx.x] = info;
     }
-    for (int i = warp; i < runs * kHeads; i += kWarps) {
-        const int h = i % kHeads;
-        int w0, w1;
-        bool begins;
-        run_of(i / kHeads, w0, w1, begins);
-        const bool ends = i / kHeads < ends_here;
-        const Meta block = begins ? open_s[w0] : Meta{0, 0, 0, 0, kHeads};
-        if (h >= block.heads) continue;
+    // An item is a head of a run.  Its run's ending piece comes from the workspace: the next item's is on its way
+    // during the sums (500 sequences of 300, 64-wide heads: 68.2 us, 72.5 with each read when it is due)
+    struct Item {
+        int h, w0, w1;
+        bool begins, ends;
+        float pm, pl;
+        float4 tail[(D + 127) / 128];
+    };
+    auto item = [&](int i, Item &x) {
+        const int r = i / a.per_pass;
+        x.h = i - r * a.per_pass;
+        run_of(r, x.w0, x.w1, x.begins);
+        x.ends = r < ends_here;
+        x.pm = -INFINITY;
+        x.pl = 0.0f;
+        if (!x.ends) return;
+        const float *tail = a.pieces + ((size_t)2 * gridDim.x + (size_t)blockIdx.x * kWarps + x.w1) * piece_floats(D);
+        if (lane == 31) {
+            x.pm = tail[kHeads * D + x.h];
+            x.pl = tail[kHeads * D + kHeads + x.h];
+        }
+#pragma unroll
+        for (int d0 = 0; d0 < D; d0 += 128)
+            x.tail[d0 / 128] = *reinterpret_cast<const float4 *>(tail + x.h * D + d0 + (D < 128 ? 4 * lane % D : 4 * lane));
+    };
+    auto join = [&](const Item &x) {
+        const int h = x.h;
+        if (x.begins && h >= open_s[x.w0].heads) return;
         // lane w has the maximum, the sum and then the weight of warp w's piece, lane 31 the ending one's
-        const float *tail = a.pieces + ((size_t)2 * gridDim.x + (size_t)blockIdx.x * kWarps + w1) * piece_floats(D);
-        const uint32_t pieces = opened & ((1u << w1) - 1) & (~0u << w0);   // (a call of few tiles leaves gaps)
-        float pm = -INFINITY, pl = 0.0f;
+        const uint32_t pieces = opened & ((1u << x.w1) - 1) & (~0u << x.w0);   // (a call of few tiles leaves gaps)
+        float pm = x.pm, pl = x.pl;
         if (pieces >> lane & 1) {
             pm = m_s[lane][h];
             pl = l_s[lane][h];
-        } else if (ends && lane == 31) {
-            pm = tail[kHeads * D + h];
-            pl = tail[kHeads * D + kHeads + h];
         }
         float m = pm;
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) m = fmaxf(m, __shfl_xor_sync(kAll, m, off));
         const float f = ex2(pm - (m == -INFINITY ? 0.0f : m));
-        const float l = warp_sum((pieces >> lane & 1) || (ends && lane == 31) ? f * pl : 0.0f);
+        const float l = warp_sum((pieces >> lane & 1) || (x.ends && lane == 31) ? f * pl : 0.0f);
 #pragma unroll
         for (int d0 = 0; d0 < D; d0 += 128) {
             const int d = d0 + 4 * lane;
             const bool in = d < D;
             float y[4] = {};
-            auto add = [&](const float *from, float f) {
-                const float4 v = *reinterpret_cast<const float4 *>(from + h * D + (in ? d : 0));
+            auto add = [&](const float4 &v, float f) {
                 y[0] += f * v.x;
                 y[1] += f * v.y;
                 y[2] += f * v.z;
                 y[3] += f * v.w;
             };
 #pragma unroll 4
-            for (int w = w0; w < w1; ++w) {
+            for (int w = x.w0; w < x.w1; ++w) {
                 const float fw = __shfl_sync(kAll, f, w);
-                if (pieces >> w & 1) add(pieces_s + (size_t)w * kHeads * D, fw);
+                if (pieces >> w & 1)
+                    add(*reinterpret_cast<const float4 *>(pieces_s + ((size_t)w * kHeads + h) * D + (in ? d : 0)), fw);
             }
             const float ft = __shfl_sync(kAll, f, 31);
-            if (ends) add(tail, ft);
-            if (begins && ends) {
+            if (x.ends) add(x.tail[d0 / 128], ft);
+            if (x.begins && x.ends) {
                 const float g = row_factor(l, a.v_scale);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) y[e] *= g;
-                const int head = block.head + h;
+                const int seq = open_s[x.w0].seq, head = open_s[x.w0].head + h;
                 if (in && a.out)
-                    *reinterpret_cast<float4 *>(a.out + (long long)block.seq * a.out_stride + (long long)head * D +
+                    *reinterpret_cast<float4 *>(a.out + (long long)seq * a.out_stride + (long long)head * D +
                                                 d) = make_float4(y[0], y[1], y[2], y[3]);
                 if (a.q8.qs)
-                    q8_block<4, 1, 2, 4>(a.q8, ((size_t)block.seq * a.Hq + head) * D + d, y, in, (d & 31) == 0);
-                if (d == 0 && a.lse) a.lse[(size_t)block.seq * a.Hq + head] = row_lse(m, l);
+                    q8_block<4, 1, 2, 4>(a.q8, ((size_t)seq * a.Hq + head) * D + d, y, in, (d & 31) == 0);
+                if (d == 0 && a.lse) a.lse[(size_t)seq * a.Hq + head] = row_lse(m, l);
             } else if (in) {
-                float *to = a.pieces + (size_t)(2 * blockIdx.x + (begins ? 1 : 0)) * piece_floats(D);
+                float *to = a.pieces + (size_t)(2 * blockIdx.x + (x.begins ? 1 : 0)) * piece_floats(D);
                 *reinterpret_cast<float4 *>(to + h * D + d) = make_float4(y[0], y[1], y[2], y[3]);
                 if (d == 0) {
                     to[kHeads * D + h] = m;
@@ -971,6 +987,16 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 }
             }
         }
+    };
+    const int items = runs * a.per_pass;
+    Item even, odd;
+    if (warp < items) item(warp, even);
+    for (int i = warp; i < items; i += 2 * kWarps) {
+        if (i + kWarps < items) item(i + kWarps, odd);
+        join(even);
+        if (i + kWarps >= items) break;
+        if (i + 2 * kWarps < items) item(i + 2 * kWarps, even);
+        join(odd);
     }
 }
 
