@@ -337,7 +337,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     int ctas;
     Walk at;
     auto share = [&]() {   // false: this CTA takes no part
-        ctas = (int)min((long long)gridDim.x, max(1ll, total / (kWarps * kMinTiles)));
+        ctas = (int)min((long long)gridDim.x, (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles));
         if (blockIdx.x >= ctas) return false;
         const uint32_t nw = ctas * kWarps;
         long long q, r;    // the first r warps have a place more
