@@ -72,7 +72,6 @@ constexpr int kJoinThreads = 256;
 constexpr int kHalf = 16;       // tokens of an MMA
 constexpr int kTile = 32;       // tokens of a step: two MMAs' worth, so that a warp has independent chains
 constexpr int kHeads = 8;       // query heads of a pass: the MMA's columns
-constexpr int kMinTiles = 1;    // places of the line a warp takes at least, before more CTAs join in
 constexpr int kBlockCost = 1;   // what a row block costs besides its tiles, in tiles (with 6, those windows took 10 % longer)
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr unsigned kAll = 0xffffffffu;
@@ -337,7 +336,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     int ctas;
     Walk at;
     auto share = [&]() {   // false: this CTA takes no part
-        ctas = (int)min((long long)gridDim.x, (total + kWarps * kMinTiles - 1) / (kWarps * kMinTiles));
+        ctas = (int)min((long long)gridDim.x, (total + kWarps - 1) / kWarps);
         if (blockIdx.x >= ctas) return false;
         const uint32_t nw = ctas * kWarps;
         long long q, r;    // the first r warps have a place more
@@ -352,8 +351,14 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         left = q + (gw < r ? 1 : 0);
         return true;
     };
+    // Few row blocks of few tiles have a CTA each and a warp a tile, so that the second kernel finds nothing open
+    // (one sequence of 300, 128-wide heads: 9.7 us, 10.8 on the line; 8 of 250, 64-wide 7.7, 9.8)
+    bool own = false;
     if (a.B <= 32) {       // every warp by itself: lane b has sequence b
-        const long long mine = lane < a.B ? places(lane) : 0;
+        const long long line = lane < a.B ? places(lane) : 0;
+        const bool few = __all_sync(kAll, line <= (kWarps + kBlockCost) * vheads);   // at most kWarps tiles in each
+        own = __shfl_sync(kAll, few && a.B * vheads <= (int)gridDim.x, 0);   // (a shuffle as above)
+        const long long mine = own && lane < a.B ? kWarps * vheads : line;
         long long incl = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -410,13 +415,13 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
         }
     }
     if (left > 0) {        // key head, pass and tile
-        const int n = at.tend - at.t0 + kBlockCost;
+        const int tiles = at.tend - at.t0, n = own ? kWarps : tiles + kBlockCost;
         const int vh = rem >> 32 ? (int)(rem / n) : (int)((uint32_t)rem / (uint32_t)n);
         const int r = (int)(rem - (long long)vh * n);
         at.kh = vh / a.passes;
         at.pass = vh - at.kh * a.passes;
-        at.t = at.t0 + max(0, r - kBlockCost);
-        left -= max(0, kBlockCost - r);
+        at.t = at.t0 + (own ? r : max(0, r - kBlockCost));
+        left -= own ? r >= tiles : max(0, kBlockCost - r);
     }
 
     // ---- the ring: the items of a tile are keys, keys, values, values, 16 tokens each
