@@ -16,13 +16,13 @@
 // returns through tensor memory; at 8 columns the tensor pipe is a third busy at
 // most, and the warp-level form needs no hand-over between warps.)
 // Measured, kernel pairs in a graph: 48 sequences of 1 to 12000 rows, 48 query
-// and 8 key heads of 128, bf16: 129 us, 5.8 TB/s (0.86 of the measured copy
+// and 8 key heads of 128, bf16: 127 us, 5.9 TB/s (0.88 of the measured copy
 // rate); one sequence of 131071, 24 and 4 heads of 256, bf16: 94 us, 5.7 TB/s; 64
-// sequences of 8000 to 24000, e4m3: 278 us, 6.3 TB/s.  What is left of the 16-bit
-// cases is their end: the SMs of some GPCs get 10 % less of the bandwidth, and
-// the shares are equal.  200 windows of up to 1024 rows, 64-wide heads, e4m3: 44 us,
-// 3.2 TB/s, bound by the instructions of 4 KB tiles and of 1600 row blocks' ends.
-// One sequence of 1000: 10 us, a chain of latencies (lengths, table, keys, two
+// sequences of 8000 to 24000, e4m3: 284 to 288 us, 6.1 TB/s.  What is left of the
+// 16-bit cases is their end: the SMs of some GPCs get 10 % less of the bandwidth, and
+// the shares are equal.  200 windows of up to 1024 rows, 64-wide heads, e4m3: 40.5 us,
+// 3.5 TB/s, bound by the instructions of 4 KB tiles and of 1600 row blocks' ends.
+// One sequence of 1000: 9.7 us, a chain of latencies (lengths, table, keys, two
 // joins) over two launches.
 //
 // Work: every (sequence, key head) has ceil(len / 32) tiles of 32 tokens (at
