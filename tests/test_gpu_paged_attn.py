@@ -194,6 +194,20 @@ def test_large_and_small_queries(dtype):
     c.check(*c.run())
 
 
+@pytest.mark.parametrize("D,dtype", [(64, E4M3), (128, BF16), (256, F16)])
+@pytest.mark.parametrize("lens,Hq,Hk,window", [
+    ([n], 8, 2, 0) for n in (255, 256, 257, 384, 385, 512, 513)] + [
+    ([300, 0, 1, 256], 32, 2, 0), ([5000, 30, 700], 6, 3, 250), ([250] * 19, 8, 8, 0), ([250] * 20, 8, 8, 0),
+    ([40] * 32, 4, 4, 0), ([256, 257], 20, 1, 0)])
+def test_few_row_blocks_of_about_a_tile_for_each_warp(D, dtype, lens, Hq, Hk, window):
+    """Around where row blocks stop having a CTA each: 8, 12 or 16 tiles of 32 rows, and as many blocks as SMs."""
+    c = Case(sum(lens) + Hq, lens, Hq, Hk, D, dtype, 32, window=window)
+    out, lse = c.run()
+    c.check(out, lse)
+    again, _ = c.run()
+    assert torch.equal(out, again)
+
+
 @pytest.mark.parametrize("k_scale", [2.0 ** -100, 2.0 ** 100])
 @pytest.mark.parametrize("dtype", [F16, BF16, E4M3])
 def test_cache_scales_far_from_one_and_queries_of_zeros(k_scale, dtype):
