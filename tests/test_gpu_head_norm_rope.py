@@ -97,6 +97,25 @@ def test_against_64_bits(D, dtype, T, Hq, Hk, rot_part, axes, interleaved, page)
     check_cache(v, x[:, Hq + Hk:].astype(np.float64), s, dtype, np.float64(np.float32(vs)), -5.0, 2.0 ** -23)
 
 
+@pytest.mark.parametrize("D,dtype", [(64, E4M3), (128, BF16), (256, F16)])
+@pytest.mark.parametrize("T,Hq,Hk", [(150, 48, 8), (700, 24, 4), (2000, 11, 3), (4500, 5, 1)])
+def test_a_long_call_equals_short_ones(D, dtype, T, Hq, Hk):
+    """How rows are dealt to warps depends on the number of tokens; what becomes of a row does not."""
+    qkv, k, v, slots, gq, gk, g = make(T, T, Hq, Hk, D, dtype, 64)
+    pos = torch.from_numpy(g.integers(0, 1 << 17, T).astype(np.int32)).cuda()
+    table = zq.rope_table(inv_freq(D))
+    q, kr, vr = parts(qkv, Hq, Hk, D)
+    out = zq.head_norm_rope(q, kr, vr, gq, gk, EPS, table, pos, zq.KVCache(k, v), slots)
+    k2, v2 = torch.full_like(k, 3.0), torch.full_like(v, -5.0)
+    cache, out2 = zq.KVCache(k2, v2), torch.empty_like(out)
+    for t in range(0, T, 61):
+        at = slice(t, t + 61)
+        zq.head_norm_rope(q[at], kr[at], vr[at], gq, gk, EPS, table, pos[at], cache, slots[at], q_out=out2[at])
+    assert torch.equal(out, out2)
+    assert torch.equal(k.view(torch.uint8), k2.view(torch.uint8))
+    assert torch.equal(v.view(torch.uint8), v2.view(torch.uint8))
+
+
 def test_no_norm_no_rotation_is_a_copy():
     """Without gammas and table queries are copied bit for bit, keys and values only rounded."""
     T, Hq, Hk, D = 19, 3, 2, 128
