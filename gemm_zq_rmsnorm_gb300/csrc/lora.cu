@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2) lora_down_kernel(const __grid_con
 }
 
 // y[t] = base[t] + scale_a B_a h_t.  Grid: (tiles, column ranges of a.blocks
-// blocks of 32).  A task is one block for one group of sixteen tokens; a warp
+// blocks of 16 or 32 outputs).  A task is one block for one group of sixteen tokens; a warp
 // takes neighbouring tasks of one block after the other, the next one's values
 // on their way while it works on one.
 // VEC: rows of base and y are 16-byte aligned and N is a multiple of four, so

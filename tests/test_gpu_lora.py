@@ -128,6 +128,16 @@ def test_long_rows_are_cut_by_the_units_of_a_tile(B, n, R):
     check(zq.lora(a, ids, A, Bm, scales, base=base), a, A, Bm, scales, base, ids)
 
 
+@pytest.mark.parametrize("R,dtype", [(8, F16), (16, BF16), (32, F16), (64, BF16)])
+@pytest.mark.parametrize("B,N,runs", [(320, 20000, False), (512, 17409, True)])
+def test_many_columns(R, dtype, B, N, runs):
+    """Enough outputs for a warp to have many tasks one after the other, in place; the last columns a part of a block."""
+    ids = np.random.default_rng(B + R).integers(-1, 6, B)
+    a, A, Bm, scales, base, ids = make(B + R, B, 64, N, R, 6, dtype, np.sort(ids) if runs else ids)
+    y = base.clone()
+    check(zq.lora(a, ids, A, Bm, scales, base=y, y=y), a, A, Bm, scales, base, ids)
+
+
 def test_large_batch_of_runs():
     B, K, N, R = 2500, 256, 128, 16
     ids = np.repeat(np.arange(7) - 1, 400)[:B]
