@@ -50,9 +50,12 @@
 // Precision: q is split exactly into parts of the cache's 16-bit type (three
 // bf16 parts; two binary16 parts after scaling the row to [1, 2), 2^-22 of its
 // largest value), every product is exact, sums are fp32; e4m3 values are binary16
-// values.  p in [0, 1] goes to the value product in as many parts (exact to 2^-24
-// in three of bf16, 2^-22 in two of binary16; two of bf16, 2^-17, would be 2 to
-// 3 % faster); l sums the unrounded p.
+// values.  p in [0, 1] goes to the value product in as many parts: three of bf16,
+// 2^-24 of p (two, 2^-17, would be 2 to 3 % faster), or two of binary16, which
+// take 2^15 p, because their smallest step is 2^-24: 2^-22 of p, or 2^-40 where
+// that is more, so that rows far below a dominant one (an attention sink, whose
+// value is often near zero) count; the output carries the 2^15 until its piece
+// is written.  l sums the unrounded p.
 #include <float.h>
 #include <math.h>
 
@@ -95,6 +98,8 @@ struct Cfg {
     static constexpr int kMerge = kWarps * kHeads * D * 4;   // the warps' open pieces, after the ring is done
     static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;   // aligned to the swizzle's 1024 bytes
     static constexpr int kSplits = TYPE == ZQ_BF16 ? 3 : 2;  // parts of q and of the weights
+    static constexpr float kWeightUp = TYPE == ZQ_BF16 ? 1.0f : 0x1p15f;   // of the weights in the value product
+    static constexpr float kWeightDown = 1.0f / kWeightUp;
     static constexpr int kSeg = kRow < 128 ? kRow : 128;          // bytes of a segment of a row
     static constexpr int kSegs = kRow / kSeg;
     static constexpr int kKBytes = kSeg / 4;            // a lane's keys of a segment: two chunks, or one
@@ -517,7 +522,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
     Meta open{0, 0, 0, 0, 0};
     float *head_piece = a.pieces + ((size_t)2 * gridDim.x + (size_t)gw) * piece_floats(D);
 
-    // the output as it stands, eight rows of D
+    // the output as it stands, without the weights' scale, eight rows of D
     auto put_rows = [&](float *to) {
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
@@ -527,10 +532,10 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 if constexpr (TYPE == ZQ_E4M3) {
                     constexpr int kPairs = C::kVRun / 2;
                     *reinterpret_cast<float2 *>(row + (8 * (i / kPairs) + g) * C::kVRun + 2 * (i % kPairs)) =
-                        make_float2(o[i][e], o[i][2 + e]);
+                        make_float2(o[i][e] * C::kWeightDown, o[i][2 + e] * C::kWeightDown);
                 } else {
-                    row[16 * i + g] = o[i][e];
-                    row[16 * i + 8 + g] = o[i][2 + e];
+                    row[16 * i + g] = o[i][e] * C::kWeightDown;
+                    row[16 * i + 8 + g] = o[i][2 + e] * C::kWeightDown;
                 }
             }
         }
@@ -692,7 +697,7 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 const float p2 = ex2(__fmaf_rn(sc[h][2], scale0, -u0m)), p3 = ex2(__fmaf_rn(sc[h][3], scale1, -u1m));
                 l0 += p0 + p2;
                 l1 += p1 + p3;
-                float r[4] = {p0, p1, p2, p3};
+                float r[4] = {p0 * C::kWeightUp, p1 * C::kWeightUp, p2 * C::kWeightUp, p3 * C::kWeightUp};
 #pragma unroll
                 for (int p = 0; p < C::kSplits; ++p) {
                     const uint32_t w0 = pack16<TYPE>(r[0], r[1]), w1 = pack16<TYPE>(r[2], r[3]);
@@ -811,8 +816,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                         float y[C::kVRun];
 #pragma unroll
                         for (int j = 0; j < C::kVRun / 2; ++j) {
-                            y[2 * j] = o[s * (C::kVRun / 2) + j][e] * f;
-                            y[2 * j + 1] = o[s * (C::kVRun / 2) + j][2 + e] * f;
+                            y[2 * j] = o[s * (C::kVRun / 2) + j][e] * C::kWeightDown * f;
+                            y[2 * j + 1] = o[s * (C::kVRun / 2) + j][2 + e] * C::kWeightDown * f;
                         }
                         const int d0 = (8 * s + g) * C::kVRun;
                         if (store && a.out) {
@@ -828,7 +833,8 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                 } else {
 #pragma unroll
                     for (int i = 0; i < D / 16; i += 2) {
-                        const float y[4] = {o[i][e] * f, o[i][2 + e] * f, o[i + 1][e] * f, o[i + 1][2 + e] * f};
+                        const float y[4] = {o[i][e] * C::kWeightDown * f, o[i][2 + e] * C::kWeightDown * f,
+                                            o[i + 1][e] * C::kWeightDown * f, o[i + 1][2 + e] * C::kWeightDown * f};
                         if (store && a.out) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) row[16 * i + 8 * k + g] = y[k];

@@ -541,8 +541,10 @@ ZQ_API int zq_head_norm_rope(const float *q, long long q_stride, const float *k,
  *           aligned; contents do not matter.  Calls that may run at the same
  *           time (other streams, captured graphs) need workspaces of their own.
  * q is not rounded: products with the cache's values are exact (an f16 or e4m3
- * cache takes q to 2^-22 of its row's largest value), sums fp32.  The result
- * does not change from one call to the next.
+ * cache takes q to 2^-22 of its row's largest value), sums fp32.  A row's weight
+ * is exp(s_j - s_max) to fp32's accuracy (an f16 or e4m3 cache takes it to 2^-22
+ * of itself, or 2^-40 where that is more).  The result does not change from one
+ * call to the next.
  * Shapes: Hq a multiple of Hk, Hq / Hk <= 64, 1 <= B <= 65535, width >= 1,
  * width * page <= 2^30, B * Hk * width < 2^40; strides multiples of 4.
  */
