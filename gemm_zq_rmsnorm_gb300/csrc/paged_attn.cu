@@ -45,7 +45,9 @@
 // paired by token first; every access falls on all banks.
 // Rows past the end, before the window or on a page outside the cache never
 // meet a product: their scores are replaced by -infinity and their value words
-// by zeros, whatever the cache holds there (infinities, NaN).
+// by zeros, whatever the cache holds there (infinities, NaN).  An infinite key
+// of a row that is attended to makes the score it stands for: -infinity weighs
+// nothing.
 //
 // Precision: q is split exactly into parts of the cache's 16-bit type (three
 // bf16 parts; two binary16 parts after scaling the row to [1, 2), 2^-22 of its
@@ -658,6 +660,9 @@ paged_attn_kernel(const __grid_constant__ PagedAttnArgs a, const __grid_constant
                     float v = acc[C::kSplits - 1][e];
 #pragma unroll
                     for (int p = C::kSplits - 2; p >= 0; --p) v += acc[p][e];
+                    // an infinite key makes the first part's score infinite, and the lower ones' NaN where those parts
+                    // are zeros or of the other sign (e4m3 has no infinities)
+                    if constexpr (TYPE != ZQ_E4M3) v = fabsf(acc[0][e]) == INFINITY ? acc[0][e] : v;
                     sc[h][e] = v;
                 }
             }

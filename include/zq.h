@@ -528,6 +528,11 @@ ZQ_API int zq_head_norm_rope(const float *q, long long q_stride, const float *k,
  * as if masked; a sequence without rows (n <= 0, or all left out) has out = 0
  * and lse = -infinity.  Nothing outside the rows is read, whatever it
  * holds; table entries past a sequence's last page may hold anything.
+ * Infinities of the cache's rows (f16 and bf16): a score of -infinity weighs
+ * nothing (a head with no other has out = 0 and lse = -infinity), one of
+ * +infinity, or a NaN, makes its head NaN; an infinite or NaN value makes its
+ * column of the output infinite or NaN.  Other heads, columns and sequences
+ * do not see them.
  *   q     : fp32, head h of sequence b at q + b * q_stride + h * D;
  *   table : int32 [B][width]; lens : int32 [B], the new token counted, cut to
  *           width * page;

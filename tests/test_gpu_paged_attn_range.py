@@ -1,5 +1,5 @@
-"""What paged attention keeps over the range of its weights: rows far below a
-dominant one.
+"""What paged attention keeps over the range of its weights and of its cache's
+values: rows far below a dominant one, infinities in the cache.
 
 Weights.  A binary16 or e4m3 cache takes a weight, relative to the largest so
 far, as two binary16 parts of its 2^15-fold: 2^-22 of itself, and 2^-40 (half a
@@ -66,3 +66,61 @@ def test_rows_far_below_a_dominant_one_count(lens, dtype, D, gap):
         assert np.all(off <= tol), (b, float((off / np.maximum(tol, 1e-300)).max()), float((off / A).max()))
         want_lse = m + np.log(total)
         assert np.all(np.abs(lse[b] - want_lse) <= e_s + 2 * tiles * 2.0 ** -24 + 2.0 ** -22 * (1 + np.abs(want_lse)))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+@pytest.mark.parametrize("at", [0, 37, 599])
+def test_scores_of_minus_infinity_weigh_nothing(D, dtype, at):
+    """A key that overflowed to an infinity: where it makes a score -infinity the row weighs nothing, whatever the
+    parts of q are (zeros, of either sign); where it makes one +infinity the head is NaN."""
+    c = Case(D, [600, 40, 1], 8, 2, D, dtype, 16)
+    page, row = int(c.table[0, at // 16]), at % 16
+    c.q[0, 4:, 7] = torch.tensor([-1.0, -1.3, -0.7123, 0.01])
+    c.k[page, 1, row, 7] = float("inf")
+    c.k[page, 0, row, 9] = float("-inf")
+    c.q[0, :4, 9] = torch.tensor([1.0, 1.3, 3.1e-5, 0.7123])
+    one = int(c.table[2, 0])
+    c.k[one, 1, 0, 5] = float("-inf")
+    c.q[2, 4:, 5] = 1.0
+    keys = c.k.clone()
+    out, lse = c.run()
+    assert out[0, 7].isnan().all() and lse[0, 7].isnan()
+    # a sequence whose only score is -infinity has nothing to see
+    assert torch.all(out[2, 4:] == 0) and torch.all(torch.isneginf(lse[2, 4:]))
+    # the others: as if the row were not there
+    keep = torch.ones(8, dtype=torch.bool)
+    keep[7] = False
+    c.k[page, :, row] = 0
+    c.k[one, 1, 0, 5] = 0
+    s, v, S = heads64(c, 0)
+    rows = np.arange(600) != at
+    s, v, S = s[rows], v[rows], S[rows]
+    m = s.max(0)
+    p = np.exp(s - m)
+    want = np.einsum("th,thd->hd", p, v) / p.sum(0)[:, None]
+    A = np.einsum("th,thd->hd", p, np.abs(v)) / p.sum(0)[:, None]
+    K = c.scale * np.abs(c.q[0].cpu().numpy()).max(-1) * np.abs(c.rows(0)[0]).sum(-1).max()
+    e_s = (D / 32 + 8) * 2.0 ** -22 * S.max(0) + 2.0 ** -22 * K + 2.0 ** -21 * (1 + np.abs(s).max(0))
+    tol = (2 * e_s + 2.0 ** -21 + 2 * 20 * 2.0 ** -22)[:, None] * A + 2.0 ** -23 * np.abs(want)
+    off = np.abs(out[0].cpu().numpy() - want)
+    assert np.all(off[keep.numpy()] <= tol[keep.numpy()]), float((off / tol)[keep.numpy()].max())
+    want_lse = (m + np.log(p.sum(0)))[keep.numpy()]
+    assert np.all(np.abs(lse[0].cpu().numpy()[keep.numpy()] - want_lse) <= e_s.max() + 2.0 ** -20 * (1 + np.abs(want_lse)))
+    # the sequence between them saw none of it
+    c.k.copy_(keys)
+    again, again_lse = c.run()
+    assert torch.equal(again[1], out[1]) and not out[1].isnan().any()
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("dtype", [F16, BF16])
+def test_an_infinite_value_spoils_its_column_only(D, dtype):
+    c = Case(D + 1, [600, 40], 8, 2, D, dtype, 16)
+    want, want_lse = c.run()
+    page = int(c.table[0, 3])
+    c.v[page, 1, 5, 11] = float("inf")
+    out, lse = c.run()
+    assert not out[0, 4:, 11].isfinite().any()
+    out[0, 4:, 11] = want[0, 4:, 11]
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
