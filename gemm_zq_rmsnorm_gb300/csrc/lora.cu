@@ -6,13 +6,13 @@
 // Two kernels, one after the other: h_t = A_a x_t split over K, then the
 // expansion of h by B_a onto base.  Bound: HBM, the adapters once, and base and
 // y (8 B N bytes); a few tokens are launch bound.  Measured in a graph: one token,
-// 1024 -> 2048, 5.9 us; 56 tokens of 12 adapters, 5120 -> 17408, R = 16, bf16:
-// 11.5 us (16.7 MB: 2.5 us at the copy rate; two launches in a row and their chains of
+// 1024 -> 2048, 7.0 us; 56 tokens of 12 adapters, 5120 -> 17408, R = 16, bf16:
+// 12.0 us (16.7 MB: 2.5 us at the copy rate; two launches in a row and their chains of
 // dependent loads are the rest); 512 tokens of 4 adapters, 17408 -> 5120, R = 64,
-// f16: 25.7 us (42 MB, 6.2 us; the first kernel's two thirds are 54 MB of 32- and 64-byte
+// f16: 25.3 us (42 MB, 6.2 us; the first kernel's two thirds are 54 MB of 32- and 64-byte
 // pieces from L2, as each 32 tokens read their adapter again, at 6.7 TB/s, and a
-// second turn where a tile has three units); 4096 tokens, 5120 -> 17408, R = 16:
-// 126 us, 4.9 TB/s.
+// second turn where a tile has three units); 4096 tokens of 4 adapters in runs,
+// 5120 -> 17408, R = 16, bf16: 113.5 us, 5.2 TB/s.
 //
 // Tokens come in tiles of 64.  A CTA sorts its tile's tokens by adapter itself
 // (64 ids: a scan of comparisons) and takes them sixteen at a time as the rows of
@@ -352,14 +352,17 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
     const int tid = threadIdx.x, warp = __shfl_sync(kAll, tid >> 5, 0), lane = tid & 31, g = lane >> 2, c = lane & 3;
     const size_t tok0 = (size_t)blockIdx.x * kTokens;
     const int block0 = blockIdx.y * a.blocks, blocks = min(a.blocks, (a.N + kBlock - 1) / kBlock - block0);
-    // The first kernel lets this one start only when all before it is complete:
-    // ids, base and weights may be read ahead of the wait, h may not.
+    // ids, base and h are outputs of kernels before this one, and their grouping chooses the weights: nothing is read
+    // ahead of the wait.  (The first kernel lets this one start only when all before it is complete, but a grid sees
+    // their writes only after a wait of its own.  Read ahead, ids and base saved 1.1 us of one token's call, 0.4
+    // of 56 tokens', nothing of 512.)
     if (tid < kTokens) {
         from_s[tid] = a.base + (a.base ? (tok0 + tid) * a.base_stride : 0);
         to_s[tid] = a.y + (tok0 + tid) * a.y_stride;
     }
+    pdl_wait();
+    pdl_launch_dependents();
     tile_open(tile, a, blockIdx.x);
-    bool waited = false;
 
     // The columns of MMA (p, i) are outputs 16 p + 4 (col / 2) + 2 i + col % 2 of
     // the block, so that lane 4g + c ends with outputs 16 p + 4c .. 4c + 3.
@@ -450,11 +453,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
         step_far();
         Task even, odd;
         if (t0 < t1) fetch(g0 + group, col_of(block), true, even);
-        if (!waited) {
-            pdl_wait();
-            pdl_launch_dependents();
-            waited = true;
-        }
         // h of the groups' members: its parts in order, times the adapter's scale, as 16-bit parts in the
         // fragments' order; R / 4 neighbouring threads have a member, four values each
         constexpr int kAhead = 4;
@@ -601,10 +599,6 @@ __global__ void __launch_bounds__(kThreads, 2) lora_up_kernel(const __grid_const
             if (task + 1 < t1) work(task + 2 < t1, odd, even);
         }
         __syncthreads();   // the fragments have been used
-    }
-    if (!waited) {
-        pdl_wait();
-        pdl_launch_dependents();
     }
     // tokens without an adapter
     if (a.base != a.y) {

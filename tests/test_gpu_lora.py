@@ -181,6 +181,50 @@ def test_beside_the_shared_projection():
         check(y, q8, A, Bm, scales, base, ids)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,R", [(1, 16), (8, 64), (56, 16)])
+def test_buffers_rewritten_by_the_kernels_before(B, R, in_place):
+    """Back to back in one graph, over and over on the same buffers: the codes, the projection's output and the ids
+    that a call reads are those of the kernels right before it, never of an earlier turn."""
+    K, N, n, turns = 1024, 1536, 5, 12
+    g = inputs.gamma(B, K)
+    W = [torch.from_numpy(inputs.q4k_weights(B + i, N, K)).cuda() for i in range(2)]
+    xs = [torch.from_numpy(inputs.activations(50 + i, B, K)).cuda() for i in range(turns)]
+    gam = torch.from_numpy(g).cuda()
+    _, A, Bm, scales, _, _ = make(19, B, K, N, R, n, BF16, [0] * B)
+    all_ids = [torch.tensor([(i + 3 * t) % (n + 1) - 1 for t in range(B)], dtype=torch.int32).cuda() for i in range(turns)]
+    q8, ids = zq.empty_q8_1(B, K), torch.zeros(B, dtype=torch.int32, device="cuda")
+    base, y = torch.zeros(B, N, device="cuda"), torch.zeros(B, N, device="cuda")
+    got = torch.zeros(turns, B, N, device="cuda")
+    ws = torch.empty(max(zq.lora_workspace_bytes(B, K, R), 256), dtype=torch.uint8, device="cuda")
+    gws = torch.empty(max(zq.gemm_workspace_bytes(N, K, B), 256), dtype=torch.uint8, device="cuda")
+
+    def turn(i, sync):
+        ids.copy_(all_ids[i])
+        zq.rmsnorm_q8_1(xs[i], gam, inputs.EPS, out=q8)
+        sync()
+        zq.q4k_gemm(W[i % 2], N, K, q8, B, y=base, workspace=gws)
+        sync()
+        to = base if in_place else y
+        zq.lora(q8, ids, A, Bm, scales, base=base, y=to, workspace=ws)
+        sync()
+        zq.lora(q8, ids, A, Bm, scales, base=to, y=got[i], workspace=ws)
+        sync()
+
+    for i in range(turns):
+        turn(i, torch.cuda.synchronize)
+    want = got.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for i in range(turns):
+            turn(i, lambda: None)
+    for _ in range(20):
+        got.fill_(7.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+
 def test_refusals():
     a, A, Bm, scales, base, ids = make(17, 4, 256, 64, 16, 2, F16, [0, 1, 0, 1])
     for bad in (dict(ids=ids.long()), dict(A=A.float()), dict(A=A.to(BF16)), dict(Bm=Bm[:, :, :8]), dict(ids=ids[:3]),
