@@ -486,10 +486,17 @@ def _stream_on(stream, index: int) -> int:
 
 
 def _new(shape, dtype, device, stream) -> torch.Tensor:
-    """A tensor for the call, which its memory outlives on the call's own stream."""
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """A tensor for a call on `stream` (None: the current one), from that
+    stream's own pool, so that it is no memory which work still queued on
+    another stream has only just given back; one for another stream than the
+    current one, where the caller goes on with it, outlives its use there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if current != stream:
+        t.record_stream(current)
     return t
 
 

@@ -104,6 +104,41 @@ def test_python_refusals_on_the_host():
         zq.rope_table([1.0, 2.0], [0], device="cpu")
 
 
+def test_tensors_of_a_call_come_from_its_streams_pool(monkeypatch):
+    """Memory that the current stream has just given back may still be in use there: what a call on another stream
+    allocates is of that stream's pool, and is kept until the current stream is done with it."""
+    torch = pytest.importorskip("torch")
+    log, active = [], ["current"]
+
+    class Use:
+        def __init__(self, stream):
+            self.stream = stream
+
+        def __enter__(self):
+            active.append(self.stream)
+
+        def __exit__(self, *_):
+            active.pop()
+
+    class Made:
+        def record_stream(self, stream):
+            log.append(("record", stream))
+
+    def empty(*args, **kw):
+        log.append(("empty", active[-1]))
+        return Made()
+
+    monkeypatch.setattr(torch.cuda, "stream", Use)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: active[-1])
+    monkeypatch.setattr(torch, "empty", empty)
+    zq._new((4,), torch.float32, "cuda:0", "other")
+    assert log == [("empty", "other"), ("record", "current")]
+    del log[:]
+    zq._new((4,), torch.float32, "cuda:0", "current")
+    zq._new((4,), torch.float32, "cuda:0", None)
+    assert log == [("empty", "current"), ("empty", "current")]
+
+
 def attn(lib, q=A16, qs=512, B=3, Hq=4, table=A16, width=2, lens=A16, scale=0.1, window=0, out=A16 + 4096, os=512,
          lse=A16, q8=None, ws=A16, wsb=1 << 30, c=None):
     return lib.zq_paged_attn(q, qs, B, Hq, cache() if c is None else c, table, width, lens, scale, window, out, os, lse,

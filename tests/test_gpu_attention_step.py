@@ -162,3 +162,45 @@ def test_tensors_off_the_current_device_are_refused(monkeypatch):
     torch.cuda.synchronize()
     for now, then in zip((layer.k.view(torch.int16), layer.q, layer.y), was):
         assert torch.equal(now, then)
+
+
+@pytest.mark.parametrize("op", ["norm", "attn", "lora"])
+def test_outputs_and_workspaces_made_for_another_stream(op):
+    """Work queued on the current stream goes on with tensors that Python has dropped already; a call on another
+    stream, which allocates as much, leaves them alone, and its own result outlives the call."""
+    layer = Layer(4, torch.bfloat16)
+    layer.give(0)
+    layer.step()
+    q, k, v = layer.qkv.split((HQ * D, HK * D, HK * D), 1)
+    call = {"norm": lambda s: zq.head_norm_rope(q, k, v, layer.gq, layer.gk, 1e-6, layer.rope, layer.pos, layer.cache,
+                                                layer.slots, stream=s),
+            "attn": lambda s: zq.paged_attn(layer.q, layer.cache, layer.table, layer.lens, stream=s),
+            "lora": lambda s: zq.lora(layer.q8x, layer.ids, *layer.lora_qkv, layer.scales, base=layer.base, stream=s)}[op]
+    want = call(None).clone()
+    sizes = {want.numel() * 4, zq.paged_attn_workspace_bytes(HQ, HK, D), zq.lora_workspace_bytes(4, K, R)}
+    other = torch.cuda.Stream()
+    big = torch.randn(4096, 4096, device="cuda")
+    for turn in range(3):
+        # queued on the current stream: long products, then sums over temporaries of the call's sizes
+        torch.cuda.synchronize()
+        x = big
+        for _ in range(20):
+            x = torch.mm(x, big) * (1 / 64)
+        sums = []
+        for n in sizes:
+            for _ in range(4):
+                t = torch.full((n,), 1, dtype=torch.uint8, device="cuda")
+                y = t + (x[0, 0] > 1e30).to(torch.uint8)     # waits for the products
+                sums.append((n, (t.sum(dtype=torch.int64), y.sum(dtype=torch.int64))))
+                del t, y
+        got = call(other)
+        back = torch.cuda.Event()
+        back.record(other)
+        torch.cuda.current_stream().wait_event(back)
+        kept = got.clone()
+        del got
+        again = call(other)      # may not take what the current stream still copies
+        torch.cuda.synchronize()
+        assert torch.equal(kept, want) and torch.equal(again, want)
+        for n, parts in sums:
+            assert all(int(p) == n for p in parts)
