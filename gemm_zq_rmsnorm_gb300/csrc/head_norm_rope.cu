@@ -10,9 +10,10 @@
 // computed once per warp and used for all of its rows.
 //
 // The angle: table entry x position modulo 2^64 is the phase in turns (the
-// integer product wraps exactly where the angle does), its top 32 bits as a
-// signed fraction give sincospi an argument in [-1, 1): no range reduction
-// and no fp64, which is slow on this GPU.
+// integer product wraps exactly where the angle does, and is right to 2^-32 turns),
+// its top 32 bits as a signed fraction, rounded to fp32 (2^-26 turns at most), give
+// sincospi an argument in [-1, 1]: no range reduction and no fp64, which is slow
+// on this GPU.
 //
 // HBM bound for long prompts: 4 D (2 Hq + 2 Hk) + 2 es D Hk bytes per token;
 // launch bound for a few tokens.  Measured in a graph: 4096 tokens of 48 + 8 + 8

@@ -702,6 +702,37 @@ int check_cache(const zq_kv_cache *c, const char *name)
     return ZQ_OK;
 }
 
+// The binary digits of 1 / (2 pi) (Machin's formula in whole numbers), enough for the largest finite double.
+constexpr uint64_t kInverseTwoPi[] = {
+    0x28be60db9391054au, 0x7f09d5f47d4d3770u, 0x36d8a5664f10e410u,
+    0x7f9458eaf7aef158u, 0x6dc91b8e909374b8u, 0x01924bba82746487u,
+    0x3f877ac72c4a69cfu, 0xba208d7d4baed121u, 0x3a671c09ad17df90u,
+    0x4e64758e60d4ce7du, 0x272117e2ef7e4a0eu, 0xc7fe25fff7816603u,
+    0xfbcbc462d6829b47u, 0xdb4d9fb3c9f2c26du, 0xd3d18fd9a797fa8bu,
+    0x5d49eeb1faf97c5eu, 0xcf41ce7de294a4bau, 0x9afed7ec47e35742u,
+    0x1580cc11bf1edaeau};
+
+// 64 of those digits after the first `at`; ahead of the point they are zeros.
+uint64_t digits(int at)
+{
+    if (at <= -64) return 0;
+    if (at < 0) return kInverseTwoPi[0] >> -at;
+    const uint64_t *w = kInverseTwoPi + at / 64;
+    return at % 64 ? w[0] << at % 64 | w[1] >> (64 - at % 64) : w[0];
+}
+
+// |x| / (2 pi) modulo 1, rounded down to a multiple of 2^-64.  (A quotient of doubles is off by 2^-53 of itself: at
+// position 2^31 by 2^-25 turns for x = 1, by 2^-21 for 100.)  |x| is m 2^at with a whole m of 53 bits, so the digits
+// that make whole turns of the product drop out before it is formed (the reduction published by Payne and Hanek).
+uint64_t turns64(double x)
+{
+    int e;
+    const uint64_t m = (uint64_t)std::ldexp(std::frexp(std::fabs(x), &e), 53);
+    const int at = e - 53;
+    const unsigned __int128 low = (unsigned __int128)m * digits(at + 128) >> 64;
+    return m * digits(at) + (uint64_t)(((unsigned __int128)m * digits(at + 64) + low) >> 64);
+}
+
 // One of the strided fp32 row blocks of the attention-side calls.
 int check_rows(const float *p, long long stride, long long width, const char *name, const char *what)
 {
@@ -724,10 +755,8 @@ int zq_rope_table(const double *inv_freq, const int *axis, int n, uint64_t *tabl
         if (!std::isfinite(inv_freq[i])) return fail(ZQ_ERR_ARG, "zq_rope_table: inv_freq[%d] is not finite", i);
         const int ax = axis ? axis[i] : 0;
         if (ax < 0 || ax > 2) return fail(ZQ_ERR_ARG, "zq_rope_table: axis[%d] = %d must be 0, 1 or 2", i, ax);
-        double turns = inv_freq[i] / 6.283185307179586477;
-        turns -= std::floor(turns);   // in [0, 1]
-        const uint64_t step = turns < 1.0 ? (uint64_t)std::ldexp(turns, 64) : 0;
-        table[i] = ((step + 2) & ~(uint64_t)3) | (uint64_t)ax;   // rounded to a multiple of four
+        const uint64_t step = (turns64(inv_freq[i]) + 2) & ~(uint64_t)3;   // rounded to a multiple of four
+        table[i] = (inv_freq[i] < 0.0 ? 0 - step : step) | (uint64_t)ax;
     }
     return ZQ_OK;
 }

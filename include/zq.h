@@ -483,10 +483,12 @@ typedef struct zq_kv_cache {
 
 /*
  * Entries of a rotation table: for each of n pairs the phase step
- * inv_freq / (2 pi) as a fraction of 2^64 turns (times a position, modulo
- * 2^64, it is the angle, to 2^-31 turns at any 32-bit position), its two low
- * bits replaced by the position axis the pair follows.  Host arrays;
- * inv_freq finite; axis 0..2, or NULL for axis 0.
+ * inv_freq / (2 pi) modulo 1 in units of 2^-64 turns, to the nearest multiple
+ * of four, its two low bits replaced by the position axis the pair follows.
+ * Times a position, modulo 2^64, it is the angle, to 2^-32 turns at any 32-bit
+ * position; the kernel takes it to 2^-25.9 turns (1e-7 radians).  Host
+ * arrays; inv_freq any finite doubles (of -f the entry of f, negated); axis
+ * 0..2, or NULL for axis 0.
  */
 ZQ_API int zq_rope_table(const double *inv_freq, const int *axis, int n, uint64_t *table);
 

@@ -80,6 +80,39 @@ def test_rope_table_values(lib):
         assert abs(off) <= 2 ** 64 * 2.0 ** -52 * max(1.0, abs(f) / (2 * math.pi))
 
 
+def inverse_two_pi(bits):
+    """floor(2^bits / (2 pi)), by Machin's formula."""
+    one = 1 << bits + 64
+
+    def atan_inverse(n):
+        total, power, k = one // n, one // n, 1
+        while power:
+            power //= -n * n
+            k += 2
+            total += power // k
+        return total
+    return (1 << 2 * bits + 64) // (8 * (4 * atan_inverse(5) - atan_inverse(239)))
+
+
+def test_rope_table_is_exact(lib):
+    """The nearest multiple of four of the exact quotient's 2^-64 turns, for frequencies of any size: at position 2^31
+    the angle is right to 2^-32 turns.  A negative frequency has the negated entry."""
+    g = np.random.default_rng(0)
+    freq = np.concatenate([1e6 ** -(np.arange(64) / 64), [1.0, 100.0, 2 * math.pi, math.nextafter(2 * math.pi, 9), 6e9, 1e22,
+                           2.0 ** 53, 2.0 ** -60, 1e-19, 5e-324, 1.7976931348623157e308, 0.0], 2.0 ** g.uniform(-70, 1024, 300)])
+    freq = np.concatenate([freq, -freq])
+    out = np.zeros(len(freq), np.uint64)
+    assert lib.zq_rope_table(freq.ctypes.data, None, len(freq), out.ctypes.data) == 0
+    bits = 2400
+    inverse = inverse_two_pi(bits)
+    for f, e in zip(freq, out):
+        num, den = abs(float(f)).as_integer_ratio()
+        turns = (num * inverse << 64) // den            # in 2^-64 turns, with `bits` more
+        off = (int(e) * (1 if f >= 0 else -1) << bits) - turns
+        off = (off + (1 << bits + 63)) % (1 << bits + 64) - (1 << bits + 63)
+        assert int(e) % 4 == 0 and abs(off) <= 2 << bits, (f, off >> bits)
+
+
 def test_rope_table_refuses(lib):
     out = np.zeros(2, np.uint64)
     f = np.array([1.0, 1.0])

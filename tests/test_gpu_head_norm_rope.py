@@ -215,3 +215,30 @@ def test_captured_and_replayed_on_another_stream():
     graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(out, -want)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_angles_at_the_farthest_positions(interleaved):
+    """Frequencies up to a hundred radians a position at positions of any size, against the exact angle: 2^-25.9 turns of
+    the table and its fp32 argument (2^-23.2 radians), 2^-22 of sine and cosine, three roundings, of a pair's norm."""
+    from test_attention_abi_cpu import inverse_two_pi
+    T, D = 12, 64
+    pos = np.array([0, 1, -1, 2 ** 31 - 1, -2 ** 31, 2 ** 31 - 12345, 123456789, 2 ** 24 + 1, 10 ** 9, 777, -10 ** 6,
+                    2 ** 30 + 1], np.int32)
+    freq = np.concatenate([[1.0, 100.0, -1.0, -100.0, 6.3], 100.0 ** -(np.arange(27) / 27)])
+    qkv, k, v, slots, _, _, _ = make(19, T, 1, 1, D, F16, 16)
+    qr, kr, vr = parts(qkv, 1, 1, D)
+    out = zq.head_norm_rope(qr, kr, vr, None, None, EPS, zq.rope_table(freq), torch.from_numpy(pos).cuda(),
+                            zq.KVCache(k, v), slots, interleaved=interleaved)
+    torch.cuda.synchronize()
+    got, x = as64(out), qkv.cpu().numpy().astype(np.float64)[:, :D]
+    inverse = inverse_two_pi(256)
+    for p, f in enumerate(freq):
+        i, j = (2 * p, 2 * p + 1) if interleaved else (p, p + D // 2)
+        num, den = float(f).as_integer_ratio()
+        turns = [((num * int(t) * inverse // den) % (1 << 256)) / 2.0 ** 256 for t in pos]
+        c, s = np.cos(2 * np.pi * np.array(turns)), np.sin(2 * np.pi * np.array(turns))
+        norm = np.hypot(x[:, i], x[:, j])
+        tol = (2.0 ** -23.2 + 2.0 ** -22 + 3 * 2.0 ** -24) * norm
+        assert np.all(np.abs(got[:, i] - (x[:, i] * c - x[:, j] * s)) <= tol), f
+        assert np.all(np.abs(got[:, j] - (x[:, j] * c + x[:, i] * s)) <= tol), f
