@@ -519,6 +519,13 @@ def _ints(t: torch.Tensor, n: int, what: str) -> int:
     return t.data_ptr()
 
 
+def _space(t: torch.Tensor, what: str):
+    """(address, bytes) of a workspace, one piece of memory."""
+    if not t.is_contiguous():
+        raise ValueError(f"{what}: the workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _q8_planes(a: Q8_1, B: int, K: int, what: str):
     """The planes of B tokens x K codes, contiguous."""
     if not (a.qs.dtype == torch.int8 and a.d.dtype == a.s.dtype == torch.float16 and a.qs.numel() == B * K
@@ -615,8 +622,8 @@ def paged_attn(q: torch.Tensor, cache: KVCache, table: torch.Tensor, lens: torch
     status = lib.zq_paged_attn(qp, qs, B, Hq, cache._ref, _ints(table, B * width, "paged_attn: table"), width,
                                _ints(lens, B, "paged_attn: lens"), D ** -0.5 if scale is None else scale, window,
                                op, os_,
-                               None if lse is None else lse.data_ptr(), q8, workspace.data_ptr(),
-                               workspace.numel() * workspace.element_size(), _stream_on(stream, cache.index))
+                               None if lse is None else lse.data_ptr(), q8, *_space(workspace, "paged_attn"),
+                               _stream_on(stream, cache.index))
     if status:
         _check(status)
     return out
@@ -663,8 +670,8 @@ def lora(a: Q8_1, ids: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, scales: 
     if scales is not None and (scales.dtype != torch.float32 or scales.numel() != n or not scales.is_contiguous()):
         raise ValueError(f"lora: scales must be {n} contiguous fp32 values")
     status = lib.zq_lora(a._c(), B, K, _ints(ids, B, "lora: ids"), n, A.data_ptr(), Bm.data_ptr(), R, _TYPES[A.dtype],
-                         None if scales is None else scales.data_ptr(), N, bp, bs, yp, ys, workspace.data_ptr(),
-                         workspace.numel() * workspace.element_size(), _stream_on(stream, dev.index))
+                         None if scales is None else scales.data_ptr(), N, bp, bs, yp, ys, *_space(workspace, "lora"),
+                         _stream_on(stream, dev.index))
     if status:
         _check(status)
     return y

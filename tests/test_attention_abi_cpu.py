@@ -172,6 +172,16 @@ def test_tensors_of_a_call_come_from_its_streams_pool(monkeypatch):
     assert log == [("empty", "current"), ("empty", "current")]
 
 
+def test_workspaces_are_one_piece_of_memory():
+    """A tensor whose elements share memory, or lie apart, has not the bytes that its size says."""
+    torch = pytest.importorskip("torch")
+    t = torch.zeros(64, dtype=torch.float32)
+    assert zq._space(t, "x") == (t.data_ptr(), 256)
+    for bad in (torch.zeros(1, dtype=torch.uint8).expand(1 << 20), t[::2], t.view(8, 8).t()):
+        with pytest.raises(ValueError):
+            zq._space(bad, "x")
+
+
 def attn(lib, q=A16, qs=512, B=3, Hq=4, table=A16, width=2, lens=A16, scale=0.1, window=0, out=A16 + 4096, os=512,
          lse=A16, q8=None, ws=A16, wsb=1 << 30, c=None):
     return lib.zq_paged_attn(q, qs, B, Hq, cache() if c is None else c, table, width, lens, scale, window, out, os, lse,

@@ -204,3 +204,15 @@ def test_outputs_and_workspaces_made_for_another_stream(op):
         assert torch.equal(kept, want) and torch.equal(again, want)
         for n, parts in sums:
             assert all(int(p) == n for p in parts)
+
+
+def test_workspaces_that_are_not_one_piece_are_refused():
+    layer = Layer(1, torch.float16)
+    layer.give(0)
+    layer.step()
+    bad = torch.zeros(1, dtype=torch.uint8, device="cuda").expand(1 << 26)
+    with pytest.raises(ValueError, match="contiguous"):
+        zq.paged_attn(layer.q, layer.cache, layer.table, layer.lens, workspace=bad)
+    with pytest.raises(ValueError, match="contiguous"):
+        zq.lora(layer.q8x, layer.ids, *layer.lora_qkv, layer.scales, base=layer.base, workspace=bad)
+    torch.cuda.synchronize()
