@@ -3,6 +3,8 @@ input to the o projection's output: RMSNorm + stacked q/k/v projection,
 adapters on it in place, head norms + rotation + cache write, paged attention
 straight to Q8_1 codes, o projection and its adapters; step by step against
 64 bits, captured and replayed token after token."""
+import threading
+
 import numpy as np
 import pytest
 
@@ -216,3 +218,37 @@ def test_workspaces_that_are_not_one_piece_are_refused():
     with pytest.raises(ValueError, match="contiguous"):
         zq.lora(layer.q8x, layer.ids, *layer.lora_qkv, layer.scales, base=layer.base, workspace=bad)
     torch.cuda.synchronize()
+
+
+def test_a_threads_first_call():
+    """Each call as the first thing that a thread does on the GPU, after other threads have made the call."""
+    layer = Layer(3, torch.float16)
+    layer.give(0)
+    layer.step()
+    torch.cuda.synchronize()
+    want = [t.clone() for t in (layer.q8x.qs, layer.base, layer.qkv, layer.q, layer.o, layer.y0)]
+    q, k, v = layer.qkv.split((HQ * D, HK * D, HK * D), 1)
+    calls = [lambda: zq.rmsnorm_q8_1(layer.x, layer.g, inputs.EPS, out=layer.q8x),
+             lambda: zq.q4k_gemm(layer.W[0], NQKV, K, layer.q8x, 3, y=layer.base, workspace=layer.ws[0]),
+             lambda: zq.lora(layer.q8x, layer.ids, *layer.lora_qkv, layer.scales, base=layer.base, y=layer.qkv,
+                             workspace=layer.ws[1]),
+             lambda: zq.head_norm_rope(q, k, v, layer.gq, layer.gk, 1e-6, layer.rope, layer.pos, layer.cache, layer.slots,
+                                       q_out=layer.q),
+             lambda: zq.paged_attn(layer.q, layer.cache, layer.table, layer.lens, out=layer.o, workspace=layer.ws[2]),
+             lambda: zq.q4k_gemm(layer.W[1], K, HQ * D, layer.q8o, 3, y=layer.y0, workspace=layer.ws[3])]
+    failed = []
+
+    def work(call):
+        try:
+            call()
+        except Exception as e:   # noqa: BLE001 -- handed to the test
+            failed.append(e)
+
+    for call in calls:
+        t = threading.Thread(target=work, args=(call,))
+        t.start()
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed
+    for a, b in zip((layer.q8x.qs, layer.base, layer.qkv, layer.q, layer.o, layer.y0), want):
+        assert torch.equal(a, b)
