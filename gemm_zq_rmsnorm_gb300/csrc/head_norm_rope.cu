@@ -21,6 +21,8 @@
 // 777 tokens of 24 + 4 + 4 heads of 256 to an e4m3 cache 11.1 us, 4.2 TB/s (one
 // round of warps, whose 8 values a lane make the instructions count); 61 tokens
 // 3.4 us, one token 2.3 us.
+#include <atomic>
+
 #include "zq_async.cuh"
 #include "zq_internal.cuh"
 #include "zq_kv.cuh"
@@ -225,13 +227,14 @@ __global__ void __launch_bounds__(kThreads) head_norm_rope_kernel(const __grid_c
 template <int D, int TYPE, bool INTER>
 cudaError_t launch_kernel(const HeadNormRopeArgs &args, cudaStream_t st)
 {
-    static int per_sm;   // CTAs that an SM holds, the same on every device of the architecture
+    static std::atomic<int> held;   // CTAs that an SM holds, the same on every device of the architecture
     auto *kernel = head_norm_rope_kernel<D, TYPE, INTER>;
+    int per_sm = held.load(std::memory_order_relaxed);
     if (!per_sm) {
-        int n = 0;
-        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0);
+        const cudaError_t e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0);
         if (e != cudaSuccess) return e;
-        per_sm = n > 0 ? n : 1;
+        if (per_sm < 1) per_sm = 1;
+        held.store(per_sm, std::memory_order_relaxed);
     }
     HeadNormRopeArgs a = args;
     const long long rows = a.Hq + 2LL * a.Hk, sms = num_sms();

@@ -61,6 +61,8 @@
 #include <float.h>
 #include <math.h>
 
+#include <atomic>
+
 #include "zq_async.cuh"
 #include "zq_internal.cuh"
 #include "zq_kv.cuh"
@@ -1132,15 +1134,15 @@ template <int D, int TYPE>
 cudaError_t launch_one(const PagedAttnArgs &a, int ctas, cudaStream_t st)
 {
     using C = Cfg<D, TYPE>;
-    static bool set[64];
+    static std::atomic<bool> set[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!set[dev]) {
+    if (!set[dev].load(std::memory_order_acquire)) {
         e = cudaFuncSetAttribute(paged_attn_kernel<D, TYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
         if (e != cudaSuccess) return e;
-        set[dev] = true;
+        set[dev].store(true, std::memory_order_release);
     }
     // [page][key head][segment][row][bytes of a segment]; a box is all segments of 16 or 32 rows
     const uint64_t page = (uint64_t)1 << a.page_shift;

@@ -10,6 +10,8 @@
 // product with a weight code sc * q4 is exact.
 #include <cuda.h>
 
+#include <atomic>
+
 #include "zq_internal.cuh"
 #include "zq_q8_1_pack.cuh"
 #include "zq_tc.cuh"
@@ -143,14 +145,17 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
 
 EncodeTiledFn encode_fn()
 {
-    static EncodeTiledFn fn = nullptr;
+    static std::atomic<EncodeTiledFn> found;
+    EncodeTiledFn fn = found.load(std::memory_order_relaxed);
     if (!fn) {
         void *ptr = nullptr;
         cudaDriverEntryPointQueryResult q;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &ptr, 12000, cudaEnableDefault, &q) ==
                 cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
+            q == cudaDriverEntryPointSuccess) {
             fn = reinterpret_cast<EncodeTiledFn>(ptr);
+            found.store(fn, std::memory_order_relaxed);
+        }
     }
     return fn;
 }

@@ -252,3 +252,35 @@ def test_a_threads_first_call():
     assert not failed
     for a, b in zip((layer.q8x.qs, layer.base, layer.qkv, layer.q, layer.o, layer.y0), want):
         assert torch.equal(a, b)
+
+
+def test_threads_with_streams_of_their_own():
+    """Calls from several threads at once, the first ones of their types and widths among them."""
+    layers = [Layer(3, dtype) for dtype in (torch.float16, torch.bfloat16) * 2]
+    for layer in layers:
+        layer.give(0)
+    torch.cuda.synchronize()
+    failed, gate = [], threading.Barrier(len(layers))
+
+    def work(layer):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                gate.wait(30)
+                for _ in range(20):
+                    layer.step()
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:   # noqa: BLE001 -- handed to the test
+            failed.append(e)
+
+    threads = [threading.Thread(target=work, args=(layer,)) for layer in layers]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for layer in layers:
+        got = layer.y.clone(), layer.o.clone(), layer.k.view(torch.int16).clone()
+        layer.step()
+        torch.cuda.synchronize()
+        assert zq.device_status() == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, (layer.y, layer.o, layer.k.view(torch.int16))))
