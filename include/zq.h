@@ -528,8 +528,11 @@ ZQ_API int zq_head_norm_rope(const float *q, long long q_stride, const float *k,
  * key head h / (Hq / Hk).  Row j is row j % page of page
  * table[b * width + j / page].  A row on a page outside the cache is left out
  * as if masked; a sequence without rows (n <= 0, or all left out) has out = 0
- * and lse = -infinity.  Nothing outside the rows is read, whatever it
- * holds; table entries past a sequence's last page may hold anything.
+ * and lse = -infinity.  Other rows of the sequence's pages may be read (tiles
+ * of 32 rows are), but change nothing whatever they hold, or while they are
+ * written.  No other page is read, and the table's entries past a sequence's
+ * last page, and those of pages that end before the tile in which its window
+ * begins, may hold anything.
  * Infinities of the cache's rows (f16 and bf16): a score of -infinity weighs
  * nothing (a head with no other has out = 0 and lse = -infinity), one of
  * +infinity, or a NaN, makes its head NaN; an infinite or NaN value makes its
