@@ -18,9 +18,10 @@
 // HBM bound for long prompts: 4 D (2 Hq + 2 Hk) + 2 es D Hk bytes per token;
 // launch bound for a few tokens.  Measured in a graph: 4096 tokens of 48 + 8 + 8
 // heads of 128 to an f16 cache 43.0 us, 5.9 TB/s (0.86 of the measured copy rate);
-// 777 tokens of 24 + 4 + 4 heads of 256 to an e4m3 cache 11.1 us, 4.2 TB/s (one
-// round of warps, whose 8 values a lane make the instructions count); 61 tokens
-// 3.4 us, one token 2.3 us.
+// 777 tokens of 24 + 4 + 4 heads of 256 to an e4m3 cache 11.0 us, 4.2 TB/s (latency:
+// one round of 19 warps an SM with two rows each on their way are 38 KB, less than
+// the copy rate wants, between a warp's start and end; issue slots 39 % busy);
+// 61 tokens 3.3 us, one token 2.5 us.
 #include <atomic>
 
 #include "zq_async.cuh"

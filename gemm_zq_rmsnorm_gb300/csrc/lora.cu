@@ -12,7 +12,7 @@
 // f16: 25.3 us (42 MB, 6.2 us; the first kernel's two thirds are 54 MB of 32- and 64-byte
 // pieces from L2, as each 32 tokens read their adapter again, at 6.7 TB/s, and a
 // second turn where a tile has three units); 4096 tokens of 4 adapters in runs,
-// 5120 -> 17408, R = 16, bf16: 113.5 us, 5.2 TB/s.
+// 5120 -> 17408, R = 16, bf16: 113 to 117 us, 5.2 TB/s.
 //
 // Tokens come in tiles of 64.  A CTA sorts its tile's tokens by adapter itself
 // (64 ids: a scan of comparisons) and takes them sixteen at a time as the rows of

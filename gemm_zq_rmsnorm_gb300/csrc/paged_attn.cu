@@ -17,13 +17,16 @@
 // most, and the warp-level form needs no hand-over between warps.)
 // Measured, kernel pairs in a graph: 48 sequences of 1 to 12000 rows, 48 query
 // and 8 key heads of 128, bf16: 127 us, 5.9 TB/s (0.88 of the measured copy
-// rate); one sequence of 131071, 24 and 4 heads of 256, bf16: 94 us, 5.7 TB/s; 64
-// sequences of 8000 to 24000, e4m3: 284 to 288 us, 6.1 TB/s.  What is left of the
+// rate); one sequence of 131071, 24 and 4 heads of 256, bf16: 95 us, 5.7 TB/s; 64
+// sequences of 8000 to 24000, e4m3: 285 to 289 us, 6.1 TB/s.  What is left of the
 // 16-bit cases is their end: the SMs of some GPCs get 10 % less of the bandwidth, and
-// the shares are equal.  200 windows of up to 1024 rows, 64-wide heads, e4m3: 40.5 us,
-// 3.5 TB/s, bound by the instructions of 4 KB tiles and of 1600 row blocks' ends.
-// One sequence of 1000: 9.7 us, a chain of latencies (lengths, table, keys, two
-// joins) over two launches.
+// the shares are equal.  200 windows of up to 1024 rows, 64-wide heads, e4m3: 40.7 us,
+// 3.5 TB/s: neither the issue slots (59 %) nor HBM are full, the chains of a 4 KB
+// tile and of 1600 row blocks' ends are the rest.
+// One sequence of 1000: 9.9 us, a chain of latencies (lengths, table, keys, two
+// joins) over two launches.  With Q8_1 codes written as well or alone: the same but for
+// the windows, 46.0 and 44.3 us.  Registers are spilled at 128-wide bf16 (104 bytes of
+// stores) and f16 (48), and at 256-wide (76 to 192).
 //
 // Work: every (sequence, key head) has ceil(len / 32) tiles of 32 tokens (at
 // least one, so that an empty row is written too); all tiles of the call form
