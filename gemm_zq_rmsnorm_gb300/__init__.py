@@ -33,7 +33,9 @@ EXPORTS = ("zq_rmsnorm_q8_1", "zq_q4k_gemv", "zq_q4k_gemv_pair", "zq_q4k_gemm",
            "zq_q5k_bytes", "zq_q6k_bytes", "zq_debug_stream_plan", "zq_debug_peak_probe",
            "zq_debug_wait_expiry", "zq_q8_1_dequant_f16", "zq_f16_gemm_workspace_bytes", "zq_f16_gemm",
            "zq_rmsnorm_q4k_gemm", "zq_copy", "zq_rope_table", "zq_head_norm_rope",
-           "zq_paged_attn_workspace_bytes", "zq_paged_attn", "zq_lora_workspace_bytes", "zq_lora")
+           "zq_paged_attn_workspace_bytes", "zq_paged_attn", "zq_lora_workspace_bytes", "zq_lora",
+           "zq_linear_attn_step", "zq_linear_attn_workspace_bytes", "zq_linear_attn", "zq_gated_norm_q8_1",
+           "zq_residual_norm_q8_1")
 
 
 class ZQError(RuntimeError):
@@ -46,6 +48,11 @@ class _Cache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("type", ctypes.c_int), ("pages", ctypes.c_int),
                 ("page", ctypes.c_int), ("Hk", ctypes.c_int), ("D", ctypes.c_int), ("k_scale", ctypes.c_float),
                 ("v_scale", ctypes.c_float)]
+
+
+class _LinearState(ctypes.Structure):
+    _fields_ = [("s", ctypes.c_void_p), ("n", ctypes.c_int), ("Hv", ctypes.c_int), ("Dk", ctypes.c_int),
+                ("Dv", ctypes.c_int)]
 
 
 class _Q8(ctypes.Structure):
@@ -105,6 +112,11 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "zq_paged_attn": ([P, ll, i, i, P, P, i, P, f, i, P, ll, P, P, P, sz, P], i),
         "zq_lora_workspace_bytes": ([i, i, i], sz),
         "zq_lora": ([_Q8, i, i, P, i, P, P, i, i, P, i, P, ll, P, ll, P, sz, P], i),
+        "zq_linear_attn_step": ([P, ll, P, ll, P, ll, i, i, P, ll, P, P, f, P, ll, P], i),
+        "zq_linear_attn_workspace_bytes": ([i, i, i, i, i], sz),
+        "zq_linear_attn": ([P, ll, P, ll, P, ll, i, i, i, P, ll, P, P, P, P, f, P, ll, P, sz, P], i),
+        "zq_gated_norm_q8_1": ([P, ll, i, i, i, P, f, P, ll, i, P, ll, P, P], i),
+        "zq_residual_norm_q8_1": ([P, ll, P, ll, i, i, P, P, ll, i, f, P, ll, P, f, P, ll, P, P], i),
         "zq_rmsnorm_q4k_gemm": ([P, P, f, i, i, P, i, P, ctypes.POINTER(_Q8), P, sz, P], i),
     }
     for name, (args, res) in sig.items():
@@ -675,6 +687,182 @@ def lora(a: Q8_1, ids: torch.Tensor, A: torch.Tensor, Bm: torch.Tensor, scales: 
     if status:
         _check(status)
     return y
+
+
+# ------------------------------------------------ recurrent mixer and block edges
+class LinearState:
+    """States of linear attention: fp32 [n][Hv][Dk][Dv] (zq_linear_state).  A
+    handle on the caller's tensor; make it once and keep it."""
+
+    __slots__ = ("s", "n", "Hv", "Dk", "Dv", "device", "index", "_c", "_ref")
+
+    def __init__(self, s: torch.Tensor):
+        if s.dim() != 4 or s.dtype != torch.float32 or not (s.is_cuda and s.is_contiguous()):
+            raise ValueError("LinearState: a contiguous fp32 CUDA tensor [n][Hv][Dk][Dv] is needed")
+        self.s = s
+        self.n, self.Hv, self.Dk, self.Dv = s.shape
+        self.device, self.index = s.device, s.device.index
+        self._c = _LinearState(s.data_ptr(), self.n, self.Hv, self.Dk, self.Dv)
+        self._ref = ctypes.byref(self._c)
+
+
+def _linear_rows(q, k, v, g, state: LinearState, out, what: str):
+    """(arguments q to v, Hk, arguments g, arguments out) of a linear attention call over T rows."""
+    T = q.shape[0]
+    qp, qs, Hk = _head_rows(q, T, state.Dk, f"{what}: q")
+    kp, ks, Hk2 = _head_rows(k, T, state.Dk, f"{what}: k")
+    vp, vs, Hv = _head_rows(v, T, state.Dv, f"{what}: v")
+    op, os_, Ho = _head_rows(out, T, state.Dv, f"{what}: out")
+    if Hk2 != Hk or Hv != state.Hv or Ho != Hv:
+        raise ValueError(f"{what}: the heads of k must be q's, those of v and out the state's")
+    gp, gs = None, 0
+    if g is not None:
+        if g.dtype != torch.float32 or g.shape != (T, Hv) or (Hv > 1 and g.stride(1) != 1):
+            raise ValueError(f"{what}: g must be fp32 [{T}][{Hv}]")
+        gp, gs = g.data_ptr(), g.stride(0) if T > 1 else Hv
+    return (qp, qs, kp, ks, vp, vs), Hk, (gp, gs), (op, os_)
+
+
+def linear_attn_step(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g, state: LinearState, slots: torch.Tensor,
+                     scale: float | None = None, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """One new token per sequence: S = exp(g) S + k v^T, out = scale S^T q, for
+    q, k [B][Hk][Dk], v [B][Hv][Dv] (or [B][heads * D], rows strided), g fp32
+    [B][Hv] or None, S the state of slots int32 [B], updated in place (see
+    zq_linear_attn_step); scale defaults to 1 / sqrt(Dk)."""
+    lib = _lib or load()
+    B = q.shape[0]
+    if out is None:
+        out = _new(v.shape, torch.float32, v.device, stream)
+    _on(state.index, "linear_attn_step", q, k, v, g, slots, out)
+    rows, Hk, gg, oo = _linear_rows(q, k, v, g, state, out, "linear_attn_step")
+    status = lib.zq_linear_attn_step(*rows, B, Hk, *gg, state._ref, _ints(slots, B, "linear_attn_step: slots"),
+                                     state.Dk ** -0.5 if scale is None else scale, *oo,
+                                     _stream_on(stream, state.index))
+    if status:
+        _check(status)
+    return out
+
+
+def linear_attn_workspace_bytes(T: int, B: int, Hv: int, Dk: int, Dv: int) -> int:
+    return int(load().zq_linear_attn_workspace_bytes(T, B, Hv, Dk, Dv))
+
+
+def linear_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g, starts: torch.Tensor, state: LinearState,
+                slots: torch.Tensor, fresh: torch.Tensor | None = None, scale: float | None = None,
+                out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """The same over prompts: the rows of sequence b are starts[b] .. starts[b +
+    1] - 1 (int32 [B + 1]) of the T rows; a sequence with fresh[b] != 0 starts
+    from zeros (see zq_linear_attn).  Rows of no sequence are not written."""
+    lib = _lib or load()
+    T, B = q.shape[0], slots.numel()
+    if out is None:
+        out = _new(v.shape, torch.float32, v.device, stream)
+    need = lib.zq_linear_attn_workspace_bytes(T, B, state.Hv, state.Dk, state.Dv)
+    if workspace is None and need:
+        workspace = _new(need, torch.uint8, v.device, stream)
+    _on(state.index, "linear_attn", q, k, v, g, starts, slots, fresh, out, workspace)
+    rows, Hk, gg, oo = _linear_rows(q, k, v, g, state, out, "linear_attn")
+    ws = (None, 0) if workspace is None else _space(workspace, "linear_attn")
+    status = lib.zq_linear_attn(*rows, T, B, Hk, *gg, _ints(starts, B + 1, "linear_attn: starts"), state._ref,
+                                _ints(slots, B, "linear_attn: slots"),
+                                None if fresh is None else _ints(fresh, B, "linear_attn: fresh"),
+                                state.Dk ** -0.5 if scale is None else scale, *oo, *ws,
+                                _stream_on(stream, state.index))
+    if status:
+        _check(status)
+    return out
+
+
+_ACTS = {"linear": 0, "sigmoid": 1, "silu": 2}   # ZQ_GATE_LINEAR, ZQ_GATE_SIGMOID, ZQ_GATE_SILU
+
+
+def _act_of(act: str, what: str) -> int:
+    if act not in _ACTS:
+        raise ValueError(f"{what}: act {act!r} is not one of {', '.join(_ACTS)}")
+    return _ACTS[act]
+
+
+def _weights(t, n: int, what: str):
+    if t is None:
+        return None
+    if t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{what} must be {n} contiguous fp32 values")
+    return t.data_ptr()
+
+
+def gated_norm_q8_1(x: torch.Tensor, gate, gamma, eps: float, D: int, act: str = "silu",
+                    out: torch.Tensor | None = None, q8_out: Q8_1 | None = None, stream=None):
+    """RMSNorm of every head of x [B][H][D] (or [B][H * D], rows strided) times
+    act(gate), to fp32 rows, Q8_1 codes, or both (see zq_gated_norm_q8_1);
+    returns out, or q8_out when only the codes are asked for.  gamma and gate
+    may be None."""
+    lib = _lib or load()
+    B = x.shape[0]
+    if not x.is_cuda:
+        raise ValueError("gated_norm_q8_1: CUDA tensors are needed")
+    if out is None and q8_out is None:
+        out = _new(x.shape, torch.float32, x.device, stream)
+    index = x.get_device()
+    _on(index, "gated_norm_q8_1", gate, gamma, out)
+    xp, xs, H = _head_rows(x, B, D, "gated_norm_q8_1: x")
+    gp, gs = None, 0
+    if gate is not None:
+        gp, gs, Hg = _head_rows(gate, B, D, "gated_norm_q8_1: gate")
+        if Hg != H:
+            raise ValueError("gated_norm_q8_1: gate must have x's heads")
+    op, os_ = None, 0
+    if out is not None:
+        op, os_, Ho = _head_rows(out, B, D, "gated_norm_q8_1: out")
+        if Ho != H:
+            raise ValueError("gated_norm_q8_1: out must have x's heads")
+    q8 = None
+    if q8_out is not None:
+        _on(index, "gated_norm_q8_1", q8_out.qs, q8_out.d, q8_out.s)
+        _q8_planes(q8_out, B, H * D, "gated_norm_q8_1: q8_out")
+        q8 = ctypes.byref(q8_out._c())
+    status = lib.zq_gated_norm_q8_1(xp, xs, B, H, D, _weights(gamma, D, "gated_norm_q8_1: gamma"), eps, gp, gs,
+                                    _act_of(act, "gated_norm_q8_1"), op, os_, q8, _stream_on(stream, index))
+    if status:
+        _check(status)
+    return q8_out if out is None else out
+
+
+def residual_norm_q8_1(x: torch.Tensor, y: torch.Tensor, gamma, eps: float, gamma_post=None, gate=None,
+                       act: str = "linear", scale: float = 1.0, x_out: torch.Tensor | None = None,
+                       out: torch.Tensor | None = None, q8_out: Q8_1 | None = None, stream=None) -> torch.Tensor:
+    """x_out = x + scale * norm(y; gamma_post) * act(gate) and the norm of it by
+    gamma, to fp32 rows (out), Q8_1 codes (q8_out), both or neither, for rows
+    [B][K], strided (see zq_residual_norm_q8_1); gate [B][K], or [K] for all
+    tokens.  Returns x_out, which may be x itself; gammas and gate may be None."""
+    lib = _lib or load()
+    if x.dim() != 2 or not x.is_cuda:
+        raise ValueError("residual_norm_q8_1: x must be a CUDA tensor [B][K]")
+    B, K = x.shape
+    if x_out is None:
+        x_out = _new(x.shape, torch.float32, x.device, stream)
+    index = x.get_device()
+    _on(index, "residual_norm_q8_1", y, gamma, gamma_post, gate, x_out, out)
+    xp, xs = _out_rows(x, B, K, "residual_norm_q8_1: x")
+    yp, ys = _out_rows(y, B, K, "residual_norm_q8_1: y")
+    rp, rs = _out_rows(x_out, B, K, "residual_norm_q8_1: x_out")
+    gp, gs = None, 0
+    if gate is not None and gate.dim() == 1:
+        gp = _weights(gate, K, "residual_norm_q8_1: gate")
+    elif gate is not None:
+        gp, gs = _out_rows(gate, B, K, "residual_norm_q8_1: gate")
+    op, os_ = (None, 0) if out is None else _out_rows(out, B, K, "residual_norm_q8_1: out")
+    q8 = None
+    if q8_out is not None:
+        _on(index, "residual_norm_q8_1", q8_out.qs, q8_out.d, q8_out.s)
+        _q8_planes(q8_out, B, K, "residual_norm_q8_1: q8_out")
+        q8 = ctypes.byref(q8_out._c())
+    status = lib.zq_residual_norm_q8_1(xp, xs, yp, ys, B, K, _weights(gamma_post, K, "residual_norm_q8_1: gamma_post"),
+                                       gp, gs, _act_of(act, "residual_norm_q8_1"), scale, rp, rs,
+                                       _weights(gamma, K, "residual_norm_q8_1: gamma"), eps, op, os_, q8,
+                                       _stream_on(stream, index))
+    if status:
+        _check(status)
+    return x_out
 
 
 # operations per probe launch, by kind (zq_debug_peak_probe)

@@ -15,6 +15,7 @@
 
 #include "zq_internal.cuh"
 #include "zq_kv.cuh"
+#include "zq_mixer.cuh"
 #include "zq_tc_common.cuh"
 
 __device__ unsigned int g_zq_device_status;
@@ -930,6 +931,192 @@ int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const void *A, c
     p.vec = N % 4 == 0 && aligned16(y) && y_stride % 4 == 0 && (!base || (aligned16(base) && base_stride % 4 == 0));
     p.h = static_cast<float *>(workspace);
     return launched(launch_lora(p, type, (cudaStream_t)stream), name);
+}
+
+namespace {
+
+int check_linear(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
+                 long long v_stride, int T, int Hk, const float *g, long long g_stride, const zq_linear_state *state,
+                 const int32_t *slots, float scale, float *out, long long out_stride, const char *name,
+                 LinearAttnArgs &a)
+{
+    if (!state || !state->s) return fail(ZQ_ERR_ARG, "%s: null state", name);
+    if (!aligned16(state->s)) return fail(ZQ_ERR_ALIGN, "%s: the state must be 16-byte aligned", name);
+    const int Hv = state->Hv, Dk = state->Dk, Dv = state->Dv;
+    if (Dk != 64 && Dk != 128) return fail(ZQ_ERR_SHAPE, "%s: Dk = %d must be 64 or 128", name, Dk);
+    if (Dv != 64 && Dv != 128 && Dv != 256) return fail(ZQ_ERR_SHAPE, "%s: Dv = %d must be 64, 128 or 256", name, Dv);
+    if (state->n < 1) return fail(ZQ_ERR_SHAPE, "%s: n = %d states", name, state->n);
+    if (Hk < 1 || Hv < Hk || Hv % Hk || Hv > 1024)
+        return fail(ZQ_ERR_SHAPE, "%s: Hv = %d must be a multiple of Hk = %d and at most 1024", name, Hv, Hk);
+    if (T < 1 || T > 1 << 24) return fail(ZQ_ERR_SHAPE, "%s: %d rows out of range", name, T);
+    if (!std::isfinite(scale)) return fail(ZQ_ERR_ARG, "%s: scale must be finite", name);
+    int st;
+    if ((st = check_rows(q, q_stride, (long long)Hk * Dk, name, "q"))) return st;
+    if ((st = check_rows(k, k_stride, (long long)Hk * Dk, name, "k"))) return st;
+    if ((st = check_rows(v, v_stride, (long long)Hv * Dv, name, "v"))) return st;
+    if ((st = check_rows(out, out_stride, (long long)Hv * Dv, name, "out"))) return st;
+    if (g && (g_stride < Hv || g_stride > 1LL << 40))
+        return fail(ZQ_ERR_SHAPE, "%s: stride %lld of g must be at least %d", name, g_stride, Hv);
+    if (!slots) return fail(ZQ_ERR_ARG, "%s: null slots", name);
+    if (!aligned4(g) || !aligned4(slots)) return fail(ZQ_ERR_ALIGN, "%s: g and slots must be 4-byte aligned", name);
+    a.q = q;
+    a.k = k;
+    a.v = v;
+    a.q_stride = q_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.T = T;
+    a.Hk = Hk;
+    a.Hv = Hv;
+    a.g = g;
+    a.g_stride = g_stride;
+    a.state = state->s;
+    a.n = state->n;
+    a.slots = slots;
+    a.scale = scale;
+    a.out = out;
+    a.out_stride = out_stride;
+    return ZQ_OK;
+}
+
+int check_gate(const float *gate, long long stride, long long width, bool one_row, int act, const char *name)
+{
+    if (act != ZQ_GATE_LINEAR && act != ZQ_GATE_SIGMOID && act != ZQ_GATE_SILU)
+        return fail(ZQ_ERR_ARG, "%s: gate activation %d unknown", name, act);
+    if (!gate || (one_row && stride == 0 && aligned16(gate))) return ZQ_OK;
+    return check_rows(gate, stride, width, name, "gate");
+}
+
+}  // namespace
+
+int zq_linear_attn_step(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
+                        long long v_stride, int B, int Hk, const float *g, long long g_stride,
+                        const zq_linear_state *state, const int32_t *slots, float scale, float *out,
+                        long long out_stride, void *stream)
+{
+    static const char *name = "zq_linear_attn_step";
+    LinearAttnArgs a{};
+    int st, dev;
+    if ((st = check_linear(q, q_stride, k, k_stride, v, v_stride, B, Hk, g, g_stride, state, slots, scale, out,
+                           out_stride, name, a)))
+        return st;
+    if (B > 65535) return fail(ZQ_ERR_SHAPE, "%s: B = %d out of range", name, B);
+    a.B = B;
+    if ((st = check_device(&dev))) return st;
+    return launched(launch_linear_attn_step(a, state->Dk, state->Dv, (cudaStream_t)stream), name);
+}
+
+size_t zq_linear_attn_workspace_bytes(int T, int B, int Hv, int Dk, int Dv)
+{
+    if (T < 1 || T > 1 << 24 || B < 1 || B > 65535 || Hv < 1 || Hv > 1024 || (Dk != 64 && Dk != 128) ||
+        (Dv != 64 && Dv != 128 && Dv != 256))
+        return 0;
+    return linear_attn_workspace(T, B, Hv, Dk, Dv);
+}
+
+int zq_linear_attn(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
+                   long long v_stride, int T, int B, int Hk, const float *g, long long g_stride, const int32_t *starts,
+                   const zq_linear_state *state, const int32_t *slots, const int32_t *fresh, float scale, float *out,
+                   long long out_stride, void *workspace, size_t workspace_bytes, void *stream)
+{
+    static const char *name = "zq_linear_attn";
+    LinearAttnArgs a{};
+    int st, dev;
+    if ((st = check_linear(q, q_stride, k, k_stride, v, v_stride, T, Hk, g, g_stride, state, slots, scale, out,
+                           out_stride, name, a)))
+        return st;
+    if (B < 1 || B > 65535) return fail(ZQ_ERR_SHAPE, "%s: B = %d out of range", name, B);
+    if (!starts) return fail(ZQ_ERR_ARG, "%s: null starts", name);
+    if (!aligned4(starts) || !aligned4(fresh))
+        return fail(ZQ_ERR_ALIGN, "%s: starts and fresh must be 4-byte aligned", name);
+    if (workspace && !aligned16(workspace)) return fail(ZQ_ERR_ALIGN, "%s: workspace must be 16-byte aligned", name);
+    a.B = B;
+    a.starts = starts;
+    a.fresh = fresh;
+    if ((st = check_device(&dev))) return st;
+    const size_t need = linear_attn_workspace(T, B, a.Hv, state->Dk, state->Dv);
+    if (need && (!workspace || workspace_bytes < need))
+        return fail(ZQ_ERR_WORKSPACE, "%s: workspace of %zu bytes required", name, need);
+    return launched(launch_linear_attn(a, state->Dk, state->Dv, workspace, (cudaStream_t)stream), name);
+}
+
+int zq_gated_norm_q8_1(const float *x, long long x_stride, int B, int H, int D, const float *gamma, float eps,
+                       const float *gate, long long gate_stride, int act, float *out, long long out_stride,
+                       const zq_q8_1 *q8_out, void *stream)
+{
+    static const char *name = "zq_gated_norm_q8_1";
+    if (D != 64 && D != 128 && D != 256) return fail(ZQ_ERR_SHAPE, "%s: D = %d must be 64, 128 or 256", name, D);
+    if (B < 1 || H < 1 || H > 65536 || (long long)B * H > INT32_MAX)
+        return fail(ZQ_ERR_SHAPE, "%s: B = %d, H = %d out of range", name, B, H);
+    if (!(eps >= 0.0f)) return fail(ZQ_ERR_ARG, "%s: eps must be >= 0", name);
+    const long long width = (long long)H * D;
+    int st, dev;
+    if ((st = check_rows(x, x_stride, width, name, "x"))) return st;
+    if ((st = check_gate(gate, gate_stride, width, false, act, name))) return st;
+    if (!out && !q8_out) return fail(ZQ_ERR_ARG, "%s: neither out nor q8_out", name);
+    if (out && (st = check_rows(out, out_stride, width, name, "out"))) return st;
+    if (out == x && out_stride != x_stride) return fail(ZQ_ERR_ARG, "%s: out in place needs x's stride", name);
+    if (!aligned16(gamma)) return fail(ZQ_ERR_ALIGN, "%s: gamma must be 16-byte aligned", name);
+    if (q8_out && (st = check_q8(*q8_out, name))) return st;
+    if ((st = check_device(&dev))) return st;
+    GatedNormArgs a{};
+    a.x = x;
+    a.x_stride = x_stride;
+    a.B = B;
+    a.H = H;
+    a.gamma = gamma;
+    a.eps = eps;
+    a.gate = gate;
+    a.gate_stride = gate_stride;
+    a.act = act;
+    a.out = out;
+    a.out_stride = out_stride;
+    if (q8_out) a.q8 = *q8_out;
+    return launched(launch_gated_norm(a, D, (cudaStream_t)stream), name);
+}
+
+int zq_residual_norm_q8_1(const float *x, long long x_stride, const float *y, long long y_stride, int B, int K,
+                          const float *gamma_post, const float *gate, long long gate_stride, int act, float scale,
+                          float *x_out, long long x_out_stride, const float *gamma, float eps, float *out,
+                          long long out_stride, const zq_q8_1 *q8_out, void *stream)
+{
+    static const char *name = "zq_residual_norm_q8_1";
+    if (B < 1 || B > 1 << 24) return fail(ZQ_ERR_SHAPE, "%s: B = %d out of range", name, B);
+    if (K < 32 || K % 32 || K > 32768)
+        return fail(ZQ_ERR_SHAPE, "%s: K = %d must be a multiple of 32 in [32, 32768]", name, K);
+    if (!(eps >= 0.0f)) return fail(ZQ_ERR_ARG, "%s: eps must be >= 0", name);
+    if (!std::isfinite(scale)) return fail(ZQ_ERR_ARG, "%s: scale must be finite", name);
+    int st, dev;
+    if ((st = check_rows(x, x_stride, K, name, "x"))) return st;
+    if ((st = check_rows(y, y_stride, K, name, "y"))) return st;
+    if ((st = check_gate(gate, gate_stride, K, true, act, name))) return st;
+    if ((st = check_rows(x_out, x_out_stride, K, name, "x_out"))) return st;
+    if ((x_out == x && x_out_stride != x_stride) || (x_out == y && x_out_stride != y_stride))
+        return fail(ZQ_ERR_ARG, "%s: x_out in place needs the same stride", name);
+    if (out && (st = check_rows(out, out_stride, K, name, "out"))) return st;
+    if (!aligned16(gamma_post) || !aligned16(gamma)) return fail(ZQ_ERR_ALIGN, "%s: gamma must be 16-byte aligned", name);
+    if (q8_out && (st = check_q8(*q8_out, name))) return st;
+    if ((st = check_device(&dev))) return st;
+    ResidualNormArgs a{};
+    a.x = x;
+    a.y = y;
+    a.x_stride = x_stride;
+    a.y_stride = y_stride;
+    a.B = B;
+    a.K = K;
+    a.gamma_post = gamma_post;
+    a.gate = gate;
+    a.gate_stride = gate_stride;
+    a.act = act;
+    a.scale = scale;
+    a.x_out = x_out;
+    a.x_out_stride = x_out_stride;
+    a.gamma = gamma;
+    a.eps = eps;
+    a.out = out;
+    a.out_stride = out_stride;
+    if (q8_out) a.q8 = *q8_out;
+    return launched(launch_residual_norm(a, (cudaStream_t)stream), name);
 }
 
 }  // extern "C"

@@ -49,6 +49,38 @@ __device__ __forceinline__ Q8Block q8_1_pack(const float (&xh)[32])
     return o;
 }
 
+// The same for a block whose values lie in 32 / E neighbouring lanes, E each: what
+// the lanes compare and add up does not depend on the order, so the bytes are
+// q8_1_pack's.  words: the lane's E codes; d, s: the block's, in every lane.
+template <int E>
+__device__ __forceinline__ void q8_1_pack_lanes(const float (&xh)[E], uint32_t (&words)[E / 4], __half &d16, __half &s16)
+{
+    float amax = 0.0f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) amax = fmaxf(amax, fabsf(xh[e]));
+#pragma unroll
+    for (int off = 16 / E; off >= 1; off >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+    const float d = __fdiv_rn(amax, 127.0f);
+    const float id = (d != 0.0f) ? __fdiv_rn(1.0f, d) : 0.0f;
+    int sum = 0;
+#pragma unroll
+    for (int v = 0; v < E / 4; ++v) {
+        words[v] = 0;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            float q = roundf(__fmul_rn(xh[4 * v + c], id));
+            q = fminf(fmaxf(q, -127.0f), 127.0f);
+            const int qi = (int)q;
+            sum += qi;
+            words[v] |= ((uint32_t)(qi & 0xFF)) << (8 * c);
+        }
+    }
+#pragma unroll
+    for (int off = 16 / E; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    d16 = __float2half_rn(d);
+    s16 = __float2half_rn(__fmul_rn(d, (float)sum));
+}
+
 // The batched projection's power-of-two scale for one token's activations:
 // k = 0 when 127 * max|d8| fits binary16 (<= 65504), else the exponent e of
 // 127 * max|d8| / 65504 = f * 2^e with f in [0.5, 1), so every |q8 * d8| *

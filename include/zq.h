@@ -597,6 +597,109 @@ ZQ_API int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const voi
                    const float *scales, int N, const float *base, long long base_stride, float *y, long long y_stride,
                    void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * ------------------------------------------- recurrent mixer and block edges
+ * What a hybrid model's recurrent layer does between its projections (MIInfer
+ * README, "Status": recurrent layers with a state of [48][128][128] ahead of the
+ * Q5_K output projection), and what lies between any block's last projection
+ * and the next one's codes.  Their int32 arrays need 4-byte alignment only.
+ *
+ * States of linear attention: fp32 [n][Hv][Dk][Dv], caller-owned device memory;
+ * a sequence's state is its slot of the n.  Dk 64 or 128, Dv 64, 128 or 256,
+ * 1 <= Hv <= 1024.
+ */
+typedef struct zq_linear_state {
+    float *s;                 /* [n][Hv][Dk][Dv] */
+    int n, Hv, Dk, Dv;
+} zq_linear_state;
+
+/*
+ * Linear attention with a decay for each head, one new token per sequence: for
+ * sequence b, value head h and key head h / (Hv / Hk)
+ *   S = exp(g) S + k v^T,   out = scale * S^T q,
+ * S being the state of slots[b], updated in place.
+ *   q, k  : fp32, head h of sequence b at q + b * q_stride + h * Dk, Hk heads
+ *           (strides in floats, multiples of 4, so the parts of a stacked
+ *           projection's row serve);  v, out : alike with Hv heads of Dv; out may
+ *           not overlap the inputs;
+ *   g     : fp32, the logarithm of the decay of head h at g + b * g_stride + h,
+ *           any value (-infinity forgets everything); NULL: no decay;
+ *   slots : int32 [B]; a sequence whose slot is outside [0, n) starts from zeros
+ *           and keeps nothing (a padded row).  The slots of a call differ: when
+ *           two are the same, that state is a mixture of the two;
+ *   scale : finite (1 / sqrt(Dk) is usual).
+ * Everything is fp32; the result does not change from one call to the next.
+ * Shapes: 1 <= B <= 65535, Hv a multiple of Hk.
+ */
+ZQ_API int zq_linear_attn_step(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
+                               long long v_stride, int B, int Hk, const float *g, long long g_stride,
+                               const zq_linear_state *state, const int32_t *slots, float scale, float *out,
+                               long long out_stride, void *stream);
+
+/*
+ * The same over prompts: B sequences of any lengths, the rows of sequence b being
+ * starts[b] .. starts[b + 1] - 1 of the call's T rows (int32 [B + 1], not
+ * decreasing; what is outside [0, T] is cut off, and rows of no sequence are
+ * neither read nor written).  Sequence b goes on from the state of slots[b], or
+ * from zeros where fresh[b] is not 0 (int32 [B], NULL: all go on; the state that
+ * is there is then not read), and leaves its last state there; a sequence without
+ * rows leaves its state as it was, or zeros.
+ *   workspace : zq_linear_attn_workspace_bytes(T, B, Hv, Dk, Dv) bytes, 16-byte
+ *           aligned; contents do not matter.  Calls that may run at the same time
+ *           (other streams, captured graphs) need workspaces of their own.
+ * Other arguments as for zq_linear_attn_step.  A NaN or infinity in a token's q,
+ * k, v or g does not reach earlier tokens, other heads or other sequences.
+ * Shapes: 1 <= T <= 2^24, 1 <= B <= 65535.
+ */
+ZQ_API size_t zq_linear_attn_workspace_bytes(int T, int B, int Hv, int Dk, int Dv);
+ZQ_API int zq_linear_attn(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
+                          long long v_stride, int T, int B, int Hk, const float *g, long long g_stride,
+                          const int32_t *starts, const zq_linear_state *state, const int32_t *slots,
+                          const int32_t *fresh, float scale, float *out, long long out_stride, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/* What a gate's values pass through before they multiply: nothing, 1 / (1 +
+ * exp(-g)), or g / (1 + exp(-g)). */
+enum { ZQ_GATE_LINEAR = 0, ZQ_GATE_SIGMOID = 1, ZQ_GATE_SILU = 2 };
+
+/*
+ * RMSNorm of every head of a mixer's output, times a gate, to the codes of the
+ * output projection's input:
+ *   y = (x r) gamma act(gate),  r = 1 / sqrt(mean(x^2) + eps) over the head's D.
+ *   x     : fp32, head h of token b at x + b * x_stride + h * D;
+ *   gamma : fp32 [D], NULL leaves the norm out;
+ *   gate  : fp32, laid out as x with gate_stride; NULL leaves the gate out;
+ *   out   : fp32, laid out as x with out_stride, may be x itself; may be NULL
+ *           when q8_out is given;
+ *   q8_out : planes of B x (H D) codes of y, packed as zq_rmsnorm_q8_1 packs xh;
+ *           may be NULL when out is given.
+ * Strides multiples of 4.  D 64, 128 or 256, 1 <= H <= 65536, B * H < 2^31.
+ */
+ZQ_API int zq_gated_norm_q8_1(const float *x, long long x_stride, int B, int H, int D, const float *gamma, float eps,
+                              const float *gate, long long gate_stride, int act, float *out, long long out_stride,
+                              const zq_q8_1 *q8_out, void *stream);
+
+/*
+ * The edge between two blocks: the norm after a block, its gate and residual
+ * scale, the residual addition, and the norm before the next block to codes:
+ *   u = (y r_y) gamma_post,   x_out = x + scale * (u act(gate)),
+ *   xh = (x_out r) gamma,     q8_out = codes of xh, out = xh.
+ *   x, y  : fp32, row b at x + b * x_stride (y alike): residual stream and block
+ *           output;  gamma_post, gamma : fp32 [K], NULL leaves that norm out;
+ *   gate  : fp32, row b at gate + b * gate_stride (gate_stride 0: one row for all
+ *           tokens); NULL leaves it out;
+ *   x_out : fp32 rows, may be x itself (or y), not a part of either;
+ *   out   : fp32 rows, may be NULL and may not overlap anything else;
+ *   q8_out : planes of B x K, may be NULL.
+ * The squares are added up in the order of zq_rmsnorm_q8_1, so the codes are
+ * those of zq_rmsnorm_q8_1 on x_out byte for byte.
+ * Strides multiples of 4.  1 <= B <= 2^24, K % 32 == 0, 32 <= K <= 32768.
+ */
+ZQ_API int zq_residual_norm_q8_1(const float *x, long long x_stride, const float *y, long long y_stride, int B, int K,
+                                 const float *gamma_post, const float *gate, long long gate_stride, int act,
+                                 float scale, float *x_out, long long x_out_stride, const float *gamma, float eps,
+                                 float *out, long long out_stride, const zq_q8_1 *q8_out, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
