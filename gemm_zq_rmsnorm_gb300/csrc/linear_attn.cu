@@ -93,26 +93,10 @@ __global__ void __launch_bounds__(kStepThreads) linear_attn_step_kernel(const __
 }
 
 template <int DK, int SL>
-__global__ void __launch_bounds__(kStepThreads) linear_attn_kernel(const __grid_constant__ LinearAttnArgs a, int Dv)
-{
-    pdl_wait();
-    pdl_launch_dependents();
-    const int slices = Dv / SL;
-    const int slice = blockIdx.x % slices, item = blockIdx.x / slices;
-    const int h = item % a.Hv, b = item / a.Hv;
-    const int slot = a.slots[b];
-    const bool kept = slot >= 0 && slot < a.n;
-    // rows outside the call's T are not touched, whatever the starts say
-    const int t0 = min(max(a.starts[b], 0), a.T), t1 = min(max(a.starts[b + 1], t0), a.T);
-    recurrence<DK, SL>(a, h, slice * SL, Dv, kept ? slot : -1, a.fresh && a.fresh[b] != 0, t0, t1);
-}
-
-template <int DK, int SL>
 cudaError_t launch_slices(const LinearAttnArgs &a, int Dv, cudaStream_t st)
 {
     const long long ctas = (long long)a.B * a.Hv * (Dv / SL);
-    return launch_pdl(a.starts ? linear_attn_kernel<DK, SL> : linear_attn_step_kernel<DK, SL>, dim3((unsigned)ctas),
-                      dim3(kStepThreads), 0, st, a, Dv);
+    return launch_pdl(linear_attn_step_kernel<DK, SL>, dim3((unsigned)ctas), dim3(kStepThreads), 0, st, a, Dv);
 }
 
 }  // namespace
@@ -121,13 +105,6 @@ cudaError_t launch_linear_attn_step(const LinearAttnArgs &a, int Dk, int Dv, cud
 {
     if (Dk == 64) return Dv == 64 ? launch_slices<64, 64>(a, Dv, st) : launch_slices<64, 128>(a, Dv, st);
     return Dv == 64 ? launch_slices<128, 64>(a, Dv, st) : launch_slices<128, 128>(a, Dv, st);
-}
-
-size_t linear_attn_workspace(int, int, int, int, int) { return 0; }
-
-cudaError_t launch_linear_attn(const LinearAttnArgs &a, int Dk, int Dv, void *, cudaStream_t st)
-{
-    return launch_linear_attn_step(a, Dk, Dv, st);
 }
 
 }  // namespace zq

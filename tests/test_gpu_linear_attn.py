@@ -143,6 +143,14 @@ def test_prompts_against_64_bits(Dk, Dv, lens, Hk, Hv):
     prompts(lens, Hk, Hv, Dk, Dv, seed=len(lens) + Hv)
 
 
+@pytest.mark.parametrize("Dk,Dv,Hk,Hv,lens", [
+    (128, 128, 1, 1, [3001]), (64, 64, 2, 2, [2048]), (128, 64, 1, 2, [700, 1, 900]), (64, 256, 1, 3, [1500]),
+    (128, 256, 1, 1, [640, 1111]), (128, 128, 4, 24, [777, 130])])
+@pytest.mark.parametrize("rate", [0.003, 1.0])
+def test_long_prompts(Dk, Dv, Hk, Hv, lens, rate):
+    prompts(lens, Hk, Hv, Dk, Dv, rate=rate, seed=3)
+
+
 def test_many_short_prompts():
     lens = [int(x) for x in np.random.default_rng(5).integers(0, 90, 300)]
     prompts(lens, 1, 2, 64, 64, seed=9)
