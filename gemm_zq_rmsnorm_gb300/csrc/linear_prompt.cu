@@ -1,38 +1,19 @@
 // linear_prompt.cu -- linear attention with a decay for each head over prompts
 // (MIInfer README, "Status": recurrent layers with a state of [heads][128][128]).
 //
-// In chunks of 64 tokens the recurrence is matrix products: with G_t the sum of g
-// from the chunk's first token to t,
-//   o_t = scale (exp(G_t) S^T q_t + sum_{s <= t} exp(G_t - G_s) (q_t . k_s) v_s),
-//   S'  = exp(G_C) S + sum_s exp(G_C - G_s) k_s v_s^T.
 // A CTA owns DVT columns of one head and walks through a segment of a sequence.
 // Each compute warp holds 16 of the columns, as the transposed state [16][Dk] in
 // MMA accumulators, whose layout is that of the MMA's second operand: the product
 // with the queries takes the state from registers.  Four more warps load and
 // convert the next chunk meanwhile.
-//
-// Every product is as exact as an fp32 one: a row x is taken as 2^e (hi + lo), two
-// binary16 parts of the row scaled to [1, 2), and a product is hi hi + hi lo + lo
-// hi (2^-22 of what bounds it; sums fp32, a chunk's sums added to the state outside
-// the tensor core, whose accumulator truncates).  Weights exp(G_t - G_s) and the
-// rows' powers of two meet in the exponent: with u_s = e_k + e_v - G_s (G in base
-// two) and M_t the largest u of s <= t, the weight in the product is 2^(u_s - M_t)
-// <= 1 and 2^(M_t + G_t) goes to the row, so that a token counts exactly where no
-// larger one of its past drowns it, and the future does not matter at all.  G and u
-// are sums in units of 2^-40.
-#include <limits.h>
-
 #include <atomic>
 
-#include "zq_async.cuh"
-#include "zq_internal.cuh"
-#include "zq_mixer.cuh"
-#include "zq_mma.cuh"
+#include "linear_prompt.cuh"
 
 namespace zq {
 namespace {
 
-constexpr int C = 64;              // tokens of a chunk
+constexpr int C = kChunk;
 constexpr int kLoaders = 4;        // warps that load
 constexpr int kSlots = 152;        // CTAs that the plan cuts long sequences for
 constexpr int kMaxCut = 512;       // sequences of a call up to which they are cut
@@ -53,23 +34,12 @@ Plan plan_of(int T, int B, int Hv, int Dv)
     return {length, T / length + B};
 }
 
-struct PromptArgs {
-    LinearAttnArgs a;
-    int Dv;
-    int length, segments;
-    float *local;              // [segments][Hv][Dv][Dk]: a segment's own state, then the one it starts from
-    long long *decay;          // [segments][Hv]: its G
-};
-
 // ---------------------------------------------------------------- shared memory of a stage
 template <int DK, int DVT>
 struct Stage {
     __half q[2][C * DK], k[2][C * DK], v[2][C * DVT];   // hi, lo; rows with swizzled 16-byte pieces
-    float uh[C], ul[C], mh[C], ml[C];                   // u and M: whole and broken part
-    float f1[C], f2[C], w[C];
+    Factors f;
     int eq[C], ekv[C];
-    float keep, add;                                    // what the state, and what the chunk's products are multiplied by
-    long long G;
 };
 
 // P in 16 x 16 blocks on and below the diagonal, block (r, c) at r (r + 1) / 2 + c
@@ -81,7 +51,7 @@ template <int DK, int DVT>
 struct Smem {
     Stage<DK, DVT> stage[2];
     Weights p[2];
-    int seq, seg, first, last, row0, row1, index;
+    Segment seg;
 };
 
 // byte offset of 16-byte piece `c` of row r in a tile of rows of D values
@@ -92,56 +62,6 @@ __device__ __forceinline__ uint32_t piece(int r, int c)
 }
 // the same in a block of 16 rows of 16
 __device__ __forceinline__ uint32_t block_piece(int r, int c) { return r * 32 + ((c ^ ((r >> 2) & 1)) << 4); }
-
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
-// two scaled values to their binary16 parts
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
-{
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
-    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(y - h.y), "f"(x - h.x));
-}
-
-__device__ __forceinline__ float exp2_fast(float x)
-{
-    float e;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x));
-    return e;
-}
-
-// exponent of a row's largest magnitude (its bits), such that the row over 2^e lies below 4
-__device__ __forceinline__ int row_exponent(uint32_t bits)
-{
-    const int e = (int)(bits >> 23) - 127;
-    return e < -126 ? -126 : e > 126 ? 126 : e;
-}
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }   // -126 <= e <= 127
-
-constexpr long long kOne = 1LL << 40;          // units of G and u
-constexpr long long kNothing = -(1LL << 60);   // u of a row of zeros
-
-// 2^(x / kOne + e) to fp32's accuracy
-__device__ __forceinline__ float exp2_units(long long x, int e)
-{
-    const long long whole = x >> 40;
-    const float part = (float)((uint32_t)(x >> 8)) * 0x1p-32f;
-    const long long n = whole + e;
-    return scalbnf(exp2f(part), (int)(n < -400 ? -400 : n > 400 ? 400 : n));
-}
 
 template <int ID_THREADS>
 __device__ __forceinline__ void bar_sync(int id)
@@ -157,127 +77,25 @@ __device__ __forceinline__ void bar_arrive(int id)
 enum { kFull = 1, kEmpty = 3, kLoad = 5, kCompute = 7 };
 
 // ---------------------------------------------------------------- loaders
-// Two neighbouring rows of one operand: a lane has four values of each when a row
-// is 128 wide, of one of them when it is 64.
-template <int D>
-struct Rows {
-    static constexpr int N = D / 64;
-    float4 x[N];
-    __device__ __forceinline__ static int row(int i) { return N == 2 ? i : (threadIdx.x & 31) >> 4; }
-    __device__ __forceinline__ static int lane() { return threadIdx.x & (D / 4 - 1); }
-    __device__ __forceinline__ void load(const float *p, long long stride, int r, int n)
-    {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = r + row(i);
-            x[i] = at < n ? *reinterpret_cast<const float4 *>(p + at * stride + 4 * lane())
-                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-    }
-    // bits of the largest magnitude of both rows, in every lane
-    __device__ __forceinline__ void largest(uint32_t (&m)[2]) const
-    {
-        uint32_t b[N];
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            b[i] = max(max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu),
-                       max(__float_as_uint(x[i].z) & 0x7fffffffu, __float_as_uint(x[i].w) & 0x7fffffffu));
-        if constexpr (N == 2) {
-            m[0] = __reduce_max_sync(0xffffffffu, b[0]);
-            m[1] = __reduce_max_sync(0xffffffffu, b[1]);
-        } else {
-            const bool second = threadIdx.x & 16;
-            m[0] = __reduce_max_sync(0xffffffffu, second ? 0u : b[0]);
-            m[1] = __reduce_max_sync(0xffffffffu, second ? b[0] : 0u);
-        }
-    }
-    // the rows over 2^e as binary16 parts; `fill`: instead of them (x when fill is 0)
-    __device__ __forceinline__ void store(__half (*dst)[C * D], int r, const int (&e)[2], const int (&fill)[2]) const
-    {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int j = row(i);
-            const float s = pow2(-(N == 2 ? e[i] : j ? e[1] : e[0]));
-            const int f = N == 2 ? fill[i] : j ? fill[1] : fill[0];
-            uint2 hi, lo;
-            split2(x[i].x * s, x[i].y * s, hi.x, lo.x);
-            split2(x[i].z * s, x[i].w * s, hi.y, lo.y);
-            if (f) {
-                hi = lo = f == 1 ? make_uint2(0u, 0u) : make_uint2(0x7e007e00u, 0x7e007e00u);   // zeros, NaN
-            }
-            const uint32_t at = piece<D>(r + j, lane() >> 1) + ((lane() & 1) << 3);
-            *reinterpret_cast<uint2 *>(reinterpret_cast<char *>(dst[0]) + at) = hi;
-            *reinterpret_cast<uint2 *>(reinterpret_cast<char *>(dst[1]) + at) = lo;
-        }
-    }
-};
-
-__device__ __forceinline__ long long shfl_up64(long long v, int d) { return __shfl_up_sync(0xffffffffu, v, d); }
-
-// G, u, M and the factors of a chunk's rows: two tokens a lane
-template <int DK, int DVT>
-__device__ __forceinline__ void factors(Stage<DK, DVT> &s, float g0, float g1, float scale)
-{
-    const int lane = threadIdx.x & 31;
-    auto units = [](float g) {   // beyond +-200 the power is 0 or infinity; NaN rows are marked elsewhere
-        g = fminf(fmaxf(g, -200.0f), 200.0f);
-        return __double2ll_rn((double)g * (1.4426950408889634074 * (double)kOne));
-    };
-    const long long a = units(g0), b = units(g1);
-    long long sum = a + b;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long o = shfl_up64(sum, d);
-        if (lane >= d) sum += o;
-    }
-    const long long G0 = sum - b, G1 = sum;
-    const int e0 = s.ekv[2 * lane], e1 = s.ekv[2 * lane + 1];
-    const long long u0 = e0 == INT_MIN ? kNothing : e0 * kOne - G0, u1 = e1 == INT_MIN ? kNothing : e1 * kOne - G1;
-    long long top = max(u0, u1);
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const long long o = shfl_up64(top, d);
-        if (lane >= d) top = max(top, o);
-    }
-    const long long before = shfl_up64(top, 1);
-    const long long M0 = lane ? max(before, u0) : u0, M1 = top;
-    const long long last = __shfl_sync(0xffffffffu, top, 31), G = __shfl_sync(0xffffffffu, sum, 31);
-    auto put = [&](int t, long long u, long long M, long long Gt) {
-        s.uh[t] = (float)(int)(u >> 40);
-        s.ul[t] = (float)((uint32_t)(u >> 8)) * 0x1p-32f;
-        s.mh[t] = (float)(int)(M >> 40);
-        s.ml[t] = (float)((uint32_t)(M >> 8)) * 0x1p-32f;
-        s.f1[t] = scale * exp2_units(M + Gt, s.eq[t]);
-        s.f2[t] = scale * exp2_units(Gt, s.eq[t]);
-        s.w[t] = exp2_units(u - last, 0);
-    };
-    put(2 * lane, u0, M0, G0);
-    put(2 * lane + 1, u1, M1, G1);
-    if (lane == 0) {
-        s.keep = exp2_units(G, 0);
-        s.add = exp2_units(G + last, 0);
-        s.G = G;
-    }
-}
-
 template <int DK, int DVT, bool STATES>
 __device__ __forceinline__ void load_chunks(const PromptArgs &p, Smem<DK, DVT> &sm, int h, int col0, int chunks)
 {
     constexpr int THREADS = (DVT / 16 + kLoaders) * 32;
+    constexpr int DEPTH = 4;   // steps of two rows on their way
     const LinearAttnArgs &a = p.a;
     const int w = (threadIdx.x >> 5) - DVT / 16, lane = threadIdx.x & 31;
     const int hk = h / (a.Hv / a.Hk);
     for (int c = 0; c < chunks; ++c) {
         Stage<DK, DVT> &s = sm.stage[c & 1];
-        const long long row = sm.row0 + c * C;
-        const int n = sm.row1 - (int)row;      // rows that there are
+        const long long row = sm.seg.row0 + c * C;
+        const int n = sm.seg.row1 - (int)row;      // rows that there are
         const float *q = a.q + row * a.q_stride + (long long)hk * DK, *k = a.k + row * a.k_stride + (long long)hk * DK;
         const float *v = a.v + row * a.v_stride + (long long)h * p.Dv + col0;
         const float *g = a.g ? a.g + row * a.g_stride + h : nullptr;
-        Rows<DK> qr[2], kr[2];
-        Rows<DVT> vr[2];
-        float gr[2];
-        float g0 = 0.0f, g1 = 0.0f;
+        Rows<DK> qr[DEPTH], kr[DEPTH];
+        Rows<DVT> vr[DEPTH];
+        float gr[DEPTH];
+        float g2[2] = {0.0f, 0.0f};   // of the warp that makes the factors
         // rows 2 (w + 4 j), 2 (w + 4 j) + 1 for j = 0 .. 7; those of j + 1 are on their way while j's are converted
         auto fetch = [&](int j, int b) {
             const int r = 2 * (w + kLoaders * j);
@@ -286,16 +104,17 @@ __device__ __forceinline__ void load_chunks(const PromptArgs &p, Smem<DK, DVT> &
             vr[b].load(v, a.v_stride, r, n);
             gr[b] = g && r + (lane & 1) < n ? g[(r + (lane & 1)) * a.g_stride] : 0.0f;
         };
-        fetch(0, 0);
+#pragma unroll
+        for (int j = 0; j < DEPTH - 1; ++j) fetch(j, j);
         if (w == 0 && g) {
-            if (2 * lane < n) g0 = g[2 * lane * a.g_stride];
-            if (2 * lane + 1 < n) g1 = g[(2 * lane + 1) * a.g_stride];
+            if (2 * lane < n) g2[0] = g[2 * lane * a.g_stride];
+            if (2 * lane + 1 < n) g2[1] = g[(2 * lane + 1) * a.g_stride];
         }
         if (c >= 2) bar_sync<THREADS>(kEmpty + (c & 1));
 #pragma unroll
         for (int j = 0; j < C / (2 * kLoaders); ++j) {
-            if (j + 1 < C / (2 * kLoaders)) fetch(j + 1, (j + 1) & 1);
-            const int r = 2 * (w + kLoaders * j), b = j & 1;
+            if (j + DEPTH - 1 < C / (2 * kLoaders)) fetch(j + DEPTH - 1, (j + DEPTH - 1) % DEPTH);
+            const int r = 2 * (w + kLoaders * j), b = j % DEPTH;
             const unsigned nan = __ballot_sync(0xffffffffu, gr[b] != gr[b]);
             uint32_t mk[2], mv[2], mq[2] = {0u, 0u};
             kr[b].largest(mk);
@@ -319,13 +138,13 @@ __device__ __forceinline__ void load_chunks(const PromptArgs &p, Smem<DK, DVT> &
                     s.eq[r + i] = eq[i];
                 }
             }
-            if (!STATES) qr[b].store(s.q, r, eq, qfill);
-            kr[b].store(s.k, r, ek, kfill);
-            vr[b].store(s.v, r, ev, vfill);
+            if (!STATES) qr[b].store(s.q[0], s.q[1], r, eq, qfill, piece<DK>);
+            kr[b].store(s.k[0], s.k[1], r, ek, kfill, piece<DK>);
+            vr[b].store(s.v[0], s.v[1], r, ev, vfill, piece<DVT>);
         }
         if (w == 0) {
             bar_sync<kLoaders * 32>(kLoad + (c & 1));
-            factors(s, g0, g1, a.scale);
+            make_factors(s.f, g2, {s.ekv[2 * lane], s.ekv[2 * lane + 1]}, {s.eq[2 * lane], s.eq[2 * lane + 1]}, a.scale);
         } else {
             bar_arrive<kLoaders * 32>(kLoad + (c & 1));
         }
@@ -364,11 +183,11 @@ __device__ __forceinline__ void scores(const Stage<DK, DVT> &s, Weights &pw, int
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
             const int tr = 16 * r + g + 8 * half;
-            const float mh = s.mh[tr], ml = s.ml[tr];
+            const float mh = s.f.mh[tr], ml = s.f.ml[tr];
 #pragma unroll
             for (int n = 0; n < 2; ++n) {
                 const int sc = 16 * c + 8 * n + 2 * t;
-                const float2 uh = *reinterpret_cast<const float2 *>(&s.uh[sc]), ul = *reinterpret_cast<const float2 *>(&s.ul[sc]);
+                const float2 uh = *reinterpret_cast<const float2 *>(&s.f.uh[sc]), ul = *reinterpret_cast<const float2 *>(&s.f.ul[sc]);
                 const float x = sc <= tr ? acc[n][2 * half] * exp2_fast((uh.x - mh) + (ul.x - ml)) : 0.0f;
                 const float y = sc + 1 <= tr ? acc[n][2 * half + 1] * exp2_fast((uh.y - mh) + (ul.y - ml)) : 0.0f;
                 uint32_t hi, lo;
@@ -394,53 +213,14 @@ linear_prompt_kernel(const __grid_constant__ PromptArgs p)
     const int tiles = p.Dv / DVT;
     const int tile = blockIdx.x % tiles, item = blockIdx.x / tiles;
     const int h = item % a.Hv, at = item / a.Hv;
-    // the segment: sequence, and which one of it
     if (threadIdx.x < 32) {
-        const int lane = threadIdx.x;
-        int seq = -1, seg = 0, last = 1;
-        if (p.length == 0) {
-            seq = at;
-        } else {
-            int base = 0;
-            for (int b0 = 0; b0 < a.B && seq < 0; b0 += 32) {
-                const int b = b0 + lane;
-                int cnt = 0;
-                if (b < a.B) {
-                    const int r0 = min(max(a.starts[b], 0), a.T), r1 = min(max(a.starts[b + 1], r0), a.T);
-                    cnt = max(1, (r1 - r0 + p.length - 1) / p.length);
-                }
-                int sum = cnt;
-#pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int o = __shfl_up_sync(0xffffffffu, sum, d);
-                    if (lane >= d) sum += o;
-                }
-                const bool mine = at >= base + sum - cnt && at < base + sum;
-                const unsigned who = __ballot_sync(0xffffffffu, mine);
-                if (who) {
-                    const int l = __ffs(who) - 1;
-                    seq = b0 + l;
-                    seg = at - base - __shfl_sync(0xffffffffu, sum - cnt, l);
-                    last = seg + 1 == __shfl_sync(0xffffffffu, cnt, l);
-                }
-                base += __shfl_sync(0xffffffffu, sum, 31);
-            }
-        }
-        if (lane == 0) {
-            sm.seq = seq;
-            sm.seg = seg;
-            sm.last = last;
-            if (seq >= 0) {
-                const int r0 = min(max(a.starts[seq], 0), a.T), r1 = min(max(a.starts[seq + 1], r0), a.T);
-                sm.row0 = r0 + seg * p.length;
-                sm.row1 = last ? r1 : sm.row0 + p.length;
-            }
-        }
+        const Segment s = find_segment(p, at);
+        if (threadIdx.x == 0) sm.seg = s;
     }
     __syncthreads();
-    const int seq = sm.seq;
-    if (seq < 0 || (STATES && sm.last)) return;
-    const int chunks = (sm.row1 - sm.row0 + C - 1) / C;
+    const int seq = sm.seg.seq;
+    if (seq < 0 || (STATES && sm.seg.last)) return;
+    const int chunks = (sm.seg.row1 - sm.seg.row0 + C - 1) / C;
     const int w = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const int col0 = tile * DVT;
     if (w >= NW) {
@@ -454,26 +234,15 @@ linear_prompt_kernel(const __grid_constant__ PromptArgs p)
     const int slot = a.slots[seq];
     const bool kept = slot >= 0 && slot < a.n;
     const int dv = col0 + 16 * w + g;
-    const bool cut = p.length != 0 && (sm.seg > 0 || !sm.last);   // the sequence has several segments
-    // states of cut sequences: [Dv][Dk]
-    float *local = p.local + ((long long)at * a.Hv + h) * p.Dv * DK;
+    const bool cut = p.length != 0 && (sm.seg.seg > 0 || !sm.seg.last);   // the sequence has several segments
+    float *local = p.local + ((long long)at * a.Hv + h) * DK * p.Dv;
     float *pool = a.state + ((long long)(kept ? slot : 0) * a.Hv + h) * DK * p.Dv;
-    if (STATES || (!cut && (!kept || (a.fresh && a.fresh[seq] != 0)))) {
+    const bool zeros = STATES || (!cut && (!kept || (a.fresh && a.fresh[seq] != 0)));
+    auto value = [&](float *of, int j, int e) { return of + (8 * j + 2 * t + (e & 1)) * p.Dv + dv + 8 * (e >> 1); };
 #pragma unroll
-        for (int j = 0; j < N8; ++j) S[j][0] = S[j][1] = S[j][2] = S[j][3] = 0.0f;
-    } else if (cut) {
+    for (int j = 0; j < N8; ++j)
 #pragma unroll
-        for (int j = 0; j < N8; ++j) {
-            const float2 x = *reinterpret_cast<const float2 *>(local + (long long)dv * DK + 8 * j + 2 * t);
-            const float2 y = *reinterpret_cast<const float2 *>(local + (long long)(dv + 8) * DK + 8 * j + 2 * t);
-            S[j][0] = x.x, S[j][1] = x.y, S[j][2] = y.x, S[j][3] = y.y;
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < N8; ++j)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[j][e] = pool[(long long)(8 * j + 2 * t + (e & 1)) * p.Dv + dv + 8 * (e >> 1)];
-    }
+        for (int e = 0; e < 4; ++e) S[j][e] = zeros ? 0.0f : *value(cut ? local : pool, j, e);
     long long G = 0;
 
     for (int c = 0; c < chunks; ++c) {
@@ -537,8 +306,8 @@ linear_prompt_kernel(const __grid_constant__ PromptArgs p)
                 ldsm4t(vl[kk], v1 + vp);
             }
             const uint32_t p0 = smem_u32(pw.p[0]), p1 = smem_u32(pw.p[1]);
-            const int rows = sm.row1 - sm.row0 - c * C;
-            float *out = a.out + (long long)(sm.row0 + c * C) * a.out_stride + (long long)h * p.Dv + col0 + 16 * w + 2 * t;
+            const int rows = sm.seg.row1 - sm.seg.row0 - c * C;
+            float *out = a.out + (long long)(sm.seg.row0 + c * C) * a.out_stride + (long long)h * p.Dv + col0 + 16 * w + 2 * t;
 #pragma unroll
             for (int m = 0; m < 4; ++m) {
                 float acc[2][4] = {};
@@ -558,7 +327,7 @@ linear_prompt_kernel(const __grid_constant__ PromptArgs p)
 #pragma unroll
                 for (int half = 0; half < 2; ++half) {
                     const int tr = 16 * m + g + 8 * half;
-                    const float f1 = s.f1[tr], f2 = s.f2[tr];
+                    const float f1 = s.f.f1[tr], f2 = s.f.f2[tr];
                     if (tr < rows)
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
@@ -579,8 +348,8 @@ linear_prompt_kernel(const __grid_constant__ PromptArgs p)
                 const uint32_t vp = piece<DVT>(16 * kk + (lane & 7) + ((lane >> 4) << 3), 2 * w + ((lane >> 3) & 1));
                 ldsm4t(xh, v0 + vp);
                 ldsm4t(xl, v1 + vp);
-                const float2 wa = *reinterpret_cast<const float2 *>(&s.w[16 * kk + 2 * t]);
-                const float2 wb = *reinterpret_cast<const float2 *>(&s.w[16 * kk + 2 * t + 8]);
+                const float2 wa = *reinterpret_cast<const float2 *>(&s.f.w[16 * kk + 2 * t]);
+                const float2 wb = *reinterpret_cast<const float2 *>(&s.f.w[16 * kk + 2 * t + 8]);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const float2 hi = __half22float2(*reinterpret_cast<const __half2 *>(&xh[i]));
@@ -590,7 +359,7 @@ linear_prompt_kernel(const __grid_constant__ PromptArgs p)
                 }
             }
             const uint32_t k0 = smem_u32(s.k[0]), k1 = smem_u32(s.k[1]);
-            const float keep = s.keep, add = s.add;
+            const float keep = s.f.keep, add = s.f.add;
 #pragma unroll
             for (int jj = 0; jj < DK / 16; ++jj) {
                 float acc[2][4] = {};
@@ -612,29 +381,22 @@ linear_prompt_kernel(const __grid_constant__ PromptArgs p)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) S[2 * jj + n][e] = __fmaf_rn(add, acc[n][e], keep * S[2 * jj + n][e]);
             }
-            G = min(max(G + s.G, -(1LL << 52)), 1LL << 52);
+            G = clamp_units(G + s.f.G);
         }
         if (c + 2 < chunks) bar_arrive<THREADS>(kEmpty + (c & 1));
     }
 
-    if (STATES) {
-#pragma unroll
-        for (int j = 0; j < N8; ++j) {
-            *reinterpret_cast<float2 *>(local + (long long)dv * DK + 8 * j + 2 * t) = make_float2(S[j][0], S[j][1]);
-            *reinterpret_cast<float2 *>(local + (long long)(dv + 8) * DK + 8 * j + 2 * t) = make_float2(S[j][2], S[j][3]);
-        }
-        if (threadIdx.x == 0 && tile == 0) p.decay[(long long)at * a.Hv + h] = G;
-    } else if (kept && sm.last) {
+    if (STATES || (kept && sm.seg.last))
 #pragma unroll
         for (int j = 0; j < N8; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) pool[(long long)(8 * j + 2 * t + (e & 1)) * p.Dv + dv + 8 * (e >> 1)] = S[j][e];
-    }
+            for (int e = 0; e < 4; ++e) *value(STATES ? local : pool, j, e) = S[j][e];
+    if (STATES && threadIdx.x == 0 && tile == 0) p.decay[(long long)at * a.Hv + h] = G;
 }
 
 // The states that the segments of cut sequences start from, in the place of their
-// own: first(i + 1) = exp(G_i) first(i) + own(i).  One thread for a value of the
-// state; grid: values / 256, heads, sequences.
+// own: first(i + 1) = exp(G_i) first(i) + own(i).  A thread has four values of the
+// state; grid: values / 1024, heads, sequences.
 __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant__ PromptArgs p, int Dk)
 {
     pdl_wait();
@@ -642,31 +404,32 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     const LinearAttnArgs &a = p.a;
     __shared__ int base_s;
     const int b = blockIdx.z, h = blockIdx.y;
-    auto count = [&](int i) {
-        const int r0 = min(max(a.starts[i], 0), a.T), r1 = min(max(a.starts[i + 1], r0), a.T);
-        return max(1, (r1 - r0 + p.length - 1) / p.length);
-    };
-    const int n = count(b);
+    const int n = segments_of(p, b);
     if (n < 2) return;
     if (threadIdx.x < 32) {   // segments of the sequences before this one
         int sum = 0;
-        for (int i = threadIdx.x; i < b; i += 32) sum += count(i);
+        for (int i = threadIdx.x; i < b; i += 32) sum += segments_of(p, i);
         sum = __reduce_add_sync(0xffffffffu, sum);
         if (threadIdx.x == 0) base_s = sum;
     }
     __syncthreads();
     const int base = base_s;
-    const int at = blockIdx.x * 256 + threadIdx.x;   // [Dv][Dk]
-    const long long size = (long long)p.Dv * Dk;
+    const long long size = (long long)p.Dv * Dk, at = 4 * (blockIdx.x * 256 + threadIdx.x);
     const int slot = a.slots[b];
-    float first = 0.0f;
+    float4 first = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (slot >= 0 && slot < a.n && !(a.fresh && a.fresh[b] != 0))
-        first = a.state[((long long)slot * a.Hv + h) * size + (long long)(at % Dk) * p.Dv + at / Dk];
+        first = *reinterpret_cast<const float4 *>(a.state + ((long long)slot * a.Hv + h) * size + at);
+    auto own = [&](int i) { return reinterpret_cast<float4 *>(p.local + ((long long)(base + i) * a.Hv + h) * size + at); };
+    float4 mine = *own(0);
     for (int i = 0; i < n; ++i) {
-        float *own = p.local + ((long long)(base + i) * a.Hv + h) * size + at;
-        const float mine = i + 1 < n ? *own : 0.0f;
-        *own = first;
-        if (i + 1 < n) first = __fmaf_rn(exp2_units(p.decay[(long long)(base + i) * a.Hv + h], 0), first, mine);
+        const float4 next = i + 2 < n ? *own(i + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // the last has none
+        *own(i) = first;
+        if (i + 1 < n) {
+            const float f = exp2_units(p.decay[(long long)(base + i) * a.Hv + h], 0);
+            first = make_float4(__fmaf_rn(f, first.x, mine.x), __fmaf_rn(f, first.y, mine.y),
+                                __fmaf_rn(f, first.z, mine.z), __fmaf_rn(f, first.w, mine.w));
+            mine = next;
+        }
     }
 }
 
@@ -692,13 +455,17 @@ cudaError_t launch_kernel(const PromptArgs &p, cudaStream_t st)
 template <int DK, int DVT>
 cudaError_t launch_shape(const PromptArgs &p, cudaStream_t st)
 {
+    auto run = [&](bool states) {
+        if constexpr (DVT == 128) return launch_linear_prompt_tc(p, DK, states, st);
+        else return states ? launch_kernel<DK, DVT, true>(p, st) : launch_kernel<DK, DVT, false>(p, st);
+    };
     if (p.length) {
-        cudaError_t e = launch_kernel<DK, DVT, true>(p, st);
+        cudaError_t e = run(true);
         if (e != cudaSuccess) return e;
-        e = launch_pdl(linear_join_kernel, dim3(DK * p.Dv / 256, p.a.Hv, p.a.B), dim3(256), 0, st, p, DK);
+        e = launch_pdl(linear_join_kernel, dim3(DK * p.Dv / 1024, p.a.Hv, p.a.B), dim3(256), 0, st, p, DK);
         if (e != cudaSuccess) return e;
     }
-    return launch_kernel<DK, DVT, false>(p, st);
+    return run(false);
 }
 
 size_t state_bytes(const Plan &plan, int Hv, int Dk, int Dv) { return (size_t)plan.segments * Hv * Dk * Dv * 4; }
