@@ -20,6 +20,7 @@
 
 #include <limits.h>
 
+#include <cuda.h>
 #include <cuda_fp16.h>
 
 #include "zq_async.cuh"
@@ -131,12 +132,25 @@ struct Factors {
     long long G;
 };
 
-// 2^(x / kOne + e) to fp32's accuracy
+// 2^(x / kOne + e), the broken part's power to 2^-22
 __device__ __forceinline__ float exp2_units(long long x, int e)
 {
-    const long long n = (x >> 40) + e;
+    const long long whole = (x >> 40) + e;
+    const int n = (int)(whole < -252 ? -252 : whole > 252 ? 252 : whole);   // 2^-252 and 2^252 as two factors: 0, infinity
     const float part = (float)((uint32_t)(x >> 8)) * 0x1p-32f;
-    return scalbnf(exp2f(part), (int)(n < -400 ? -400 : n > 400 ? 400 : n));
+    return exp2_fast(part) * pow2(n >> 1) * pow2(n - (n >> 1));
+}
+
+// x log2 e in units of 2^-40, to 2^-33 of itself and half a unit: the significand times 2^32 log2 e, shifted
+__device__ __forceinline__ long long log2_units(float x)
+{
+    // beyond +-200 the power is 0 or infinity; NaN is marked elsewhere
+    x = fminf(fmaxf(x, -200.0f), 200.0f);
+    const uint32_t bits = __float_as_uint(x) & 0x7fffffffu;
+    const int shift = 142 - (int)(bits >> 23);   // 15 - e, at least 8
+    const uint64_t product = (uint64_t)((bits & 0x7fffffu) | 0x800000u) * 6196328019ull;
+    const long long r = shift > 62 ? 0 : (long long)((product + (1ull << (shift - 1))) >> shift);
+    return x < 0.0f ? -r : r;
 }
 
 __device__ __forceinline__ long long clamp_units(long long G) { return min(max(G, -(1LL << 52)), 1LL << 52); }
@@ -147,12 +161,8 @@ __device__ __forceinline__ void make_factors(Factors &s, const float (&g)[2], co
                                              float scale)
 {
     const int lane = threadIdx.x & 31;
-    auto units = [](float x) {   // beyond +-200 the power is 0 or infinity; NaN is marked elsewhere
-        x = fminf(fmaxf(x, -200.0f), 200.0f);
-        return __double2ll_rn((double)x * (1.4426950408889634074 * (double)kOne));
-    };
-    const long long b = units(g[1]);
-    long long sum = units(g[0]) + b;
+    const long long b = log2_units(g[1]);
+    long long sum = log2_units(g[0]) + b;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
         const long long o = __shfl_up_sync(0xffffffffu, sum, d);
@@ -222,19 +232,35 @@ struct Rows {
                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
     }
-    // bits of the largest magnitude of both rows, in every lane
-    __device__ __forceinline__ void largest(uint32_t (&m)[2]) const
+    // from rows in shared memory, one after another
+    __device__ __forceinline__ void load_shared(const float *p)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = reinterpret_cast<const float4 *>(p + row(i) * D)[lane()];
+    }
+    // rows r, r + 1: zeros from row n on
+    __device__ __forceinline__ void cut(int r, int n)
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (r + row(i) >= n) x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    // bits of the largest magnitude of both rows, in every lane; NANS: a NaN is the largest (else it is passed over)
+    template <bool NANS = true>
+    __device__ __forceinline__ void largest(uint32_t &first, uint32_t &second) const
     {
         uint32_t b[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) b[i] = max(max(magnitude(x[i].x), magnitude(x[i].y)), max(magnitude(x[i].z), magnitude(x[i].w)));
+        for (int i = 0; i < N; ++i)
+            b[i] = NANS ? max(max(magnitude(x[i].x), magnitude(x[i].y)), max(magnitude(x[i].z), magnitude(x[i].w)))
+                        : __float_as_uint(fmaxf(fmaxf(fabsf(x[i].x), fabsf(x[i].y)), fmaxf(fabsf(x[i].z), fabsf(x[i].w))));
         if constexpr (N == 2) {
-            m[0] = __reduce_max_sync(0xffffffffu, b[0]);
-            m[1] = __reduce_max_sync(0xffffffffu, b[1]);
+            first = __reduce_max_sync(0xffffffffu, b[0]);
+            second = __reduce_max_sync(0xffffffffu, b[1]);
         } else {
-            const bool second = threadIdx.x & 16;
-            m[0] = __reduce_max_sync(0xffffffffu, second ? 0u : b[0]);
-            m[1] = __reduce_max_sync(0xffffffffu, second ? b[0] : 0u);
+            const bool half = threadIdx.x & 16;
+            first = __reduce_max_sync(0xffffffffu, half ? 0u : b[0]);
+            second = __reduce_max_sync(0xffffffffu, half ? b[0] : 0u);
         }
     }
     // the rows over 2^e as binary16 parts at(row, 16-byte piece) bytes into hi and lo; fill: instead of them 1 zeros, 2 NaN

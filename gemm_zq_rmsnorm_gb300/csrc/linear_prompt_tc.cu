@@ -8,13 +8,13 @@
 //   O1 [128][64] = S^T Q^T   (S^T, 128 x Dk, in tensor memory; Q in shared)
 //   O2 [128][64] = V^T P^T   (V^T, 128 x 64, in tensor memory; P in shared)
 // each as three products of binary16 parts, the small ones first.  The state itself
-// stays in the registers of eight warps (two threads for a column), which add U to
+// stays in the registers of sixteen warps (four threads for a column), which add U to
 // it, split it for the next chunk and put O1 and O2 together.
 //
 // Warps: 0 issues the MMAs; 1..3 compute the scores and weights P (mma.sync: 64 x 64
 // on and below the diagonal is too small a tile); 4..7 convert queries and keys;
 // 8..11 values, a lane for a column (128-byte loads), and the chunk's factors;
-// 12..19 the state.  Keys and queries are two stages deep, P too; the key tile serves
+// 12..27 the state.  Keys and queries are two stages deep, P too; the key tile serves
 // the scores as rows and U as columns (the same bytes, a descriptor of the other
 // order).
 //
@@ -29,24 +29,32 @@ namespace zq {
 namespace {
 
 constexpr int C = kChunk;
-constexpr int kWarpP = 1, kWarpL = 4, kWarpV = 8, kWarpE = 12, kWarps = 20;   // first warp of each role; 0 issues
+constexpr int kWarpP = 1, kWarpL = 4, kWarpV = 8, kWarpE = 12, kWarps = 28;   // first warp of each role; 0 issues
 constexpr int kThreads = kWarps * 32;
 // tensor memory columns
 constexpr int kO1 = 0, kO2 = 64, kU = 128, kSh = 256, kSl = 320, kVh = 384, kVl = 416, kWh = 448, kWl = 480;
+static_assert(kVl - kVh == kWl - kWh, "low parts behind high ones");
 
-template <int DK>
+constexpr int kRawRows = 4;        // rows of a copy
+
+template <int DK, int DV>
 struct Smem {
     __half q[2][2][C * DK], k[2][2][C * DK];   // [stage][part]: rows in tiles of 64 columns, 128-byte swizzle
-    __half p[2][2][C * C];                     // [stage][part], rows of 64 tokens
-    Factors f[4];
-    uint32_t vmax[4][C];                       // largest magnitudes of the values of 32 columns
-    float vscale[C];                           // 2^-e of the values' rows
-    float wscale[C];                           // that times w
-    int ek[2][C], eq[2][C];
-    uint32_t smax[2][128];
-    uint64_t qk_full[2], qk_empty[2], p_full[2], p_empty[2], fact[4], v_full, s_full, o_full, o_empty, u_full, u_empty;
+    __half p[2][C * C];                        // [part], rows of 64 tokens
+    struct Raw {                               // rows as they come, of one converting warp
+        float q[kRawRows * DK], k[kRawRows * DK];
+    } raw[4][2];
+    float v[C * DV];                           // values as they come
+    struct alignas(16) Chunk : Factors {       // read four values at a time
+        float vscale[C], wscale[C];            // 2^-e of the values' rows, and that times w
+        int some_bad;
+    } f[4];
+    alignas(16) uint32_t mq[2][C], mk[2][C], mv[2][C];   // bits of the rows' largest magnitudes
+    uint32_t smax[4][128];
+    uint64_t raw_full[4][2], qk_full[2], qk_empty[2], fact[4];
+    uint64_t values, sizes, p_full, w_full, v_full, s_full, o_full, o_empty, u_full, u_empty;
     uint32_t tmem;
-    int abort, any_bad;
+    int abort;
     Segment seg;
 };
 
@@ -64,21 +72,63 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
                  : "r"(taddr));
 }
 
+// The warp waits for a phase.  Many waiting warps share the issue slots (and the
+// instruction cache) with the ones that work, so the loop is as short as it can be,
+// and of every group of warps one waits here while the others sleep in a named
+// barrier; the limit and the others' failure are looked at every 512 probes.
+__device__ __forceinline__ void wait_phase(uint64_t *bar, int parity, volatile int *abort_flag, unsigned int *status)
+{
+    uint64_t since = 0;
+    for (;;) {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 64;\n\t"
+            "AGAIN:\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
+            "sub.u32 n, n, 1;\n\tsetp.ne.u32 q, n, 0;\n\t"
+            "@q bra AGAIN;\n\t"
+            "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_u32(bar)), "r"((uint32_t)(parity & 1))
+            : "memory");
+        if (__all_sync(0xffffffffu, done) || __any_sync(0xffffffffu, *abort_flag)) return;
+        const uint64_t now = global_ns();
+        if (!since) since = now;
+        if (now - since > kWaitLimitNs) {
+            flag_timeout(status);
+            *abort_flag = 1;
+        }
+    }
+}
+
 // B from columns: bit 16 of the instruction descriptor
 __host__ __device__ constexpr uint32_t idesc_b_columns(uint32_t M, uint32_t N) { return idesc_f16_f32(M, N) | 1u << 16; }
 
-template <int DK, bool STATES>
-__global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p)
+template <int DK, int DV, bool STATES>
+__global__ void __launch_bounds__(kThreads, 1)
+linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
 {
+    constexpr int QUARTERS = DV / 32;   // of the tensor memory's lanes that are in use
     extern __shared__ char raw[];
-    Smem<DK> &sm = *reinterpret_cast<Smem<DK> *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    // (an offset, not a rounded address: the compiler goes on seeing shared memory)
+    Smem<DK, DV> &sm = *reinterpret_cast<Smem<DK, DV> *>(raw + (-smem_u32(raw) & 1023u));
     const LinearAttnArgs &a = p.a;
     const int w = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     volatile int *abort_flag = &sm.abort;
     unsigned int *status = p.status;
-    auto wait = [&](uint64_t &bar, int parity) {   // by the whole warp
-        wait_fast(&bar, (uint32_t)(parity & 1), abort_flag, status);
-        __syncwarp();
+    auto wait = [&](uint64_t &bar, int parity) { wait_phase(&bar, parity, abort_flag, status); };
+    // the same for a group of warps: its first one waits, the others in its named barrier
+    auto sync = [&](int group) {
+        named_bar(group == kWarpP ? 1 : group == kWarpL ? 2 : group == kWarpV ? 3 : 4,
+                  group == kWarpP ? 96 : group == kWarpL ? 128 : (group == kWarpE ? 4 : 1) * 32 * QUARTERS);
     };
     auto arrive = [&](uint64_t &bar) {   // one arrival of the warp
         __syncwarp();
@@ -90,16 +140,22 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.qk_full[i], 4);
             mbar_init(&sm.qk_empty[i], STATES ? 1 : 1 + 3);
-            mbar_init(&sm.p_full[i], 3);
-            mbar_init(&sm.p_empty[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&sm.fact[i], 1);
-        mbar_init(&sm.v_full, 4);
-        mbar_init(&sm.s_full, 8);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&sm.fact[i], 1);
+            mbar_init(&sm.raw_full[i][0], 1);
+            mbar_init(&sm.raw_full[i][1], 1);
+        }
+        mbar_init(&sm.values, 1);
+        mbar_init(&sm.sizes, 4);
+        mbar_init(&sm.p_full, 3);
+        mbar_init(&sm.w_full, QUARTERS);
+        mbar_init(&sm.v_full, QUARTERS);
+        mbar_init(&sm.s_full, 4 * QUARTERS);
         mbar_init(&sm.o_full, 1);
-        mbar_init(&sm.o_empty, 8);
+        mbar_init(&sm.o_empty, 4 * QUARTERS);
         mbar_init(&sm.u_full, 1);
-        mbar_init(&sm.u_empty, 8);
+        mbar_init(&sm.u_empty, 4 * QUARTERS);
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -108,9 +164,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
             reinterpret_cast<uint4 *>(sm.p)[i] = make_uint4(0u, 0u, 0u, 0u);
     fence_async_smem();
     pdl_wait();   // the projection's rows, the starts and the states come from earlier kernels
-    const int tiles = p.Dv / 128;
+    const int tiles = p.Dv / DV;
     const int tile = blockIdx.x % tiles, item = blockIdx.x / tiles;
-    const int h = item % a.Hv, at = item / a.Hv, col0 = tile * 128;
+    const int h = item % a.Hv, at = item / a.Hv, col0 = tile * DV;
     if (w == 4) {
         const Segment s = find_segment(p, at);
         if (lane == 0) sm.seg = s;
@@ -133,12 +189,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1, ph = c >> 1;
             wait(sm.qk_full[st], ph);
-            wait(sm.v_full, c);
+            wait(sm.w_full, c);
             if (c) wait(sm.u_empty, c - 1);
             tc_fence_after();
             const uint32_t kh = smem_u32(sm.k[st][0]), kl = smem_u32(sm.k[st][1]);
             if (!*abort_flag && leader) {
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 3; ++i) {   // lo hi, hi lo, hi hi
                     const uint32_t av = tmem + (i == 0 ? kWl : kWh), b = i == 1 ? kl : kh;
 #pragma unroll
@@ -156,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
             tc_fence_after();
             const uint32_t qh = smem_u32(sm.q[st][0]), ql = smem_u32(sm.q[st][1]);
             if (!*abort_flag && leader) {
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 3; ++i) {
                     const uint32_t as = tmem + (i == 0 ? kSl : kSh), b = i == 1 ? ql : qh;
 #pragma unroll
@@ -165,13 +221,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
                                    smem_desc(b + (kk >> 2) * (C * 128) + (kk & 3) * 32, 16, 1024, kLayoutSw128), id_o,
                                    i || kk);
                 }
+                mma_commit(&sm.qk_empty[st]);
             }
             __syncwarp();
-            wait(sm.p_full[st], ph);
+            wait(sm.v_full, c);
+            wait(sm.p_full, c);
             tc_fence_after();
-            const uint32_t p0 = smem_u32(sm.p[st][0]), p1 = smem_u32(sm.p[st][1]);
+            const uint32_t p0 = smem_u32(sm.p[0]), p1 = smem_u32(sm.p[1]);
             if (!*abort_flag && leader) {
-#pragma unroll
+#pragma unroll 1
                 for (int i = 0; i < 3; ++i) {
                     const uint32_t av = tmem + (i == 0 ? kVl : kVh), b = i == 1 ? p1 : p0;
 #pragma unroll
@@ -179,8 +237,6 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
                         mma_f16_ta(tmem + kO2, av + 8 * kk, smem_desc(b + kk * 32, 16, 1024, kLayoutSw128), id_o, i || kk);
                 }
                 mma_commit(&sm.o_full);
-                mma_commit(&sm.qk_empty[st]);
-                mma_commit(&sm.p_empty[st]);
             }
             __syncwarp();
         }
@@ -188,29 +244,21 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
         // ------------------------------------------------------------ scores and weights
         if (!STATES) {
             const int g = lane >> 2, t = lane & 3, wp = w - kWarpP;
+            // blocks (r, c) of 16 x 16, c <= r: a row of four, a row of three, a row of two and one
+            const int first = wp ? 1 + 3 * wp : 0, end = wp ? 4 + 3 * wp : 4;
             for (int c = 0; c < chunks; ++c) {
                 const int st = c & 1, ph = c >> 1;
-                wait(sm.qk_full[st], ph);
+                if (wp == 0) wait(sm.qk_full[st], ph);
+                sync(kWarpP);
                 const uint32_t q0 = smem_u32(sm.q[st][0]), q1 = smem_u32(sm.q[st][1]), k0 = smem_u32(sm.k[st][0]),
                                k1 = smem_u32(sm.k[st][1]);
-                // blocks (r, c) of 16 x 16, c <= r: a row of four, a row of three, a row of two and one
-                const int first = wp ? 1 + 3 * wp : 0, count = wp ? 3 : 4;
-                float acc[4][2][4];
-                auto block = [&](int i, int &r, int &cc) {
-                    i += first;
-                    r = i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0;
-                    cc = i < 4 ? 3 - i : i < 7 ? 6 - i : i < 9 ? 8 - i : 0;
-                };
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i >= count) break;
-                    int r, cc;
-                    block(i, r, cc);
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][n][e] = 0.0f;
-                    float small[2][4] = {};   // the products of a low part, apart: the accumulator cuts off
+                const Factors &f = sm.f[c & 3];
+                char *p0 = reinterpret_cast<char *>(sm.p[0]), *p1 = reinterpret_cast<char *>(sm.p[1]);
+#pragma unroll 1
+                for (int i = first; i < end; ++i) {
+                    const int r = i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0, cc = i < 4 ? 3 - i : i < 7 ? 6 - i : i < 9 ? 8 - i : 0;
+                    // the products of a low part apart: the accumulator cuts off
+                    float acc[2][4] = {}, hl[2][4] = {}, lh[2][4] = {};
                     const int ar = 16 * r + (lane & 15), br = 16 * cc + (lane & 7) + ((lane >> 4) << 3);
 #pragma unroll
                     for (int kk = 0; kk < DK / 16; ++kk) {
@@ -223,26 +271,18 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
                         ldsm4(bl, k1 + bp);
 #pragma unroll
                         for (int n = 0; n < 2; ++n) {
-                            mma16<ZQ_F16>(acc[i][n], ah[0], ah[1], ah[2], ah[3], bh[2 * n], bh[2 * n + 1]);
-                            mma16<ZQ_F16>(small[n], ah[0], ah[1], ah[2], ah[3], bl[2 * n], bl[2 * n + 1]);
-                            mma16<ZQ_F16>(small[n], al[0], al[1], al[2], al[3], bh[2 * n], bh[2 * n + 1]);
+                            mma16<ZQ_F16>(acc[n], ah[0], ah[1], ah[2], ah[3], bh[2 * n], bh[2 * n + 1]);
+                            mma16<ZQ_F16>(hl[n], ah[0], ah[1], ah[2], ah[3], bl[2 * n], bl[2 * n + 1]);
+                            mma16<ZQ_F16>(lh[n], al[0], al[1], al[2], al[3], bh[2 * n], bh[2 * n + 1]);
                         }
                     }
-#pragma unroll
-                    for (int n = 0; n < 2; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) acc[i][n][e] += small[n][e];
-                }
-                arrive(sm.qk_empty[st]);
-                wait(sm.fact[c & 3], c >> 2);
-                if (c >= 2) wait(sm.p_empty[st], ph - 1);
-                const Factors &f = sm.f[c & 3];
-                char *p0 = reinterpret_cast<char *>(sm.p[st][0]), *p1 = reinterpret_cast<char *>(sm.p[st][1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (i >= count) break;
-                    int r, cc;
-                    block(i, r, cc);
+                    if (i == first) {
+                        if (wp == 0) {
+                            wait(sm.fact[c & 3], c >> 2);
+                            if (c) wait(sm.o_full, c - 1);   // the weights have been read
+                        }
+                        sync(kWarpP);
+                    }
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         const int tr = 16 * r + g + 8 * half;
@@ -252,228 +292,348 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
                             const int sc = 16 * cc + 8 * n + 2 * t;
                             const float2 uh = *reinterpret_cast<const float2 *>(&f.uh[sc]),
                                          ul = *reinterpret_cast<const float2 *>(&f.ul[sc]);
-                            const float x = sc <= tr ? acc[i][n][2 * half] * exp2_fast((uh.x - mh) + (ul.x - ml)) : 0.0f;
-                            const float y =
-                                sc + 1 <= tr ? acc[i][n][2 * half + 1] * exp2_fast((uh.y - mh) + (ul.y - ml)) : 0.0f;
+                            const float x = acc[n][2 * half] + (hl[n][2 * half] + lh[n][2 * half]),
+                                        y = acc[n][2 * half + 1] + (hl[n][2 * half + 1] + lh[n][2 * half + 1]);
                             uint32_t hi, lo;
-                            split2(x, y, hi, lo);
+                            split2(sc <= tr ? x * exp2_fast((uh.x - mh) + (ul.x - ml)) : 0.0f,
+                                   sc + 1 <= tr ? y * exp2_fast((uh.y - mh) + (ul.y - ml)) : 0.0f, hi, lo);
                             const uint32_t to = tile_piece<C>(tr, 2 * cc + n) + 4 * t;
                             *reinterpret_cast<uint32_t *>(p0 + to) = hi;
                             *reinterpret_cast<uint32_t *>(p1 + to) = lo;
                         }
                     }
                 }
+                arrive(sm.qk_empty[st]);
                 fence_async_smem();
-                arrive(sm.p_full[st]);
+                arrive(sm.p_full);
             }
         }
     } else if (w < kWarpV) {
-        // ------------------------------------------------------------ queries and keys
-        constexpr int STEPS = C / 8, DEPTH = 3;   // two rows of each a step
+        // ------------------------------------------------------------ rows: parts of queries and keys, factors
+        // warp wl has the rows 16 wl .. of a chunk, in slots of four: two slots on their way
+        constexpr int SLOTS = C / 4 / kRawRows;
+        static_assert(kRawRows == 4 && SLOTS == 4, "steps of two rows in slots of four");
         const int wl = w - kWarpL;
         const int none[2] = {0, 0};
+        int asked = 0;
+        auto request = [&](int i) {   // slot i, counted from the segment's start
+            if (i >= chunks * SLOTS || *abort_flag) return;
+            asked = i + 1;
+            if (lane == 0) {
+                typename Smem<DK, DV>::Raw &r = sm.raw[wl][i & 1];
+                uint64_t *bar = &sm.raw_full[wl][i & 1];
+                const int row = seg.row0 + i / SLOTS * C + 16 * wl + i % SLOTS * kRawRows;
+                mbar_arrive_expect_tx(bar, kRawRows * 4 * (STATES ? 1 : 2) * DK);
+                if (!STATES) tma_load_2d(r.q, &map_q, hk * DK, row, bar);
+                tma_load_2d(r.k, &map_k, hk * DK, row, bar);
+            }
+            __syncwarp();
+        };
+        request(0);
+        request(1);
+        // steps of two rows: while one is converted the next is read and its largest magnitudes are found
+        struct Step {
+            Rows<DK> q, k;
+            uint32_t mq[2], mk[2];
+        } step[2];
+        auto read = [&](Step &x, int i) {   // step i of the segment
+            if (i >= chunks * (C / 8)) return;
+            const int slot = i >> 1, pair = i & 1, r = 16 * wl + 2 * (i & 7);
+            if (!pair) wait(sm.raw_full[wl][slot & 1], slot >> 1);
+            const typename Smem<DK, DV>::Raw &raw = sm.raw[wl][slot & 1];
+            if (!STATES) x.q.load_shared(raw.q + 2 * pair * DK);
+            x.k.load_shared(raw.k + 2 * pair * DK);
+            const int n = seg.row1 - seg.row0 - (i >> 3) * C;
+            if (r + 2 > n) {
+                if (!STATES) x.q.cut(r, n);
+                x.k.cut(r, n);
+            }
+            if (!STATES) x.q.template largest<false>(x.mq[0], x.mq[1]);
+            x.k.template largest<false>(x.mk[0], x.mk[1]);
+            if (pair) {
+                fence_async_smem();   // the slot is read before the next copy writes it
+                __syncwarp();
+                request(slot + 2);
+            }
+        };
+        read(step[0], 0);
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
             const long long row = seg.row0 + c * C;
             const int n = seg.row1 - (int)row;
-            const float *q = a.q + row * a.q_stride + (long long)hk * DK, *k = a.k + row * a.k_stride + (long long)hk * DK;
-            Rows<DK> qr[DEPTH], kr[DEPTH];
-            auto fetch = [&](int j) {
-                const int r = 2 * (wl + 4 * j);
-                if (!STATES) qr[j % DEPTH].load(q, a.q_stride, r, n);
-                kr[j % DEPTH].load(k, a.k_stride, r, n);
-            };
-#pragma unroll
-            for (int j = 0; j < DEPTH - 1; ++j) fetch(j);
-            if (c >= 2) wait(sm.qk_empty[st], (c >> 1) - 1);
-#pragma unroll
-            for (int j = 0; j < STEPS; ++j) {
-                if (j + DEPTH - 1 < STEPS) fetch(j + DEPTH - 1);
-                const int r = 2 * (wl + 4 * j);
-                auto convert = [&](const Rows<DK> &x, __half(&dst)[2][C * DK], int *exponents) {
-                    uint32_t m[2];
-                    x.largest(m);
-                    const int e[2] = {row_exponent(m[0]), row_exponent(m[1])};
-                    // a row of zeros is told apart; an infinity or NaN gives parts that are NaN, and so a row of NaN
-                    if (lane < 2) exponents[r + lane] = (lane ? m[1] : m[0]) ? (lane ? e[1] : e[0]) : INT_MIN;
-                    x.store(dst[0], dst[1], r, e, none, tile_piece<DK>);
-                };
-                if (!STATES) convert(qr[j % DEPTH], sm.q[st], sm.eq[st]);
-                convert(kr[j % DEPTH], sm.k[st], sm.ek[st]);
-            }
-            fence_async_smem();
-            arrive(sm.qk_full[st]);
-        }
-    } else if (w < kWarpE) {
-        // ------------------------------------------------------------ values and factors
-        const int quarter = w & 3, column = 32 * quarter + lane;   // tensor memory lanes of this warp
-        const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-        const bool maker = quarter == 3;
-        for (int c = 0; c < chunks; ++c) {
-            const long long row = seg.row0 + c * C;
-            const int n = seg.row1 - (int)row;
-            const float *v = a.v + row * a.v_stride + (long long)h * p.Dv + col0 + column;
-            float x[C];
-#pragma unroll
-            for (int s = 0; s < C; ++s) x[s] = s < n ? v[s * a.v_stride] : 0.0f;
+            const bool maker = (c & 3) == wl;
             float g[2] = {0.0f, 0.0f};
             if (maker && a.g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (2 * lane + i < n) g[i] = a.g[(row + 2 * lane + i) * a.g_stride + h];
-#pragma unroll
-            for (int s = 0; s < C; ++s) {
-                const uint32_t m = __reduce_max_sync(0xffffffffu, magnitude(x[s]));
-                if (lane == (s & 31)) sm.vmax[quarter][s] = m;
+            if (c >= 2) {
+                if (wl == 0) wait(sm.qk_empty[st], (c >> 1) - 1);
+                sync(kWarpL);
             }
-            named_bar(1, 128);
-            int ev[2] = {0, 0};
-            bool bad[2] = {false, false}, zero[2] = {false, false};
-            if (maker) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int s = 2 * lane + i;
-                    const uint32_t m = max(max(sm.vmax[0][s], sm.vmax[1][s]), max(sm.vmax[2][s], sm.vmax[3][s]));
-                    ev[i] = row_exponent(m);
-                    zero[i] = m == 0u;
-                    // a token whose value or decay is not finite: its weights become NaN, and so its own row, all
-                    // later ones and the state; the value itself must not meet the zero weights of earlier rows
-                    bad[i] = m >= 0x7f800000u || g[i] != g[i];
-                    sm.vscale[s] = bad[i] ? 0.0f : pow2(-ev[i]);
-                }
-                const int some = __any_sync(0xffffffffu, bad[0] || bad[1]);
-                if (lane == 0) sm.any_bad = some;
-            }
-            named_bar(1, 128);
-            if (sm.any_bad)
-#pragma unroll
-                for (int s = 0; s < C; ++s) x[s] = sm.vscale[s] == 0.0f ? 0.0f : x[s];
-            if (maker) {
-                wait(sm.qk_full[c & 1], c >> 1);
-                Factors &f = sm.f[c & 3];
-                int ekv[2], eq[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int s = 2 * lane + i, ek = sm.ek[c & 1][s];
-                    ekv[i] = !bad[i] && (zero[i] || ek == INT_MIN) ? INT_MIN : (bad[i] ? 0 : ev[i]) + max(ek, -126);
-                    eq[i] = STATES ? 0 : max(sm.eq[c & 1][s], -126);
-                }
-                make_factors(f, g, ekv, eq, a.scale);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int s = 2 * lane + i;
-                    if (bad[i]) f.uh[s] = __int_as_float(0x7fc00000);
-                    sm.wscale[s] = bad[i] ? __int_as_float(0x7fc00000) : f.w[s] * pow2(-ev[i]);
-                }
-                arrive(sm.fact[c & 3]);
-            }
-            // the last chunk's MMAs have read what is written now
-            if (c) wait(STATES ? sm.u_full : sm.o_full, c - 1);
-            tc_fence_after();
-            auto parts = [&](const float *scale, int hi, int lo) {
-#pragma unroll
-                for (int b = 0; b < C / 16; ++b) {
-                    uint32_t ph[8], pl[8];
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float2 f = *reinterpret_cast<const float2 *>(scale + 16 * b + 2 * i);
-                        split2(x[16 * b + 2 * i] * f.x, x[16 * b + 2 * i + 1] * f.y, ph[i], pl[i]);
-                    }
-                    tmem_st8(lanes + hi + 8 * b, ph);
-                    tmem_st8(lanes + lo + 8 * b, pl);
+            auto convert = [&](const Step &x, int j) {
+                const int r = 16 * wl + 2 * j;
+                // an infinity or NaN gives parts that are NaN
+                if (!STATES)
+                    x.q.store(sm.q[st][0], sm.q[st][1], r, {row_exponent(x.mq[0]), row_exponent(x.mq[1])}, none,
+                              tile_piece<DK>);
+                x.k.store(sm.k[st][0], sm.k[st][1], r, {row_exponent(x.mk[0]), row_exponent(x.mk[1])}, none, tile_piece<DK>);
+                if (lane < 2) {
+                    if (!STATES) sm.mq[st][r + lane] = lane ? x.mq[1] : x.mq[0];
+                    sm.mk[st][r + lane] = lane ? x.mk[1] : x.mk[0];
                 }
             };
-            if (!STATES) parts(sm.vscale, kVh, kVl);
-            named_bar(1, 128);
-            parts(sm.wscale, kWh, kWl);
-            tmem_wait_st();
-            tc_fence_before();
-            arrive(sm.v_full);
+#pragma unroll 1
+            for (int j = 0; j < C / 8; j += 2) {
+                read(step[1], c * (C / 8) + j + 1);
+                convert(step[0], j);
+                read(step[0], c * (C / 8) + j + 2);
+                convert(step[1], j + 1);
+            }
+            fence_async_smem();
+            arrive(sm.qk_full[st]);
+            // the sizes of the values' rows
+            if (wl == 0) wait(sm.values, c);
+            sync(kWarpL);
+#pragma unroll 1
+            for (int r = 16 * wl; r < 16 * wl + 16; r += 8) {
+                Rows<DV> v[4];
+                uint32_t m[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i].load_shared(sm.v + (r + 2 * i) * DV);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i].largest(m[2 * i], m[2 * i + 1]);
+                if (lane == 0) {
+                    *reinterpret_cast<uint4 *>(&sm.mv[st][r]) = make_uint4(m[0], m[1], m[2], m[3]);
+                    *reinterpret_cast<uint4 *>(&sm.mv[st][r + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
+                }
+            }
+            arrive(sm.sizes);
+            if (maker) {
+                wait(sm.sizes, c);
+                typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
+                int ekv[2], eq[2], ev[2];
+                bool bad[2], odd[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int s = 2 * lane + i;
+                    const uint32_t mk = sm.mk[st][s], mv = sm.mv[st][s];
+                    ev[i] = row_exponent(mv);
+                    // a token whose value or decay is not finite: its weights become NaN, and so its own row, all
+                    // later ones and the state; the value itself must not meet the zero weights of earlier rows.  (One
+                    // of the key does the same by the key's parts.)
+                    bad[i] = s < n && (mv >= 0x7f800000u || g[i] != g[i]);
+                    odd[i] = mv >= 0x7f800000u || bad[i];   // (the rows behind the last are somebody else's)
+                    ekv[i] = !bad[i] && (s >= n || mk == 0u || mv == 0u) ? INT_MIN : ev[i] + row_exponent(mk);
+                    eq[i] = STATES ? 0 : row_exponent(sm.mq[st][s]);
+                }
+                make_factors(f, g, ekv, eq, a.scale);
+                const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int s = 2 * lane + i;
+                    const float x = pow2(-ev[i]);
+                    if (bad[i]) f.uh[s] = nan;
+                    f.vscale[s] = bad[i] || s >= n ? 0.0f : x;
+                    f.wscale[s] = s >= n ? 0.0f : bad[i] ? nan : f.w[s] * x;
+                }
+                const int some = __any_sync(0xffffffffu, odd[0] || odd[1]);
+                if (lane == 0) f.some_bad = some;
+                arrive(sm.fact[c & 3]);
+            }
         }
+        // copies still on their way when a wait has run out
+        for (int i = max(0, asked - 2); i < asked; ++i) mbar_wait_for(&sm.raw_full[wl][i & 1], (i >> 1) & 1, nullptr, 1000000ull);
+    } else if (w < kWarpE) {
+        // ------------------------------------------------------------ values
+        const int quarter = w & 3, column = 32 * quarter + lane;   // tensor memory lanes of this warp
+        const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
+        const int last = quarter < QUARTERS ? chunks : 0;
+        int asked = 0;
+        auto request = [&](int c) {   // the values of a chunk
+            if (c < chunks && w == kWarpV && !*abort_flag) {
+                asked = c + 1;
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(&sm.values, C * DV * 4);
+                    tma_load_2d(sm.v, &map_v, h * p.Dv + col0, seg.row0 + c * C, &sm.values);
+                }
+                __syncwarp();
+            }
+        };
+        request(0);
+        for (int c = 0; c < last; ++c) {
+            const typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
+            // weighted for the state, then as they are for the output; read twice rather than kept (the code of a
+            // kernel with so many kinds of warps has to stay small: unrolled over 64 tokens it ran at half the speed)
+#pragma unroll 1
+            for (int pass = 0; pass < (STATES ? 1 : 2); ++pass) {
+                if (w == kWarpV) {
+                    if (!pass) {
+                        wait(sm.values, c);
+                        wait(sm.fact[c & 3], c >> 2);
+                    }
+                    // the last chunk's MMAs have read what is written now
+                    if (c) wait(pass ? sm.o_full : sm.u_full, c - 1);
+                }
+                sync(kWarpV);
+                tc_fence_after();
+                const float *scale = pass ? f.vscale : f.wscale;
+                uint32_t to = lanes + (pass ? kVh : kWh);
+#pragma unroll 1
+                for (int b = 0; b < C / 16; ++b, to += 8) {
+                    float x[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) x[i] = sm.v[(16 * b + i) * DV + column];
+                    if (f.some_bad)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) x[i] = f.vscale[16 * b + i] == 0.0f ? 0.0f : x[i];
+                    uint32_t ph[8], pl[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i += 2) {
+                        const float4 y = *reinterpret_cast<const float4 *>(scale + 16 * b + 2 * i);
+                        split2(x[2 * i] * y.x, x[2 * i + 1] * y.y, ph[i], pl[i]);
+                        split2(x[2 * i + 2] * y.z, x[2 * i + 3] * y.w, ph[i + 1], pl[i + 1]);
+                    }
+                    tmem_st8(to, ph);
+                    tmem_st8(to + (kVl - kVh), pl);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                arrive(pass ? sm.v_full : sm.w_full);
+            }
+            fence_async_smem();   // the values are read before the next ones come
+            sync(kWarpV);
+            request(c + 1);
+        }
+        // a copy still on its way when a wait has run out
+        if (asked) mbar_wait_for(&sm.values, (asked - 1) & 1, nullptr, 1000000ull);
     } else {
         // ------------------------------------------------------------ state and output
-        const int quarter = w & 3, half = (w - kWarpE) >> 2, column = 32 * quarter + lane;
+        const int quarter = w & 3, part = (w - kWarpE) >> 2, column = 32 * quarter + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-        constexpr int N = DK / 2;   // values of the state of a thread: rows half * N ..
+        constexpr int N = DK / 4;   // values of the state of a thread: rows part * N ..
         const bool cut = p.length != 0 && (seg.seg > 0 || !seg.last);
         const int slot = any ? a.slots[seg.seq] : -1;
         const bool kept = slot >= 0 && slot < a.n;
-        const long long place = (long long)half * N * p.Dv + col0 + column;
+        const long long place = (long long)part * N * p.Dv + col0 + column;
         float *local = p.local + ((long long)at * a.Hv + h) * DK * p.Dv + place;
         float *pool = a.state + ((long long)(kept ? slot : 0) * a.Hv + h) * DK * p.Dv + place;
-        const bool zeros = !any || STATES || (!cut && (!kept || (a.fresh && a.fresh[seg.seq] != 0)));
+        const bool mine = any && quarter < QUARTERS;
+        const int last = mine ? chunks : 0;
+        const bool zeros = !mine || STATES || (!cut && (!kept || (a.fresh && a.fresh[seg.seq] != 0)));
         float S[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) S[i] = zeros ? 0.0f : (cut ? local : pool)[(long long)i * p.Dv];
         long long G = 0;
+        // the registers hold S / 2^exponent, the exponent kept while the column's largest magnitude stays within
+        // 1 .. 2^15, set anew for 2^8 .. 2^9 when it leaves
         int exponent = 0;
-        // the state's parts for the next product with the queries
-        auto publish = [&]() {
-            uint32_t m = 0;
+        auto rescale = [&](int to) {
+            to = max(-126, min(126, to));
+            const float s = pow2(max(-126, min(126, exponent - to)));
+            exponent = to;
 #pragma unroll
-            for (int i = 0; i < N; ++i) m = max(m, magnitude(S[i]));
-            sm.smax[half][column] = m;
-            named_bar(2, 256);
-            m = max(m, sm.smax[half ^ 1][column]);
-            exponent = row_exponent(m);
-            const float s = pow2(-exponent);
+            for (int i = 0; i < N; ++i) S[i] *= s;
+        };
+        // the state's parts for the next product with the queries; between: what has to be over before they are written
+        auto publish = [&](auto between) {
+            float most = 0.0f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) most = fmaxf(most, fabsf(S[i]));   // (a NaN needs no scale)
+            sm.smax[part][column] = __float_as_uint(most);
+            between();
+            sync(kWarpE);
+            tc_fence_after();
+            const uint32_t m = max(max(sm.smax[0][column], sm.smax[1][column]), max(sm.smax[2][column], sm.smax[3][column]));
+            if (__any_sync(0xffffffffu, m < 0x3f800000u || m >= 0x47000000u))
+                rescale(m == 0u ? 0 : exponent + row_exponent(m) - 8);
 #pragma unroll
             for (int b = 0; b < N / 16; ++b) {
                 uint32_t ph[8], pl[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split2(S[16 * b + 2 * i] * s, S[16 * b + 2 * i + 1] * s, ph[i], pl[i]);
-                tmem_st8(lanes + kSh + half * (N / 2) + 8 * b, ph);
-                tmem_st8(lanes + kSl + half * (N / 2) + 8 * b, pl);
+                for (int i = 0; i < 8; ++i) split2(S[16 * b + 2 * i], S[16 * b + 2 * i + 1], ph[i], pl[i]);
+                tmem_st8(lanes + kSh + part * (N / 2) + 8 * b, ph);
+                tmem_st8(lanes + kSl + part * (N / 2) + 8 * b, pl);
             }
             tmem_wait_st();
             tc_fence_before();
-            named_bar(2, 256);   // the maxima are read before the next ones are written
             arrive(sm.s_full);
         };
-        if (!STATES && chunks) publish();
-        for (int c = 0; c < chunks; ++c) {
+        if (!STATES && last) publish([] {});
+        for (int c = 0; c < last; ++c) {
             const Factors &f = sm.f[c & 3];
-            wait(sm.fact[c & 3], c >> 2);
-            wait(sm.u_full, c);
+            if (w == kWarpE) {
+                wait(sm.fact[c & 3], c >> 2);
+                wait(sm.u_full, c);
+            }
+            sync(kWarpE);   // (the maxima of the last chunk have been read, too)
             tc_fence_after();
-            const float keep = f.keep, add = f.add;
+            const float xs = pow2(exponent);   // of the state that O1 was made with
+            const float keep = f.keep;
+            float add = f.add * pow2(-exponent);
+            // what is added is far above the state: by its size, before it overflows
+            if (__any_sync(0xffffffffu, !(add < 0x1p40f))) {
+                rescale(max(exponent, row_exponent(magnitude(f.add))));
+                add = f.add * pow2(-exponent);
+            }
 #pragma unroll
             for (int b = 0; b < N / 16; ++b) {
                 uint32_t u[16];
-                tmem_ld16(lanes + kU + half * N + 16 * b, u);
+                tmem_ld16(lanes + kU + part * N + 16 * b, u);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; ++i) S[16 * b + i] = __fmaf_rn(add, __uint_as_float(u[i]), keep * S[16 * b + i]);
             }
-            G = clamp_units(G + f.G);
+            if (STATES) G = clamp_units(G + f.G);
             tc_fence_before();
             arrive(sm.u_empty);
             if (STATES) continue;
-            wait(sm.o_full, c);
-            tc_fence_after();
-            const float xs = pow2(exponent);
-            if (c + 1 < chunks) publish();
-            const int n = seg.row1 - seg.row0 - c * C;
-            float *out = a.out + (long long)(seg.row0 + c * C + 32 * half) * a.out_stride + (long long)h * p.Dv + col0 + column;
-#pragma unroll
-            for (int b = 0; b < 4; ++b) {
+            auto products = [&] {
+                if (w == kWarpE) wait(sm.o_full, c);
+            };
+            if (c + 1 < chunks) {
+                publish(products);
+            } else {
+                products();
+                sync(kWarpE);
+                tc_fence_after();
+            }
+            const int n = seg.row1 - seg.row0 - c * C - 16 * part;
+            float *out = a.out + (long long)(seg.row0 + c * C + 16 * part) * a.out_stride + (long long)h * p.Dv + col0;
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b) {
                 uint32_t o1[8], o2[8];
-                tmem_ld8(lanes + kO1 + 32 * half + 8 * b, o1);
-                tmem_ld8(lanes + kO2 + 32 * half + 8 * b, o2);
+                tmem_ld8(lanes + kO1 + 16 * part + 8 * b, o1);
+                tmem_ld8(lanes + kO2 + 16 * part + 8 * b, o2);
                 tmem_wait_ld();
+                float y[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const int t = 32 * half + 8 * b + i;
-                    const float y = __fmaf_rn(f.f1[t], __uint_as_float(o2[i]), f.f2[t] * (__uint_as_float(o1[i]) * xs));
-                    if (t < n) out[(8 * b + i) * a.out_stride] = y;
+                for (int i = 0; i < 8; i += 4) {
+                    const float4 f1 = *reinterpret_cast<const float4 *>(&f.f1[16 * part + 8 * b + i]),
+                                 f2 = *reinterpret_cast<const float4 *>(&f.f2[16 * part + 8 * b + i]);
+                    auto one = [&](int j, float u, float v) {
+                        return __fmaf_rn(u, __uint_as_float(o2[j]), v * (__uint_as_float(o1[j]) * xs));
+                    };
+                    y[i] = one(i, f1.x, f2.x);
+                    y[i + 1] = one(i + 1, f1.y, f2.y);
+                    y[i + 2] = one(i + 2, f1.z, f2.z);
+                    y[i + 3] = one(i + 3, f1.w, f2.w);
+                }
+                if (8 * b + 8 <= n) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) (out + (8 * b + i) * a.out_stride)[(unsigned)column] = y[i];
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        if (8 * b + i < n) (out + (8 * b + i) * a.out_stride)[(unsigned)column] = y[i];
                 }
             }
             tc_fence_before();
             arrive(sm.o_empty);
         }
-        if (any && (STATES || (kept && seg.last))) {
+        if (mine && (STATES || (kept && seg.last))) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) (STATES ? local : pool)[(long long)i * p.Dv] = S[i];
+            for (int i = 0; i < N; ++i) (STATES ? local : pool)[(long long)i * p.Dv] = S[i] * pow2(exponent);
         }
         if (STATES && any && tile == 0 && w == kWarpE && lane == 0) p.decay[(long long)at * a.Hv + h] = G;
     }
@@ -485,12 +645,12 @@ __global__ void __launch_bounds__(kThreads, 1) linear_prompt_tc_kernel(const __g
     }
 }
 
-template <int DK, bool STATES>
+template <int DK, int DV, bool STATES>
 cudaError_t launch(const PromptArgs &p, cudaStream_t st)
 {
     static std::atomic<bool> ready[64];
-    auto *kernel = linear_prompt_tc_kernel<DK, STATES>;
-    constexpr int smem = sizeof(Smem<DK>) + 1024;
+    auto *kernel = linear_prompt_tc_kernel<DK, DV, STATES>;
+    constexpr int smem = sizeof(Smem<DK, DV>) + 1024;
     static_assert(smem <= 227 * 1024, "a CTA's shared memory");
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -500,18 +660,34 @@ cudaError_t launch(const PromptArgs &p, cudaStream_t st)
         if (e != cudaSuccess) return e;
         ready[dev & 63].store(true, std::memory_order_release);
     }
-    const long long ctas = (long long)p.segments * p.a.Hv * (p.Dv / 128);
+    const long long ctas = (long long)p.segments * p.a.Hv * (p.Dv / DV);
     PromptArgs args = p;
     args.status = device_status_word();
-    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, st, args);
+    const LinearAttnArgs &a = p.a;
+    CUtensorMap map[3];
+    auto rows = [&](int i, const float *x, int heads, int D, long long stride) {
+        const uint64_t cols = (uint64_t)heads * D;
+        return make_tmap_rows_f32(&map[i], x, cols, a.T, a.T > 1 ? (uint64_t)stride : cols, i < 2 ? DK : DV,
+                                  i < 2 ? kRawRows : C);
+    };
+    if ((e = rows(0, a.q, a.Hk, DK, a.q_stride)) != cudaSuccess || (e = rows(1, a.k, a.Hk, DK, a.k_stride)) != cudaSuccess ||
+        (e = rows(2, a.v, a.Hv, p.Dv, a.v_stride)) != cudaSuccess)
+        return e;
+    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, st, args, map[0], map[1], map[2]);
+}
+
+template <int DK, int DV>
+cudaError_t launch_either(const PromptArgs &p, bool states, cudaStream_t st)
+{
+    return states ? launch<DK, DV, true>(p, st) : launch<DK, DV, false>(p, st);
 }
 
 }  // namespace
 
 cudaError_t launch_linear_prompt_tc(const PromptArgs &p, int Dk, bool states, cudaStream_t st)
 {
-    if (Dk == 64) return states ? launch<64, true>(p, st) : launch<64, false>(p, st);
-    return states ? launch<128, true>(p, st) : launch<128, false>(p, st);
+    if (Dk == 64) return p.Dv == 64 ? launch_either<64, 64>(p, states, st) : launch_either<64, 128>(p, states, st);
+    return p.Dv == 64 ? launch_either<128, 64>(p, states, st) : launch_either<128, 128>(p, states, st);
 }
 
 }  // namespace zq

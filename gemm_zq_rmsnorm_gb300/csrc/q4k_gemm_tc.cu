@@ -236,6 +236,18 @@ cudaError_t make_tmap_u8(CUtensorMap *m, int rank, const void *base, const uint6
     });
 }
 
+cudaError_t make_tmap_rows_f32(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t stride,
+                               uint32_t box_cols, uint32_t box_rows)
+{
+    const cuuint64_t dims[2] = {cols, rows}, strides[1] = {stride * 4};
+    const cuuint32_t box[2] = {box_cols, box_rows}, estr[2] = {1, 1};
+    return encode_tmap([&](EncodeTiledFn fn) {
+        return fn(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, const_cast<void *>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    });
+}
+
 cudaError_t launch_q8_to_f16(const int8_t *qs, __half *out, size_t n, cudaStream_t st)
 {
     const size_t n16 = n / 16;

@@ -74,6 +74,10 @@ cudaError_t make_tmap_2d(CUtensorMap *m, CUtensorMapDataType dt, uint32_t esize,
 cudaError_t make_tmap_u8(CUtensorMap *m, int rank, const void *base, const uint64_t *dims, const uint64_t *strides,
                          const uint32_t *box, CUtensorMapSwizzle sw);
 
+// fp32 rows of `cols` values, `stride` floats apart, box box_cols x box_rows.
+cudaError_t make_tmap_rows_f32(CUtensorMap *m, const void *base, uint64_t cols, uint64_t rows, uint64_t stride,
+                               uint32_t box_cols, uint32_t box_rows);
+
 // q8 activation codes -> fp16 (exact), n codes, n a multiple of 16.
 cudaError_t launch_q8_to_f16(const int8_t *qs, __half *out, size_t n, cudaStream_t st);
 
