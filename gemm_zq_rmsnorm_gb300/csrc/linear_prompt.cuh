@@ -232,18 +232,21 @@ struct Rows {
                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
         }
     }
+    // the same rows, or later ones, into L2: one request a 128-byte line
+    __device__ __forceinline__ void ahead(const float *p, long long stride, int r, int n) const
+    {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int at = r + row(i);
+            if (at < n && (lane() & 7) == 0)
+                asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at * stride + 4 * lane()));
+        }
+    }
     // from rows in shared memory, one after another
     __device__ __forceinline__ void load_shared(const float *p)
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) x[i] = reinterpret_cast<const float4 *>(p + row(i) * D)[lane()];
-    }
-    // rows r, r + 1: zeros from row n on
-    __device__ __forceinline__ void cut(int r, int n)
-    {
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            if (r + row(i) >= n) x[i] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     }
     // bits of the largest magnitude of both rows, in every lane; NANS: a NaN is the largest (else it is passed over)
     template <bool NANS = true>

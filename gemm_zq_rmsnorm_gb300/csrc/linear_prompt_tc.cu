@@ -11,12 +11,11 @@
 // stays in the registers of sixteen warps (four threads for a column), which add U to
 // it, split it for the next chunk and put O1 and O2 together.
 //
-// Warps: 0 issues the MMAs; 1..3 compute the scores and weights P (mma.sync: 64 x 64
-// on and below the diagonal is too small a tile); 4..7 convert queries and keys;
-// 8..11 values, a lane for a column (128-byte loads), and the chunk's factors;
-// 12..27 the state.  Keys and queries are two stages deep, P too; the key tile serves
-// the scores as rows and U as columns (the same bytes, a descriptor of the other
-// order).
+// and the scores Q K^T the same way.  Warps: 0 and 1 weigh scores; 2 issues the MMAs; 3
+// makes the chunk's factors; 4..11 convert queries and keys; 12..15 values, a lane for
+// a column; 16..31 the state.  Keys and queries are two stages deep; the key tile
+// serves the scores as rows and U as columns (the same bytes, a descriptor of the
+// other order).
 //
 // Every wait is bounded: after one has run out no MMA is issued any more, the
 // others return at once and the kernel ends (its results are invalid).
@@ -29,30 +28,27 @@ namespace zq {
 namespace {
 
 constexpr int C = kChunk;
-constexpr int kWarpP = 1, kWarpL = 4, kWarpV = 8, kWarpE = 12, kWarps = 28;   // first warp of each role; 0 issues
+constexpr int kWarpM = 2, kWarpF = 3, kWarpL = 4, kWarpV = 12, kWarpE = 16, kWarps = 32;   // first of each role
+constexpr int LW = kWarpV - kWarpL;
+constexpr int kLoadRows = C / LW;  // rows of a chunk of a warp that converts
 constexpr int kThreads = kWarps * 32;
 // tensor memory columns
 constexpr int kO1 = 0, kO2 = 64, kU = 128, kSh = 256, kSl = 320, kVh = 384, kVl = 416, kWh = 448, kWl = 480;
 static_assert(kVl - kVh == kWl - kWh, "low parts behind high ones");
 
-constexpr int kRawRows = 4;        // rows of a copy
-
 template <int DK, int DV>
 struct Smem {
     __half q[2][2][C * DK], k[2][2][C * DK];   // [stage][part]: rows in tiles of 64 columns, 128-byte swizzle
     __half p[2][C * C];                        // [part], rows of 64 tokens
-    struct Raw {                               // rows as they come, of one converting warp
-        float q[kRawRows * DK], k[kRawRows * DK];
-    } raw[4][2];
-    float v[C * DV];                           // values as they come
+    float v[2][C * DV];                        // [chunk's parity]: values as they come
     struct alignas(16) Chunk : Factors {       // read four values at a time
         float vscale[C], wscale[C];            // 2^-e of the values' rows, and that times w
         int some_bad;
     } f[4];
     alignas(16) uint32_t mq[2][C], mk[2][C], mv[2][C];   // bits of the rows' largest magnitudes
     uint32_t smax[4][128];
-    uint64_t raw_full[4][2], qk_full[2], qk_empty[2], fact[4];
-    uint64_t values, sizes, p_full, w_full, v_full, s_full, o_full, o_empty, u_full, u_empty;
+    uint64_t qk_full[2], qk_empty[2], values[2], fact[4];
+    uint64_t scores, scores_read, sizes, p_full, w_full, v_full, s_full, o_full, o_empty, u_full, u_empty;
     uint32_t tmem;
     int abort;
     Segment seg;
@@ -76,7 +72,7 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
 // instruction cache) with the ones that work, so the loop is as short as it can be,
 // and of every group of warps one waits here while the others sleep in a named
 // barrier; the limit and the others' failure are looked at every 512 probes.
-__device__ __forceinline__ void wait_phase(uint64_t *bar, int parity, volatile int *abort_flag, unsigned int *status)
+__device__ __noinline__ void wait_long(uint64_t *bar, int parity, volatile int *abort_flag, unsigned int *status)
 {
     uint64_t since = 0;
     for (;;) {
@@ -108,13 +104,47 @@ __device__ __forceinline__ void wait_phase(uint64_t *bar, int parity, volatile i
     }
 }
 
+__device__ __forceinline__ void wait_phase(uint64_t *bar, int parity, volatile int *abort_flag, unsigned int *status)
+{
+    if (!__all_sync(0xffffffffu, mbar_try_wait(bar, (uint32_t)(parity & 1)))) wait_long(bar, parity, abort_flag, status);
+}
+
 // B from columns: bit 16 of the instruction descriptor
 __host__ __device__ constexpr uint32_t idesc_b_columns(uint32_t M, uint32_t N) { return idesc_f16_f32(M, N) | 1u << 16; }
 
+// Sixteen columns of the scores, from tensor memory: weighted, as parts, to P.  The
+// warp has the rows 32 quarter .., a lane each; columns 16 j ...
+template <int DK, int DV>
+__device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, uint32_t tmem, int quarter, int j)
+{
+    const int lane = threadIdx.x & 31, tr = 32 * quarter + lane;
+    uint32_t s[16];
+    tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + kU + 16 * j, s);
+    const float mh = f.mh[tr], ml = f.ml[tr];
+    tmem_wait_ld();
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; i += 2) {
+            const int sc = 16 * j + 8 * half + 2 * i;
+            const float4 uh = *reinterpret_cast<const float4 *>(&f.uh[sc]), ul = *reinterpret_cast<const float4 *>(&f.ul[sc]);
+            auto one = [&](int e, float h, float l) {
+                const float x = __uint_as_float(s[8 * half + 2 * i + e]) * exp2_fast((h - mh) + (l - ml));
+                return sc + e <= tr ? x : 0.0f;
+            };
+            split2(one(0, uh.x, ul.x), one(1, uh.y, ul.y), hi[i], lo[i]);
+            split2(one(2, uh.z, ul.z), one(3, uh.w, ul.w), hi[i + 1], lo[i + 1]);
+        }
+        const uint32_t to = tile_piece<C>(tr, 2 * j + half);
+        *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(sm.p[0]) + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(sm.p[1]) + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    }
+}
+
 template <int DK, int DV, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
-linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap map_q,
-                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
+linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap map_v)
 {
     constexpr int QUARTERS = DV / 32;   // of the tensor memory's lanes that are in use
     extern __shared__ char raw[];
@@ -127,28 +157,27 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     auto wait = [&](uint64_t &bar, int parity) { wait_phase(&bar, parity, abort_flag, status); };
     // the same for a group of warps: its first one waits, the others in its named barrier
     auto sync = [&](int group) {
-        named_bar(group == kWarpP ? 1 : group == kWarpL ? 2 : group == kWarpV ? 3 : 4,
-                  group == kWarpP ? 96 : group == kWarpL ? 128 : (group == kWarpE ? 4 : 1) * 32 * QUARTERS);
+        named_bar(group == kWarpL ? 2 : group == kWarpV ? 3 : 4,
+                  group == kWarpL ? 32 * LW : group == kWarpE ? 128 * QUARTERS : 128);
     };
     auto arrive = [&](uint64_t &bar) {   // one arrival of the warp
         __syncwarp();
         if (lane == 0) mbar_arrive(&bar);
     };
 
-    if (w == 0) tmem_alloc(&sm.tmem, 512);
+    if (w == kWarpM) tmem_alloc(&sm.tmem, 512);
     if (threadIdx.x == 32) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.qk_full[i], 4);
-            mbar_init(&sm.qk_empty[i], STATES ? 1 : 1 + 3);
+            mbar_init(&sm.qk_full[i], LW);
+            mbar_init(&sm.qk_empty[i], 1);
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(&sm.fact[i], 1);
-            mbar_init(&sm.raw_full[i][0], 1);
-            mbar_init(&sm.raw_full[i][1], 1);
-        }
-        mbar_init(&sm.values, 1);
-        mbar_init(&sm.sizes, 4);
+        for (int i = 0; i < 4; ++i) mbar_init(&sm.fact[i], 1);
+        mbar_init(&sm.values[0], 1);
+        mbar_init(&sm.values[1], 1);
+        mbar_init(&sm.sizes, LW);
         mbar_init(&sm.p_full, 3);
+        mbar_init(&sm.scores, 1);
+        mbar_init(&sm.scores_read, 3);
         mbar_init(&sm.w_full, QUARTERS);
         mbar_init(&sm.v_full, QUARTERS);
         mbar_init(&sm.s_full, 4 * QUARTERS);
@@ -167,7 +196,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     const int tiles = p.Dv / DV;
     const int tile = blockIdx.x % tiles, item = blockIdx.x / tiles;
     const int h = item % a.Hv, at = item / a.Hv, col0 = tile * DV;
-    if (w == 4) {
+    if (w == kWarpL) {
         const Segment s = find_segment(p, at);
         if (lane == 0) sm.seg = s;
     }
@@ -182,20 +211,59 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     const bool any = seg.seq >= 0 && !(STATES && seg.last);
     const int hk = h / (a.Hv / a.Hk);
 
-    if (w == 0) {
+    if (w == kWarpM) {
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t id_u = idesc_b_columns(128, DK), id_o = idesc_f16_f32(128, C);
         const bool leader = elect_one();
-        for (int c = 0; c < chunks; ++c) {
-            const int st = c & 1, ph = c >> 1;
-            wait(sm.qk_full[st], ph);
-            wait(sm.w_full, c);
+        auto rows_at = [](uint32_t tile, int kk) {   // of a tile of rows, columns 16 kk ..
+            return smem_desc(tile + (kk >> 2) * (C * 128) + (kk & 3) * 32, 16, 1024, kLayoutSw128);
+        };
+        auto scores = [&](int c) {   // Q K^T in U's place; lanes 64 .. hold the product of whatever lies behind the queries
+            const int st = c & 1;
+            wait(sm.qk_full[st], c >> 1);
             if (c) wait(sm.u_empty, c - 1);
+            tc_fence_after();
+            const uint32_t qh = smem_u32(sm.q[st][0]), ql = smem_u32(sm.q[st][1]), kh = smem_u32(sm.k[st][0]),
+                           kl = smem_u32(sm.k[st][1]);
+            if (!*abort_flag && leader) {
+#pragma unroll 1
+                for (int i = 0; i < 3; ++i) {   // lo hi, hi lo, hi hi
+                    const uint32_t x = i == 0 ? ql : qh, y = i == 1 ? kl : kh;
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk) mma_f16(tmem + kU, rows_at(x, kk), rows_at(y, kk), id_o, i || kk);
+                }
+                mma_commit(&sm.scores);
+            }
+            __syncwarp();
+        };
+        if (!STATES && chunks) scores(0);
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1;
+            if (!STATES) {
+                wait(sm.s_full, c);
+                if (c) wait(sm.o_empty, c - 1);
+                tc_fence_after();
+                const uint32_t qh = smem_u32(sm.q[st][0]), ql = smem_u32(sm.q[st][1]);
+                if (!*abort_flag && leader) {
+#pragma unroll 1
+                    for (int i = 0; i < 3; ++i) {
+                        const uint32_t as = tmem + (i == 0 ? kSl : kSh), b = i == 1 ? ql : qh;
+#pragma unroll
+                        for (int kk = 0; kk < DK / 16; ++kk) mma_f16_ta(tmem + kO1, as + 8 * kk, rows_at(b, kk), id_o, i || kk);
+                    }
+                }
+                __syncwarp();
+                wait(sm.scores_read, c);
+            } else {
+                wait(sm.qk_full[st], c >> 1);
+                if (c) wait(sm.u_empty, c - 1);
+            }
+            wait(sm.w_full, c);
             tc_fence_after();
             const uint32_t kh = smem_u32(sm.k[st][0]), kl = smem_u32(sm.k[st][1]);
             if (!*abort_flag && leader) {
 #pragma unroll 1
-                for (int i = 0; i < 3; ++i) {   // lo hi, hi lo, hi hi
+                for (int i = 0; i < 3; ++i) {
                     const uint32_t av = tmem + (i == 0 ? kWl : kWh), b = i == 1 ? kl : kh;
 #pragma unroll
                     for (int kk = 0; kk < C / 16; ++kk)
@@ -203,27 +271,10 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                                    i || kk);
                 }
                 mma_commit(&sm.u_full);
-                if (STATES) mma_commit(&sm.qk_empty[st]);
-            }
-            __syncwarp();
-            if (STATES) continue;
-            wait(sm.s_full, c);
-            if (c) wait(sm.o_empty, c - 1);
-            tc_fence_after();
-            const uint32_t qh = smem_u32(sm.q[st][0]), ql = smem_u32(sm.q[st][1]);
-            if (!*abort_flag && leader) {
-#pragma unroll 1
-                for (int i = 0; i < 3; ++i) {
-                    const uint32_t as = tmem + (i == 0 ? kSl : kSh), b = i == 1 ? ql : qh;
-#pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk)
-                        mma_f16_ta(tmem + kO1, as + 8 * kk,
-                                   smem_desc(b + (kk >> 2) * (C * 128) + (kk & 3) * 32, 16, 1024, kLayoutSw128), id_o,
-                                   i || kk);
-                }
                 mma_commit(&sm.qk_empty[st]);
             }
             __syncwarp();
+            if (STATES) continue;
             wait(sm.v_full, c);
             wait(sm.p_full, c);
             tc_fence_after();
@@ -233,174 +284,128 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 for (int i = 0; i < 3; ++i) {
                     const uint32_t av = tmem + (i == 0 ? kVl : kVh), b = i == 1 ? p1 : p0;
 #pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk)
-                        mma_f16_ta(tmem + kO2, av + 8 * kk, smem_desc(b + kk * 32, 16, 1024, kLayoutSw128), id_o, i || kk);
+                    for (int kk = 0; kk < C / 16; ++kk) mma_f16_ta(tmem + kO2, av + 8 * kk, rows_at(b, kk), id_o, i || kk);
                 }
                 mma_commit(&sm.o_full);
             }
             __syncwarp();
+            if (c + 1 < chunks) scores(c + 1);
         }
-    } else if (w < kWarpL) {
-        // ------------------------------------------------------------ scores and weights
-        if (!STATES) {
-            const int g = lane >> 2, t = lane & 3, wp = w - kWarpP;
-            // blocks (r, c) of 16 x 16, c <= r: a row of four, a row of three, a row of two and one
-            const int first = wp ? 1 + 3 * wp : 0, end = wp ? 4 + 3 * wp : 4;
+    } else if (w < kWarpM) {
+        // ------------------------------------------------------------ weights of the scores
+        // warp 0 the rows 0 .. 31 (32 columns), warp 1 the first half of the rows 32 .. 63, a warp of the values the other
+        if (!STATES)
             for (int c = 0; c < chunks; ++c) {
-                const int st = c & 1, ph = c >> 1;
-                if (wp == 0) wait(sm.qk_full[st], ph);
-                sync(kWarpP);
-                const uint32_t q0 = smem_u32(sm.q[st][0]), q1 = smem_u32(sm.q[st][1]), k0 = smem_u32(sm.k[st][0]),
-                               k1 = smem_u32(sm.k[st][1]);
-                const Factors &f = sm.f[c & 3];
-                char *p0 = reinterpret_cast<char *>(sm.p[0]), *p1 = reinterpret_cast<char *>(sm.p[1]);
+                wait(sm.fact[c & 3], c >> 2);
+                if (c) wait(sm.o_full, c - 1);   // the last weights have been read
+                wait(sm.scores, c);
+                tc_fence_after();
 #pragma unroll 1
-                for (int i = first; i < end; ++i) {
-                    const int r = i < 4 ? 3 : i < 7 ? 2 : i < 9 ? 1 : 0, cc = i < 4 ? 3 - i : i < 7 ? 6 - i : i < 9 ? 8 - i : 0;
-                    // the products of a low part apart: the accumulator cuts off
-                    float acc[2][4] = {}, hl[2][4] = {}, lh[2][4] = {};
-                    const int ar = 16 * r + (lane & 15), br = 16 * cc + (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk) {
-                        uint32_t ah[4], al[4], bh[4], bl[4];
-                        const uint32_t ap = tile_piece<DK>(ar, 2 * kk + (lane >> 4)),
-                                       bp = tile_piece<DK>(br, 2 * kk + ((lane >> 3) & 1));
-                        ldsm4(ah, q0 + ap);
-                        ldsm4(bh, k0 + bp);
-                        ldsm4(al, q1 + ap);
-                        ldsm4(bl, k1 + bp);
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            mma16<ZQ_F16>(acc[n], ah[0], ah[1], ah[2], ah[3], bh[2 * n], bh[2 * n + 1]);
-                            mma16<ZQ_F16>(hl[n], ah[0], ah[1], ah[2], ah[3], bl[2 * n], bl[2 * n + 1]);
-                            mma16<ZQ_F16>(lh[n], al[0], al[1], al[2], al[3], bh[2 * n], bh[2 * n + 1]);
-                        }
-                    }
-                    if (i == first) {
-                        if (wp == 0) {
-                            wait(sm.fact[c & 3], c >> 2);
-                            if (c) wait(sm.o_full, c - 1);   // the weights have been read
-                        }
-                        sync(kWarpP);
-                    }
-#pragma unroll
-                    for (int half = 0; half < 2; ++half) {
-                        const int tr = 16 * r + g + 8 * half;
-                        const float mh = f.mh[tr], ml = f.ml[tr];
-#pragma unroll
-                        for (int n = 0; n < 2; ++n) {
-                            const int sc = 16 * cc + 8 * n + 2 * t;
-                            const float2 uh = *reinterpret_cast<const float2 *>(&f.uh[sc]),
-                                         ul = *reinterpret_cast<const float2 *>(&f.ul[sc]);
-                            const float x = acc[n][2 * half] + (hl[n][2 * half] + lh[n][2 * half]),
-                                        y = acc[n][2 * half + 1] + (hl[n][2 * half + 1] + lh[n][2 * half + 1]);
-                            uint32_t hi, lo;
-                            split2(sc <= tr ? x * exp2_fast((uh.x - mh) + (ul.x - ml)) : 0.0f,
-                                   sc + 1 <= tr ? y * exp2_fast((uh.y - mh) + (ul.y - ml)) : 0.0f, hi, lo);
-                            const uint32_t to = tile_piece<C>(tr, 2 * cc + n) + 4 * t;
-                            *reinterpret_cast<uint32_t *>(p0 + to) = hi;
-                            *reinterpret_cast<uint32_t *>(p1 + to) = lo;
-                        }
-                    }
-                }
-                arrive(sm.qk_empty[st]);
+                for (int j = 0; j < 2; ++j) weigh_scores<DK, DV>(sm, sm.f[c & 3], tmem, w, j);
+                tc_fence_before();
                 fence_async_smem();
+                arrive(sm.scores_read);
                 arrive(sm.p_full);
             }
-        }
-    } else if (w < kWarpV) {
-        // ------------------------------------------------------------ rows: parts of queries and keys, factors
-        // warp wl has the rows 16 wl .. of a chunk, in slots of four: two slots on their way
-        constexpr int SLOTS = C / 4 / kRawRows;
-        static_assert(kRawRows == 4 && SLOTS == 4, "steps of two rows in slots of four");
-        const int wl = w - kWarpL;
-        const int none[2] = {0, 0};
-        int asked = 0;
-        auto request = [&](int i) {   // slot i, counted from the segment's start
-            if (i >= chunks * SLOTS || *abort_flag) return;
-            asked = i + 1;
-            if (lane == 0) {
-                typename Smem<DK, DV>::Raw &r = sm.raw[wl][i & 1];
-                uint64_t *bar = &sm.raw_full[wl][i & 1];
-                const int row = seg.row0 + i / SLOTS * C + 16 * wl + i % SLOTS * kRawRows;
-                mbar_arrive_expect_tx(bar, kRawRows * 4 * (STATES ? 1 : 2) * DK);
-                if (!STATES) tma_load_2d(r.q, &map_q, hk * DK, row, bar);
-                tma_load_2d(r.k, &map_k, hk * DK, row, bar);
-            }
-            __syncwarp();
-        };
-        request(0);
-        request(1);
-        // steps of two rows: while one is converted the next is read and its largest magnitudes are found
-        struct Step {
-            Rows<DK> q, k;
-            uint32_t mq[2], mk[2];
-        } step[2];
-        auto read = [&](Step &x, int i) {   // step i of the segment
-            if (i >= chunks * (C / 8)) return;
-            const int slot = i >> 1, pair = i & 1, r = 16 * wl + 2 * (i & 7);
-            if (!pair) wait(sm.raw_full[wl][slot & 1], slot >> 1);
-            const typename Smem<DK, DV>::Raw &raw = sm.raw[wl][slot & 1];
-            if (!STATES) x.q.load_shared(raw.q + 2 * pair * DK);
-            x.k.load_shared(raw.k + 2 * pair * DK);
-            const int n = seg.row1 - seg.row0 - (i >> 3) * C;
-            if (r + 2 > n) {
-                if (!STATES) x.q.cut(r, n);
-                x.k.cut(r, n);
-            }
-            if (!STATES) x.q.template largest<false>(x.mq[0], x.mq[1]);
-            x.k.template largest<false>(x.mk[0], x.mk[1]);
-            if (pair) {
-                fence_async_smem();   // the slot is read before the next copy writes it
-                __syncwarp();
-                request(slot + 2);
-            }
-        };
-        read(step[0], 0);
+    } else if (w == kWarpF) {
+        // ------------------------------------------------------------ a chunk's factors
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
             const long long row = seg.row0 + c * C;
             const int n = seg.row1 - (int)row;
-            const bool maker = (c & 3) == wl;
             float g[2] = {0.0f, 0.0f};
-            if (maker && a.g)
+            if (a.g)
 #pragma unroll
                 for (int i = 0; i < 2; ++i)
                     if (2 * lane + i < n) g[i] = a.g[(row + 2 * lane + i) * a.g_stride + h];
-            if (c >= 2) {
-                if (wl == 0) wait(sm.qk_empty[st], (c >> 1) - 1);
-                sync(kWarpL);
+            wait(sm.qk_full[st], c >> 1);
+            wait(sm.sizes, c);
+            typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
+            int ekv[2], eq[2], ev[2];
+            bool bad[2], odd[2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int s = 2 * lane + i;
+                const uint32_t mk = sm.mk[st][s], mv = sm.mv[st][s];
+                ev[i] = row_exponent(mv);
+                // a token whose value or decay is not finite: its weights become NaN, and so its own row, all
+                // later ones and the state; the value itself must not meet the zero weights of earlier rows.  (One
+                // of the key does the same by the key's parts.)
+                bad[i] = s < n && (mv >= 0x7f800000u || g[i] != g[i]);
+                odd[i] = mv >= 0x7f800000u || bad[i];   // (the rows behind the last are somebody else's)
+                ekv[i] = !bad[i] && (s >= n || mk == 0u || mv == 0u) ? INT_MIN : ev[i] + row_exponent(mk);
+                eq[i] = STATES ? 0 : row_exponent(sm.mq[st][s]);
             }
+            make_factors(f, g, ekv, eq, a.scale);
+            const float nan = __int_as_float(0x7fc00000);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int s = 2 * lane + i;
+                const float x = pow2(-ev[i]);
+                if (bad[i]) f.uh[s] = nan;
+                f.vscale[s] = bad[i] || s >= n ? 0.0f : x;
+                f.wscale[s] = s >= n ? 0.0f : bad[i] ? nan : f.w[s] * x;
+            }
+            const int some = __any_sync(0xffffffffu, odd[0] || odd[1]);
+            if (lane == 0) f.some_bad = some;
+            arrive(sm.fact[c & 3]);
+        }
+    } else if (w < kWarpV) {
+        // ------------------------------------------------------------ rows: parts of queries and keys, factors
+        // warp wl has the rows kLoadRows wl .. of a chunk, in steps of two: the next two are on their way while two are
+        // converted, and those of the next chunk on their way to L2
+        constexpr int STEPS = kLoadRows / 2;
+        static_assert(STEPS % 2 == 0, "two steps a turn of the loop");
+        const int wl = w - kWarpL;
+        const int none[2] = {0, 0};
+        struct Step {
+            Rows<DK> q, k;
+        } step[2];
+        const int rows = chunks ? seg.row1 - seg.row0 : 0;
+        const float *qp = a.q + seg.row0 * a.q_stride + (long long)hk * DK, *kp = a.k + seg.row0 * a.k_stride + (long long)hk * DK;
+        auto read = [&](Step &x, int i) {   // step i of the segment
+            const int r = i / STEPS * C + kLoadRows * wl + 2 * (i % STEPS);
+            if (!STATES) x.q.load(qp, a.q_stride, r, rows);
+            x.k.load(kp, a.k_stride, r, rows);
+            if (!STATES) x.q.ahead(qp, a.q_stride, r + C, rows);
+            x.k.ahead(kp, a.k_stride, r + C, rows);
+        };
+        read(step[0], 0);
+        for (int c = 0; c < chunks; ++c) {
+            const int st = c & 1;
+            if (c >= 2) wait(sm.qk_empty[st], (c >> 1) - 1);
             auto convert = [&](const Step &x, int j) {
-                const int r = 16 * wl + 2 * j;
+                const int r = kLoadRows * wl + 2 * j;
+                uint32_t mq[2], mk[2];
+                if (!STATES) x.q.template largest<false>(mq[0], mq[1]);
+                x.k.template largest<false>(mk[0], mk[1]);
                 // an infinity or NaN gives parts that are NaN
                 if (!STATES)
-                    x.q.store(sm.q[st][0], sm.q[st][1], r, {row_exponent(x.mq[0]), row_exponent(x.mq[1])}, none,
-                              tile_piece<DK>);
-                x.k.store(sm.k[st][0], sm.k[st][1], r, {row_exponent(x.mk[0]), row_exponent(x.mk[1])}, none, tile_piece<DK>);
+                    x.q.store(sm.q[st][0], sm.q[st][1], r, {row_exponent(mq[0]), row_exponent(mq[1])}, none, tile_piece<DK>);
+                x.k.store(sm.k[st][0], sm.k[st][1], r, {row_exponent(mk[0]), row_exponent(mk[1])}, none, tile_piece<DK>);
                 if (lane < 2) {
-                    if (!STATES) sm.mq[st][r + lane] = lane ? x.mq[1] : x.mq[0];
-                    sm.mk[st][r + lane] = lane ? x.mk[1] : x.mk[0];
+                    if (!STATES) sm.mq[st][r + lane] = lane ? mq[1] : mq[0];
+                    sm.mk[st][r + lane] = lane ? mk[1] : mk[0];
                 }
             };
 #pragma unroll 1
-            for (int j = 0; j < C / 8; j += 2) {
-                read(step[1], c * (C / 8) + j + 1);
+            for (int j = 0; j < STEPS; j += 2) {
+                read(step[1], c * STEPS + j + 1);
                 convert(step[0], j);
-                read(step[0], c * (C / 8) + j + 2);
+                read(step[0], c * STEPS + j + 2);
                 convert(step[1], j + 1);
             }
             fence_async_smem();
             arrive(sm.qk_full[st]);
             // the sizes of the values' rows
-            if (wl == 0) wait(sm.values, c);
-            sync(kWarpL);
-#pragma unroll 1
-            for (int r = 16 * wl; r < 16 * wl + 16; r += 8) {
+            wait(sm.values[st], c >> 1);
+            static_assert(kLoadRows == 8, "eight rows at a time");
+            {
+                const int r = kLoadRows * wl;
                 Rows<DV> v[4];
                 uint32_t m[8];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) v[i].load_shared(sm.v + (r + 2 * i) * DV);
+                for (int i = 0; i < 4; ++i) v[i].load_shared(sm.v[st] + (r + 2 * i) * DV);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) v[i].largest(m[2 * i], m[2 * i + 1]);
                 if (lane == 0) {
@@ -409,59 +414,26 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 }
             }
             arrive(sm.sizes);
-            if (maker) {
-                wait(sm.sizes, c);
-                typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
-                int ekv[2], eq[2], ev[2];
-                bool bad[2], odd[2];
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int s = 2 * lane + i;
-                    const uint32_t mk = sm.mk[st][s], mv = sm.mv[st][s];
-                    ev[i] = row_exponent(mv);
-                    // a token whose value or decay is not finite: its weights become NaN, and so its own row, all
-                    // later ones and the state; the value itself must not meet the zero weights of earlier rows.  (One
-                    // of the key does the same by the key's parts.)
-                    bad[i] = s < n && (mv >= 0x7f800000u || g[i] != g[i]);
-                    odd[i] = mv >= 0x7f800000u || bad[i];   // (the rows behind the last are somebody else's)
-                    ekv[i] = !bad[i] && (s >= n || mk == 0u || mv == 0u) ? INT_MIN : ev[i] + row_exponent(mk);
-                    eq[i] = STATES ? 0 : row_exponent(sm.mq[st][s]);
-                }
-                make_factors(f, g, ekv, eq, a.scale);
-                const float nan = __int_as_float(0x7fc00000);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int s = 2 * lane + i;
-                    const float x = pow2(-ev[i]);
-                    if (bad[i]) f.uh[s] = nan;
-                    f.vscale[s] = bad[i] || s >= n ? 0.0f : x;
-                    f.wscale[s] = s >= n ? 0.0f : bad[i] ? nan : f.w[s] * x;
-                }
-                const int some = __any_sync(0xffffffffu, odd[0] || odd[1]);
-                if (lane == 0) f.some_bad = some;
-                arrive(sm.fact[c & 3]);
-            }
         }
-        // copies still on their way when a wait has run out
-        for (int i = max(0, asked - 2); i < asked; ++i) mbar_wait_for(&sm.raw_full[wl][i & 1], (i >> 1) & 1, nullptr, 1000000ull);
     } else if (w < kWarpE) {
         // ------------------------------------------------------------ values
         const int quarter = w & 3, column = 32 * quarter + lane;   // tensor memory lanes of this warp
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
-        const int last = quarter < QUARTERS ? chunks : 0;
+        const bool mine = quarter < QUARTERS;
         int asked = 0;
         auto request = [&](int c) {   // the values of a chunk
             if (c < chunks && w == kWarpV && !*abort_flag) {
                 asked = c + 1;
                 if (lane == 0) {
-                    mbar_arrive_expect_tx(&sm.values, C * DV * 4);
-                    tma_load_2d(sm.v, &map_v, h * p.Dv + col0, seg.row0 + c * C, &sm.values);
+                    mbar_arrive_expect_tx(&sm.values[c & 1], C * DV * 4);
+                    tma_load_2d(sm.v[c & 1], &map_v, h * p.Dv + col0, seg.row0 + c * C, &sm.values[c & 1]);
                 }
                 __syncwarp();
             }
         };
         request(0);
-        for (int c = 0; c < last; ++c) {
+        request(1);
+        for (int c = 0; c < chunks; ++c) {
             const typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
             // weighted for the state, then as they are for the output; read twice rather than kept (the code of a
             // kernel with so many kinds of warps has to stay small: unrolled over 64 tokens it ran at half the speed)
@@ -469,7 +441,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             for (int pass = 0; pass < (STATES ? 1 : 2); ++pass) {
                 if (w == kWarpV) {
                     if (!pass) {
-                        wait(sm.values, c);
+                        wait(sm.values[c & 1], c >> 1);
                         wait(sm.fact[c & 3], c >> 2);
                     }
                     // the last chunk's MMAs have read what is written now
@@ -477,13 +449,24 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 }
                 sync(kWarpV);
                 tc_fence_after();
+                if (!STATES && pass && quarter == 1) {   // the scores' rows 32 .. 63, columns 32 ..
+                    wait(sm.scores, c);
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int j = 2; j < 4; ++j) weigh_scores<DK, DV>(sm, f, tmem, 1, j);
+                    tc_fence_before();
+                    fence_async_smem();
+                    arrive(sm.scores_read);
+                    arrive(sm.p_full);
+                }
+                if (!mine) continue;
                 const float *scale = pass ? f.vscale : f.wscale;
                 uint32_t to = lanes + (pass ? kVh : kWh);
 #pragma unroll 1
                 for (int b = 0; b < C / 16; ++b, to += 8) {
                     float x[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = sm.v[(16 * b + i) * DV + column];
+                    for (int i = 0; i < 16; ++i) x[i] = sm.v[c & 1][(16 * b + i) * DV + column];
                     if (f.some_bad)
 #pragma unroll
                         for (int i = 0; i < 16; ++i) x[i] = f.vscale[16 * b + i] == 0.0f ? 0.0f : x[i];
@@ -501,12 +484,11 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 tc_fence_before();
                 arrive(pass ? sm.v_full : sm.w_full);
             }
-            fence_async_smem();   // the values are read before the next ones come
-            sync(kWarpV);
-            request(c + 1);
+            sync(kWarpV);   // the values are read before the next ones come
+            request(c + 2);
         }
-        // a copy still on its way when a wait has run out
-        if (asked) mbar_wait_for(&sm.values, (asked - 1) & 1, nullptr, 1000000ull);
+        // copies still on their way when a wait has run out
+        for (int i = max(0, asked - 2); i < asked; ++i) mbar_wait_for(&sm.values[i & 1], (i >> 1) & 1, nullptr, 1000000ull);
     } else {
         // ------------------------------------------------------------ state and output
         const int quarter = w & 3, part = (w - kWarpE) >> 2, column = 32 * quarter + lane;
@@ -639,7 +621,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     }
     tc_fence_before();
     __syncthreads();
-    if (w == 0) {
+    if (w == kWarpM) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -664,16 +646,10 @@ cudaError_t launch(const PromptArgs &p, cudaStream_t st)
     PromptArgs args = p;
     args.status = device_status_word();
     const LinearAttnArgs &a = p.a;
-    CUtensorMap map[3];
-    auto rows = [&](int i, const float *x, int heads, int D, long long stride) {
-        const uint64_t cols = (uint64_t)heads * D;
-        return make_tmap_rows_f32(&map[i], x, cols, a.T, a.T > 1 ? (uint64_t)stride : cols, i < 2 ? DK : DV,
-                                  i < 2 ? kRawRows : C);
-    };
-    if ((e = rows(0, a.q, a.Hk, DK, a.q_stride)) != cudaSuccess || (e = rows(1, a.k, a.Hk, DK, a.k_stride)) != cudaSuccess ||
-        (e = rows(2, a.v, a.Hv, p.Dv, a.v_stride)) != cudaSuccess)
-        return e;
-    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, st, args, map[0], map[1], map[2]);
+    CUtensorMap map_v;
+    const uint64_t cols = (uint64_t)a.Hv * p.Dv;
+    if ((e = make_tmap_rows_f32(&map_v, a.v, cols, a.T, a.T > 1 ? (uint64_t)a.v_stride : cols, DV, C)) != cudaSuccess) return e;
+    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, st, args, map_v);
 }
 
 template <int DK, int DV>
