@@ -223,23 +223,15 @@ struct Rows {
     float4 x[N];
     __device__ __forceinline__ static int row(int i) { return N == 2 ? i : (threadIdx.x & 31) >> 4; }
     __device__ __forceinline__ static int lane() { return threadIdx.x & (D / 4 - 1); }
-    __device__ __forceinline__ void load(const float *p, long long stride, int r, int n)
+    // rows r and r + 1 of rows `stride` bytes apart, zeros from row n on
+    __device__ __forceinline__ void load(const float *p, int stride, int r, int n)
     {
+        const char *base = reinterpret_cast<const char *>(p + 4 * lane());
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int at = r + row(i);
-            x[i] = at < n ? *reinterpret_cast<const float4 *>(p + at * stride + 4 * lane())
+            x[i] = at < n ? *reinterpret_cast<const float4 *>(base + (long long)at * stride)
                           : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        }
-    }
-    // the same rows, or later ones, into L2: one request a 128-byte line
-    __device__ __forceinline__ void ahead(const float *p, long long stride, int r, int n) const
-    {
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = r + row(i);
-            if (at < n && (lane() & 7) == 0)
-                asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at * stride + 4 * lane()));
         }
     }
     // from rows in shared memory, one after another

@@ -144,7 +144,8 @@ __device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, ui
 
 template <int DK, int DV, bool STATES>
 __global__ void __launch_bounds__(kThreads, 1)
-linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap map_v)
+linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_constant__ CUtensorMap map_q,
+                        const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v)
 {
     constexpr int QUARTERS = DV / 32;   // of the tensor memory's lanes that are in use
     extern __shared__ char raw[];
@@ -353,7 +354,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     } else if (w < kWarpV) {
         // ------------------------------------------------------------ rows: parts of queries and keys, factors
         // warp wl has the rows kLoadRows wl .. of a chunk, in steps of two: the next two are on their way while two are
-        // converted, and those of the next chunk on their way to L2
+        // converted (from L2, where they come with the values)
         constexpr int STEPS = kLoadRows / 2;
         static_assert(STEPS % 2 == 0, "two steps a turn of the loop");
         const int wl = w - kWarpL;
@@ -363,12 +364,11 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         } step[2];
         const int rows = chunks ? seg.row1 - seg.row0 : 0;
         const float *qp = a.q + seg.row0 * a.q_stride + (long long)hk * DK, *kp = a.k + seg.row0 * a.k_stride + (long long)hk * DK;
+        const int qs = 4 * (int)a.q_stride, ks = 4 * (int)a.k_stride;
         auto read = [&](Step &x, int i) {   // step i of the segment
             const int r = i / STEPS * C + kLoadRows * wl + 2 * (i % STEPS);
-            if (!STATES) x.q.load(qp, a.q_stride, r, rows);
-            x.k.load(kp, a.k_stride, r, rows);
-            if (!STATES) x.q.ahead(qp, a.q_stride, r + C, rows);
-            x.k.ahead(kp, a.k_stride, r + C, rows);
+            if (!STATES) x.q.load(qp, qs, r, rows);
+            x.k.load(kp, ks, r, rows);
         };
         read(step[0], 0);
         for (int c = 0; c < chunks; ++c) {
@@ -421,10 +421,12 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
         const bool mine = quarter < QUARTERS;
         int asked = 0;
-        auto request = [&](int c) {   // the values of a chunk
+        auto request = [&](int c) {   // the values of a chunk, its queries and keys as far as L2
             if (c < chunks && w == kWarpV && !*abort_flag) {
                 asked = c + 1;
                 if (lane == 0) {
+                    if (!STATES) tma_prefetch_2d(&map_q, hk * DK, seg.row0 + c * C);
+                    tma_prefetch_2d(&map_k, hk * DK, seg.row0 + c * C);
                     mbar_arrive_expect_tx(&sm.values[c & 1], C * DV * 4);
                     tma_load_2d(sm.v[c & 1], &map_v, h * p.Dv + col0, seg.row0 + c * C, &sm.values[c & 1]);
                 }
@@ -581,7 +583,9 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 tc_fence_after();
             }
             const int n = seg.row1 - seg.row0 - c * C - 16 * part;
-            float *out = a.out + (long long)(seg.row0 + c * C + 16 * part) * a.out_stride + (long long)h * p.Dv + col0;
+            char *out = reinterpret_cast<char *>(a.out + (seg.row0 + c * C + 16 * part) * a.out_stride + (long long)h * p.Dv +
+                                                 col0 + column);
+            const int os = 4 * (int)a.out_stride;
 #pragma unroll 1
             for (int b = 0; b < 2; ++b) {
                 uint32_t o1[8], o2[8];
@@ -603,11 +607,11 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 }
                 if (8 * b + 8 <= n) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) (out + (8 * b + i) * a.out_stride)[(unsigned)column] = y[i];
+                    for (int i = 0; i < 8; ++i) *reinterpret_cast<float *>(out + (long long)(8 * b + i) * os) = y[i];
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i)
-                        if (8 * b + i < n) (out + (8 * b + i) * a.out_stride)[(unsigned)column] = y[i];
+                        if (8 * b + i < n) *reinterpret_cast<float *>(out + (long long)(8 * b + i) * os) = y[i];
                 }
             }
             tc_fence_before();
@@ -646,10 +650,15 @@ cudaError_t launch(const PromptArgs &p, cudaStream_t st)
     PromptArgs args = p;
     args.status = device_status_word();
     const LinearAttnArgs &a = p.a;
-    CUtensorMap map_v;
-    const uint64_t cols = (uint64_t)a.Hv * p.Dv;
-    if ((e = make_tmap_rows_f32(&map_v, a.v, cols, a.T, a.T > 1 ? (uint64_t)a.v_stride : cols, DV, C)) != cudaSuccess) return e;
-    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, st, args, map_v);
+    CUtensorMap map[3];
+    auto rows = [&](int i, const float *x, int heads, int D, long long stride, int box) {
+        const uint64_t cols = (uint64_t)heads * D;
+        return make_tmap_rows_f32(&map[i], x, cols, a.T, a.T > 1 ? (uint64_t)stride : cols, box, C);
+    };
+    if ((e = rows(0, a.q, a.Hk, DK, a.q_stride, DK)) != cudaSuccess || (e = rows(1, a.k, a.Hk, DK, a.k_stride, DK)) != cudaSuccess ||
+        (e = rows(2, a.v, a.Hv, p.Dv, a.v_stride, DV)) != cudaSuccess)
+        return e;
+    return launch_pdl(kernel, dim3((unsigned)ctas), dim3(kThreads), smem, st, args, map[0], map[1], map[2]);
 }
 
 template <int DK, int DV>

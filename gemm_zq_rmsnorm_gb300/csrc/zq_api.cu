@@ -955,8 +955,9 @@ int check_linear(const float *q, long long q_stride, const float *k, long long k
     if ((st = check_rows(k, k_stride, (long long)Hk * Dk, name, "k"))) return st;
     if ((st = check_rows(v, v_stride, (long long)Hv * Dv, name, "v"))) return st;
     if ((st = check_rows(out, out_stride, (long long)Hv * Dv, name, "out"))) return st;
-    if (g && (g_stride < Hv || g_stride > 1LL << 40))
-        return fail(ZQ_ERR_SHAPE, "%s: stride %lld of g must be at least %d", name, g_stride, Hv);
+    for (long long stride : {q_stride, k_stride, v_stride, out_stride, g ? g_stride : 0})
+        if (stride >= 1LL << 29) return fail(ZQ_ERR_SHAPE, "%s: stride %lld must be below 2^29", name, stride);
+    if (g && g_stride < Hv) return fail(ZQ_ERR_SHAPE, "%s: stride %lld of g must be at least %d", name, g_stride, Hv);
     if (!slots) return fail(ZQ_ERR_ARG, "%s: null slots", name);
     if (!aligned4(g) || !aligned4(slots)) return fail(ZQ_ERR_ALIGN, "%s: g and slots must be 4-byte aligned", name);
     a.q = q;

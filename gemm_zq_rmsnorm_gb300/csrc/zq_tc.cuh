@@ -161,6 +161,14 @@ __device__ __forceinline__ void tma_load_5d(void *dst, const CUtensorMap *map, i
         : "memory");
 }
 
+// The box into L2, no wait.
+__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int x, int y)
+{
+    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global [%0, {%1, %2}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y)
+                 : "memory");
+}
+
 // ---- TMA tiled stores (bulk async-groups of the issuing thread) ---------
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, const void *src)
 {

@@ -619,8 +619,8 @@ typedef struct zq_linear_state {
  *   S = exp(g) S + k v^T,   out = scale * S^T q,
  * S being the state of slots[b], updated in place.
  *   q, k  : fp32, head h of sequence b at q + b * q_stride + h * Dk, Hk heads
- *           (strides in floats, multiples of 4, so the parts of a stacked
- *           projection's row serve);  v, out : alike with Hv heads of Dv; out may
+ *           (strides in floats, multiples of 4 below 2^29, so the parts of a
+ *           stacked projection's row serve);  v, out : alike with Hv heads of Dv; out may
  *           not overlap the inputs;
  *   g     : fp32, the logarithm of the decay of head h at g + b * g_stride + h,
  *           any value (-infinity forgets everything); NULL: no decay;

@@ -33,7 +33,7 @@ def prompt(lib, q=A16, qs=256, k=A16, ks=256, v=A16, vs=512, T=30, B=3, Hk=2, g=
 
 BOTH = [(dict(q=None), -1), (dict(q=A8), -3), (dict(qs=252), -2), (dict(qs=258), -2), (dict(k=None), -1),
         (dict(ks=0), -2), (dict(v=A8), -3), (dict(vs=508), -2), (dict(out=None), -1), (dict(out=A8), -3),
-        (dict(os=-512), -2), (dict(g=A2), -3), (dict(gs=3), -2), (dict(gs=-4), -2), (dict(slots=None), -1),
+        (dict(os=-512), -2), (dict(g=A2), -3), (dict(gs=3), -2), (dict(gs=-4), -2), (dict(vs=1 << 29), -2), (dict(gs=1 << 29), -2), (dict(slots=None), -1),
         (dict(slots=A2), -3), (dict(scale=math.nan), -1), (dict(scale=math.inf), -1), (dict(Hk=0), -2),
         (dict(Hk=3), -2), (dict(Hk=8, qs=1024, ks=1024), -2), (dict(B=0), -2), (dict(B=65536), -2)]
 STATES = [(dict(s=None), -1), (dict(s=A8), -3), (dict(n=0), -2), (dict(Hv=0), -2), (dict(Hv=1026), -2),
