@@ -12,10 +12,10 @@
 // hi (2^-22 of what bounds it; sums fp32, a chunk's sums added to the state outside
 // the tensor core, whose accumulator truncates).  Weights exp(G_t - G_s) and the
 // rows' powers of two meet in the exponent: with u_s = e_k + e_v - G_s (G in base
-// two) and M_t the largest u of s <= t, the weight in the product is 2^(u_s - M_t)
-// <= 1 and 2^(M_t + G_t) goes to the row, so that a token counts exactly where no
-// larger one of its past drowns it, and the future does not matter at all.  G and u
-// are sums in units of 2^-40.
+// two) and M_t the whole number above the largest u of s <= t, the weight in the
+// product is 2^(u_s - M_t) <= 1 and 2^(M_t + G_t) goes to the row, so that a token
+// counts exactly where no larger one of its past drowns it, and the future does not
+// matter at all.  G is a sum in units of 2^-32.
 #pragma once
 
 #include <limits.h>
@@ -96,12 +96,41 @@ __device__ __forceinline__ Segment find_segment(const PromptArgs &p, int at)
 }
 
 // ---------------------------------------------------------------- parts of values
-// two scaled values to their binary16 parts
-__device__ __forceinline__ void split2(float x, float y, uint32_t &hi, uint32_t &lo)
+// two products, sums, and fused products and sums in one instruction
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
 {
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(y), "f"(x));
-    const float2 h = __half22float2(*reinterpret_cast<const __half2 *>(&hi));
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(y - h.y), "f"(x - h.x));
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 z, x, y, z;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+
+// two scaled values to their binary16 parts
+__device__ __forceinline__ void split2(float2 x, uint32_t &hi, uint32_t &lo)
+{
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(hi) : "f"(x.y), "f"(x.x));
+    const float2 rest = fma2(__half22float2(*reinterpret_cast<const __half2 *>(&hi)), make_float2(-1.0f, -1.0f), x);
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(lo) : "f"(rest.y), "f"(rest.x));
 }
 
 __device__ __forceinline__ float exp2_fast(float x)
@@ -122,41 +151,44 @@ __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) <
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
 
 // ---------------------------------------------------------------- a chunk's factors
-constexpr long long kOne = 1LL << 40;          // units of G and u
-constexpr long long kNothing = -(1LL << 60);   // u of a row of zeros
+// G in units of 2^-32: a whole part in the high word, a broken one in the low word
+constexpr int kNothing = -(1 << 20);           // whole part of u of a row of zeros
 
 struct Factors {
-    float uh[kChunk], ul[kChunk], mh[kChunk], ml[kChunk];   // u and M: whole and broken part
-    float f1[kChunk], f2[kChunk], w[kChunk];                // the rows' factors, the tokens' weights in the state
-    float keep, add;                                        // what the state, and what the chunk's sums are multiplied by
+    float uh[kChunk], ul[kChunk], m[kChunk];   // u, whole and broken part; M
+    float f1[kChunk], f2[kChunk], w[kChunk];   // the rows' factors, the tokens' weights in the state
+    float keep, add;                           // what the state, and what the chunk's sums are multiplied by
     long long G;
 };
 
-// 2^(x / kOne + e), the broken part's power to 2^-22
-__device__ __forceinline__ float exp2_units(long long x, int e)
-{
-    const long long whole = (x >> 40) + e;
-    const int n = (int)(whole < -252 ? -252 : whole > 252 ? 252 : whole);   // 2^-252 and 2^252 as two factors: 0, infinity
-    const float part = (float)((uint32_t)(x >> 8)) * 0x1p-32f;
-    return exp2_fast(part) * pow2(n >> 1) * pow2(n - (n >> 1));
-}
+__device__ __forceinline__ int whole(long long x) { return (int)(x >> 32); }
+__device__ __forceinline__ float broken(long long x) { return (float)(uint32_t)x * 0x1p-32f; }
 
-// x log2 e in units of 2^-40, to 2^-33 of itself and half a unit: the significand times 2^32 log2 e, shifted
+// 2^(n + part), the part's power to 2^-22; 0 below the normal numbers
+__device__ __forceinline__ float exp2_parts(int n, float part)
+{
+    const float x = exp2_fast(part) * pow2(max(-126, min(127, n)));
+    return n < -126 ? 0.0f : n > 127 ? __int_as_float(0x7f800000) : x;
+}
+__device__ __forceinline__ float exp2_units(long long x) { return exp2_parts(whole(x), broken(x)); }
+
+// x log2 e in units, to 2^-33 of itself and half a unit: the significand times 2^32 log2 e, shifted
 __device__ __forceinline__ long long log2_units(float x)
 {
     // beyond +-200 the power is 0 or infinity; NaN is marked elsewhere
     x = fminf(fmaxf(x, -200.0f), 200.0f);
     const uint32_t bits = __float_as_uint(x) & 0x7fffffffu;
-    const int shift = 142 - (int)(bits >> 23);   // 15 - e, at least 8
+    const int shift = min(63, 150 - (int)(bits >> 23));   // 23 - e, at least 16
     const uint64_t product = (uint64_t)((bits & 0x7fffffu) | 0x800000u) * 6196328019ull;
-    const long long r = shift > 62 ? 0 : (long long)((product + (1ull << (shift - 1))) >> shift);
+    const long long r = (long long)((product + (1ull << (shift - 1))) >> shift);
     return x < 0.0f ? -r : r;
 }
 
-__device__ __forceinline__ long long clamp_units(long long G) { return min(max(G, -(1LL << 52)), 1LL << 52); }
+__device__ __forceinline__ long long clamp_units(long long G) { return min(max(G, -(1LL << 44)), 1LL << 44); }
 
 // The factors of a chunk's rows, by one warp with two tokens a lane: their decays,
 // exponents of key and value together (INT_MIN: one of them is zero) and of the query.
+// M need only be near the largest u: it is the whole number above it.
 __device__ __forceinline__ void make_factors(Factors &s, const float (&g)[2], const int (&ekv)[2], const int (&eq)[2],
                                              float scale)
 {
@@ -168,35 +200,40 @@ __device__ __forceinline__ void make_factors(Factors &s, const float (&g)[2], co
         const long long o = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += o;
     }
-    const long long Gt[2] = {sum - b, sum};
-    long long u[2], M[2];
+    const long long G[2] = {sum - b, sum};
+    int uw[2], M[2];
+    float ub[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) u[i] = ekv[i] == INT_MIN ? kNothing : ekv[i] * kOne - Gt[i];
-    long long top = max(u[0], u[1]);
+    for (int i = 0; i < 2; ++i) {
+        uw[i] = ekv[i] == INT_MIN ? kNothing : ekv[i] + whole(-G[i]);
+        ub[i] = broken(-G[i]);
+    }
+    int top = max(uw[0], uw[1]);
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, top, d);
+        const int o = __shfl_up_sync(0xffffffffu, top, d);
         if (lane >= d) top = max(top, o);
     }
-    const long long before = __shfl_up_sync(0xffffffffu, top, 1);
-    M[0] = lane ? max(before, u[0]) : u[0];
-    M[1] = top;
-    const long long last = __shfl_sync(0xffffffffu, top, 31), G = __shfl_sync(0xffffffffu, sum, 31);
+    const int before = __shfl_up_sync(0xffffffffu, top, 1);
+    M[0] = (lane ? max(before, uw[0]) : uw[0]) + 1;
+    M[1] = top + 1;
+    const int last = __shfl_sync(0xffffffffu, M[1], 31);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
-        s.uh[t] = (float)(int)(u[i] >> 40);
-        s.ul[t] = (float)((uint32_t)(u[i] >> 8)) * 0x1p-32f;
-        s.mh[t] = (float)(int)(M[i] >> 40);
-        s.ml[t] = (float)((uint32_t)(M[i] >> 8)) * 0x1p-32f;
-        s.f1[t] = scale * exp2_units(M[i] + Gt[i], eq[i]);
-        s.f2[t] = scale * exp2_units(Gt[i], eq[i]);
-        s.w[t] = exp2_units(u[i] - last, 0);
+        s.uh[t] = (float)uw[i];
+        s.ul[t] = ub[i];
+        s.m[t] = (float)M[i];
+        const int n = whole(G[i]) + eq[i];
+        const float part = broken(G[i]);
+        s.f1[t] = scale * exp2_parts(n + M[i], part);
+        s.f2[t] = scale * exp2_parts(n, part);
+        s.w[t] = exp2_parts(uw[i] - last, ub[i]);
     }
-    if (lane == 0) {
-        s.keep = exp2_units(G, 0);
-        s.add = exp2_units(G + last, 0);
-        s.G = G;
+    if (lane == 31) {
+        s.keep = exp2_units(sum);
+        s.add = exp2_parts(whole(sum) + last, broken(sum));
+        s.G = sum;
     }
 }
 
@@ -268,8 +305,8 @@ struct Rows {
             const float s = pow2(-(N == 2 ? e[i] : j ? e[1] : e[0]));
             const int f = N == 2 ? fill[i] : j ? fill[1] : fill[0];
             uint2 h, l;
-            split2(x[i].x * s, x[i].y * s, h.x, l.x);
-            split2(x[i].z * s, x[i].w * s, h.y, l.y);
+            split2(mul2(make_float2(x[i].x, x[i].y), make_float2(s, s)), h.x, l.x);
+            split2(mul2(make_float2(x[i].z, x[i].w), make_float2(s, s)), h.y, l.y);
             if (f) h = l = f == 1 ? make_uint2(0u, 0u) : make_uint2(0x7e007e00u, 0x7e007e00u);
             const uint32_t to = at(r + j, lane() >> 1) + ((lane() & 1) << 3);
             *reinterpret_cast<uint2 *>(reinterpret_cast<char *>(hi) + to) = h;

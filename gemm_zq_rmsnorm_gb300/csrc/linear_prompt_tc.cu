@@ -11,11 +11,11 @@
 // stays in the registers of sixteen warps (four threads for a column), which add U to
 // it, split it for the next chunk and put O1 and O2 together.
 //
-// and the scores Q K^T the same way.  Warps: 0 and 1 weigh scores; 2 issues the MMAs; 3
-// makes the chunk's factors; 4..11 convert queries and keys; 12..15 values, a lane for
-// a column; 16..31 the state.  Keys and queries are two stages deep; the key tile
-// serves the scores as rows and U as columns (the same bytes, a descriptor of the
-// other order).
+// and the scores Q K^T the same way.  Warps: 0, 1 and 5 weigh scores, 0 makes the
+// chunk's factors as well; 2 issues the MMAs; 3, 4 and 6..11 convert queries and keys;
+// 12..15 values, a lane for a column; 16..31 the state.  Keys and queries are two
+// stages deep; the key tile serves the scores as rows and U as columns (the same
+// bytes, a descriptor of the other order).
 //
 // Every wait is bounded: after one has run out no MMA is issued any more, the
 // others return at once and the kernel ends (its results are invalid).
@@ -28,8 +28,9 @@ namespace zq {
 namespace {
 
 constexpr int C = kChunk;
-constexpr int kWarpM = 2, kWarpF = 3, kWarpL = 4, kWarpV = 12, kWarpE = 16, kWarps = 32;   // first of each role
-constexpr int LW = kWarpV - kWarpL;
+// the warps' parts; a warp can reach the tensor memory lanes 32 (its number mod 4) .. only, which is why 5 weighs scores
+constexpr int kWarpM = 2, kWarpV = 12, kWarpE = 16, kWarps = 32, LW = 8;
+__device__ __forceinline__ bool weighs(int w) { return w == 0 || w == 1 || w == 5; }
 constexpr int kLoadRows = C / LW;  // rows of a chunk of a warp that converts
 constexpr int kThreads = kWarps * 32;
 // tensor memory columns
@@ -120,7 +121,7 @@ __device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, ui
     const int lane = threadIdx.x & 31, tr = 32 * quarter + lane;
     uint32_t s[16];
     tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + kU + 16 * j, s);
-    const float mh = f.mh[tr], ml = f.ml[tr];
+    const float m = -f.m[tr];
     tmem_wait_ld();
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
@@ -129,12 +130,15 @@ __device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, ui
         for (int i = 0; i < 4; i += 2) {
             const int sc = 16 * j + 8 * half + 2 * i;
             const float4 uh = *reinterpret_cast<const float4 *>(&f.uh[sc]), ul = *reinterpret_cast<const float4 *>(&f.ul[sc]);
-            auto one = [&](int e, float h, float l) {
-                const float x = __uint_as_float(s[8 * half + 2 * i + e]) * exp2_fast((h - mh) + (l - ml));
-                return sc + e <= tr ? x : 0.0f;
+            auto two = [&](int e, float2 h, float2 l, uint32_t &phi, uint32_t &plo) {
+                const float2 x = add2(add2(h, make_float2(m, m)), l);
+                float2 y = mul2(make_float2(__uint_as_float(s[8 * half + 2 * i + e]), __uint_as_float(s[8 * half + 2 * i + e + 1])),
+                                make_float2(exp2_fast(x.x), exp2_fast(x.y)));
+                if (j >= 2 * quarter) y = make_float2(sc + e <= tr ? y.x : 0.0f, sc + e + 1 <= tr ? y.y : 0.0f);
+                split2(y, phi, plo);
             };
-            split2(one(0, uh.x, ul.x), one(1, uh.y, ul.y), hi[i], lo[i]);
-            split2(one(2, uh.z, ul.z), one(3, uh.w, ul.w), hi[i + 1], lo[i + 1]);
+            two(0, make_float2(uh.x, uh.y), make_float2(ul.x, ul.y), hi[i], lo[i]);
+            two(2, make_float2(uh.z, uh.w), make_float2(ul.z, ul.w), hi[i + 1], lo[i + 1]);
         }
         const uint32_t to = tile_piece<C>(tr, 2 * j + half);
         *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(sm.p[0]) + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
@@ -156,10 +160,9 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     volatile int *abort_flag = &sm.abort;
     unsigned int *status = p.status;
     auto wait = [&](uint64_t &bar, int parity) { wait_phase(&bar, parity, abort_flag, status); };
-    // the same for a group of warps: its first one waits, the others in its named barrier
+    // of a group of warps one waits, the others in the group's named barrier
     auto sync = [&](int group) {
-        named_bar(group == kWarpL ? 2 : group == kWarpV ? 3 : 4,
-                  group == kWarpL ? 32 * LW : group == kWarpE ? 128 * QUARTERS : 128);
+        named_bar(group == kWarpV ? 1 : group == kWarpE ? 2 : 3, group == kWarpV ? 128 : group == kWarpE ? 128 * QUARTERS : 32 * LW);
     };
     auto arrive = [&](uint64_t &bar) {   // one arrival of the warp
         __syncwarp();
@@ -197,7 +200,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     const int tiles = p.Dv / DV;
     const int tile = blockIdx.x % tiles, item = blockIdx.x / tiles;
     const int h = item % a.Hv, at = item / a.Hv, col0 = tile * DV;
-    if (w == kWarpL) {
+    if (w == 3) {
         const Segment s = find_segment(p, at);
         if (lane == 0) sm.seg = s;
     }
@@ -216,22 +219,26 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         // ------------------------------------------------------------ MMAs
         constexpr uint32_t id_u = idesc_b_columns(128, DK), id_o = idesc_f16_f32(128, C);
         const bool leader = elect_one();
-        auto rows_at = [](uint32_t tile, int kk) {   // of a tile of rows, columns 16 kk ..
-            return smem_desc(tile + (kk >> 2) * (C * 128) + (kk & 3) * 32, 16, 1024, kLayoutSw128);
-        };
+        // Descriptors as their low word (address, offset between 64-column tiles) and a constant high one, so that an MMA
+        // takes an addition or two: with the issue slots shared by eight warps every instruction between two MMAs counts.
+        constexpr uint32_t high = 1024 >> 4 | 1u << 14 | kLayoutSw128 << 29;
+        auto low = [](const void *tile) { return smem_u32(tile) >> 4 | (uint32_t)(C * 128 >> 4) << 16; };
+        auto desc = [](uint32_t lo) { return (uint64_t)high << 32 | lo; };
+        auto rows_at = [](int kk) { return (uint32_t)(((kk >> 2) * (C * 128) + (kk & 3) * 32) >> 4); };   // columns 16 kk ..
+        constexpr uint32_t part = C * DK * 2 >> 4, stage = 2 * part, ppart = C * C * 2 >> 4;
+        const uint32_t q0 = low(sm.q[0][0]), k0 = low(sm.k[0][0]), p0 = low(sm.p[0]);
         auto scores = [&](int c) {   // Q K^T in U's place; lanes 64 .. hold the product of whatever lies behind the queries
             const int st = c & 1;
             wait(sm.qk_full[st], c >> 1);
             if (c) wait(sm.u_empty, c - 1);
             tc_fence_after();
-            const uint32_t qh = smem_u32(sm.q[st][0]), ql = smem_u32(sm.q[st][1]), kh = smem_u32(sm.k[st][0]),
-                           kl = smem_u32(sm.k[st][1]);
             if (!*abort_flag && leader) {
-#pragma unroll 1
-                for (int i = 0; i < 3; ++i) {   // lo hi, hi lo, hi hi
-                    const uint32_t x = i == 0 ? ql : qh, y = i == 1 ? kl : kh;
 #pragma unroll
-                    for (int kk = 0; kk < DK / 16; ++kk) mma_f16(tmem + kU, rows_at(x, kk), rows_at(y, kk), id_o, i || kk);
+                for (int i = 0; i < 3; ++i) {   // lo hi, hi lo, hi hi
+                    const uint32_t x = q0 + st * stage + (i == 0 ? part : 0), y = k0 + st * stage + (i == 1 ? part : 0);
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk)
+                        mma_f16(tmem + kU, desc(x + rows_at(kk)), desc(y + rows_at(kk)), id_o, i || kk);
                 }
                 mma_commit(&sm.scores);
             }
@@ -244,13 +251,13 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 wait(sm.s_full, c);
                 if (c) wait(sm.o_empty, c - 1);
                 tc_fence_after();
-                const uint32_t qh = smem_u32(sm.q[st][0]), ql = smem_u32(sm.q[st][1]);
                 if (!*abort_flag && leader) {
-#pragma unroll 1
-                    for (int i = 0; i < 3; ++i) {
-                        const uint32_t as = tmem + (i == 0 ? kSl : kSh), b = i == 1 ? ql : qh;
 #pragma unroll
-                        for (int kk = 0; kk < DK / 16; ++kk) mma_f16_ta(tmem + kO1, as + 8 * kk, rows_at(b, kk), id_o, i || kk);
+                    for (int i = 0; i < 3; ++i) {
+                        const uint32_t as = tmem + (i == 0 ? kSl : kSh), b = q0 + st * stage + (i == 1 ? part : 0);
+#pragma unroll
+                        for (int kk = 0; kk < DK / 16; ++kk)
+                            mma_f16_ta(tmem + kO1, as + 8 * kk, desc(b + rows_at(kk)), id_o, i || kk);
                     }
                 }
                 __syncwarp();
@@ -261,15 +268,13 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             }
             wait(sm.w_full, c);
             tc_fence_after();
-            const uint32_t kh = smem_u32(sm.k[st][0]), kl = smem_u32(sm.k[st][1]);
             if (!*abort_flag && leader) {
-#pragma unroll 1
+#pragma unroll
                 for (int i = 0; i < 3; ++i) {
-                    const uint32_t av = tmem + (i == 0 ? kWl : kWh), b = i == 1 ? kl : kh;
+                    const uint32_t av = tmem + (i == 0 ? kWl : kWh), b = k0 + st * stage + (i == 1 ? part : 0);
 #pragma unroll
                     for (int kk = 0; kk < C / 16; ++kk)
-                        mma_f16_ta(tmem + kU, av + 8 * kk, smem_desc(b + kk * 2048, C * 128, 1024, kLayoutSw128), id_u,
-                                   i || kk);
+                        mma_f16_ta(tmem + kU, av + 8 * kk, desc(b + (kk * 2048 >> 4)), id_u, i || kk);
                 }
                 mma_commit(&sm.u_full);
                 mma_commit(&sm.qk_empty[st]);
@@ -279,38 +284,23 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             wait(sm.v_full, c);
             wait(sm.p_full, c);
             tc_fence_after();
-            const uint32_t p0 = smem_u32(sm.p[0]), p1 = smem_u32(sm.p[1]);
             if (!*abort_flag && leader) {
-#pragma unroll 1
-                for (int i = 0; i < 3; ++i) {
-                    const uint32_t av = tmem + (i == 0 ? kVl : kVh), b = i == 1 ? p1 : p0;
 #pragma unroll
-                    for (int kk = 0; kk < C / 16; ++kk) mma_f16_ta(tmem + kO2, av + 8 * kk, rows_at(b, kk), id_o, i || kk);
+                for (int i = 0; i < 3; ++i) {
+                    const uint32_t av = tmem + (i == 0 ? kVl : kVh), b = p0 + (i == 1 ? ppart : 0);
+#pragma unroll
+                    for (int kk = 0; kk < C / 16; ++kk) mma_f16_ta(tmem + kO2, av + 8 * kk, desc(b + rows_at(kk)), id_o, i || kk);
                 }
                 mma_commit(&sm.o_full);
             }
             __syncwarp();
             if (c + 1 < chunks) scores(c + 1);
         }
-    } else if (w < kWarpM) {
-        // ------------------------------------------------------------ weights of the scores
-        // warp 0 the rows 0 .. 31 (32 columns), warp 1 the first half of the rows 32 .. 63, a warp of the values the other
-        if (!STATES)
-            for (int c = 0; c < chunks; ++c) {
-                wait(sm.fact[c & 3], c >> 2);
-                if (c) wait(sm.o_full, c - 1);   // the last weights have been read
-                wait(sm.scores, c);
-                tc_fence_after();
-#pragma unroll 1
-                for (int j = 0; j < 2; ++j) weigh_scores<DK, DV>(sm, sm.f[c & 3], tmem, w, j);
-                tc_fence_before();
-                fence_async_smem();
-                arrive(sm.scores_read);
-                arrive(sm.p_full);
-            }
-    } else if (w == kWarpF) {
-        // ------------------------------------------------------------ a chunk's factors
-        for (int c = 0; c < chunks; ++c) {
+    } else if (weighs(w)) {
+        // ------------------------------------------------------------ a chunk's factors (warp 0) and the scores' weights
+        // warp 0 has the rows 0 .. 31 (32 columns), the others the rows 32 .. 63, half of the columns each
+        const int quarter = w & 3, first = w == 5 ? 2 : 0;
+        auto factors = [&](int c) {
             const int st = c & 1;
             const long long row = seg.row0 + c * C;
             const int n = seg.row1 - (int)row;
@@ -350,6 +340,21 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             const int some = __any_sync(0xffffffffu, odd[0] || odd[1]);
             if (lane == 0) f.some_bad = some;
             arrive(sm.fact[c & 3]);
+        };
+        for (int c = -1; c < chunks; ++c) {   // the factors are a chunk ahead
+            if (!STATES && c >= 0) {
+                if (w) wait(sm.fact[c & 3], c >> 2);
+                if (c) wait(sm.o_full, c - 1);   // the last weights have been read
+                wait(sm.scores, c);
+                tc_fence_after();
+#pragma unroll 1
+                for (int j = first; j < first + 2; ++j) weigh_scores<DK, DV>(sm, sm.f[c & 3], tmem, quarter, j);
+                tc_fence_before();
+                fence_async_smem();
+                arrive(sm.scores_read);
+                arrive(sm.p_full);
+            }
+            if (w == 0 && c + 1 < chunks) factors(c + 1);
         }
     } else if (w < kWarpV) {
         // ------------------------------------------------------------ rows: parts of queries and keys, factors
@@ -357,7 +362,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         // converted (from L2, where they come with the values)
         constexpr int STEPS = kLoadRows / 2;
         static_assert(STEPS % 2 == 0, "two steps a turn of the loop");
-        const int wl = w - kWarpL;
+        const int wl = w < 5 ? w - 3 : w - 4;
         const int none[2] = {0, 0};
         struct Step {
             Rows<DK> q, k;
@@ -373,7 +378,10 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         read(step[0], 0);
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
-            if (c >= 2) wait(sm.qk_empty[st], (c >> 1) - 1);
+            if (c >= 2) {
+                if (wl == 0) wait(sm.qk_empty[st], (c >> 1) - 1);
+                sync(0);
+            }
             auto convert = [&](const Step &x, int j) {
                 const int r = kLoadRows * wl + 2 * j;
                 uint32_t mq[2], mk[2];
@@ -451,16 +459,6 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 }
                 sync(kWarpV);
                 tc_fence_after();
-                if (!STATES && pass && quarter == 1) {   // the scores' rows 32 .. 63, columns 32 ..
-                    wait(sm.scores, c);
-                    tc_fence_after();
-#pragma unroll 1
-                    for (int j = 2; j < 4; ++j) weigh_scores<DK, DV>(sm, f, tmem, 1, j);
-                    tc_fence_before();
-                    fence_async_smem();
-                    arrive(sm.scores_read);
-                    arrive(sm.p_full);
-                }
                 if (!mine) continue;
                 const float *scale = pass ? f.vscale : f.wscale;
                 uint32_t to = lanes + (pass ? kVh : kWh);
@@ -476,8 +474,8 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
 #pragma unroll
                     for (int i = 0; i < 8; i += 2) {
                         const float4 y = *reinterpret_cast<const float4 *>(scale + 16 * b + 2 * i);
-                        split2(x[2 * i] * y.x, x[2 * i + 1] * y.y, ph[i], pl[i]);
-                        split2(x[2 * i + 2] * y.z, x[2 * i + 3] * y.w, ph[i + 1], pl[i + 1]);
+                        split2(mul2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(y.x, y.y)), ph[i], pl[i]);
+                        split2(mul2(make_float2(x[2 * i + 2], x[2 * i + 3]), make_float2(y.z, y.w)), ph[i + 1], pl[i + 1]);
                     }
                     tmem_st8(to, ph);
                     tmem_st8(to + (kVl - kVh), pl);
@@ -535,7 +533,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             for (int b = 0; b < N / 16; ++b) {
                 uint32_t ph[8], pl[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) split2(S[16 * b + 2 * i], S[16 * b + 2 * i + 1], ph[i], pl[i]);
+                for (int i = 0; i < 8; ++i) split2(make_float2(S[16 * b + 2 * i], S[16 * b + 2 * i + 1]), ph[i], pl[i]);
                 tmem_st8(lanes + kSh + part * (N / 2) + 8 * b, ph);
                 tmem_st8(lanes + kSl + part * (N / 2) + 8 * b, pl);
             }
@@ -566,7 +564,13 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 tmem_ld16(lanes + kU + part * N + 16 * b, u);
                 tmem_wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) S[16 * b + i] = __fmaf_rn(add, __uint_as_float(u[i]), keep * S[16 * b + i]);
+                for (int i = 0; i < 16; i += 2) {
+                    float *x = &S[16 * b + i];
+                    const float2 y = fma2(make_float2(add, add), make_float2(__uint_as_float(u[i]), __uint_as_float(u[i + 1])),
+                                          mul2(make_float2(keep, keep), make_float2(x[0], x[1])));
+                    x[0] = y.x;
+                    x[1] = y.y;
+                }
             }
             if (STATES) G = clamp_units(G + f.G);
             tc_fence_before();
@@ -597,13 +601,15 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 for (int i = 0; i < 8; i += 4) {
                     const float4 f1 = *reinterpret_cast<const float4 *>(&f.f1[16 * part + 8 * b + i]),
                                  f2 = *reinterpret_cast<const float4 *>(&f.f2[16 * part + 8 * b + i]);
-                    auto one = [&](int j, float u, float v) {
-                        return __fmaf_rn(u, __uint_as_float(o2[j]), v * (__uint_as_float(o1[j]) * xs));
+                    auto two = [&](int j, float u0, float u1, float v0, float v1) {
+                        const float2 state = mul2(make_float2(__uint_as_float(o1[j]), __uint_as_float(o1[j + 1])), make_float2(xs, xs));
+                        const float2 r = fma2(make_float2(u0, u1), make_float2(__uint_as_float(o2[j]), __uint_as_float(o2[j + 1])),
+                                              mul2(make_float2(v0, v1), state));
+                        y[j] = r.x;
+                        y[j + 1] = r.y;
                     };
-                    y[i] = one(i, f1.x, f2.x);
-                    y[i + 1] = one(i + 1, f1.y, f2.y);
-                    y[i + 2] = one(i + 2, f1.z, f2.z);
-                    y[i + 3] = one(i + 3, f1.w, f2.w);
+                    two(i, f1.x, f1.y, f2.x, f2.y);
+                    two(i + 2, f1.z, f1.w, f2.z, f2.w);
                 }
                 if (8 * b + 8 <= n) {
 #pragma unroll
