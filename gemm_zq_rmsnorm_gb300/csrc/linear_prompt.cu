@@ -1,20 +1,17 @@
-// linear_prompt.cu -- linear attention with a decay for each head over prompts
-// (MIInfer README, "Status": recurrent layers with a state of [heads][128][128]).
+// linear_prompt.cu -- linear attention with a decay for each head over prompts: the
+// cut of long sequences into segments and the join of their states (MIInfer README,
+// "Status": recurrent layers with a state of [heads][128][128]).
 //
-// A CTA owns DVT columns of one head and walks through a segment of a sequence.
-// Each compute warp holds 16 of the columns, as the transposed state [16][Dk] in
-// MMA accumulators, whose layout is that of the MMA's second operand: the product
-// with the queries takes the state from registers.  Four more warps load and
-// convert the next chunk meanwhile.
-#include <atomic>
-
+// A CTA walks through a sequence chunk after chunk, so a few long sequences of a few
+// heads would leave most of the GPU idle.  Then every sequence is cut into segments:
+// a first kernel finds what each adds to the state (a third of a chunk's work), a
+// second one makes the states that they start from, and the third does the rest.
 #include "linear_prompt.cuh"
 
 namespace zq {
 namespace {
 
 constexpr int C = kChunk;
-constexpr int kLoaders = 4;        // warps that load
 constexpr int kSlots = 152;        // CTAs that the plan cuts long sequences for
 constexpr int kMaxCut = 512;       // sequences of a call up to which they are cut
 

@@ -378,10 +378,8 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         read(step[0], 0);
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
-            if (c >= 2) {
-                if (wl == 0) wait(sm.qk_empty[st], (c >> 1) - 1);
-                sync(0);
-            }
+            if (c >= 2 && wl == 0) wait(sm.qk_empty[st], (c >> 1) - 1);
+            sync(0);   // (also: no warp's count in `sizes` is a chunk ahead of another's)
             auto convert = [&](const Step &x, int j) {
                 const int r = kLoadRows * wl + 2 * j;
                 uint32_t mq[2], mk[2];
