@@ -63,16 +63,14 @@ __global__ void __launch_bounds__(kThreads) gated_norm_kernel(const __grid_const
     }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
+        float e[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
         if (a.gate) {
-            y[i].x = gated(y[i].x, gt[i].x, a.act);
-            y[i].y = gated(y[i].y, gt[i].y, a.act);
-            y[i].z = gated(y[i].z, gt[i].z, a.act);
-            y[i].w = gated(y[i].w, gt[i].w, a.act);
+            const float g[4] = {gt[i].x, gt[i].y, gt[i].z, gt[i].w};
+            gate_values(e, g, a.act);
         }
-        if (a.out && live) *reinterpret_cast<float4 *>(a.out + b * a.out_stride + h * D + col + i * 128) = y[i];
+        if (a.out && live) *reinterpret_cast<float4 *>(a.out + b * a.out_stride + h * D + col + i * 128) = make_float4(e[0], e[1], e[2], e[3]);
         if (a.q8.qs) {
             const long long o = ((long long)b * a.H + h) * D + col + i * 128;
-            const float e[4] = {y[i].x, y[i].y, y[i].z, y[i].w};
             uint32_t code[1];
             __half d, s;
             q8_1_pack_lanes<4>(e, code, d, s);

@@ -78,12 +78,20 @@ __device__ __forceinline__ float sigmoid32(float g)
     return r;
 }
 
-// x times the gate
-__device__ __forceinline__ float gated(float x, float g, int act)
+// values times their gates (the choice is the call's, made once for all of them)
+template <int E>
+__device__ __forceinline__ void gate_values(float (&x)[E], const float (&g)[E], int act)
 {
-    if (act == ZQ_GATE_LINEAR) return x * g;
-    const float s = sigmoid32(g);
-    return x * (act == ZQ_GATE_SILU ? g * s : s);
+    if (act == ZQ_GATE_LINEAR) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] *= g[e];
+    } else if (act == ZQ_GATE_SIGMOID) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] *= sigmoid32(g[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[e] *= g[e] * sigmoid32(g[e]);
+    }
 }
 
 }  // namespace zq

@@ -65,15 +65,15 @@ __device__ __forceinline__ void q8_1_pack_lanes(const float (&xh)[E], uint32_t (
     int sum = 0;
 #pragma unroll
     for (int v = 0; v < E / 4; ++v) {
-        words[v] = 0;
+        int q[4];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            float q = roundf(__fmul_rn(xh[4 * v + c], id));
-            q = fminf(fmaxf(q, -127.0f), 127.0f);
-            const int qi = (int)q;
-            sum += qi;
-            words[v] |= ((uint32_t)(qi & 0xFF)) << (8 * c);
-        }
+        for (int c = 0; c < 4; ++c)
+            q[c] = (int)fminf(fmaxf(roundf(__fmul_rn(xh[4 * v + c], id)), -127.0f), 127.0f);
+        // four codes to a word, the first in the low byte
+        uint32_t upper;
+        asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, 0;" : "=r"(upper) : "r"(q[3]), "r"(q[2]));
+        asm("cvt.pack.sat.s8.s32.b32 %0, %1, %2, %3;" : "=r"(words[v]) : "r"(q[1]), "r"(q[0]), "r"(upper));
+        sum = __dp4a((int)words[v], 0x01010101, sum);
     }
 #pragma unroll
     for (int off = 16 / E; off >= 1; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);

@@ -691,8 +691,9 @@ ZQ_API int zq_gated_norm_q8_1(const float *x, long long x_stride, int B, int H, 
  *   x_out : fp32 rows, may be x itself (or y), not a part of either;
  *   out   : fp32 rows, may be NULL and may not overlap anything else;
  *   q8_out : planes of B x K, may be NULL.
- * The squares are added up in the order of zq_rmsnorm_q8_1, so the codes are
- * those of zq_rmsnorm_q8_1 on x_out byte for byte.
+ * The squares of x_out are added up in the order of zq_rmsnorm_q8_1, so the codes
+ * are those of zq_rmsnorm_q8_1 on x_out byte for byte.  The result does not change
+ * from one call to the next.
  * Strides multiples of 4.  1 <= B <= 2^24, K % 32 == 0, 32 <= K <= 32768.
  */
 ZQ_API int zq_residual_norm_q8_1(const float *x, long long x_stride, const float *y, long long y_stride, int B, int K,
