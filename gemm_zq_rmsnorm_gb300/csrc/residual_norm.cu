@@ -3,14 +3,18 @@
 // the next block packed to Q8_1 (ZINC docs "ROCm backend", "Build and verify":
 // normalisation and Q8 packing in one per-token kernel).
 //
-// One CTA per token.  Four lanes share a 32-value block, eight neighbouring
-// values each, so that a warp reads 1 KB of consecutive bytes; the whole row
-// stays in registers between its two norms, and every value of x and y is read
-// once.  The norm before the next block adds its squares up in the library's
-// fixed order (the block's fma chain runs through its four lanes), so the codes
-// are those of zq_rmsnorm_q8_1 on x_out, byte for byte.
+// One CTA for a token (or for several in turn).  Four lanes share a 32-value block,
+// eight neighbouring values each, so that a warp reads 1 KB of consecutive bytes; the
+// whole row stays in registers between its two norms, and every value of x and y is
+// read once.  The norm before the next block adds its squares up in the library's
+// fixed order (the block's fma chain runs through its four lanes), so the codes are
+// those of zq_rmsnorm_q8_1 on x_out, byte for byte.
 //
-// HBM bound: 8 bytes a value read (12 with a gate), 4 + 1.125 written.
+// HBM bound: 8 bytes a value read (12 with a gate), 4 + 1.125 written.  4096 x 5120
+// with a norm after the block and a gate 64.5 us, 5.6 TB/s (0.82 of the measured copy
+// rate; issue slots 54 % busy: about 60 instructions a value for the gate, the two
+// norms and the packing); 61 tokens 3.7 us, one 3.6 (2.5 at 1024): two barriers and a
+// chain of dependent loads.
 #include <algorithm>
 #include <atomic>
 
@@ -23,7 +27,7 @@
 namespace zq {
 namespace {
 
-constexpr int kMaxK = 32768, kMaxRowsK = 16384;
+constexpr int kMaxK = 32768, kMaxRowsK = 8192;
 
 __device__ __forceinline__ void load8(const float *p, float (&x)[8])
 {
@@ -261,10 +265,14 @@ cudaError_t launch_residual_norm(const ResidualNormArgs &a, cudaStream_t st)
 {
     const int eights = a.K / 8;
     auto threads = [&](int passes) { return ((eights + passes - 1) / passes + 31) / 32 * 32; };
-    if (a.B > 2 * num_sms() && a.K <= kMaxRowsK)
-        return eights <= 1024 ? launch_rows<2, 512, 64>(a, threads(2), st) : launch_rows<4, 512, 120>(a, threads(4), st);
+    // Rows of 5120 with a norm after the block, in turn against a CTA each: 1000 tokens 21.9 us and 20.2, 2000 33.3 and
+    // 32.0, 4096 with a gate 64.5 and 74; of 8192, 2000 tokens 48.8 and 49.6.
+    if (a.K <= kMaxRowsK && (long long)a.B * a.K >= 10000000) return launch_rows<2, 512, 64>(a, threads(2), st);
     auto direct = [&](auto *kernel, int passes) { return launch_pdl(kernel, dim3((unsigned)a.B), dim3(threads(passes)), 0, st, a); };
-    if (eights <= 1024) return direct(residual_norm_kernel<1, 1024>, 1);
+    // Two pieces a thread let two CTAs run on an SM where they are wide enough for one to fill it: 400 rows of 5120 9.2 us
+    // with one piece, 6.9 with two; 1000 of 8192 34.6 and 29.5; but 400 of 1024 3.1 and 3.6.
+    if (eights <= 1024)
+        return a.B > 2 * num_sms() && a.K > 4096 ? direct(residual_norm_kernel<2, 512>, 2) : direct(residual_norm_kernel<1, 1024>, 1);
     if (eights <= 2048) return direct(residual_norm_kernel<2, 1024>, 2);
     return direct(residual_norm_kernel<4, 1024>, 4);
 }
