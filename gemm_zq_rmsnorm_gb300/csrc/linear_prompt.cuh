@@ -26,7 +26,6 @@
 #include "zq_async.cuh"
 #include "zq_internal.cuh"
 #include "zq_mixer.cuh"
-#include "zq_mma.cuh"
 
 namespace zq {
 
@@ -237,21 +236,6 @@ __device__ __forceinline__ void make_factors(Factors &s, const float (&g)[2], co
     }
 }
 
-__device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm4t(uint32_t (&r)[4], uint32_t addr)
-{
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-
 // Two neighbouring rows of one operand: a lane has four values of each when a row
 // is 128 wide, of one of them when it is 64.
 template <int D>
@@ -295,19 +279,17 @@ struct Rows {
             second = __reduce_max_sync(0xffffffffu, half ? b[0] : 0u);
         }
     }
-    // the rows over 2^e as binary16 parts at(row, 16-byte piece) bytes into hi and lo; fill: instead of them 1 zeros, 2 NaN
+    // the rows over 2^e as binary16 parts at(row, 16-byte piece) bytes into hi and lo
     template <typename At>
-    __device__ __forceinline__ void store(__half *hi, __half *lo, int r, const int (&e)[2], const int (&fill)[2], At at) const
+    __device__ __forceinline__ void store(__half *hi, __half *lo, int r, const int (&e)[2], At at) const
     {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int j = row(i);
             const float s = pow2(-(N == 2 ? e[i] : j ? e[1] : e[0]));
-            const int f = N == 2 ? fill[i] : j ? fill[1] : fill[0];
             uint2 h, l;
             split2(mul2(make_float2(x[i].x, x[i].y), make_float2(s, s)), h.x, l.x);
             split2(mul2(make_float2(x[i].z, x[i].w), make_float2(s, s)), h.y, l.y);
-            if (f) h = l = f == 1 ? make_uint2(0u, 0u) : make_uint2(0x7e007e00u, 0x7e007e00u);
             const uint32_t to = at(r + j, lane() >> 1) + ((lane() & 1) << 3);
             *reinterpret_cast<uint2 *>(reinterpret_cast<char *>(hi) + to) = h;
             *reinterpret_cast<uint2 *>(reinterpret_cast<char *>(lo) + to) = l;

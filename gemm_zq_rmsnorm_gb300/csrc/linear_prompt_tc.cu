@@ -363,7 +363,6 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         constexpr int STEPS = kLoadRows / 2;
         static_assert(STEPS % 2 == 0, "two steps a turn of the loop");
         const int wl = w < 5 ? w - 3 : w - 4;
-        const int none[2] = {0, 0};
         struct Step {
             Rows<DK> q, k;
         } step[2];
@@ -387,8 +386,8 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 x.k.template largest<false>(mk[0], mk[1]);
                 // an infinity or NaN gives parts that are NaN
                 if (!STATES)
-                    x.q.store(sm.q[st][0], sm.q[st][1], r, {row_exponent(mq[0]), row_exponent(mq[1])}, none, tile_piece<DK>);
-                x.k.store(sm.k[st][0], sm.k[st][1], r, {row_exponent(mk[0]), row_exponent(mk[1])}, none, tile_piece<DK>);
+                    x.q.store(sm.q[st][0], sm.q[st][1], r, {row_exponent(mq[0]), row_exponent(mq[1])}, tile_piece<DK>);
+                x.k.store(sm.k[st][0], sm.k[st][1], r, {row_exponent(mk[0]), row_exponent(mk[1])}, tile_piece<DK>);
                 if (lane < 2) {
                     if (!STATES) sm.mq[st][r + lane] = lane ? mq[1] : mq[0];
                     sm.mk[st][r + lane] = lane ? mk[1] : mk[0];
