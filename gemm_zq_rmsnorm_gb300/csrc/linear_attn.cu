@@ -5,17 +5,18 @@
 // S <- exp(g) S + k v^T,  o = scale * S^T q, for every value head h with the key
 // head h / (Hv / Hk).
 //
-// A CTA owns 32 columns of one head's state, in registers: thread (r, c) holds
-// rows r, r + 32, ... of the four columns 4 c, so that a row of the slice is one
-// line of memory.  The token's decay, key and value update the values where they
+// A CTA owns 64 columns of one head's state, in registers: thread (r, c) holds
+// rows r, r + 16, ... of the four columns 4 c, so that a row of the slice is two
+// lines of memory.  The token's decay, key and value update the values where they
 // are, and the products with the query are added up over the rows by shuffles and
 // once through shared memory, in an order that the sizes alone give.
 //
 // HBM bound: every state is read and written once, and not read again before the
-// next token, so it passes through L2 as streaming data.  61 sequences of 48 heads
-// of 128 x 128: 57.4 us, 6.7 TB/s (0.985 of the measured copy rate); without the
-// streaming accesses 66; with slices of 64 columns 61.3 and of 128 66.8, whose CTAs
-// are fewer and end together.  One sequence 2.2 us: one round of loads.
+// next token, so it passes through L2 as streaming data.  What decides is how much of
+// it an SM has on its way: four CTAs an SM (64 registers a thread, 128 KB of state)
+// reach 57.7 us for 61 sequences of 48 heads of 128 x 128, 6.7 TB/s (0.98 of the measured
+// copy rate); five with 48 registers 60.8, eight with slices of 32 columns 63.9, two
+// with slices of 128 66.8.  One sequence 2.2 us: one round of loads.
 #include "zq_async.cuh"
 #include "zq_internal.cuh"
 #include "zq_mixer.cuh"
@@ -24,10 +25,10 @@ namespace zq {
 namespace {
 
 constexpr int kStepThreads = 256;
-constexpr int SL = 32;   // columns of a slice
+constexpr int SL = 64;   // columns of a slice
 
 template <int DK>
-__global__ void __launch_bounds__(kStepThreads) linear_attn_step_kernel(const __grid_constant__ LinearAttnArgs a, int Dv)
+__global__ void __launch_bounds__(kStepThreads, 4) linear_attn_step_kernel(const __grid_constant__ LinearAttnArgs a, int Dv)
 {
     constexpr int C = SL / 4;            // threads of a row
     constexpr int R = kStepThreads / C;  // rows of one pass
@@ -39,29 +40,36 @@ __global__ void __launch_bounds__(kStepThreads) linear_attn_step_kernel(const __
     const int slices = Dv / SL;
     const int col0 = (int)(blockIdx.x % slices) * SL, item = blockIdx.x / slices;
     const int h = item % a.Hv, hk = h / (a.Hv / a.Hk);
-    const long long b = item / a.Hv, slot = a.slots[b];
+    const long long b = item / a.Hv;
+    const int slot = a.slots[b];
+    const float g = a.g ? a.g[b * a.g_stride + h] : 0.0f;
+    const float *q = a.q + b * a.q_stride + (long long)hk * DK + r;
+    const float *k = a.k + b * a.k_stride + (long long)hk * DK + r;
+    const float4 v = *reinterpret_cast<const float4 *>(a.v + b * a.v_stride + (long long)h * Dv + col0 + 4 * c);
+    float kr[N], qr[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        kr[i] = k[i * R];
+        qr[i] = q[i * R];
+    }
     const bool kept = slot >= 0 && slot < a.n;
-    float *sp = a.state + ((slot * a.Hv + h) * DK + r) * Dv + col0 + 4 * c;
+    float *sp = a.state + (((long long)slot * a.Hv + h) * DK + r) * Dv + col0 + 4 * c;
     float4 s[N];
 #pragma unroll
     for (int i = 0; i < N; ++i)
         s[i] = kept ? __ldcs(reinterpret_cast<const float4 *>(sp + (long long)i * R * Dv)) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-    const float *q = a.q + b * a.q_stride + (long long)hk * DK + r;
-    const float *k = a.k + b * a.k_stride + (long long)hk * DK + r;
-    const float4 v = *reinterpret_cast<const float4 *>(a.v + b * a.v_stride + (long long)h * Dv + col0 + 4 * c);
-    const float decay = a.g ? expf(a.g[b * a.g_stride + h]) : 1.0f;
+    const float decay = expf(g);
     float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float kr = k[i * R], qr = q[i * R];
-        s[i].x = __fmaf_rn(s[i].x, decay, kr * v.x);
-        s[i].y = __fmaf_rn(s[i].y, decay, kr * v.y);
-        s[i].z = __fmaf_rn(s[i].z, decay, kr * v.z);
-        s[i].w = __fmaf_rn(s[i].w, decay, kr * v.w);
-        o.x = __fmaf_rn(qr, s[i].x, o.x);
-        o.y = __fmaf_rn(qr, s[i].y, o.y);
-        o.z = __fmaf_rn(qr, s[i].z, o.z);
-        o.w = __fmaf_rn(qr, s[i].w, o.w);
+        s[i].x = __fmaf_rn(s[i].x, decay, kr[i] * v.x);
+        s[i].y = __fmaf_rn(s[i].y, decay, kr[i] * v.y);
+        s[i].z = __fmaf_rn(s[i].z, decay, kr[i] * v.z);
+        s[i].w = __fmaf_rn(s[i].w, decay, kr[i] * v.w);
+        o.x = __fmaf_rn(qr[i], s[i].x, o.x);
+        o.y = __fmaf_rn(qr[i], s[i].y, o.y);
+        o.z = __fmaf_rn(qr[i], s[i].z, o.z);
+        o.w = __fmaf_rn(qr[i], s[i].w, o.w);
     }
     if (kept)
 #pragma unroll
