@@ -41,7 +41,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     const LinearAttnArgs &a = p.a;
     __shared__ int base_s;
     const int b = blockIdx.z, h = blockIdx.y;
-    const int n = segments_of(p, b);
+    int n = segments_of(p, b);
     if (n < 2) return;
     if (threadIdx.x < 32) {   // segments of the sequences before this one
         int sum = 0;
@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     }
     __syncthreads();
     const int base = base_s;
+    n = min(n, p.segments - base);   // starts that decrease could make more than there is room for
     const long long size = (long long)p.Dv * Dk, at = 4 * (blockIdx.x * 256 + threadIdx.x);
     const int slot = a.slots[b];
     float4 first = make_float4(0.0f, 0.0f, 0.0f, 0.0f);

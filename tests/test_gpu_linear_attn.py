@@ -14,6 +14,7 @@ rounding, for every 64 tokens at worst: T / 64 * 2^-17.
 Root mean squares are near 2^-22 by the same steps with random signs; more than
 2^-20 (2^-19 over thousands of tokens) would be a part that went missing."""
 import math
+import threading
 
 import numpy as np
 import pytest
@@ -252,6 +253,74 @@ def test_starts_outside_the_rows_are_cut_off():
     want = zq.linear_attn(q, k, v, g, torch.tensor([0, 10, 35, 40, 40], dtype=torch.int32, device="cuda"),
                           zq.LinearState(p2), slots)
     assert torch.equal(got, want) and torch.equal(pool, p2) and torch.equal(pool[3], before[3])
+
+
+def test_decreasing_starts_stay_inside():
+    """Sequences that overlap are nobody's prompt; the call stays within its rows, states and workspace."""
+    Dk, Dv, T, B = 64, 64, 1500, 9
+    q, k, v, g, pool = make(14, T, 1, 1, Dk, Dv, B + 1)
+    kept = pool[B].clone()
+    starts = torch.tensor([0, T, 0, T, 0, T, 0, T, 0, T], dtype=torch.int32, device="cuda")
+    need = zq.linear_attn_workspace_bytes(T, B, 1, Dk, Dv)
+    room = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
+    out = torch.full((T + 1, Dv), 5.0, device="cuda")
+    zq.linear_attn(q, k, v, g, starts, zq.LinearState(pool), torch.arange(B, dtype=torch.int32, device="cuda"), out=out[:T],
+                   workspace=room[:need])
+    torch.cuda.synchronize()
+    assert need and bool((room[need:] == 77).all()) and bool((out[T] == 5.0).all()) and torch.equal(pool[B], kept)
+    assert zq.device_status() == 0
+
+
+@pytest.mark.parametrize("Dk,Dv", [(64, 64), (128, 256)])
+def test_no_decay_and_one_row(Dk, Dv):
+    """g left out is a decay of one; rows of one token may have any stride."""
+    q, k, v, g, pool = make(15, 200, 2, 4, Dk, Dv, 2)
+    slot = torch.tensor([1], dtype=torch.int32, device="cuda")
+    for T in (1, 70, 200):
+        starts = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        before, p2 = pool.clone(), pool.clone()
+        got = zq.linear_attn(q[:T], k[:T], v[:T], None, starts, zq.LinearState(pool), slot)
+        same = zq.linear_attn(q[:T], k[:T], v[:T], torch.zeros_like(g[:T]), starts, zq.LinearState(p2), slot)
+        assert torch.equal(got, same) and torch.equal(pool, p2) and torch.equal(pool[0], before[0])
+        o, S, bo, bs = ref.recurrence(heads(q[:T], Dk), heads(k[:T], Dk), heads(v[:T], Dv), None, before[1], Dk ** -0.5)
+        check(heads(got, Dv), o, bo[..., None], 2.0 ** -16 + T / 64 * 2.0 ** -17, 2.0 ** -20, T)
+        check(pool[1], S, bs[:, None, None], (1 + T / 64) * 2.0 ** -17, 2.0 ** -20, T)
+        step = zq.linear_attn_step(q[:1], k[:1], v[:1], None, zq.LinearState(before.clone()), slot)
+        o, _, bo, _ = ref.recurrence(heads(q[:1], Dk), heads(k[:1], Dk), heads(v[:1], Dv), None, before[1], Dk ** -0.5)
+        check(heads(step, Dv), o, bo[..., None], 2.0 ** -18, 2.0 ** -21, "step")
+
+
+def test_two_threads_with_streams_of_their_own():
+    """The first calls of new threads, at the same time, each on its stream and with its own workspace."""
+    cases = [make(16 + i, 700, 1, 3, 128, 128, 2) for i in range(2)]
+    ints = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 650, 700], [1, 0])]
+
+    def run(i, pool, stream):
+        q, k, v, g, _ = cases[i]
+        outs = []
+        for _ in range(4):
+            outs.append(zq.linear_attn(q, k, v, g, ints[0], zq.LinearState(pool), ints[1], stream=stream))
+            outs.append(zq.linear_attn_step(q[:2], k[:2], v[:2], g[:2], zq.LinearState(pool), ints[1], stream=stream))
+        return outs
+    wants = []
+    for i in range(2):
+        pool = cases[i][4].clone()
+        wants.append((run(i, pool, None), pool))
+    torch.cuda.synchronize()
+    got = [None, None]
+
+    def thread(i):
+        stream, pool = torch.cuda.Stream(), cases[i][4].clone()
+        torch.cuda.synchronize()
+        got[i] = run(i, pool, stream), pool
+        stream.synchronize()
+    threads = [threading.Thread(target=thread, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for (a, pa), (b, pb) in zip(got, wants):
+        assert torch.equal(pa, pb) and all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_sequences_without_a_state():
