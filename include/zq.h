@@ -647,7 +647,11 @@ ZQ_API int zq_linear_attn_step(const float *q, long long q_stride, const float *
  *   workspace : zq_linear_attn_workspace_bytes(T, B, Hv, Dk, Dv) bytes, 16-byte
  *           aligned; contents do not matter.  Calls that may run at the same time
  *           (other streams, captured graphs) need workspaces of their own.
- * Other arguments as for zq_linear_attn_step.  A NaN or infinity in a token's q,
+ * Other arguments as for zq_linear_attn_step.  Within a chunk of 64 tokens products
+ * are taken of values split into two binary16 parts (2^-22 of the rows' norms), sums
+ * are fp32; the result does not change from one call to the next.  The kernel's
+ * waits are bounded: one that runs out leaves its output invalid and shows in
+ * zq_device_status.  A NaN or infinity in a token's q,
  * k, v or g does not reach earlier tokens, other heads or other sequences.
  * Shapes: 1 <= T <= 2^24, 1 <= B <= 65535.
  */
@@ -659,7 +663,8 @@ ZQ_API int zq_linear_attn(const float *q, long long q_stride, const float *k, lo
                           size_t workspace_bytes, void *stream);
 
 /* What a gate's values pass through before they multiply: nothing, 1 / (1 +
- * exp(-g)), or g / (1 + exp(-g)). */
+ * exp(-g)), or g / (1 + exp(-g)); the sigmoid to about 2^-21 of itself, and zero
+ * where it is below 2^-126. */
 enum { ZQ_GATE_LINEAR = 0, ZQ_GATE_SIGMOID = 1, ZQ_GATE_SILU = 2 };
 
 /*
