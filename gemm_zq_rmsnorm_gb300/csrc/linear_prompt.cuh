@@ -55,20 +55,22 @@ __device__ __forceinline__ int segments_of(const PromptArgs &p, int b)
 
 struct Segment {
     int seq, seg, last, row0, row1;   // seq < 0: there is none
+    int place;                        // its number of all segments
 };
 
-// Segment number `at` of the call, by one warp.
-__device__ __forceinline__ Segment find_segment(const PromptArgs &p, int at)
+// Segment number `at` of the call, or of those that are not their sequence's last,
+// by one warp.
+__device__ __forceinline__ Segment find_segment(const PromptArgs &p, int at, bool but_last)
 {
     const LinearAttnArgs &a = p.a;
     const int lane = threadIdx.x & 31;
-    Segment s{-1, 0, 1, 0, 0};
+    Segment s{-1, 0, 1, 0, 0, at};
     if (p.length == 0) {
         s.seq = at;
     } else {
         int base = 0;
         for (int b0 = 0; b0 < a.B && s.seq < 0; b0 += 32) {
-            const int cnt = b0 + lane < a.B ? segments_of(p, b0 + lane) : 0;
+            const int cnt = b0 + lane < a.B ? segments_of(p, b0 + lane) - but_last : 0;
             int sum = cnt;
 #pragma unroll
             for (int d = 1; d < 32; d <<= 1) {
@@ -80,12 +82,13 @@ __device__ __forceinline__ Segment find_segment(const PromptArgs &p, int at)
                 const int l = __ffs(who) - 1;
                 s.seq = b0 + l;
                 s.seg = at - base - __shfl_sync(0xffffffffu, sum - cnt, l);
-                s.last = s.seg + 1 == __shfl_sync(0xffffffffu, cnt, l);
+                s.last = !but_last && s.seg + 1 == __shfl_sync(0xffffffffu, cnt, l);
             }
             base += __shfl_sync(0xffffffffu, sum, 31);
         }
     }
     if (s.seq >= 0) {
+        if (but_last) s.place += s.seq;   // a last segment of each sequence before
         int r0, r1;
         sequence_rows(a, s.seq, r0, r1);
         s.row0 = r0 + s.seg * p.length;
@@ -185,11 +188,8 @@ __device__ __forceinline__ long long log2_units(float x)
 
 __device__ __forceinline__ long long clamp_units(long long G) { return min(max(G, -(1LL << 44)), 1LL << 44); }
 
-// The factors of a chunk's rows, by one warp with two tokens a lane: their decays,
-// exponents of key and value together (INT_MIN: one of them is zero) and of the query.
-// M need only be near the largest u: it is the whole number above it.
-__device__ __forceinline__ void make_factors(Factors &s, const float (&g)[2], const int (&ekv)[2], const int (&eq)[2],
-                                             float scale)
+// G of a chunk's tokens from their decays, by one warp with two tokens a lane.
+__device__ __forceinline__ void sum_decays(const float (&g)[2], long long (&G)[2])
 {
     const int lane = threadIdx.x & 31;
     const long long b = log2_units(g[1]);
@@ -199,7 +199,17 @@ __device__ __forceinline__ void make_factors(Factors &s, const float (&g)[2], co
         const long long o = __shfl_up_sync(0xffffffffu, sum, d);
         if (lane >= d) sum += o;
     }
-    const long long G[2] = {sum - b, sum};
+    G[0] = sum - b;
+    G[1] = sum;
+}
+
+// The factors of a chunk's rows, by the same warp: from G, the exponents of key and
+// value together (INT_MIN: one of them is zero) and of the query.  M need only be near
+// the largest u: it is the whole number above it.
+__device__ __forceinline__ void make_factors(Factors &s, const long long (&G)[2], const int (&ekv)[2], const int (&eq)[2],
+                                             float scale)
+{
+    const int lane = threadIdx.x & 31;
     int uw[2], M[2];
     float ub[2];
 #pragma unroll
@@ -230,9 +240,9 @@ __device__ __forceinline__ void make_factors(Factors &s, const float (&g)[2], co
         s.w[t] = exp2_parts(uw[i] - last, ub[i]);
     }
     if (lane == 31) {
-        s.keep = exp2_units(sum);
-        s.add = exp2_parts(whole(sum) + last, broken(sum));
-        s.G = sum;
+        s.keep = exp2_units(G[1]);
+        s.add = exp2_parts(whole(G[1]) + last, broken(G[1]));
+        s.G = G[1];
     }
 }
 

@@ -11,11 +11,12 @@
 // stays in the registers of sixteen warps (four threads for a column), which add U to
 // it, split it for the next chunk and put O1 and O2 together.
 //
-// and the scores Q K^T the same way.  Warps: 0, 1 and 5 weigh scores, 0 makes the
-// chunk's factors as well; 2 issues the MMAs; 3, 4 and 6..11 convert queries and keys;
-// 12..15 values, a lane for a column; 16..31 the state.  Keys and queries are two
-// stages deep; the key tile serves the scores as rows and U as columns (the same
-// bytes, a descriptor of the other order).
+// and the scores Q K^T the same way, in U's place.  Warps: 0, 1 and 5 weigh scores, 0
+// makes the chunk's factors as well; 2 issues the MMAs; 3, 4 and 6..11 convert queries
+// and keys; 12..15 values for the output, a lane for a column, and the sizes of their
+// rows; 16..31 the state and the values weighted for it.  Keys and queries are two
+// stages deep; the key tile serves the scores as rows and U as columns (the same bytes,
+// a descriptor of the other order).
 //
 // Every wait is bounded: after one has run out no MMA is issued any more, the
 // others return at once and the kernel ends (its results are invalid).
@@ -35,6 +36,7 @@ constexpr int kLoadRows = C / LW;  // rows of a chunk of a warp that converts
 constexpr int kThreads = kWarps * 32;
 // tensor memory columns
 constexpr int kO1 = 0, kO2 = 64, kU = 128, kSh = 256, kSl = 320, kVh = 384, kVl = 416, kWh = 448, kWl = 480;
+constexpr int kU2 = 0;   // a second U where there is no output
 static_assert(kVl - kVh == kWl - kWh, "low parts behind high ones");
 
 template <int DK, int DV>
@@ -48,8 +50,8 @@ struct Smem {
     } f[4];
     alignas(16) uint32_t mq[2][C], mk[2][C], mv[2][C];   // bits of the rows' largest magnitudes
     uint32_t smax[4][128];
-    uint64_t qk_full[2], qk_empty[2], values[2], fact[4];
-    uint64_t scores, scores_read, sizes, p_full, w_full, v_full, s_full, o_full, o_empty, u_full, u_empty;
+    uint64_t qk_full[2], qk_empty[2], values[2], sizes[2], w_full[2], fact[4];
+    uint64_t scores, scores_read, p_full, v_full, s_full, o_full, o_empty, u_full, u_empty[2];
     uint32_t tmem;
     int abort;
     Segment seg;
@@ -67,6 +69,12 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
                  : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x4.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3])
+                 : "memory");
 }
 
 // The warp waits for a phase.  Many waiting warps share the issue slots (and the
@@ -113,37 +121,65 @@ __device__ __forceinline__ void wait_phase(uint64_t *bar, int parity, volatile i
 // B from columns: bit 16 of the instruction descriptor
 __host__ __device__ constexpr uint32_t idesc_b_columns(uint32_t M, uint32_t N) { return idesc_f16_f32(M, N) | 1u << 16; }
 
-// Sixteen columns of the scores, from tensor memory: weighted, as parts, to P.  The
-// warp has the rows 32 quarter .., a lane each; columns 16 j ...
+// 32 columns of the scores, from tensor memory: weighted, as parts to P.  The warp has
+// the rows 32 quarter .., a lane each; columns 32 side ...  All of them are taken before
+// the first is weighted, since the chunk's U waits for their place.
 template <int DK, int DV>
-__device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, uint32_t tmem, int quarter, int j)
+__device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, uint32_t tmem, int quarter, int side)
 {
     const int lane = threadIdx.x & 31, tr = 32 * quarter + lane;
-    uint32_t s[16];
-    tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + kU + 16 * j, s);
+    uint32_t s[2][16];
+    tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + kU + 32 * side, s[0]);
+    tmem_ld16(tmem + ((uint32_t)(32 * quarter) << 16) + kU + 32 * side + 16, s[1]);
     const float m = -f.m[tr];
     tmem_wait_ld();
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sm.scores_read);
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
+    for (int piece = 0; piece < 4; ++piece) {
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-            const int sc = 16 * j + 8 * half + 2 * i;
+            const int sc = 32 * side + 8 * piece + 2 * i;
             const float4 uh = *reinterpret_cast<const float4 *>(&f.uh[sc]), ul = *reinterpret_cast<const float4 *>(&f.ul[sc]);
             auto two = [&](int e, float2 h, float2 l, uint32_t &phi, uint32_t &plo) {
                 const float2 x = add2(add2(h, make_float2(m, m)), l);
-                float2 y = mul2(make_float2(__uint_as_float(s[8 * half + 2 * i + e]), __uint_as_float(s[8 * half + 2 * i + e + 1])),
+                const uint32_t *y0 = &s[piece >> 1][8 * (piece & 1) + 2 * i + e];
+                float2 y = mul2(make_float2(__uint_as_float(y0[0]), __uint_as_float(y0[1])),
                                 make_float2(exp2_fast(x.x), exp2_fast(x.y)));
-                if (j >= 2 * quarter) y = make_float2(sc + e <= tr ? y.x : 0.0f, sc + e + 1 <= tr ? y.y : 0.0f);
+                if (side == quarter) y = make_float2(sc + e <= tr ? y.x : 0.0f, sc + e + 1 <= tr ? y.y : 0.0f);
                 split2(y, phi, plo);
             };
             two(0, make_float2(uh.x, uh.y), make_float2(ul.x, ul.y), hi[i], lo[i]);
             two(2, make_float2(uh.z, uh.w), make_float2(ul.z, ul.w), hi[i + 1], lo[i + 1]);
         }
-        const uint32_t to = tile_piece<C>(tr, 2 * j + half);
+        const uint32_t to = tile_piece<C>(tr, 4 * side + piece);
         *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(sm.p[0]) + to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
         *reinterpret_cast<uint4 *>(reinterpret_cast<char *>(sm.p[1]) + to) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     }
+}
+
+// Eight tokens' values of the lane's column, scaled, as parts to tensor memory.
+template <int DK, int DV>
+__device__ __forceinline__ void value_parts(const Smem<DK, DV> &sm, const typename Smem<DK, DV>::Chunk &f, const float *scale, int c,
+                                            int first, int column, uint32_t to)
+{
+    float x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = sm.v[c & 1][(first + i) * DV + column];
+    if (f.some_bad)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = f.vscale[first + i] == 0.0f ? 0.0f : x[i];
+    uint32_t ph[4], pl[4];
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) {
+        const float4 y = *reinterpret_cast<const float4 *>(scale + first + 2 * i);
+        split2(mul2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(y.x, y.y)), ph[i], pl[i]);
+        split2(mul2(make_float2(x[2 * i + 2], x[2 * i + 3]), make_float2(y.z, y.w)), ph[i + 1], pl[i + 1]);
+    }
+    tmem_st4(to, ph);
+    tmem_st4(to + (kVl - kVh), pl);
 }
 
 template <int DK, int DV, bool STATES>
@@ -174,21 +210,22 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.qk_full[i], LW);
             mbar_init(&sm.qk_empty[i], 1);
+            mbar_init(&sm.sizes[i], 4);
+            mbar_init(&sm.w_full[i], 4 * QUARTERS);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sm.fact[i], 1);
         mbar_init(&sm.values[0], 1);
         mbar_init(&sm.values[1], 1);
-        mbar_init(&sm.sizes, LW);
         mbar_init(&sm.p_full, 3);
         mbar_init(&sm.scores, 1);
         mbar_init(&sm.scores_read, 3);
-        mbar_init(&sm.w_full, QUARTERS);
         mbar_init(&sm.v_full, QUARTERS);
         mbar_init(&sm.s_full, 4 * QUARTERS);
         mbar_init(&sm.o_full, 1);
         mbar_init(&sm.o_empty, 4 * QUARTERS);
         mbar_init(&sm.u_full, 1);
-        mbar_init(&sm.u_empty, 4 * QUARTERS);
+        mbar_init(&sm.u_empty[0], 4 * QUARTERS);
+        mbar_init(&sm.u_empty[1], 4 * QUARTERS);
         sm.abort = 0;
         fence_mbar_init();
     }
@@ -201,7 +238,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     const int tile = blockIdx.x % tiles, item = blockIdx.x / tiles;
     const int h = item % a.Hv, at = item / a.Hv, col0 = tile * DV;
     if (w == 3) {
-        const Segment s = find_segment(p, at);
+        const Segment s = find_segment(p, at, STATES);
         if (lane == 0) sm.seg = s;
     }
     tc_fence_before();
@@ -211,8 +248,8 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     pdl_launch_dependents();
     const uint32_t tmem = sm.tmem;
     const Segment seg = sm.seg;
-    const int chunks = seg.seq < 0 || (STATES && seg.last) ? 0 : (seg.row1 - seg.row0 + C - 1) / C;
-    const bool any = seg.seq >= 0 && !(STATES && seg.last);
+    const bool any = seg.seq >= 0;
+    const int chunks = any ? (seg.row1 - seg.row0 + C - 1) / C : 0;
     const int hk = h / (a.Hv / a.Hk);
 
     if (w == kWarpM) {
@@ -230,7 +267,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         auto scores = [&](int c) {   // Q K^T in U's place; lanes 64 .. hold the product of whatever lies behind the queries
             const int st = c & 1;
             wait(sm.qk_full[st], c >> 1);
-            if (c) wait(sm.u_empty, c - 1);
+            if (c) wait(sm.u_empty[0], c - 1);
             tc_fence_after();
             if (!*abort_flag && leader) {
 #pragma unroll
@@ -248,25 +285,12 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
             if (!STATES) {
-                wait(sm.s_full, c);
-                if (c) wait(sm.o_empty, c - 1);
-                tc_fence_after();
-                if (!*abort_flag && leader) {
-#pragma unroll
-                    for (int i = 0; i < 3; ++i) {
-                        const uint32_t as = tmem + (i == 0 ? kSl : kSh), b = q0 + st * stage + (i == 1 ? part : 0);
-#pragma unroll
-                        for (int kk = 0; kk < DK / 16; ++kk)
-                            mma_f16_ta(tmem + kO1, as + 8 * kk, desc(b + rows_at(kk)), id_o, i || kk);
-                    }
-                }
-                __syncwarp();
                 wait(sm.scores_read, c);
             } else {
                 wait(sm.qk_full[st], c >> 1);
-                if (c) wait(sm.u_empty, c - 1);
+                if (c >= 2) wait(sm.u_empty[st], (c >> 1) - 1);
             }
-            wait(sm.w_full, c);
+            wait(sm.w_full[st], c >> 1);
             tc_fence_after();
             if (!*abort_flag && leader) {
 #pragma unroll
@@ -274,13 +298,27 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     const uint32_t av = tmem + (i == 0 ? kWl : kWh), b = k0 + st * stage + (i == 1 ? part : 0);
 #pragma unroll
                     for (int kk = 0; kk < C / 16; ++kk)
-                        mma_f16_ta(tmem + kU, av + 8 * kk, desc(b + (kk * 2048 >> 4)), id_u, i || kk);
+                        mma_f16_ta(tmem + (STATES && st ? kU2 : kU), av + 8 * kk, desc(b + (kk * 2048 >> 4)), id_u, i || kk);
                 }
                 mma_commit(&sm.u_full);
-                mma_commit(&sm.qk_empty[st]);
+                if (STATES) mma_commit(&sm.qk_empty[st]);
             }
             __syncwarp();
             if (STATES) continue;
+            wait(sm.s_full, c);
+            if (c) wait(sm.o_empty, c - 1);
+            tc_fence_after();
+            if (!*abort_flag && leader) {
+#pragma unroll
+                for (int i = 0; i < 3; ++i) {
+                    const uint32_t as = tmem + (i == 0 ? kSl : kSh), b = q0 + st * stage + (i == 1 ? part : 0);
+#pragma unroll
+                    for (int kk = 0; kk < DK / 16; ++kk)
+                        mma_f16_ta(tmem + kO1, as + 8 * kk, desc(b + rows_at(kk)), id_o, i || kk);
+                }
+                mma_commit(&sm.qk_empty[st]);
+            }
+            __syncwarp();
             wait(sm.v_full, c);
             wait(sm.p_full, c);
             tc_fence_after();
@@ -299,18 +337,24 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     } else if (weighs(w)) {
         // ------------------------------------------------------------ a chunk's factors (warp 0) and the scores' weights
         // warp 0 has the rows 0 .. 31 (32 columns), the others the rows 32 .. 63, half of the columns each
-        const int quarter = w & 3, first = w == 5 ? 2 : 0;
-        auto factors = [&](int c) {
-            const int st = c & 1;
-            const long long row = seg.row0 + c * C;
-            const int n = seg.row1 - (int)row;
-            float g[2] = {0.0f, 0.0f};
-            if (a.g)
+        const int quarter = w & 3, side = w == 5;
+        float next[2];   // decays of the next chunk
+        auto decays = [&](int c) {
 #pragma unroll
-                for (int i = 0; i < 2; ++i)
-                    if (2 * lane + i < n) g[i] = a.g[(row + 2 * lane + i) * a.g_stride + h];
+            for (int i = 0; i < 2; ++i) {
+                const long long row = (long long)seg.row0 + c * C + 2 * lane + i;
+                next[i] = a.g && row < seg.row1 ? a.g[row * a.g_stride + h] : 0.0f;
+            }
+        };
+        if (w == 0 && chunks) decays(0);
+        auto factors = [&](int c) {
+            const int st = c & 1, n = seg.row1 - seg.row0 - c * C;
+            const float g[2] = {next[0], next[1]};
+            decays(c + 1);
+            long long G[2];
+            sum_decays(g, G);
             wait(sm.qk_full[st], c >> 1);
-            wait(sm.sizes, c);
+            wait(sm.sizes[st], c >> 1);
             typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
             int ekv[2], eq[2], ev[2];
             bool bad[2], odd[2];
@@ -327,7 +371,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 ekv[i] = !bad[i] && (s >= n || mk == 0u || mv == 0u) ? INT_MIN : ev[i] + row_exponent(mk);
                 eq[i] = STATES ? 0 : row_exponent(sm.mq[st][s]);
             }
-            make_factors(f, g, ekv, eq, a.scale);
+            make_factors(f, G, ekv, eq, a.scale);
             const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -347,11 +391,8 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 if (c) wait(sm.o_full, c - 1);   // the last weights have been read
                 wait(sm.scores, c);
                 tc_fence_after();
-#pragma unroll 1
-                for (int j = first; j < first + 2; ++j) weigh_scores<DK, DV>(sm, sm.f[c & 3], tmem, quarter, j);
-                tc_fence_before();
+                weigh_scores<DK, DV>(sm, sm.f[c & 3], tmem, quarter, side);
                 fence_async_smem();
-                arrive(sm.scores_read);
                 arrive(sm.p_full);
             }
             if (w == 0 && c + 1 < chunks) factors(c + 1);
@@ -378,7 +419,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         for (int c = 0; c < chunks; ++c) {
             const int st = c & 1;
             if (c >= 2 && wl == 0) wait(sm.qk_empty[st], (c >> 1) - 1);
-            sync(0);   // (also: no warp's count in `sizes` is a chunk ahead of another's)
+            sync(0);
             auto convert = [&](const Step &x, int j) {
                 const int r = kLoadRows * wl + 2 * j;
                 uint32_t mq[2], mk[2];
@@ -402,23 +443,6 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             }
             fence_async_smem();
             arrive(sm.qk_full[st]);
-            // the sizes of the values' rows
-            wait(sm.values[st], c >> 1);
-            static_assert(kLoadRows == 8, "eight rows at a time");
-            {
-                const int r = kLoadRows * wl;
-                Rows<DV> v[4];
-                uint32_t m[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i].load_shared(sm.v[st] + (r + 2 * i) * DV);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i].largest(m[2 * i], m[2 * i + 1]);
-                if (lane == 0) {
-                    *reinterpret_cast<uint4 *>(&sm.mv[st][r]) = make_uint4(m[0], m[1], m[2], m[3]);
-                    *reinterpret_cast<uint4 *>(&sm.mv[st][r + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
-                }
-            }
-            arrive(sm.sizes);
         }
     } else if (w < kWarpE) {
         // ------------------------------------------------------------ values
@@ -438,50 +462,48 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 __syncwarp();
             }
         };
+        // bits of the largest magnitudes of the values' rows, sixteen rows a warp
+        auto sizes = [&](int c) {
+            if (c >= chunks) return;
+            if (w == kWarpV) wait(sm.values[c & 1], c >> 1);
+            sync(kWarpV);
+#pragma unroll 1
+            for (int r = 16 * (w - kWarpV); r < 16 * (w - kWarpV) + 16; r += 8) {
+                Rows<DV> v[4];
+                uint32_t m[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i].load_shared(sm.v[c & 1] + (r + 2 * i) * DV);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i].largest(m[2 * i], m[2 * i + 1]);
+                if (lane == 0) {
+                    *reinterpret_cast<uint4 *>(&sm.mv[c & 1][r]) = make_uint4(m[0], m[1], m[2], m[3]);
+                    *reinterpret_cast<uint4 *>(&sm.mv[c & 1][r + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
+                }
+            }
+            arrive(sm.sizes[c & 1]);
+        };
         request(0);
         request(1);
+        sizes(0);
         for (int c = 0; c < chunks; ++c) {
-            const typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
-            // weighted for the state, then as they are for the output; read twice rather than kept (the code of a
-            // kernel with so many kinds of warps has to stay small: unrolled over 64 tokens it ran at half the speed)
-#pragma unroll 1
-            for (int pass = 0; pass < (STATES ? 1 : 2); ++pass) {
+            sizes(c + 1);
+            if (!STATES) {
                 if (w == kWarpV) {
-                    if (!pass) {
-                        wait(sm.values[c & 1], c >> 1);
-                        wait(sm.fact[c & 3], c >> 2);
-                    }
-                    // the last chunk's MMAs have read what is written now
-                    if (c) wait(pass ? sm.o_full : sm.u_full, c - 1);
+                    wait(sm.fact[c & 3], c >> 2);
+                    if (c) wait(sm.o_full, c - 1);   // the last chunk's MMAs have read what is written now
                 }
                 sync(kWarpV);
                 tc_fence_after();
-                if (!mine) continue;
-                const float *scale = pass ? f.vscale : f.wscale;
-                uint32_t to = lanes + (pass ? kVh : kWh);
+                if (mine) {
 #pragma unroll 1
-                for (int b = 0; b < C / 16; ++b, to += 8) {
-                    float x[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) x[i] = sm.v[c & 1][(16 * b + i) * DV + column];
-                    if (f.some_bad)
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) x[i] = f.vscale[16 * b + i] == 0.0f ? 0.0f : x[i];
-                    uint32_t ph[8], pl[8];
-#pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float4 y = *reinterpret_cast<const float4 *>(scale + 16 * b + 2 * i);
-                        split2(mul2(make_float2(x[2 * i], x[2 * i + 1]), make_float2(y.x, y.y)), ph[i], pl[i]);
-                        split2(mul2(make_float2(x[2 * i + 2], x[2 * i + 3]), make_float2(y.z, y.w)), ph[i + 1], pl[i + 1]);
-                    }
-                    tmem_st8(to, ph);
-                    tmem_st8(to + (kVl - kVh), pl);
+                    for (int b = 0; b < C / 8; ++b) value_parts(sm, sm.f[c & 3], sm.f[c & 3].vscale, c, 8 * b, column, lanes + kVh + 4 * b);
+                    tmem_wait_st();
+                    tc_fence_before();
+                    arrive(sm.v_full);
                 }
-                tmem_wait_st();
-                tc_fence_before();
-                arrive(pass ? sm.v_full : sm.w_full);
+                sync(kWarpV);   // the values are read before the next ones come, by the state's warps as well
             }
-            sync(kWarpV);   // the values are read before the next ones come
+            if (w == kWarpV) wait(sm.w_full[c & 1], c >> 1);
             request(c + 2);
         }
         // copies still on their way when a wait has run out
@@ -495,7 +517,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         const int slot = any ? a.slots[seg.seq] : -1;
         const bool kept = slot >= 0 && slot < a.n;
         const long long place = (long long)part * N * p.Dv + col0 + column;
-        float *local = p.local + ((long long)at * a.Hv + h) * DK * p.Dv + place;
+        float *local = p.local + ((long long)seg.place * a.Hv + h) * DK * p.Dv + place;
         float *pool = a.state + ((long long)(kept ? slot : 0) * a.Hv + h) * DK * p.Dv + place;
         const bool mine = any && quarter < QUARTERS;
         const int last = mine ? chunks : 0;
@@ -538,15 +560,29 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             tc_fence_before();
             arrive(sm.s_full);
         };
+        // the values weighted for the state, sixteen tokens a warp
+        auto weighted = [&](int c) {
+            if (w == kWarpE) {
+                wait(sm.values[c & 1], c >> 1);
+                wait(sm.fact[c & 3], c >> 2);
+            }
+            sync(kWarpE);
+            tc_fence_after();
+#pragma unroll 1
+            for (int b = 0; b < 2; ++b)
+                value_parts(sm, sm.f[c & 3], sm.f[c & 3].wscale, c, 16 * part + 8 * b, column, lanes + kWh + 8 * part + 4 * b);
+            tmem_wait_st();
+            tc_fence_before();
+            arrive(sm.w_full[c & 1]);
+        };
         if (!STATES && last) publish([] {});
+        if (last) weighted(0);
         for (int c = 0; c < last; ++c) {
             const Factors &f = sm.f[c & 3];
-            if (w == kWarpE) {
-                wait(sm.fact[c & 3], c >> 2);
-                wait(sm.u_full, c);
-            }
+            if (w == kWarpE) wait(sm.u_full, c);
             sync(kWarpE);   // (the maxima of the last chunk have been read, too)
             tc_fence_after();
+            if (STATES && c + 1 < chunks) weighted(c + 1);
             const float xs = pow2(exponent);   // of the state that O1 was made with
             const float keep = f.keep;
             float add = f.add * pow2(-exponent);
@@ -558,7 +594,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
 #pragma unroll
             for (int b = 0; b < N / 16; ++b) {
                 uint32_t u[16];
-                tmem_ld16(lanes + kU + part * N + 16 * b, u);
+                tmem_ld16(lanes + (STATES && (c & 1) ? kU2 : kU) + part * N + 16 * b, u);
                 tmem_wait_ld();
 #pragma unroll
                 for (int i = 0; i < 16; i += 2) {
@@ -571,12 +607,13 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             }
             if (STATES) G = clamp_units(G + f.G);
             tc_fence_before();
-            arrive(sm.u_empty);
+            arrive(sm.u_empty[STATES ? c & 1 : 0]);
             if (STATES) continue;
             auto products = [&] {
                 if (w == kWarpE) wait(sm.o_full, c);
             };
             if (c + 1 < chunks) {
+                weighted(c + 1);
                 publish(products);
             } else {
                 products();
@@ -624,7 +661,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
 #pragma unroll
             for (int i = 0; i < N; ++i) (STATES ? local : pool)[(long long)i * p.Dv] = S[i] * pow2(exponent);
         }
-        if (STATES && any && tile == 0 && w == kWarpE && lane == 0) p.decay[(long long)at * a.Hv + h] = G;
+        if (STATES && any && tile == 0 && w == kWarpE && lane == 0) p.decay[(long long)seg.place * a.Hv + h] = G;
     }
     tc_fence_before();
     __syncthreads();
@@ -649,7 +686,8 @@ cudaError_t launch(const PromptArgs &p, cudaStream_t st)
         if (e != cudaSuccess) return e;
         ready[dev & 63].store(true, std::memory_order_release);
     }
-    const long long ctas = (long long)p.segments * p.a.Hv * (p.Dv / DV);
+    // segments that are not the last of their sequence are full ones
+    const long long ctas = (long long)(STATES ? p.a.T / p.length : p.segments) * p.a.Hv * (p.Dv / DV);
     PromptArgs args = p;
     args.status = device_status_word();
     const LinearAttnArgs &a = p.a;
