@@ -35,7 +35,10 @@ struct PromptArgs {
     LinearAttnArgs a;
     int Dv;
     int length, segments;      // tokens of a segment (a multiple of kChunk; 0: sequences are not cut), segments at most
-    float *local;              // [segments][Hv][Dk][Dv]: a segment's own state, then the one it starts from
+    int few;                   // few segments of a sequence: each makes the state that it starts from itself
+    // [segments][Hv][Dk][Dv]: a segment's own state, then the one it starts from; few: its own state, and in the place of a
+    // sequence's last segment what the sequence starts from
+    float *local;
     long long *decay;          // [segments][Hv]: its G
     unsigned int *status;
 };
@@ -55,7 +58,7 @@ __device__ __forceinline__ int segments_of(const PromptArgs &p, int b)
 
 struct Segment {
     int seq, seg, last, row0, row1;   // seq < 0: there is none
-    int place;                        // its number of all segments
+    int place, count;                 // its number of all segments, the sequence's segments
 };
 
 // Segment number `at` of the call, or of those that are not their sequence's last,
@@ -64,7 +67,7 @@ __device__ __forceinline__ Segment find_segment(const PromptArgs &p, int at, boo
 {
     const LinearAttnArgs &a = p.a;
     const int lane = threadIdx.x & 31;
-    Segment s{-1, 0, 1, 0, 0, at};
+    Segment s{-1, 0, 1, 0, 0, at, 1};
     if (p.length == 0) {
         s.seq = at;
     } else {
@@ -82,7 +85,8 @@ __device__ __forceinline__ Segment find_segment(const PromptArgs &p, int at, boo
                 const int l = __ffs(who) - 1;
                 s.seq = b0 + l;
                 s.seg = at - base - __shfl_sync(0xffffffffu, sum - cnt, l);
-                s.last = !but_last && s.seg + 1 == __shfl_sync(0xffffffffu, cnt, l);
+                s.count = __shfl_sync(0xffffffffu, cnt, l) + but_last;
+                s.last = s.seg + 1 == s.count;
             }
             base += __shfl_sync(0xffffffffu, sum, 31);
         }
@@ -205,7 +209,8 @@ __device__ __forceinline__ void sum_decays(const float (&g)[2], long long (&G)[2
 
 // The factors of a chunk's rows, by the same warp: from G, the exponents of key and
 // value together (INT_MIN: one of them is zero) and of the query.  M need only be near
-// the largest u: it is the whole number above it.
+// the largest u: it is the whole number above it.  OUT: with those of the output.
+template <bool OUT>
 __device__ __forceinline__ void make_factors(Factors &s, const long long (&G)[2], const int (&ekv)[2], const int (&eq)[2],
                                              float scale)
 {
@@ -217,26 +222,32 @@ __device__ __forceinline__ void make_factors(Factors &s, const long long (&G)[2]
         uw[i] = ekv[i] == INT_MIN ? kNothing : ekv[i] + whole(-G[i]);
         ub[i] = broken(-G[i]);
     }
-    int top = max(uw[0], uw[1]);
+    int top = max(uw[0], uw[1]), last;
+    if (OUT) {
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, top, d);
-        if (lane >= d) top = max(top, o);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, top, d);
+            if (lane >= d) top = max(top, o);
+        }
+        const int before = __shfl_up_sync(0xffffffffu, top, 1);
+        M[0] = (lane ? max(before, uw[0]) : uw[0]) + 1;
+        M[1] = top + 1;
+        last = __shfl_sync(0xffffffffu, M[1], 31);
+    } else {
+        last = __reduce_max_sync(0xffffffffu, top) + 1;
     }
-    const int before = __shfl_up_sync(0xffffffffu, top, 1);
-    M[0] = (lane ? max(before, uw[0]) : uw[0]) + 1;
-    M[1] = top + 1;
-    const int last = __shfl_sync(0xffffffffu, M[1], 31);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
-        s.uh[t] = (float)uw[i];
-        s.ul[t] = ub[i];
-        s.m[t] = (float)M[i];
-        const int n = whole(G[i]) + eq[i];
-        const float part = broken(G[i]);
-        s.f1[t] = scale * exp2_parts(n + M[i], part);
-        s.f2[t] = scale * exp2_parts(n, part);
+        if (OUT) {
+            s.uh[t] = (float)uw[i];
+            s.ul[t] = ub[i];
+            s.m[t] = (float)M[i];
+            const int n = whole(G[i]) + eq[i];
+            const float part = broken(G[i]);
+            s.f1[t] = scale * exp2_parts(n + M[i], part);
+            s.f2[t] = scale * exp2_parts(n, part);
+        }
         s.w[t] = exp2_parts(uw[i] - last, ub[i]);
     }
     if (lane == 31) {

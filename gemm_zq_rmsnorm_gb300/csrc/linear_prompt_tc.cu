@@ -371,7 +371,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 ekv[i] = !bad[i] && (s >= n || mk == 0u || mv == 0u) ? INT_MIN : ev[i] + row_exponent(mk);
                 eq[i] = STATES ? 0 : row_exponent(sm.mq[st][s]);
             }
-            make_factors(f, G, ekv, eq, a.scale);
+            make_factors<!STATES>(f, G, ekv, eq, a.scale);
             const float nan = __int_as_float(0x7fc00000);
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -451,7 +451,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         const bool mine = quarter < QUARTERS;
         int asked = 0;
         auto request = [&](int c) {   // the values of a chunk, its queries and keys as far as L2
-            if (c < chunks && w == kWarpV && !*abort_flag) {
+            if (c < chunks && w == kWarpV && !__any_sync(0xffffffffu, *abort_flag)) {
                 asked = c + 1;
                 if (lane == 0) {
                     if (!STATES) tma_prefetch_2d(&map_q, hk * DK, seg.row0 + c * C);
@@ -513,18 +513,37 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         const int quarter = w & 3, part = (w - kWarpE) >> 2, column = 32 * quarter + lane;
         const uint32_t lanes = tmem + ((uint32_t)(32 * quarter) << 16);
         constexpr int N = DK / 4;   // values of the state of a thread: rows part * N ..
-        const bool cut = p.length != 0 && (seg.seg > 0 || !seg.last);
+        const bool cut = p.length != 0 && seg.count > 1;
+        // (starts that decrease could make more segments than there is room for)
+        const int start = min(seg.place - seg.seg + seg.count, p.segments) - 1;   // where `few` keeps what the sequence starts from
         const int slot = any ? a.slots[seg.seq] : -1;
         const bool kept = slot >= 0 && slot < a.n;
-        const long long place = (long long)part * N * p.Dv + col0 + column;
-        float *local = p.local + ((long long)seg.place * a.Hv + h) * DK * p.Dv + place;
-        float *pool = a.state + ((long long)(kept ? slot : 0) * a.Hv + h) * DK * p.Dv + place;
+        const long long place = (long long)part * N * p.Dv + col0 + column, size = (long long)DK * p.Dv;
+        auto local = [&](int number) { return p.local + ((long long)number * a.Hv + h) * size + place; };
+        float *pool = a.state + ((long long)(kept ? slot : 0) * a.Hv + h) * size + place;
         const bool mine = any && quarter < QUARTERS;
         const int last = mine ? chunks : 0;
-        const bool zeros = !mine || STATES || (!cut && (!kept || (a.fresh && a.fresh[seg.seq] != 0)));
+        const bool zeros = !kept || (a.fresh && a.fresh[seg.seq] != 0);
         float S[N];
 #pragma unroll
-        for (int i = 0; i < N; ++i) S[i] = zeros ? 0.0f : (cut ? local : pool)[(long long)i * p.Dv];
+        for (int i = 0; i < N; ++i) S[i] = 0.0f;
+        if (STATES) {
+            // what the sequence starts from, before its last segment replaces it
+            if (mine && p.few && seg.seg == 0)
+#pragma unroll 4
+                for (int i = 0; i < N; ++i)
+                    local(start)[(long long)i * p.Dv] = zeros ? 0.0f : pool[(long long)i * p.Dv];
+        } else if (mine && (cut || !zeros)) {
+            const float *from = !cut ? pool : local(p.few ? start : seg.place);
+#pragma unroll
+            for (int i = 0; i < N; ++i) S[i] = from[(long long)i * p.Dv];
+            for (int j = cut && p.few ? seg.place - seg.seg : seg.place; j < seg.place; ++j) {
+                const float f = exp2_units(p.decay[(long long)j * a.Hv + h]);
+                const float *own = local(j);
+#pragma unroll
+                for (int i = 0; i < N; ++i) S[i] = __fmaf_rn(f, S[i], own[(long long)i * p.Dv]);
+            }
+        }
         long long G = 0;
         // the registers hold S / 2^exponent, the exponent kept while the column's largest magnitude stays within
         // 1 .. 2^15, set anew for 2^8 .. 2^9 when it leaves
@@ -659,7 +678,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         }
         if (mine && (STATES || (kept && seg.last))) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) (STATES ? local : pool)[(long long)i * p.Dv] = S[i] * pow2(exponent);
+            for (int i = 0; i < N; ++i) (STATES ? local(seg.place) : pool)[(long long)i * p.Dv] = S[i] * pow2(exponent);
         }
         if (STATES && any && tile == 0 && w == kWarpE && lane == 0) p.decay[(long long)seg.place * a.Hv + h] = G;
     }

@@ -255,15 +255,16 @@ def test_starts_outside_the_rows_are_cut_off():
     assert torch.equal(got, want) and torch.equal(pool, p2) and torch.equal(pool[3], before[3])
 
 
-def test_decreasing_starts_stay_inside():
+@pytest.mark.parametrize("Hv", [1, 48])
+def test_decreasing_starts_stay_inside(Hv):
     """Sequences that overlap are nobody's prompt; the call stays within its rows, states and workspace."""
     Dk, Dv, T, B = 64, 64, 1500, 9
-    q, k, v, g, pool = make(14, T, 1, 1, Dk, Dv, B + 1)
+    q, k, v, g, pool = make(14, T, 1, Hv, Dk, Dv, B + 1)
     kept = pool[B].clone()
     starts = torch.tensor([0, T, 0, T, 0, T, 0, T, 0, T], dtype=torch.int32, device="cuda")
-    need = zq.linear_attn_workspace_bytes(T, B, 1, Dk, Dv)
+    need = zq.linear_attn_workspace_bytes(T, B, Hv, Dk, Dv)
     room = torch.full((need + 4096,), 77, dtype=torch.uint8, device="cuda")
-    out = torch.full((T + 1, Dv), 5.0, device="cuda")
+    out = torch.full((T + 1, Hv * Dv), 5.0, device="cuda")
     zq.linear_attn(q, k, v, g, starts, zq.LinearState(pool), torch.arange(B, dtype=torch.int32, device="cuda"), out=out[:T],
                    workspace=room[:need])
     torch.cuda.synchronize()
@@ -288,6 +289,13 @@ def test_no_decay_and_one_row(Dk, Dv):
         step = zq.linear_attn_step(q[:1], k[:1], v[:1], None, zq.LinearState(before.clone()), slot)
         o, _, bo, _ = ref.recurrence(heads(q[:1], Dk), heads(k[:1], Dk), heads(v[:1], Dv), None, before[1], Dk ** -0.5)
         check(heads(step, Dv), o, bo[..., None], 2.0 ** -18, 2.0 ** -21, "step")
+
+
+@pytest.mark.parametrize("Hk,Hv,Dv", [(16, 48, 128), (2, 38, 64), (20, 40, 256)])
+def test_prompts_cut_into_few_segments(Hk, Hv, Dv):
+    """Two to four segments of a sequence, going on from their state or fresh, beside sequences that are not cut."""
+    prompts([2900, 40, 0, 700], Hk, Hv, 64, Dv, seed=Hv, fresh=[False, True, False, False])
+    prompts([600, 1800], Hk, Hv, 128, Dv, seed=Hv + 1, fresh=[True, False])
 
 
 def test_two_threads_with_streams_of_their_own():
