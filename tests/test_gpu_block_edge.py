@@ -128,6 +128,45 @@ def test_residual_norm(B, K, post, gate, act, scale):
     same_codes(q8, out)
 
 
+@pytest.mark.parametrize("B,K", [(2003, 5120), (1251, 8192), (9777, 1056), (312513, 32)])
+@pytest.mark.parametrize("post,gate,act", [(False, None, "linear"), (True, "rows", "silu"), (True, "row", "sigmoid")])
+def test_residual_norm_of_many_rows(B, K, post, gate, act):
+    """From ten million values on, CTAs take their rows in turn while the next ones are on their way."""
+    assert B * K >= 10 ** 7
+    x, y = randn(B, B, K), randn(K, B, K + 4)[:, 4:]
+    gamma, gamma_post = 0.5 + randn(1, K).abs(), 0.5 + randn(2, K).abs() if post else None
+    gt = {None: None, "rows": randn(3, B, K + 4)[:, :K], "row": randn(4, K)}[gate]
+    q8, out = zq.empty_q8_1(B, K), torch.empty(B, K, device="cuda")
+    got = zq.residual_norm_q8_1(x, y, gamma, EPS, gamma_post=gamma_post, gate=gt, act=act, scale=0.5, out=out, q8_out=q8)
+    u, want = edge_want(x, y, gamma, gamma_post, gt, act, 0.5)
+    tol = 2.0 ** -17 if post else 2.0 ** -20
+    assert bool(((got.double() - want).abs() <= tol * u.abs() + 2.0 ** -24 * want.abs()).all())
+    xh = ref.norm(got, gamma, EPS)
+    assert bool(((out.double() - xh).abs() <= 2.0 ** -17 * xh.abs()).all())
+    same = zq.rmsnorm_q8_1(got, gamma, EPS)
+    assert torch.equal(q8.qs, same.qs) and torch.equal(q8.d, same.d) and torch.equal(q8.s, same.s)
+    for into in (x, y):                                   # in place of either
+        before = into.clone()
+        again = zq.residual_norm_q8_1(x, y, gamma, EPS, gamma_post=gamma_post, gate=gt, act=act, scale=0.5, x_out=into)
+        assert again is into and torch.equal(into, got)
+        into.copy_(before)
+    assert zq.device_status() == 0
+
+
+@pytest.mark.parametrize("B,H,D", [(701, 48, 128), (20837, 3, 64), (1303, 13, 256)])
+def test_gated_norm_of_many_rows(B, H, D):
+    """From four million values on a warp has two groups of rows on their way when it packs codes."""
+    assert B * H * D >= 4 * 10 ** 6
+    x, gate, gamma = randn(B, B, H * D), randn(H, B, H * D + 4)[:, 4:], 0.5 + randn(D, D).abs()
+    q8 = zq.empty_q8_1(B, H * D)
+    out = zq.gated_norm_q8_1(x, gate, gamma, EPS, D, out=torch.empty_like(x), q8_out=q8)
+    want = ref.norm(x.reshape(B, H, D), gamma, EPS).reshape(B, H * D) * ref.act(gate, "silu")
+    assert bool(((out.double() - want).abs() <= 2.0 ** -17 * want.abs() + 1e-37).all())
+    same_codes(q8, out)
+    alone = zq.gated_norm_q8_1(x, gate, gamma, EPS, D)    # fp32 rows: one group a warp
+    assert torch.equal(alone, out)
+
+
 def test_residual_in_place_alone_and_without_norm():
     x, y, gamma = randn(1, 9, 640), randn(2, 9, 640), randn(3, 640)
     want = zq.residual_norm_q8_1(x, y, None, 0.0, scale=0.5)
