@@ -318,9 +318,8 @@ struct Rows {
     }
 };
 
-// The kernel on the 5th-generation tensor cores (linear_prompt_tc.cu), 128 columns
-// of a head a CTA: Dv a multiple of 128.  states: every segment's own state, but a
-// sequence's last one's.
+// The kernel on the 5th-generation tensor cores (linear_prompt_tc.cu).  states: every
+// segment's own state, but a sequence's last one's.
 cudaError_t launch_linear_prompt_tc(const PromptArgs &p, int Dk, bool states, cudaStream_t st);
 
 }  // namespace zq
