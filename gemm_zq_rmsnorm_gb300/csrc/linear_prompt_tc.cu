@@ -170,6 +170,25 @@ __device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, ui
     }
 }
 
+// Bits of the largest magnitudes of 32 values' rows of a chunk, by a warp.
+template <int DK, int DV>
+__device__ __forceinline__ void value_sizes(Smem<DK, DV> &sm, int c, int first)
+{
+#pragma unroll 1
+    for (int r = first; r < first + 32; r += 8) {
+        Rows<DV> v[4];
+        uint32_t m[8];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i].load_shared(sm.v[c & 1] + (r + 2 * i) * DV);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i].largest(m[2 * i], m[2 * i + 1]);
+        if ((threadIdx.x & 31) == 0) {
+            *reinterpret_cast<uint4 *>(&sm.mv[c & 1][r]) = make_uint4(m[0], m[1], m[2], m[3]);
+            *reinterpret_cast<uint4 *>(&sm.mv[c & 1][r + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
+        }
+    }
+}
+
 // Eight tokens' values of the lane's column, scaled, as parts to tensor memory.
 template <int DK, int DV>
 __device__ __forceinline__ void value_parts(const Smem<DK, DV> &sm, const typename Smem<DK, DV>::Chunk &f, const float *scale, int c,
@@ -220,7 +239,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sm.qk_full[i], LW);
             mbar_init(&sm.qk_empty[i], 1);
-            mbar_init(&sm.sizes[i], 4);
+            mbar_init(&sm.sizes[i], 2);
             mbar_init(&sm.w_full[i], 4 * QUARTERS);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sm.fact[i], 1);
@@ -395,7 +414,12 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             if (lane == 0) f.some_bad = some;
             arrive(sm.fact[c & 3]);
         };
-        for (int c = -1; c < chunks; ++c) {   // the factors are a chunk ahead
+        for (int c = -1; c < chunks; ++c) {   // the sizes and the factors are a chunk ahead
+            if (w && c + 1 < chunks) {
+                wait(sm.values[(c + 1) & 1], (c + 1) >> 1);
+                value_sizes(sm, c + 1, 32 * side);
+                arrive(sm.sizes[(c + 1) & 1]);
+            }
             if (!STATES && c >= 0) {
                 if (w) wait(sm.fact[c & 3], c >> 2);
                 if (c) wait(sm.o_full, c - 1);   // the last weights have been read
@@ -472,33 +496,12 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 __syncwarp();
             }
         };
-        // bits of the largest magnitudes of the values' rows, sixteen rows a warp
-        auto sizes = [&](int c) {
-            if (c >= chunks) return;
-            if (w == kWarpV) wait(sm.values[c & 1], c >> 1);
-            sync(kWarpV);
-#pragma unroll 1
-            for (int r = 16 * (w - kWarpV); r < 16 * (w - kWarpV) + 16; r += 8) {
-                Rows<DV> v[4];
-                uint32_t m[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i].load_shared(sm.v[c & 1] + (r + 2 * i) * DV);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) v[i].largest(m[2 * i], m[2 * i + 1]);
-                if (lane == 0) {
-                    *reinterpret_cast<uint4 *>(&sm.mv[c & 1][r]) = make_uint4(m[0], m[1], m[2], m[3]);
-                    *reinterpret_cast<uint4 *>(&sm.mv[c & 1][r + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
-                }
-            }
-            arrive(sm.sizes[c & 1]);
-        };
         request(0);
         request(1);
-        sizes(0);
         for (int c = 0; c < chunks; ++c) {
-            sizes(c + 1);
             if (!STATES) {
                 if (w == kWarpV) {
+                    wait(sm.values[c & 1], c >> 1);
                     wait(sm.fact[c & 3], c >> 2);
                     if (c) wait(sm.o_full, c - 1);   // the last chunk's MMAs have read what is written now
                 }
