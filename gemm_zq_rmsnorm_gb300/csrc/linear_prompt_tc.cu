@@ -492,6 +492,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                     tma_prefetch_2d(&map_k, hk * DK, seg.row0 + c * C);
                     mbar_arrive_expect_tx(&sm.values[c & 1], C * DV * 4);
                     tma_load_2d(sm.v[c & 1], &map_v, h * p.Dv + col0, seg.row0 + c * C, &sm.values[c & 1]);
+                    if (c + 1 < chunks) tma_prefetch_2d(&map_v, h * p.Dv + col0, seg.row0 + (c + 1) * C);
                 }
                 __syncwarp();
             }
