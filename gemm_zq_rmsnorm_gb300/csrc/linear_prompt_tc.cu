@@ -170,23 +170,29 @@ __device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, ui
     }
 }
 
-// Bits of the largest magnitudes of 32 values' rows of a chunk, by a warp.
+// the largest magnitude of three, NaN if one is
+__device__ __forceinline__ float largest3(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Bits of the largest magnitudes of 32 values' rows of a chunk, by a warp, a lane each
+// (every lane starts at another piece of its row, so that the lanes' banks differ).
 template <int DK, int DV>
 __device__ __forceinline__ void value_sizes(Smem<DK, DV> &sm, int c, int first)
 {
-#pragma unroll 1
-    for (int r = first; r < first + 32; r += 8) {
-        Rows<DV> v[4];
-        uint32_t m[8];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i].load_shared(sm.v[c & 1] + (r + 2 * i) * DV);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i].largest(m[2 * i], m[2 * i + 1]);
-        if ((threadIdx.x & 31) == 0) {
-            *reinterpret_cast<uint4 *>(&sm.mv[c & 1][r]) = make_uint4(m[0], m[1], m[2], m[3]);
-            *reinterpret_cast<uint4 *>(&sm.mv[c & 1][r + 4]) = make_uint4(m[4], m[5], m[6], m[7]);
-        }
+    const int lane = threadIdx.x & 31;
+    const float4 *row = reinterpret_cast<const float4 *>(sm.v[c & 1] + (first + lane) * DV);
+    float m[2] = {0.0f, 0.0f};
+#pragma unroll 8
+    for (int i = 0; i < DV / 4; ++i) {
+        const float4 x = row[(i + lane) & (DV / 4 - 1)];
+        m[0] = largest3(m[0], x.x, x.y);
+        m[1] = largest3(m[1], x.z, x.w);
     }
+    sm.mv[c & 1][first + lane] = __float_as_uint(largest3(m[0], m[1], 0.0f));
 }
 
 // Eight tokens' values of the lane's column, scaled, as parts to tensor memory.
