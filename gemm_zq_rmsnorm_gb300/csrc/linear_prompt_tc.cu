@@ -12,21 +12,22 @@
 // threads for a column), which add U to it, split it for the next chunk and put O1 and
 // O2 together.
 //
-// Warps: 0, 1 and 5 weigh scores, 0 makes the chunk's factors as well; 2 issues the
-// MMAs; 3, 4 and 6..11 convert queries and keys; 12..15 values for the output, a lane
-// for a column, and the sizes of their rows; 16..31 the state and the values weighted
-// for it.  Keys and queries are two stages deep; the key tile serves the scores as rows
-// and U as columns (the same bytes, a descriptor of the other order).  Every barrier is
-// one that its waiters cannot be two phases behind: where they could, there are two,
-// for even and odd chunks.
+// Warps: 0, 1 and 5 weigh scores, 0 makes the chunk's factors as well, 1 and 5 find the
+// sizes of the values' rows; 2 issues the MMAs; 3, 4 and 6..11 convert queries and keys;
+// 12..15 values for the output, a lane for a column; 16..31 the state and the values
+// weighted for it.  Keys and queries are two stages deep; the key tile serves the scores
+// as rows and U as columns (the same bytes, a descriptor of the other order).  Every
+// barrier is one that its waiters cannot be two phases behind: where they could, there
+// are two, for even and odd chunks.
 //
 // What bounds it is instructions and the steps that wait for one another, not memory:
-// a chunk of 128 x 128 takes about 7000 cycles (issue slots 60 % busy, tensor pipe 30 %,
-// HBM 34 %).  4096 tokens of 48 heads 134 us (floor by bytes 40, by products 42), 16384
-// of 8 heads 114, 24 prompts of up to 1500 tokens with 32 heads of 128 x 64 190, one of
-// 37 tokens 6.1.  All 512 columns of tensor memory are in use, so U and the scores share
-// theirs; mma.sync beside these MMAs slowed both (214 us), and values unrolled over a
-// whole chunk, or waits in every warp, lose to the instruction cache and the issue slots.
+// a chunk of 128 x 128 takes about 6700 cycles (issue slots 60 % busy, tensor pipe a
+// third, HBM as well).  4096 tokens of 48 heads 125.6 us (floor by bytes 40, by products
+// 42), 16384 of 8 heads 107, 24 prompts of up to 1500 tokens with 32 heads of 128 x 64
+// 182, one of 37 tokens 5.9.  All 512 columns of tensor memory are in use, so U and the
+// scores share theirs; mma.sync beside these MMAs slowed both (214 us), and values
+// unrolled over a whole chunk, or waits in every warp, lose to the instruction cache and
+// the issue slots.
 //
 // Every wait is bounded: after one has run out no MMA is issued any more, the
 // others return at once and the kernel ends (its results are invalid).
@@ -373,7 +374,8 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         // ------------------------------------------------------------ a chunk's factors (warp 0) and the scores' weights
         // warp 0 has the rows 0 .. 31 (32 columns), the others the rows 32 .. 63, half of the columns each
         const int quarter = w & 3, side = w == 5;
-        float next[2];   // decays of the next chunk
+        float next[2], g[2];   // decays of the chunk after the next and of the next
+        long long G[2];        // and their sums
         auto decays = [&](int c) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -382,12 +384,13 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             }
         };
         if (w == 0 && chunks) decays(0);
+        auto sums = [&](int c) {
+            g[0] = next[0], g[1] = next[1];
+            decays(c + 1);
+            sum_decays(g, G);
+        };
         auto factors = [&](int c) {
             const int st = c & 1, n = seg.row1 - seg.row0 - c * C;
-            const float g[2] = {next[0], next[1]};
-            decays(c + 1);
-            long long G[2];
-            sum_decays(g, G);
             wait(sm.qk_full[st], c >> 1);
             wait(sm.sizes[st], c >> 1);
             typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
@@ -426,6 +429,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 value_sizes(sm, c + 1, 32 * side);
                 arrive(sm.sizes[(c + 1) & 1]);
             }
+            if (w == 0 && c + 1 < chunks) sums(c + 1);   // (while the scores are on their way)
             if (!STATES && c >= 0) {
                 if (w) wait(sm.fact[c & 3], c >> 2);
                 if (c) wait(sm.o_full, c - 1);   // the last weights have been read
@@ -648,17 +652,16 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             tc_fence_before();
             arrive(sm.u_empty[STATES ? c & 1 : 0]);
             if (STATES) continue;
-            auto products = [&] {
-                if (w == kWarpE) wait(sm.o_full, c);
-            };
             if (c + 1 < chunks) {
                 weighted(c + 1);
-                publish(products);
-            } else {
-                products();
-                sync(kWarpE);
-                tc_fence_after();
+                // the queries' product with the last parts is done, and so is their place
+                publish([&] {
+                    if (w == kWarpE) wait(sm.qk_empty[c & 1], c >> 1);
+                });
             }
+            if (w == kWarpE) wait(sm.o_full, c);
+            sync(kWarpE);
+            tc_fence_after();
             const int n = seg.row1 - seg.row0 - c * C - 16 * part;
             char *out = reinterpret_cast<char *>(a.out + (seg.row0 + c * C + 16 * part) * a.out_stride + (long long)h * p.Dv +
                                                  col0 + column);
