@@ -298,6 +298,40 @@ def test_prompts_cut_into_few_segments(Hk, Hv, Dv):
     prompts([600, 1800], Hk, Hv, 128, Dv, seed=Hv + 1, fresh=[True, False])
 
 
+def test_few_segments_captured_and_replayed():
+    """One captured call whose sequences are cut into few segments serves other starts, slots and states."""
+    Dk, Dv, Hk, Hv, T, B = 64, 64, 2, 40, 700, 3
+    q, k, v, g, pool = make(40, T, Hk, Hv, Dk, Dv, B)
+    ints = [torch.tensor(x, dtype=torch.int32, device="cuda") for x in ([0, 500, 600, 700], [0, 1, 2], [0, 1, 0])]
+    ws = torch.empty(zq.linear_attn_workspace_bytes(T, B, Hv, Dk, Dv), dtype=torch.uint8, device="cuda")
+    state, out = zq.LinearState(pool), torch.empty(T, Hv * Dv, device="cuda")
+
+    def call():
+        zq.linear_attn(q, k, v, g, ints[0], state, ints[1], fresh=ints[2], out=out, workspace=ws)
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for starts, slots, fresh in (([0, 0, 700, 700], [1, 2, 0], [0, 0, 1]), ([0, 20, 300, 690], [2, 0, 1], [1, 0, 0])):
+        for t, x in zip(ints, (starts, slots, fresh)):
+            t.copy_(torch.tensor(x, dtype=torch.int32))
+        v.neg_()
+        before = pool.clone()
+        ws.fill_(255)                      # NaN wherever something would be read that was not written
+        graph.replay()
+        graph.replay()                     # goes on from the first one's states
+        torch.cuda.synchronize()
+        got, left = out.clone(), pool.clone()
+        pool.copy_(before)
+        call()
+        call()
+        torch.cuda.synchronize()
+        used = slice(starts[0], starts[-1])
+        assert torch.equal(got[used], out[used]) and torch.equal(left, pool)
+        assert torch.isfinite(got[used]).all() and torch.isfinite(left).all()
+
+
 def test_two_threads_with_streams_of_their_own():
     """The first calls of new threads, at the same time, each on its stream and with its own workspace."""
     cases = [make(16 + i, 700, 1, 3, 128, 128, 2) for i in range(2)]
