@@ -34,8 +34,8 @@ EXPORTS = ("zq_rmsnorm_q8_1", "zq_q4k_gemv", "zq_q4k_gemv_pair", "zq_q4k_gemm",
            "zq_debug_wait_expiry", "zq_q8_1_dequant_f16", "zq_f16_gemm_workspace_bytes", "zq_f16_gemm",
            "zq_rmsnorm_q4k_gemm", "zq_copy", "zq_rope_table", "zq_head_norm_rope",
            "zq_paged_attn_workspace_bytes", "zq_paged_attn", "zq_lora_workspace_bytes", "zq_lora",
-           "zq_linear_attn_step", "zq_linear_attn_workspace_bytes", "zq_linear_attn", "zq_gated_norm_q8_1",
-           "zq_residual_norm_q8_1")
+           "zq_linear_attn_step", "zq_linear_attn_workspace_bytes", "zq_linear_attn", "zq_debug_linear_segments",
+           "zq_gated_norm_q8_1", "zq_residual_norm_q8_1")
 
 
 class ZQError(RuntimeError):
@@ -115,6 +115,7 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "zq_linear_attn_step": ([P, ll, P, ll, P, ll, i, i, P, ll, P, P, f, P, ll, P], i),
         "zq_linear_attn_workspace_bytes": ([i, i, i, i, i], sz),
         "zq_linear_attn": ([P, ll, P, ll, P, ll, i, i, i, P, ll, P, P, P, P, f, P, ll, P, sz, P], i),
+        "zq_debug_linear_segments": ([P, i, i, i, i, P], i),
         "zq_gated_norm_q8_1": ([P, ll, i, i, i, P, f, P, ll, i, P, ll, P, P], i),
         "zq_residual_norm_q8_1": ([P, ll, P, ll, i, i, P, P, ll, i, f, P, ll, P, f, P, ll, P, P], i),
         "zq_rmsnorm_q4k_gemm": ([P, P, f, i, i, P, i, P, ctypes.POINTER(_Q8), P, sz, P], i),
@@ -771,6 +772,16 @@ def linear_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g, starts: to
     if status:
         _check(status)
     return out
+
+
+def debug_linear_segments(starts, T: int, Hv: int, Dv: int) -> dict:
+    """How linear_attn cuts its sequences into segments, for starts [B + 1] on
+    the host (see zq_debug_linear_segments): length, segments, and (first,
+    count) of every sequence."""
+    B = len(starts) - 1
+    out = (ctypes.c_int32 * (2 + 2 * B))()
+    _check(load().zq_debug_linear_segments((ctypes.c_int32 * (B + 1))(*starts), T, B, Hv, Dv, out))
+    return {"length": out[0], "segments": out[1], "of": [(out[2 + 2 * b], out[3 + 2 * b]) for b in range(B)]}
 
 
 _ACTS = {"linear": 0, "sigmoid": 1, "silu": 2}   # ZQ_GATE_LINEAR, ZQ_GATE_SIGMOID, ZQ_GATE_SILU

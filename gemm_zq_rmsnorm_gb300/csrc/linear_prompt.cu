@@ -57,7 +57,8 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
     }
     __syncthreads();
     const int base = base_s;
-    n = min(n, p.segments - base);   // starts that decrease could make more than there is room for
+    n = within_room(p, base, n);
+    if (n < 1) return;
     const long long size = (long long)p.Dv * Dk, at = 4 * (blockIdx.x * 256 + threadIdx.x);
     const int slot = a.slots[b];
     float4 first = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -93,6 +94,24 @@ cudaError_t launch_shape(const PromptArgs &p, int Dk, cudaStream_t st)
 size_t state_bytes(const Plan &plan, int Hv, int Dk, int Dv) { return (size_t)plan.segments * Hv * Dk * Dv * 4; }
 
 }  // namespace
+
+void linear_segments(const LinearAttnArgs &a, int Dv, int32_t *out)
+{
+    const Plan plan = plan_of(a.T, a.B, a.Hv, Dv);
+    PromptArgs p{};
+    p.a = a;
+    p.length = plan.length;
+    p.segments = plan.segments;
+    out[0] = plan.length;
+    out[1] = plan.segments;
+    int base = 0;
+    for (int b = 0; b < a.B; ++b) {
+        const int n = plan.length ? segments_of(p, b) : 1;
+        out[2 + 2 * b] = base;
+        out[3 + 2 * b] = within_room(p, base, n);
+        base += n;
+    }
+}
 
 size_t linear_attn_workspace(int T, int B, int Hv, int Dk, int Dv)
 {

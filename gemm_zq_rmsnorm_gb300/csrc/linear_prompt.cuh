@@ -44,16 +44,24 @@ struct PromptArgs {
 };
 
 // the rows of sequence b, within the call's rows whatever the starts say
-__device__ __forceinline__ void sequence_rows(const LinearAttnArgs &a, int b, int &r0, int &r1)
+__host__ __device__ __forceinline__ void sequence_rows(const LinearAttnArgs &a, int b, int &r0, int &r1)
 {
-    r0 = min(max(a.starts[b], 0), a.T);
-    r1 = min(max(a.starts[b + 1], r0), a.T);
+    const int s0 = a.starts[b] < 0 ? 0 : a.starts[b], s1 = a.starts[b + 1];
+    r0 = s0 < a.T ? s0 : a.T;
+    r1 = s1 < r0 ? r0 : s1 < a.T ? s1 : a.T;
 }
-__device__ __forceinline__ int segments_of(const PromptArgs &p, int b)
+__host__ __device__ __forceinline__ int segments_of(const PromptArgs &p, int b)
 {
     int r0, r1;
     sequence_rows(p.a, b, r0, r1);
-    return max(1, (r1 - r0 + p.length - 1) / p.length);
+    return r0 == r1 ? 1 : (r1 - r0 + p.length - 1) / p.length;
+}
+// How many of a sequence's n segments, the first of them number `base` of the call, there is room for: all of them, but
+// where starts decrease there may be more segments than states in the workspace.
+__host__ __device__ __forceinline__ int within_room(const PromptArgs &p, int base, int n)
+{
+    const int room = p.segments - base;
+    return room < 0 ? 0 : n < room ? n : room;
 }
 
 struct Segment {

@@ -1041,6 +1041,21 @@ int zq_linear_attn(const float *q, long long q_stride, const float *k, long long
     return launched(launch_linear_attn(a, state->Dk, state->Dv, workspace, (cudaStream_t)stream), name);
 }
 
+int zq_debug_linear_segments(const int32_t *starts, int T, int B, int Hv, int Dv, int32_t *out)
+{
+    static const char *name = "zq_debug_linear_segments";
+    if (!starts || !out) return fail(ZQ_ERR_ARG, "%s: null starts or out", name);
+    if (T < 1 || T > 1 << 24 || B < 1 || B > 65535 || Hv < 1 || Hv > 1024 || (Dv != 64 && Dv != 128 && Dv != 256))
+        return fail(ZQ_ERR_SHAPE, "%s: T = %d, B = %d, Hv = %d, Dv = %d out of range", name, T, B, Hv, Dv);
+    LinearAttnArgs a{};
+    a.T = T;
+    a.B = B;
+    a.Hv = Hv;
+    a.starts = starts;
+    linear_segments(a, Dv, out);
+    return ZQ_OK;
+}
+
 int zq_gated_norm_q8_1(const float *x, long long x_stride, int B, int H, int D, const float *gamma, float eps,
                        const float *gate, long long gate_stride, int act, float *out, long long out_stride,
                        const zq_q8_1 *q8_out, void *stream)

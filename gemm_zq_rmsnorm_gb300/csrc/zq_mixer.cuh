@@ -26,6 +26,8 @@ struct LinearAttnArgs {
 };
 cudaError_t launch_linear_attn_step(const LinearAttnArgs &a, int Dk, int Dv, cudaStream_t st);
 size_t linear_attn_workspace(int T, int B, int Hv, int Dk, int Dv);
+// the cut of a call into segments, for starts in host memory (zq_debug_linear_segments)
+void linear_segments(const LinearAttnArgs &a, int Dv, int32_t *out);
 cudaError_t launch_linear_attn(const LinearAttnArgs &a, int Dk, int Dv, void *workspace, cudaStream_t st);
 
 struct GatedNormArgs {

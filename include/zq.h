@@ -662,6 +662,15 @@ ZQ_API int zq_linear_attn(const float *q, long long q_stride, const float *k, lo
                           const int32_t *fresh, float scale, float *out, long long out_stride, void *workspace,
                           size_t workspace_bytes, void *stream);
 
+/*
+ * Test hook: how zq_linear_attn cuts a call's sequences into segments (host-side, no
+ * device needed), starts and out being host memory.  out[2 + 2 B] receives: tokens of
+ * a segment (0: sequences are not cut), segments that the workspace has room for, and
+ * for every sequence the number of its first segment and how many of its segments
+ * there is room for (all of them when the starts do not decrease).
+ */
+ZQ_API int zq_debug_linear_segments(const int32_t *starts, int T, int B, int Hv, int Dv, int32_t *out);
+
 /* What a gate's values pass through before they multiply: nothing, 1 / (1 +
  * exp(-g)), or g / (1 + exp(-g)); the sigmoid to about 2^-21 of itself, and zero
  * where it is below 2^-126. */
