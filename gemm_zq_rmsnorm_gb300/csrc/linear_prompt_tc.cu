@@ -574,10 +574,15 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         int exponent = 0;
         auto rescale = [&](int to) {
             to = max(-126, min(126, to));
-            const float s = pow2(max(-126, min(126, exponent - to)));
+            int by = exponent - to;
             exponent = to;
+            do {   // (once, unless it is more than 126)
+                const int step = max(-126, min(126, by));
+                const float s = pow2(step);
 #pragma unroll
-            for (int i = 0; i < N; ++i) S[i] *= s;
+                for (int i = 0; i < N; ++i) S[i] *= s;
+                by -= step;
+            } while (__any_sync(0xffffffffu, by != 0));
         };
         // the state's parts for the next product with the queries; between: what has to be over before they are written
         auto publish = [&](auto between) {
@@ -629,9 +634,10 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             const float xs = pow2(exponent);   // of the state that O1 was made with
             const float keep = f.keep;
             float add = f.add * pow2(-exponent);
-            // what is added is far above the state: by its size, before it overflows
+            // What is added is far above the state: the exponent goes as far as the sums need, and no farther, since a
+            // column of values that are zero keeps its state.
             if (__any_sync(0xffffffffu, !(add < 0x1p40f))) {
-                rescale(max(exponent, row_exponent(magnitude(f.add))));
+                rescale(max(exponent, row_exponent(magnitude(f.add)) - 56));
                 add = f.add * pow2(-exponent);
             }
 #pragma unroll
