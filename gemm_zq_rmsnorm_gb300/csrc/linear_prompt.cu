@@ -70,9 +70,9 @@ __global__ void __launch_bounds__(256) linear_join_kernel(const __grid_constant_
         const float4 next = i + 2 < n ? *own(i + 1) : make_float4(0.0f, 0.0f, 0.0f, 0.0f);   // the last has none
         *own(i) = first;
         if (i + 1 < n) {
-            const float f = exp2_units(p.decay[(long long)(base + i) * a.Hv + h]);
-            first = make_float4(__fmaf_rn(f, first.x, mine.x), __fmaf_rn(f, first.y, mine.y),
-                                __fmaf_rn(f, first.z, mine.z), __fmaf_rn(f, first.w, mine.w));
+            const long long f = p.decay[(long long)(base + i) * a.Hv + h];
+            first = make_float4(decayed(first.x, f, mine.x), decayed(first.y, f, mine.y), decayed(first.z, f, mine.z),
+                                decayed(first.w, f, mine.w));
             mine = next;
         }
     }

@@ -167,38 +167,73 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 // ---------------------------------------------------------------- a chunk's factors
 // G in units of 2^-32: a whole part in the high word, a broken one in the low word
 constexpr int kNothing = -(1 << 20);           // whole part of u of a row of zeros
+constexpr int kReach = 40;                     // the sums of a chunk reach at most this far above a state's exponent
 
-struct Factors {
+struct alignas(16) Factors {                   // (arrays of tokens are read four values at a time)
     float uh[kChunk], ul[kChunk], m[kChunk];   // u, whole and broken part; M
-    float f1[kChunk], f2[kChunk], w[kChunk];   // the rows' factors, the tokens' weights in the state
-    float keep, add;                           // what the state, and what the chunk's sums are multiplied by
+    int gw[kChunk];                            // G, whole and broken part
+    float gb[kChunk];
+    float f1[kChunk], f2[kChunk];              // the rows' factors
+    float part[kChunk];                        // the rows' factors where fp32 does not hold them: f2 = part 2^n,
+    int n[kChunk];                             // f1 = part 2^(n + M)
+    int wide;                                  // a row needs these (make_factors)
+    // OUT: what a state in registers is multiplied by, when its exponent is low .. low + range; the sums' factor is then
+    // gpart 2^(low + kReach - exponent)
+    struct alignas(16) Update {
+        float keep, gpart;
+        int low;
+        unsigned range;
+    } update;
+    int grow, reach;                           // keep is gpart 2^grow, the sums' factor gpart 2^reach
+    float keep, add;                           // !OUT: what the state, and what the chunk's sums are multiplied by
+    long long scale;                           // !OUT: the power of two (in units) that the state counts in
     long long G;
 };
+
+// values of two neighbouring tokens
+template <typename T>
+__device__ __forceinline__ void store2(T *p, T a, T b)
+{
+    struct alignas(8) Two { T a, b; };
+    *reinterpret_cast<Two *>(p) = {a, b};
+}
 
 __device__ __forceinline__ int whole(long long x) { return (int)(x >> 32); }
 __device__ __forceinline__ float broken(long long x) { return (float)(uint32_t)x * 0x1p-32f; }
 
-// 2^(n + part), the part's power to 2^-22; 0 below the normal numbers
-__device__ __forceinline__ float exp2_parts(int n, float part)
+// x 2^n; 0 below the normal numbers' powers
+__device__ __forceinline__ float times_pow2(float x, int n)
 {
-    const float x = exp2_fast(part) * pow2(max(-126, min(127, n)));
-    return n < -126 ? 0.0f : n > 127 ? __int_as_float(0x7f800000) : x;
+    const float y = x * pow2(max(-126, min(127, n)));
+    return n < -126 ? 0.0f : n > 127 ? y * pow2(min(127, n - 127)) : y;
 }
+// 2^(n + part), the part's power to 2^-22
+__device__ __forceinline__ float exp2_parts(int n, float part) { return times_pow2(exp2_fast(part), n); }
 __device__ __forceinline__ float exp2_units(long long x) { return exp2_parts(whole(x), broken(x)); }
+
+// x 2^units + y, for powers of any size: a large x stays a number below them
+__device__ __forceinline__ float decayed(float x, long long units, float y)
+{
+    const int n = whole(units);
+    const float part = exp2_fast(broken(units));
+    return n >= -126 && n < 127 ? __fmaf_rn(part * pow2(n), x, y) : ldexpf(x, n) * part + y;
+}
 
 // x log2 e in units, to 2^-33 of itself and half a unit: the significand times 2^32 log2 e, shifted
 __device__ __forceinline__ long long log2_units(float x)
 {
-    // beyond +-200 the power is 0 or infinity; NaN is marked elsewhere
-    x = fminf(fmaxf(x, -200.0f), 200.0f);
+    // e^-600 empties any state for any query, and the other end is infinity; NaN is marked elsewhere
+    x = fminf(fmaxf(x, -600.0f), 600.0f);
     const uint32_t bits = __float_as_uint(x) & 0x7fffffffu;
-    const int shift = min(63, 150 - (int)(bits >> 23));   // 23 - e, at least 16
+    const int shift = min(63, 150 - (int)(bits >> 23));   // 23 - e, at least 14
     const uint64_t product = (uint64_t)((bits & 0x7fffffu) | 0x800000u) * 6196328019ull;
     const long long r = (long long)((product + (1ull << (shift - 1))) >> shift);
     return x < 0.0f ? -r : r;
 }
 
 __device__ __forceinline__ long long clamp_units(long long G) { return min(max(G, -(1LL << 44)), 1LL << 44); }
+// the least power that a state counts in (its values are zero)
+constexpr long long kNoScale = -(1LL << 53);
 
 // G of a chunk's tokens from their decays, by one warp with two tokens a lane.
 __device__ __forceinline__ void sum_decays(const float (&g)[2], long long (&G)[2])
@@ -215,12 +250,14 @@ __device__ __forceinline__ void sum_decays(const float (&g)[2], long long (&G)[2
     G[1] = sum;
 }
 
-// The factors of a chunk's rows, by the same warp: from G, the exponents of key and
-// value together (INT_MIN: one of them is zero) and of the query.  M need only be near
-// the largest u: it is the whole number above it.  OUT: with those of the output.
+// What a chunk's weights are made of, by the same warp: from G and the exponents of key and
+// value together (INT_MIN: one of them is zero).  M need only be near the largest u: it is
+// the whole number above it.  w: the tokens' weights in the state.  OUT: with M of every row.  !OUT: the state counts in
+// 2^counts, which follows its decays and the chunk's sums, whichever is larger, so that no
+// decay of many chunks empties the registers; one of its two factors is 1.
 template <bool OUT>
-__device__ __forceinline__ void make_factors(Factors &s, const long long (&G)[2], const int (&ekv)[2], const int (&eq)[2],
-                                             float scale)
+__device__ __forceinline__ void make_weights(Factors &s, const long long (&G)[2], const int (&ekv)[2], float (&w)[2],
+                                             long long &counts)
 {
     const int lane = threadIdx.x & 31;
     int uw[2], M[2];
@@ -244,25 +281,67 @@ __device__ __forceinline__ void make_factors(Factors &s, const long long (&G)[2]
     } else {
         last = __reduce_max_sync(0xffffffffu, top) + 1;
     }
+    if (OUT) {
+        store2(s.uh + 2 * lane, (float)uw[0], (float)uw[1]);
+        store2(s.ul + 2 * lane, ub[0], ub[1]);
+        store2(s.m + 2 * lane, (float)M[0], (float)M[1]);
+        store2(s.gw + 2 * lane, whole(G[0]), whole(G[1]));
+        store2(s.gb + 2 * lane, broken(G[0]), broken(G[1]));
+    }
+    w[0] = exp2_parts(uw[0] - last, ub[0]);
+    w[1] = exp2_parts(uw[1] - last, ub[1]);
+    if (lane == 31) {
+        if (OUT) {
+            // The state stays in its scale unless the sums are far above it, or far below (2^-80: a state of zeros), or the
+            // decay would empty the registers although the state still counts beside the sums (2^-60).
+            const int grow = whole(G[1]), reach = grow + last;
+            s.update = {exp2_units(G[1]), exp2_fast(broken(G[1])), grow > 90 ? INT_MAX / 2 : reach - kReach,
+                        (unsigned)(grow < -90 ? min(120, max(0, kReach - 60 - grow)) : 120)};
+            s.grow = grow;
+            s.reach = reach;
+        } else {
+            const long long state = max(counts + G[1], kNoScale), sums = G[1] + ((long long)last << 32);
+            counts = max(state, sums);
+            s.keep = exp2_units(state - counts);
+            s.add = exp2_units(sums - counts);
+            s.scale = counts;
+        }
+        s.G = G[1];
+    }
+}
+
+// The factors of a chunk's rows of the output, by another warp, from what those have left
+// and the largest magnitudes of the queries; the call's scale is scale 2^scale_exponent.
+//
+// wide: a row's factors are not all numbers that fp32 holds, although what they belong to
+// may be (a query of 2^100 for tokens of 2^-110; a large state after decays of 2^-150): a
+// power above 2^100, f1 below the normal numbers, or f2 below them where its term still
+// counts.  That term is at most 2^(37 + n) for a state whose exponent is not above 0, and
+// counts from 2^-149 and from 2^-40 of the row's own tokens on.
+__device__ __forceinline__ void make_factors(Factors &s, const uint32_t *mq, float scale, int scale_exponent)
+{
+    const int lane = threadIdx.x & 31;
+    bool wide = false;
+    float part[2], f1[2], f2[2];
+    int n[2];
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
         const int t = 2 * lane + i;
-        if (OUT) {
-            s.uh[t] = (float)uw[i];
-            s.ul[t] = ub[i];
-            s.m[t] = (float)M[i];
-            const int n = whole(G[i]) + eq[i];
-            const float part = broken(G[i]);
-            s.f1[t] = scale * exp2_parts(n + M[i], part);
-            s.f2[t] = scale * exp2_parts(n, part);
-        }
-        s.w[t] = exp2_parts(uw[i] - last, ub[i]);
+        // (zeros need no factor)
+        n[i] = s.gw[t] + scale_exponent + (mq[t] ? row_exponent(mq[t]) : 0);
+        const int x = n[i] + (int)s.m[t];
+        part[i] = scale * exp2_fast(s.gb[t]);
+        // (pow2(-127) is 0)
+        f1[i] = part[i] * pow2(max(-127, min(127, x)));
+        f2[i] = part[i] * pow2(max(-127, min(127, n[i])));
+        wide |= max(n[i], x) > 100 || (x < -126 && x > -300) || (n[i] < -126 && n[i] + 37 >= max(-149, x - 40));
     }
-    if (lane == 31) {
-        s.keep = exp2_units(G[1]);
-        s.add = exp2_parts(whole(G[1]) + last, broken(G[1]));
-        s.G = G[1];
-    }
+    store2(s.f1 + 2 * lane, f1[0], f1[1]);
+    store2(s.f2 + 2 * lane, f2[0], f2[1]);
+    store2(s.part + 2 * lane, part[0], part[1]);
+    store2(s.n + 2 * lane, n[0], n[1]);
+    wide = __any_sync(0xffffffffu, wide);
+    if (lane == 0) s.wide = wide;
 }
 
 // Two neighbouring rows of one operand: a lane has four values of each when a row

@@ -48,6 +48,7 @@ constexpr int kThreads = kWarps * 32;
 // tensor memory columns
 constexpr int kO1 = 0, kO2 = 64, kU = 128, kSh = 256, kSl = 320, kVh = 384, kVl = 416, kWh = 448, kWl = 480;
 constexpr int kU2 = 0;   // a second U where there is no output
+constexpr int kEmpty = -1000;  // exponent of a column of the state that is zero
 static_assert(kVl - kVh == kWl - kWh, "low parts behind high ones");
 
 template <int DK, int DV>
@@ -56,7 +57,7 @@ struct Smem {
     __half p[2][C * C];                        // [part], rows of 64 tokens
     float v[2][C * DV];                        // [chunk's parity]: values as they come
     struct alignas(16) Chunk : Factors {       // read four values at a time
-        float vscale[C], wscale[C];            // 2^-e of the values' rows, and that times w
+        alignas(16) float vscale[C], wscale[C];   // 2^-e of the values' rows, and that times w
         int some_bad;
     } f[4];
     alignas(16) uint32_t mq[2][C], mk[2][C], mv[2][C];   // bits of the rows' largest magnitudes
@@ -79,6 +80,13 @@ __device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t (&r)[8])
 {
     asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(taddr));
+}
+
+__device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4])
+{
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(taddr));
 }
 
@@ -216,6 +224,34 @@ __device__ __forceinline__ void value_parts(const Smem<DK, DV> &sm, const typena
     }
     tmem_st4(to, ph);
     tmem_st4(to + (kVl - kVh), pl);
+}
+
+// Sixteen rows of the output where fp32 does not hold the rows' factors or their
+// products with the state's exponent, while the output itself may be a number like any
+// other (a state of 2^100 after decays of 2^-150; a query of 2^-100 for a state of 2^120).
+// Both of a row's terms count from the larger one, and the power of two comes last.
+// Where the factors are numbers the result is the same, bit for bit.
+//
+// A chunk needs it when its factors say so (`wide`), a warp when its state's exponent is
+// above 0.
+__device__ __noinline__ void far_outputs(const Factors &f, int first, uint32_t o1_at, uint32_t o2_at, char *out, int os, int n,
+                                         int exponent)
+{
+#pragma unroll 1
+    for (int b = 0; b < 16; b += 4) {
+        uint32_t o1[4], o2[4];
+        tmem_ld4(o1_at + b, o1);
+        tmem_ld4(o2_at + b, o2);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int t = first + b + i, x = f.n[t] + (int)f.m[t], e = f.n[t] + exponent;
+            const float part = f.part[t], state = __uint_as_float(o1[i]);
+            const int base = state == 0.0f ? x : max(x, e);
+            const float y = __fmaf_rn(times_pow2(part, x - base), __uint_as_float(o2[i]), times_pow2(part * state, min(0, e - base)));
+            if (b + i < n) *reinterpret_cast<float *>(out + (long long)(b + i) * os) = ldexpf(y, base);
+        }
+    }
 }
 
 template <int DK, int DV, bool STATES>
@@ -376,6 +412,9 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         const int quarter = w & 3, side = w == 5;
         float next[2], g[2];   // decays of the chunk after the next and of the next
         long long G[2];        // and their sums
+        long long counts = kNoScale;
+        int scale_exponent;
+        const float scale = frexpf(a.scale, &scale_exponent);
         auto decays = [&](int c) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -394,31 +433,34 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             wait(sm.qk_full[st], c >> 1);
             wait(sm.sizes[st], c >> 1);
             typename Smem<DK, DV>::Chunk &f = sm.f[c & 3];
-            int ekv[2], eq[2], ev[2];
+            int ekv[2], ev[2];
+            float weight[2];
             bool bad[2], odd[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int s = 2 * lane + i;
                 const uint32_t mk = sm.mk[st][s], mv = sm.mv[st][s];
                 ev[i] = row_exponent(mv);
-                // a token whose value or decay is not finite: its weights become NaN, and so its own row, all
-                // later ones and the state; the value itself must not meet the zero weights of earlier rows.  (One
-                // of the key does the same by the key's parts.)
-                bad[i] = s < n && (mv >= 0x7f800000u || g[i] != g[i]);
+                // a token whose value is not finite, or whose decay is none or infinity: its weights become NaN, and so
+                // its own row, all later ones and the state; the value itself must not meet the zero weights of earlier
+                // rows.  (One of the key does the same by the key's parts.)
+                bad[i] = s < n && (mv >= 0x7f800000u || !(g[i] < __int_as_float(0x7f800000)));
                 odd[i] = mv >= 0x7f800000u || bad[i];   // (the rows behind the last are somebody else's)
                 ekv[i] = !bad[i] && (s >= n || mk == 0u || mv == 0u) ? INT_MIN : ev[i] + row_exponent(mk);
-                eq[i] = STATES ? 0 : row_exponent(sm.mq[st][s]);
             }
-            make_factors<!STATES>(f, G, ekv, eq, a.scale);
+            make_weights<!STATES>(f, G, ekv, weight, counts);
             const float nan = __int_as_float(0x7fc00000);
+            float vscale[2], wscale[2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int s = 2 * lane + i;
                 const float x = pow2(-ev[i]);
                 if (bad[i]) f.uh[s] = nan;
-                f.vscale[s] = bad[i] || s >= n ? 0.0f : x;
-                f.wscale[s] = s >= n ? 0.0f : bad[i] ? nan : f.w[s] * x;
+                vscale[i] = bad[i] || s >= n ? 0.0f : x;
+                wscale[i] = s >= n ? 0.0f : bad[i] ? nan : weight[i] * x;
             }
+            store2(f.vscale + 2 * lane, vscale[0], vscale[1]);
+            store2(f.wscale + 2 * lane, wscale[0], wscale[1]);
             const int some = __any_sync(0xffffffffu, odd[0] || odd[1]);
             if (lane == 0) f.some_bad = some;
             arrive(sm.fact[c & 3]);
@@ -432,6 +474,8 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             if (w == 0 && c + 1 < chunks) sums(c + 1);   // (while the scores are on their way)
             if (!STATES && c >= 0) {
                 if (w) wait(sm.fact[c & 3], c >> 2);
+                // (what the output alone needs: its warps come to it by way of p_full)
+                if (w == 1) make_factors(sm.f[c & 3], sm.mq[c & 1], scale, scale_exponent);
                 if (c) wait(sm.o_full, c - 1);   // the last weights have been read
                 wait(sm.scores, c);
                 tc_fence_after();
@@ -551,6 +595,15 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         float S[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) S[i] = 0.0f;
+        // The registers hold S / 2^exponent, the exponent kept while the column's largest magnitude stays within
+        // 1 .. 2^15, set anew for 2^8 .. 2^9 when it leaves.  (STATES: all of them count in the factors' `scale`.)
+        int exponent = 0;
+        // 2^units of a head's decays as two factors, since a large state may stay a number below what fp32 holds of it
+        auto factors_of = [](long long units, float &rest) {
+            const int n = whole(units), first = max(-126, min(126, n));
+            rest = n < -252 ? 0.0f : pow2(min(126, n - first));
+            return exp2_fast(broken(units)) * pow2(first);
+        };
         if (STATES) {
             // what the sequence starts from, before its last segment replaces it
             if (mine && p.few && seg.seg == 0)
@@ -562,28 +615,18 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
 #pragma unroll
             for (int i = 0; i < N; ++i) S[i] = from[(long long)i * p.Dv];
             for (int j = cut && p.few ? seg.place - seg.seg : seg.place; j < seg.place; ++j) {
-                const float f = exp2_units(p.decay[(long long)j * a.Hv + h]);
+                float rest;
+                const float f = factors_of(p.decay[(long long)j * a.Hv + h], rest);
                 const float *own = local(j);
+                if (rest != 1.0f)
+#pragma unroll
+                    for (int i = 0; i < N; ++i) S[i] *= rest;
 #pragma unroll
                 for (int i = 0; i < N; ++i) S[i] = __fmaf_rn(f, S[i], own[(long long)i * p.Dv]);
             }
         }
         long long G = 0;
-        // the registers hold S / 2^exponent, the exponent kept while the column's largest magnitude stays within
-        // 1 .. 2^15, set anew for 2^8 .. 2^9 when it leaves
-        int exponent = 0;
-        auto rescale = [&](int to) {
-            to = max(-126, min(126, to));
-            int by = exponent - to;
-            exponent = to;
-            do {   // (once, unless it is more than 126)
-                const int step = max(-126, min(126, by));
-                const float s = pow2(step);
-#pragma unroll
-                for (int i = 0; i < N; ++i) S[i] *= s;
-                by -= step;
-            } while (__any_sync(0xffffffffu, by != 0));
-        };
+        auto limit = [](int to) { return max(-126, min(126, to)); };
         // the state's parts for the next product with the queries; between: what has to be over before they are written
         auto publish = [&](auto between) {
             float most = 0.0f;
@@ -594,8 +637,13 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             sync(kWarpE);
             tc_fence_after();
             const uint32_t m = max(max(sm.smax[0][column], sm.smax[1][column]), max(sm.smax[2][column], sm.smax[3][column]));
-            if (__any_sync(0xffffffffu, m < 0x3f800000u || m >= 0x47000000u))
-                rescale(m == 0u ? 0 : exponent + row_exponent(m) - 8);
+            if (__any_sync(0xffffffffu, m < 0x3f800000u || m >= 0x47000000u)) {
+                const int to = max(exponent - 126, limit(exponent + row_exponent(m) - 8));
+                const float s = pow2(m == 0u ? 0 : exponent - to);
+#pragma unroll
+                for (int i = 0; i < N; ++i) S[i] *= s;
+                exponent = m == 0u ? kEmpty : to;
+            }
 #pragma unroll
             for (int b = 0; b < N / 16; ++b) {
                 uint32_t ph[8], pl[8];
@@ -631,14 +679,25 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             sync(kWarpE);   // (the maxima of the last chunk have been read, too)
             tc_fence_after();
             if (STATES && c + 1 < chunks) weighted(c + 1);
-            const float xs = pow2(exponent);   // of the state that O1 was made with
-            const float keep = f.keep;
-            float add = f.add * pow2(-exponent);
-            // What is added is far above the state: the exponent goes as far as the sums need, and no farther, since a
-            // column of values that are zero keeps its state.
-            if (__any_sync(0xffffffffu, !(add < 0x1p40f))) {
-                rescale(max(exponent, row_exponent(magnitude(f.add)) - 56));
-                add = f.add * pow2(-exponent);
+            const int was = exponent;              // of the state that O1 was made with
+            float keep, add;
+            if (STATES) {
+                keep = f.keep;
+                add = f.add;
+            } else {
+                const Factors::Update update = f.update;
+                keep = update.keep;
+                int n = update.low - exponent;
+                // Out of its scale the state's exponent goes with the decay, or as far as the sums need.  No farther, since a
+                // column of values that are zero keeps its state (as far as 2^-210 of the sums).
+                if (__any_sync(0xffffffffu, (unsigned)-n > update.range)) {
+                    const bool empty = exponent == kEmpty;
+                    const int grow = f.grow, reach = f.reach, from = exponent + grow;
+                    exponent = limit(empty ? reach - 8 : max(from, reach - 84));
+                    n = max(-127, min(127, reach - exponent)) - kReach;
+                    keep = empty ? 0.0f : times_pow2(update.gpart, from - exponent);
+                }
+                add = update.gpart * pow2(n + kReach);           // (pow2(-127) is 0)
             }
 #pragma unroll
             for (int b = 0; b < N / 16; ++b) {
@@ -672,8 +731,11 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             char *out = reinterpret_cast<char *>(a.out + (seg.row0 + c * C + 16 * part) * a.out_stride + (long long)h * p.Dv +
                                                  col0 + column);
             const int os = 4 * (int)a.out_stride;
+            const bool far = __any_sync(0xffffffffu, f.wide || was > 0);
+            const float xs = pow2(max(-127, was));
+            if (far) far_outputs(f, 16 * part, lanes + kO1 + 16 * part, lanes + kO2 + 16 * part, out, os, n, was);
 #pragma unroll 1
-            for (int b = 0; b < 2; ++b) {
+            for (int b = far ? 2 : 0; b < 2; ++b) {
                 uint32_t o1[8], o2[8];
                 tmem_ld8(lanes + kO1 + 16 * part + 8 * b, o1);
                 tmem_ld8(lanes + kO2 + 16 * part + 8 * b, o2);
@@ -706,8 +768,10 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             arrive(sm.o_empty);
         }
         if (mine && (STATES || (kept && seg.last))) {
+            float rest = 1.0f;
+            const float f = STATES ? factors_of(sm.f[(chunks - 1) & 3].scale, rest) : pow2(max(-127, exponent));
 #pragma unroll
-            for (int i = 0; i < N; ++i) (STATES ? local(seg.place) : pool)[(long long)i * p.Dv] = S[i] * pow2(exponent);
+            for (int i = 0; i < N; ++i) (STATES ? local(seg.place) : pool)[(long long)i * p.Dv] = S[i] * f * rest;
         }
         if (STATES && any && tile == 0 && w == kWarpE && lane == 0) p.decay[(long long)seg.place * a.Hv + h] = G;
     }
