@@ -7,15 +7,17 @@
 //   o_t = scale (exp(G_t) S^T q_t + sum_{s <= t} exp(G_t - G_s) (q_t . k_s) v_s),
 //   S'  = exp(G_C) S + sum_s exp(G_C - G_s) k_s v_s^T.
 //
-// Every product is as exact as an fp32 one: a row x is taken as 2^e (hi + lo), two
-// binary16 parts of the row scaled to [1, 2), and a product is hi hi + hi lo + lo
-// hi (2^-22 of what bounds it; sums fp32, a chunk's sums added to the state outside
-// the tensor core, whose accumulator truncates).  Weights exp(G_t - G_s) and the
-// rows' powers of two meet in the exponent: with u_s = e_k + e_v - G_s (G in base
-// two) and M_t the whole number above the largest u of s <= t, the weight in the
-// product is 2^(u_s - M_t) <= 1 and 2^(M_t + G_t) goes to the row, so that a token
-// counts exactly where no larger one of its past drowns it, and the future does not
-// matter at all.  G is a sum in units of 2^-32.
+// Every product is taken of two binary16 parts of each factor: a row x is 2^e (hi + lo),
+// the parts being those of the row scaled to [2^14, 2^15), so that each value keeps 22 bits
+// of its own unless it is 2^25 below the row's largest; a product is hi hi + hi lo + lo hi
+// (2^-22 of itself; sums fp32, a chunk's sums added to the state outside the tensor core,
+// whose accumulator truncates).  (Scaled to [1, 2), the low parts end at 2^-25 of the row's
+// largest value: a channel 1000 times the others, which the other factor lacks, cost 8.7e-6
+// of a score's root mean square.)  Weights exp(G_t - G_s) and the rows' powers of two meet
+// in the exponent: with u_s = e_k + e_v - G_s (G in base two) and M_t the whole number above
+// the largest u of s <= t, the weight in the product is 2^(u_s - M_t) <= 1 and 2^(M_t + G_t)
+// goes to the row, so that a token counts exactly where no larger one of its past drowns
+// it, and the future does not matter at all.  G is a sum in units of 2^-32.
 #pragma once
 
 #include <limits.h>
@@ -154,12 +156,10 @@ __device__ __forceinline__ float exp2_fast(float x)
     return e;
 }
 
-// exponent of a row's largest magnitude (its bits), such that the row over 2^e lies below 4
-__device__ __forceinline__ int row_exponent(uint32_t bits)
-{
-    const int e = (int)(bits >> 23) - 127;
-    return e < -126 ? -126 : e > 126 ? 126 : e;
-}
+// exponent of a magnitude (its bits)
+__device__ __forceinline__ int exponent_of(uint32_t bits) { return (int)(bits >> 23) - 127; }
+// that of a row, from its largest magnitude: the row over 2^e lies below 2^15
+__device__ __forceinline__ int row_exponent(uint32_t bits) { return max(exponent_of(bits) - 14, -126); }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((127 + e) << 23); }   // -126 <= e <= 127
 
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7fffffffu; }
@@ -167,6 +167,9 @@ __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(
 // ---------------------------------------------------------------- a chunk's factors
 // G in units of 2^-32: a whole part in the high word, a broken one in the low word
 constexpr int kNothing = -(1 << 20);           // whole part of u of a row of zeros
+// Scores are below 2^37 and lose this many powers of two before they are parts below 2^15.  (By a product of their
+// own: in the weights' exponent, whose sum is an fp32 number, they would cost it bits.)
+constexpr int kRoom = 22;
 constexpr int kReach = 40;                     // the sums of a chunk reach at most this far above a state's exponent
 
 struct alignas(16) Factors {                   // (arrays of tokens are read four values at a time)
@@ -175,7 +178,7 @@ struct alignas(16) Factors {                   // (arrays of tokens are read fou
     float gb[kChunk];
     float f1[kChunk], f2[kChunk];              // the rows' factors
     float part[kChunk];                        // the rows' factors where fp32 does not hold them: f2 = part 2^n,
-    int n[kChunk];                             // f1 = part 2^(n + M)
+    int n[kChunk];                             // f1 = part 2^(n + M + kRoom)
     int wide;                                  // a row needs these (make_factors)
     // OUT: what a state in registers is multiplied by, when its exponent is low .. low + range; the sums' factor is then
     // gpart 2^(low + kReach - exponent)
@@ -292,11 +295,11 @@ __device__ __forceinline__ void make_weights(Factors &s, const long long (&G)[2]
     w[1] = exp2_parts(uw[1] - last, ub[1]);
     if (lane == 31) {
         if (OUT) {
-            // The state stays in its scale unless the sums are far above it, or far below (2^-80: a state of zeros), or the
-            // decay would empty the registers although the state still counts beside the sums (2^-60).
+            // The state stays in its scale unless the sums are far above it, or far below (a state of zeros), or the decay
+            // would empty the registers although the state (2^8 and more there) still counts beside the sums (near 2^28).
             const int grow = whole(G[1]), reach = grow + last;
             s.update = {exp2_units(G[1]), exp2_fast(broken(G[1])), grow > 90 ? INT_MAX / 2 : reach - kReach,
-                        (unsigned)(grow < -90 ? min(120, max(0, kReach - 60 - grow)) : 120)};
+                        (unsigned)(grow < -90 ? min(150, -grow) : 150)};
             s.grow = grow;
             s.reach = reach;
         } else {
@@ -316,8 +319,8 @@ __device__ __forceinline__ void make_weights(Factors &s, const long long (&G)[2]
 // wide: a row's factors are not all numbers that fp32 holds, although what they belong to
 // may be (a query of 2^100 for tokens of 2^-110; a large state after decays of 2^-150): a
 // power above 2^100, f1 below the normal numbers, or f2 below them where its term still
-// counts.  That term is at most 2^(37 + n) for a state whose exponent is not above 0, and
-// counts from 2^-149 and from 2^-40 of the row's own tokens on.
+// counts.  That term is at most 2^(57 + n) for a state whose exponent is at most 20, and
+// counts from 2^-149 and from 2^-40 of the row's own tokens (near 2^(20 + x), x the power of f1) on.
 __device__ __forceinline__ void make_factors(Factors &s, const uint32_t *mq, float scale, int scale_exponent)
 {
     const int lane = threadIdx.x & 31;
@@ -329,12 +332,12 @@ __device__ __forceinline__ void make_factors(Factors &s, const uint32_t *mq, flo
         const int t = 2 * lane + i;
         // (zeros need no factor)
         n[i] = s.gw[t] + scale_exponent + (mq[t] ? row_exponent(mq[t]) : 0);
-        const int x = n[i] + (int)s.m[t];
+        const int x = n[i] + (int)s.m[t] + kRoom;
         part[i] = scale * exp2_fast(s.gb[t]);
         // (pow2(-127) is 0)
         f1[i] = part[i] * pow2(max(-127, min(127, x)));
         f2[i] = part[i] * pow2(max(-127, min(127, n[i])));
-        wide |= max(n[i], x) > 100 || (x < -126 && x > -300) || (n[i] < -126 && n[i] + 37 >= max(-149, x - 40));
+        wide |= max(n[i], x) > 100 || (x < -126 && x > -300) || (n[i] < -126 && n[i] + 57 >= max(-149, x - 20));
     }
     store2(s.f1 + 2 * lane, f1[0], f1[1]);
     store2(s.f2 + 2 * lane, f2[0], f2[1]);

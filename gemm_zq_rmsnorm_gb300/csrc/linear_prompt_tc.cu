@@ -167,6 +167,7 @@ __device__ __noinline__ void weigh_scores(Smem<DK, DV> &sm, const Factors &f, ui
                 const uint32_t *y0 = &s[piece >> 1][8 * (piece & 1) + 2 * i + e];
                 float2 y = mul2(make_float2(__uint_as_float(y0[0]), __uint_as_float(y0[1])),
                                 make_float2(exp2_fast(x.x), exp2_fast(x.y)));
+                y = mul2(y, make_float2(pow2(-kRoom), pow2(-kRoom)));
                 if (side == quarter) y = make_float2(sc + e <= tr ? y.x : 0.0f, sc + e + 1 <= tr ? y.y : 0.0f);
                 split2(y, phi, plo);
             };
@@ -233,7 +234,7 @@ __device__ __forceinline__ void value_parts(const Smem<DK, DV> &sm, const typena
 // Where the factors are numbers the result is the same, bit for bit.
 //
 // A chunk needs it when its factors say so (`wide`), a warp when its state's exponent is
-// above 0.
+// above 20 (values of 2^31 and more).
 __device__ __noinline__ void far_outputs(const Factors &f, int first, uint32_t o1_at, uint32_t o2_at, char *out, int os, int n,
                                          int exponent)
 {
@@ -245,7 +246,7 @@ __device__ __noinline__ void far_outputs(const Factors &f, int first, uint32_t o
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = first + b + i, x = f.n[t] + (int)f.m[t], e = f.n[t] + exponent;
+            const int t = first + b + i, x = f.n[t] + (int)f.m[t] + kRoom, e = f.n[t] + exponent;
             const float part = f.part[t], state = __uint_as_float(o1[i]);
             const int base = state == 0.0f ? x : max(x, e);
             const float y = __fmaf_rn(times_pow2(part, x - base), __uint_as_float(o2[i]), times_pow2(part * state, min(0, e - base)));
@@ -596,7 +597,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
 #pragma unroll
         for (int i = 0; i < N; ++i) S[i] = 0.0f;
         // The registers hold S / 2^exponent, the exponent kept while the column's largest magnitude stays within
-        // 1 .. 2^15, set anew for 2^8 .. 2^9 when it leaves.  (STATES: all of them count in the factors' `scale`.)
+        // 2^8 .. 2^15, set anew for 2^11 .. 2^12 when it leaves.  (STATES: all of them count in the factors' `scale`.)
         int exponent = 0;
         // 2^units of a head's decays as two factors, since a large state may stay a number below what fp32 holds of it
         auto factors_of = [](long long units, float &rest) {
@@ -637,8 +638,8 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             sync(kWarpE);
             tc_fence_after();
             const uint32_t m = max(max(sm.smax[0][column], sm.smax[1][column]), max(sm.smax[2][column], sm.smax[3][column]));
-            if (__any_sync(0xffffffffu, m < 0x3f800000u || m >= 0x47000000u)) {
-                const int to = max(exponent - 126, limit(exponent + row_exponent(m) - 8));
+            if (__any_sync(0xffffffffu, m < 0x43800000u || m >= 0x47000000u)) {
+                const int to = max(exponent - 126, limit(exponent + exponent_of(m) - 11));
                 const float s = pow2(m == 0u ? 0 : exponent - to);
 #pragma unroll
                 for (int i = 0; i < N; ++i) S[i] *= s;
@@ -693,7 +694,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
                 if (__any_sync(0xffffffffu, (unsigned)-n > update.range)) {
                     const bool empty = exponent == kEmpty;
                     const int grow = f.grow, reach = f.reach, from = exponent + grow;
-                    exponent = limit(empty ? reach - 8 : max(from, reach - 84));
+                    exponent = limit(empty ? reach + 22 : max(from, reach - 84));
                     n = max(-127, min(127, reach - exponent)) - kReach;
                     keep = empty ? 0.0f : times_pow2(update.gpart, from - exponent);
                 }
@@ -731,7 +732,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             char *out = reinterpret_cast<char *>(a.out + (seg.row0 + c * C + 16 * part) * a.out_stride + (long long)h * p.Dv +
                                                  col0 + column);
             const int os = 4 * (int)a.out_stride;
-            const bool far = __any_sync(0xffffffffu, f.wide || was > 0);
+            const bool far = __any_sync(0xffffffffu, f.wide || was > 20);
             const float xs = pow2(max(-127, was));
             if (far) far_outputs(f, 16 * part, lanes + kO1 + 16 * part, lanes + kO2 + 16 * part, out, os, n, was);
 #pragma unroll 1
