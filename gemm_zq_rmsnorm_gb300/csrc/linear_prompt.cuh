@@ -42,6 +42,8 @@ struct PromptArgs {
     // sequence's last segment what the sequence starts from
     float *local;
     long long *decay;          // [segments][Hv]: its G
+    float scale;               // a.scale is scale 2^scale_exponent, scale below 1
+    int scale_exponent;
     unsigned int *status;
 };
 

@@ -32,6 +32,7 @@
 // Every wait is bounded: after one has run out no MMA is issued any more, the
 // others return at once and the kernel ends (its results are invalid).
 #include <atomic>
+#include <cmath>
 
 #include "linear_prompt.cuh"
 #include "zq_tc_common.cuh"
@@ -414,8 +415,6 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         float next[2], g[2];   // decays of the chunk after the next and of the next
         long long G[2];        // and their sums
         long long counts = kNoScale;
-        int scale_exponent;
-        const float scale = frexpf(a.scale, &scale_exponent);
         auto decays = [&](int c) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -476,7 +475,7 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
             if (!STATES && c >= 0) {
                 if (w) wait(sm.fact[c & 3], c >> 2);
                 // (what the output alone needs: its warps come to it by way of p_full)
-                if (w == 1) make_factors(sm.f[c & 3], sm.mq[c & 1], scale, scale_exponent);
+                if (w == 1) make_factors(sm.f[c & 3], sm.mq[c & 1], p.scale, p.scale_exponent);
                 if (c) wait(sm.o_full, c - 1);   // the last weights have been read
                 wait(sm.scores, c);
                 tc_fence_after();
@@ -803,6 +802,7 @@ cudaError_t launch(const PromptArgs &p, cudaStream_t st)
     const long long ctas = (long long)(STATES ? p.a.T / p.length : p.segments) * p.a.Hv * (p.Dv / DV);
     PromptArgs args = p;
     args.status = device_status_word();
+    args.scale = std::frexp(p.a.scale, &args.scale_exponent);
     const LinearAttnArgs &a = p.a;
     CUtensorMap map[3];
     auto rows = [&](int i, const float *x, int heads, int D, long long stride, int box) {
