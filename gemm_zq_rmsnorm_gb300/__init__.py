@@ -35,6 +35,7 @@ EXPORTS = ("zq_rmsnorm_q8_1", "zq_q4k_gemv", "zq_q4k_gemv_pair", "zq_q4k_gemm",
            "zq_rmsnorm_q4k_gemm", "zq_copy", "zq_rope_table", "zq_head_norm_rope",
            "zq_paged_attn_workspace_bytes", "zq_paged_attn", "zq_lora_workspace_bytes", "zq_lora",
            "zq_linear_attn_step", "zq_linear_attn_workspace_bytes", "zq_linear_attn", "zq_debug_linear_segments",
+           "zq_debug_linear_attn_expiry",
            "zq_gated_norm_q8_1", "zq_residual_norm_q8_1")
 
 
@@ -116,6 +117,8 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         "zq_linear_attn_workspace_bytes": ([i, i, i, i, i], sz),
         "zq_linear_attn": ([P, ll, P, ll, P, ll, i, i, i, P, ll, P, P, P, P, f, P, ll, P, sz, P], i),
         "zq_debug_linear_segments": ([P, i, i, i, i, P], i),
+        "zq_debug_linear_attn_expiry": ([P, ll, P, ll, P, ll, i, i, i, P, ll, P, P, P, P, f, P, ll, P, sz, i, i, ctypes.c_uint,
+                                         P], i),
         "zq_gated_norm_q8_1": ([P, ll, i, i, i, P, f, P, ll, i, P, ll, P, P], i),
         "zq_residual_norm_q8_1": ([P, ll, P, ll, i, i, P, P, ll, i, f, P, ll, P, f, P, ll, P, P], i),
         "zq_rmsnorm_q4k_gemm": ([P, P, f, i, i, P, i, P, ctypes.POINTER(_Q8), P, sz, P], i),
@@ -754,6 +757,18 @@ def linear_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g, starts: to
     """The same over prompts: the rows of sequence b are starts[b] .. starts[b +
     1] - 1 (int32 [B + 1]) of the T rows; a sequence with fresh[b] != 0 starts
     from zeros (see zq_linear_attn).  Rows of no sequence are not written."""
+    return _linear_attn((_lib or load()).zq_linear_attn, (), q, k, v, g, starts, state, slots, fresh, scale, out, workspace, stream)
+
+
+def debug_linear_attn_expiry(q, k, v, g, starts, state: LinearState, slots, withhold_chunk: int, values: bool = False,
+                             wait_us: int = 1000, out=None, workspace=None, stream=None) -> torch.Tensor:
+    """linear_attn whose waits give up after wait_us, one of them for more than
+    comes (see zq_debug_linear_attn_expiry); the expiry shows in device_status()."""
+    return _linear_attn((_lib or load()).zq_debug_linear_attn_expiry, (values, withhold_chunk, wait_us), q, k, v, g, starts, state,
+                        slots, None, None, out, workspace, stream)
+
+
+def _linear_attn(call, more, q, k, v, g, starts, state, slots, fresh, scale, out, workspace, stream):
     lib = _lib or load()
     T, B = q.shape[0], slots.numel()
     if out is None:
@@ -764,11 +779,9 @@ def linear_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g, starts: to
     _on(state.index, "linear_attn", q, k, v, g, starts, slots, fresh, out, workspace)
     rows, Hk, gg, oo = _linear_rows(q, k, v, g, state, out, "linear_attn")
     ws = (None, 0) if workspace is None else _space(workspace, "linear_attn")
-    status = lib.zq_linear_attn(*rows, T, B, Hk, *gg, _ints(starts, B + 1, "linear_attn: starts"), state._ref,
-                                _ints(slots, B, "linear_attn: slots"),
-                                None if fresh is None else _ints(fresh, B, "linear_attn: fresh"),
-                                state.Dk ** -0.5 if scale is None else scale, *oo, *ws,
-                                _stream_on(stream, state.index))
+    status = call(*rows, T, B, Hk, *gg, _ints(starts, B + 1, "linear_attn: starts"), state._ref,
+                  _ints(slots, B, "linear_attn: slots"), None if fresh is None else _ints(fresh, B, "linear_attn: fresh"),
+                  state.Dk ** -0.5 if scale is None else scale, *oo, *ws, *more, _stream_on(stream, state.index))
     if status:
         _check(status)
     return out

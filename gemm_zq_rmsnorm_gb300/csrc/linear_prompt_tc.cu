@@ -30,7 +30,8 @@
 // the issue slots.
 //
 // Every wait is bounded: after one has run out no MMA is issued any more, the
-// others return at once and the kernel ends (its results are invalid).
+// others return at once and the kernel ends (its results are invalid), when the copies
+// and MMAs on their way have come in.
 #include <atomic>
 #include <cmath>
 
@@ -65,8 +66,10 @@ struct Smem {
     uint32_t smax[4][128];
     uint64_t qk_full[2], qk_empty[2], values[2], sizes[2], w_full[2], fact[4];
     uint64_t scores, scores_read, p_full, v_full, s_full, o_full, o_empty, u_full, u_empty[2];
+    uint64_t drained;
     uint32_t tmem;
     int abort;
+    unsigned int wait_us;   // the waits' limit (behind `abort`)
     Segment seg;
 };
 
@@ -100,14 +103,15 @@ __device__ __forceinline__ void tmem_st4(uint32_t taddr, const uint32_t (&r)[4])
 // The warp waits for a phase.  Many waiting warps share the issue slots (and the
 // instruction cache) with the ones that work, so the loop is as short as it can be,
 // and of every group of warps one waits here while the others sleep in a named
-// barrier; the limit and the others' failure are looked at every 512 probes.
+// barrier; the limit and the others' failure are looked at after 8 probes and then every
+// 64 (of which each lets the warp sleep for a while by itself).
 __device__ __noinline__ void wait_long(uint64_t *bar, int parity, volatile int *abort_flag, unsigned int *status)
 {
     uint64_t since = 0;
-    for (;;) {
+    for (uint32_t turns = 1;; turns = 8) {
         uint32_t done;
         asm volatile(
-            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 64;\n\t"
+            "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, %3;\n\t"
             "AGAIN:\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
             "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t@p bra DONE;\n\t"
@@ -121,12 +125,12 @@ __device__ __noinline__ void wait_long(uint64_t *bar, int parity, volatile int *
             "@q bra AGAIN;\n\t"
             "DONE:\n\tselp.u32 %0, 1, 0, p;\n\t}"
             : "=r"(done)
-            : "r"(smem_u32(bar)), "r"((uint32_t)(parity & 1))
+            : "r"(smem_u32(bar)), "r"((uint32_t)(parity & 1)), "r"(turns)
             : "memory");
         if (__all_sync(0xffffffffu, done) || __any_sync(0xffffffffu, *abort_flag)) return;
         const uint64_t now = global_ns();
         if (!since) since = now;
-        if (now - since > kWaitLimitNs) {
+        if (now - since > 1000ull * *reinterpret_cast<volatile unsigned int *>(abort_flag + 1)) {
             flag_timeout(status);
             *abort_flag = 1;
         }
@@ -282,14 +286,13 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     if (w == kWarpM) tmem_alloc(&sm.tmem, 512);
     if (threadIdx.x == 32) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&sm.qk_full[i], LW);
+            mbar_init(&sm.qk_full[i], LW + (a.withhold_rows == i + 1));
             mbar_init(&sm.qk_empty[i], 1);
             mbar_init(&sm.sizes[i], 2);
             mbar_init(&sm.w_full[i], 4 * QUARTERS);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&sm.fact[i], 1);
-        mbar_init(&sm.values[0], 1);
-        mbar_init(&sm.values[1], 1);
+        for (int i = 0; i < 2; ++i) mbar_init(&sm.values[i], 1 + (a.withhold_values == i + 1));
         mbar_init(&sm.p_full, 3);
         mbar_init(&sm.scores, 1);
         mbar_init(&sm.scores_read, 3);
@@ -300,7 +303,9 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
         mbar_init(&sm.u_full, 1);
         mbar_init(&sm.u_empty[0], 4 * QUARTERS);
         mbar_init(&sm.u_empty[1], 4 * QUARTERS);
+        mbar_init(&sm.drained, 1);
         sm.abort = 0;
+        sm.wait_us = a.wait_us ? a.wait_us : (unsigned int)(kWaitLimitNs / 1000);
         fence_mbar_init();
     }
     if (!STATES)   // P above the diagonal's blocks stays zero
@@ -778,6 +783,11 @@ linear_prompt_tc_kernel(const __grid_constant__ PromptArgs p, const __grid_const
     tc_fence_before();
     __syncthreads();
     if (w == kWarpM) {
+        if (*abort_flag) {   // MMAs still on their way when a wait has run out
+            if (elect_one()) mma_commit(&sm.drained);
+            __syncwarp();
+            mbar_wait_for(&sm.drained, 0, nullptr, 1000000ull);
+        }
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }

@@ -1015,13 +1015,14 @@ size_t zq_linear_attn_workspace_bytes(int T, int B, int Hv, int Dk, int Dv)
     return linear_attn_workspace(T, B, Hv, Dk, Dv);
 }
 
-int zq_linear_attn(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
-                   long long v_stride, int T, int B, int Hk, const float *g, long long g_stride, const int32_t *starts,
-                   const zq_linear_state *state, const int32_t *slots, const int32_t *fresh, float scale, float *out,
-                   long long out_stride, void *workspace, size_t workspace_bytes, void *stream)
+namespace {
+
+// a: what zq_debug_linear_attn_expiry adds
+int linear_attn(const float *q, long long q_stride, const float *k, long long k_stride, const float *v, long long v_stride,
+                int T, int B, int Hk, const float *g, long long g_stride, const int32_t *starts, const zq_linear_state *state,
+                const int32_t *slots, const int32_t *fresh, float scale, float *out, long long out_stride, void *workspace,
+                size_t workspace_bytes, LinearAttnArgs a, const char *name, void *stream)
 {
-    static const char *name = "zq_linear_attn";
-    LinearAttnArgs a{};
     int st, dev;
     if ((st = check_linear(q, q_stride, k, k_stride, v, v_stride, T, Hk, g, g_stride, state, slots, scale, out,
                            out_stride, name, a)))
@@ -1039,6 +1040,34 @@ int zq_linear_attn(const float *q, long long q_stride, const float *k, long long
     if (need && (!workspace || workspace_bytes < need))
         return fail(ZQ_ERR_WORKSPACE, "%s: workspace of %zu bytes required", name, need);
     return launched(launch_linear_attn(a, state->Dk, state->Dv, workspace, (cudaStream_t)stream), name);
+}
+
+}  // namespace
+
+int zq_linear_attn(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
+                   long long v_stride, int T, int B, int Hk, const float *g, long long g_stride, const int32_t *starts,
+                   const zq_linear_state *state, const int32_t *slots, const int32_t *fresh, float scale, float *out,
+                   long long out_stride, void *workspace, size_t workspace_bytes, void *stream)
+{
+    return linear_attn(q, q_stride, k, k_stride, v, v_stride, T, B, Hk, g, g_stride, starts, state, slots, fresh, scale, out,
+                       out_stride, workspace, workspace_bytes, LinearAttnArgs{}, "zq_linear_attn", stream);
+}
+
+int zq_debug_linear_attn_expiry(const float *q, long long q_stride, const float *k, long long k_stride, const float *v,
+                                long long v_stride, int T, int B, int Hk, const float *g, long long g_stride,
+                                const int32_t *starts, const zq_linear_state *state, const int32_t *slots,
+                                const int32_t *fresh, float scale, float *out, long long out_stride, void *workspace,
+                                size_t workspace_bytes, int withhold_values, int withhold_chunk, unsigned int wait_us,
+                                void *stream)
+{
+    static const char *name = "zq_debug_linear_attn_expiry";
+    if (withhold_chunk < 0 || withhold_chunk > 1 || wait_us < 1 || wait_us > 2000000u)
+        return fail(ZQ_ERR_ARG, "%s: withhold_chunk = %d, wait_us = %u out of range", name, withhold_chunk, wait_us);
+    LinearAttnArgs a{};
+    a.wait_us = wait_us;
+    (withhold_values ? a.withhold_values : a.withhold_rows) = withhold_chunk + 1;
+    return linear_attn(q, q_stride, k, k_stride, v, v_stride, T, B, Hk, g, g_stride, starts, state, slots, fresh, scale, out,
+                       out_stride, workspace, workspace_bytes, a, name, stream);
 }
 
 int zq_debug_linear_segments(const int32_t *starts, int T, int B, int Hv, int Dv, int32_t *out)

@@ -23,6 +23,10 @@ struct LinearAttnArgs {
     float scale;
     float *out;
     long long out_stride;
+    // zq_debug_linear_attn_expiry: the waits' limit (0: kWaitLimitNs), and the chunk (1 or 2, 0: none) whose queries and keys,
+    // or whose values, are never all there
+    unsigned int wait_us;
+    int withhold_rows, withhold_values;
 };
 cudaError_t launch_linear_attn_step(const LinearAttnArgs &a, int Dk, int Dv, cudaStream_t st);
 size_t linear_attn_workspace(int T, int B, int Hv, int Dk, int Dv);

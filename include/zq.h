@@ -671,6 +671,20 @@ ZQ_API int zq_linear_attn(const float *q, long long q_stride, const float *k, lo
  */
 ZQ_API int zq_debug_linear_segments(const int32_t *starts, int T, int B, int Hv, int Dv, int32_t *out);
 
+/*
+ * Test hook: zq_linear_attn whose waits give up after wait_us (1 .. 2000000) microseconds,
+ * with one arrival more than there are expected in every sequence (or segment of one) that
+ * comes to its chunk withhold_chunk (0 or 1, of 64 tokens): of queries and keys, or
+ * (withhold_values != 0) of values.  The kernels end, with results that are invalid, and
+ * zq_device_status reports the expiry.
+ */
+ZQ_API int zq_debug_linear_attn_expiry(const float *q, long long q_stride, const float *k, long long k_stride,
+                                       const float *v, long long v_stride, int T, int B, int Hk, const float *g,
+                                       long long g_stride, const int32_t *starts, const zq_linear_state *state,
+                                       const int32_t *slots, const int32_t *fresh, float scale, float *out,
+                                       long long out_stride, void *workspace, size_t workspace_bytes,
+                                       int withhold_values, int withhold_chunk, unsigned int wait_us, void *stream);
+
 /* What a gate's values pass through before they multiply: nothing, 1 / (1 +
  * exp(-g)), or g / (1 + exp(-g)); the sigmoid to about 2^-21 of itself, and zero
  * where it is below 2^-126. */

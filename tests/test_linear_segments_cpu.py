@@ -1,6 +1,7 @@
 """The cut of prompts into segments (zq_debug_linear_segments: the code that the
 kernels run, here on the host): every segment that is read or written has its place
 in the workspace, whatever the starts are."""
+import ctypes
 import random
 
 import pytest
@@ -65,3 +66,16 @@ def test_refuses(bad, status):
     assert e.value.status == status
     out = zq.load()
     assert out.zq_debug_linear_segments(None, 10, 1, 1, 64, None) == -1
+
+
+@pytest.mark.parametrize("chunk,wait_us,status", [(-1, 1000, -1), (2, 1000, -1), (0, 0, -1), (1, 2000001, -1)])
+def test_expiry_hook_refuses(chunk, wait_us, status):
+    """zq_debug_linear_attn_expiry: chunk and limit, then what zq_linear_attn refuses."""
+    lib, at = zq.load(), 0x10000           # fake, never-dereferenced device addresses
+    state = ctypes.byref(zq._LinearState(at, 4, 4, 128, 128))
+
+    def call(c, us, T=30):
+        return lib.zq_debug_linear_attn_expiry(at, 256, at, 256, at, 512, T, 3, 2, at, 4, at, state, at, None, 0.1, at, 512, at,
+                                               1 << 40, 1, c, us, None)
+    assert call(chunk, wait_us) == status and lib.zq_last_error()
+    assert call(0, 1000, T=0) == -2
