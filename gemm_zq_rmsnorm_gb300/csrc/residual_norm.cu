@@ -265,9 +265,15 @@ cudaError_t launch_residual_norm(const ResidualNormArgs &a, cudaStream_t st)
 {
     const int eights = a.K / 8;
     auto threads = [&](int passes) { return ((eights + passes - 1) / passes + 31) / 32 * 32; };
-    // Rows of 5120 with a norm after the block, in turn against a CTA each: 1000 tokens 21.9 us and 20.2, 2000 33.3 and
-    // 32.0, 4096 with a gate 64.5 and 74; of 8192, 2000 tokens 48.8 and 49.6.
-    if (a.K <= kMaxRowsK && (long long)a.B * a.K >= 10000000) return launch_rows<2, 512, 64>(a, threads(2), st);
+    // Rows in turn against a CTA each, us (inputs larger than L2, norm after the block).  With a gate, whose row is one more
+    // to wait for: 1000 x 5120 23.2 and 22.5, 1750 x 5120 32.3 and 32.9, 4096 x 5120 62.3 and 69.7, 1250 x 8192 38.3 and
+    // 38.7; but short rows leave such a CTA little to do beside its waits: 16000 x 1024 55.5 and 53.6, 40000 x 256 51.5 and
+    // 42.6.  Without one: 2000 x 5120 32.3 and 30.1, 3000 x 5120 42.9 and 41.7, 4096 x 5120 53.8 and 54.1, 3000 x 8192 64.8
+    // and 66.1; of up to 4096, where a CTA each has one piece a thread, 3000 x 4096 34.8 and 40.5, 10000 x 1024 28.2 and
+    // 28.8, 40000 x 256 41.3 and 42.1.
+    const long long values = (long long)a.B * a.K;
+    const bool in_turn = a.gate ? a.K > 1024 && values >= 9000000 : values >= (a.K > 4096 ? 18000000 : 10000000);
+    if (a.K <= kMaxRowsK && in_turn) return launch_rows<2, 512, 64>(a, threads(2), st);
     auto direct = [&](auto *kernel, int passes) { return launch_pdl(kernel, dim3((unsigned)a.B), dim3(threads(passes)), 0, st, a); };
     // Two pieces a thread let two CTAs run on an SM where they are wide enough for one to fill it: 400 rows of 5120 9.2 us
     // with one piece, 6.9 with two; 1000 of 8192 34.6 and 29.5; but 400 of 1024 3.1 and 3.6.
