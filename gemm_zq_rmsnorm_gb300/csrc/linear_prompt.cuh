@@ -306,7 +306,7 @@ __device__ __forceinline__ void make_weights(Factors &s, const long long (&G)[2]
             s.reach = reach;
         } else {
             const long long state = max(counts + G[1], kNoScale), sums = G[1] + ((long long)last << 32);
-            counts = max(state, sums);
+            counts = min(max(state, sums), -kNoScale);
             s.keep = exp2_units(state - counts);
             s.add = exp2_units(sums - counts);
             s.scale = counts;

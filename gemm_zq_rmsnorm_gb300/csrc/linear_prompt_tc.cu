@@ -50,7 +50,7 @@ constexpr int kThreads = kWarps * 32;
 // tensor memory columns
 constexpr int kO1 = 0, kO2 = 64, kU = 128, kSh = 256, kSl = 320, kVh = 384, kVl = 416, kWh = 448, kWl = 480;
 constexpr int kU2 = 0;   // a second U where there is no output
-constexpr int kEmpty = -1000;  // exponent of a column of the state that is zero
+constexpr int kEmpty = -(1 << 30);   // exponent of a column of the state that is zero
 static_assert(kVl - kVh == kWl - kWh, "low parts behind high ones");
 
 template <int DK, int DV>

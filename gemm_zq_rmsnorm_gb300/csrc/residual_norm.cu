@@ -11,7 +11,7 @@
 // those of zq_rmsnorm_q8_1 on x_out, byte for byte.
 //
 // HBM bound: 8 bytes a value read (12 with a gate), 4 + 1.125 written.  4096 x 5120
-// with a norm after the block and a gate 64.5 us, 5.6 TB/s (0.82 of the measured copy
+// with a norm after the block and a gate 62 us, 5.8 TB/s (0.85 of the measured copy
 // rate; issue slots 54 % busy: about 60 instructions a value for the gate, the two
 // norms and the packing); 61 tokens 3.7 us, one 3.6 (2.5 at 1024): two barriers and a
 // chain of dependent loads.
@@ -275,8 +275,10 @@ cudaError_t launch_residual_norm(const ResidualNormArgs &a, cudaStream_t st)
     const bool in_turn = a.gate ? a.K > 1024 && values >= 9000000 : values >= (a.K > 4096 ? 18000000 : 10000000);
     if (a.K <= kMaxRowsK && in_turn) return launch_rows<2, 512, 64>(a, threads(2), st);
     auto direct = [&](auto *kernel, int passes) { return launch_pdl(kernel, dim3((unsigned)a.B), dim3(threads(passes)), 0, st, a); };
-    // Two pieces a thread let two CTAs run on an SM where they are wide enough for one to fill it: 400 rows of 5120 9.2 us
-    // with one piece, 6.9 with two; 1000 of 8192 34.6 and 29.5; but 400 of 1024 3.1 and 3.6.
+    // Two pieces a thread let two CTAs run on an SM where they are wide enough for one to fill it: with one piece and with
+    // two, us (inputs larger than L2, norm after the block), 400 rows of 5120 9.9 and 9.2, 1000 18.9 and 18.7, of 8192 400
+    // rows 16.1 and 14.2, 1000 34.9 and 27.5; 512 of 5120 are 11.8 and 12.7 (they just fill one piece's waves), 61 3.7 and
+    // 4.1, 400 of 1024 3.0 and 3.5.
     if (eights <= 1024)
         return a.B > 2 * num_sms() && a.K > 4096 ? direct(residual_norm_kernel<2, 512>, 2) : direct(residual_norm_kernel<1, 1024>, 1);
     if (eights <= 2048) return direct(residual_norm_kernel<2, 1024>, 2);

@@ -171,3 +171,20 @@ def test_forgetting_leaves_nothing_of_the_largest_state(Dk, Dv):
     q[3:] *= 2.0 ** 70
     out, S, o, want = call(q, zeros(T, Dk), zeros(T, Dv), g, S0, 1.0, 80)
     assert bool((out[3:] == 0).all()) and bool((S == 0).all()) and bool(torch.isfinite(out).all())
+
+
+@pytest.mark.parametrize("Dk,Dv", SHAPES)
+@pytest.mark.parametrize("e", [-40, -50, -60, -70, -85, -100])
+def test_a_first_token_that_is_forgotten_in_its_chunk(Dk, Dv, e):
+    """A state of zeros, one small token, and decays that leave nothing of it: sums of 2^-1000 are zeros."""
+    T = 192
+    k, v, g = zeros(T, Dk), randn(62, T, Dv), zeros(T, 1)
+    k[0] = 2.0 ** e * signs(61, Dk)
+    v[0] *= 2.0 ** e
+    g[10] = -float("inf")
+    for heads in (1, 80):
+        out, S, o, want = call(randn(63, T, Dk), k, v, g, zeros(Dk, Dv), 1.0, heads)
+        assert bool((want == 0).all()) and bool((S == 0).all())
+        assert bool((out[10:] == 0).all()) and bool(torch.isfinite(out).all())
+        # (below 2^-126 a value is held to half of 2^-149: the norm of the first ten rows to that much)
+        assert float((out - o).norm()) <= 2.0 ** -18 * float(o.norm()) + (10 * Dv) ** 0.5 * 2.0 ** -149
