@@ -1,6 +1,6 @@
 // linear_attn.cu -- linear attention with a decay for each head: the step of
-// one token per sequence (MIInfer README, "Status": recurrent layers whose state
-// is [heads][128][128]).
+// one token per sequence.  (Not the delta rule of MIInfer's recurrent layers, README,
+// "Status", whose state has the same sizes.)
 //
 // S <- exp(g) S + k v^T,  o = scale * S^T q, for every value head h with the key
 // head h / (Hv / Hk).

@@ -1,10 +1,9 @@
 // linear_prompt.cu -- linear attention with a decay for each head over prompts: the
-// cut of long sequences into segments and the join of their states (MIInfer README,
-// "Status": recurrent layers with a state of [heads][128][128]).
+// cut of long sequences into segments and the join of their states.
 //
 // A CTA walks through a sequence chunk after chunk, so a few long sequences of a few
 // heads would leave most of the GPU idle.  Then every sequence is cut into segments:
-// a first kernel finds what each but the last adds to the state (40 of 126 us at 4096
+// a first kernel finds what each but the last adds to the state (42 of 129 us at 4096
 // tokens of 48 heads), a second one makes the states that many segments start from,
 // and the third does the rest.
 #include "linear_prompt.cuh"

@@ -9,7 +9,7 @@
 //
 // Every product is taken of two binary16 parts of each factor: a row x is 2^e (hi + lo),
 // the parts being those of the row scaled to [2^14, 2^15), so that each value keeps 22 bits
-// of its own unless it is 2^25 below the row's largest; a product is hi hi + hi lo + lo hi
+// of its own unless it is 2^16 below the row's largest (then 2^-39 of that); a product is hi hi + hi lo + lo hi
 // (2^-22 of itself; sums fp32, a chunk's sums added to the state outside the tensor core,
 // whose accumulator truncates).  (Scaled to [1, 2), the low parts end at 2^-25 of the row's
 // largest value: a channel 1000 times the others, which the other factor lacks, cost 8.7e-6

@@ -12,8 +12,8 @@
 // threads for a column), which add U to it, split it for the next chunk and put O1 and
 // O2 together.
 //
-// Warps: 0, 1 and 5 weigh scores, 0 makes the chunk's factors as well, 1 and 5 find the
-// sizes of the values' rows; 2 issues the MMAs; 3, 4 and 6..11 convert queries and keys;
+// Warps: 0, 1 and 5 weigh scores, 0 makes the chunk's weights and the state's factors as
+// well, 1 those of the output's rows, 1 and 5 find the sizes of the values' rows; 2 issues the MMAs; 3, 4 and 6..11 convert queries and keys;
 // 12..15 values for the output, a lane for a column; 16..31 the state and the values
 // weighted for it.  Keys and queries are two stages deep; the key tile serves the scores
 // as rows and U as columns (the same bytes, a descriptor of the other order).  Every
@@ -21,10 +21,11 @@
 // are two, for even and odd chunks.
 //
 // What bounds it is instructions and the steps that wait for one another, not memory:
-// a chunk of 128 x 128 takes about 6700 cycles (issue slots 60 % busy, tensor pipe a
-// third, HBM as well).  4096 tokens of 48 heads 125.6 us (floor by bytes 40, by products
-// 42), 16384 of 8 heads 107, 24 prompts of up to 1500 tokens with 32 heads of 128 x 64
-// 182, one of 37 tokens 5.9.  All 512 columns of tensor memory are in use, so U and the
+// a chunk of 128 x 128 takes about 6800 cycles (issue slots 60 % busy, tensor pipe a
+// third, HBM as well).  4096 tokens of 48 heads 129 us (floor by bytes 40, by products
+// 42), 16384 of 8 heads 113, 24 prompts of up to 1500 tokens with 32 heads of 128 x 64
+// 187, one of 37 tokens 6.4.  Keeping exponents beside the registers (see Factors) is 1 to
+// 3 % of that.  All 512 columns of tensor memory are in use, so U and the
 // scores share theirs; mma.sync beside these MMAs slowed both (214 us), and values
 // unrolled over a whole chunk, or waits in every warp, lose to the instruction cache and
 // the issue slots.

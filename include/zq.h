@@ -599,10 +599,13 @@ ZQ_API int zq_lora(zq_q8_1 a, int B, int K, const int32_t *ids, int n, const voi
 
 /*
  * ------------------------------------------- recurrent mixer and block edges
- * What a hybrid model's recurrent layer does between its projections (MIInfer
- * README, "Status": recurrent layers with a state of [48][128][128] ahead of the
- * Q5_K output projection), and what lies between any block's last projection
- * and the next one's codes.  Their int32 arrays need 4-byte alignment only.
+ * What a hybrid model's recurrent layer with a scalar decay does between its
+ * projections, and what lies between any block's last projection and the next one's
+ * codes.  The recurrence is S = exp(g) S + k v^T.  It is not the delta rule of the
+ * layers that MIInfer's README names ("Status": DeltaNet, a state of [48][128][128]
+ * ahead of the Q5_K output projection), which takes from v what the state already
+ * returns for k: those need another operator, of the same sizes.  The int32 arrays of
+ * these calls need 4-byte alignment only.
  *
  * States of linear attention: fp32 [n][Hv][Dk][Dv], caller-owned device memory;
  * a sequence's state is its slot of the n.  Dk 64 or 128, Dv 64, 128 or 256,
@@ -623,7 +626,7 @@ typedef struct zq_linear_state {
  *           stacked projection's row serve);  v, out : alike with Hv heads of Dv; out may
  *           not overlap the inputs;
  *   g     : fp32, the logarithm of the decay of head h at g + b * g_stride + h,
- *           any value (-infinity forgets everything); NULL: no decay;
+ *           any value below infinity (-infinity forgets every finite state); NULL: no decay;
  *   slots : int32 [B]; a sequence whose slot is outside [0, n) starts from zeros
  *           and keeps nothing (a padded row).  The slots of a call differ: when
  *           two are the same, that state is a mixture of the two;
@@ -648,8 +651,12 @@ ZQ_API int zq_linear_attn_step(const float *q, long long q_stride, const float *
  *           aligned; contents do not matter.  Calls that may run at the same time
  *           (other streams, captured graphs) need workspaces of their own.
  * Other arguments as for zq_linear_attn_step.  Within a chunk of 64 tokens products
- * are taken of values split into two binary16 parts (2^-22 of the rows' norms), sums
- * are fp32; the result does not change from one call to the next.  The kernel's
+ * are taken of values split into two binary16 parts, which keep 22 bits of a value down to
+ * 2^-16 of its row's largest (of q, k or v; of the state 2^-10 of its column's) and 2^-39
+ * (2^-33) of the largest below that, and a token counts to 2^-22 of the norms of the
+ * largest token before it; sums are fp32, with additions that cut off.  Powers of two are kept beside the values, so that
+ * what a step's fp32 operations can hold is held here, however far a chunk's decays or
+ * sizes go.  The result does not change from one call to the next.  The kernel's
  * waits are bounded: one that runs out leaves its output invalid and shows in
  * zq_device_status.  A NaN or infinity in a token's q,
  * k, v or g does not reach earlier tokens, other heads or other sequences.
